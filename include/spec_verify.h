@@ -56,7 +56,9 @@ typedef enum {
   SPEC_ERR_BAD_INPUT_DATA = 5  /* reserved: data errors are reported per request, see below */
 } spec_status_t;
 
-typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype_t;
+/* SPEC_E4M3 (8-bit floats: 4 exponent bits, 3 mantissa bits, largest 448, no infinities) names
+ * the element type of an 8-bit cache in spec_kv_fork; the 8-bit cache's own entry points imply it. */
+typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1, SPEC_E4M3 = 2 } spec_dtype_t;
 typedef enum { SPEC_DRAFT_LOGITS = 0, SPEC_DRAFT_PROBS = 1 } spec_draft_kind_t;
 typedef enum {
   SPEC_SIBLING_RESIDUAL = 0,   /* default: child k is tested against the k-fold residual */
@@ -431,6 +433,169 @@ spec_status_t spec_echo_select_pack(const spec_draft_pool* pool, int32_t K_max,
                                     int32_t* node_offset, int32_t* parent, int32_t* tokens,
                                     int32_t* depth, int32_t* draft_row, int32_t* source,
                                     void* workspace, size_t ws_bytes, spec_stream_t stream);
+
+/* ==========================================================================================
+ * The K/V cache in 8 bits -- no counterpart on the pages beyond [SURV 12.4.3] (paged caches).
+ * A cache of e4m3 codes [num_blocks][H_kv][block_size][head_dim] (one byte each, 16-byte aligned)
+ * with one fp32 scale for each (block, KV head) in [num_blocks][H_kv], K and V apart:
+ *   value = code * scale.
+ * Scales are finite and >= 0.  spec_kv8_append writes powers of two in [2^-100, 2^119]; another
+ * writer may use any scale there or 0 (the attention reads a V scale below 2^-100 as 2^-100).
+ * A block that receives rows belongs to one request (pages shared by a fork are only read).
+ * head_dim is a multiple of 16, at most 256.  Round by round: spec_tree_build, rotary embedding,
+ * spec_kv8_append of the tree's rows at slots prefix_len .., spec_tree_attention_kv8,
+ * spec_verify, spec_kv8_compact.
+ * ========================================================================================== */
+
+/* ------------------------------------------------------------------------------------------
+ * spec_kv8_append
+ * Quantises new K/V rows into the pages: row row_offset[r] + i of k_new / v_new goes to logical
+ * slot start[r] + i of request r, i < row_offset[r+1] - row_offset[r] (any length: one token, a
+ * tree, a prompt).  For each block, head and cache written, with a = the largest finite |x| of
+ * its new rows and `need` = the smallest power of two s with a <= 448 s, clamped to
+ * [2^-100, 2^119]:
+ *   a block that already holds rows before start[r]: s = max(old scale, need); if s > old, its
+ *     earlier rows become e4m3(code * (old / s)) (exact for powers of two except for codes that
+ *     leave e4m3's normal range);
+ *   any other block: s = need;
+ *   new rows: e4m3(x / s), to nearest even; |x / s| > 448 and infinities saturate, NaN stays NaN.
+ * Rows of the block after the appended ones keep their codes (their values, if any, are stale).
+ *   k_new, v_new: [N][H_kv][head_dim] of `dtype`, token n at n * k_ld (v_ld) elements (>= H_kv *
+ *   head_dim, 16-byte multiples), so that slices of a fused projection need no copy; rows from
+ *   row_offset[B] on are ignored.  start [B], row_offset [B+1], block_table
+ *   [B][max_blocks_per_req], req_status [B] int32.
+ * Data errors: a request with other req_status bits than SPEC_REQ_BAD_BLOCK is not touched; a
+ * negative start or inconsistent row_offset gives SPEC_REQ_BAD_SIZE and nothing is written;
+ * rows whose page is beyond the table row or outside [0, num_blocks) are not written and give
+ * SPEC_REQ_BAD_BLOCK.
+ * Errors: SPEC_ERR_INVALID_ARG (null / misaligned pointers, bad sizes or strides),
+ * SPEC_ERR_UNSUPPORTED (head_dim not a multiple of 16 or above 256, block_size above 1024, more
+ * than 2^31 - 1 rows of pages), SPEC_ERR_CUDA.
+ * ------------------------------------------------------------------------------------------ */
+typedef struct {
+  spec_dtype_t dtype;          /* of k_new and v_new */
+  int32_t B, N, H_kv, head_dim, block_size, num_blocks, max_blocks_per_req;
+  int64_t k_ld, v_ld;          /* elements between tokens */
+  const void* k_new;
+  const void* v_new;
+  void* k_cache;
+  void* v_cache;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* block_table;
+  const int32_t* start;
+  const int32_t* row_offset;
+  int32_t* req_status;
+} spec_kv8_append_params;
+
+spec_status_t spec_kv8_append(const spec_kv8_append_params* p, spec_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * spec_tree_attention_kv8
+ * spec_tree_attention over an 8-bit cache: the same visibility (the prefix, ancestors and the
+ * node itself; a tree of one node is plain decoding), K = k code * k_scale, V likewise.  A row
+ * that sees no key (an empty mask row and no prefix) gets O = 0 and LSE = -infinity.  q and o
+ * have `dtype`; scores, softmax statistics and the output are accumulated in fp32.
+ * Every H_q / H_kv ratio, block_size and head_dim (multiple of 16, <= 256) is accepted; BF16
+ * with head_dim 128, block_size 16, 32, 64 or 128 and H_q / H_kv <= 16 runs on the tcgen05
+ * tensor cores, everything else on a CUDA-core kernel.
+ * Requests with req_status bits other than BAD_BLOCK and TIMEOUT, or with T_r > T_max, have no
+ * rows written; a request whose live slots lie beyond its table row gets SPEC_REQ_BAD_BLOCK and
+ * no rows written; one with a bad block id gets SPEC_REQ_BAD_BLOCK and unspecified rows.
+ * workspace: spec_attention_kv8_workspace_size bytes, 256-byte aligned, contents arbitrary; calls
+ * that may overlap on the GPU (other streams, captured graphs) need one each.
+ * Errors: as spec_tree_attention.
+ * ------------------------------------------------------------------------------------------ */
+typedef struct {
+  spec_dtype_t dtype;          /* of q and o */
+  int32_t B, N, T_max;
+  int32_t H_q, H_kv, head_dim;
+  int32_t block_size, num_blocks, max_blocks_per_req;
+  float scale;                 /* <= 0 selects 1/sqrt(head_dim) */
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* block_table;
+  const int32_t* prefix_len;
+  const int32_t* node_offset;
+  const uint32_t* anc_mask;
+  void* o;
+  float* lse;                  /* may be NULL */
+  int32_t* req_status;
+} spec_attn_kv8_params;
+
+size_t spec_attention_kv8_workspace_size(const spec_attn_kv8_params* p);
+spec_status_t spec_tree_attention_kv8(const spec_attn_kv8_params* p, void* workspace,
+                                      size_t ws_bytes, spec_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * spec_kv8_compact
+ * spec_kv_compact in an 8-bit cache: new[P_r + d] = old[P_r + path[r][d]] for every layer, KV
+ * head, K and V.  A block that receives rows takes as scale s the largest among the scales of
+ * the blocks its rows come from and, if it holds rows below P_r, its own; each of its rows
+ * becomes e4m3(code * (its old scale / s)) (bits copied where the scales are equal).  Blocks none
+ * of whose rows move keep their codes and scale.
+ * new_kv_len, slot_map, blocks_in_use and the data errors are spec_kv_compact's.
+ * Layouts: k_cache, v_cache layer 0 with layer_stride bytes between layers; k_scale, v_scale
+ * [num_blocks][H_kv] with scale_layer_stride floats between layers.
+ * Errors: SPEC_ERR_INVALID_ARG, SPEC_ERR_UNSUPPORTED (as spec_kv8_append), SPEC_ERR_CUDA.
+ * ------------------------------------------------------------------------------------------ */
+typedef struct {
+  int32_t B, H_kv, head_dim, block_size, num_blocks, max_blocks_per_req, num_layers, max_path;
+  int64_t layer_stride, scale_layer_stride;
+  void* k_cache;
+  void* v_cache;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* block_table;
+  const int32_t* prefix_len;
+  const int32_t* path;
+  const int32_t* n_acc;
+  int32_t* req_status;
+  int32_t* new_kv_len;
+  int32_t* slot_map;
+  int32_t* blocks_in_use;
+} spec_kv8_compact_params;
+
+spec_status_t spec_kv8_compact(const spec_kv8_compact_params* p, spec_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * spec_kv_fork
+ * Child sequences of cached ones (several samples of one prompt, branches of a search).  Fork f
+ * makes request dst[f] continue request src[f] of length L = kv_len[src[f]]: the first
+ * L / block_size entries of its block_table row become the parent's (shared, read-only from then
+ * on); if L % block_size > 0 the next entry becomes new_block[f], a page of the caller's, and the
+ * parent's rows of that page are copied into it for every layer, head, K and V (and the page's
+ * scales in an 8-bit cache); kv_len[dst[f]] = L.  Other entries of the child's row stay.
+ * `dtype` SPEC_F32, SPEC_BF16 or SPEC_E4M3; k_scale and v_scale are required for SPEC_E4M3 and
+ * ignored otherwise.  block_table [B][max_blocks_per_req], kv_len [B]: in / out.
+ * fork_status [F]: 0, or the fork was left undone: SPEC_REQ_BAD_PARENT (src or dst outside
+ * [0, B), dst of another fork too, dst a src of this call, or new_block[f] named by another fork
+ * that copies a partial page),
+ * SPEC_REQ_BAD_SIZE (L < 0 or pages beyond the table row), SPEC_REQ_BAD_BLOCK (new_block[f] or a
+ * page of the parent outside [0, num_blocks), or new_block[f] one of the parent's pages).
+ * Layouts: layer_stride elements between layers of the caches, scale_layer_stride floats.
+ * Errors: SPEC_ERR_INVALID_ARG, SPEC_ERR_UNSUPPORTED (more than 65535 layers), SPEC_ERR_CUDA.
+ * ------------------------------------------------------------------------------------------ */
+typedef struct {
+  spec_dtype_t dtype;
+  int32_t B, F, H_kv, head_dim, block_size, num_blocks, max_blocks_per_req, num_layers;
+  int64_t layer_stride, scale_layer_stride;
+  void* k_cache;
+  void* v_cache;
+  float* k_scale;
+  float* v_scale;
+  int32_t* block_table;
+  int32_t* kv_len;
+  const int32_t* src;
+  const int32_t* dst;
+  const int32_t* new_block;
+  int32_t* fork_status;
+} spec_fork_params;
+
+spec_status_t spec_kv_fork(const spec_fork_params* p, spec_stream_t stream);
 
 /* Human-readable name of a status code (static storage, never NULL). */
 const char* spec_status_string(spec_status_t status);

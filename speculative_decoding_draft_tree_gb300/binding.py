@@ -14,7 +14,7 @@ import torch
 from . import build as _build
 
 SPEC_OK, SPEC_ERR_INVALID_ARG, SPEC_ERR_UNSUPPORTED, SPEC_ERR_CUDA = 0, 1, 2, 3
-SPEC_F32, SPEC_BF16 = 0, 1
+SPEC_F32, SPEC_BF16, SPEC_E4M3 = 0, 1, 2
 SPEC_DRAFT_LOGITS, SPEC_DRAFT_PROBS = 0, 1
 SPEC_SIBLING_RESIDUAL, SPEC_SIBLING_INDEPENDENT, SPEC_SIBLING_MULTI_DRAFT = 0, 1, 2
 SPEC_VERIFY_PATH_AUTO, SPEC_VERIFY_PATH_SPLIT, SPEC_VERIFY_PATH_WALK = 0, 1, 2
@@ -26,7 +26,8 @@ EXPORTS = ["spec_tree_build", "spec_tree_rope_kv_write", "spec_tree_build_rope_k
            "spec_status_string", "spec_last_cuda_error", "spec_draft_init",
            "spec_draft_expand_select", "spec_draft_topk_append", "spec_echo_workspace_size",
            "spec_echo_select_pack", "spec_debug_draft_copy_stall", "spec_verify_compact",
-           "spec_kernel_launches"]
+           "spec_kernel_launches", "spec_kv8_append", "spec_tree_attention_kv8",
+           "spec_attention_kv8_workspace_size", "spec_kv8_compact", "spec_kv_fork"]
 
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
@@ -69,6 +70,44 @@ class SpecRopeParams(ctypes.Structure):
                 ("base", ctypes.c_double), ("q_in", _vp), ("q_out", _vp), ("k_new", _vp),
                 ("v_new", _vp), ("k_cache", _vp), ("v_cache", _vp), ("block_table", _vp),
                 ("prefix_len", _vp), ("node_offset", _vp), ("pos_id", _vp), ("req_status", _vp)]
+
+
+class SpecKv8AppendParams(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("B", _i32), ("N", _i32), ("H_kv", _i32),
+                ("head_dim", _i32), ("block_size", _i32), ("num_blocks", _i32),
+                ("max_blocks_per_req", _i32), ("k_ld", _i64), ("v_ld", _i64), ("k_new", _vp),
+                ("v_new", _vp), ("k_cache", _vp), ("v_cache", _vp), ("k_scale", _vp),
+                ("v_scale", _vp), ("block_table", _vp), ("start", _vp), ("row_offset", _vp),
+                ("req_status", _vp)]
+
+
+class SpecAttnKv8Params(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("B", _i32), ("N", _i32), ("T_max", _i32),
+                ("H_q", _i32), ("H_kv", _i32), ("head_dim", _i32), ("block_size", _i32),
+                ("num_blocks", _i32), ("max_blocks_per_req", _i32), ("scale", ctypes.c_float),
+                ("q", _vp), ("k_cache", _vp), ("v_cache", _vp), ("k_scale", _vp),
+                ("v_scale", _vp), ("block_table", _vp), ("prefix_len", _vp),
+                ("node_offset", _vp), ("anc_mask", _vp), ("o", _vp), ("lse", _vp),
+                ("req_status", _vp)]
+
+
+class SpecKv8CompactParams(ctypes.Structure):
+    _fields_ = [("B", _i32), ("H_kv", _i32), ("head_dim", _i32), ("block_size", _i32),
+                ("num_blocks", _i32), ("max_blocks_per_req", _i32), ("num_layers", _i32),
+                ("max_path", _i32), ("layer_stride", _i64), ("scale_layer_stride", _i64),
+                ("k_cache", _vp), ("v_cache", _vp), ("k_scale", _vp), ("v_scale", _vp),
+                ("block_table", _vp), ("prefix_len", _vp), ("path", _vp), ("n_acc", _vp),
+                ("req_status", _vp), ("new_kv_len", _vp), ("slot_map", _vp),
+                ("blocks_in_use", _vp)]
+
+
+class SpecForkParams(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("B", _i32), ("F", _i32), ("H_kv", _i32),
+                ("head_dim", _i32), ("block_size", _i32), ("num_blocks", _i32),
+                ("max_blocks_per_req", _i32), ("num_layers", _i32), ("layer_stride", _i64),
+                ("scale_layer_stride", _i64), ("k_cache", _vp), ("v_cache", _vp),
+                ("k_scale", _vp), ("v_scale", _vp), ("block_table", _vp), ("kv_len", _vp),
+                ("src", _vp), ("dst", _vp), ("new_block", _vp), ("fork_status", _vp)]
 
 
 class SpecDraftPool(ctypes.Structure):
@@ -135,6 +174,17 @@ def load_library(build_if_missing=False):
     lib.spec_echo_select_pack.restype = st
     lib.spec_echo_select_pack.argtypes = [ctypes.POINTER(SpecDraftPool), _i32, _vp, _vp, _vp,
                                           _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+    lib.spec_kv8_append.restype = st
+    lib.spec_kv8_append.argtypes = [ctypes.POINTER(SpecKv8AppendParams), _vp]
+    lib.spec_tree_attention_kv8.restype = st
+    lib.spec_tree_attention_kv8.argtypes = [ctypes.POINTER(SpecAttnKv8Params), _vp,
+                                            ctypes.c_size_t, _vp]
+    lib.spec_attention_kv8_workspace_size.restype = ctypes.c_size_t
+    lib.spec_attention_kv8_workspace_size.argtypes = [ctypes.POINTER(SpecAttnKv8Params)]
+    lib.spec_kv8_compact.restype = st
+    lib.spec_kv8_compact.argtypes = [ctypes.POINTER(SpecKv8CompactParams), _vp]
+    lib.spec_kv_fork.restype = st
+    lib.spec_kv_fork.argtypes = [ctypes.POINTER(SpecForkParams), _vp]
     lib.spec_kernel_launches.restype = ctypes.c_uint64
     lib.spec_kernel_launches.argtypes = []
     lib.spec_status_string.restype = ctypes.c_char_p
@@ -384,6 +434,188 @@ def compact_params(k_cache, v_cache, block_table, prefix_len, path, n_acc, req_s
 def spec_kv_compact(params, stream=None):
     code = load_library().spec_kv_compact(ctypes.byref(params), _stream(stream))
     _check(code, "spec_kv_compact")
+
+
+# ----------------------------------------------------------------------------------------------
+# The K/V cache in 8 bits: e4m3 codes (torch.float8_e4m3fn, or the same bytes as uint8) and one
+# fp32 scale for each (block, KV head).
+def _need_kv8(k_cache, v_cache, k_scale, v_scale, layers):
+    """Checks an 8-bit cache ([L,] num_blocks, H_kv, block_size, head_dim; scales without the last
+    two) and returns its shape."""
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _need(t, None, n)
+        if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+            raise ValueError(f"{n} must be torch.float8_e4m3fn or torch.uint8, got {t.dtype}")
+        if t.dim() != 4 + layers or t.shape != k_cache.shape:
+            raise ValueError(f"{n} must be [{'L, ' if layers else ''}num_blocks, H_kv, "
+                             "block_size, head_dim], k_cache and v_cache alike")
+    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        _need(t, torch.float32, n)
+        if t.shape != k_cache.shape[:-2]:
+            raise ValueError(f"{n} must be {tuple(k_cache.shape[:-2])}, got {tuple(t.shape)}")
+    return tuple(k_cache.shape)
+
+
+def _need_shape(t, shape, name, dtype=torch.int32):
+    _need(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def kv8_append_params(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, start,
+                      row_offset, req_status):
+    """k_new / v_new: [N, H_kv, head_dim] (fp32 or bf16; tokens may be strided, as slices of a
+    fused projection are); k_cache / v_cache: one layer, [num_blocks, H_kv, block_size, head_dim];
+    row row_offset[r] + i goes to slot start[r] + i of request r."""
+    num_blocks, H_kv, bs, d = _need_kv8(k_cache, v_cache, k_scale, v_scale, 0)
+    for t, n in ((k_new, "k_new"), (v_new, "v_new")):
+        if t is None or not t.is_cuda:
+            raise ValueError(f"{n} must be a CUDA tensor")
+        if t.dtype != k_new.dtype:
+            raise ValueError(f"{n} must be {k_new.dtype}, got {t.dtype}")
+        if t.dim() != 3 or tuple(t.shape) != (k_new.shape[0], H_kv, d):
+            raise ValueError(f"{n} must be [N, {H_kv}, {d}], got {tuple(t.shape)}")
+        if t.shape[0] > 0 and (t.stride(2) != 1 or (H_kv > 1 and t.stride(1) != d)):
+            raise ValueError(f"{n}: the rows of a token must be contiguous")
+    B = block_table.shape[0]
+    _need(block_table, torch.int32, "block_table")
+    _need_shape(start, (B,), "start")
+    _need_shape(row_offset, (B + 1,), "row_offset")
+    _need_shape(req_status, (B,), "req_status")
+    p = SpecKv8AppendParams()
+    p.dtype = _dtype_code(k_new)
+    p.B, p.N, p.H_kv, p.head_dim = B, k_new.shape[0], H_kv, d
+    p.block_size, p.num_blocks, p.max_blocks_per_req = bs, num_blocks, block_table.shape[1]
+    p.k_ld = k_new.stride(0) if p.N > 1 else H_kv * d
+    p.v_ld = v_new.stride(0) if p.N > 1 else H_kv * d
+    p.k_new, p.v_new = k_new.data_ptr(), v_new.data_ptr()
+    p.k_cache, p.v_cache = k_cache.data_ptr(), v_cache.data_ptr()
+    p.k_scale, p.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
+    p.block_table, p.start = block_table.data_ptr(), start.data_ptr()
+    p.row_offset, p.req_status = row_offset.data_ptr(), req_status.data_ptr()
+    return p
+
+
+def spec_kv8_append(params, stream=None):
+    """Quantise new K/V rows into the 8-bit cache (params from kv8_append_params)."""
+    code = load_library().spec_kv8_append(ctypes.byref(params), _stream(stream))
+    _check(code, "spec_kv8_append")
+
+
+def attention_kv8_params(q, k_cache, v_cache, k_scale, v_scale, block_table, prefix_len,
+                         node_offset, anc_mask, T_max, o, lse, req_status, scale=0.0):
+    """attention_params over one layer of an 8-bit cache; lse may be None."""
+    num_blocks, H_kv, bs, d = _need_kv8(k_cache, v_cache, k_scale, v_scale, 0)
+    _need(q, None, "q")
+    if q.dim() != 3 or q.shape[2] != d:
+        raise ValueError(f"q must be [N, H_q, {d}], got {tuple(q.shape)}")
+    N, H_q = q.shape[0], q.shape[1]
+    _need_shape(o, q.shape, "o", q.dtype)
+    if lse is not None:
+        _need_shape(lse, (N, H_q), "lse", torch.float32)
+    B = block_table.shape[0]
+    _need(block_table, torch.int32, "block_table")
+    _need_shape(prefix_len, (B,), "prefix_len")
+    _need_shape(node_offset, (B + 1,), "node_offset")
+    _need_shape(anc_mask, (N, (int(T_max) + 31) // 32), "anc_mask")
+    _need_shape(req_status, (B,), "req_status")
+    p = SpecAttnKv8Params()
+    p.dtype = _dtype_code(q)
+    p.B, p.N, p.T_max, p.H_q, p.H_kv, p.head_dim = B, N, int(T_max), H_q, H_kv, d
+    p.block_size, p.num_blocks, p.max_blocks_per_req = bs, num_blocks, block_table.shape[1]
+    p.scale = scale
+    p.q, p.k_cache, p.v_cache = q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()
+    p.k_scale, p.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
+    p.block_table, p.prefix_len = block_table.data_ptr(), prefix_len.data_ptr()
+    p.node_offset, p.anc_mask = node_offset.data_ptr(), anc_mask.data_ptr()
+    p.o, p.lse = o.data_ptr(), None if lse is None else lse.data_ptr()
+    p.req_status = req_status.data_ptr()
+    return p
+
+
+def spec_attention_kv8_workspace_size(params):
+    return int(load_library().spec_attention_kv8_workspace_size(ctypes.byref(params)))
+
+
+def spec_tree_attention_kv8(params, workspace, stream=None):
+    """Tree attention over the 8-bit cache; calls that may overlap need a workspace each."""
+    wsz = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    code = load_library().spec_tree_attention_kv8(ctypes.byref(params), _ptr(workspace), wsz,
+                                                  _stream(stream))
+    _check(code, "spec_tree_attention_kv8")
+
+
+def kv8_compact_params(k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, path, n_acc,
+                       req_status, new_kv_len, slot_map, blocks_in_use, max_path):
+    """compact_params for an 8-bit cache: [L, num_blocks, H_kv, block_size, head_dim], scales
+    [L, num_blocks, H_kv]."""
+    L, nb, H_kv, bs, d = _need_kv8(k_cache, v_cache, k_scale, v_scale, 1)
+    B = block_table.shape[0]
+    _need(block_table, torch.int32, "block_table")
+    for t, n in ((prefix_len, "prefix_len"), (n_acc, "n_acc"), (req_status, "req_status"),
+                 (new_kv_len, "new_kv_len"), (blocks_in_use, "blocks_in_use")):
+        _need_shape(t, (B,), n)
+    _need_shape(path, (B, max_path), "path")
+    _need_shape(slot_map, (B, max_path, 2), "slot_map")
+    p = SpecKv8CompactParams()
+    p.B, p.H_kv, p.head_dim, p.block_size, p.num_blocks = B, H_kv, d, bs, nb
+    p.max_blocks_per_req, p.num_layers, p.max_path = block_table.shape[1], L, max_path
+    p.layer_stride, p.scale_layer_stride = nb * H_kv * bs * d, nb * H_kv
+    p.k_cache, p.v_cache = k_cache.data_ptr(), v_cache.data_ptr()
+    p.k_scale, p.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
+    p.block_table, p.prefix_len = block_table.data_ptr(), prefix_len.data_ptr()
+    p.path, p.n_acc, p.req_status = path.data_ptr(), n_acc.data_ptr(), req_status.data_ptr()
+    p.new_kv_len, p.slot_map = new_kv_len.data_ptr(), slot_map.data_ptr()
+    p.blocks_in_use = blocks_in_use.data_ptr()
+    return p
+
+
+def spec_kv8_compact(params, stream=None):
+    """Commit the accepted path in the 8-bit cache, every layer (params from kv8_compact_params)."""
+    code = load_library().spec_kv8_compact(ctypes.byref(params), _stream(stream))
+    _check(code, "spec_kv8_compact")
+
+
+def kv_fork_params(k_cache, v_cache, block_table, kv_len, src, dst, new_block, fork_status,
+                   k_scale=None, v_scale=None):
+    """k_cache / v_cache: [L, num_blocks, H_kv, block_size, head_dim], fp32, bf16 or 8-bit (then
+    with k_scale / v_scale [L, num_blocks, H_kv]); block_table [B, max_blocks], kv_len [B] (both
+    updated); src, dst, new_block, fork_status [F]."""
+    if k_scale is not None or v_scale is not None:
+        L, nb, H_kv, bs, d = _need_kv8(k_cache, v_cache, k_scale, v_scale, 1)
+        code = SPEC_E4M3
+    else:
+        _need(k_cache, None, "k_cache")
+        code = _dtype_code(k_cache)
+        if k_cache.dim() != 5:
+            raise ValueError("k_cache must be [L, num_blocks, H_kv, block_size, head_dim]")
+        _need_shape(v_cache, k_cache.shape, "v_cache", k_cache.dtype)
+        L, nb, H_kv, bs, d = k_cache.shape
+    _need(block_table, torch.int32, "block_table")
+    _need_shape(kv_len, (block_table.shape[0],), "kv_len")
+    F = src.numel()
+    for t, n in ((src, "src"), (dst, "dst"), (new_block, "new_block"),
+                 (fork_status, "fork_status")):
+        _need_shape(t, (F,), n)
+    p = SpecForkParams()
+    p.dtype, p.B, p.F = code, block_table.shape[0], F
+    p.H_kv, p.head_dim, p.block_size, p.num_blocks = H_kv, d, bs, nb
+    p.max_blocks_per_req, p.num_layers = block_table.shape[1], L
+    p.layer_stride, p.scale_layer_stride = nb * H_kv * bs * d, nb * H_kv
+    p.k_cache, p.v_cache = k_cache.data_ptr(), v_cache.data_ptr()
+    p.k_scale = None if k_scale is None else k_scale.data_ptr()
+    p.v_scale = None if v_scale is None else v_scale.data_ptr()
+    p.block_table, p.kv_len = block_table.data_ptr(), kv_len.data_ptr()
+    p.src, p.dst, p.new_block = src.data_ptr(), dst.data_ptr(), new_block.data_ptr()
+    p.fork_status = fork_status.data_ptr()
+    return p
+
+
+def spec_kv_fork(params, stream=None):
+    """Child sequences of cached ones: shared full pages, the partial page copied."""
+    code = load_library().spec_kv_fork(ctypes.byref(params), _stream(stream))
+    _check(code, "spec_kv_fork")
 
 
 # ----------------------------------------------------------------------------------------------

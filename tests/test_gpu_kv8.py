@@ -1,0 +1,524 @@
+"""GPU parity of the 8-bit cache's operators (append, tree attention, compaction, fork) with the
+fp64 oracle.  Codes, scales, tables and lengths are compared bit for bit: every quantisation is one
+division by (or product with) an fp32 number and one rounding to e4m3.  Attention's bars are in
+kv8_util.check_attention."""
+import numpy as np
+import pytest
+import torch
+
+import kv8_util as U
+from oracle import kv8 as K
+from speculative_decoding_draft_tree_gb300 import binding as B
+
+pytestmark = pytest.mark.gpu
+E4M3 = U.E4M3
+
+
+# ------------------------------------------------------------------------------------ append
+class AppendCase:
+    def __init__(self, start, sizes, H=2, d=128, bs=16, dtype=torch.bfloat16, seed=0, pad=0, fused=False, width=None, extra=3):
+        rng = np.random.default_rng(seed)
+        need = [-(-(max(p, 0) + t) // bs) for p, t in zip(start, sizes)]
+        self.nb = sum(need) + extra
+        self.table_np = U.table_for(need, self.nb, rng, width)
+        (self.k, self.ks), (self.v, self.vs) = [tuple(t[0] for t in U.random_cache(1, self.nb, H, bs, d, rng)) for _ in range(2)]
+        off = np.concatenate([[0], np.cumsum(sizes)]).astype(int)
+        self.N = int(off[-1]) + pad
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        mag = torch.exp2(torch.rand((self.N, H, 1), generator=g, device="cuda") * 8 - 4)
+        x = lambda: (torch.randn((self.N, H, d), generator=g, device="cuda") * mag).to(dtype)  # noqa: E731
+        if fused:    # slices of a fused projection: q heads, k heads, v heads of each token
+            qkv = torch.zeros((self.N, 3 * H + 2 * H, d), dtype=dtype, device="cuda")
+            qkv[:, 3 * H:4 * H], qkv[:, 4 * H:] = x(), x()
+            self.k_new, self.v_new = qkv[:, 3 * H:4 * H], qkv[:, 4 * H:]
+        else:
+            self.k_new, self.v_new = x(), x()
+        self.start, self.off, self.bs = start, off, bs
+        self.table = torch.from_numpy(self.table_np).cuda()
+        self.status = torch.zeros(len(start), dtype=torch.int32, device="cuda")
+
+    def run(self, stream=None):
+        self.held = (U.ints(self.start), U.ints(self.off.tolist()))
+        p = B.kv8_append_params(self.k_new, self.v_new, self.k, self.v, self.ks, self.vs, self.table, *self.held, self.status)
+        B.spec_kv8_append(p, stream)
+        torch.cuda.synchronize()
+
+    def check(self):
+        st0 = self.status.cpu().numpy().copy()
+        want = []
+        for codes, scale, x in ((self.k, self.ks, self.k_new), (self.v, self.vs, self.v_new)):
+            c, s = U.values(codes), scale.double().cpu().numpy()
+            added = K.append(c, s, x.double().cpu().numpy(), self.table.cpu().numpy(), self.start, self.off, self.bs, st0)
+            want.append((c, s))
+        self.run()
+        for (c, s), codes, scale in zip(want, (self.k, self.v), (self.ks, self.vs)):
+            np.testing.assert_array_equal(scale.double().cpu().numpy(), s)
+            np.testing.assert_array_equal(U.values(codes), c)
+        assert self.status.cpu().tolist() == [int(a) | b for a, b in zip(st0, added)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("bs,d,H", [(16, 128, 2), (16, 64, 3), (32, 128, 1), (64, 128, 5), (128, 256, 2), (1, 16, 2), (7, 48, 9), (1000, 128, 1)])
+def test_append_shapes(bs, d, H, dtype):
+    AppendCase([0, 5, 37, 16, 63], [1, 40, 3, 16, 130], H=H, d=d, bs=bs, dtype=dtype).check()
+
+
+def test_append_single_tokens_and_empty_requests():
+    AppendCase([0, 15, 16, 17, 31, 255, 4], [1, 1, 0, 1, 1, 1, 0]).check()
+
+
+def test_append_many_requests():
+    rng = np.random.default_rng(4)
+    AppendCase(rng.integers(0, 90, 700).tolist(), rng.integers(0, 4, 700).tolist(), H=1, d=32).check()
+
+
+def test_append_long_prompt_in_wide_windows():
+    # enough tokens that a CTA's window is a whole block
+    AppendCase([3, 0, 250], [5000, 777, 9000], H=32, d=128).check()
+
+
+def test_append_ignores_rows_behind_the_last_sequence():
+    c = AppendCase([2, 9], [5, 6], pad=21)
+    c.k_new[11:] = float("nan")
+    c.check()
+
+
+def test_append_from_a_fused_projection():
+    AppendCase([2, 9, 30], [5, 40, 1], H=3, fused=True).check()
+    AppendCase([2, 9, 30], [5, 40, 1], H=3, fused=True, dtype=torch.float32, bs=64).check()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_append_special_values(dtype):
+    c = AppendCase([7, 0, 5, 0, 0, 3], [4, 3, 3, 20, 2, 2], dtype=dtype, seed=3)
+    c.k_new[0, 0, 5], c.k_new[1, 1, 7], c.v_new[2, 0, 0] = float("inf"), float("-inf"), float("nan")
+    c.k_new[4:7] = 0                     # a fresh block of zeros
+    c.v_new[7:10] = 1e-38                # far below the smallest scale's subnormals
+    c.k_new[7:10, 0] = 3e38              # saturates at the largest scale
+    c.v_new[30:32] = float("nan")        # nothing finite
+    c.check()
+
+
+def test_append_keeps_a_scale_that_is_no_power_of_two():
+    c = AppendCase([7, 3], [4, 5], seed=5)
+    c.ks *= 0.37
+    c.vs *= 1e-3                         # grows: the earlier rows are requantised by a rounded ratio
+    c.check()
+
+
+def test_append_twice_is_idempotent():
+    c = AppendCase([7, 3], [40, 5], seed=6)
+    c.check()
+    before = (c.k.view(torch.uint8).clone(), c.ks.clone(), c.v.view(torch.uint8).clone(), c.vs.clone())
+    c.run()
+    for a, b in zip(before, (c.k.view(torch.uint8), c.ks, c.v.view(torch.uint8), c.vs)):
+        assert torch.equal(a, b)
+
+
+def test_append_data_errors():
+    c = AppendCase([4, -3, 5, 2, 60, 8], [20, 4, 3, 40, 30, 4], seed=7, width=4)   # 60 + 30 slots: beyond 4 pages
+    c.table[0, 1] = 9999                 # rows of that page only are left out
+    c.table[3, 0] = -1
+    c.status[2] = 4                      # flagged by an earlier call: not touched
+    c.check()
+    st = c.status.cpu().tolist()
+    assert st[0] == 32 and st[1] == 2 and st[2] == 4 and st[3] == 32 and st[4] == 32 and st[5] == 0
+
+
+def test_append_inconsistent_offsets():
+    c = AppendCase([0, 0, 0], [6, 6, 6], seed=8)
+    c.off = np.array([0, 6, 12, 30])     # the last request claims rows past N
+    c.check()
+    assert c.status.cpu().tolist() == [0, 0, 2]
+
+
+def test_append_on_another_stream_and_in_a_graph():
+    a, b = AppendCase([7, 3, 31], [4, 35, 1], seed=9), AppendCase([7, 3, 31], [4, 35, 1], seed=9)
+    a.run()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    start, off = U.ints(b.start), U.ints(b.off.tolist())
+    p = B.kv8_append_params(b.k_new, b.v_new, b.k, b.v, b.ks, b.vs, b.table, start, off, b.status)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        B.spec_kv8_append(p, side)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(a.k.view(torch.uint8), b.k.view(torch.uint8)) and torch.equal(a.vs, b.vs)
+
+
+# --------------------------------------------------------------------------------- attention
+@pytest.mark.parametrize("Hq,H", [(1, 1), (4, 4), (8, 2), (8, 1), (16, 1), (5, 1), (14, 2), (6, 2)])
+@pytest.mark.parametrize("T", [1, 5])
+def test_attention_head_layouts(Hq, H, T):
+    c = U.AttnCase([0, 1, 15, 16, 130, 300], [T] * 6, Hq, H)
+    c.run()
+    U.check_attention(c)
+    assert c.status.cpu().tolist() == [0] * 6
+
+
+@pytest.mark.parametrize("bs", [16, 32, 64, 128])
+@pytest.mark.parametrize("sizes", [[1, 1, 1], [3, 1, 7], [40, 17, 64], [129, 5, 256]])
+def test_attention_block_sizes(bs, sizes):
+    c = U.AttnCase([0, 127, 401], sizes, 4, 2, bs=bs, seed=bs)
+    c.run()
+    U.check_attention(c)
+
+
+@pytest.mark.parametrize("d,bs,Hq,H,dtype", [(64, 16, 4, 2, torch.bfloat16), (128, 16, 4, 2, torch.float32), (256, 16, 4, 1, torch.bfloat16),
+                                             (48, 7, 3, 1, torch.float32), (16, 1, 2, 2, torch.float32), (128, 24, 34, 1, torch.bfloat16),
+                                             (128, 256, 4, 4, torch.bfloat16)])
+def test_attention_other_shapes(d, bs, Hq, H, dtype):
+    c = U.AttnCase([0, 33, 500], [1, 6, 20], Hq, H, d=d, bs=bs, dtype=dtype, seed=d)
+    c.run()
+    U.check_attention(c)
+
+
+def test_attention_long_prefixes_are_split_and_joined():
+    c = U.AttnCase([9001, 3, 4100], [1, 1, 1], 8, 2, seed=11)
+    c.run()
+    U.check_attention(c)
+    c = U.AttnCase([5003, 70], [34, 9], 4, 2, seed=12)
+    c.run()
+    U.check_attention(c)
+
+
+def test_attention_many_requests():
+    rng = np.random.default_rng(5)
+    c = U.AttnCase(rng.integers(0, 60, 600).tolist(), rng.integers(1, 3, 600).tolist(), 2, 1, seed=13)
+    c.run()
+    U.check_attention(c)
+
+
+@pytest.mark.parametrize("T", [2, 6, 40])
+def test_attention_rows_that_see_nothing(T):
+    bits = [0] * T + U.chain_bits(T) + [0] * T
+    c = U.AttnCase([0, 5, 0], [T] * 3, 4, 2, bits=bits, seed=14)
+    c.run()
+    U.check_attention(c)
+
+
+@pytest.mark.parametrize("T", [6, 40])
+def test_attention_arbitrary_masks(T):
+    rng = np.random.default_rng(15)
+    bits = [int.from_bytes(rng.bytes(8), "little") & ((1 << T) - 1) for _ in range(2 * T)]
+    c = U.AttnCase([0, 118], [T, T], 4, 1, bits=bits, T_max=64, seed=15)
+    c.run()
+    U.check_attention(c)
+
+
+@pytest.mark.parametrize("T", [1, 30])
+@pytest.mark.parametrize("q_scale,spread", [(20.0, 2), (1e-3, 20), (1e-20, 3), (1.0, 60)])
+def test_attention_magnitudes(T, q_scale, spread):
+    """Peaked and flat rows, tiny queries, block scales that differ by many binades."""
+    c = U.AttnCase([400, 77], [T, T], 4, 2, q_scale=q_scale, spread=spread, seed=16)
+    if spread == 60:
+        c.ks.mul_(2.0 ** -50)          # the scores stay finite: only V's scales spread
+        c.ks.clamp_(min=2.0 ** -12, max=2.0 ** -8)
+    c.run()
+    U.check_attention(c)
+
+
+def test_attention_rows_of_very_different_size():
+    c = U.AttnCase([200], [4], 4, 1, seed=17)
+    c.q *= torch.tensor([1.0, 1e-6, 1e6, 0.0], device="cuda").to(torch.bfloat16)[None, :, None]
+    c.q[:, 2] *= 1e-5
+    c.run()
+    U.check_attention(c)
+
+
+def test_attention_explicit_scale_and_no_lse():
+    c = U.AttnCase([200, 4], [3, 20], 4, 2, seed=18)
+    c.run(scale=0.02)
+    U.check_attention(c, scale=float(np.float32(0.02)))
+    o = c.o.clone()
+    c.o.fill_(0)
+    c.lse.fill_(5.0)
+    c.run(scale=0.02, lse=None)
+    assert torch.equal(o, c.o) and (c.lse == 5.0).all()
+
+
+@pytest.mark.parametrize("T", [1, 3, 20, 60])
+def test_attention_leaves_rows_behind_the_last_sequence(T):
+    c = U.AttnCase([30, 61], [T, T], 8, 2, pad_rows=9, seed=19)
+    c.run()
+    U.check_attention(c)
+    assert (c.o[c.N:] == 77).all() and (c.lse[c.N:] == 55).all()
+
+
+@pytest.mark.parametrize("T", [1, 4, 24])
+def test_attention_flagged_and_inconsistent_requests(T):
+    c = U.AttnCase([30, 61, 200, 9, 40], [T] * 5, 4, 2, seed=20, width=14)
+    c.status[1] = 1                     # an earlier call refused its tree
+    c.prefix_t[3] = -5
+    c.table[2, 3] = 12345               # a page outside the pool
+    c.prefix_t[4] = 2000                # slots beyond the table row
+    c.run()
+    st = c.status.cpu().tolist()
+    assert st == [0, 1, 32, 0, 32]
+    for r in (1, 3, 4):
+        assert (c.o[r * T:(r + 1) * T] == 77).all()
+    c.prefix = [30, 0, 0, 0, 0]
+    c.table_np = np.maximum(c.table_np, 0)
+    U.check_attention(c, rows=slice(0, T))
+
+
+def test_attention_larger_t_max_than_any_tree():
+    for T_max in (64, 256):
+        c = U.AttnCase([30, 61], [3, 20], 4, 2, T_max=T_max, seed=21)
+        c.run()
+        U.check_attention(c)
+
+
+def test_attention_trees_beyond_t_max_are_left_out():
+    c = U.AttnCase([30, 61], [3, 20], 4, 2, seed=22)
+    c.T_max = 8
+    c.anc = c.anc[:, :1].contiguous()
+    c.run()
+    assert (c.o[3:] == 77).all() and (c.o[:3] != 77).all()
+
+
+def test_attention_two_streams_with_a_workspace_each_and_graph_replays():
+    a = U.AttnCase([700, 61], [1, 1], 8, 2, seed=23)
+    b = U.AttnCase([900, 333], [20, 20], 8, 2, seed=24)
+    want = [t.clone() for t in a.run() + b.run()]
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    graphs = []
+    for c, s in ((a, s1), (b, s2)):
+        c.o.zero_()
+        c.p = c.params()
+        c.ws = torch.empty(max(256, B.spec_attention_kv8_workspace_size(c.p)), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for c, s in ((a, s1), (b, s2)):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            B.spec_tree_attention_kv8(c.p, c.ws, s)
+        graphs.append(g)
+    for _ in range(5):
+        with torch.cuda.stream(s1):
+            graphs[0].replay()
+        with torch.cuda.stream(s2):
+            graphs[1].replay()
+    torch.cuda.synchronize()
+    for t, w in zip((a.o, a.lse, b.o, b.lse), want):
+        assert torch.equal(t, w)
+
+
+# -------------------------------------------------------------------------------- compaction
+class CompactCase:
+    def __init__(self, prefix, T, n_acc, L=2, H=2, d=128, bs=16, seed=0, paths=None):
+        rng = np.random.default_rng(seed)
+        Bn = len(prefix)
+        need = [-(-(p + T) // bs) for p in prefix]
+        nb = sum(need) + 2
+        self.table_np = U.table_for(need, nb, rng)
+        self.k, self.ks = U.random_cache(L, nb, H, bs, d, rng)
+        self.v, self.vs = U.random_cache(L, nb, H, bs, d, rng)
+        path = np.full((Bn, T), -1, dtype=np.int32)
+        for r in range(Bn):
+            if paths is not None:
+                path[r, :len(paths[r])] = paths[r]
+            elif n_acc[r] >= 0:
+                path[r, 0] = 0
+                path[r, 1:n_acc[r] + 1] = np.sort(rng.permutation(np.arange(1, T))[:n_acc[r]])
+        self.path, self.n_acc, self.prefix, self.bs, self.T = path, n_acc, prefix, bs, T
+        self.status = torch.zeros(Bn, dtype=torch.int32, device="cuda")
+        self.out = [torch.full((Bn,), -7, dtype=torch.int32, device="cuda") for _ in range(2)]
+        self.moves = torch.full((Bn, T, 2), -7, dtype=torch.int32, device="cuda")
+        self.table = torch.from_numpy(self.table_np).cuda()
+
+    def run(self):
+        self.held = (U.ints(self.prefix), torch.from_numpy(self.path).cuda(), U.ints(self.n_acc))
+        p = B.kv8_compact_params(self.k, self.v, self.ks, self.vs, self.table, self.held[0], self.held[1], self.held[2],
+                                 self.status, self.out[0], self.moves, self.out[1], self.T)
+        B.spec_kv8_compact(p)
+        torch.cuda.synchronize()
+
+    def check(self, status=None):
+        st0 = self.status.cpu().tolist()
+        status = st0 if status is None else status
+        n_ok = [n if s == 0 and n < self.T else -1 for n, s in zip(self.n_acc, status)]
+        want = []
+        for codes, scale in ((self.k, self.ks), (self.v, self.vs)):
+            c, s = U.values(codes), scale.double().cpu().numpy()
+            for layer in range(c.shape[0]):
+                K.compact(c[layer], s[layer], self.table.cpu().numpy(), self.prefix, self.path, n_ok, self.bs)
+            want.append((c, s))
+        self.run()
+        for (c, s), codes, scale in zip(want, (self.k, self.v), (self.ks, self.vs)):
+            np.testing.assert_array_equal(scale.double().cpu().numpy(), s)
+            np.testing.assert_array_equal(U.values(codes), c)
+        assert self.status.cpu().tolist() == status
+        lens = [p + n + 1 if n >= 0 else p for p, n in zip(self.prefix, n_ok)]
+        assert self.out[0].cpu().tolist() == lens
+        assert self.out[1].cpu().tolist() == [-(-n // self.bs) for n in lens]
+        m = self.moves.cpu().numpy()
+        for r, (p, n) in enumerate(zip(self.prefix, n_ok)):
+            for d in range(self.T):
+                assert m[r, d].tolist() == ([p + self.path[r, d], p + d] if d <= n else [-1, -1])
+
+
+@pytest.mark.parametrize("bs,d,H", [(16, 128, 2), (32, 128, 5), (64, 64, 1), (128, 256, 2), (4, 16, 3), (1, 48, 2), (300, 128, 1)])
+def test_compact_shapes(bs, d, H):
+    CompactCase([0, 15, 16, 37, 200], 40, [0, 7, 3, 39, 12], H=H, d=d, bs=bs).check()
+
+
+def test_compact_long_paths():
+    CompactCase([3, 130], 256, [255, 200], L=1, H=1, bs=64, seed=2).check()
+
+
+def test_compact_partly_identical_paths_and_repeats():
+    CompactCase([5, 12, 30], 20, [3, 5, 4], paths=[[0, 1, 2, 3], [0, 1, 2, 9, 10, 17], [0, 6, 6, 6, 8]], seed=3).check()
+
+
+def test_compact_scales_that_are_no_powers_of_two():
+    c = CompactCase([5, 12], 20, [3, 5], seed=4)
+    c.ks *= 0.37
+    c.vs *= torch.rand_like(c.vs) + 0.5
+    c.check()
+
+
+def test_compact_rollback_and_data_errors():
+    c = CompactCase([5, 12, 30, 8, 16, 7], 20, [3, -1, 4, 2, 3, 25], seed=5)
+    c.status[0] = 4
+    c.path[3, 1] = 0                      # not above its step
+    c.table[4] = -1
+    c.check(status=[4, 0, 0, 1, 32, 0])
+
+
+# -------------------------------------------------------------------------------------- fork
+class ForkCase:
+    def __init__(self, lens, src, dst, dtype="e4m3", L=2, H=2, d=128, bs=16, seed=0, fresh=None):
+        rng = np.random.default_rng(seed)
+        need = [-(-n // bs) for n in lens]
+        F = len(src)
+        nb = sum(need) + F + 2
+        t = U.table_for(need, sum(need) or 1, rng, width=max(need) + 1)
+        self.table = torch.from_numpy(t).cuda()
+        self.fresh = [sum(need) + i for i in rng.permutation(F)] if fresh is None else fresh
+        self.ks = self.vs = None
+        if dtype == "e4m3":
+            self.k, self.ks = U.random_cache(L, nb, H, bs, d, rng)
+            self.v, self.vs = U.random_cache(L, nb, H, bs, d, rng)
+        else:
+            td = torch.bfloat16 if dtype == "bf16" else torch.float32
+            self.k, self.v = (torch.from_numpy(rng.normal(size=(L, nb, H, bs, d))).to(td).cuda() for _ in range(2))
+        self.lens, self.src, self.dst, self.bs = lens, src, dst, bs
+        self.kv_len = U.ints(lens)
+        self.status = torch.full((F,), -7, dtype=torch.int32, device="cuda")
+
+    def bits(self):
+        es = self.k.element_size()
+        as_int = {1: torch.uint8, 2: torch.int16, 4: torch.int32}[es]
+        return [t.view(as_int) for t in (self.k, self.v)] + ([self.ks, self.vs] if self.ks is not None else [])
+
+    def check(self, status=None):
+        status = status or [0] * len(self.src)
+        want = [t.clone() for t in self.bits()]
+        table, kv = self.table.clone(), list(self.lens)
+        for f, (a, c) in enumerate(zip(self.src, self.dst)):
+            if status[f]:
+                continue
+            full, rem = self.lens[a] // self.bs, self.lens[a] % self.bs
+            table[c, :full] = self.table[a, :full]
+            kv[c] = self.lens[a]
+            if rem:
+                pb, nb = int(self.table[a, full]), self.fresh[f]
+                table[c, full] = nb
+                for t in want[:2]:
+                    t[:, nb, :, :rem] = t[:, pb, :, :rem]
+                for t in want[2:]:
+                    t[:, nb] = t[:, pb]
+        held = (U.ints(self.src), U.ints(self.dst), U.ints(self.fresh))
+        B.spec_kv_fork(B.kv_fork_params(self.k, self.v, self.table, self.kv_len, *held, self.status, self.ks, self.vs))
+        torch.cuda.synchronize()
+        assert self.status.cpu().tolist() == status
+        assert self.kv_len.cpu().tolist() == kv and torch.equal(self.table, table)
+        for t, w in zip(self.bits(), want):
+            assert torch.equal(t, w)
+
+
+@pytest.mark.parametrize("dtype", ["e4m3", "bf16", "f32"])
+@pytest.mark.parametrize("bs,d,H", [(16, 128, 2), (64, 128, 3), (7, 16, 1), (16, 48, 40)])
+def test_fork_shapes(dtype, bs, d, H):
+    ForkCase([0, 1, 15, 16, 100, 3, 3, 3, 3, 3, 3], [0, 1, 2, 3, 4, 4], [5, 6, 7, 8, 9, 10], dtype, H=H, d=d, bs=bs).check()
+
+
+def test_fork_many():
+    n = 300
+    ForkCase([100 + i for i in range(4)] + [0] * n, [i % 4 for i in range(n)], [4 + i for i in range(n)], L=1, H=1, d=16).check()
+
+
+def test_fork_refuses_what_would_depend_on_order():
+    # 0: fine; 1: child twice; 2: child twice; 3: child is a parent of another; 4: bad ids; 5: itself
+    ForkCase([20, 20, 20, 20, 20, 20, 20], [0, 0, 0, 1, 9, 6], [2, 3, 3, 0, 4, 6]).check([0, 1, 1, 1, 1, 1])
+
+
+def test_fork_refuses_bad_pages_and_lengths():
+    c = ForkCase([20, 20, 20, 20, 32, 20, 20, 20, 20, 20, 20], [0, 1, 2, 3, 4], [5, 6, 7, 8, 9], seed=3)
+    c.fresh[0] = 9999
+    c.fresh[1] = int(c.table[1, 0])
+    c.table[2, 0] = -1
+    c.fresh[4] = -1                       # whole pages only: no fresh page is read
+    c.check([32, 32, 32, 0, 0])
+    c = ForkCase([20, 20, 20, 20, 16], [0, 1, 4], [2, 3, 0], seed=4, fresh=[6, 6, 6])
+    c.dst = [2, 3, 0]
+    c.src = [1, 1, 4]
+    c.check([1, 1, 0])                    # one fresh page for two copies; the third copies nothing
+    c = ForkCase([20, 20, 20], [0], [1], seed=5)
+    c.lens[0] = -4
+    c.kv_len[0] = -4
+    c.check([2])
+
+
+# ---------------------------------------------------------------------------------- together
+def test_a_decoding_loop_over_the_cache():
+    """Prompt, forked samples, single tokens: append -> fork -> append -> attention, each step against
+    the oracle run on the same rows from the start."""
+    H, Hq, bs, d = 2, 8, 16, 128
+    rng = np.random.default_rng(31)
+    g = torch.Generator(device="cuda").manual_seed(31)
+    nb, prompt, forks, steps = 40, 37, 3, 20
+    Bn = 1 + forks
+    k, ks = torch.zeros((1, nb, H, bs, d), device="cuda").to(E4M3), torch.zeros((1, nb, H), device="cuda")
+    v, vs = torch.zeros_like(k), torch.zeros_like(ks)
+    ids = rng.permutation(nb)
+    table_np = np.full((Bn, 5), -1, dtype=np.int32)
+    table_np[0] = ids[:5]
+    for r in range(1, Bn):
+        table_np[r, 3:] = ids[5 + 3 * r:7 + 3 * r]
+    table, status = torch.from_numpy(table_np).cuda(), torch.zeros(Bn, dtype=torch.int32, device="cuda")
+    rows = lambda n: torch.randn((n, H, d), generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    ok, oks, ov, ovs = U.values(k)[0], ks[0].double().cpu().numpy(), U.values(v)[0], vs[0].double().cpu().numpy()
+
+    def append(kn, vn, start, off):
+        args = (U.ints(start), U.ints(off))
+        B.spec_kv8_append(B.kv8_append_params(kn, vn, k[0], v[0], ks[0], vs[0], table, *args, status))
+        K.append(ok, oks, kn.double().cpu().numpy(), table.cpu().numpy(), start, off, bs)
+        K.append(ov, ovs, vn.double().cpu().numpy(), table.cpu().numpy(), start, off, bs)
+        torch.cuda.synchronize()
+
+    append(rows(prompt), rows(prompt), [0] * Bn, [0] + [prompt] * Bn)
+    kv_len, fs = U.ints([prompt] + [0] * forks), torch.zeros(forks, dtype=torch.int32, device="cuda")
+    fresh = [int(ids[5 + 3 * r + 2]) for r in range(1, Bn)]
+    held = (U.ints([0] * forks), U.ints(list(range(1, Bn))), U.ints(fresh))
+    B.spec_kv_fork(B.kv_fork_params(k, v, table, kv_len, *held, fs, ks, vs))
+    torch.cuda.synchronize()
+    assert fs.cpu().tolist() == [0] * forks and kv_len.cpu().tolist() == [prompt] * Bn
+    last = int(table_np[0, prompt // bs])
+    for nbk in fresh:
+        for arr in (ok, ov):
+            arr[nbk, :, :prompt % bs] = arr[last, :, :prompt % bs]
+        oks[nbk], ovs[nbk] = oks[last], ovs[last]
+    for step in range(steps):
+        P = prompt + step
+        append(rows(Bn), rows(Bn), [P] * Bn, list(range(Bn + 1)))
+        np.testing.assert_array_equal(U.values(k)[0], ok)
+        np.testing.assert_array_equal(vs[0].double().cpu().numpy(), ovs)
+        if step % 7 == 0:
+            c = U.AttnCase([P] * Bn, [1] * Bn, Hq, H, seed=step, poison=False)
+            c.k, c.ks, c.v, c.vs, c.table, c.table_np = k[0], ks[0], v[0], vs[0], table, table.cpu().numpy()
+            c.run()
+            U.check_attention(c)
+    assert status.cpu().tolist() == [0] * Bn
