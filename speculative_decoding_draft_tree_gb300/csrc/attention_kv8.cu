@@ -167,6 +167,10 @@ __global__ void __launch_bounds__(kv8_simt::kThreads) attn_kv8_simt_kernel(AttnK
   }
 }
 
+bool attn_kv8_tc_takes(const AttnKv8Dev& a, bool bf16);
+size_t attn_kv8_tc_workspace(const AttnKv8Dev& a);
+spec_status_t launch_attn_kv8_tc(const AttnKv8Dev& a, void* ws, size_t ws_bytes, cudaStream_t s);
+
 static spec_status_t check_attn_kv8(const spec_attn_kv8_params* p) {
   if (!p) return SPEC_ERR_INVALID_ARG;
   if (p->dtype != SPEC_F32 && p->dtype != SPEC_BF16) return SPEC_ERR_INVALID_ARG;
@@ -208,7 +212,8 @@ extern "C" {
 
 size_t spec_attention_kv8_workspace_size(const spec_attn_kv8_params* p) {
   if (spec::check_attn_kv8(p) != SPEC_OK) return 0;
-  return 256;
+  const spec::AttnKv8Dev d = spec::make_dev(p);
+  return spec::attn_kv8_tc_takes(d, p->dtype == SPEC_BF16) ? spec::attn_kv8_tc_workspace(d) : 256;
 }
 
 spec_status_t spec_tree_attention_kv8(const spec_attn_kv8_params* p, void* workspace,
@@ -219,6 +224,8 @@ spec_status_t spec_tree_attention_kv8(const spec_attn_kv8_params* p, void* works
   if (p->N == 0) return SPEC_OK;
   const AttnKv8Dev d = make_dev(p);
   const cudaStream_t s = (cudaStream_t)stream;
+  if (attn_kv8_tc_takes(d, p->dtype == SPEC_BF16))
+    return launch_attn_kv8_tc(d, workspace, ws_bytes, s);
   const int chunks = (d.G + kv8_simt::kHeads - 1) / kv8_simt::kHeads;
   const long long ys = (long long)d.H_kv * chunks;
   if (ys > 65535) return SPEC_ERR_UNSUPPORTED;

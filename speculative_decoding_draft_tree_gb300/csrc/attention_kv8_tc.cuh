@@ -1,0 +1,465 @@
+// The partition of spec_tree_attention_kv8's work over persistent CTAs, the page copies and the
+// tensor-core forms that its kernels share.
+//
+// Work unit = (request r, KV head h, tile of query rows); its K/V is read in tiles of 128 slots.
+// The units are laid end to end (request, head, row tile) as one stream of K/V tiles that is cut
+// into equal contiguous ranges, one per CTA.  A unit cut by a range boundary is computed in
+// pieces: each writes its normalised output and log-sum-exp, and the CTA holding the first piece
+// leaves a record from which a second launch joins them.
+//
+// 8-bit codes go to tcgen05.mma kind::f8f6f4 as they are.  The other operand of each product keeps
+// its precision as the sum of two e4m3 pieces, hi = e4m3(x) and lo = e4m3(x - hi), both multiplied
+// into the same fp32 accumulator: a bf16 query is exactly hi + lo (4 + 4 significant bits) but
+// for elements 2^-18 of the row's largest, a softmax weight keeps 8 bits.  fp8 products run at
+// twice the bf16 rate, so the two pieces cost what one bf16 product does, and K and V are read by
+// the tensor core where TMA put them, one byte an element: converting them to bf16 first would
+// move 6 bytes of shared memory an element against 2, more than the SM has at HBM speed.
+#pragma once
+
+#include <cudaTypedefs.h>
+
+#include "attention_kv8.cuh"
+#include "tc_ptx.cuh"
+
+namespace spec {
+namespace kv8tc {
+
+constexpr int kD = 128;
+constexpr int kBN = 128;                          // slots of a K/V tile
+constexpr int kTile = kBN * kD;                   // bytes
+constexpr long long kWaitLimit = 4000000000LL;    // clock cycles (~2 s)
+constexpr int kMaxCtas = 1024;
+// Weights enter the products as 2^(y - ref + kShift); the reference moves when a y passes it by
+// more than 1, so that they stay below 2^(kShift + 1) = 256 <= 448 and a row's largest is at
+// least 2^(kShift - 1).
+constexpr float kShift = 7.f;
+constexpr float kCeil = 8.f;
+constexpr float kMinVScale = 7.888609052210118e-31f;   // 2^-100
+
+struct MergeRec {
+  int np, h, mt, o, T, ca, slot0;
+};
+
+struct TcDev {
+  AttnKv8Dev a;
+  int tpt;              // tree tokens of a row tile
+  int log2bs;
+  int kv_rows;          // a row past the cache: TMA fills zeros there
+  int ctas, min_tiles;
+  int part_rows;        // rows of a piece
+  MergeRec* recs;       // [ctas]
+  float* part_o;        // [2 ctas][part_rows][128]
+  float* part_lse;      // [2 ctas][part_rows], log2
+};
+
+struct ReqGeom {
+  int o, T, P, mts, nts, units;
+};
+__device__ __forceinline__ ReqGeom req_geom(const TcDev& d, int r) {
+  ReqGeom g;
+  g.o = d.a.node_offset[r];
+  g.T = d.a.node_offset[r + 1] - g.o;
+  g.P = d.a.prefix_len[r];
+  const bool ok = kv8_live(d.a, r, g.T, g.P) == Kv8Live::yes && g.o >= 0 && g.o + g.T <= d.a.N;
+  g.mts = ok ? (g.T + d.tpt - 1) / d.tpt : 0;
+  g.nts = ok ? (g.P + g.T + kBN - 1) / kBN : 0;
+  g.units = d.a.H_kv * g.mts;
+  return g;
+}
+
+struct Range {
+  long long total, t0, t1;   // tiles of the stream; this CTA's
+  int C;                     // ranges
+  int r0, r1;                // requests holding tiles t0 and t1 - 1
+  long long rbeg0, rbeg1;    // their first tiles
+};
+__device__ __forceinline__ long long range_start(long long total, int C, int c) {
+  return total * c / C;
+}
+__device__ __forceinline__ int range_of(long long t, long long total, int C) {
+  const long long c = ((t + 1) * C + total - 1) / total - 1;
+  return int(c < 0 ? 0 : (c >= C ? C - 1 : c));
+}
+
+// Every thread computes the same Range.  s64: scratch of kThreads / 32 + 2 entries, s32 of two.
+template <int kThreads>
+__device__ Range cta_range(const TcDev& d, long long* s64, int* s32) {
+  constexpr int kW = kThreads / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  long long mine = 0;
+  for (int r = tid; r < d.a.B; r += kThreads) {
+    const ReqGeom g = req_geom(d, r);
+    mine += (long long)g.units * g.nts;
+    if (blockIdx.x == 0 && kv8_live(d.a, r, g.T, g.P) == Kv8Live::beyond_table)
+      atomicOr(&d.a.req_status[r], SPEC_REQ_BAD_BLOCK);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) s64[warp] = mine;
+  if (tid < 2) s32[tid] = -1;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kW; ++w) total += s64[w];
+  Range R;
+  R.total = total;
+  R.C = int(max(1LL, min((long long)d.ctas, total / d.min_tiles)));
+  R.t0 = R.t1 = 0;
+  R.r0 = R.r1 = 0;
+  R.rbeg0 = R.rbeg1 = 0;
+  const int c = blockIdx.x;
+  if (total == 0 || c >= R.C) return R;
+  R.t0 = range_start(total, R.C, c);
+  R.t1 = range_start(total, R.C, c + 1);
+  long long base = 0;
+  for (int r00 = 0; r00 < d.a.B; r00 += kThreads) {
+    __syncthreads();
+    const int r = r00 + tid;
+    long long tiles = 0;
+    if (r < d.a.B) {
+      const ReqGeom g = req_geom(d, r);
+      tiles = (long long)g.units * g.nts;
+    }
+    long long incl = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) s64[warp] = incl;
+    __syncthreads();
+    long long before = 0, chunk = 0;
+#pragma unroll
+    for (int w = 0; w < kW; ++w) {
+      if (w < warp) before += s64[w];
+      chunk += s64[w];
+    }
+    const long long hi = base + before + incl, lo = hi - tiles;
+    const bool found = base + chunk > R.t1 - 1;
+    if (tiles > 0 && lo <= R.t0 && R.t0 < hi) {
+      s32[0] = r;
+      s64[kW] = lo;
+    }
+    if (tiles > 0 && lo <= R.t1 - 1 && R.t1 - 1 < hi) {
+      s32[1] = r;
+      s64[kW + 1] = lo;
+    }
+    base += chunk;
+    if (found) break;
+  }
+  __syncthreads();
+  R.r0 = s32[0];
+  R.rbeg0 = s64[kW];
+  R.r1 = s32[1];
+  R.rbeg1 = s64[kW + 1];
+  // both are always found; anything else would index out of bounds: no work
+  if (R.r0 < 0 || R.r0 >= d.a.B || R.r1 < R.r0 || R.r1 >= d.a.B) R.t0 = R.t1 = 0;
+  return R;
+}
+
+// Tiles [j0, j1) of unit (r, h, row tile mt).
+struct Item {
+  int r, h, mt, j0, j1;
+  int slot;               // >= 0: a piece of a cut unit, written to part_o[slot]
+  int o, T, P;
+};
+struct ItemIter {
+  long long t, rbeg, rend;
+  int r;
+  ReqGeom g;
+  __device__ __forceinline__ void start(const TcDev& d, const Range& R) {
+    t = R.t0;
+    r = R.r0;
+    rbeg = rend = R.rbeg0;
+    if (t < R.t1) {
+      g = req_geom(d, r);
+      rend = rbeg + (long long)g.units * g.nts;
+    }
+  }
+  __device__ __forceinline__ bool next(const TcDev& d, const Range& R, Item& it) {
+    if (t >= R.t1) return false;
+    while (t >= rend) {
+      if (r + 1 >= d.a.B) return false;
+      ++r;
+      g = req_geom(d, r);
+      rbeg = rend;
+      rend = rbeg + (long long)g.units * g.nts;
+    }
+    const long long off = t - rbeg;
+    const int u = int(off / g.nts);
+    it.r = r;
+    it.h = u / g.mts;
+    it.mt = u - it.h * g.mts;
+    it.j0 = int(off - (long long)u * g.nts);
+    it.j1 = int(min((long long)g.nts, (long long)it.j0 + (R.t1 - t)));
+    it.o = g.o;
+    it.T = g.T;
+    it.P = g.P;
+    const bool partial = it.j0 > 0 || it.j1 < g.nts;
+    it.slot = partial ? (t == R.t0 ? 2 * int(blockIdx.x) : 2 * int(blockIdx.x) + 1) : -1;
+    t += it.j1 - it.j0;
+    return true;
+  }
+};
+
+// Thread 0 of CTA c: the record of the unit holding the range's last tile, if it starts in this
+// range and continues past it.  Piece p > 0 starts range ca + p and lies in slot 2 (ca + p).
+__device__ __forceinline__ void write_merge_record(const TcDev& d, const Range& R) {
+  MergeRec rec;
+  rec.np = rec.h = rec.mt = rec.o = rec.T = rec.ca = rec.slot0 = 0;
+  if (R.t0 < R.t1) {
+    const ReqGeom g = req_geom(d, R.r1);
+    const int u = int((R.t1 - 1 - R.rbeg1) / g.nts);
+    const long long ubeg = R.rbeg1 + (long long)u * g.nts;
+    if (ubeg >= R.t0 && ubeg + g.nts > R.t1) {
+      rec.ca = int(blockIdx.x);
+      rec.np = range_of(ubeg + g.nts - 1, R.total, R.C) - rec.ca + 1;
+      rec.h = u / g.mts;
+      rec.mt = u - rec.h * g.mts;
+      rec.o = g.o;
+      rec.T = g.T;
+      rec.slot0 = ubeg > R.t0 ? 2 * rec.ca + 1 : 2 * rec.ca;
+    }
+  }
+  d.recs[blockIdx.x] = rec;
+}
+
+// ------------------------------------------------------------------------------ waits
+__device__ __forceinline__ bool wait1(uint64_t* bar, int parity, volatile int* abort) {
+  return tc::mbar_wait(bar, uint32_t(parity & 1), abort, kWaitLimit);
+}
+// all lanes wait; the outcome is the warp's
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, int parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, wait1(bar, parity, abort));
+}
+// one lane waits, the warp gets the outcome
+__device__ __forceinline__ bool lane0_wait(uint64_t* bar, int parity, volatile int* abort) {
+  bool r = true;
+  if ((threadIdx.x & 31) == 0) r = wait1(bar, parity, abort);
+  return __shfl_sync(0xffffffffu, r ? 1 : 0, 0) != 0;
+}
+
+// ------------------------------------------------------------------------------ page copies
+// One warp brings the K (or V) tiles of the CTA's items into a ring of stages.  Lanes below
+// 128 / bs hold the tile's page ids, fetched a tile ahead; consecutive pages come as one 16 KB
+// box, others as a box each.  Pages past the request or with a bad id are read from a row past
+// the cache, which TMA fills with zeros.  Every copy issued is waited for before return.
+__device__ __forceinline__ void page_producer(const TcDev& d, const Range& R,
+                                              const CUtensorMap* map, const CUtensorMap* wide,
+                                              int nstage, uint8_t* ring, uint64_t* full,
+                                              uint64_t* empty, bool flag_bad, int* abort_flag) {
+  const int lane = threadIdx.x & 31;
+  const int bs = d.a.bs, ppt = kBN >> d.log2bs, page_bytes = bs * kD;
+  int kt = 0;
+  bool ok = true;
+  ItemIter iter;
+  iter.start(d, R);
+  Item it;
+  while (ok && iter.next(d, R, it)) {
+    const int nblk = (it.P + it.T + bs - 1) >> d.log2bs;
+    const int32_t* table = d.a.block_table + size_t(it.r) * d.a.max_blocks;
+    auto page_of = [&](int j) -> int {
+      int pb = -1;
+      const int lb = j * ppt + lane;
+      if (lane < ppt && lb < nblk) {
+        pb = table[lb];
+        if (pb < 0 || pb >= d.a.num_blocks) {
+          if (flag_bad) atomicOr(&d.a.req_status[it.r], SPEC_REQ_BAD_BLOCK);
+          pb = -2;
+        }
+      }
+      return pb;
+    };
+    int cur = page_of(it.j0);
+    for (int j = it.j0; j < it.j1; ++j, ++kt) {
+      const int next = j + 1 < it.j1 ? page_of(j + 1) : -1;
+      const int st = kt % nstage, use = kt / nstage;
+      if (use > 0 && !lane0_wait(empty + st, use - 1, abort_flag)) {
+        ok = false;
+        break;
+      }
+      const int first = __shfl_sync(0xffffffffu, cur, 0);
+      const bool run = __all_sync(0xffffffffu, lane >= ppt || cur == first + lane) && first >= 0;
+      if (lane == 0) tc::mbar_arrive_expect_tx(full + st, kTile);
+      __syncwarp();
+      uint8_t* dst = ring + st * kTile;
+      if (run) {
+        if (lane == 0) tc::tma_load_4d(dst, wide, 0, 0, it.h, first, full + st);
+      } else if (lane < ppt) {
+        const int row = cur >= 0 ? (cur * d.a.H_kv + it.h) * bs : d.kv_rows;
+        tc::tma_load_2d(dst + lane * page_bytes, map, 0, row, full + st);
+      }
+      __syncwarp();
+      cur = next;
+    }
+  }
+  if (lane == 0) {
+    if (!ok) *reinterpret_cast<volatile int*>(abort_flag) = 1;
+    for (int k = max(0, kt - nstage); k < kt; ++k)
+      tc::mbar_wait(full + k % nstage, (k / nstage) & 1, abort_flag, kWaitLimit / 8);
+  }
+  __syncwarp();
+}
+
+// The scales of each tile's pages into a ring: k[i] = K scale, lv[i] = log2 of the V scale, iv[i]
+// its reciprocal, i < 128 / bs.  One warp, two tiles at a time (lanes 16 t + 0..7: K, + 8..15: V),
+// far enough ahead of the softmax to hide both dependent loads.
+struct ScaleSlot {
+  float k[8], lv[8], iv[8];
+};
+constexpr int kScaleRing = 8;
+__device__ __forceinline__ void scale_producer(const TcDev& d, const Range& R, ScaleSlot* ring,
+                                               uint64_t* full, uint64_t* empty, int* abort_flag) {
+  const int lane = threadIdx.x & 31;
+  const int ppt = kBN >> d.log2bs, i = lane & 7, sub = lane >> 4;
+  const bool is_v = lane & 8;
+  const float* scale = is_v ? d.a.v_scale : d.a.k_scale;
+  int kt = 0;
+  bool ok = true;
+  ItemIter iter;
+  iter.start(d, R);
+  Item it;
+  while (ok && iter.next(d, R, it)) {
+    const int nblk = (it.P + it.T + d.a.bs - 1) >> d.log2bs;
+    const int32_t* table = d.a.block_table + size_t(it.r) * d.a.max_blocks;
+    auto page_of = [&](int j) -> int {
+      const int lb = (j + sub) * ppt + i;
+      int pb = -1;
+      if (i < ppt && j + sub < it.j1 && lb < nblk) pb = table[lb];
+      return pb >= 0 && pb < d.a.num_blocks ? pb : -1;
+    };
+    int cur = page_of(it.j0);
+    for (int j = it.j0; j < it.j1; j += 2) {
+      float s = cur >= 0 ? scale[size_t(cur) * d.a.H_kv + it.h] : 0.f;
+      const int next = page_of(j + 2);
+      const int n = min(2, it.j1 - j);
+      for (int u = 0; u < n; ++u) {
+        const int slot = (kt + u) % kScaleRing, use = (kt + u) / kScaleRing;
+        if (use > 0 && !lane0_wait(empty + slot, use - 1, abort_flag)) ok = false;
+      }
+      if (!ok) break;
+      if (sub < n) {
+        ScaleSlot* o = ring + (kt + sub) % kScaleRing;
+        if (!is_v) {
+          o->k[i] = s;
+        } else {
+          // a V scale of 0 (a block of zeros) must not make 0 * infinity
+          s = fmaxf(s, kMinVScale);
+          o->lv[i] = log2f(s);
+          o->iv[i] = 1.f / s;
+        }
+      }
+      __syncwarp();
+      if (lane == 0)
+        for (int u = 0; u < n; ++u) tc::mbar_arrive(full + (kt + u) % kScaleRing);
+      kt += n;
+      cur = next;
+    }
+  }
+  if (lane == 0 && !ok) *reinterpret_cast<volatile int*>(abort_flag) = 1;
+  __syncwarp();
+}
+
+// ------------------------------------------------------------------------------ number forms
+// eight bf16 query elements, scaled, as two pieces of eight e4m3 codes each
+__device__ __forceinline__ void split_q8(const uint4& w, float inv, uint2& hi, uint2& lo) {
+  float f[8];
+  elem<__nv_bfloat16>::unpack(w, f);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] *= inv;
+  hi.x = kv8::pack_e4m3x4(f[0], f[1], f[2], f[3]);
+  hi.y = kv8::pack_e4m3x4(f[4], f[5], f[6], f[7]);
+  float b[4];
+  kv8::unpack_e4m3x4(hi.x, b);
+  lo.x = kv8::pack_e4m3x4(f[0] - b[0], f[1] - b[1], f[2] - b[2], f[3] - b[3]);
+  kv8::unpack_e4m3x4(hi.y, b);
+  lo.y = kv8::pack_e4m3x4(f[4] - b[0], f[5] - b[1], f[6] - b[2], f[7] - b[3]);
+}
+// two weights as two pieces of two codes each (16-bit words), by way of fp16: 11 bits, the
+// remainder after the first piece is exact
+__device__ __forceinline__ void split_p2(float a, float b, uint32_t& hi, uint32_t& lo) {
+  uint32_t w, back, rest;
+  uint16_t h, l;
+  asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(w) : "f"(a), "f"(b));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(w));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(h));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(w), "r"(back));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(rest));
+  hi = h;
+  lo = l;
+}
+
+// D[tmem] (+)= A[smem] * B[smem], kind::f8f6f4 (e4m3 codes, fp32 accumulate), K = 32
+__device__ __forceinline__ void mma_e4m3_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// the same with A in tensor memory, four codes to a 32-bit column
+__device__ __forceinline__ void mma_e4m3_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Instruction descriptor of kind::f8f6f4: fp32 accumulator (bits 4-5 = 1), A and B e4m3 (both
+// type fields 0), major-ness in bits 15 / 16 (1 = MN-major), N >> 3 in bits 17-22, M >> 4 in 24-28.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool b_mn) {
+  return (1u << 4) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) | (uint32_t(N >> 3) << 17) |
+         (uint32_t(M >> 4) << 24);
+}
+
+// Reductions of 16 values a lane over the 32 lanes: every exchange halves what a lane holds, 16
+// shuffles instead of 80.  Lane l ends with the result of row row16(l) (l and l ^ 1 alike).
+__device__ __forceinline__ int row16(int lane) {
+  return ((lane >> 4) & 1) * 8 + ((lane >> 3) & 1) * 4 + ((lane >> 2) & 1) * 2 + ((lane >> 1) & 1);
+}
+template <bool kMax>
+__device__ __forceinline__ float reduce16(const float (&v)[16], int lane) {
+  auto op = [](float x, float y) { return kMax ? fmaxf(x, y) : x + y; };
+  float a8[8], a4[4], a2[2], r;
+  const bool b4 = lane & 16, b3 = lane & 8, b2 = lane & 4, b1 = lane & 2;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float keep = b4 ? v[i + 8] : v[i], send = b4 ? v[i] : v[i + 8];
+    a8[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, 16));
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float keep = b3 ? a8[i + 4] : a8[i], send = b3 ? a8[i] : a8[i + 4];
+    a4[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, 8));
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float keep = b2 ? a4[i + 2] : a4[i], send = b2 ? a4[i] : a4[i + 2];
+    a2[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, 4));
+  }
+  const float keep = b1 ? a2[1] : a2[0], send = b1 ? a2[0] : a2[1];
+  r = op(keep, __shfl_xor_sync(0xffffffffu, send, 2));
+  return op(r, __shfl_xor_sync(0xffffffffu, r, 1));
+}
+
+// OR of a predicate over the `n` threads of named barrier `id`
+__device__ __forceinline__ bool bar_any(int id, int n, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred a, b;\n\t"
+      "setp.ne.u32 a, %3, 0;\n\t"
+      "barrier.cta.red.or.pred b, %1, %2, a;\n\t"
+      "selp.u32 %0, 1, 0, b;\n\t}"
+      : "=r"(r) : "r"(id), "r"(n), "r"(p ? 1u : 0u) : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void bar_sync(int id, int n) {
+  asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+
+}  // namespace kv8tc
+}  // namespace spec
