@@ -302,18 +302,16 @@ __device__ __forceinline__ void page_producer(const TcDev& d, const Range& R,
 }
 
 // The scales of each tile's pages into a ring: k[i] = K scale, lv[i] = log2 of the V scale, iv[i]
-// its reciprocal, i < 128 / bs.  One warp, two tiles at a time (lanes 16 t + 0..7: K, + 8..15: V),
-// far enough ahead of the softmax to hide both dependent loads.
+// its reciprocal, i < 128 / bs.  One warp, four tiles at a time (lanes 8 u .. 8 u + 7: tile u), far
+// enough ahead of the softmax to hide its dependent loads.
 struct ScaleSlot {
   float k[8], lv[8], iv[8];
 };
-constexpr int kScaleRing = 8;
+constexpr int kScaleRing = 16;
 __device__ __forceinline__ void scale_producer(const TcDev& d, const Range& R, ScaleSlot* ring,
                                                uint64_t* full, uint64_t* empty, int* abort_flag) {
   const int lane = threadIdx.x & 31;
-  const int ppt = kBN >> d.log2bs, i = lane & 7, sub = lane >> 4;
-  const bool is_v = lane & 8;
-  const float* scale = is_v ? d.a.v_scale : d.a.k_scale;
+  const int ppt = kBN >> d.log2bs, i = lane & 7, sub = lane >> 3;
   int kt = 0;
   bool ok = true;
   ItemIter iter;
@@ -329,31 +327,30 @@ __device__ __forceinline__ void scale_producer(const TcDev& d, const Range& R, S
       return pb >= 0 && pb < d.a.num_blocks ? pb : -1;
     };
     int cur = page_of(it.j0);
-    for (int j = it.j0; j < it.j1; j += 2) {
-      float s = cur >= 0 ? scale[size_t(cur) * d.a.H_kv + it.h] : 0.f;
-      const int next = page_of(j + 2);
-      const int n = min(2, it.j1 - j);
+    for (int j = it.j0; j < it.j1; j += 4) {
+      float ks = 0.f, vs = 0.f;
+      if (cur >= 0) {
+        ks = d.a.k_scale[size_t(cur) * d.a.H_kv + it.h];
+        vs = d.a.v_scale[size_t(cur) * d.a.H_kv + it.h];
+      }
+      cur = page_of(j + 4);
+      const int n = min(4, it.j1 - j);
       for (int u = 0; u < n; ++u) {
-        const int slot = (kt + u) % kScaleRing, use = (kt + u) / kScaleRing;
-        if (use > 0 && !lane0_wait(empty + slot, use - 1, abort_flag)) ok = false;
+        const int use = (kt + u) / kScaleRing;
+        if (use > 0 && !lane0_wait(empty + (kt + u) % kScaleRing, use - 1, abort_flag)) ok = false;
       }
       if (!ok) break;
       if (sub < n) {
         ScaleSlot* o = ring + (kt + sub) % kScaleRing;
-        if (!is_v) {
-          o->k[i] = s;
-        } else {
-          // a V scale of 0 (a block of zeros) must not make 0 * infinity
-          s = fmaxf(s, kMinVScale);
-          o->lv[i] = log2f(s);
-          o->iv[i] = 1.f / s;
-        }
+        // a V scale of 0 (a block of zeros) must not make 0 * infinity
+        vs = fmaxf(vs, kMinVScale);
+        o->k[i] = ks;
+        o->lv[i] = log2f(vs);
+        o->iv[i] = 1.f / vs;
       }
       __syncwarp();
-      if (lane == 0)
-        for (int u = 0; u < n; ++u) tc::mbar_arrive(full + (kt + u) % kScaleRing);
+      if (lane < n) tc::mbar_arrive(full + (kt + lane) % kScaleRing);
       kt += n;
-      cur = next;
     }
   }
   if (lane == 0 && !ok) *reinterpret_cast<volatile int*>(abort_flag) = 1;
@@ -416,34 +413,33 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool 
          (uint32_t(M >> 4) << 24);
 }
 
-// Reductions of 16 values a lane over the 32 lanes: every exchange halves what a lane holds, 16
-// shuffles instead of 80.  Lane l ends with the result of row row16(l) (l and l ^ 1 alike).
-__device__ __forceinline__ int row16(int lane) {
-  return ((lane >> 4) & 1) * 8 + ((lane >> 3) & 1) * 4 + ((lane >> 2) & 1) * 2 + ((lane >> 1) & 1);
+// Reductions of NR values a lane over the 32 lanes: each of the first exchanges halves what a lane
+// holds, about NR shuffles instead of 5 NR.  Lane l ends with the result of row red_row<NR>(l).
+template <int NR>
+__device__ __forceinline__ int red_row(int lane) {
+  int r = 0;
+#pragma unroll
+  for (int w = NR / 2, b = 16; w >= 1; w /= 2, b /= 2) r += (lane & b) ? w : 0;
+  return r;
 }
-template <bool kMax>
-__device__ __forceinline__ float reduce16(const float (&v)[16], int lane) {
+template <int NR, bool kMax>
+__device__ __forceinline__ float red_rows(const float (&v)[NR], int lane) {
   auto op = [](float x, float y) { return kMax ? fmaxf(x, y) : x + y; };
-  float a8[8], a4[4], a2[2], r;
-  const bool b4 = lane & 16, b3 = lane & 8, b2 = lane & 4, b1 = lane & 2;
+  float a[NR];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float keep = b4 ? v[i + 8] : v[i], send = b4 ? v[i] : v[i + 8];
-    a8[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, 16));
-  }
+  for (int i = 0; i < NR; ++i) a[i] = v[i];
+  int b = 16;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float keep = b3 ? a8[i + 4] : a8[i], send = b3 ? a8[i] : a8[i + 4];
-    a4[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, 8));
-  }
+  for (int w = NR / 2; w >= 1; w /= 2, b /= 2) {
+    const bool up = lane & b;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float keep = b2 ? a4[i + 2] : a4[i], send = b2 ? a4[i] : a4[i + 2];
-    a2[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, 4));
+    for (int i = 0; i < w; ++i) {
+      const float keep = up ? a[i + w] : a[i], send = up ? a[i] : a[i + w];
+      a[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, b));
+    }
   }
-  const float keep = b1 ? a2[1] : a2[0], send = b1 ? a2[0] : a2[1];
-  r = op(keep, __shfl_xor_sync(0xffffffffu, send, 2));
-  return op(r, __shfl_xor_sync(0xffffffffu, r, 1));
+  for (; b >= 1; b /= 2) a[0] = op(a[0], __shfl_xor_sync(0xffffffffu, a[0], b));
+  return a[0];
 }
 
 // OR of a predicate over the `n` threads of named barrier `id`
