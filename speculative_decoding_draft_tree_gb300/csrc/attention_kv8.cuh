@@ -29,7 +29,7 @@ enum class Kv8Live { yes, no, beyond_table };
 __device__ __forceinline__ Kv8Live kv8_live(const AttnKv8Dev& a, int r, int T, int P) {
   const int st = a.req_status[r] & ~(SPEC_REQ_BAD_BLOCK | SPEC_REQ_TIMEOUT);
   if (st != 0 || T < 1 || T > a.T_max || P < 0) return Kv8Live::no;
-  return ((long long)P + T + a.bs - 1) / a.bs <= a.max_blocks ? Kv8Live::yes : Kv8Live::beyond_table;
+  return (long long)P + T <= (long long)a.max_blocks * a.bs ? Kv8Live::yes : Kv8Live::beyond_table;
 }
 
 }  // namespace spec

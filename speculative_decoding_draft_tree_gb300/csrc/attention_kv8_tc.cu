@@ -10,7 +10,7 @@
 // its own, and a third warpgroup joins the two and writes a unit's rows while they go on with the
 // next one (accumulators are double-buffered by unit).
 // Warps: 0 copies K, 2 copies V, 1 issues the scores' products, 3 the output's, 4-7 and 8-11
-// softmax, 12-15 output, 16 brings the queries and splits them, 17 brings the scales.
+// softmax, 12-15 split the queries and write the output, 16 brings the scales, 17 walks the items.
 //
 // Scales: a score is code product * (K scale of the slot's page * the row's query scale); the V
 // scale joins the exponent, y = score + log2(V scale), and the weight 2^(y - ref) goes into the
@@ -69,6 +69,7 @@ struct Shared {
   int s32[2];
   uint32_t tmem;
   int abort;
+  ItemRing items;
 };
 template <int NR>
 constexpr int smem_bytes() {
@@ -106,46 +107,45 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
   Shared<NR>& sh = *reinterpret_cast<Shared<NR>*>(base + L::kSmemBar);
   const AttnKv8Dev& a = d.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_wait();
-  pdl_trigger();
-  const Range R = cta_range<kThreads>(d, sh.s64, sh.s32);
-  if (tid == 0) write_merge_record(d, R);
-  if (R.t0 >= R.t1) return;                  // uniform; nothing allocated yet
-  if (tid == 0) {
-    for (int b = 0; b < 2; ++b) {
-      tc::mbar_init(&sh.q_full[b], 1);
-      tc::mbar_init(&sh.q_empty[b], 9);      // the issuer's commit and the 8 softmax warps
-      for (int g = 0; g < 2; ++g) {
-        tc::mbar_init(&sh.s_full[g][b], 1);
-        tc::mbar_init(&sh.s_free[g][b], 4);
-        tc::mbar_init(&sh.p_full[g][b], 4);
-        tc::mbar_init(&sh.pv_done[g][b], 1);
-      }
-      tc::mbar_init(&sh.sum_full[b], 8);
-      tc::mbar_init(&sh.o_full[b], 1);
-      tc::mbar_init(&sh.o_free[b], 4);
-      tc::mbar_init(&sh.drain[b], 1);
-    }
-    for (int s = 0; s < kKStages; ++s) {
-      tc::mbar_init(&sh.k_full[s], 1);
-      tc::mbar_init(&sh.k_empty[s], 1);
-    }
-    for (int s = 0; s < kVStages; ++s) {
-      tc::mbar_init(&sh.v_full[s], 1);
-      tc::mbar_init(&sh.v_empty[s], 1);
-    }
-    for (int s = 0; s < kScaleRing; ++s) {
-      tc::mbar_init(&sh.sc_full[s], 1);
-      tc::mbar_init(&sh.sc_empty[s], 4);
-    }
-    sh.abort = 0;
-    tc::fence_mbar_init();
-  }
+  // what needs no input comes before the wait for the kernel before
   if (warp == 0) {
     tc::tmem_alloc(&sh.tmem, L::kTmemCols);
     tc::tmem_relinquish();
+    if (lane == 0) {
+      tc::prefetch_tensormap(&mK);
+      tc::prefetch_tensormap(&mKw);
+      tc::prefetch_tensormap(&mV);
+      tc::prefetch_tensormap(&mVw);
+    }
+  } else if (warp == 1) {
+    auto init = [&](uint64_t* bar, int n, int count) {
+      if (lane < n) tc::mbar_init(bar + lane, count);
+    };
+    init(sh.q_full, 2, 4);                   // the output warps
+    init(sh.q_empty, 2, 9);                  // the issuer's commit and the 8 softmax warps
+    init(sh.k_full, kKStages, 1);
+    init(sh.k_empty, kKStages, 1);
+    init(sh.v_full, kVStages, 1);
+    init(sh.v_empty, kVStages, 1);
+    init(&sh.s_full[0][0], 4, 1);
+    init(&sh.s_free[0][0], 4, 4);
+    init(&sh.p_full[0][0], 4, 4);
+    init(&sh.pv_done[0][0], 4, 1);
+    init(sh.sum_full, 2, 8);
+    init(sh.o_full, 2, 1);
+    init(sh.o_free, 2, 4);
+    init(sh.sc_full, kScaleRing, 1);
+    init(sh.sc_empty, kScaleRing, 4);
+    init(sh.drain, 2, 1);
+    init(sh.items.full, kItemRing, 1);
+    init(sh.items.empty, kItemRing, 17);     // warps 0-16
+    if (lane == 0) sh.abort = 0;
+    tc::fence_mbar_init();
   }
+  pdl_wait();
+  pdl_trigger();
   tc::tc_fence_before();
+  const Range R = cta_range<kThreads>(d, sh.s64, sh.s32);   // (its barriers order the set-up)
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = sh.tmem;
@@ -153,63 +153,18 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
 
   if (warp < 4 || warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtlRegs));
-    if (warp == 0) {
-      page_producer(d, R, &mK, &mKw, kKStages, sK, sh.k_full, sh.k_empty, true, &sh.abort);
-    } else if (warp == 2) {
-      page_producer(d, R, &mV, &mVw, kVStages, sV, sh.v_full, sh.v_empty, false, &sh.abort);
-    } else if (warp == 17) {
-      scale_producer(d, R, sh.sc, sh.sc_full, sh.sc_empty, &sh.abort);
+    if (warp == 0 || warp == 2) {
+      const bool k = warp == 0;
+      page_producer(d, sh.items, k ? &mK : &mV, k ? &mKw : &mVw, k ? kKStages : kVStages,
+                    k ? sK : sV, k ? sh.k_full : sh.v_full, k ? sh.k_empty : sh.v_empty, k,
+                    &sh.abort);
     } else if (warp == 16) {
-      // =================================================================== queries
-      // a row to each half warp; its scale brings its largest element into (224, 448]
-      const int c = lane & 15;
-      ItemIter iter;
-      iter.start(d, R);
-      Item it;
-      bool ok = true;
-      for (int li = 0; ok && iter.next(d, R, it); ++li) {
-        const int b = li & 1, use = li >> 1;
-        if (use > 0 && !lane0_wait(&sh.q_empty[b], use - 1, abort_flag)) {
-          ok = false;
-          break;
-        }
-        uint8_t* p = sQ + b * L::kPair;
-#pragma unroll 1
-        for (int k0 = 0; k0 < NR; k0 += 8) {       // four rows a lane in flight
-          uint4 w[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int n = k0 + 2 * k + (lane >> 4), t = n / a.G, g = n - t * a.G;
-            w[k] = make_uint4(0, 0, 0, 0);
-            if (t < it.T)
-              w[k] = __ldg(reinterpret_cast<const uint4*>(
-                         static_cast<const __nv_bfloat16*>(a.q) +
-                         (size_t(it.o + t) * a.H_q + it.h * a.G + g) * kD) + c);
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int n = k0 + 2 * k + (lane >> 4);
-            float f[8], m = 0.f;
-            elem<__nv_bfloat16>::unpack(w[k], f);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) m = fabsf(f[e]) <= FLT_MAX ? fmaxf(m, fabsf(f[e])) : m;
-#pragma unroll
-            for (int s = 8; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-            const float sq = kv8::need_scale(m);
-            uint2 hi, lo;
-            split_q8(w[k], __uint_as_float((254u << 23) - __float_as_uint(sq)), hi, lo);
-            const int off =
-                (n >> 3) * 1024 + (n & 7) * 128 + (((c >> 1) ^ (n & 7)) << 4) + (c & 1) * 8;
-            *reinterpret_cast<uint2*>(p + off) = hi;
-            *reinterpret_cast<uint2*>(p + L::kPiece + off) = lo;
-            if (c == 0) sh.qmul[b][n] = sq * a.scale_log2;
-          }
-        }
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sh.q_full[b]);
-      }
-      if (!ok && lane == 0) *abort_flag = 1;
+      scale_producer(d, sh.items, sh.sc, sh.sc_full, sh.sc_empty, &sh.abort);
+    } else if (warp == 17) {
+      if (lane == 0) item_producer(d, R, sh.items, abort_flag);
+      __syncwarp();
+    } else if (warp == 18) {
+      if (lane == 0) write_merge_record(d, R);
       __syncwarp();
     } else if (warp == 1 || warp == 3) {
       // =================================================================== MMA issuers
@@ -223,16 +178,23 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
         const uint64_t dV = tc::smem_desc(tc::smem_u32(sV), kTile, 1024);
         int kt = 0;                    // tiles so far; group = parity of the tile's number
         bool ok = true;
-        ItemIter iter;
-        iter.start(d, R);
-        Item it;
-        for (int li = 0; ok && iter.next(d, R, it); ++li) {
+#pragma unroll 1
+        for (int li = 0; ok; ++li) {
+          Item it;                     // (one lane: its own wait and arrival)
+          {
+            const int s = li % kItemRing;
+            ok = wait1(&sh.items.full[s], li / kItemRing, abort_flag);
+            it = sh.items.item[s];
+            tc::mbar_arrive(&sh.items.empty[s]);
+            if (!ok || it.r < 0) break;
+          }
           const int par = li & 1;
           if (is_qk ? !wait1(&sh.q_full[par], li >> 1, abort_flag)
                     : (li > 1 && !wait1(&sh.o_free[par], (li >> 1) - 1, abort_flag))) {
             ok = false;
             break;
           }
+#pragma unroll 1
           for (int j = it.j0; j < it.j1; ++j, ++kt) {
             const int g = kt & 1, b = (kt >> 1) & 1, use = kt >> 2;
             if (is_qk) {
@@ -294,10 +256,12 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
     const int chunk = kl >> 4;
     int kt = 0;
     bool ok = true;                                  // no early exit: see the file's comment
-    ItemIter iter;
-    iter.start(d, R);
     Item it;
-    for (int li = 0; iter.next(d, R, it); ++li) {
+#pragma unroll 1
+    for (int li = 0;; ++li) {
+      // the group leaves together: an expired wait in one warp must not leave the others at a
+      // barrier
+      if (bar_any(bar_g, 128, !next_item(sh.items, li, it, abort_flag))) break;
       const int par = li & 1;
       const int T = it.T, P = it.P, kv_len = P + T;
       const int nt = it.j1 - it.j0;
@@ -311,6 +275,7 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
         lsum[n] = 0.f;
       }
       bool fresh = true;                             // nothing accumulated in this unit yet
+#pragma unroll 1
       for (int i = (kt ^ grp) & 1; i < nt; i += 2, fresh = false) {
         const int kg = kt + i;                       // the tile's number in the CTA's stream
         const int b = (kg >> 1) & 1, use = kg >> 2;
@@ -337,8 +302,12 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
           if (key < kv_len) {
             const uint32_t* anc = a.anc + size_t(it.o) * a.W + ((key - P) >> 5);
             const int sh_ = (key - P) & 31;
-            for (int t = 0; t < T; ++t)
-              if ((__ldg(anc + t * a.W) >> sh_) & 1u) vis |= ((1u << a.G) - 1u) << (t * a.G);
+            uint32_t w[NR];
+#pragma unroll
+            for (int t = 0; t < NR; ++t) w[t] = t < T ? __ldg(anc + t * a.W) : 0u;
+#pragma unroll
+            for (int t = 0; t < NR; ++t)
+              if ((w[t] >> sh_) & 1u) vis |= ((1u << a.G) - 1u) << (t * a.G);
           }
         }
         float y[NR], zmax = -INFINITY;
@@ -441,20 +410,73 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
     }
     if (!ok) *abort_flag = 1;
   } else {
-    // ===================================================================== output
+    // ===================================================================== queries, output
+    // Queries two units ahead, then the output of the unit that is done.
     const int q = warp & 3;
     const uint32_t lane_addr = uint32_t(q * 32) << 16;
     const int col = q * 32 + lane;
     bool ok = true;
-    ItemIter iter;
-    iter.start(d, R);
-    Item it;
-    for (int li = 0; iter.next(d, R, it); ++li) {
+    struct Unit {
+      int o, T, h, slot;
+    };
+    auto fetch = [&](int li, Unit& u) -> bool {
+      Item it;
+      const bool has = __all_sync(0xffffffffu, next_item(sh.items, li, it, abort_flag));
+      u.o = it.o;
+      u.T = it.T;
+      u.h = it.h;
+      u.slot = it.slot;
+      return has;
+    };
+    // a row to each half warp, 16 bytes a lane; the row's scale brings its largest element into
+    // (224, 448]
+    auto put_q = [&](int li, const Unit& u) {
+      const int b = li & 1, c = lane & 15;
+      uint8_t* p = sQ + b * L::kPair;
+      if (li > 1) ok &= idle_wait(&sh.q_empty[b], (li >> 1) - 1, abort_flag);
+#pragma unroll 1
+      for (int n = q * 2 + (lane >> 4); n < NR; n += 8) {
+        const int t = n / a.G, g = n - t * a.G;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (t < u.T)
+          w = __ldg(reinterpret_cast<const uint4*>(
+                        static_cast<const __nv_bfloat16*>(a.q) +
+                        (size_t(u.o + t) * a.H_q + u.h * a.G + g) * kD) + c);
+        float f[8], m = 0.f;
+        elem<__nv_bfloat16>::unpack(w, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = fabsf(f[e]) <= FLT_MAX ? fmaxf(m, fabsf(f[e])) : m;
+#pragma unroll
+        for (int s = 8; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+        const float sq = kv8::need_scale(m);
+        uint2 hi, lo;
+        split_q8(w, __uint_as_float((254u << 23) - __float_as_uint(sq)), hi, lo);
+        const int off = (n >> 3) * 1024 + (n & 7) * 128 + (((c >> 1) ^ (n & 7)) << 4) + (c & 1) * 8;
+        *reinterpret_cast<uint2*>(p + off) = hi;
+        *reinterpret_cast<uint2*>(p + L::kPiece + off) = lo;
+        if (c == 0) sh.qmul[b][n] = sq * a.scale_log2;
+      }
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sh.q_full[b]);
+    };
+    Unit cur, next, after;
+    bool has = fetch(0, cur), has_next = false;
+    if (has) {
+      put_q(0, cur);
+      has_next = fetch(1, next);
+      if (has_next) put_q(1, next);
+    }
+#pragma unroll 1
+    for (int li = 0; has; ++li) {
+      const bool has_after = has_next && fetch(li + 2, after);
       const int par = li & 1;
-      const int nrows = it.T * a.G;                  // <= NR
-      ok &= wait1(&sh.sum_full[par], li >> 1, abort_flag);
-      // lane n: row n's weights of the two groups' accumulators and its log-sum-exp
-      const int rn = lane < NR ? lane : 0;
+      const int nrows = cur.T * a.G;                 // <= NR
+      ok &= idle_wait(&sh.sum_full[par], li >> 1, abort_flag);
+      // lane n: row n's place, the weights of the two groups' accumulators, its log-sum-exp
+      const int rn = lane < NR ? lane : 0, rt = rn / a.G;
+      const int row = cur.slot < 0 ? (cur.o + rt) * a.H_q + cur.h * a.G + (rn - rt * a.G)
+                                   : cur.slot * d.part_rows + rn;
       const float a0 = sh.add[par][0][rn], a1 = sh.add[par][1][rn];
       const float top = fminf(a0, a1);               // of the larger reference
       float w0 = a0 == INFINITY ? 0.f : ex2(top - a0);
@@ -470,40 +492,43 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
       const float lse2 = l > 0.f ? log2f(l) - top : -INFINITY;
       w0 *= inv;
       w1 *= inv;
-      ok &= wait1(&sh.o_full[par], li >> 1, abort_flag);
+      ok &= idle_wait(&sh.o_full[par], li >> 1, abort_flag);
       __syncwarp();
       tc::tc_fence_after();
-      uint32_t o0[kN], o1[kN];
-      tmem_ld<kN>(tmem + lane_addr + L::kTmemO + par * kN, o0);
-      tmem_ld<kN>(tmem + lane_addr + L::kTmemO + (2 + par) * kN, o1);
+      // (an accumulator that took no product in this unit has weight 0 and stale columns)
+      uint32_t ov[kN];
+      float v[NR];
+      tmem_ld<kN>(tmem + lane_addr + L::kTmemO + par * kN, ov);
+      tc::tmem_ld_wait();
+#pragma unroll
+      for (int n = 0; n < NR; ++n) {
+        const float u = __shfl_sync(0xffffffffu, w0, n);
+        v[n] = u > 0.f ? (__uint_as_float(ov[n]) + __uint_as_float(ov[n + NR])) * u : 0.f;
+      }
+      tmem_ld<kN>(tmem + lane_addr + L::kTmemO + (2 + par) * kN, ov);
       tc::tmem_ld_wait();
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sh.o_free[par]);
 #pragma unroll
       for (int n = 0; n < NR; ++n) {
-        const float u0 = __shfl_sync(0xffffffffu, w0, n), u1 = __shfl_sync(0xffffffffu, w1, n);
-        if (n >= nrows) continue;
-        // an accumulator that took no product in this unit has weight 0 and stale columns
-        float v = u0 > 0.f ? (__uint_as_float(o0[n]) + __uint_as_float(o0[n + NR])) * u0 : 0.f;
-        if (u1 > 0.f) v = fmaf(__uint_as_float(o1[n]) + __uint_as_float(o1[n + NR]), u1, v);
-        if (it.slot < 0) {
-          const int t = n / a.G;
-          const size_t row = size_t(it.o + t) * a.H_q + it.h * a.G + (n - t * a.G);
-          static_cast<__nv_bfloat16*>(a.o)[row * kD + col] = __float2bfloat16_rn(v);
-        } else {
-          d.part_o[(size_t(it.slot) * d.part_rows + n) * kD + col] = v;
+        const float u = __shfl_sync(0xffffffffu, w1, n);
+        if (u > 0.f) v[n] = fmaf(__uint_as_float(ov[n]) + __uint_as_float(ov[n + NR]), u, v[n]);
+        const size_t at = size_t(__shfl_sync(0xffffffffu, row, n)) * kD + col;
+        if (n < nrows) {
+          if (cur.slot < 0) static_cast<__nv_bfloat16*>(a.o)[at] = __float2bfloat16_rn(v[n]);
+          else d.part_o[at] = v[n];
         }
       }
       if (q == 0 && lane < nrows) {
-        if (it.slot >= 0) {
-          d.part_lse[size_t(it.slot) * d.part_rows + lane] = lse2;
-        } else if (a.lse) {
-          const int t = lane / a.G;
-          a.lse[size_t(it.o + t) * a.H_q + it.h * a.G + (lane - t * a.G)] =
-              lse2 * 0.6931471805599453f;
-        }
+        if (cur.slot >= 0) d.part_lse[row] = lse2;
+        else if (a.lse) a.lse[row] = lse2 * 0.6931471805599453f;
       }
+      if (has_after) put_q(li + 2, after);
+      cur = next;
+      next = after;
+      has = has_next;
+      has_next = has_after;
     }
     if (!ok) *abort_flag = 1;
   }
@@ -513,6 +538,7 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
     ItemIter iter;
     iter.start(d, R);
     Item it;
+#pragma unroll 1
     while (iter.next(d, R, it)) atomicOr(&a.req_status[it.r], SPEC_REQ_TIMEOUT);
   }
   tc::tc_fence_after();
@@ -533,6 +559,7 @@ __global__ void __launch_bounds__(256) attn_kv8_join_kernel(TcDev d) {
   const int t = rec.mt * d.tpt + m / a.G, g = m % a.G;
   if (m >= d.tpt * a.G || t >= rec.T) return;
   float M = -INFINITY, sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
   for (int p0 = 0; p0 < rec.np; p0 += 4) {
     float ls[4];
     float4 v[4];

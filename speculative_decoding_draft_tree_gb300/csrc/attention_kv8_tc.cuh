@@ -29,10 +29,11 @@ constexpr int kBN = 128;                          // slots of a K/V tile
 constexpr int kTile = kBN * kD;                   // bytes
 constexpr long long kWaitLimit = 4000000000LL;    // clock cycles (~2 s)
 constexpr int kMaxCtas = 1024;
-// Weights enter the products as 2^(y - ref + kShift); the reference moves when a y passes it by
-// more than 1, so that they stay below 2^(kShift + 1) = 256 <= 448 and a row's largest is at
-// least 2^(kShift - 1).
-constexpr float kShift = 7.f;
+// Weights enter the products as 2^(y - ref + kShift); the reference, a maximum seen before, moves
+// when a y passes it by more than 2, so that they stay below 2^8 <= 448 and a row's largest is at
+// least 2^kShift.  Two binades of slack: with one, the chains' units spent more on moving
+// references than on weights.
+constexpr float kShift = 6.f;
 constexpr float kCeil = 8.f;
 constexpr float kMinVScale = 7.888609052210118e-31f;   // 2^-100
 
@@ -67,18 +68,35 @@ __device__ __forceinline__ ReqGeom req_geom(const TcDev& d, int r) {
   return g;
 }
 
+// `total` tiles in C ranges, the first `rem` of them one tile longer than `quot`
+struct Cut {
+  long long quot;
+  int rem;
+};
 struct Range {
   long long total, t0, t1;   // tiles of the stream; this CTA's
   int C;                     // ranges
+  Cut cut;
   int r0, r1;                // requests holding tiles t0 and t1 - 1
   long long rbeg0, rbeg1;    // their first tiles
 };
-__device__ __forceinline__ long long range_start(long long total, int C, int c) {
-  return total * c / C;
+// quotient of a 64-bit count, which fits 32 bits but in absurd calls
+__device__ __noinline__ long long div64(long long n, long long m) { return n / m; }
+__device__ __forceinline__ long long div_count(long long n, long long m) {
+  return (n | m) >> 31 ? div64(n, m) : (long long)(uint32_t(n) / uint32_t(m));
 }
-__device__ __forceinline__ int range_of(long long t, long long total, int C) {
-  const long long c = ((t + 1) * C + total - 1) / total - 1;
-  return int(c < 0 ? 0 : (c >= C ? C - 1 : c));
+__device__ __forceinline__ Cut make_cut(long long total, int C) {
+  Cut k;
+  k.quot = div_count(total, C);
+  k.rem = int(total - k.quot * C);
+  return k;
+}
+__device__ __forceinline__ long long range_start(const Cut& k, int c) {
+  return k.quot * c + min(c, k.rem);
+}
+__device__ __forceinline__ int range_of(const Cut& k, long long t) {
+  const long long longer = (k.quot + 1) * k.rem;
+  return t < longer ? int(div_count(t, k.quot + 1)) : k.rem + int(div_count(t - longer, k.quot));
 }
 
 // Every thread computes the same Range.  s64: scratch of kThreads / 32 + 2 entries, s32 of two.
@@ -86,11 +104,19 @@ template <int kThreads>
 __device__ Range cta_range(const TcDev& d, long long* s64, int* s32) {
   constexpr int kW = kThreads / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  long long mine = 0;
-  for (int r = tid; r < d.a.B; r += kThreads) {
+  auto tiles_of = [&](int r) -> long long {
     const ReqGeom g = req_geom(d, r);
-    mine += (long long)g.units * g.nts;
-    if (blockIdx.x == 0 && kv8_live(d.a, r, g.T, g.P) == Kv8Live::beyond_table)
+    return (long long)g.units * g.nts;
+  };
+  long long mine = 0, first = 0;
+#pragma unroll 1
+  for (int r = tid; r < d.a.B; r += kThreads) {
+    const long long n = tiles_of(r);
+    if (r == tid) first = n;
+    mine += n;
+    if (blockIdx.x == 0 && n == 0 &&
+        kv8_live(d.a, r, d.a.node_offset[r + 1] - d.a.node_offset[r], d.a.prefix_len[r]) ==
+            Kv8Live::beyond_table)
       atomicOr(&d.a.req_status[r], SPEC_REQ_BAD_BLOCK);
   }
 #pragma unroll
@@ -103,23 +129,22 @@ __device__ Range cta_range(const TcDev& d, long long* s64, int* s32) {
   for (int w = 0; w < kW; ++w) total += s64[w];
   Range R;
   R.total = total;
-  R.C = int(max(1LL, min((long long)d.ctas, total / d.min_tiles)));
+  R.C = int(max(1LL, min((long long)d.ctas, div_count(total, d.min_tiles))));
+  R.cut = make_cut(total, R.C);
   R.t0 = R.t1 = 0;
   R.r0 = R.r1 = 0;
   R.rbeg0 = R.rbeg1 = 0;
   const int c = blockIdx.x;
   if (total == 0 || c >= R.C) return R;
-  R.t0 = range_start(total, R.C, c);
-  R.t1 = range_start(total, R.C, c + 1);
+  R.t0 = range_start(R.cut, c);
+  R.t1 = range_start(R.cut, c + 1);
   long long base = 0;
+#pragma unroll 1
   for (int r00 = 0; r00 < d.a.B; r00 += kThreads) {
     __syncthreads();
     const int r = r00 + tid;
-    long long tiles = 0;
-    if (r < d.a.B) {
-      const ReqGeom g = req_geom(d, r);
-      tiles = (long long)g.units * g.nts;
-    }
+    long long tiles = r00 == 0 ? first : 0;
+    if (r00 > 0 && r < d.a.B) tiles = tiles_of(r);
     long long incl = tiles;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -178,6 +203,7 @@ struct ItemIter {
   }
   __device__ __forceinline__ bool next(const TcDev& d, const Range& R, Item& it) {
     if (t >= R.t1) return false;
+#pragma unroll 1
     while (t >= rend) {
       if (r + 1 >= d.a.B) return false;
       ++r;
@@ -186,7 +212,7 @@ struct ItemIter {
       rend = rbeg + (long long)g.units * g.nts;
     }
     const long long off = t - rbeg;
-    const int u = int(off / g.nts);
+    const int u = int(div_count(off, g.nts));
     it.r = r;
     it.h = u / g.mts;
     it.mt = u - it.h * g.mts;
@@ -202,6 +228,16 @@ struct ItemIter {
   }
 };
 
+// One lane walks the range and hands the items to the other roles through a ring in shared memory,
+// so that the loads and divisions of the walk are done once and ahead of time (each role walking
+// for itself made the kernel 137 KB of instructions, more than the instruction cache holds: every
+// unit began with a few microseconds of misses).  r < 0 ends the stream.
+constexpr int kItemRing = 4;
+struct ItemRing {
+  uint64_t full[kItemRing], empty[kItemRing];
+  Item item[kItemRing];
+};
+
 // Thread 0 of CTA c: the record of the unit holding the range's last tile, if it starts in this
 // range and continues past it.  Piece p > 0 starts range ca + p and lies in slot 2 (ca + p).
 __device__ __forceinline__ void write_merge_record(const TcDev& d, const Range& R) {
@@ -209,11 +245,11 @@ __device__ __forceinline__ void write_merge_record(const TcDev& d, const Range& 
   rec.np = rec.h = rec.mt = rec.o = rec.T = rec.ca = rec.slot0 = 0;
   if (R.t0 < R.t1) {
     const ReqGeom g = req_geom(d, R.r1);
-    const int u = int((R.t1 - 1 - R.rbeg1) / g.nts);
+    const int u = int(div_count(R.t1 - 1 - R.rbeg1, g.nts));
     const long long ubeg = R.rbeg1 + (long long)u * g.nts;
     if (ubeg >= R.t0 && ubeg + g.nts > R.t1) {
       rec.ca = int(blockIdx.x);
-      rec.np = range_of(ubeg + g.nts - 1, R.total, R.C) - rec.ca + 1;
+      rec.np = range_of(R.cut, ubeg + g.nts - 1) - rec.ca + 1;
       rec.h = u / g.mts;
       rec.mt = u - rec.h * g.mts;
       rec.o = g.o;
@@ -228,15 +264,54 @@ __device__ __forceinline__ void write_merge_record(const TcDev& d, const Range& 
 __device__ __forceinline__ bool wait1(uint64_t* bar, int parity, volatile int* abort) {
   return tc::mbar_wait(bar, uint32_t(parity & 1), abort, kWaitLimit);
 }
-// all lanes wait; the outcome is the warp's
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, int parity, volatile int* abort) {
-  return __all_sync(0xffffffffu, wait1(bar, parity, abort));
+// The same for roles that run ahead of or behind the tiles: they look again every ~100 ns and
+// leave the shared-memory pipe to the warps on the critical path.
+__device__ __forceinline__ bool idle_wait(uint64_t* bar, int parity, volatile int* abort) {
+  if (tc::mbar_try_wait(bar, uint32_t(parity & 1))) return true;
+  const long long t0 = clock64();
+#pragma unroll 1
+  while (true) {
+    if (tc::mbar_try_wait(bar, uint32_t(parity & 1))) return true;
+    if (*abort || clock64() - t0 > kWaitLimit) return false;
+    __nanosleep(100);
+  }
 }
 // one lane waits, the warp gets the outcome
+template <bool kIdle>
 __device__ __forceinline__ bool lane0_wait(uint64_t* bar, int parity, volatile int* abort) {
   bool r = true;
-  if ((threadIdx.x & 31) == 0) r = wait1(bar, parity, abort);
+  if ((threadIdx.x & 31) == 0)
+    r = kIdle ? idle_wait(bar, parity, abort) : wait1(bar, parity, abort);
   return __shfl_sync(0xffffffffu, r ? 1 : 0, 0) != 0;
+}
+
+// ------------------------------------------------------------------------------ items
+// the walking lane
+__device__ __forceinline__ void item_producer(const TcDev& d, const Range& R, ItemRing& ring,
+                                              volatile int* abort) {
+  ItemIter iter;
+  iter.start(d, R);
+  Item it;
+  bool more = true;
+#pragma unroll 1
+  for (int li = 0; more; ++li) {
+    more = iter.next(d, R, it);
+    if (!more) it.r = -1;
+    const int s = li % kItemRing;
+    if (li >= kItemRing && !idle_wait(&ring.empty[s], li / kItemRing - 1, abort)) return;
+    ring.item[s] = it;
+    tc::mbar_arrive(&ring.full[s]);
+  }
+}
+// The li-th item, for every lane of a warp; false at the end of the stream or on an expired wait.
+// `arrivals` of the ring's empty barrier: one a warp.
+__device__ __forceinline__ bool next_item(ItemRing& ring, int li, Item& it, volatile int* abort) {
+  const int s = li % kItemRing;
+  const bool ok = wait1(&ring.full[s], li / kItemRing, abort);
+  it = ring.item[s];
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) tc::mbar_arrive(&ring.empty[s]);
+  return ok && it.r >= 0;
 }
 
 // ------------------------------------------------------------------------------ page copies
@@ -244,7 +319,7 @@ __device__ __forceinline__ bool lane0_wait(uint64_t* bar, int parity, volatile i
 // 128 / bs hold the tile's page ids, fetched a tile ahead; consecutive pages come as one 16 KB
 // box, others as a box each.  Pages past the request or with a bad id are read from a row past
 // the cache, which TMA fills with zeros.  Every copy issued is waited for before return.
-__device__ __forceinline__ void page_producer(const TcDev& d, const Range& R,
+__device__ __forceinline__ void page_producer(const TcDev& d, ItemRing& items,
                                               const CUtensorMap* map, const CUtensorMap* wide,
                                               int nstage, uint8_t* ring, uint64_t* full,
                                               uint64_t* empty, bool flag_bad, int* abort_flag) {
@@ -252,10 +327,9 @@ __device__ __forceinline__ void page_producer(const TcDev& d, const Range& R,
   const int bs = d.a.bs, ppt = kBN >> d.log2bs, page_bytes = bs * kD;
   int kt = 0;
   bool ok = true;
-  ItemIter iter;
-  iter.start(d, R);
   Item it;
-  while (ok && iter.next(d, R, it)) {
+#pragma unroll 1
+  for (int li = 0; ok && __all_sync(0xffffffffu, next_item(items, li, it, abort_flag)); ++li) {
     const int nblk = (it.P + it.T + bs - 1) >> d.log2bs;
     const int32_t* table = d.a.block_table + size_t(it.r) * d.a.max_blocks;
     auto page_of = [&](int j) -> int {
@@ -271,10 +345,11 @@ __device__ __forceinline__ void page_producer(const TcDev& d, const Range& R,
       return pb;
     };
     int cur = page_of(it.j0);
+#pragma unroll 1
     for (int j = it.j0; j < it.j1; ++j, ++kt) {
       const int next = j + 1 < it.j1 ? page_of(j + 1) : -1;
       const int st = kt % nstage, use = kt / nstage;
-      if (use > 0 && !lane0_wait(empty + st, use - 1, abort_flag)) {
+      if (use > 0 && !lane0_wait<false>(empty + st, use - 1, abort_flag)) {
         ok = false;
         break;
       }
@@ -295,6 +370,7 @@ __device__ __forceinline__ void page_producer(const TcDev& d, const Range& R,
   }
   if (lane == 0) {
     if (!ok) *reinterpret_cast<volatile int*>(abort_flag) = 1;
+#pragma unroll 1
     for (int k = max(0, kt - nstage); k < kt; ++k)
       tc::mbar_wait(full + k % nstage, (k / nstage) & 1, abort_flag, kWaitLimit / 8);
   }
@@ -308,16 +384,15 @@ struct ScaleSlot {
   float k[8], lv[8], iv[8];
 };
 constexpr int kScaleRing = 16;
-__device__ __forceinline__ void scale_producer(const TcDev& d, const Range& R, ScaleSlot* ring,
+__device__ __forceinline__ void scale_producer(const TcDev& d, ItemRing& items, ScaleSlot* ring,
                                                uint64_t* full, uint64_t* empty, int* abort_flag) {
   const int lane = threadIdx.x & 31;
   const int ppt = kBN >> d.log2bs, i = lane & 7, sub = lane >> 3;
   int kt = 0;
   bool ok = true;
-  ItemIter iter;
-  iter.start(d, R);
   Item it;
-  while (ok && iter.next(d, R, it)) {
+#pragma unroll 1
+  for (int li = 0; ok && __all_sync(0xffffffffu, next_item(items, li, it, abort_flag)); ++li) {
     const int nblk = (it.P + it.T + d.a.bs - 1) >> d.log2bs;
     const int32_t* table = d.a.block_table + size_t(it.r) * d.a.max_blocks;
     auto page_of = [&](int j) -> int {
@@ -326,18 +401,28 @@ __device__ __forceinline__ void scale_producer(const TcDev& d, const Range& R, S
       if (i < ppt && j + sub < it.j1 && lb < nblk) pb = table[lb];
       return pb >= 0 && pb < d.a.num_blocks ? pb : -1;
     };
-    int cur = page_of(it.j0);
-    for (int j = it.j0; j < it.j1; j += 4) {
-      float ks = 0.f, vs = 0.f;
-      if (cur >= 0) {
-        ks = d.a.k_scale[size_t(cur) * d.a.H_kv + it.h];
-        vs = d.a.v_scale[size_t(cur) * d.a.H_kv + it.h];
+    // the scales of the four tiles ahead and the page ids of the four after those are in flight
+    float ks_n, vs_n;
+    auto scales_of = [&](int pb) {
+      ks_n = vs_n = 0.f;
+      if (pb >= 0) {
+        ks_n = d.a.k_scale[size_t(pb) * d.a.H_kv + it.h];
+        vs_n = d.a.v_scale[size_t(pb) * d.a.H_kv + it.h];
       }
-      cur = page_of(j + 4);
+    };
+    scales_of(page_of(it.j0));
+    int ahead = page_of(it.j0 + 4);
+#pragma unroll 1
+    for (int j = it.j0; j < it.j1; j += 4) {
+      const float ks = ks_n;
+      float vs = vs_n;
+      scales_of(ahead);
+      ahead = page_of(j + 8);
       const int n = min(4, it.j1 - j);
+#pragma unroll 1
       for (int u = 0; u < n; ++u) {
         const int use = (kt + u) / kScaleRing;
-        if (use > 0 && !lane0_wait(empty + (kt + u) % kScaleRing, use - 1, abort_flag)) ok = false;
+        if (use > 0 && !lane0_wait<true>(empty + (kt + u) % kScaleRing, use - 1, abort_flag)) ok = false;
       }
       if (!ok) break;
       if (sub < n) {
@@ -438,6 +523,7 @@ __device__ __forceinline__ float red_rows(const float (&v)[NR], int lane) {
       a[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, b));
     }
   }
+#pragma unroll 1
   for (; b >= 1; b /= 2) a[0] = op(a[0], __shfl_xor_sync(0xffffffffu, a[0], b));
   return a[0];
 }
