@@ -65,10 +65,8 @@ struct Shared {
   float mx[2][4][NR];             // per group and warp: row maxima of an update
   float sum[2][2][4][NR];         // per unit parity, group and warp: row sums
   float add[2][2][NR];            // per unit parity and group: kShift - reference
-  long long s64[kThreads / 32 + 2];
-  int s32[2];
   uint32_t tmem;
-  int abort;
+  int abort, r0, r1;              // r0 .. r1: the requests of the range
   ItemRing items;
 };
 template <int NR>
@@ -142,11 +140,10 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
     if (lane == 0) sh.abort = 0;
     tc::fence_mbar_init();
   }
+  tc::tc_fence_before();
+  __syncthreads();
   pdl_wait();
   pdl_trigger();
-  tc::tc_fence_before();
-  const Range R = cta_range<kThreads>(d, sh.s64, sh.s32);   // (its barriers order the set-up)
-  __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = sh.tmem;
   volatile int* abort_flag = &sh.abort;
@@ -161,10 +158,13 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
     } else if (warp == 16) {
       scale_producer(d, sh.items, sh.sc, sh.sc_full, sh.sc_empty, &sh.abort);
     } else if (warp == 17) {
-      if (lane == 0) item_producer(d, R, sh.items, abort_flag);
-      __syncwarp();
-    } else if (warp == 18) {
-      if (lane == 0) write_merge_record(d, R);
+      const Range R = warp_range(d);
+      if (lane == 0) {
+        sh.r0 = R.r0;
+        sh.r1 = R.t0 < R.t1 ? R.r1 : -1;
+        item_producer(d, R, sh.items, abort_flag);
+        write_merge_record(d, R);
+      }
       __syncwarp();
     } else if (warp == 1 || warp == 3) {
       // =================================================================== MMA issuers
@@ -534,13 +534,9 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
   }
   tc::tc_fence_before();
   __syncthreads();
-  if (*abort_flag && tid == 0) {
-    ItemIter iter;
-    iter.start(d, R);
-    Item it;
+  if (*abort_flag)                           // every request of the range is unreliable
 #pragma unroll 1
-    while (iter.next(d, R, it)) atomicOr(&a.req_status[it.r], SPEC_REQ_TIMEOUT);
-  }
+    for (int r = sh.r0 + tid; r <= sh.r1; r += kThreads) atomicOr(&a.req_status[r], SPEC_REQ_TIMEOUT);
   tc::tc_fence_after();
   if (warp == 0) tc::tmem_dealloc(tmem, L::kTmemCols);
 }

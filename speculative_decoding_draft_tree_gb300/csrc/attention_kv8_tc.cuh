@@ -99,34 +99,28 @@ __device__ __forceinline__ int range_of(const Cut& k, long long t) {
   return t < longer ? int(div_count(t, k.quot + 1)) : k.rem + int(div_count(t - longer, k.quot));
 }
 
-// Every thread computes the same Range.  s64: scratch of kThreads / 32 + 2 entries, s32 of two.
-template <int kThreads>
-__device__ Range cta_range(const TcDev& d, long long* s64, int* s32) {
-  constexpr int kW = kThreads / 32;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// The walking warp's range (every lane gets it): pass 1 sums the requests' tiles, pass 2 scans them
+// for the requests that hold the range's ends.  The first kHeld requests' counts stay in registers.
+__device__ __forceinline__ Range warp_range(const TcDev& d) {
+  constexpr int kHeld = 2;           // chunks of 32 requests
+  const int lane = threadIdx.x & 31;
   auto tiles_of = [&](int r) -> long long {
+    if (r >= d.a.B) return 0;
     const ReqGeom g = req_geom(d, r);
+    if (blockIdx.x == 0 && g.units == 0 && kv8_live(d.a, r, g.T, g.P) == Kv8Live::beyond_table)
+      atomicOr(&d.a.req_status[r], SPEC_REQ_BAD_BLOCK);
     return (long long)g.units * g.nts;
   };
-  long long mine = 0, first = 0;
-#pragma unroll 1
-  for (int r = tid; r < d.a.B; r += kThreads) {
-    const long long n = tiles_of(r);
-    if (r == tid) first = n;
-    mine += n;
-    if (blockIdx.x == 0 && n == 0 &&
-        kv8_live(d.a, r, d.a.node_offset[r + 1] - d.a.node_offset[r], d.a.prefix_len[r]) ==
-            Kv8Live::beyond_table)
-      atomicOr(&d.a.req_status[r], SPEC_REQ_BAD_BLOCK);
+  long long held[kHeld], total = 0;
+#pragma unroll
+  for (int c = 0; c < kHeld; ++c) {
+    held[c] = tiles_of(c * 32 + lane);
+    total += held[c];
   }
+#pragma unroll 2
+  for (int r = kHeld * 32 + lane; r < d.a.B; r += 32) total += tiles_of(r);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) s64[warp] = mine;
-  if (tid < 2) s32[tid] = -1;
-  __syncthreads();
-  long long total = 0;
-#pragma unroll
-  for (int w = 0; w < kW; ++w) total += s64[w];
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   Range R;
   R.total = total;
   R.C = int(max(1LL, min((long long)d.ctas, div_count(total, d.min_tiles))));
@@ -134,51 +128,38 @@ __device__ Range cta_range(const TcDev& d, long long* s64, int* s32) {
   R.t0 = R.t1 = 0;
   R.r0 = R.r1 = 0;
   R.rbeg0 = R.rbeg1 = 0;
-  const int c = blockIdx.x;
-  if (total == 0 || c >= R.C) return R;
-  R.t0 = range_start(R.cut, c);
-  R.t1 = range_start(R.cut, c + 1);
+  if (total == 0 || int(blockIdx.x) >= R.C) return R;
+  R.t0 = range_start(R.cut, blockIdx.x);
+  R.t1 = range_start(R.cut, blockIdx.x + 1);
   long long base = 0;
 #pragma unroll 1
-  for (int r00 = 0; r00 < d.a.B; r00 += kThreads) {
-    __syncthreads();
-    const int r = r00 + tid;
-    long long tiles = r00 == 0 ? first : 0;
-    if (r00 > 0 && r < d.a.B) tiles = tiles_of(r);
-    long long incl = tiles;
+  for (int c = 0; c * 32 < d.a.B; ++c) {
+    const int r = c * 32 + lane;
+    long long n = 0;
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) n = c == k ? held[k] : n;
+    if (c >= kHeld) n = tiles_of(r);
+    long long hi = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += x;
+      const long long x = __shfl_up_sync(0xffffffffu, hi, o);
+      if (lane >= o) hi += x;
     }
-    if (lane == 31) s64[warp] = incl;
-    __syncthreads();
-    long long before = 0, chunk = 0;
-#pragma unroll
-    for (int w = 0; w < kW; ++w) {
-      if (w < warp) before += s64[w];
-      chunk += s64[w];
+    hi += base;
+    const long long lo = hi - n;
+    const uint32_t m0 = __ballot_sync(0xffffffffu, n > 0 && lo <= R.t0 && R.t0 < hi);
+    const uint32_t m1 = __ballot_sync(0xffffffffu, n > 0 && lo <= R.t1 - 1 && R.t1 - 1 < hi);
+    if (m0) {
+      R.r0 = c * 32 + __ffs(m0) - 1;
+      R.rbeg0 = __shfl_sync(0xffffffffu, lo, __ffs(m0) - 1);
     }
-    const long long hi = base + before + incl, lo = hi - tiles;
-    const bool found = base + chunk > R.t1 - 1;
-    if (tiles > 0 && lo <= R.t0 && R.t0 < hi) {
-      s32[0] = r;
-      s64[kW] = lo;
+    if (m1) {
+      R.r1 = c * 32 + __ffs(m1) - 1;
+      R.rbeg1 = __shfl_sync(0xffffffffu, lo, __ffs(m1) - 1);
+      break;
     }
-    if (tiles > 0 && lo <= R.t1 - 1 && R.t1 - 1 < hi) {
-      s32[1] = r;
-      s64[kW + 1] = lo;
-    }
-    base += chunk;
-    if (found) break;
+    base = __shfl_sync(0xffffffffu, hi, 31);
   }
-  __syncthreads();
-  R.r0 = s32[0];
-  R.rbeg0 = s64[kW];
-  R.r1 = s32[1];
-  R.rbeg1 = s64[kW + 1];
-  // both are always found; anything else would index out of bounds: no work
-  if (R.r0 < 0 || R.r0 >= d.a.B || R.r1 < R.r0 || R.r1 >= d.a.B) R.t0 = R.t1 = 0;
   return R;
 }
 
@@ -238,7 +219,7 @@ struct ItemRing {
   Item item[kItemRing];
 };
 
-// Thread 0 of CTA c: the record of the unit holding the range's last tile, if it starts in this
+// One lane of CTA c: the record of the unit holding the range's last tile, if it starts in this
 // range and continues past it.  Piece p > 0 starts range ca + p and lies in slot 2 (ca + p).
 __device__ __forceinline__ void write_merge_record(const TcDev& d, const Range& R) {
   MergeRec rec;
@@ -325,54 +306,59 @@ __device__ __forceinline__ void page_producer(const TcDev& d, ItemRing& items,
                                               uint64_t* empty, bool flag_bad, int* abort_flag) {
   const int lane = threadIdx.x & 31;
   const int bs = d.a.bs, ppt = kBN >> d.log2bs, page_bytes = bs * kD;
-  int kt = 0;
+  int st = 0, use = 0, issued = 0;         // the stage and how often the ring has gone round
   bool ok = true;
   Item it;
 #pragma unroll 1
   for (int li = 0; ok && __all_sync(0xffffffffu, next_item(items, li, it, abort_flag)); ++li) {
     const int nblk = (it.P + it.T + bs - 1) >> d.log2bs;
     const int32_t* table = d.a.block_table + size_t(it.r) * d.a.max_blocks;
-    auto page_of = [&](int j) -> int {
-      int pb = -1;
+    auto page_of = [&](int j) -> int {     // -1: past the request or the item
       const int lb = j * ppt + lane;
-      if (lane < ppt && lb < nblk) {
-        pb = table[lb];
-        if (pb < 0 || pb >= d.a.num_blocks) {
-          if (flag_bad) atomicOr(&d.a.req_status[it.r], SPEC_REQ_BAD_BLOCK);
-          pb = -2;
-        }
-      }
-      return pb;
+      return lane < ppt && j < it.j1 && lb < nblk ? __ldg(table + lb) : -1;
     };
-    int cur = page_of(it.j0);
+    int cur = page_of(it.j0), next = page_of(it.j0 + 1);
 #pragma unroll 1
-    for (int j = it.j0; j < it.j1; ++j, ++kt) {
-      const int next = j + 1 < it.j1 ? page_of(j + 1) : -1;
-      const int st = kt % nstage, use = kt / nstage;
+    for (int j = it.j0; j < it.j1; ++j) {
+      const int after = page_of(j + 2);
       if (use > 0 && !lane0_wait<false>(empty + st, use - 1, abort_flag)) {
         ok = false;
         break;
       }
+      const bool good = cur >= 0 && cur < d.a.num_blocks;
+      if (flag_bad && !good && lane < ppt && j * ppt + lane < nblk)
+        atomicOr(&d.a.req_status[it.r], SPEC_REQ_BAD_BLOCK);
       const int first = __shfl_sync(0xffffffffu, cur, 0);
-      const bool run = __all_sync(0xffffffffu, lane >= ppt || cur == first + lane) && first >= 0;
+      const bool run = __all_sync(0xffffffffu, lane >= ppt || (good && cur == first + lane));
       if (lane == 0) tc::mbar_arrive_expect_tx(full + st, kTile);
       __syncwarp();
       uint8_t* dst = ring + st * kTile;
       if (run) {
         if (lane == 0) tc::tma_load_4d(dst, wide, 0, 0, it.h, first, full + st);
       } else if (lane < ppt) {
-        const int row = cur >= 0 ? (cur * d.a.H_kv + it.h) * bs : d.kv_rows;
+        const int row = good ? (cur * d.a.H_kv + it.h) * bs : d.kv_rows;
         tc::tma_load_2d(dst + lane * page_bytes, map, 0, row, full + st);
       }
       __syncwarp();
       cur = next;
+      next = after;
+      ++issued;
+      if (++st == nstage) {
+        st = 0;
+        ++use;
+      }
     }
   }
   if (lane == 0) {
     if (!ok) *reinterpret_cast<volatile int*>(abort_flag) = 1;
+    // the copies of the last round: `st` and after belong to the round before
+    const int n = min(issued, nstage);
 #pragma unroll 1
-    for (int k = max(0, kt - nstage); k < kt; ++k)
-      tc::mbar_wait(full + k % nstage, (k / nstage) & 1, abort_flag, kWaitLimit / 8);
+    for (int k = 1; k <= n; ++k) {
+      const int s = st - k < 0 ? st - k + nstage : st - k;
+      const int u = st - k < 0 ? use - 1 : use;
+      tc::mbar_wait(full + s, u & 1, abort_flag, kWaitLimit / 8);
+    }
   }
   __syncwarp();
 }
