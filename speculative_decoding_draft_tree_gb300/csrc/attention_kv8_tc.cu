@@ -12,6 +12,14 @@
 // Warps: 0 copies K, 2 copies V, 1 issues the scores' products, 3 the output's, 4-7 and 8-11
 // softmax, 12-15 split the queries and write the output, 16 brings the scales, 17 walks the items.
 //
+// attn_kv8_tile_kernel: longer units in tiles of 128 query rows (G heads x 128 / G tree tokens).
+// S = Q K^T (M = N = 128, both pieces of Q into one accumulator), P's pieces written to TMEM as the
+// A operand of O += P V.  S and P are double-buffered, so the next tile's scores and the last
+// one's output are formed while the softmax works; TMEM columns: S 0-255, O 256-383, P 384-511.
+// One query row a thread pair: warps q + 4 and q + 8 take 64 of a tile's keys each, agree on the
+// row's reference at a barrier of the two, and keep a sum each.  Bound by the tensor core (1024
+// clocks a tile at the e4m3 rate) and the softmax's issue slots about equally.
+//
 // Scales: a score is code product * (K scale of the slot's page * the row's query scale); the V
 // scale joins the exponent, y = score + log2(V scale), and the weight 2^(y - ref) goes into the
 // product with V's codes while the row sum takes 2^(y - ref) / (V scale).  So the weights that
@@ -541,6 +549,505 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
   if (warp == 0) tc::tmem_dealloc(tmem, L::kTmemCols);
 }
 
+// ------------------------------------------------------------------------------ long units
+namespace tile {
+constexpr int kRows = 128;
+constexpr int kThreads = 640;
+constexpr int kCtlRegs = 72;       // as in rows::
+constexpr int kSoftmaxRegs = 120;
+constexpr int kKStages = 4;
+constexpr int kVStages = 4;
+constexpr int kPair = 2 * kTile;                         // Q's two pieces
+constexpr int kSmemQ = 0;                                // 2 buffers
+constexpr int kSmemK = kSmemQ + 2 * kPair;
+constexpr int kSmemV = kSmemK + kKStages * kTile;
+constexpr int kSmemBar = kSmemV + kVStages * kTile;
+constexpr uint32_t kTmemO = 256, kTmemP = 384;
+
+struct Shared {
+  uint64_t q_full[2], q_empty[2];
+  uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
+  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
+  uint64_t sum_full[2], sum_free[2], o_full, o_free;
+  uint64_t sc_full[kScaleRing], sc_empty[kScaleRing], drain[2];
+  ScaleSlot sc[kScaleRing];
+  float qmul[2][kRows];
+  float mx[2][kRows];             // per half: row maxima of an update
+  float sum[2][2][kRows];         // per unit parity and half
+  float add[2][kRows];            // per unit parity: kShift - reference
+  uint32_t tmem;
+  int abort, r0, r1;
+  ItemRing items;
+};
+constexpr int kSmemBytes = kSmemBar + int(sizeof(Shared)) + 1024;
+static_assert(kSmemBytes <= 232448, "fits one CTA's shared memory");
+}  // namespace tile
+
+// 32 ancestor bits of a row's words from tree index `pos` on (0 outside the row)
+__device__ __forceinline__ uint32_t anc_window(const uint32_t* row, int W, int pos) {
+  if (row == nullptr || pos <= -32 || pos >= 32 * W) return 0u;
+  const int wi = pos >> 5, sh = pos & 31;                // wi >= -1
+  const uint32_t lo = wi >= 0 ? __ldg(row + wi) : 0u;
+  const uint32_t hi = wi + 1 < W ? __ldg(row + wi + 1) : 0u;
+  return __funnelshift_r(lo, hi, sh);
+}
+
+__global__ void __launch_bounds__(tile::kThreads, 1)
+attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
+                     const __grid_constant__ CUtensorMap mKw,
+                     const __grid_constant__ CUtensorMap mVw, TcDev d) {
+  using namespace tile;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint8_t* sQ = base + kSmemQ;
+  uint8_t* sK = base + kSmemK;
+  uint8_t* sV = base + kSmemV;
+  Shared& sh = *reinterpret_cast<Shared*>(base + kSmemBar);
+  const AttnKv8Dev& a = d.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (warp == 0) {
+    tc::tmem_alloc(&sh.tmem, 512);
+    tc::tmem_relinquish();
+    if (lane == 0) {
+      tc::prefetch_tensormap(&mK);
+      tc::prefetch_tensormap(&mKw);
+      tc::prefetch_tensormap(&mV);
+      tc::prefetch_tensormap(&mVw);
+    }
+  } else if (warp == 1) {
+    auto init = [&](uint64_t* bar, int n, int count) {
+      if (lane < n) tc::mbar_init(bar + lane, count);
+    };
+    init(sh.q_full, 2, 4);                   // the output warps
+    init(sh.q_empty, 2, 9);                  // the issuer's commit and the 8 softmax warps
+    init(sh.k_full, kKStages, 1);
+    init(sh.k_empty, kKStages, 1);
+    init(sh.v_full, kVStages, 1);
+    init(sh.v_empty, kVStages, 1);
+    init(sh.s_full, 2, 1);
+    init(sh.s_free, 2, 8);
+    init(sh.p_full, 2, 8);
+    init(sh.pv_done, 2, 1);
+    init(sh.sum_full, 2, 8);
+    init(sh.sum_free, 2, 4);
+    init(&sh.o_full, 1, 1);
+    init(&sh.o_free, 1, 4);
+    init(sh.sc_full, kScaleRing, 1);
+    init(sh.sc_empty, kScaleRing, 8);
+    init(sh.drain, 2, 1);
+    init(sh.items.full, kItemRing, 1);
+    init(sh.items.empty, kItemRing, 17);     // warps 0-16
+    if (lane == 0) sh.abort = 0;
+    tc::fence_mbar_init();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+  tc::tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  volatile int* abort_flag = &sh.abort;
+
+  if (warp < 4 || warp >= 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtlRegs));
+    if (warp == 0 || warp == 2) {
+      const bool k = warp == 0;
+      page_producer(d, sh.items, k ? &mK : &mV, k ? &mKw : &mVw, k ? kKStages : kVStages,
+                    k ? sK : sV, k ? sh.k_full : sh.v_full, k ? sh.k_empty : sh.v_empty, k,
+                    &sh.abort);
+    } else if (warp == 16) {
+      scale_producer(d, sh.items, sh.sc, sh.sc_full, sh.sc_empty, &sh.abort);
+    } else if (warp == 17) {
+      const Range R = warp_range(d);
+      if (lane == 0) {
+        sh.r0 = R.r0;
+        sh.r1 = R.t0 < R.t1 ? R.r1 : -1;
+        item_producer(d, R, sh.items, abort_flag);
+        write_merge_record(d, R);
+      }
+      __syncwarp();
+    } else if (warp == 1 || warp == 3) {
+      // =================================================================== MMA issuers
+      if (lane == 0) {
+        const bool is_qk = warp == 1;
+        const uint32_t id_qk = idesc_e4m3(128, 128, false, false);
+        const uint32_t id_pv = idesc_e4m3(128, 128, false, true);
+        const uint64_t dQ = tc::smem_desc(tc::smem_u32(sQ), 16, 1024);
+        const uint64_t dK = tc::smem_desc(tc::smem_u32(sK), 16, 1024);
+        const uint64_t dV = tc::smem_desc(tc::smem_u32(sV), kTile, 1024);
+        int kt = 0;
+        bool ok = true;
+#pragma unroll 1
+        for (int li = 0; ok; ++li) {
+          Item it;                     // (one lane: its own wait and arrival)
+          {
+            const int s = li % kItemRing;
+            ok = wait1(&sh.items.full[s], li / kItemRing, abort_flag);
+            it = sh.items.item[s];
+            tc::mbar_arrive(&sh.items.empty[s]);
+            if (!ok || it.r < 0) break;
+          }
+          const int par = li & 1;
+          if (is_qk ? !wait1(&sh.q_full[par], li >> 1, abort_flag)
+                    : (li > 0 && !wait1(&sh.o_free, li - 1, abort_flag))) {
+            ok = false;
+            break;
+          }
+#pragma unroll 1
+          for (int j = it.j0; j < it.j1; ++j, ++kt) {
+            const int b = kt & 1, use = kt >> 1;
+            if (is_qk) {
+              const int st = kt % kKStages;
+              if (!wait1(&sh.k_full[st], kt / kKStages, abort_flag) ||
+                  (use > 0 && !wait1(&sh.s_free[b], use - 1, abort_flag))) {
+                ok = false;
+                break;
+              }
+              tc::tc_fence_after();
+              const uint32_t tS = tmem + b * 128;
+              const uint64_t kb = dK + uint64_t(st) * (kTile >> 4);
+              const uint64_t qa = dQ + uint64_t(par) * (kPair >> 4);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                mma_e4m3_ss(tS, qa + 2 * k, kb + 2 * k, id_qk, k > 0 ? 1u : 0u);
+                mma_e4m3_ss(tS, qa + (kTile >> 4) + 2 * k, kb + 2 * k, id_qk, 1u);
+              }
+              tc::mma_commit(&sh.s_full[b]);
+              tc::mma_commit(&sh.k_empty[st]);
+              if (j == it.j1 - 1) tc::mma_commit(&sh.q_empty[par]);
+            } else {
+              const int st = kt % kVStages;
+              if (!wait1(&sh.p_full[b], use, abort_flag) ||
+                  !wait1(&sh.v_full[st], kt / kVStages, abort_flag)) {
+                ok = false;
+                break;
+              }
+              tc::tc_fence_after();
+              const uint32_t tP = tmem + kTmemP + b * 64;
+              const uint64_t vb = dV + uint64_t(st) * (kTile >> 4);
+              const bool first = j == it.j0;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {        // 32 slots: 8 columns of P, 32 rows of V
+                mma_e4m3_ts(tmem + kTmemO, tP + 8 * k, vb + k * (4096 >> 4), id_pv,
+                            (k > 0 || !first) ? 1u : 0u);
+                mma_e4m3_ts(tmem + kTmemO, tP + 32 + 8 * k, vb + k * (4096 >> 4), id_pv, 1u);
+              }
+              tc::mma_commit(&sh.v_empty[st]);
+              tc::mma_commit(&sh.pv_done[b]);
+              if (j == it.j1 - 1) tc::mma_commit(&sh.o_full);
+            }
+          }
+        }
+        if (!ok) *abort_flag = 1;
+        tc::mma_commit(&sh.drain[is_qk ? 0 : 1]);
+        volatile int never = 0;
+        tc::mbar_wait(&sh.drain[is_qk ? 0 : 1], 0, &never, kWaitLimit / 8);
+      }
+      __syncwarp();
+    }
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    // ===================================================================== softmax
+    const int half = (warp - 4) >> 2, q = warp & 3;
+    const uint32_t lane_addr = uint32_t(q * 32) << 16;
+    const int m = q * 32 + lane;                     // this thread's row of the tile
+    const int bar_q = 1 + q;
+    const int tl = m / a.G;
+    int kt = 0;
+    bool ok = true;                                  // no early exit: see the file's comment
+    Item it;
+#pragma unroll 1
+    for (int li = 0;; ++li) {
+      if (bar_any(bar_q, 64, !next_item(sh.items, li, it, abort_flag))) break;
+      const int par = li & 1;
+      const int P = it.P, kv_len = it.P + it.T;
+      const int t = it.mt * d.tpt + tl;
+      const bool valid = tl < d.tpt && t < it.T;
+      const uint32_t* arow = valid ? a.anc + size_t(it.o + t) * a.W : nullptr;
+      // a warp pair without a row only keeps the handshakes: its rows of P feed its rows of O
+      const bool live = __any_sync(0xffffffffu, valid);
+      ok &= wait1(&sh.q_full[par], li >> 1, abort_flag);
+      const float qm = sh.qmul[par][m];
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sh.q_empty[par]);
+      float add = INFINITY, lsum = 0.f;
+#pragma unroll 1
+      for (int j = it.j0; j < it.j1; ++j, ++kt) {
+        const int b = kt & 1, use = kt >> 1, slot = kt % kScaleRing;
+        ok &= wait1(&sh.sc_full[slot], kt / kScaleRing, abort_flag);
+        ok &= wait1(&sh.s_full[b], use, abort_flag);
+        __syncwarp();
+        tc::tc_fence_after();
+        if (live) {
+          const ScaleSlot& sc = sh.sc[slot];
+          uint32_t x[2][32];
+          tc::tmem_ld32(tmem + lane_addr + b * 128 + half * 64, x[0]);
+          tc::tmem_ld32(tmem + lane_addr + b * 128 + half * 64 + 32, x[1]);
+          tc::tmem_ld_wait();
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&sh.s_free[b]);
+          float ymax = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {              // 16 keys have one scale
+            const int page = (half * 64 + 16 * i) >> d.log2bs;
+            const float mul = sc.k[page] * qm, lv = sc.lv[page];
+            const uint64_t mul2 = f2_pack(mul, mul), lv2 = f2_pack(lv, lv);
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              uint32_t& x0 = x[i >> 1][(i & 1) * 16 + e];
+              uint32_t& x1 = x[i >> 1][(i & 1) * 16 + e + 1];
+              float y0, y1;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(x0), __uint_as_float(x1)), mul2, lv2), y0, y1);
+              x0 = __float_as_uint(y0);
+              x1 = __float_as_uint(y1);
+            }
+          }
+          const int key0 = j * kBN + half * 64;
+          if (key0 + 64 > P) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const int k0 = key0 + 32 * c, pre = P - k0;
+              uint32_t vis = anc_window(arow, a.W, k0 - P);
+              vis |= pre >= 32 ? 0xFFFFFFFFu : pre > 0 ? (1u << pre) - 1u : 0u;
+              const int left = kv_len - k0;          // (mask bits past the tree count for nothing)
+              vis &= left >= 32 ? 0xFFFFFFFFu : left > 0 ? (1u << left) - 1u : 0u;
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!((vis >> e) & 1u)) x[c][e] = __float_as_uint(-INFINITY);
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; e += 2)
+              ymax = fmax3(ymax, __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
+          if (bar_any(bar_q, 64, ymax + add > kCeil)) {
+            // some row's reference moves up to its maximum so far
+            sh.mx[half][m] = ymax;
+            bar_sync(bar_q, 64);
+            const float ref = fmaxf(fmaxf(ymax, sh.mx[1 - half][m]), kShift - add);
+            const float now = kShift - ref;
+            const float factor = add == INFINITY ? 1.f : ex2(now - add);
+            add = now;
+            lsum *= factor;
+            if (j > it.j0 && __any_sync(0xffffffffu, factor != 1.f)) {
+              ok &= wait1(&sh.pv_done[(kt - 1) & 1], (kt - 1) >> 1, abort_flag);
+              __syncwarp();
+              tc::tc_fence_after();
+#pragma unroll 1
+              for (int c0 = 0; c0 < 64; c0 += 16) {
+                uint32_t ov[16];
+                const uint32_t to = tmem + lane_addr + kTmemO + half * 64 + c0;
+                tc::tmem_ld16(to, ov);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  ov[e] = __float_as_uint(__uint_as_float(ov[e]) * factor);
+                tc::tmem_st16(to, ov);
+              }
+              tc::tmem_st_wait();
+            }
+          }
+          const float shift = add == INFINITY ? 0.f : add;   // nothing visible yet: weights 0
+          uint32_t hi[16], lo[16];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint64_t shift2 = f2_pack(shift, shift);
+            uint64_t acc = f2_pack(0.f, 0.f);
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+              const uint32_t* xe = &x[i >> 1][(i & 1) * 16 + e];
+              float y0, y1, y2, y3;
+              f2_unpack(f2_add(f2_pack(__uint_as_float(xe[0]), __uint_as_float(xe[1])), shift2), y0, y1);
+              f2_unpack(f2_add(f2_pack(__uint_as_float(xe[2]), __uint_as_float(xe[3])), shift2), y2, y3);
+              const float p0 = ex2(y0), p1 = ex2(y1), p2 = ex2(y2), p3 = ex2(y3);
+              acc = f2_add(acc, f2_pack(p0, p1));
+              acc = f2_add(acc, f2_pack(p2, p3));
+              uint32_t h0, l0, h1, l1;
+              split_p2(p0, p1, h0, l0);
+              split_p2(p2, p3, h1, l1);
+              hi[i * 4 + e / 4] = h0 | (h1 << 16);
+              lo[i * 4 + e / 4] = l0 | (l1 << 16);
+            }
+            float s0, s1;
+            f2_unpack(acc, s0, s1);
+            lsum = fmaf(s0 + s1, sc.iv[(half * 64 + 16 * i) >> d.log2bs], lsum);
+          }
+          // P's buffer, once the product that last read it is done
+          if (use > 0) ok &= wait1(&sh.pv_done[b], use - 1, abort_flag);
+          __syncwarp();
+          tc::tc_fence_after();
+          const uint32_t tP = tmem + lane_addr + kTmemP + b * 64 + half * 16;
+          tc::tmem_st16(tP, hi);
+          tc::tmem_st16(tP + 32, lo);
+          tc::tmem_st_wait();
+        } else {
+          if (lane == 0) tc::mbar_arrive(&sh.s_free[b]);
+          if (use > 0) ok &= wait1(&sh.pv_done[b], use - 1, abort_flag);
+          __syncwarp();
+        }
+        if (lane == 0) tc::mbar_arrive(&sh.sc_empty[slot]);
+        // the unit's last tile: stale V rows past the end (NaN codes) times zero must stay zero
+        if (half == 0 && j * kBN + kBN > kv_len) {
+          const int st = kt % kVStages;
+          ok &= wait1(&sh.v_full[st], kt / kVStages, abort_flag);
+          if (j * kBN + m >= kv_len) {
+            uint4* row = reinterpret_cast<uint4*>(sV + st * kTile + m * 128);
+#pragma unroll
+            for (int x8 = 0; x8 < 8; ++x8) row[x8] = make_uint4(0, 0, 0, 0);
+          }
+          tc::fence_proxy_async_smem();
+        }
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sh.p_full[b]);
+      }
+      if (li > 1) ok &= wait1(&sh.sum_free[par], (li >> 1) - 1, abort_flag);
+      sh.sum[par][half][m] = lsum;
+      if (half == 0) sh.add[par][m] = add;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sh.sum_full[par]);
+    }
+    if (!ok) *abort_flag = 1;
+  } else {
+    // ===================================================================== queries, output
+    const int q = warp & 3;
+    const uint32_t lane_addr = uint32_t(q * 32) << 16;
+    const int m = q * 32 + lane;
+    const int tl = m / a.G, gl = m - tl * a.G;       // token and head of this thread's output row
+    bool ok = true;
+    struct Unit {
+      int o, T, h, mt, slot;
+    };
+    auto fetch = [&](int li, Unit& u) -> bool {
+      Item it;
+      const bool has = __all_sync(0xffffffffu, next_item(sh.items, li, it, abort_flag));
+      u.o = it.o;
+      u.T = it.T;
+      u.h = it.h;
+      u.mt = it.mt;
+      u.slot = it.slot;
+      return has;
+    };
+    // a row to each half warp, 16 bytes a lane, two rows of it in flight
+    auto put_q = [&](int li, const Unit& u) {
+      const int b = li & 1, c = lane & 15;
+      uint8_t* p = sQ + b * kPair;
+      if (li > 1) ok &= idle_wait(&sh.q_empty[b], (li >> 1) - 1, abort_flag);
+      auto load = [&](int n) -> uint4 {
+        const int rl = n / a.G, g = n - rl * a.G, t = u.mt * d.tpt + rl;
+        if (n >= kRows || rl >= d.tpt || t >= u.T) return make_uint4(0, 0, 0, 0);
+        return __ldg(reinterpret_cast<const uint4*>(
+                         static_cast<const __nv_bfloat16*>(a.q) +
+                         (size_t(u.o + t) * a.H_q + u.h * a.G + g) * kD) + c);
+      };
+      const int n0 = q * 2 + (lane >> 4);
+      uint4 w0 = load(n0), w1 = load(n0 + 8), w2 = load(n0 + 16);
+#pragma unroll 1
+      for (int n = n0; n < kRows; n += 8) {
+        const uint4 w = w0;
+        w0 = w1;
+        w1 = w2;
+        w2 = load(n + 24);
+        float f[8], mx = 0.f;
+        elem<__nv_bfloat16>::unpack(w, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mx = fabsf(f[e]) <= FLT_MAX ? fmaxf(mx, fabsf(f[e])) : mx;
+#pragma unroll
+        for (int s = 8; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+        const float sq = kv8::need_scale(mx);
+        uint2 hi, lo;
+        split_q8(w, __uint_as_float((254u << 23) - __float_as_uint(sq)), hi, lo);
+        const int off = (n >> 3) * 1024 + (n & 7) * 128 + (((c >> 1) ^ (n & 7)) << 4) + (c & 1) * 8;
+        *reinterpret_cast<uint2*>(p + off) = hi;
+        *reinterpret_cast<uint2*>(p + kTile + off) = lo;
+        if (c == 0) sh.qmul[b][n] = sq * a.scale_log2;
+      }
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sh.q_full[b]);
+    };
+    Unit cur, next, after;
+    bool has = fetch(0, cur), has_next = false;
+    if (has) {
+      put_q(0, cur);
+      has_next = fetch(1, next);
+      if (has_next) put_q(1, next);
+    }
+#pragma unroll 1
+    for (int li = 0; has; ++li) {
+      const bool has_after = has_next && fetch(li + 2, after);
+      const int par = li & 1;
+      const int t = cur.mt * d.tpt + tl;
+      const bool valid = tl < d.tpt && t < cur.T;
+      ok &= idle_wait(&sh.sum_full[par], li >> 1, abort_flag);
+      const float l = sh.sum[par][0][m] + sh.sum[par][1][m], add = sh.add[par][m];
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float lse2 = l > 0.f ? log2f(l) - add : -INFINITY;
+      const size_t row = cur.slot < 0 ? size_t(cur.o + t) * a.H_q + cur.h * a.G + gl
+                                      : size_t(cur.slot) * kRows + m;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sh.sum_free[par]);
+      ok &= wait1(&sh.o_full, li, abort_flag);
+      __syncwarp();
+      tc::tc_fence_after();
+#pragma unroll 1
+      for (int c0 = 0; c0 < 128; c0 += 32) {
+        uint32_t ov[32];
+        __syncwarp();
+        tc::tmem_ld32(tmem + lane_addr + kTmemO + c0, ov);
+        tc::tmem_ld_wait();
+        if (c0 == 96) {                              // O is read: the next unit may begin
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&sh.o_free);
+        }
+        // (a row that saw nothing may hold whatever P's other rows left: 0 by definition)
+        if (!valid) continue;
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) {
+          float v[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) v[u] = l > 0.f ? __uint_as_float(ov[e + u]) * inv : 0.f;
+          if (cur.slot < 0) {
+            uint32_t w[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const __nv_bfloat162 z = __floats2bfloat162_rn(v[2 * u], v[2 * u + 1]);
+              w[u] = *reinterpret_cast<const uint32_t*>(&z);
+            }
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + row * kD + c0 + e) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+          } else {
+            float4* o4 = reinterpret_cast<float4*>(d.part_o + row * kD + c0 + e);
+            o4[0] = make_float4(v[0], v[1], v[2], v[3]);
+            o4[1] = make_float4(v[4], v[5], v[6], v[7]);
+          }
+        }
+      }
+      if (valid) {
+        if (cur.slot >= 0) d.part_lse[row] = lse2;
+        else if (a.lse) a.lse[row] = lse2 * 0.6931471805599453f;
+      }
+      if (has_after) put_q(li + 2, after);
+      cur = next;
+      next = after;
+      has = has_next;
+      has_next = has_after;
+    }
+    if (!ok) *abort_flag = 1;
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (*abort_flag)                           // every request of the range is unreliable
+#pragma unroll 1
+    for (int r = sh.r0 + tid; r <= sh.r1; r += kThreads) atomicOr(&a.req_status[r], SPEC_REQ_TIMEOUT);
+  tc::tc_fence_after();
+  if (warp == 0) tc::tmem_dealloc(tmem, 512);
+}
+
 // ------------------------------------------------------------------------------ join of pieces
 // CTA (c, y): eight rows of the cut unit of record c, one a warp, lane l columns 4 l .. 4 l + 3.
 // Four pieces' loads at a time are in flight.
@@ -565,7 +1072,7 @@ __global__ void __launch_bounds__(256) attn_kv8_join_kernel(TcDev d) {
       ls[u] = -INFINITY;
       v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (p < rec.np) {
-        const size_t row = size_t(p == 0 ? rec.slot0 : 2 * (rec.ca + p)) * d.part_rows + m;
+        const size_t row = size_t(p == 0 ? rec.slot0 : 2 * (int(blockIdx.x) + (p << d.pair))) * d.part_rows + m;
         ls[u] = d.part_lse[row];
         v[u] = reinterpret_cast<const float4*>(d.part_o + row * kD)[lane];
       }
@@ -652,7 +1159,10 @@ static bool encode_maps(PFN_cuTensorMapEncodeTiled_v12000 enc, const AttnKv8Dev&
 }
 
 // query rows of a unit's row tile
-static int rows_of(const AttnKv8Dev& a) { return a.T_max * a.G <= 8 ? 8 : 16; }
+static int rows_of(const AttnKv8Dev& a) {
+  const int rows = a.T_max * a.G;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : tile::kRows;
+}
 
 static int device_ctas() {
   const int sms = sm_count_current_device();
@@ -664,7 +1174,7 @@ static int device_ctas() {
 // Whether the tensor-core kernels take this call.
 bool attn_kv8_tc_takes(const AttnKv8Dev& a, bool bf16) {
   return bf16 && a.d == 128 && (a.bs == 16 || a.bs == 32 || a.bs == 64 || a.bs == 128) &&
-         a.G <= 16 && (long long)a.T_max * a.G <= 16 &&
+         a.G <= 16 &&
          (long long)a.num_blocks * a.H_kv * a.bs + 128 < (1LL << 31);
 }
 
@@ -685,6 +1195,7 @@ spec_status_t launch_attn_kv8_tc(const AttnKv8Dev& a, void* ws, size_t ws_bytes,
   d.kv_rows = a.num_blocks * a.H_kv * a.bs;
   d.ctas = ctas;
   d.min_tiles = 2;
+  d.pair = a.T_max * a.G > tile::kRows && ctas > 1;
   const WsLayout lay = ws_layout(ctas, d.part_rows);
   if (!ws || ws_bytes < lay.total || (reinterpret_cast<uintptr_t>(ws) & 255u))
     return SPEC_ERR_INVALID_ARG;
@@ -697,13 +1208,17 @@ spec_status_t launch_attn_kv8_tc(const AttnKv8Dev& a, void* ws, size_t ws_bytes,
   CUtensorMap mK, mV, mKw, mVw;
   if (!encode_maps(enc, a, a.k, &mK, &mKw) || !encode_maps(enc, a, a.v, &mV, &mVw))
     return SPEC_ERR_INVALID_ARG;
-  static DeviceOnce raised8, raised16;
+  static DeviceOnce raised8, raised16, raised_tile;
   spec_status_t st = raise_dyn_smem_once(attn_kv8_rows_kernel<8>, rows::smem_bytes<8>(), raised8);
   if (st == SPEC_OK)
     st = raise_dyn_smem_once(attn_kv8_rows_kernel<16>, rows::smem_bytes<16>(), raised16);
+  if (st == SPEC_OK) st = raise_dyn_smem_once(attn_kv8_tile_kernel, tile::kSmemBytes, raised_tile);
   if (st != SPEC_OK) return st;
   cudaError_t e =
-      d.part_rows == 8
+      d.part_rows == tile::kRows
+          ? launch_pdl(attn_kv8_tile_kernel, dim3(ctas), dim3(tile::kThreads),
+                       size_t(tile::kSmemBytes), s, mK, mV, mKw, mVw, d)
+      : d.part_rows == 8
           ? launch_pdl(attn_kv8_rows_kernel<8>, dim3(ctas), dim3(rows::kThreads),
                        size_t(rows::smem_bytes<8>()), s, mK, mV, mKw, mVw, d)
           : launch_pdl(attn_kv8_rows_kernel<16>, dim3(ctas), dim3(rows::kThreads),

@@ -6,6 +6,11 @@
 // into equal contiguous ranges, one per CTA.  A unit cut by a range boundary is computed in
 // pieces: each writes its normalised output and log-sum-exp, and the CTA holding the first piece
 // leaves a record from which a second launch joins them.
+// Where requests have several row tiles, CTAs work in pairs (`pair`): a stream element is two
+// units, one for each CTA of the pair -- two row tiles of one head, which read the same K/V tiles
+// at the same pace, so that the second reader finds them in L2; or, of an odd last row tile, two
+// heads.  (Without the pairs the row tiles' passes over a long cache lie too far apart for L2, and
+// K and V come from HBM once a row tile.)
 //
 // 8-bit codes go to tcgen05.mma kind::f8f6f4 as they are.  The other operand of each product keeps
 // its precision as the sum of two e4m3 pieces, hi = e4m3(x) and lo = e4m3(x - hi), both multiplied
@@ -38,7 +43,7 @@ constexpr float kCeil = 8.f;
 constexpr float kMinVScale = 7.888609052210118e-31f;   // 2^-100
 
 struct MergeRec {
-  int np, h, mt, o, T, ca, slot0;
+  int np, h, mt, o, T, slot0;
 };
 
 struct TcDev {
@@ -47,6 +52,7 @@ struct TcDev {
   int log2bs;
   int kv_rows;          // a row past the cache: TMA fills zeros there
   int ctas, min_tiles;
+  int pair;             // 1: CTAs 2 c, 2 c + 1 share range c
   int part_rows;        // rows of a piece
   MergeRec* recs;       // [ctas]
   float* part_o;        // [2 ctas][part_rows][128]
@@ -64,8 +70,27 @@ __device__ __forceinline__ ReqGeom req_geom(const TcDev& d, int r) {
   const bool ok = kv8_live(d.a, r, g.T, g.P) == Kv8Live::yes && g.o >= 0 && g.o + g.T <= d.a.N;
   g.mts = ok ? (g.T + d.tpt - 1) / d.tpt : 0;
   g.nts = ok ? (g.P + g.T + kBN - 1) / kBN : 0;
-  g.units = d.a.H_kv * g.mts;
+  g.units = d.pair ? d.a.H_kv * (g.mts >> 1) + (g.mts & 1) * ((d.a.H_kv + 1) >> 1)
+                   : d.a.H_kv * g.mts;
   return g;
+}
+// This CTA's range and its place in it.
+__device__ __forceinline__ int range_id(const TcDev& d) { return int(blockIdx.x) >> d.pair; }
+// Head and row tile of the u-th stream element for this CTA; h = H_kv: none.
+__device__ __forceinline__ void unit_of(const TcDev& d, const ReqGeom& g, int u, int& h, int& mt) {
+  if (!d.pair) {
+    h = u / g.mts;
+    mt = u - h * g.mts;
+    return;
+  }
+  const int rank = blockIdx.x & 1, twos = g.mts >> 1, whole = d.a.H_kv * twos;
+  if (u < whole) {
+    h = u / twos;
+    mt = 2 * (u - h * twos) + rank;
+  } else {
+    h = min(2 * (u - whole) + rank, d.a.H_kv);
+    mt = g.mts - 1;
+  }
 }
 
 // `total` tiles in C ranges, the first `rem` of them one tile longer than `quot`
@@ -123,14 +148,15 @@ __device__ __forceinline__ Range warp_range(const TcDev& d) {
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   Range R;
   R.total = total;
-  R.C = int(max(1LL, min((long long)d.ctas, div_count(total, d.min_tiles))));
+  R.C = int(max(1LL, min((long long)(d.ctas >> d.pair), div_count(total, d.min_tiles))));
   R.cut = make_cut(total, R.C);
   R.t0 = R.t1 = 0;
   R.r0 = R.r1 = 0;
   R.rbeg0 = R.rbeg1 = 0;
-  if (total == 0 || int(blockIdx.x) >= R.C) return R;
-  R.t0 = range_start(R.cut, blockIdx.x);
-  R.t1 = range_start(R.cut, blockIdx.x + 1);
+  const int id = range_id(d);
+  if (total == 0 || id >= R.C) return R;
+  R.t0 = range_start(R.cut, id);
+  R.t1 = range_start(R.cut, id + 1);
   long long base = 0;
 #pragma unroll 1
   for (int c = 0; c * 32 < d.a.B; ++c) {
@@ -183,29 +209,31 @@ struct ItemIter {
     }
   }
   __device__ __forceinline__ bool next(const TcDev& d, const Range& R, Item& it) {
-    if (t >= R.t1) return false;
 #pragma unroll 1
-    while (t >= rend) {
-      if (r + 1 >= d.a.B) return false;
-      ++r;
-      g = req_geom(d, r);
-      rbeg = rend;
-      rend = rbeg + (long long)g.units * g.nts;
+    while (t < R.t1) {
+#pragma unroll 1
+      while (t >= rend) {
+        if (r + 1 >= d.a.B) return false;
+        ++r;
+        g = req_geom(d, r);
+        rbeg = rend;
+        rend = rbeg + (long long)g.units * g.nts;
+      }
+      const long long off = t - rbeg;
+      const int u = int(div_count(off, g.nts));
+      it.r = r;
+      unit_of(d, g, u, it.h, it.mt);
+      it.j0 = int(off - (long long)u * g.nts);
+      it.j1 = int(min((long long)g.nts, (long long)it.j0 + (R.t1 - t)));
+      it.o = g.o;
+      it.T = g.T;
+      it.P = g.P;
+      const bool partial = it.j0 > 0 || it.j1 < g.nts;
+      it.slot = partial ? (t == R.t0 ? 2 * int(blockIdx.x) : 2 * int(blockIdx.x) + 1) : -1;
+      t += it.j1 - it.j0;
+      if (it.h < d.a.H_kv) return true;
     }
-    const long long off = t - rbeg;
-    const int u = int(div_count(off, g.nts));
-    it.r = r;
-    it.h = u / g.mts;
-    it.mt = u - it.h * g.mts;
-    it.j0 = int(off - (long long)u * g.nts);
-    it.j1 = int(min((long long)g.nts, (long long)it.j0 + (R.t1 - t)));
-    it.o = g.o;
-    it.T = g.T;
-    it.P = g.P;
-    const bool partial = it.j0 > 0 || it.j1 < g.nts;
-    it.slot = partial ? (t == R.t0 ? 2 * int(blockIdx.x) : 2 * int(blockIdx.x) + 1) : -1;
-    t += it.j1 - it.j0;
-    return true;
+    return false;
   }
 };
 
@@ -219,23 +247,21 @@ struct ItemRing {
   Item item[kItemRing];
 };
 
-// One lane of CTA c: the record of the unit holding the range's last tile, if it starts in this
-// range and continues past it.  Piece p > 0 starts range ca + p and lies in slot 2 (ca + p).
+// One lane of each CTA: the record of its unit of the range's last tile, if that unit starts in
+// this range and continues past it.  Piece p > 0 starts range id + p: slot 2 (CTA + (p << pair)).
 __device__ __forceinline__ void write_merge_record(const TcDev& d, const Range& R) {
   MergeRec rec;
-  rec.np = rec.h = rec.mt = rec.o = rec.T = rec.ca = rec.slot0 = 0;
+  rec.np = rec.h = rec.mt = rec.o = rec.T = rec.slot0 = 0;
   if (R.t0 < R.t1) {
     const ReqGeom g = req_geom(d, R.r1);
     const int u = int(div_count(R.t1 - 1 - R.rbeg1, g.nts));
     const long long ubeg = R.rbeg1 + (long long)u * g.nts;
-    if (ubeg >= R.t0 && ubeg + g.nts > R.t1) {
-      rec.ca = int(blockIdx.x);
-      rec.np = range_of(R.cut, ubeg + g.nts - 1) - rec.ca + 1;
-      rec.h = u / g.mts;
-      rec.mt = u - rec.h * g.mts;
+    unit_of(d, g, u, rec.h, rec.mt);
+    if (ubeg >= R.t0 && ubeg + g.nts > R.t1 && rec.h < d.a.H_kv) {
+      rec.np = range_of(R.cut, ubeg + g.nts - 1) - range_id(d) + 1;
       rec.o = g.o;
       rec.T = g.T;
-      rec.slot0 = ubeg > R.t0 ? 2 * rec.ca + 1 : 2 * rec.ca;
+      rec.slot0 = 2 * int(blockIdx.x) + (ubeg > R.t0 ? 1 : 0);
     }
   }
   d.recs[blockIdx.x] = rec;
