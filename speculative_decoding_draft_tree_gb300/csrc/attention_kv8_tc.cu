@@ -13,12 +13,16 @@
 // softmax, 12-15 split the queries and write the output, 16 brings the scales, 17 walks the items.
 //
 // attn_kv8_tile_kernel: longer units in tiles of 128 query rows (G heads x 128 / G tree tokens).
-// S = Q K^T (M = N = 128, both pieces of Q into one accumulator), P's pieces written to TMEM as the
-// A operand of O += P V.  S and P are double-buffered, so the next tile's scores and the last
-// one's output are formed while the softmax works; TMEM columns: S 0-255, O 256-383, P 384-511.
-// One query row a thread pair: warps q + 4 and q + 8 take 64 of a tile's keys each, agree on the
-// row's reference at a barrier of the two, and keep a sum each.  Bound by the tensor core (1024
-// clocks a tile at the e4m3 rate) and the softmax's issue slots about equally.
+// S = Q K^T (M = N = 128, both pieces of Q into one accumulator); P's pieces go to TMEM as the A
+// operand of O += P V (TMEM columns: S 0-255, O 256-383, P 384-511).  Bound by the softmax's
+// instructions before the tensor core (1024 clocks a tile at the e4m3 rate): exponentials and e4m3
+// packing run at 32 results a clock and SM, most of the rest at 64.  So two sets of eight warps
+// take alternate tiles, one's waits under the other's arithmetic, with S and P buffers of their
+// own, and P is split the cheapest way: hi is e5m2, which is the upper byte of an fp16 (a rounding
+// add and a mask), lo = e4m3(p - hi); e5m2's range also leaves the reference five binades of
+// slack.  A row belongs to four threads: two a set, each with 64 of a tile's keys, that agree on
+// the row's reference at a barrier; the sets pass it on tile by tile.
+// Warps: 0-3 as above, 4-19 softmax, 20-23 queries and output, 24 scales, 25 items.
 //
 // Scales: a score is code product * (K scale of the slot's page * the row's query scale); the V
 // scale joins the exponent, y = score + log2(V scale), and the weight 2^(y - ref) goes into the
@@ -553,8 +557,14 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
 namespace tile {
 constexpr int kRows = 128;
 constexpr int kThreads = 640;
-constexpr int kCtlRegs = 72;       // as in rows::
-constexpr int kSoftmaxRegs = 120;
+constexpr int kCtlRegs = 72;       // warps 0-3 and 16-19
+constexpr int kSoftmaxRegs = 120;  // warps 4-11
+constexpr int kOutRegs = 96;       // warps 12-15, as launched
+static_assert(256 * kCtlRegs + 256 * kSoftmaxRegs + 128 * kOutRegs <= kThreads * 96, "register split");
+// Weights are 2^(y - ref + kLift); the reference moves when one passes 2^kTop (hi reaches 57344, lo
+// takes an eighth).  lo's step is 2^-9, i.e. 2^-12 of a row's largest weight; below that hi alone
+// still has three bits.
+constexpr float kLift = 3.f, kTop = 11.f;
 constexpr int kKStages = 4;
 constexpr int kVStages = 4;
 constexpr int kPair = 2 * kTile;                         // Q's two pieces
@@ -574,7 +584,7 @@ struct Shared {
   float qmul[2][kRows];
   float mx[2][kRows];             // per half: row maxima of an update
   float sum[2][2][kRows];         // per unit parity and half
-  float add[2][kRows];            // per unit parity: kShift - reference
+  float add[2][kRows];            // per unit parity: kLift - reference
   uint32_t tmem;
   int abort, r0, r1;
   ItemRing items;
@@ -672,7 +682,7 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
       if (lane == 0) {
         const bool is_qk = warp == 1;
         const uint32_t id_qk = idesc_e4m3(128, 128, false, false);
-        const uint32_t id_pv = idesc_e4m3(128, 128, false, true);
+        const uint32_t id_lo = idesc_e4m3(128, 128, false, true), id_hi = id_lo | kIdescAE5m2;
         const uint64_t dQ = tc::smem_desc(tc::smem_u32(sQ), 16, 1024);
         const uint64_t dK = tc::smem_desc(tc::smem_u32(sK), 16, 1024);
         const uint64_t dV = tc::smem_desc(tc::smem_u32(sV), kTile, 1024);
@@ -724,14 +734,14 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
                 break;
               }
               tc::tc_fence_after();
-              const uint32_t tP = tmem + kTmemP + b * 64;
               const uint64_t vb = dV + uint64_t(st) * (kTile >> 4);
               const bool first = j == it.j0;
 #pragma unroll
               for (int k = 0; k < 4; ++k) {        // 32 slots: 8 columns of P, 32 rows of V
-                mma_e4m3_ts(tmem + kTmemO, tP + 8 * k, vb + k * (4096 >> 4), id_pv,
+                const uint32_t tP = tmem + kTmemP + b * 64 + 8 * k;
+                mma_e4m3_ts(tmem + kTmemO, tP, vb + k * (4096 >> 4), id_hi,
                             (k > 0 || !first) ? 1u : 0u);
-                mma_e4m3_ts(tmem + kTmemO, tP + 32 + 8 * k, vb + k * (4096 >> 4), id_pv, 1u);
+                mma_e4m3_ts(tmem + kTmemO, tP + 32, vb + k * (4096 >> 4), id_lo, 1u);
               }
               tc::mma_commit(&sh.v_empty[st]);
               tc::mma_commit(&sh.pv_done[b]);
@@ -752,7 +762,7 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
     const int half = (warp - 4) >> 2, q = warp & 3;
     const uint32_t lane_addr = uint32_t(q * 32) << 16;
     const int m = q * 32 + lane;                     // this thread's row of the tile
-    const int bar_q = 1 + q;
+    const int bar_q = 1 + q;                         // the two warps of this quarter
     const int tl = m / a.G;
     int kt = 0;
     bool ok = true;                                  // no early exit: see the file's comment
@@ -765,7 +775,7 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
       const int t = it.mt * d.tpt + tl;
       const bool valid = tl < d.tpt && t < it.T;
       const uint32_t* arow = valid ? a.anc + size_t(it.o + t) * a.W : nullptr;
-      // a warp pair without a row only keeps the handshakes: its rows of P feed its rows of O
+      // a quarter without a row only keeps the handshakes: its rows of P feed its rows of O
       const bool live = __any_sync(0xffffffffu, valid);
       ok &= wait1(&sh.q_full[par], li >> 1, abort_flag);
       const float qm = sh.qmul[par][m];
@@ -775,62 +785,78 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
 #pragma unroll 1
       for (int j = it.j0; j < it.j1; ++j, ++kt) {
         const int b = kt & 1, use = kt >> 1, slot = kt % kScaleRing;
+        const int key0 = j * kBN + half * 64;
         ok &= wait1(&sh.sc_full[slot], kt / kScaleRing, abort_flag);
         ok &= wait1(&sh.s_full[b], use, abort_flag);
+        // P's buffer, once the product that last read it is done
+        if (use > 0) ok &= wait1(&sh.pv_done[b], use - 1, abort_flag);
         __syncwarp();
         tc::tc_fence_after();
         if (live) {
           const ScaleSlot& sc = sh.sc[slot];
-          uint32_t x[2][32];
-          tc::tmem_ld32(tmem + lane_addr + b * 128 + half * 64, x[0]);
-          tc::tmem_ld32(tmem + lane_addr + b * 128 + half * 64 + 32, x[1]);
-          tc::tmem_ld_wait();
-          tc::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&sh.s_free[b]);
-          float ymax = -INFINITY;
+          const uint32_t tS = tmem + lane_addr + b * 128 + half * 64;
+          const uint32_t tP = tmem + lane_addr + kTmemP + b * 64 + half * 16;
+          // the weights of this thread's 64 keys against the reference kLift - add, as the two
+          // pieces of P; `top`: the largest exponent, `sum`: of the weights over the V scales
+          float top, sum;
+          auto weights = [&](float add) {
+            const float shift = add == INFINITY ? 0.f : add;   // no key seen yet
+            uint32_t x[2][32];
+            tc::tmem_ld32(tS, x[0]);
+            tc::tmem_ld32(tS + 32, x[1]);
+            tc::tmem_ld_wait();
+            if (key0 + 64 > P) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {              // 16 keys have one scale
-            const int page = (half * 64 + 16 * i) >> d.log2bs;
-            const float mul = sc.k[page] * qm, lv = sc.lv[page];
-            const uint64_t mul2 = f2_pack(mul, mul), lv2 = f2_pack(lv, lv);
+              for (int c = 0; c < 2; ++c) {
+                const int k0 = key0 + 32 * c, pre = P - k0, left = kv_len - k0;
+                uint32_t vis = anc_window(arow, a.W, k0 - P);
+                vis |= pre >= 32 ? 0xFFFFFFFFu : pre > 0 ? (1u << pre) - 1u : 0u;
+                // (mask bits past the tree count for nothing)
+                vis &= left >= 32 ? 0xFFFFFFFFu : left > 0 ? (1u << left) - 1u : 0u;
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              uint32_t& x0 = x[i >> 1][(i & 1) * 16 + e];
-              uint32_t& x1 = x[i >> 1][(i & 1) * 16 + e + 1];
-              float y0, y1;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(x0), __uint_as_float(x1)), mul2, lv2), y0, y1);
-              x0 = __float_as_uint(y0);
-              x1 = __float_as_uint(y1);
+                for (int e = 0; e < 32; ++e)
+                  if (!((vis >> e) & 1u)) x[c][e] = __float_as_uint(-INFINITY);
+              }
             }
-          }
-          const int key0 = j * kBN + half * 64;
-          if (key0 + 64 > P) {
+            top = -INFINITY;
+            sum = 0.f;
+            uint32_t hi[16], lo[16];
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const int k0 = key0 + 32 * c, pre = P - k0;
-              uint32_t vis = anc_window(arow, a.W, k0 - P);
-              vis |= pre >= 32 ? 0xFFFFFFFFu : pre > 0 ? (1u << pre) - 1u : 0u;
-              const int left = kv_len - k0;          // (mask bits past the tree count for nothing)
-              vis &= left >= 32 ? 0xFFFFFFFFu : left > 0 ? (1u << left) - 1u : 0u;
+            for (int g = 0; g < 4; ++g) {              // 16 keys of one page
+              const int page = (half * 64 + 16 * g) >> d.log2bs;
+              // (never 0, which would make a masked key's -infinity a NaN)
+              const float mul = fmaxf(sc.k[page] * qm, FLT_MIN), lift = sc.lv[page] + shift;
+              float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!((vis >> e) & 1u)) x[c][e] = __float_as_uint(-INFINITY);
+              for (int e = 0; e < 16; e += 4) {
+                float z[4], p[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                  z[u] = fmaf(__uint_as_float(x[g >> 1][(g & 1) * 16 + e + u]), mul, lift);
+                top = fmax3(fmax3(top, z[0], z[1]), z[2], z[3]);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) p[u] = ex2(z[u]);
+                s0 += p[0] + p[1];
+                s1 += p[2] + p[3];
+                split_p4(p, hi[g * 4 + e / 4], lo[g * 4 + e / 4]);
+              }
+              sum = fmaf(s0 + s1, sc.iv[page], sum);
             }
-          }
-#pragma unroll
-          for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int e = 0; e < 32; e += 2)
-              ymax = fmax3(ymax, __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
-          if (bar_any(bar_q, 64, ymax + add > kCeil)) {
+            tc::tmem_st16(tP, hi);
+            tc::tmem_st16(tP + 32, lo);
+            top -= shift;
+          };
+          // The weights are formed on the expectation that the tile does not move the reference,
+          // and formed again where it does.
+          weights(add);
+          if (bar_any(bar_q, 64, top + add > kTop)) {
             // some row's reference moves up to its maximum so far
-            sh.mx[half][m] = ymax;
+            sh.mx[half][m] = top;
             bar_sync(bar_q, 64);
-            const float ref = fmaxf(fmaxf(ymax, sh.mx[1 - half][m]), kShift - add);
-            const float now = kShift - ref;
-            const float factor = add == INFINITY ? 1.f : ex2(now - add);
-            add = now;
+            const float ref = fmaxf(fmaxf(top, sh.mx[1 - half][m]), kLift - add);
+            const float next = kLift - ref;
+            const float factor = add == INFINITY ? 1.f : ex2(next - add);
+            add = next;
             lsum *= factor;
             if (j > it.j0 && __any_sync(0xffffffffu, factor != 1.f)) {
               ok &= wait1(&sh.pv_done[(kt - 1) & 1], (kt - 1) >> 1, abort_flag);
@@ -847,48 +873,18 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
                   ov[e] = __float_as_uint(__uint_as_float(ov[e]) * factor);
                 tc::tmem_st16(to, ov);
               }
-              tc::tmem_st_wait();
             }
+            weights(add);
           }
-          const float shift = add == INFINITY ? 0.f : add;   // nothing visible yet: weights 0
-          uint32_t hi[16], lo[16];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint64_t shift2 = f2_pack(shift, shift);
-            uint64_t acc = f2_pack(0.f, 0.f);
-#pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-              const uint32_t* xe = &x[i >> 1][(i & 1) * 16 + e];
-              float y0, y1, y2, y3;
-              f2_unpack(f2_add(f2_pack(__uint_as_float(xe[0]), __uint_as_float(xe[1])), shift2), y0, y1);
-              f2_unpack(f2_add(f2_pack(__uint_as_float(xe[2]), __uint_as_float(xe[3])), shift2), y2, y3);
-              const float p0 = ex2(y0), p1 = ex2(y1), p2 = ex2(y2), p3 = ex2(y3);
-              acc = f2_add(acc, f2_pack(p0, p1));
-              acc = f2_add(acc, f2_pack(p2, p3));
-              uint32_t h0, l0, h1, l1;
-              split_p2(p0, p1, h0, l0);
-              split_p2(p2, p3, h1, l1);
-              hi[i * 4 + e / 4] = h0 | (h1 << 16);
-              lo[i * 4 + e / 4] = l0 | (l1 << 16);
-            }
-            float s0, s1;
-            f2_unpack(acc, s0, s1);
-            lsum = fmaf(s0 + s1, sc.iv[(half * 64 + 16 * i) >> d.log2bs], lsum);
-          }
-          // P's buffer, once the product that last read it is done
-          if (use > 0) ok &= wait1(&sh.pv_done[b], use - 1, abort_flag);
-          __syncwarp();
-          tc::tc_fence_after();
-          const uint32_t tP = tmem + lane_addr + kTmemP + b * 64 + half * 16;
-          tc::tmem_st16(tP, hi);
-          tc::tmem_st16(tP + 32, lo);
+          lsum += sum;
           tc::tmem_st_wait();
-        } else {
-          if (lane == 0) tc::mbar_arrive(&sh.s_free[b]);
-          if (use > 0) ok &= wait1(&sh.pv_done[b], use - 1, abort_flag);
-          __syncwarp();
+          tc::tc_fence_before();
         }
-        if (lane == 0) tc::mbar_arrive(&sh.sc_empty[slot]);
+        __syncwarp();
+        if (lane == 0) {
+          tc::mbar_arrive(&sh.s_free[b]);
+          tc::mbar_arrive(&sh.sc_empty[slot]);
+        }
         // the unit's last tile: stale V rows past the end (NaN codes) times zero must stay zero
         if (half == 0 && j * kBN + kBN > kv_len) {
           const int st = kt % kVStages;
@@ -899,9 +895,8 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
             for (int x8 = 0; x8 < 8; ++x8) row[x8] = make_uint4(0, 0, 0, 0);
           }
           tc::fence_proxy_async_smem();
+          __syncwarp();
         }
-        tc::tc_fence_before();
-        __syncwarp();
         if (lane == 0) tc::mbar_arrive(&sh.p_full[b]);
       }
       if (li > 1) ok &= wait1(&sh.sum_free[par], (li >> 1) - 1, abort_flag);

@@ -483,6 +483,31 @@ __device__ __forceinline__ void split_p2(float a, float b, uint32_t& hi, uint32_
   lo = l;
 }
 
+// four weights (below 2^13) as two pieces of four codes: hi in e5m2, the upper byte of the fp16
+// value rounded to nearest, lo = e4m3 of the exact remainder (at most an eighth)
+__device__ __forceinline__ void split_p4(const float (&p)[4], uint32_t& hi, uint32_t& lo) {
+  uint32_t w0, w1, r0, r1;
+  uint16_t l0, l1;
+  asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(w0) : "f"(p[0]), "f"(p[1]));
+  asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(w1) : "f"(p[2]), "f"(p[3]));
+  const uint32_t h0 = (w0 + 0x00800080u) & 0xFF00FF00u, h1 = (w1 + 0x00800080u) & 0xFF00FF00u;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r0) : "r"(w0), "r"(h0));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r1) : "r"(w1), "r"(h1));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l0) : "r"(r0));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l1) : "r"(r1));
+  hi = __byte_perm(h0, h1, 0x7531);
+  lo = uint32_t(l0) | (uint32_t(l1) << 16);
+}
+
+// 32 lanes x 8 consecutive 32-bit columns
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+        "r"(r[7])
+      : "memory");
+}
+
 // D[tmem] (+)= A[smem] * B[smem], kind::f8f6f4 (e4m3 codes, fp32 accumulate), K = 32
 __device__ __forceinline__ void mma_e4m3_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                             uint32_t idesc, uint32_t accumulate) {
@@ -509,6 +534,8 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool 
   return (1u << 4) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) | (uint32_t(N >> 3) << 17) |
          (uint32_t(M >> 4) << 24);
 }
+
+constexpr uint32_t kIdescAE5m2 = 1u << 7;   // A's type field: e5m2
 
 // Reductions of NR values a lane over the 32 lanes: each of the first exchanges halves what a lane
 // holds, about NR shuffles instead of 5 NR.  Lane l ends with the result of row red_row<NR>(l).

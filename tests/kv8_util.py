@@ -129,8 +129,12 @@ def check_attention(case, rows=None, scale=None):
     which the row's largest element is above 224: 2^-17.8 max|q| for each element; the products are
     exact and summed in fp32 (2^-17 of the sum of their magnitudes covers the tensor core's sums).  E is
     the sum of both: a weight is off by a factor within e^E.
-    Weights: 11-bit halves split into two e4m3 pieces, off by 2^-8 + 2^-11 of themselves or by 2^-10
-    of a range in which a row's largest weight is at least 64, i.e. 2^-16 of the largest.
+    Weights, units of at most 16 query rows: 11-bit halves split into two e4m3 pieces, each rounded to
+    within 2^-4 of itself, so off by 2^-8 + 2^-11 of themselves or (where the second piece is
+    subnormal) by 2^-10 of a range in which a row's largest weight is at least 2^6: 2^-16 of the largest.
+    Longer units: the first piece is e5m2, rounded to within 2^-3 of the weight, so the second, e4m3 of
+    that remainder, leaves 2^-4 2^-3 = 2^-7 (and the halves' 2^-11), or 2^-10 of a range in which a
+    row's largest weight is at least 2^3: 2^-13 of the largest.
     Output: that, and one rounding to bf16 (2^-8 of the value).  fp32 queries take the CUDA-core
     kernel: fp32 products and sums over the row (2^-17 relative bounds them), exp2 within 2^-21.
     """
@@ -142,7 +146,9 @@ def check_attention(case, rows=None, scale=None):
     if f32:
         tol = 2 * E[..., None] * mass + 2.0 ** -17 * mass
     else:
-        tol = (2 * E[..., None] + 2.0 ** -8 + 2.0 ** -11) * mass + 2.0 ** -16 * tail + 2.0 ** -8 * np.abs(o)
+        few = case.T_max * (case.q.shape[1] // case.ks.shape[1]) <= 16
+        rel, least = (2.0 ** -8, 2.0 ** -16) if few else (2.0 ** -7, 2.0 ** -13)
+        tol = (2 * E[..., None] + rel + 2.0 ** -11) * mass + least * tail + 2.0 ** -8 * np.abs(o)
     sel = slice(None) if rows is None else rows
     bad = np.abs(go - o)[sel] > tol[sel] + 1e-30
     assert not bad.any(), (int(bad.sum()), float(np.abs(go - o).max()))
