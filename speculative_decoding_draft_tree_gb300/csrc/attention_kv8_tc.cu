@@ -572,19 +572,18 @@ constexpr int kSmemQ = 0;                                // 2 buffers
 constexpr int kSmemK = kSmemQ + 2 * kPair;
 constexpr int kSmemV = kSmemK + kKStages * kTile;
 constexpr int kSmemBar = kSmemV + kVStages * kTile;
-constexpr uint32_t kTmemO = 256, kTmemP = 384;
+constexpr uint32_t kTmemO = 256;
 
 struct Shared {
   uint64_t q_full[2], q_empty[2];
   uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
-  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
+  uint64_t s_full[2], p_full[2][2], pv_done[2];
   uint64_t sum_full[2], sum_free[2], o_full, o_free;
   uint64_t sc_full[kScaleRing], sc_empty[kScaleRing], drain[2];
   ScaleSlot sc[kScaleRing];
   float qmul[2][kRows];
-  float mx[2][kRows];             // per half: row maxima of an update
   float sum[2][2][kRows];         // per unit parity and half
-  float add[2][kRows];            // per unit parity: kLift - reference
+  float add[2][2][kRows];         // per unit parity and half: kLift - reference
   uint32_t tmem;
   int abort, r0, r1;
   ItemRing items;
@@ -636,8 +635,7 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
     init(sh.v_full, kVStages, 1);
     init(sh.v_empty, kVStages, 1);
     init(sh.s_full, 2, 1);
-    init(sh.s_free, 2, 8);
-    init(sh.p_full, 2, 8);
+    init(&sh.p_full[0][0], 4, 4);
     init(sh.pv_done, 2, 1);
     init(sh.sum_full, 2, 8);
     init(sh.sum_free, 2, 4);
@@ -709,8 +707,10 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
             const int b = kt & 1, use = kt >> 1;
             if (is_qk) {
               const int st = kt % kKStages;
-              if (!wait1(&sh.k_full[st], kt / kKStages, abort_flag) ||
-                  (use > 0 && !wait1(&sh.s_free[b], use - 1, abort_flag))) {
+              const int slot = kt % kScaleRing;
+              if (!wait1(&sh.sc_full[slot], kt / kScaleRing, abort_flag) ||
+                  !wait1(&sh.k_full[st], kt / kKStages, abort_flag) ||
+                  (use > 0 && !wait1(&sh.pv_done[b], use - 1, abort_flag))) {
                 ok = false;
                 break;
               }
@@ -728,21 +728,25 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
               if (j == it.j1 - 1) tc::mma_commit(&sh.q_empty[par]);
             } else {
               const int st = kt % kVStages;
-              if (!wait1(&sh.p_full[b], use, abort_flag) ||
-                  !wait1(&sh.v_full[st], kt / kVStages, abort_flag)) {
+              if (!wait1(&sh.v_full[st], kt / kVStages, abort_flag)) {
                 ok = false;
                 break;
               }
-              tc::tc_fence_after();
               const uint64_t vb = dV + uint64_t(st) * (kTile >> 4);
-              const bool first = j == it.j0;
+              const uint32_t acc = j > it.j0 ? 1u : 0u;
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {        // 32 slots: 8 columns of P, 32 rows of V
-                const uint32_t tP = tmem + kTmemP + b * 64 + 8 * k;
-                mma_e4m3_ts(tmem + kTmemO, tP, vb + k * (4096 >> 4), id_hi,
-                            (k > 0 || !first) ? 1u : 0u);
-                mma_e4m3_ts(tmem + kTmemO, tP + 32, vb + k * (4096 >> 4), id_lo, 1u);
+              for (int hf = 0; hf < 2; ++hf) {     // a half's 64 slots into its accumulator
+                ok = ok && wait1(&sh.p_full[hf][b], use, abort_flag);
+                tc::tc_fence_after();
+                const uint32_t tO = tmem + kTmemO + hf * 128, tP = tmem + b * 128 + hf * 64;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {      // 32 slots: 8 columns of P, 32 rows of V
+                  const uint64_t vk = vb + (2 * hf + k) * (4096 >> 4);
+                  mma_e4m3_ts(tO, tP + 8 * k, vk, id_hi, k > 0 ? 1u : acc);
+                  mma_e4m3_ts(tO, tP + 16 + 8 * k, vk, id_lo, 1u);
+                }
               }
+              if (!ok) break;
               tc::mma_commit(&sh.v_empty[st]);
               tc::mma_commit(&sh.pv_done[b]);
               if (j == it.j1 - 1) tc::mma_commit(&sh.o_full);
@@ -762,14 +766,13 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
     const int half = (warp - 4) >> 2, q = warp & 3;
     const uint32_t lane_addr = uint32_t(q * 32) << 16;
     const int m = q * 32 + lane;                     // this thread's row of the tile
-    const int bar_q = 1 + q;                         // the two warps of this quarter
     const int tl = m / a.G;
     int kt = 0;
     bool ok = true;                                  // no early exit: see the file's comment
     Item it;
 #pragma unroll 1
     for (int li = 0;; ++li) {
-      if (bar_any(bar_q, 64, !next_item(sh.items, li, it, abort_flag))) break;
+      if (!__all_sync(0xffffffffu, next_item(sh.items, li, it, abort_flag))) break;
       const int par = li & 1;
       const int P = it.P, kv_len = it.P + it.T;
       const int t = it.mt * d.tpt + tl;
@@ -786,19 +789,16 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
       for (int j = it.j0; j < it.j1; ++j, ++kt) {
         const int b = kt & 1, use = kt >> 1, slot = kt % kScaleRing;
         const int key0 = j * kBN + half * 64;
-        ok &= wait1(&sh.sc_full[slot], kt / kScaleRing, abort_flag);
-        ok &= wait1(&sh.s_full[b], use, abort_flag);
-        // P's buffer, once the product that last read it is done
-        if (use > 0) ok &= wait1(&sh.pv_done[b], use - 1, abort_flag);
+        ok &= wait1(&sh.s_full[b], use, abort_flag);   // (the issuer has waited for the scales)
         __syncwarp();
         tc::tc_fence_after();
         if (live) {
           const ScaleSlot& sc = sh.sc[slot];
           const uint32_t tS = tmem + lane_addr + b * 128 + half * 64;
-          const uint32_t tP = tmem + lane_addr + kTmemP + b * 64 + half * 16;
           // the weights of this thread's 64 keys against the reference kLift - add, as the two
           // pieces of P; `top`: the largest exponent, `sum`: of the weights over the V scales
           float top, sum;
+          uint32_t hi[16], lo[16];
           auto weights = [&](float add) {
             const float shift = add == INFINITY ? 0.f : add;   // no key seen yet
             uint32_t x[2][32];
@@ -820,19 +820,22 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
             }
             top = -INFINITY;
             sum = 0.f;
-            uint32_t hi[16], lo[16];
 #pragma unroll
             for (int g = 0; g < 4; ++g) {              // 16 keys of one page
               const int page = (half * 64 + 16 * g) >> d.log2bs;
               // (never 0, which would make a masked key's -infinity a NaN)
               const float mul = fmaxf(sc.k[page] * qm, FLT_MIN), lift = sc.lv[page] + shift;
+              const uint64_t mul2 = f2_pack(mul, mul), lift2 = f2_pack(lift, lift);
               float s0 = 0.f, s1 = 0.f;
 #pragma unroll
               for (int e = 0; e < 16; e += 4) {
                 float z[4], p[4];
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
-                  z[u] = fmaf(__uint_as_float(x[g >> 1][(g & 1) * 16 + e + u]), mul, lift);
+                for (int u = 0; u < 4; u += 2) {
+                  const uint32_t* xe = &x[g >> 1][(g & 1) * 16 + e + u];
+                  f2_unpack(f2_fma(f2_pack(__uint_as_float(xe[0]), __uint_as_float(xe[1])), mul2, lift2),
+                            z[u], z[u + 1]);
+                }
                 top = fmax3(fmax3(top, z[0], z[1]), z[2], z[3]);
 #pragma unroll
                 for (int u = 0; u < 4; ++u) p[u] = ex2(z[u]);
@@ -842,19 +845,13 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
               }
               sum = fmaf(s0 + s1, sc.iv[page], sum);
             }
-            tc::tmem_st16(tP, hi);
-            tc::tmem_st16(tP + 32, lo);
             top -= shift;
           };
-          // The weights are formed on the expectation that the tile does not move the reference,
-          // and formed again where it does.
+          // The weights are formed on the expectation that the tile does not move a row's reference,
+          // and formed again where it does (they stay in registers until then: P lies over S).
           weights(add);
-          if (bar_any(bar_q, 64, top + add > kTop)) {
-            // some row's reference moves up to its maximum so far
-            sh.mx[half][m] = top;
-            bar_sync(bar_q, 64);
-            const float ref = fmaxf(fmaxf(top, sh.mx[1 - half][m]), kLift - add);
-            const float next = kLift - ref;
+          if (__any_sync(0xffffffffu, top + add > kTop)) {
+            const float ref = fmaxf(top, kLift - add), next = kLift - ref;
             const float factor = add == INFINITY ? 1.f : ex2(next - add);
             add = next;
             lsum *= factor;
@@ -863,45 +860,47 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
               __syncwarp();
               tc::tc_fence_after();
 #pragma unroll 1
-              for (int c0 = 0; c0 < 64; c0 += 16) {
-                uint32_t ov[16];
-                const uint32_t to = tmem + lane_addr + kTmemO + half * 64 + c0;
-                tc::tmem_ld16(to, ov);
+              for (int c0 = 0; c0 < 128; c0 += 32) {
+                uint32_t ov[32];
+                const uint32_t to = tmem + lane_addr + kTmemO + half * 128 + c0;
+                tc::tmem_ld32(to, ov);
                 tc::tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
+                for (int e = 0; e < 32; ++e)
                   ov[e] = __float_as_uint(__uint_as_float(ov[e]) * factor);
-                tc::tmem_st16(to, ov);
+                tc::tmem_st32(to, ov);
               }
             }
             weights(add);
           }
+          tc::tmem_st16(tS, hi);
+          tc::tmem_st16(tS + 16, lo);
           lsum += sum;
           tc::tmem_st_wait();
-          tc::tc_fence_before();
         }
+        tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          tc::mbar_arrive(&sh.s_free[b]);
-          tc::mbar_arrive(&sh.sc_empty[slot]);
-        }
-        // the unit's last tile: stale V rows past the end (NaN codes) times zero must stay zero
-        if (half == 0 && j * kBN + kBN > kv_len) {
-          const int st = kt % kVStages;
+        // the unit's last tile: stale V rows past the end (NaN codes) times zero must stay zero;
+        // each half clears its own 64 keys' rows
+        if (j * kBN + kBN > kv_len) {
+          const int st = kt % kVStages, row = half * 64 + (m >> 1);
           ok &= wait1(&sh.v_full[st], kt / kVStages, abort_flag);
-          if (j * kBN + m >= kv_len) {
-            uint4* row = reinterpret_cast<uint4*>(sV + st * kTile + m * 128);
+          if (j * kBN + row >= kv_len) {
+            uint4* to = reinterpret_cast<uint4*>(sV + st * kTile + row * 128 + (m & 1) * 64);
 #pragma unroll
-            for (int x8 = 0; x8 < 8; ++x8) row[x8] = make_uint4(0, 0, 0, 0);
+            for (int c = 0; c < 4; ++c) to[c] = make_uint4(0, 0, 0, 0);
           }
           tc::fence_proxy_async_smem();
           __syncwarp();
         }
-        if (lane == 0) tc::mbar_arrive(&sh.p_full[b]);
+        if (lane == 0) {
+          tc::mbar_arrive(&sh.sc_empty[slot]);
+          tc::mbar_arrive(&sh.p_full[half][b]);
+        }
       }
       if (li > 1) ok &= wait1(&sh.sum_free[par], (li >> 1) - 1, abort_flag);
       sh.sum[par][half][m] = lsum;
-      if (half == 0) sh.add[par][m] = add;
+      sh.add[par][half][m] = add;
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sh.sum_full[par]);
     }
@@ -978,9 +977,14 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
       const int t = cur.mt * d.tpt + tl;
       const bool valid = tl < d.tpt && t < cur.T;
       ok &= idle_wait(&sh.sum_full[par], li >> 1, abort_flag);
-      const float l = sh.sum[par][0][m] + sh.sum[par][1][m], add = sh.add[par][m];
+      // the halves' accumulators on the larger of their references
+      const float a0 = sh.add[par][0][m], a1 = sh.add[par][1][m], add = fminf(a0, a1);
+      float w0 = a0 == INFINITY ? 0.f : ex2(add - a0), w1 = a1 == INFINITY ? 0.f : ex2(add - a1);
+      const float l = sh.sum[par][0][m] * w0 + sh.sum[par][1][m] * w1;
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const float lse2 = l > 0.f ? log2f(l) - add : -INFINITY;
+      w0 *= inv;
+      w1 *= inv;
       const size_t row = cur.slot < 0 ? size_t(cur.o + t) * a.H_q + cur.h * a.G + gl
                                       : size_t(cur.slot) * kRows + m;
       __syncwarp();
@@ -989,12 +993,13 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
       __syncwarp();
       tc::tc_fence_after();
 #pragma unroll 1
-      for (int c0 = 0; c0 < 128; c0 += 32) {
-        uint32_t ov[32];
+      for (int c0 = 0; c0 < 128; c0 += 16) {
+        uint32_t o0[16], o1[16];
         __syncwarp();
-        tc::tmem_ld32(tmem + lane_addr + kTmemO + c0, ov);
+        tc::tmem_ld16(tmem + lane_addr + kTmemO + c0, o0);
+        tc::tmem_ld16(tmem + lane_addr + kTmemO + 128 + c0, o1);
         tc::tmem_ld_wait();
-        if (c0 == 96) {                              // O is read: the next unit may begin
+        if (c0 == 112) {                             // O is read: the next unit may begin
           tc::tc_fence_before();
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&sh.o_free);
@@ -1002,10 +1007,13 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
         // (a row that saw nothing may hold whatever P's other rows left: 0 by definition)
         if (!valid) continue;
 #pragma unroll
-        for (int e = 0; e < 32; e += 8) {
+        for (int e = 0; e < 16; e += 8) {
           float v[8];
 #pragma unroll
-          for (int u = 0; u < 8; ++u) v[u] = l > 0.f ? __uint_as_float(ov[e + u]) * inv : 0.f;
+          for (int u = 0; u < 8; ++u) {
+            v[u] = w0 > 0.f ? __uint_as_float(o0[e + u]) * w0 : 0.f;
+            if (w1 > 0.f) v[u] = fmaf(__uint_as_float(o1[e + u]), w1, v[u]);
+          }
           if (cur.slot < 0) {
             uint32_t w[4];
 #pragma unroll

@@ -486,17 +486,15 @@ __device__ __forceinline__ void split_p2(float a, float b, uint32_t& hi, uint32_
 // four weights (below 2^13) as two pieces of four codes: hi in e5m2, the upper byte of the fp16
 // value rounded to nearest, lo = e4m3 of the exact remainder (at most an eighth)
 __device__ __forceinline__ void split_p4(const float (&p)[4], uint32_t& hi, uint32_t& lo) {
-  uint32_t w0, w1, r0, r1;
-  uint16_t l0, l1;
-  asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(w0) : "f"(p[0]), "f"(p[1]));
-  asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(w1) : "f"(p[2]), "f"(p[3]));
-  const uint32_t h0 = (w0 + 0x00800080u) & 0xFF00FF00u, h1 = (w1 + 0x00800080u) & 0xFF00FF00u;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r0) : "r"(w0), "r"(h0));
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r1) : "r"(w1), "r"(h1));
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l0) : "r"(r0));
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l1) : "r"(r1));
-  hi = __byte_perm(h0, h1, 0x7531);
-  lo = uint32_t(l0) | (uint32_t(l1) << 16);
+  asm("{\n\t.reg .b32 w0, w1, h0, h1, r0, r1;\n\t.reg .b16 l0, l1;\n\t"
+      "cvt.rn.f16x2.f32 w0, %3, %2;\n\tcvt.rn.f16x2.f32 w1, %5, %4;\n\t"
+      "add.u32 h0, w0, 0x00800080;\n\tadd.u32 h1, w1, 0x00800080;\n\t"
+      "and.b32 h0, h0, 0xFF00FF00;\n\tand.b32 h1, h1, 0xFF00FF00;\n\t"
+      "sub.rn.f16x2 r0, w0, h0;\n\tsub.rn.f16x2 r1, w1, h1;\n\t"
+      "prmt.b32 %0, h0, h1, 0x7531;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 l0, r0;\n\tcvt.rn.satfinite.e4m3x2.f16x2 l1, r1;\n\t"
+      "mov.b32 %1, {l0, l1};\n\t}"
+      : "=r"(hi), "=r"(lo) : "f"(p[0]), "f"(p[1]), "f"(p[2]), "f"(p[3]));
 }
 
 // 32 lanes x 8 consecutive 32-bit columns
