@@ -445,7 +445,7 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
     auto put_q = [&](int li, const Unit& u) {
       const int b = li & 1, c = lane & 15;
       uint8_t* p = sQ + b * L::kPair;
-      if (li > 1) ok &= idle_wait(&sh.q_empty[b], (li >> 1) - 1, abort_flag);
+      if (li > 1) ok &= wait1(&sh.q_empty[b], (li >> 1) - 1, abort_flag);
 #pragma unroll 1
       for (int n = q * 2 + (lane >> 4); n < NR; n += 8) {
         const int t = n / a.G, g = n - t * a.G;
@@ -484,7 +484,7 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
       const bool has_after = has_next && fetch(li + 2, after);
       const int par = li & 1;
       const int nrows = cur.T * a.G;                 // <= NR
-      ok &= idle_wait(&sh.sum_full[par], li >> 1, abort_flag);
+      ok &= wait1(&sh.sum_full[par], li >> 1, abort_flag);
       // lane n: row n's place, the weights of the two groups' accumulators, its log-sum-exp
       const int rn = lane < NR ? lane : 0, rt = rn / a.G;
       const int row = cur.slot < 0 ? (cur.o + rt) * a.H_q + cur.h * a.G + (rn - rt * a.G)
@@ -504,7 +504,7 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
       const float lse2 = l > 0.f ? log2f(l) - top : -INFINITY;
       w0 *= inv;
       w1 *= inv;
-      ok &= idle_wait(&sh.o_full[par], li >> 1, abort_flag);
+      ok &= wait1(&sh.o_full[par], li >> 1, abort_flag);
       __syncwarp();
       tc::tc_fence_after();
       // (an accumulator that took no product in this unit has weight 0 and stale columns)
@@ -929,7 +929,7 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
     auto put_q = [&](int li, const Unit& u) {
       const int b = li & 1, c = lane & 15;
       uint8_t* p = sQ + b * kPair;
-      if (li > 1) ok &= idle_wait(&sh.q_empty[b], (li >> 1) - 1, abort_flag);
+      if (li > 1) ok &= wait1(&sh.q_empty[b], (li >> 1) - 1, abort_flag);
       auto load = [&](int n) -> uint4 {
         const int rl = n / a.G, g = n - rl * a.G, t = u.mt * d.tpt + rl;
         if (n >= kRows || rl >= d.tpt || t >= u.T) return make_uint4(0, 0, 0, 0);
@@ -976,7 +976,7 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
       const int par = li & 1;
       const int t = cur.mt * d.tpt + tl;
       const bool valid = tl < d.tpt && t < cur.T;
-      ok &= idle_wait(&sh.sum_full[par], li >> 1, abort_flag);
+      ok &= wait1(&sh.sum_full[par], li >> 1, abort_flag);
       // the halves' accumulators on the larger of their references
       const float a0 = sh.add[par][0][m], a1 = sh.add[par][1][m], add = fminf(a0, a1);
       float w0 = a0 == INFINITY ? 0.f : ex2(add - a0), w1 = a1 == INFINITY ? 0.f : ex2(add - a1);

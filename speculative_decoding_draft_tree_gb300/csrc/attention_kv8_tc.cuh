@@ -268,27 +268,29 @@ __device__ __forceinline__ void write_merge_record(const TcDev& d, const Range& 
 }
 
 // ------------------------------------------------------------------------------ waits
-__device__ __forceinline__ bool wait1(uint64_t* bar, int parity, volatile int* abort) {
-  return tc::mbar_wait(bar, uint32_t(parity & 1), abort, kWaitLimit);
+// One look at a barrier's phase that lets the hardware suspend the thread for up to ~20 us: a
+// waiting warp leaves its issue slots to the others.  (Polling took a quarter of all instructions.)
+__device__ __forceinline__ bool try_wait_suspended(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(tc::smem_u32(bar)), "r"(parity), "r"(20000u) : "memory");
+  return ok != 0;
 }
-// The same for roles that run ahead of or behind the tiles: they look again every ~100 ns and
-// leave the shared-memory pipe to the warps on the critical path.
-__device__ __forceinline__ bool idle_wait(uint64_t* bar, int parity, volatile int* abort) {
+__device__ __forceinline__ bool wait1(uint64_t* bar, int parity, volatile int* abort) {
   if (tc::mbar_try_wait(bar, uint32_t(parity & 1))) return true;
   const long long t0 = clock64();
 #pragma unroll 1
-  while (true) {
-    if (tc::mbar_try_wait(bar, uint32_t(parity & 1))) return true;
+  while (!try_wait_suspended(bar, uint32_t(parity & 1)))
     if (*abort || clock64() - t0 > kWaitLimit) return false;
-    __nanosleep(100);
-  }
+  return true;
 }
 // one lane waits, the warp gets the outcome
-template <bool kIdle>
 __device__ __forceinline__ bool lane0_wait(uint64_t* bar, int parity, volatile int* abort) {
   bool r = true;
-  if ((threadIdx.x & 31) == 0)
-    r = kIdle ? idle_wait(bar, parity, abort) : wait1(bar, parity, abort);
+  if ((threadIdx.x & 31) == 0) r = wait1(bar, parity, abort);
   return __shfl_sync(0xffffffffu, r ? 1 : 0, 0) != 0;
 }
 
@@ -305,7 +307,7 @@ __device__ __forceinline__ void item_producer(const TcDev& d, const Range& R, It
     more = iter.next(d, R, it);
     if (!more) it.r = -1;
     const int s = li % kItemRing;
-    if (li >= kItemRing && !idle_wait(&ring.empty[s], li / kItemRing - 1, abort)) return;
+    if (li >= kItemRing && !wait1(&ring.empty[s], li / kItemRing - 1, abort)) return;
     ring.item[s] = it;
     tc::mbar_arrive(&ring.full[s]);
   }
@@ -347,7 +349,7 @@ __device__ __forceinline__ void page_producer(const TcDev& d, ItemRing& items,
 #pragma unroll 1
     for (int j = it.j0; j < it.j1; ++j) {
       const int after = page_of(j + 2);
-      if (use > 0 && !lane0_wait<false>(empty + st, use - 1, abort_flag)) {
+      if (use > 0 && !lane0_wait(empty + st, use - 1, abort_flag)) {
         ok = false;
         break;
       }
@@ -434,7 +436,7 @@ __device__ __forceinline__ void scale_producer(const TcDev& d, ItemRing& items, 
 #pragma unroll 1
       for (int u = 0; u < n; ++u) {
         const int use = (kt + u) / kScaleRing;
-        if (use > 0 && !lane0_wait<true>(empty + (kt + u) % kScaleRing, use - 1, abort_flag)) ok = false;
+        if (use > 0 && !lane0_wait(empty + (kt + u) % kScaleRing, use - 1, abort_flag)) ok = false;
       }
       if (!ok) break;
       if (sub < n) {
