@@ -556,11 +556,11 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
 // ------------------------------------------------------------------------------ long units
 namespace tile {
 constexpr int kRows = 128;
-constexpr int kThreads = 640;
-constexpr int kCtlRegs = 72;       // warps 0-3 and 16-19
-constexpr int kSoftmaxRegs = 120;  // warps 4-11
-constexpr int kOutRegs = 96;       // warps 12-15, as launched
-static_assert(256 * kCtlRegs + 256 * kSoftmaxRegs + 128 * kOutRegs <= kThreads * 96, "register split");
+constexpr int kThreads = 896;
+constexpr int kCtlRegs = 56;       // warps 0-3 and 24-27
+constexpr int kSoftmaxRegs = 80;   // warps 4-19
+constexpr int kOutRegs = 72;       // warps 20-23, as launched
+static_assert(256 * kCtlRegs + 512 * kSoftmaxRegs + 128 * kOutRegs <= kThreads * 72, "register split");
 // Weights are 2^(y - ref + kLift); the reference moves when one passes 2^kTop (hi reaches 57344, lo
 // takes an eighth).  lo's step is 2^-9, i.e. 2^-12 of a row's largest weight; below that hi alone
 // still has three bits.
@@ -582,7 +582,8 @@ struct Shared {
   uint64_t sc_full[kScaleRing], sc_empty[kScaleRing], drain[2];
   ScaleSlot sc[kScaleRing];
   float qmul[2][kRows];
-  float sum[2][2][kRows];         // per unit parity and half
+  float mx[4][kRows];             // per quarter of the keys: row maxima of an update
+  float sum[2][4][kRows];         // per unit parity and quarter
   float add[2][2][kRows];         // per unit parity and half: kLift - reference
   uint32_t tmem;
   int abort, r0, r1;
@@ -629,23 +630,23 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
       if (lane < n) tc::mbar_init(bar + lane, count);
     };
     init(sh.q_full, 2, 4);                   // the output warps
-    init(sh.q_empty, 2, 9);                  // the issuer's commit and the 8 softmax warps
+    init(sh.q_empty, 2, 17);                 // the issuer's commit and the 16 softmax warps
     init(sh.k_full, kKStages, 1);
     init(sh.k_empty, kKStages, 1);
     init(sh.v_full, kVStages, 1);
     init(sh.v_empty, kVStages, 1);
     init(sh.s_full, 2, 1);
-    init(&sh.p_full[0][0], 4, 4);
+    init(&sh.p_full[0][0], 4, 8);
     init(sh.pv_done, 2, 1);
-    init(sh.sum_full, 2, 8);
+    init(sh.sum_full, 2, 16);
     init(sh.sum_free, 2, 4);
     init(&sh.o_full, 1, 1);
     init(&sh.o_free, 1, 4);
     init(sh.sc_full, kScaleRing, 1);
-    init(sh.sc_empty, kScaleRing, 8);
+    init(sh.sc_empty, kScaleRing, 16);
     init(sh.drain, 2, 1);
     init(sh.items.full, kItemRing, 1);
-    init(sh.items.empty, kItemRing, 17);     // warps 0-16
+    init(sh.items.empty, kItemRing, 25);     // warps 0-24
     if (lane == 0) sh.abort = 0;
     tc::fence_mbar_init();
   }
@@ -657,16 +658,16 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
   const uint32_t tmem = sh.tmem;
   volatile int* abort_flag = &sh.abort;
 
-  if (warp < 4 || warp >= 16) {
+  if (warp < 4 || warp >= 24) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtlRegs));
     if (warp == 0 || warp == 2) {
       const bool k = warp == 0;
       page_producer(d, sh.items, k ? &mK : &mV, k ? &mKw : &mVw, k ? kKStages : kVStages,
                     k ? sK : sV, k ? sh.k_full : sh.v_full, k ? sh.k_empty : sh.v_empty, k,
                     &sh.abort);
-    } else if (warp == 16) {
+    } else if (warp == 24) {
       scale_producer(d, sh.items, sh.sc, sh.sc_full, sh.sc_empty, &sh.abort);
-    } else if (warp == 17) {
+    } else if (warp == 25) {
       const Range R = warp_range(d);
       if (lane == 0) {
         sh.r0 = R.r0;
@@ -677,47 +678,37 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
       __syncwarp();
     } else if (warp == 1 || warp == 3) {
       // =================================================================== MMA issuers
-      if (lane == 0) {
-        const bool is_qk = warp == 1;
-        const uint32_t id_qk = idesc_e4m3(128, 128, false, false);
-        const uint32_t id_lo = idesc_e4m3(128, 128, false, true), id_hi = id_lo | kIdescAE5m2;
-        const uint64_t dQ = tc::smem_desc(tc::smem_u32(sQ), 16, 1024);
-        const uint64_t dK = tc::smem_desc(tc::smem_u32(sK), 16, 1024);
-        const uint64_t dV = tc::smem_desc(tc::smem_u32(sV), kTile, 1024);
-        int kt = 0;
-        bool ok = true;
+      // the whole warp walks the tiles, so that addresses and descriptors are uniform values; one
+      // elected lane issues
+      const bool is_qk = warp == 1;
+      const uint32_t id_qk = idesc_e4m3(128, 128, false, false);
+      const uint32_t id_lo = idesc_e4m3(128, 128, false, true), id_hi = id_lo | kIdescAE5m2;
+      const uint64_t dQ = tc::smem_desc(tc::smem_u32(sQ), 16, 1024);
+      const uint64_t dK = tc::smem_desc(tc::smem_u32(sK), 16, 1024);
+      const uint64_t dV = tc::smem_desc(tc::smem_u32(sV), kTile, 1024);
+      int kt = 0;
+      bool ok = true;
+      Item it;
 #pragma unroll 1
-        for (int li = 0; ok; ++li) {
-          Item it;                     // (one lane: its own wait and arrival)
-          {
-            const int s = li % kItemRing;
-            ok = wait1(&sh.items.full[s], li / kItemRing, abort_flag);
-            it = sh.items.item[s];
-            tc::mbar_arrive(&sh.items.empty[s]);
-            if (!ok || it.r < 0) break;
-          }
-          const int par = li & 1;
-          if (is_qk ? !wait1(&sh.q_full[par], li >> 1, abort_flag)
-                    : (li > 0 && !wait1(&sh.o_free, li - 1, abort_flag))) {
-            ok = false;
-            break;
-          }
+      for (int li = 0; ok && __all_sync(0xffffffffu, next_item(sh.items, li, it, abort_flag)); ++li) {
+        const int par = li & 1;
+        if (is_qk) ok = wait1(&sh.q_full[par], li >> 1, abort_flag);
+        else if (li > 0) ok = wait1(&sh.o_free, li - 1, abort_flag);
 #pragma unroll 1
-          for (int j = it.j0; j < it.j1; ++j, ++kt) {
-            const int b = kt & 1, use = kt >> 1;
-            if (is_qk) {
-              const int st = kt % kKStages;
-              const int slot = kt % kScaleRing;
-              if (!wait1(&sh.sc_full[slot], kt / kScaleRing, abort_flag) ||
-                  !wait1(&sh.k_full[st], kt / kKStages, abort_flag) ||
-                  (use > 0 && !wait1(&sh.pv_done[b], use - 1, abort_flag))) {
-                ok = false;
-                break;
-              }
-              tc::tc_fence_after();
-              const uint32_t tS = tmem + b * 128;
-              const uint64_t kb = dK + uint64_t(st) * (kTile >> 4);
-              const uint64_t qa = dQ + uint64_t(par) * (kPair >> 4);
+        for (int j = it.j0; j < it.j1; ++j, ++kt) {
+          const int b = kt & 1, use = kt >> 1;
+          if (is_qk) {
+            const int st = kt % kKStages, slot = kt % kScaleRing;
+            ok = ok && wait1(&sh.sc_full[slot], kt / kScaleRing, abort_flag) &&
+                 wait1(&sh.k_full[st], kt / kKStages, abort_flag) &&
+                 (use == 0 || wait1(&sh.pv_done[b], use - 1, abort_flag));
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc::tc_fence_after();
+            const uint32_t tS = tmem + b * 128;
+            const uint64_t kb = dK + uint64_t(st) * (kTile >> 4);
+            const uint64_t qa = dQ + uint64_t(par) * (kPair >> 4);
+            if (elect_one()) {
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 mma_e4m3_ss(tS, qa + 2 * k, kb + 2 * k, id_qk, k > 0 ? 1u : 0u);
@@ -726,53 +717,62 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
               tc::mma_commit(&sh.s_full[b]);
               tc::mma_commit(&sh.k_empty[st]);
               if (j == it.j1 - 1) tc::mma_commit(&sh.q_empty[par]);
-            } else {
-              const int st = kt % kVStages;
-              if (!wait1(&sh.v_full[st], kt / kVStages, abort_flag)) {
-                ok = false;
-                break;
-              }
-              const uint64_t vb = dV + uint64_t(st) * (kTile >> 4);
-              const uint32_t acc = j > it.j0 ? 1u : 0u;
+            }
+            __syncwarp();
+          } else {
+            const int st = kt % kVStages;
+            ok = ok && wait1(&sh.v_full[st], kt / kVStages, abort_flag);
+            const uint64_t vb = dV + uint64_t(st) * (kTile >> 4);
+            const uint32_t acc = j > it.j0 ? 1u : 0u;
 #pragma unroll
-              for (int hf = 0; hf < 2; ++hf) {     // a half's 64 slots into its accumulator
-                ok = ok && wait1(&sh.p_full[hf][b], use, abort_flag);
-                tc::tc_fence_after();
-                const uint32_t tO = tmem + kTmemO + hf * 128, tP = tmem + b * 128 + hf * 64;
+            for (int hf = 0; hf < 2; ++hf) {       // a half's 64 slots into its accumulator
+              ok = __all_sync(0xffffffffu, ok && wait1(&sh.p_full[hf][b], use, abort_flag));
+              if (!ok) break;
+              tc::tc_fence_after();
+              const uint32_t tO = tmem + kTmemO + hf * 128;
+              if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {      // 32 slots: 8 columns of P, 32 rows of V
                   const uint64_t vk = vb + (2 * hf + k) * (4096 >> 4);
-                  mma_e4m3_ts(tO, tP + 8 * k, vk, id_hi, k > 0 ? 1u : acc);
-                  mma_e4m3_ts(tO, tP + 16 + 8 * k, vk, id_lo, 1u);
+                  const uint32_t tP = tmem + b * 128 + hf * 64 + k * 32;
+                  mma_e4m3_ts(tO, tP, vk, id_hi, k > 0 ? 1u : acc);
+                  mma_e4m3_ts(tO, tP + 8, vk, id_lo, 1u);
+                }
+                if (hf == 1) {
+                  tc::mma_commit(&sh.v_empty[st]);
+                  tc::mma_commit(&sh.pv_done[b]);
+                  if (j == it.j1 - 1) tc::mma_commit(&sh.o_full);
                 }
               }
-              if (!ok) break;
-              tc::mma_commit(&sh.v_empty[st]);
-              tc::mma_commit(&sh.pv_done[b]);
-              if (j == it.j1 - 1) tc::mma_commit(&sh.o_full);
+              __syncwarp();
             }
+            if (!ok) break;
           }
         }
-        if (!ok) *abort_flag = 1;
-        tc::mma_commit(&sh.drain[is_qk ? 0 : 1]);
-        volatile int never = 0;
-        tc::mbar_wait(&sh.drain[is_qk ? 0 : 1], 0, &never, kWaitLimit / 8);
       }
+      if (!ok) *abort_flag = 1;
+      // nothing issued here may still run when TMEM is released (bounded, abort or not)
+      if (elect_one()) tc::mma_commit(&sh.drain[is_qk ? 0 : 1]);
+      __syncwarp();
+      volatile int never = 0;
+      tc::mbar_wait(&sh.drain[is_qk ? 0 : 1], 0, &never, kWaitLimit / 8);
       __syncwarp();
     }
-  } else if (warp < 12) {
+  } else if (warp < 20) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ===================================================================== softmax
-    const int half = (warp - 4) >> 2, q = warp & 3;
+    const int part = (warp - 4) >> 2, half = part >> 1, q = warp & 3;   // quarter, half of the keys
     const uint32_t lane_addr = uint32_t(q * 32) << 16;
     const int m = q * 32 + lane;                     // this thread's row of the tile
+    const int bar_h = 1 + half * 4 + q;              // the two warps of these rows and this half
     const int tl = m / a.G;
     int kt = 0;
     bool ok = true;                                  // no early exit: see the file's comment
     Item it;
 #pragma unroll 1
     for (int li = 0;; ++li) {
-      if (!__all_sync(0xffffffffu, next_item(sh.items, li, it, abort_flag))) break;
+      // the pair leaves together: an expired wait in one must not leave the other at a barrier
+      if (bar_any(bar_h, 64, !next_item(sh.items, li, it, abort_flag))) break;
       const int par = li & 1;
       const int P = it.P, kv_len = it.P + it.T;
       const int t = it.mt * d.tpt + tl;
@@ -788,41 +788,37 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
 #pragma unroll 1
       for (int j = it.j0; j < it.j1; ++j, ++kt) {
         const int b = kt & 1, use = kt >> 1, slot = kt % kScaleRing;
-        const int key0 = j * kBN + half * 64;
+        const int key0 = j * kBN + part * 32;
         ok &= wait1(&sh.s_full[b], use, abort_flag);   // (the issuer has waited for the scales)
         __syncwarp();
         tc::tc_fence_after();
         if (live) {
           const ScaleSlot& sc = sh.sc[slot];
-          const uint32_t tS = tmem + lane_addr + b * 128 + half * 64;
-          // the weights of this thread's 64 keys against the reference kLift - add, as the two
+          const uint32_t tS = tmem + lane_addr + b * 128 + part * 32;
+          // the weights of this thread's 32 keys against the reference kLift - add, as the two
           // pieces of P; `top`: the largest exponent, `sum`: of the weights over the V scales
           float top, sum;
-          uint32_t hi[16], lo[16];
+          uint32_t hi[8], lo[8];
           auto weights = [&](float add) {
             const float shift = add == INFINITY ? 0.f : add;   // no key seen yet
-            uint32_t x[2][32];
-            tc::tmem_ld32(tS, x[0]);
-            tc::tmem_ld32(tS + 32, x[1]);
+            uint32_t x[32];
+            tc::tmem_ld32(tS, x);
             tc::tmem_ld_wait();
-            if (key0 + 64 > P) {
+            if (key0 + 32 > P) {
+              const int pre = P - key0, left = kv_len - key0;
+              uint32_t vis = anc_window(arow, a.W, key0 - P);
+              vis |= pre >= 32 ? 0xFFFFFFFFu : pre > 0 ? (1u << pre) - 1u : 0u;
+              // (mask bits past the tree count for nothing)
+              vis &= left >= 32 ? 0xFFFFFFFFu : left > 0 ? (1u << left) - 1u : 0u;
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                const int k0 = key0 + 32 * c, pre = P - k0, left = kv_len - k0;
-                uint32_t vis = anc_window(arow, a.W, k0 - P);
-                vis |= pre >= 32 ? 0xFFFFFFFFu : pre > 0 ? (1u << pre) - 1u : 0u;
-                // (mask bits past the tree count for nothing)
-                vis &= left >= 32 ? 0xFFFFFFFFu : left > 0 ? (1u << left) - 1u : 0u;
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (!((vis >> e) & 1u)) x[c][e] = __float_as_uint(-INFINITY);
-              }
+              for (int e = 0; e < 32; ++e)
+                if (!((vis >> e) & 1u)) x[e] = __float_as_uint(-INFINITY);
             }
             top = -INFINITY;
             sum = 0.f;
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {              // 16 keys of one page
-              const int page = (half * 64 + 16 * g) >> d.log2bs;
+            for (int g = 0; g < 2; ++g) {              // 16 keys of one page
+              const int page = (part * 32 + 16 * g) >> d.log2bs;
               // (never 0, which would make a masked key's -infinity a NaN)
               const float mul = fmaxf(sc.k[page] * qm, FLT_MIN), lift = sc.lv[page] + shift;
               const uint64_t mul2 = f2_pack(mul, mul), lift2 = f2_pack(lift, lift);
@@ -832,7 +828,7 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
                 float z[4], p[4];
 #pragma unroll
                 for (int u = 0; u < 4; u += 2) {
-                  const uint32_t* xe = &x[g >> 1][(g & 1) * 16 + e + u];
+                  const uint32_t* xe = &x[16 * g + e + u];
                   f2_unpack(f2_fma(f2_pack(__uint_as_float(xe[0]), __uint_as_float(xe[1])), mul2, lift2),
                             z[u], z[u + 1]);
                 }
@@ -850,8 +846,10 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
           // The weights are formed on the expectation that the tile does not move a row's reference,
           // and formed again where it does (they stay in registers until then: P lies over S).
           weights(add);
-          if (__any_sync(0xffffffffu, top + add > kTop)) {
-            const float ref = fmaxf(top, kLift - add), next = kLift - ref;
+          if (bar_any(bar_h, 64, top + add > kTop)) {
+            sh.mx[part][m] = top;
+            bar_sync(bar_h, 64);
+            const float ref = fmaxf(fmaxf(top, sh.mx[part ^ 1][m]), kLift - add), next = kLift - ref;
             const float factor = add == INFINITY ? 1.f : ex2(next - add);
             add = next;
             lsum *= factor;
@@ -860,9 +858,10 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
               __syncwarp();
               tc::tc_fence_after();
 #pragma unroll 1
-              for (int c0 = 0; c0 < 128; c0 += 32) {
+              for (int c0 = 0; c0 < 64; c0 += 32) {    // each of the pair half the columns
                 uint32_t ov[32];
-                const uint32_t to = tmem + lane_addr + kTmemO + half * 128 + c0;
+                const uint32_t to =
+                    tmem + lane_addr + kTmemO + half * 128 + (part & 1) * 64 + c0;
                 tc::tmem_ld32(to, ov);
                 tc::tmem_ld_wait();
 #pragma unroll
@@ -873,22 +872,22 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
             }
             weights(add);
           }
-          tc::tmem_st16(tS, hi);
-          tc::tmem_st16(tS + 16, lo);
+          tmem_st8(tS, hi);
+          tmem_st8(tS + 8, lo);
           lsum += sum;
           tc::tmem_st_wait();
         }
         tc::tc_fence_before();
         __syncwarp();
         // the unit's last tile: stale V rows past the end (NaN codes) times zero must stay zero;
-        // each half clears its own 64 keys' rows
+        // each quarter clears its own 32 keys' rows
         if (j * kBN + kBN > kv_len) {
-          const int st = kt % kVStages, row = half * 64 + (m >> 1);
+          const int st = kt % kVStages, row = part * 32 + (m >> 2);
           ok &= wait1(&sh.v_full[st], kt / kVStages, abort_flag);
           if (j * kBN + row >= kv_len) {
-            uint4* to = reinterpret_cast<uint4*>(sV + st * kTile + row * 128 + (m & 1) * 64);
+            uint4* to = reinterpret_cast<uint4*>(sV + st * kTile + row * 128 + (m & 3) * 32);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) to[c] = make_uint4(0, 0, 0, 0);
+            for (int c = 0; c < 2; ++c) to[c] = make_uint4(0, 0, 0, 0);
           }
           tc::fence_proxy_async_smem();
           __syncwarp();
@@ -899,8 +898,8 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
         }
       }
       if (li > 1) ok &= wait1(&sh.sum_free[par], (li >> 1) - 1, abort_flag);
-      sh.sum[par][half][m] = lsum;
-      sh.add[par][half][m] = add;
+      sh.sum[par][part][m] = lsum;
+      if (!(part & 1)) sh.add[par][half][m] = add;
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sh.sum_full[par]);
     }
@@ -980,7 +979,8 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
       // the halves' accumulators on the larger of their references
       const float a0 = sh.add[par][0][m], a1 = sh.add[par][1][m], add = fminf(a0, a1);
       float w0 = a0 == INFINITY ? 0.f : ex2(add - a0), w1 = a1 == INFINITY ? 0.f : ex2(add - a1);
-      const float l = sh.sum[par][0][m] * w0 + sh.sum[par][1][m] * w1;
+      const float l = (sh.sum[par][0][m] + sh.sum[par][1][m]) * w0 +
+                      (sh.sum[par][2][m] + sh.sum[par][3][m]) * w1;
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const float lse2 = l > 0.f ? log2f(l) - add : -INFINITY;
       w0 *= inv;
