@@ -572,19 +572,20 @@ constexpr int kSmemQ = 0;                                // 2 buffers
 constexpr int kSmemK = kSmemQ + 2 * kPair;
 constexpr int kSmemV = kSmemK + kKStages * kTile;
 constexpr int kSmemBar = kSmemV + kVStages * kTile;
-constexpr uint32_t kTmemO = 256;
+constexpr int kBufs = 3;                                 // S, with P over it
+constexpr uint32_t kTmemO = kBufs * 128;
 
 struct Shared {
   uint64_t q_full[2], q_empty[2];
   uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
-  uint64_t s_full[2], p_full[2][2], pv_done[2];
+  uint64_t s_full[kBufs], p_full[kBufs], pv_done[kBufs];
   uint64_t sum_full[2], sum_free[2], o_full, o_free;
   uint64_t sc_full[kScaleRing], sc_empty[kScaleRing], drain[2];
   ScaleSlot sc[kScaleRing];
   float qmul[2][kRows];
   float mx[4][kRows];             // per quarter of the keys: row maxima of an update
   float sum[2][4][kRows];         // per unit parity and quarter
-  float add[2][2][kRows];         // per unit parity and half: kLift - reference
+  float add[2][kRows];            // per unit parity: kLift - reference
   uint32_t tmem;
   int abort, r0, r1;
   ItemRing items;
@@ -635,9 +636,9 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
     init(sh.k_empty, kKStages, 1);
     init(sh.v_full, kVStages, 1);
     init(sh.v_empty, kVStages, 1);
-    init(sh.s_full, 2, 1);
-    init(&sh.p_full[0][0], 4, 8);
-    init(sh.pv_done, 2, 1);
+    init(sh.s_full, kBufs, 1);
+    init(sh.p_full, kBufs, 16);
+    init(sh.pv_done, kBufs, 1);
     init(sh.sum_full, 2, 16);
     init(sh.sum_free, 2, 4);
     init(&sh.o_full, 1, 1);
@@ -696,7 +697,7 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
         else if (li > 0) ok = wait1(&sh.o_free, li - 1, abort_flag);
 #pragma unroll 1
         for (int j = it.j0; j < it.j1; ++j, ++kt) {
-          const int b = kt & 1, use = kt >> 1;
+          const int b = kt % kBufs, use = kt / kBufs;
           if (is_qk) {
             const int st = kt % kKStages, slot = kt % kScaleRing;
             ok = ok && wait1(&sh.sc_full[slot], kt / kScaleRing, abort_flag) &&
@@ -721,32 +722,23 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
             __syncwarp();
           } else {
             const int st = kt % kVStages;
-            ok = ok && wait1(&sh.v_full[st], kt / kVStages, abort_flag);
-            const uint64_t vb = dV + uint64_t(st) * (kTile >> 4);
-            const uint32_t acc = j > it.j0 ? 1u : 0u;
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {       // a half's 64 slots into its accumulator
-              ok = __all_sync(0xffffffffu, ok && wait1(&sh.p_full[hf][b], use, abort_flag));
-              if (!ok) break;
-              tc::tc_fence_after();
-              const uint32_t tO = tmem + kTmemO + hf * 128;
-              if (elect_one()) {
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {      // 32 slots: 8 columns of P, 32 rows of V
-                  const uint64_t vk = vb + (2 * hf + k) * (4096 >> 4);
-                  const uint32_t tP = tmem + b * 128 + hf * 64 + k * 32;
-                  mma_e4m3_ts(tO, tP, vk, id_hi, k > 0 ? 1u : acc);
-                  mma_e4m3_ts(tO, tP + 8, vk, id_lo, 1u);
-                }
-                if (hf == 1) {
-                  tc::mma_commit(&sh.v_empty[st]);
-                  tc::mma_commit(&sh.pv_done[b]);
-                  if (j == it.j1 - 1) tc::mma_commit(&sh.o_full);
-                }
-              }
-              __syncwarp();
-            }
+            ok = __all_sync(0xffffffffu, ok && wait1(&sh.v_full[st], kt / kVStages, abort_flag) &&
+                                             wait1(&sh.p_full[b], use, abort_flag));
             if (!ok) break;
+            tc::tc_fence_after();
+            const uint64_t vb = dV + uint64_t(st) * (kTile >> 4);
+            const uint32_t tP = tmem + b * 128, acc = j > it.j0 ? 1u : 0u;
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {        // a quarter's 32 slots: 8 columns of P, 32 rows of V
+                mma_e4m3_ts(tmem + kTmemO, tP + 32 * k, vb + k * (4096 >> 4), id_hi, k > 0 ? 1u : acc);
+                mma_e4m3_ts(tmem + kTmemO, tP + 32 * k + 8, vb + k * (4096 >> 4), id_lo, 1u);
+              }
+              tc::mma_commit(&sh.v_empty[st]);
+              tc::mma_commit(&sh.pv_done[b]);
+              if (j == it.j1 - 1) tc::mma_commit(&sh.o_full);
+            }
+            __syncwarp();
           }
         }
       }
@@ -761,18 +753,18 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
   } else if (warp < 20) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ===================================================================== softmax
-    const int part = (warp - 4) >> 2, half = part >> 1, q = warp & 3;   // quarter, half of the keys
+    const int part = (warp - 4) >> 2, q = warp & 3;  // quarter of a tile's keys; of its rows
     const uint32_t lane_addr = uint32_t(q * 32) << 16;
     const int m = q * 32 + lane;                     // this thread's row of the tile
-    const int bar_h = 1 + half * 4 + q;              // the two warps of these rows and this half
+    const int bar_q = 1 + q;                         // the four warps of these rows
     const int tl = m / a.G;
     int kt = 0;
     bool ok = true;                                  // no early exit: see the file's comment
     Item it;
 #pragma unroll 1
     for (int li = 0;; ++li) {
-      // the pair leaves together: an expired wait in one must not leave the other at a barrier
-      if (bar_any(bar_h, 64, !next_item(sh.items, li, it, abort_flag))) break;
+      // the four leave together: an expired wait in one must not leave the others at a barrier
+      if (bar_any(bar_q, 128, !next_item(sh.items, li, it, abort_flag))) break;
       const int par = li & 1;
       const int P = it.P, kv_len = it.P + it.T;
       const int t = it.mt * d.tpt + tl;
@@ -787,7 +779,7 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
       float add = INFINITY, lsum = 0.f;
 #pragma unroll 1
       for (int j = it.j0; j < it.j1; ++j, ++kt) {
-        const int b = kt & 1, use = kt >> 1, slot = kt % kScaleRing;
+        const int b = kt % kBufs, use = kt / kBufs, slot = kt % kScaleRing;
         const int key0 = j * kBN + part * 32;
         ok &= wait1(&sh.s_full[b], use, abort_flag);   // (the issuer has waited for the scales)
         __syncwarp();
@@ -846,29 +838,26 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
           // The weights are formed on the expectation that the tile does not move a row's reference,
           // and formed again where it does (they stay in registers until then: P lies over S).
           weights(add);
-          if (bar_any(bar_h, 64, top + add > kTop)) {
+          if (bar_any(bar_q, 128, top + add > kTop)) {
             sh.mx[part][m] = top;
-            bar_sync(bar_h, 64);
-            const float ref = fmaxf(fmaxf(top, sh.mx[part ^ 1][m]), kLift - add), next = kLift - ref;
+            bar_sync(bar_q, 128);
+            const float ref = fmaxf(fmaxf(fmaxf(sh.mx[0][m], sh.mx[1][m]), fmaxf(sh.mx[2][m], sh.mx[3][m])),
+                                    kLift - add);
+            const float next = kLift - ref;
             const float factor = add == INFINITY ? 1.f : ex2(next - add);
             add = next;
             lsum *= factor;
             if (j > it.j0 && __any_sync(0xffffffffu, factor != 1.f)) {
-              ok &= wait1(&sh.pv_done[(kt - 1) & 1], (kt - 1) >> 1, abort_flag);
+              ok &= wait1(&sh.pv_done[(kt - 1) % kBufs], (kt - 1) / kBufs, abort_flag);
               __syncwarp();
               tc::tc_fence_after();
-#pragma unroll 1
-              for (int c0 = 0; c0 < 64; c0 += 32) {    // each of the pair half the columns
-                uint32_t ov[32];
-                const uint32_t to =
-                    tmem + lane_addr + kTmemO + half * 128 + (part & 1) * 64 + c0;
-                tc::tmem_ld32(to, ov);
-                tc::tmem_ld_wait();
+              uint32_t ov[32];                         // each of the four a quarter of the columns
+              const uint32_t to = tmem + lane_addr + kTmemO + part * 32;
+              tc::tmem_ld32(to, ov);
+              tc::tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  ov[e] = __float_as_uint(__uint_as_float(ov[e]) * factor);
-                tc::tmem_st32(to, ov);
-              }
+              for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * factor);
+              tc::tmem_st32(to, ov);
             }
             weights(add);
           }
@@ -894,12 +883,12 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
         }
         if (lane == 0) {
           tc::mbar_arrive(&sh.sc_empty[slot]);
-          tc::mbar_arrive(&sh.p_full[half][b]);
+          tc::mbar_arrive(&sh.p_full[b]);
         }
       }
       if (li > 1) ok &= wait1(&sh.sum_free[par], (li >> 1) - 1, abort_flag);
       sh.sum[par][part][m] = lsum;
-      if (!(part & 1)) sh.add[par][half][m] = add;
+      if (part == 0) sh.add[par][m] = add;
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sh.sum_full[par]);
     }
@@ -976,15 +965,10 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
       const int t = cur.mt * d.tpt + tl;
       const bool valid = tl < d.tpt && t < cur.T;
       ok &= wait1(&sh.sum_full[par], li >> 1, abort_flag);
-      // the halves' accumulators on the larger of their references
-      const float a0 = sh.add[par][0][m], a1 = sh.add[par][1][m], add = fminf(a0, a1);
-      float w0 = a0 == INFINITY ? 0.f : ex2(add - a0), w1 = a1 == INFINITY ? 0.f : ex2(add - a1);
-      const float l = (sh.sum[par][0][m] + sh.sum[par][1][m]) * w0 +
-                      (sh.sum[par][2][m] + sh.sum[par][3][m]) * w1;
+      const float l = (sh.sum[par][0][m] + sh.sum[par][1][m]) + (sh.sum[par][2][m] + sh.sum[par][3][m]);
+      const float add = sh.add[par][m];
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const float lse2 = l > 0.f ? log2f(l) - add : -INFINITY;
-      w0 *= inv;
-      w1 *= inv;
       const size_t row = cur.slot < 0 ? size_t(cur.o + t) * a.H_q + cur.h * a.G + gl
                                       : size_t(cur.slot) * kRows + m;
       __syncwarp();
@@ -993,13 +977,12 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
       __syncwarp();
       tc::tc_fence_after();
 #pragma unroll 1
-      for (int c0 = 0; c0 < 128; c0 += 16) {
-        uint32_t o0[16], o1[16];
+      for (int c0 = 0; c0 < 128; c0 += 32) {
+        uint32_t ov[32];
         __syncwarp();
-        tc::tmem_ld16(tmem + lane_addr + kTmemO + c0, o0);
-        tc::tmem_ld16(tmem + lane_addr + kTmemO + 128 + c0, o1);
+        tc::tmem_ld32(tmem + lane_addr + kTmemO + c0, ov);
         tc::tmem_ld_wait();
-        if (c0 == 112) {                             // O is read: the next unit may begin
+        if (c0 == 96) {                              // O is read: the next unit may begin
           tc::tc_fence_before();
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&sh.o_free);
@@ -1007,13 +990,10 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
         // (a row that saw nothing may hold whatever P's other rows left: 0 by definition)
         if (!valid) continue;
 #pragma unroll
-        for (int e = 0; e < 16; e += 8) {
+        for (int e = 0; e < 32; e += 8) {
           float v[8];
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            v[u] = w0 > 0.f ? __uint_as_float(o0[e + u]) * w0 : 0.f;
-            if (w1 > 0.f) v[u] = fmaf(__uint_as_float(o1[e + u]), w1, v[u]);
-          }
+          for (int u = 0; u < 8; ++u) v[u] = l > 0.f ? __uint_as_float(ov[e + u]) * inv : 0.f;
           if (cur.slot < 0) {
             uint32_t w[4];
 #pragma unroll
