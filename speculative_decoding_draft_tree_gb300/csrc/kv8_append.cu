@@ -29,14 +29,28 @@ struct AppendDev {
   int32_t* req_status;
   int64_t k_ld_bytes, v_ld_bytes;
   int32_t B, N, H_kv, d, bs, num_blocks, max_blocks, window;
+  uint32_t columns;   // CTAs over the (head, cache) units
 };
 
 constexpr int kAppendThreads = 256;
 constexpr int kHold = 8;   // vectors a thread keeps in registers
+constexpr int kAppendCtas = 304;
 
-template <typename T> struct Codes;   // the codes of one 16-byte vector of x
+// The codes of one 16-byte vector of x, and its largest magnitude: NaN is passed over, infinity is
+// not (the kernel looks again, element by element, where one turns up).
+template <typename T> struct Codes;
 template <> struct Codes<__nv_bfloat16> {
   using type = uint2;
+  __device__ __forceinline__ static uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  __device__ __forceinline__ static float top(float m, const uint4& v) {
+    const uint32_t k = 0x7FFF7FFFu;
+    const uint32_t a = max2(max2(v.x & k, v.y & k), max2(v.z & k, v.w & k));
+    return fmaxf(m, fmaxf(bf16_lo(a), bf16_hi(a)));
+  }
   __device__ __forceinline__ static type make(const float (&f)[8]) {
     return make_uint2(kv8::pack_e4m3x4(f[0], f[1], f[2], f[3]),
                       kv8::pack_e4m3x4(f[4], f[5], f[6], f[7]));
@@ -44,6 +58,10 @@ template <> struct Codes<__nv_bfloat16> {
 };
 template <> struct Codes<float> {
   using type = uint32_t;
+  __device__ __forceinline__ static float top(float m, const uint4& v) {
+    m = fmaxf(m, fmaxf(fabsf(__uint_as_float(v.x)), fabsf(__uint_as_float(v.y))));
+    return fmaxf(m, fmaxf(fabsf(__uint_as_float(v.z)), fabsf(__uint_as_float(v.w))));
+  }
   __device__ __forceinline__ static type make(const float (&f)[4]) {
     return kv8::pack_e4m3x4(f[0], f[1], f[2], f[3]);
   }
@@ -57,12 +75,14 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(AppendDev a)
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31;
   const int team = tid / kTeam, tt = tid % kTeam;
-  const int n0 = blockIdx.x * a.window, n1 = min(a.N, n0 + a.window);
+  // heads vary fastest over the CTAs: a token's heads are neighbours in x
+  const int win = int(blockIdx.x / a.columns), column = int(blockIdx.x - uint32_t(win) * a.columns);
+  const int n0 = win * a.window, n1 = min(a.N, n0 + a.window);
   // the request of token n0: as many requests end at or before it
   int r = 0;
   for (int i = 0; i < a.B; i += kAppendThreads)
     r += __syncthreads_count(i + tid < a.B && a.row_offset[i + tid + 1] <= n0);
-  const int unit = blockIdx.y * kTeams + team;      // (head, cache)
+  const int unit = column * kTeams + team;          // (head, cache)
   const bool mine = unit < 2 * a.H_kv;
   const int h = unit >> 1;
   const bool is_v = unit & 1;
@@ -71,6 +91,12 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(AppendDev a)
   uint8_t* cache = is_v ? a.v_cache : a.k_cache;
   float* scale = is_v ? a.v_scale : a.k_scale;
   const int vpr = a.d / E;                          // vectors per row
+  // a thread's vectors are kTeam apart: the same column of every (kTeam / vpr)-th row where a row's
+  // vectors divide the team
+  const bool even = kTeam % vpr == 0;
+  const int r0 = tt / vpr;
+  const char* const x0 = x + int64_t(r0) * ld + (tt - r0 * vpr) * 16;
+  const int64_t step = int64_t(kTeam / vpr) * ld;
   __shared__ float s_max[kAppendThreads / 32];
   int n = n0;
   while (n < n1 && r < a.B) {                       // uniform across the CTA
@@ -98,6 +124,29 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(AppendDev a)
     }
     const int lb = slot / a.bs;
     const int pb = lb < a.max_blocks ? a.block_table[size_t(r) * a.max_blocks + lb] : -1;
+    const int nv = mine ? seg * vpr : 0;            // this team's vectors
+    const char* const xn = x0 + int64_t(n) * ld;
+    auto load = [&](int q) -> uint4 {               // vector tt + q kTeam
+      if (even) return ld_stream16(xn + q * step);
+      const int i = tt + q * kTeam, rr = i / vpr;
+      return ld_stream16(x + int64_t(n + rr) * ld + (i - rr * vpr) * 16);
+    };
+    uint4 v[kHold];
+    float m = 0.f;
+    // (the rows are on their way before the page id is looked at)
+#pragma unroll
+    for (int q = 0; q < kHold; ++q) {
+      const int i = tt + q * kTeam;
+      if (i < nv) v[q] = load(q);
+    }
+    // the next block's rows into L2
+    if (mine) {
+      const int lines = (int(a.d * sizeof(T)) + 127) / 128, rows = min(a.bs, n1 - (n + seg));
+      for (int i = tt; i < rows * lines; i += kTeam) {
+        const int rr = i / lines;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(x + int64_t(n + seg + rr) * ld + (i - rr * lines) * 128));
+      }
+    }
     if (pb < 0 || pb >= a.num_blocks) {
       if (tid == 0) atomicOr(&a.req_status[r], SPEC_REQ_BAD_BLOCK);
       n += seg;
@@ -105,39 +154,34 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(AppendDev a)
     }
     const size_t sidx = size_t(pb) * a.H_kv + (mine ? h : 0);
     uint8_t* page = cache + sidx * size_t(a.bs) * a.d;
-    const int nv = mine ? seg * vpr : 0;            // this team's vectors
     const float old = row > 0 ? scale[sidx] : 0.f;
-    auto load = [&](int i) -> uint4 {
-      const int rr = i / vpr, c = i - rr * vpr;
-      return ld_stream16(x + int64_t(n + rr) * ld + c * 16);
-    };
-    uint4 v[kHold];
-    float m = 0.f;
-    auto take = [&](const uint4& w) {
-      float f[E];
-      elem<T>::unpack(w, f);
+    // the team's maximum
+    auto over_team = [&](float m) -> float {
+      m = warp_max(m);
+      if (W > 1) {
+        __syncthreads();                            // s_max of the block before has been read
+        if (lane == 0) s_max[tid >> 5] = m;
+        __syncthreads();
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float ab = fabsf(f[e]);
-        m = ab <= FLT_MAX ? fmaxf(m, ab) : m;
+        for (int w = 0; w < W; ++w) m = fmaxf(m, s_max[team * W + w]);
       }
+      return m;
     };
-#pragma unroll
-    for (int q = 0; q < kHold; ++q) {
-      const int i = tt + q * kTeam;
-      if (i < nv) v[q] = load(i);
-    }
 #pragma unroll
     for (int q = 0; q < kHold; ++q)
-      if (tt + q * kTeam < nv) take(v[q]);
-    for (int i = tt + kHold * kTeam; i < nv; i += kTeam) take(load(i));
-    m = warp_max(m);
-    if (W > 1) {
-      __syncthreads();                              // s_max of the block before has been read
-      if (lane == 0) s_max[tid >> 5] = m;
-      __syncthreads();
+      if (tt + q * kTeam < nv) m = Codes<T>::top(m, v[q]);
+    for (int q = kHold; tt + q * kTeam < nv; ++q) m = Codes<T>::top(m, load(q));
+    m = over_team(m);
+    if (W > 1 ? __syncthreads_or(m > FLT_MAX) : m > FLT_MAX) {   // an infinity: finite values only
+      m = 0.f;
+#pragma unroll 1
+      for (int q = 0; tt + q * kTeam < nv; ++q) {
+        float f[E];
+        elem<T>::unpack(load(q), f);
 #pragma unroll
-      for (int w = 0; w < W; ++w) m = fmaxf(m, s_max[team * W + w]);
+        for (int e = 0; e < E; ++e) m = fabsf(f[e]) <= FLT_MAX ? fmaxf(m, fabsf(f[e])) : m;
+      }
+      m = over_team(m);
     }
     const float s = fmaxf(old, kv8::need_scale(m));
     // a power of two's reciprocal is exact, and so is multiplying by it (scales another writer
@@ -146,20 +190,32 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(AppendDev a)
     const bool pow2 = (sb & 0x807FFFFFu) == 0 && sb >= (uint32_t(kv8::kMinScaleExp) << 23) &&
                       sb <= (uint32_t(kv8::kMaxScaleExp) << 23);
     const float inv = pow2 ? __uint_as_float((254u << 23) - sb) : 0.f;
-    auto put = [&](int i, const uint4& w) {
-      float f[E];
-      elem<T>::unpack(w, f);
+    // E codes a vector, the rows of a block next to each other
+    auto* const to = reinterpret_cast<typename Codes<T>::type*>(page + size_t(row) * a.d) + tt;
+    if (pow2) {
+      auto put = [&](int q, const uint4& w) {
+        float f[E];
+        elem<T>::unpack(w, f);
 #pragma unroll
-      for (int e = 0; e < E; ++e) f[e] = pow2 ? f[e] * inv : __fdiv_rn(f[e], s);
-      // E codes a vector, the rows of a block next to each other
-      reinterpret_cast<typename Codes<T>::type*>(page + size_t(row) * a.d)[i] = Codes<T>::make(f);
-    };
+        for (int e = 0; e < E; ++e) f[e] *= inv;
+        to[q * kTeam] = Codes<T>::make(f);
+      };
 #pragma unroll
-    for (int q = 0; q < kHold; ++q) {
-      const int i = tt + q * kTeam;
-      if (i < nv) put(i, v[q]);
+      for (int q = 0; q < kHold; ++q)
+        if (tt + q * kTeam < nv) put(q, v[q]);
+      for (int q = kHold; tt + q * kTeam < nv; ++q) put(q, load(q));
+    } else {
+      // (apart from the loop above: with the division as a branch inside it, the whole kernel took
+      // 1.7 times as long)
+#pragma unroll 1
+      for (int q = 0; tt + q * kTeam < nv; ++q) {
+        float f[E];
+        elem<T>::unpack(load(q), f);
+#pragma unroll
+        for (int e = 0; e < E; ++e) f[e] = __fdiv_rn(f[e], s);
+        to[q * kTeam] = Codes<T>::make(f);
+      }
     }
-    for (int i = tt + kHold * kTeam; i < nv; i += kTeam) put(i, load(i));
     if (mine && row > 0 && s > old) {
       const float ratio = __fdiv_rn(old, s);
       uint4* p = reinterpret_cast<uint4*>(page);
@@ -174,9 +230,8 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(AppendDev a)
 
 template <typename T, int W>
 static cudaError_t launch_append(const AppendDev& d, cudaStream_t s) {
-  const int teams = kAppendThreads / (32 * W);
-  const dim3 grid((d.N + d.window - 1) / d.window, (2 * d.H_kv + teams - 1) / teams);
-  return launch_pdl(kv8_append_kernel<T, W>, grid, dim3(kAppendThreads), 0, s, d);
+  const long long ctas = (long long)d.columns * ((d.N + d.window - 1) / d.window);
+  return launch_pdl(kv8_append_kernel<T, W>, dim3(unsigned(ctas)), dim3(kAppendThreads), 0, s, d);
 }
 
 template <typename T>
@@ -223,8 +278,16 @@ extern "C" spec_status_t spec_kv8_append(const spec_kv8_append_params* p, spec_s
   d.v_ld_bytes = p->v_ld * es;
   d.B = p->B; d.N = p->N; d.H_kv = p->H_kv; d.d = p->head_dim; d.bs = p->block_size;
   d.num_blocks = p->num_blocks; d.max_blocks = p->max_blocks_per_req;
+  // Windows as long as they leave kAppendCtas CTAs: a CTA's first loads (which request, where it
+  // starts) are a chain of their own, so long calls give a CTA several blocks.
+  const int es4 = p->dtype == SPEC_BF16 ? 2 : 4;
+  const long long block_bytes = (long long)p->block_size * p->head_dim * es4;
+  const int teams = block_bytes <= 4096 ? 8 : block_bytes <= 8192 ? 4 : block_bytes <= 16384 ? 2 : 1;
+  const long long columns = (2LL * p->H_kv + teams - 1) / teams;
+  d.columns = uint32_t(columns);
   d.window = 1;
-  while (d.window < p->block_size && (long long)p->N * p->H_kv / d.window > 16384) d.window *= 2;
+  while (d.window < 8 * p->block_size && p->N * columns / (2 * d.window) >= kAppendCtas) d.window *= 2;
+  if (columns * ((p->N + d.window - 1) / d.window) >= (1LL << 31)) return SPEC_ERR_UNSUPPORTED;
   const cudaStream_t s = (cudaStream_t)stream;
   return launch_result(p->dtype == SPEC_BF16 ? launch_append_w<__nv_bfloat16>(d, s)
                                              : launch_append_w<float>(d, s));
