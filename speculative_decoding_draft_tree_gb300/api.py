@@ -90,6 +90,7 @@ class VerifyStep:
                                      self.path, self.n_acc, self.req_status, self.new_kv_len,
                                      self.slot_map, self.blocks_in_use, w.max_path)
         self.rope_p = None
+        self.kv8 = None
 
     def enable_rope(self, q_raw, k_new, v_new, base=10000.0, rotary_dim=None, interleaved=False,
                     fused=True):
@@ -99,11 +100,38 @@ class VerifyStep:
         inside the tree build's launch (spec_tree_build_rope_kv_write) instead of as a call of
         its own after it."""
         w = self.w
+        if self.kv8 is not None:
+            raise ValueError("enable_rope writes the 16- or 32-bit cache; with enable_kv8, pass "
+                             "rotated keys as k_new")
         self.rope_fused = fused
         self.rope_inputs = (q_raw, k_new, v_new)
         self.rope_p = B.rope_params(q_raw, w.q, k_new, v_new, self.k_layer0, self.v_layer0,
                                     w.block_table, w.prefix_len, w.node_offset, self.pos_id,
                                     self.req_status, base, rotary_dim, interleaved)
+
+    def enable_kv8(self, k_cache, v_cache, k_scale, v_scale, k_new, v_new):
+        """Run every round over an 8-bit cache instead of the workload's: codes [L, num_blocks,
+        H_kv, block_size, d] (torch.float8_e4m3fn or uint8) with scales [L, num_blocks, H_kv],
+        addressed by the workload's block table.  The round quantises the tree tokens' rows k_new,
+        v_new ([N, H_kv, d], keys already rotated) into layer 0's tree slots, attends over layer 0
+        and commits the accepted path in every layer."""
+        w = self.w
+        if self.rope_p is not None:
+            raise ValueError("enable_kv8 does not combine with enable_rope, which writes the 16- "
+                             "or 32-bit cache; pass rotated keys as k_new")
+        self.kv8 = (k_cache, v_cache, k_scale, v_scale, k_new, v_new)
+        self.kv8_append_p = B.kv8_append_params(k_new, v_new, k_cache[0], v_cache[0], k_scale[0],
+                                                v_scale[0], w.block_table, w.prefix_len,
+                                                w.node_offset, self.req_status)
+        self.kv8_attn = B.attention_kv8_params(w.q, k_cache[0], v_cache[0], k_scale[0], v_scale[0],
+                                               w.block_table, w.prefix_len, w.node_offset,
+                                               self.anc_mask, w.T_max, self.o, self.lse,
+                                               self.req_status)
+        self.kv8_ws = _ws(B.spec_attention_kv8_workspace_size(self.kv8_attn), w.target.device)
+        self.kv8_comp = B.kv8_compact_params(k_cache, v_cache, k_scale, v_scale, w.block_table,
+                                             w.prefix_len, self.path, self.n_acc, self.req_status,
+                                             self.new_kv_len, self.slot_map, self.blocks_in_use,
+                                             w.max_path)
 
     # individual stages ---------------------------------------------------------------------
     def tree_build_rope(self, stream=None):
@@ -120,18 +148,32 @@ class VerifyStep:
     def rope(self, stream=None):
         B.spec_tree_rope_kv_write(self.rope_p, stream)
 
+    def append(self, stream=None):
+        """The tree tokens' K/V rows into the 8-bit cache (enable_kv8 only)."""
+        B.spec_kv8_append(self.kv8_append_p, stream)
+
     def attention(self, stream=None):
-        B.spec_tree_attention(self.attn, self.attn_ws, stream)
+        if self.kv8 is not None:
+            B.spec_tree_attention_kv8(self.kv8_attn, self.kv8_ws, stream)
+        else:
+            B.spec_tree_attention(self.attn, self.attn_ws, stream)
 
     def verify(self, stream=None):
         B.spec_verify(self.ver, self.ver_ws, stream)
 
     def compact(self, stream=None):
-        B.spec_kv_compact(self.comp, stream)
+        if self.kv8 is not None:
+            B.spec_kv8_compact(self.kv8_comp, stream)
+        else:
+            B.spec_kv_compact(self.comp, stream)
 
     def verify_compact(self, stream=None):
         """verify() then compact() as one call (spec_verify_compact: one kernel for both when
-        the verification takes its one-launch form)."""
+        the verification takes its one-launch form; over an 8-bit cache always two calls)."""
+        if self.kv8 is not None:
+            self.verify(stream)
+            self.compact(stream)
+            return
         B.spec_verify_compact(self.ver, self.comp, self.ver_ws, stream)
 
     def run(self, stream=None):
@@ -139,13 +181,16 @@ class VerifyStep:
         (1 + 2 + 1 kernel launches on the stream; for trees of more than 32 nodes the
         verification and compaction take 1 + 1 launches in the walk form, the default from a
         vocabulary of 65536, and 2 + 1 in the two-launch form); with enable_rope, the tree build and
-        the rotary step share one launch, or run as two calls when fused=False."""
+        the rotary step share one launch, or run as two calls when fused=False.  With enable_kv8:
+        tree build, append, attention, verification and compaction over the 8-bit cache."""
         if self.rope_p is not None and self.rope_fused:
             self.tree_build_rope(stream)
         else:
             self.tree_build(stream)
             if self.rope_p is not None:
                 self.rope(stream)
+        if self.kv8 is not None:
+            self.append(stream)
         self.attention(stream)
         self.verify_compact(stream)
 
@@ -228,6 +273,8 @@ class VerifyStep:
         step = VerifyStep(dataclasses.replace(self.w, **fresh), self.sibling_rule,
                           self.lse is not None, self.verify_path)
         step._in_pack = pack
+        if self.kv8 is not None:
+            step.enable_kv8(*self.kv8)
         return step
 
     def host_output_buffers(self) -> Dict[str, torch.Tensor]:

@@ -68,7 +68,7 @@ template <> struct Codes<float> {
 };
 
 template <typename T, int W>
-__global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(AppendDev a) {
+__global__ void __launch_bounds__(kAppendThreads, 3) kv8_append_kernel(AppendDev a) {
   constexpr int E = elem<T>::per16;
   constexpr int kTeam = 32 * W, kTeams = kAppendThreads / kTeam;
   pdl_wait();

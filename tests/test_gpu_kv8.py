@@ -522,3 +522,117 @@ def test_a_decoding_loop_over_the_cache():
             c.run()
             U.check_attention(c)
     assert status.cpu().tolist() == [0] * Bn
+
+
+def _round_case(cid, layers, seed=41):
+    from speculative_decoding_draft_tree_gb300 import workloads as W
+    from speculative_decoding_draft_tree_gb300.api import VerifyStep
+    w = W.make_config(cid, scale="small", device="cuda", num_layers=layers)
+    rng = np.random.default_rng(seed)
+    nb, H, bs, d = w.k_cache.shape[1:]
+    k, ks = U.random_cache(layers, nb, H, bs, d, rng, junk=False)
+    v, vs = U.random_cache(layers, nb, H, bs, d, rng, junk=False)
+    k_new, v_new = W.new_tree_kv(w)
+    step = VerifyStep(w)
+    step.enable_kv8(k, v, ks, vs, k_new, v_new)
+    return w, step, (k, v, ks, vs, k_new, v_new)
+
+
+@pytest.mark.parametrize("cid", [1, 2, 3, 4, 5])
+def test_a_verification_round_over_the_cache(cid):
+    """VerifyStep.run over an 8-bit cache: append, attention, verification and compaction against
+    the oracles run one after the other."""
+    import parity_util as PU
+    w, step, (k, v, ks, vs, k_new, v_new) = _round_case(cid, 2)
+    snap = PU.snapshot(w)
+    no, prefix, table = snap["node_offset"], snap["prefix_len"], snap["block_table"]
+    cache = [[U.values(c[layer]), s[layer].double().cpu().numpy()] for c, s in ((k, ks), (v, vs)) for layer in range(2)]
+    for (c, s), x in ((cache[0], k_new), (cache[2], v_new)):
+        K.append(c, s, x.double().cpu().numpy(), table, prefix, no, w.bs)
+    step.run()
+    torch.cuda.synchronize()
+    PU.check_tree(w, step, snap)
+    PU.check_verify(w, step, PU.oracle_verify(w, snap))
+    c = U.AttnCase.__new__(U.AttnCase)
+    c.N, c.T_max, c.bs, c.prefix, c.off_np, c.table_np = w.N, w.T_max, w.bs, prefix, no, table
+    c.q, c.o, c.lse = w.q, step.o, step.lse
+    words = step.anc_mask.cpu().numpy().view(np.uint32)
+    c.bits = [sum(int(x) << (32 * j) for j, x in enumerate(row)) for row in words]
+    # attention ran before the compaction: the oracle takes the appended cache
+    c.oracle = lambda scale=None: K.tree_attention(
+        w.q.double().cpu().numpy(), cache[0][0], cache[0][1], cache[2][0], cache[2][1], table, prefix, no,
+        [[(b >> j) & 1 for j in range(w.T_max)] for b in c.bits], w.bs, scale)
+    c.ks = ks[0]
+    U.check_attention(c)
+    path, n_acc = step.path.cpu().numpy(), step.n_acc.cpu().numpy()
+    for (codes, scale), (gc, gs) in zip(cache, [(t[layer], u[layer]) for t, u in ((k, ks), (v, vs)) for layer in range(2)]):
+        K.compact(codes, scale, table, prefix, path, n_acc, w.bs)
+        np.testing.assert_array_equal(U.values(gc), codes)
+        np.testing.assert_array_equal(gs.double().cpu().numpy(), scale)
+    assert step.new_kv_len.cpu().tolist() == [int(p) + int(n) + 1 for p, n in zip(prefix, n_acc)]
+
+
+def test_rounds_over_the_cache_from_a_graph_and_a_pipeline():
+    """The same round captured as a graph, and submitted through RoundPipeline, gives run()'s bits."""
+    from speculative_decoding_draft_tree_gb300.api import RoundPipeline
+    names = ("o", "lse", "out_tokens", "out_len", "path", "n_acc", "new_kv_len", "slot_map")
+    w, step, cache = _round_case(4, 1)
+    before = [t.clone() for t in cache[:4]]
+    step.run()
+    torch.cuda.synchronize()
+    want = [getattr(step, n).clone() for n in names] + [t.clone() for t in cache[:4]]
+
+    def back():
+        for t, b in zip(cache[:4], before):
+            t.copy_(b)
+    back()
+    g = step.capture_graph()
+    g.replay()
+    torch.cuda.synchronize()
+    same = lambda a, b: torch.equal(a.view(torch.uint8), b.view(torch.uint8))  # noqa: E731
+    for t, x in zip([getattr(step, n) for n in names] + list(cache[:4]), want):
+        assert same(t, x)
+    back()
+    pipe = RoundPipeline(step)
+    i = pipe.submit(pipe.pinned_host_inputs())
+    pipe.finish()
+    torch.cuda.synchronize()
+    out = pipe.host_outputs(i)
+    assert torch.equal(out["out_tokens"], want[names.index("out_tokens")].cpu())
+    assert torch.equal(out["new_kv_len"], want[names.index("new_kv_len")].cpu())
+    for t, x in zip(cache[:4], want[len(names):]):
+        assert same(t, x)
+
+
+def test_enable_kv8_and_enable_rope_exclude_each_other():
+    w, step, (k, v, ks, vs, k_new, v_new) = _round_case(2, 1)
+    with pytest.raises(ValueError, match="rotated"):
+        step.enable_rope(w.q.clone(), k_new, v_new)
+    from speculative_decoding_draft_tree_gb300.api import VerifyStep
+    other = VerifyStep(w)
+    other.enable_rope(w.q.clone(), k_new, v_new)
+    with pytest.raises(ValueError, match="enable_rope"):
+        other.enable_kv8(k, v, ks, vs, k_new, v_new)
+
+
+# ------------------------------------------------------------------ refusals of the binding
+def test_binding_refuses_wrong_shapes_and_types():
+    c = U.AttnCase([20, 3], [2, 4], 4, 2)
+    bad = [dict(q=c.q.double()), dict(o=c.o[:1]), dict(lse=c.lse[:, :1]), dict(anc_mask=c.anc[:1]), dict(T_max=64),
+           dict(k_scale=c.ks[:1]), dict(v_cache=c.v.float()), dict(k_cache=c.k[:, :, :8].contiguous()),
+           dict(prefix_len=c.prefix_t[:1]), dict(node_offset=c.off[:1]), dict(req_status=c.status.long()),
+           dict(block_table=c.table.cpu()), dict(q=c.q[:, ::2])]
+    for kw in bad:
+        with pytest.raises(ValueError):
+            c.params(**kw)
+    p = c.params()
+    with pytest.raises(B.SpecError, match="INVALID_ARG"):          # no workspace
+        B.spec_tree_attention_kv8(p, None)
+    with pytest.raises(B.SpecError, match="INVALID_ARG"):          # a small one
+        B.spec_tree_attention_kv8(p, torch.empty(256, dtype=torch.uint8, device="cuda"))
+    a = AppendCase([2], [5])
+    with pytest.raises(ValueError, match="contiguous"):
+        B.kv8_append_params(a.k_new.transpose(1, 2).contiguous().transpose(1, 2), a.v_new, a.k, a.v, a.ks, a.vs, a.table,
+                            U.ints([2]), U.ints([0, 5]), a.status)
+    with pytest.raises(ValueError, match="v_new"):
+        B.kv8_append_params(a.k_new, a.v_new.float(), a.k, a.v, a.ks, a.vs, a.table, U.ints([2]), U.ints([0, 5]), a.status)
