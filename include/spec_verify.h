@@ -440,7 +440,8 @@ spec_status_t spec_echo_select_pack(const spec_draft_pool* pool, int32_t K_max,
  * with one fp32 scale for each (block, KV head) in [num_blocks][H_kv], K and V apart:
  *   value = code * scale.
  * Scales are finite and >= 0.  spec_kv8_append writes powers of two in [2^-100, 2^119]; another
- * writer may use any scale there or 0 (the attention reads a V scale below 2^-100 as 2^-100).
+ * writer may use any scale there or 0 (the attention reads a V scale below 2^-100 as 2^-100, and
+ * the V scales of one request's live pages in one head may lie at most 2^100 apart).
  * A block that receives rows belongs to one request (pages shared by a fork are only read).
  * head_dim is a multiple of 16, at most 256.  Round by round: spec_tree_build, rotary embedding,
  * spec_kv8_append of the tree's rows at slots prefix_len .., spec_tree_attention_kv8,
@@ -495,7 +496,10 @@ spec_status_t spec_kv8_append(const spec_kv8_append_params* p, spec_stream_t str
  * spec_tree_attention over an 8-bit cache: the same visibility (the prefix, ancestors and the
  * node itself; a tree of one node is plain decoding), K = k code * k_scale, V likewise.  A row
  * that sees no key (an empty mask row and no prefix) gets O = 0 and LSE = -infinity.  q and o
- * have `dtype`; scores, softmax statistics and the output are accumulated in fp32.
+ * have `dtype` and q is finite; scores, softmax statistics and the output are accumulated in fp32.
+ * On the tensor cores a bf16 q and the weights enter the e4m3 products as two pieces each (q exact
+ * to 2^-18 of its row's largest element; weights to 2^-8 of themselves, 2^-7 in units of more than
+ * 16 query rows).
  * Every H_q / H_kv ratio, block_size and head_dim (multiple of 16, <= 256) is accepted; BF16
  * with head_dim 128, block_size 16, 32, 64 or 128 and H_q / H_kv <= 16 runs on the tcgen05
  * tensor cores, everything else on a CUDA-core kernel.

@@ -458,6 +458,24 @@ def _need_kv8(k_cache, v_cache, k_scale, v_scale, layers):
     return tuple(k_cache.shape)
 
 
+def _held(p, *tensors):
+    """Keeps the tensors whose addresses `p` holds alive with it, and notes their device."""
+    p._tensors = [t for t in tensors if t is not None]
+    devices = {t.device for t in p._tensors}
+    if len(devices) != 1:
+        raise ValueError(f"all tensors must be on one device, got {sorted(map(str, devices))}")
+    p._device = p._tensors[0].device.index
+    return p
+
+
+def _on_device(p):
+    """The library launches on the current device: it has to be the tensors'."""
+    if torch.cuda.current_device() != p._device:
+        raise ValueError(f"the tensors are on cuda:{p._device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return ctypes.byref(p)
+
+
 def _need_shape(t, shape, name, dtype=torch.int32):
     _need(t, dtype, name)
     if tuple(t.shape) != tuple(shape):
@@ -496,12 +514,13 @@ def kv8_append_params(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_ta
     p.k_scale, p.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
     p.block_table, p.start = block_table.data_ptr(), start.data_ptr()
     p.row_offset, p.req_status = row_offset.data_ptr(), req_status.data_ptr()
-    return p
+    return _held(p, k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_table, start,
+                 row_offset, req_status)
 
 
 def spec_kv8_append(params, stream=None):
     """Quantise new K/V rows into the 8-bit cache (params from kv8_append_params)."""
-    code = load_library().spec_kv8_append(ctypes.byref(params), _stream(stream))
+    code = load_library().spec_kv8_append(_on_device(params), _stream(stream))
     _check(code, "spec_kv8_append")
 
 
@@ -533,7 +552,8 @@ def attention_kv8_params(q, k_cache, v_cache, k_scale, v_scale, block_table, pre
     p.node_offset, p.anc_mask = node_offset.data_ptr(), anc_mask.data_ptr()
     p.o, p.lse = o.data_ptr(), None if lse is None else lse.data_ptr()
     p.req_status = req_status.data_ptr()
-    return p
+    return _held(p, q, k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, node_offset,
+                 anc_mask, o, lse, req_status)
 
 
 def spec_attention_kv8_workspace_size(params):
@@ -543,7 +563,7 @@ def spec_attention_kv8_workspace_size(params):
 def spec_tree_attention_kv8(params, workspace, stream=None):
     """Tree attention over the 8-bit cache; calls that may overlap need a workspace each."""
     wsz = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    code = load_library().spec_tree_attention_kv8(ctypes.byref(params), _ptr(workspace), wsz,
+    code = load_library().spec_tree_attention_kv8(_on_device(params), _ptr(workspace), wsz,
                                                   _stream(stream))
     _check(code, "spec_tree_attention_kv8")
 
@@ -570,12 +590,13 @@ def kv8_compact_params(k_cache, v_cache, k_scale, v_scale, block_table, prefix_l
     p.path, p.n_acc, p.req_status = path.data_ptr(), n_acc.data_ptr(), req_status.data_ptr()
     p.new_kv_len, p.slot_map = new_kv_len.data_ptr(), slot_map.data_ptr()
     p.blocks_in_use = blocks_in_use.data_ptr()
-    return p
+    return _held(p, k_cache, v_cache, k_scale, v_scale, block_table, prefix_len, path, n_acc,
+                 req_status, new_kv_len, slot_map, blocks_in_use)
 
 
 def spec_kv8_compact(params, stream=None):
     """Commit the accepted path in the 8-bit cache, every layer (params from kv8_compact_params)."""
-    code = load_library().spec_kv8_compact(ctypes.byref(params), _stream(stream))
+    code = load_library().spec_kv8_compact(_on_device(params), _stream(stream))
     _check(code, "spec_kv8_compact")
 
 
@@ -611,12 +632,13 @@ def kv_fork_params(k_cache, v_cache, block_table, kv_len, src, dst, new_block, f
     p.block_table, p.kv_len = block_table.data_ptr(), kv_len.data_ptr()
     p.src, p.dst, p.new_block = src.data_ptr(), dst.data_ptr(), new_block.data_ptr()
     p.fork_status = fork_status.data_ptr()
-    return p
+    return _held(p, k_cache, v_cache, block_table, kv_len, src, dst, new_block, fork_status,
+                 k_scale, v_scale)
 
 
 def spec_kv_fork(params, stream=None):
     """Child sequences of cached ones: shared full pages, the partial page copied."""
-    code = load_library().spec_kv_fork(ctypes.byref(params), _stream(stream))
+    code = load_library().spec_kv_fork(_on_device(params), _stream(stream))
     _check(code, "spec_kv_fork")
 
 

@@ -180,80 +180,75 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
       __syncwarp();
     } else if (warp == 1 || warp == 3) {
       // =================================================================== MMA issuers
-      if (lane == 0) {
-        const bool is_qk = warp == 1;
-        const uint32_t id_qk = idesc_e4m3(128, kN, false, false);
-        const uint32_t id_pv = idesc_e4m3(128, kN, true, false);
-        const uint64_t dQ = tc::smem_desc(tc::smem_u32(sQ), 16, 1024);
-        const uint64_t dP = tc::smem_desc(tc::smem_u32(sP), 16, 1024);
-        const uint64_t dK = tc::smem_desc(tc::smem_u32(sK), 16, 1024);
-        const uint64_t dV = tc::smem_desc(tc::smem_u32(sV), kTile, 1024);
-        int kt = 0;                    // tiles so far; group = parity of the tile's number
-        bool ok = true;
+      // the whole warp walks the tiles, so that addresses and descriptors are uniform values; one
+      // elected lane issues
+      const bool is_qk = warp == 1;
+      const uint32_t id_qk = idesc_e4m3(128, kN, false, false);
+      const uint32_t id_pv = idesc_e4m3(128, kN, true, false);
+      const uint64_t dQ = tc::smem_desc(tc::smem_u32(sQ), 16, 1024);
+      const uint64_t dP = tc::smem_desc(tc::smem_u32(sP), 16, 1024);
+      const uint64_t dK = tc::smem_desc(tc::smem_u32(sK), 16, 1024);
+      const uint64_t dV = tc::smem_desc(tc::smem_u32(sV), kTile, 1024);
+      int kt = 0;                      // tiles so far; group = parity of the tile's number
+      bool ok = true;
+      Item it;
 #pragma unroll 1
-        for (int li = 0; ok; ++li) {
-          Item it;                     // (one lane: its own wait and arrival)
-          {
-            const int s = li % kItemRing;
-            ok = wait1(&sh.items.full[s], li / kItemRing, abort_flag);
-            it = sh.items.item[s];
-            tc::mbar_arrive(&sh.items.empty[s]);
-            if (!ok || it.r < 0) break;
-          }
-          const int par = li & 1;
-          if (is_qk ? !wait1(&sh.q_full[par], li >> 1, abort_flag)
-                    : (li > 1 && !wait1(&sh.o_free[par], (li >> 1) - 1, abort_flag))) {
-            ok = false;
-            break;
-          }
+      for (int li = 0; ok && __all_sync(0xffffffffu, next_item(sh.items, li, it, abort_flag)); ++li) {
+        const int par = li & 1;
+        if (is_qk) ok = wait1(&sh.q_full[par], li >> 1, abort_flag);
+        else if (li > 1) ok = wait1(&sh.o_free[par], (li >> 1) - 1, abort_flag);
 #pragma unroll 1
-          for (int j = it.j0; j < it.j1; ++j, ++kt) {
-            const int g = kt & 1, b = (kt >> 1) & 1, use = kt >> 2;
-            if (is_qk) {
-              const int st = kt % kKStages;
-              if (!wait1(&sh.k_full[st], kt / kKStages, abort_flag) ||
-                  (use > 0 && !wait1(&sh.s_free[g][b], use - 1, abort_flag))) {
-                ok = false;
-                break;
-              }
-              tc::tc_fence_after();
-              const uint32_t tS = tmem + (g * 2 + b) * kN;
-              const uint64_t ka = dK + uint64_t(st) * (kTile >> 4);
-              const uint64_t qb = dQ + uint64_t(par) * (L::kPair >> 4);
+        for (int j = it.j0; j < it.j1; ++j, ++kt) {
+          const int g = kt & 1, b = (kt >> 1) & 1, use = kt >> 2;
+          if (is_qk) {
+            const int st = kt % kKStages;
+            ok = ok && wait1(&sh.k_full[st], kt / kKStages, abort_flag) &&
+                 (use == 0 || wait1(&sh.s_free[g][b], use - 1, abort_flag));
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc::tc_fence_after();
+            const uint32_t tS = tmem + (g * 2 + b) * kN;
+            const uint64_t ka = dK + uint64_t(st) * (kTile >> 4);
+            const uint64_t qb = dQ + uint64_t(par) * (L::kPair >> 4);
+            if (elect_one()) {
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 mma_e4m3_ss(tS, ka + 2 * k, qb + 2 * k, id_qk, k > 0 ? 1u : 0u);
               tc::mma_commit(&sh.s_full[g][b]);
               tc::mma_commit(&sh.k_empty[st]);
               if (j == it.j1 - 1) tc::mma_commit(&sh.q_empty[par]);
-            } else {
-              const int st = kt % kVStages;
-              const bool first = j - it.j0 < 2;   // the group's first tile of the unit
-              if (!wait1(&sh.p_full[g][b], use, abort_flag) ||
-                  !wait1(&sh.v_full[st], kt / kVStages, abort_flag)) {
-                ok = false;
-                break;
-              }
-              tc::tc_fence_after();
-              const uint32_t tO = tmem + L::kTmemO + (g * 2 + par) * kN;
-              const uint64_t va = dV + uint64_t(st) * (kTile >> 4);
-              const uint64_t pb = dP + uint64_t(g * 2 + b) * (L::kPair >> 4);
+            }
+            __syncwarp();
+          } else {
+            const int st = kt % kVStages;
+            const bool first = j - it.j0 < 2;     // the group's first tile of the unit
+            ok = ok && wait1(&sh.p_full[g][b], use, abort_flag) &&
+                 wait1(&sh.v_full[st], kt / kVStages, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc::tc_fence_after();
+            const uint32_t tO = tmem + L::kTmemO + (g * 2 + par) * kN;
+            const uint64_t va = dV + uint64_t(st) * (kTile >> 4);
+            const uint64_t pb = dP + uint64_t(g * 2 + b) * (L::kPair >> 4);
+            if (elect_one()) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k)          // 32 slots a step: four groups of 8 V rows
+              for (int k = 0; k < 4; ++k)            // 32 slots a step: four groups of 8 V rows
                 mma_e4m3_ss(tO, va + k * (4096 >> 4), pb + 2 * k, id_pv,
                             (k > 0 || !first) ? 1u : 0u);
               tc::mma_commit(&sh.v_empty[st]);
               tc::mma_commit(&sh.pv_done[g][b]);
               if (j == it.j1 - 1) tc::mma_commit(&sh.o_full[par]);
             }
+            __syncwarp();
           }
         }
-        if (!ok) *abort_flag = 1;
-        // nothing issued here may still run when TMEM is released (bounded, abort or not)
-        tc::mma_commit(&sh.drain[is_qk ? 0 : 1]);
-        volatile int never = 0;
-        tc::mbar_wait(&sh.drain[is_qk ? 0 : 1], 0, &never, kWaitLimit / 8);
       }
+      if (!ok) *abort_flag = 1;
+      // nothing issued here may still run when TMEM is released (bounded, abort or not)
+      if (elect_one()) tc::mma_commit(&sh.drain[is_qk ? 0 : 1]);
+      __syncwarp();
+      volatile int never = 0;
+      tc::mbar_wait(&sh.drain[is_qk ? 0 : 1], 0, &never, kWaitLimit / 8);
       __syncwarp();
     }
   } else if (warp < 12) {

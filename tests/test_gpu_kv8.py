@@ -184,6 +184,14 @@ def test_attention_long_prefixes_are_split_and_joined():
     U.check_attention(c)
 
 
+@pytest.mark.parametrize("Hq,H", [(4, 1), (12, 3), (8, 2), (32, 2)])
+def test_attention_several_row_tiles(Hq, H):
+    """Row tiles in pairs, odd last ones shared out by heads, odd numbers of heads."""
+    c = U.AttnCase([700, 3, 129, 0], [70, 200, 9, 33], Hq, H, seed=25)
+    c.run()
+    U.check_attention(c)
+
+
 def test_attention_many_requests():
     rng = np.random.default_rng(5)
     c = U.AttnCase(rng.integers(0, 60, 600).tolist(), rng.integers(1, 3, 600).tolist(), 2, 1, seed=13)
@@ -616,6 +624,20 @@ def test_enable_kv8_and_enable_rope_exclude_each_other():
 
 
 # ------------------------------------------------------------------ refusals of the binding
+def test_parameters_hold_their_tensors_and_their_device():
+    c = U.AttnCase([20, 3], [2, 4], 4, 2)
+    want = c.run()[0].clone()
+    p = c.params(q=c.q.clone(), block_table=c.table.clone(), prefix_len=c.prefix_t.clone(), node_offset=c.off.clone())
+    junk = [torch.full((1 << 12,), 2 ** 30, dtype=torch.int32, device="cuda") for _ in range(64)]   # takes freed memory
+    c.o.zero_()
+    B.spec_tree_attention_kv8(p, torch.empty(B.spec_attention_kv8_workspace_size(p), dtype=torch.uint8, device="cuda"))
+    torch.cuda.synchronize()
+    assert torch.equal(c.o, want) and len(junk) == 64
+    p._device = 7                         # as if the tensors were on another device than the current one
+    with pytest.raises(ValueError, match="current device"):
+        B.spec_tree_attention_kv8(p, None)
+
+
 def test_binding_refuses_wrong_shapes_and_types():
     c = U.AttnCase([20, 3], [2, 4], 4, 2)
     bad = [dict(q=c.q.double()), dict(o=c.o[:1]), dict(lse=c.lse[:, :1]), dict(anc_mask=c.anc[:1]), dict(T_max=64),
