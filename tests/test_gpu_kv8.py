@@ -192,6 +192,29 @@ def test_attention_several_row_tiles(Hq, H):
     U.check_attention(c)
 
 
+@pytest.mark.parametrize("Hq,H,T", [(1, 1, 32), (2, 2, 17), (8, 2, 8), (16, 1, 2), (6, 2, 10), (14, 2, 3), (9, 1, 2)])
+def test_attention_units_of_17_to_32_rows(Hq, H, T):
+    """The rows between the two forms' bounds: prefixes around tiles, split ones, smaller trees, masks."""
+    c = U.AttnCase([0, 5, 119, 128, 1500, 300], [T, 1, T, T - 1, T, T], Hq, H, seed=Hq + T)
+    c.run()
+    U.check_attention(c)
+    rng = np.random.default_rng(T)
+    bits = [int(rng.integers(0, 1 << T)) if i % 3 else 0 for i in range(2 * T)]
+    c = U.AttnCase([0, 121], [T, T], Hq, H, bits=bits, seed=Hq)
+    c.run()
+    U.check_attention(c)
+
+
+@pytest.mark.parametrize("q_scale,spread", [(20.0, 2), (1e-20, 3), (1.0, 60)])
+def test_attention_units_of_24_rows_of_unlike_magnitudes(q_scale, spread):
+    c = U.AttnCase([900, 77, 2000], [6, 6, 2], 8, 2, q_scale=q_scale, spread=spread, seed=26)
+    if spread == 60:
+        c.ks.mul_(2.0 ** -50)          # the scores stay finite: only V's scales spread
+        c.ks.clamp_(min=2.0 ** -12, max=2.0 ** -8)
+    c.run()
+    U.check_attention(c)
+
+
 def test_attention_many_requests():
     rng = np.random.default_rng(5)
     c = U.AttnCase(rng.integers(0, 60, 600).tolist(), rng.integers(1, 3, 600).tolist(), 2, 1, seed=13)
