@@ -501,7 +501,7 @@ spec_status_t spec_kv8_append(const spec_kv8_append_params* p, spec_stream_t str
  * to 2^-18 of its row's largest element; weights to 2^-8 of themselves, 2^-7 in units of more than
  * 16 query rows).
  * Every H_q / H_kv ratio, block_size and head_dim (multiple of 16, <= 256) is accepted; BF16
- * with head_dim 128, block_size 16, 32, 64 or 128 and H_q / H_kv <= 16 runs on the tcgen05
+ * with head_dim 128, block_size 16, 32, 64 or 128 and H_q / H_kv <= 128 runs on the tcgen05
  * tensor cores, everything else on a CUDA-core kernel.
  * Requests with req_status bits other than BAD_BLOCK and TIMEOUT, or with T_r > T_max, have no
  * rows written; a request whose live slots lie beyond its table row gets SPEC_REQ_BAD_BLOCK and

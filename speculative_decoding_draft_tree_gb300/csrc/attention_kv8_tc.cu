@@ -11,18 +11,25 @@
 // next one (accumulators are double-buffered by unit).
 // Warps: 0 copies K, 2 copies V, 1 issues the scores' products, 3 the output's, 4-7 and 8-11
 // softmax, 12-15 split the queries and write the output, 16 brings the scales, 17 walks the items.
+// Measured: 64 single tokens over 1024 .. 32768 slots (2.2 GB) 340 us, 6.5 TB/s, 96% of the copy
+// rate; 16 chains of 6, 32 KV heads, 2048 slots (271 MB) 52.5 us, 5.2 TB/s; one token over 2047
+// slots (4 MB) 10.7 us, all of it latency: the start, the walk to the first page, a tile, the join.
 //
 // attn_kv8_tile_kernel: longer units in tiles of 128 query rows (G heads x 128 / G tree tokens).
 // S = Q K^T (M = N = 128, both pieces of Q into one accumulator); P's pieces go to TMEM as the A
-// operand of O += P V (TMEM columns: S 0-255, O 256-383, P 384-511).  Bound by the softmax's
-// instructions before the tensor core (1024 clocks a tile at the e4m3 rate): exponentials and e4m3
-// packing run at 32 results a clock and SM, most of the rest at 64.  So two sets of eight warps
-// take alternate tiles, one's waits under the other's arithmetic, with S and P buffers of their
-// own, and P is split the cheapest way: hi is e5m2, which is the upper byte of an fp16 (a rounding
-// add and a mask), lo = e4m3(p - hi); e5m2's range also leaves the reference five binades of
-// slack.  A row belongs to four threads: two a set, each with 64 of a tile's keys, that agree on
-// the row's reference at a barrier; the sets pass it on tile by tile.
+// operand of O += P V.  Bound by the softmax's instructions before the tensor core (1024 clocks a
+// tile at the e4m3 rate; a tile takes ~2450): exponentials and e4m3 packing run at 32 results a
+// clock and SM, most of the rest at 64.  So P is split the cheapest way: hi is e5m2, which is the
+// upper byte of an fp16 (a rounding add and a mask), lo = e4m3(p - hi); e5m2's range also leaves
+// the reference eight binades of slack, so that it rarely moves.  A row belongs to four threads of
+// four warps, each with 32 of a tile's keys: they form weights against the present reference at
+// once and vote on it meanwhile; where the vote says that it moves, they agree on the new one and
+// form them again.  Three S buffers (TMEM columns 0-383, P over S) keep the scores of the next
+// tiles coming while one is in the softmax and one in the output's product; O has columns 384-511.
 // Warps: 0-3 as above, 4-19 softmax, 20-23 queries and output, 24 scales, 25 items.
+// Measured: 32 trees of 46 over 8192 slots (32 query heads on 8) 280 us, 706 TFLOP/s of scores and
+// output, the tensor pipe busy 42% of the time; 64 ragged trees over 1024 .. 32768 slots (64 query
+// heads on 8) 1380 us, 890 TFLOP/s.  The bf16 cache takes 289 and 1554 us on these shapes.
 //
 // Scales: a score is code product * (K scale of the slot's page * the row's query scale); the V
 // scale joins the exponent, y = score + log2(V scale), and the weight 2^(y - ref) goes into the
@@ -1136,7 +1143,10 @@ static bool encode_maps(PFN_cuTensorMapEncodeTiled_v12000 enc, const AttnKv8Dev&
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// query rows of a unit's row tile
+// Query rows of a unit's row tile: the smallest form that holds a request's rows.  Over 8192 slots,
+// 16 requests, 8 KV heads: 8 rows 51.8 us in the form of 8, 58.1 in that of 16, 78.3 in tiles of
+// 128; 16 rows 61.0 and 79.9.  (A form of 32 rows was slower than the tiles: 24 rows 95.6 us
+// against 82.2.)
 static int rows_of(const AttnKv8Dev& a) {
   const int rows = a.T_max * a.G;
   return rows <= 8 ? 8 : rows <= 16 ? 16 : tile::kRows;
@@ -1149,10 +1159,12 @@ static int device_ctas() {
 
 }  // namespace kv8tc
 
-// Whether the tensor-core kernels take this call.
+// Whether the tensor-core kernels take this call: their types and tile shapes, a row tile that holds
+// a token's query heads, row coordinates of TMA in 32 bits.  (32 and 64 query heads of one KV head,
+// 64 x 1 and 16 x 4 tokens over 8192 slots: 48 and 44 us here, 1120 and 1596 us on CUDA cores.)
 bool attn_kv8_tc_takes(const AttnKv8Dev& a, bool bf16) {
   return bf16 && a.d == 128 && (a.bs == 16 || a.bs == 32 || a.bs == 64 || a.bs == 128) &&
-         a.G <= 16 &&
+         a.G <= kv8tc::tile::kRows &&
          (long long)a.num_blocks * a.H_kv * a.bs + 128 < (1LL << 31);
 }
 
@@ -1172,7 +1184,7 @@ spec_status_t launch_attn_kv8_tc(const AttnKv8Dev& a, void* ws, size_t ws_bytes,
   d.log2bs = a.bs == 16 ? 4 : a.bs == 32 ? 5 : a.bs == 64 ? 6 : 7;
   d.kv_rows = a.num_blocks * a.H_kv * a.bs;
   d.ctas = ctas;
-  d.min_tiles = 2;
+  d.min_tiles = 2;   // one token over 2047 slots: 10.8 us; 12.1 with 1, 11.4 with 4, 14.0 with 8
   d.pair = a.T_max * a.G > tile::kRows && ctas > 1;
   const WsLayout lay = ws_layout(ctas, d.part_rows);
   if (!ws || ws_bytes < lay.total || (reinterpret_cast<uintptr_t>(ws) & 255u))

@@ -10,12 +10,14 @@
 // units, one for each CTA of the pair -- two row tiles of one head, which read the same K/V tiles
 // at the same pace, so that the second reader finds them in L2; or, of an odd last row tile, two
 // heads.  (Without the pairs the row tiles' passes over a long cache lie too far apart for L2, and
-// K and V come from HBM once a row tile.)
+// K and V come from HBM once a row tile: 64 ragged trees, 432 rows a head, 1376 us with, 1437
+// without.)
 //
 // 8-bit codes go to tcgen05.mma kind::f8f6f4 as they are.  The other operand of each product keeps
-// its precision as the sum of two e4m3 pieces, hi = e4m3(x) and lo = e4m3(x - hi), both multiplied
+// its precision as the sum of two 8-bit pieces, hi = e4m3(x) and lo = e4m3(x - hi), both multiplied
 // into the same fp32 accumulator: a bf16 query is exactly hi + lo (4 + 4 significant bits) but
-// for elements 2^-18 of the row's largest, a softmax weight keeps 8 bits.  fp8 products run at
+// for elements 2^-18 of the row's largest, a softmax weight keeps 8 bits (7 where hi is e5m2, in
+// the kernel of long units).  fp8 products run at
 // twice the bf16 rate, so the two pieces cost what one bf16 product does, and K and V are read by
 // the tensor core where TMA put them, one byte an element: converting them to bf16 first would
 // move 6 bytes of shared memory an element against 2, more than the SM has at HBM speed.

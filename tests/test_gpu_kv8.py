@@ -215,6 +215,15 @@ def test_attention_units_of_24_rows_of_unlike_magnitudes(q_scale, spread):
     U.check_attention(c)
 
 
+@pytest.mark.parametrize("Hq,H", [(32, 1), (40, 2), (71, 1), (128, 1), (130, 1), (192, 3)])
+@pytest.mark.parametrize("T", [1, 9])
+def test_attention_many_query_heads_of_a_kv_head(Hq, H, T):
+    """Row tiles of few tokens, down to one; past 128 heads the CUDA-core kernel."""
+    c = U.AttnCase([0, 130, 700], [T, T, 1], Hq, H, seed=Hq)
+    c.run()
+    U.check_attention(c)
+
+
 def test_attention_many_requests():
     rng = np.random.default_rng(5)
     c = U.AttnCase(rng.integers(0, 60, 600).tolist(), rng.integers(1, 3, 600).tolist(), 2, 1, seed=13)
@@ -501,6 +510,56 @@ def test_fork_refuses_bad_pages_and_lengths():
     c.lens[0] = -4
     c.kv_len[0] = -4
     c.check([2])
+
+
+# ------------------------------------------------------------------------------ far addresses
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_pages_beyond_four_gigabytes(dtype):
+    """The same calls on a small pool and on one whose pages lie past 2^32 bytes: bit for bit alike."""
+    H, Hq, bs, d, L, far = 8, 16, 16, 128, 2, 2 ** 32 // (8 * 16 * 128)
+    start, n = [0, 37, 200], [50, 6, 1]
+    off = np.concatenate([[0], np.cumsum(n)]).tolist()
+    g = torch.Generator(device="cuda").manual_seed(50)
+    kn, vn = (torch.randn((off[-1], H, d), generator=g, device="cuda").to(dtype) for _ in range(2))
+    q = torch.randn((off[-1], Hq, d), generator=g, device="cuda").to(dtype)
+    rng = np.random.default_rng(51)
+    ids = U.table_for([5, 5, 15], 40, rng, 16)
+    seeds = [U.random_cache(1, 40, H, bs, d, rng, junk=False) for _ in range(2)]
+    results = []
+    for shift in (0, far):
+        nb = 40 + shift
+        (k, ks), (v, vs) = [(torch.zeros((L, nb, H, bs, d), dtype=torch.uint8, device="cuda"), torch.zeros((L, nb, H), device="cuda"))
+                            for _ in range(2)]
+        for (c, s), (c0, s0) in zip(((k, ks), (v, vs)), seeds):
+            c[1, shift:] = c0[0].view(torch.uint8)
+            s[1, shift:] = s0[0]
+        k, v = k.view(U.E4M3), v.view(U.E4M3)
+        table = torch.from_numpy(np.where(ids >= 0, ids + shift, ids).astype(np.int32)).cuda()
+        st = torch.zeros(3, dtype=torch.int32, device="cuda")
+        held = (U.ints(start), U.ints(off))
+        B.spec_kv8_append(B.kv8_append_params(kn, vn, k[1], v[1], ks[1], vs[1], table, *held, st))
+        o, lse = torch.zeros_like(q), torch.zeros((off[-1], Hq), device="cuda")
+        bits = [b for t in n for b in U.chain_bits(t)]
+        p = B.attention_kv8_params(q=q, k_cache=k[1], v_cache=v[1], k_scale=ks[1], v_scale=vs[1], block_table=table,
+                                   prefix_len=held[0], node_offset=held[1], anc_mask=U.mask_words(bits, 50), T_max=50, o=o, lse=lse,
+                                   req_status=st)
+        B.spec_tree_attention_kv8(p, torch.empty(max(256, B.spec_attention_kv8_workspace_size(p)), dtype=torch.uint8, device="cuda"))
+        path = torch.tensor([[0, 5, 49], [0, 3, 5], [0, 0, 0]], dtype=torch.int32, device="cuda")
+        outs = [U.ints([0] * 3), torch.zeros((3, 3, 2), dtype=torch.int32, device="cuda"), U.ints([0] * 3)]
+        B.spec_kv8_compact(B.kv8_compact_params(k, v, ks, vs, table, held[0], path, U.ints([2, 2, 0]), st, *outs, 3))
+        lens, fs = outs[0].clone(), U.ints([0])
+        wide = torch.cat([table, torch.full_like(table[:1], -1)])
+        lens = torch.cat([lens, U.ints([0])])
+        fresh = int(np.setdiff1d(np.arange(40), ids)[0])
+        B.spec_kv_fork(B.kv_fork_params(k, v, wide, lens, U.ints([1]), U.ints([3]), U.ints([fresh + shift]), fs, ks, vs))
+        torch.cuda.synchronize()
+        assert st.cpu().tolist() == [0] * 3 and fs.cpu().tolist() == [0] and lens.cpu().tolist() == [3, 40, 201, 40]
+        back = [t[:, shift:].cpu() for t in (k.view(torch.uint8), v.view(torch.uint8), ks, vs)]
+        results.append([o.cpu(), lse.cpu(), outs[1].cpu(), wide.cpu() - shift * (wide.cpu() >= 0).int()] + back)
+        del k, v, ks, vs, p
+        torch.cuda.empty_cache()
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
 
 
 # ---------------------------------------------------------------------------------- together
