@@ -496,7 +496,9 @@ spec_status_t spec_kv8_append(const spec_kv8_append_params* p, spec_stream_t str
  * spec_tree_attention over an 8-bit cache: the same visibility (the prefix, ancestors and the
  * node itself; a tree of one node is plain decoding), K = k code * k_scale, V likewise.  A row
  * that sees no key (an empty mask row and no prefix) gets O = 0 and LSE = -infinity.  q and o
- * have `dtype` and q is finite; scores, softmax statistics and the output are accumulated in fp32.
+ * have `dtype`, q holds no infinities; scores, softmax statistics and the output are accumulated in
+ * fp32.  A NaN (in q, in a code) makes the rows that see it NaN and no others: O and LSE for one in q
+ * or K; O alone for one in V, its column at least.
  * On the tensor cores a bf16 q and the weights enter the e4m3 products as two pieces each (q exact
  * to 2^-18 of its row's largest element; weights to 2^-8 of themselves, 2^-7 in units of more than
  * 16 query rows).

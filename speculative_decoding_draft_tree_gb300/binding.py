@@ -562,6 +562,10 @@ def spec_attention_kv8_workspace_size(params):
 
 def spec_tree_attention_kv8(params, workspace, stream=None):
     """Tree attention over the 8-bit cache; calls that may overlap need a workspace each."""
+    if workspace is not None:
+        _need(workspace, None, "workspace")
+        if workspace.device.index != params._device:
+            raise ValueError(f"workspace must be on cuda:{params._device}")
     wsz = 0 if workspace is None else workspace.numel() * workspace.element_size()
     code = load_library().spec_tree_attention_kv8(_on_device(params), _ptr(workspace), wsz,
                                                   _stream(stream))

@@ -159,12 +159,12 @@ __global__ void __launch_bounds__(kv8_simt::kThreads) attn_kv8_simt_kernel(AttnK
       sum += s_l[w][g] * f;
       v += s_o[w][g][c] * f;
     }
-    const float y = sum > 0.f ? v / sum : 0.f;      // a row that sees nothing is 0
+    const float y = sum == 0.f ? 0.f : v / sum;     // a row that sees nothing is 0
     if constexpr (sizeof(T) == 2) out[i] = __float2bfloat16_rn(y);
     else out[i] = y;
     if (c == 0 && a.lse)
       a.lse[size_t(n) * a.H_q + h * a.G + g0 + g] =
-          sum > 0.f ? (M + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+          sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
   }
 }
 

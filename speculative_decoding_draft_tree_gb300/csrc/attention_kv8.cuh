@@ -29,7 +29,9 @@ enum class Kv8Live { yes, no, beyond_table };
 __device__ __forceinline__ Kv8Live kv8_live(const AttnKv8Dev& a, int r, int T, int P) {
   const int st = a.req_status[r] & ~(SPEC_REQ_BAD_BLOCK | SPEC_REQ_TIMEOUT);
   if (st != 0 || T < 1 || T > a.T_max || P < 0) return Kv8Live::no;
-  return (long long)P + T <= (long long)a.max_blocks * a.bs ? Kv8Live::yes : Kv8Live::beyond_table;
+  // (slot numbers and a tile past them stay in 32 bits)
+  const long long end = min((long long)a.max_blocks * a.bs, (long long)INT32_MAX - 1024);
+  return (long long)P + T <= end ? Kv8Live::yes : Kv8Live::beyond_table;
 }
 
 }  // namespace spec

@@ -106,6 +106,29 @@ __device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[N]) {
   else tc::tmem_st32(addr, r);
 }
 
+// A V row of a tile in shared memory; a warp's lanes hold neighbouring rows and start at different
+// vectors of them, in different banks.  (Not unrolled: the masked tiles are few.)
+__device__ __forceinline__ void clear_row(uint8_t* row) {
+  uint4* w = reinterpret_cast<uint4*>(row);
+#pragma unroll 1
+  for (int x = 0; x < 8; ++x) w[(x + threadIdx.x) & 7] = make_uint4(0, 0, 0, 0);
+}
+__device__ __forceinline__ bool has_nan(const uint8_t* row) {
+  const uint4* w = reinterpret_cast<const uint4*>(row);
+  uint32_t hit = 0;
+#pragma unroll
+  for (int x = 0; x < 8; ++x) {
+    const uint4 v = w[(x + threadIdx.x) & 7];
+    hit |= nan_bytes(v.x) | nan_bytes(v.y) | nan_bytes(v.z) | nan_bytes(v.w);
+  }
+  return hit != 0;
+}
+__device__ __forceinline__ void clear_nan(uint8_t* row) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(row);
+#pragma unroll 1
+  for (int x = 0; x < 32; ++x) w[x] &= ~((nan_bytes(w[x]) >> 7) * 255u);
+}
+
 template <int NR>
 __global__ void __launch_bounds__(rows::kThreads, 1)
 attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
@@ -392,14 +415,20 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
           pc[L::kPiece + o0] = uint8_t(lo);
           pc[L::kPiece + o1] = uint8_t(lo >> 8);
         }
-        // the unit's last tile: stale V rows past the end (NaN codes) times zero must stay zero
-        if ((it.j0 + i) * kBN + kBN > kv_len) {
+        // where keys are masked a NaN code of V times a zero weight must stay zero: stale rows past
+        // the end are cleared, and a tree slot's NaN moves from V to the weights of the rows that
+        // see it
+        if (masked) {
           const int st = kg % kVStages;
           ok &= wait1(&sh.v_full[st], kg / kVStages, abort_flag);
+          uint8_t* row = sV + st * kTile + kl * 128;
           if (key >= kv_len) {
-            uint4* row = reinterpret_cast<uint4*>(sV + st * kTile + kl * 128);
-#pragma unroll
-            for (int x = 0; x < 8; ++x) row[x] = make_uint4(0, 0, 0, 0);
+            clear_row(row);
+          } else if (key >= P && (~vis & ((1u << (T * a.G)) - 1u)) != 0 && has_nan(row)) {
+            clear_nan(row);                            // (T G <= 16; some row does not see it)
+#pragma unroll 1
+            for (int n = 0; n < NR; ++n)
+              if ((vis >> n) & 1u) pc[(n >> 3) * 1024 + (n & 7) * 128 + ((chunk ^ (n & 7)) << 4)] = 0x7F;
           }
         }
         tc::fence_proxy_async_smem();
@@ -502,8 +531,8 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
         l1 += sh.sum[par][1][w][rn];
       }
       const float l = l0 * w0 + l1 * w1;
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      const float lse2 = l > 0.f ? log2f(l) - top : -INFINITY;
+      const float inv = l == 0.f ? 0.f : 1.f / l;    // (NaN stays NaN)
+      const float lse2 = l == 0.f ? -INFINITY : log2f(l) - top;
       w0 *= inv;
       w1 *= inv;
       ok &= wait1(&sh.o_full[par], li >> 1, abort_flag);
@@ -517,7 +546,7 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
 #pragma unroll
       for (int n = 0; n < NR; ++n) {
         const float u = __shfl_sync(0xffffffffu, w0, n);
-        v[n] = u > 0.f ? (__uint_as_float(ov[n]) + __uint_as_float(ov[n + NR])) * u : 0.f;
+        v[n] = u != 0.f ? (__uint_as_float(ov[n]) + __uint_as_float(ov[n + NR])) * u : 0.f;
       }
       tmem_ld<kN>(tmem + lane_addr + L::kTmemO + (2 + par) * kN, ov);
       tc::tmem_ld_wait();
@@ -527,7 +556,7 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
 #pragma unroll
       for (int n = 0; n < NR; ++n) {
         const float u = __shfl_sync(0xffffffffu, w1, n);
-        if (u > 0.f) v[n] = fmaf(__uint_as_float(ov[n]) + __uint_as_float(ov[n + NR]), u, v[n]);
+        if (u != 0.f) v[n] = fmaf(__uint_as_float(ov[n]) + __uint_as_float(ov[n + NR]), u, v[n]);
         const size_t at = size_t(__shfl_sync(0xffffffffu, row, n)) * kD + col;
         if (n < nrows) {
           if (cur.slot < 0) static_cast<__nv_bfloat16*>(a.o)[at] = __float2bfloat16_rn(v[n]);
@@ -588,6 +617,7 @@ struct Shared {
   float mx[4][kRows];             // per quarter of the keys: row maxima of an update
   float sum[2][4][kRows];         // per unit parity and quarter
   float add[2][kRows];            // per unit parity: kLift - reference
+  int v_nan[kBufs][kBN];          // per buffer and slot: 1 + the last tile whose V had a NaN there
   uint32_t tmem;
   int abort, r0, r1;
   ItemRing items;
@@ -653,6 +683,7 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
     if (lane == 0) sh.abort = 0;
     tc::fence_mbar_init();
   }
+  if (tid < kBufs * kBN) (&sh.v_nan[0][0])[tid] = 0;
   tc::tc_fence_before();
   __syncthreads();
   pdl_wait();
@@ -787,23 +818,45 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
         __syncwarp();
         tc::tc_fence_after();
         if (live) {
+          // where keys are masked a NaN code of V times a zero weight must stay zero: stale rows
+          // past the end are cleared, and a tree slot's NaN moves from V to the weights of the
+          // rows that see it.  The warps of these keys do so each for itself; the one that clears a
+          // NaN has left word of it before, for those that look later.
+          const bool masked = j * kBN + kBN > P;
+          if (masked) {
+            const int st = kt % kVStages, at = part * 32 + lane;
+            ok &= wait1(&sh.v_full[st], kt / kVStages, abort_flag);
+            uint8_t* row = sV + st * kTile + at * 128;
+            if (j * kBN + at >= kv_len) {
+              clear_row(row);
+            } else if (j * kBN + at >= P) {
+              const bool found = has_nan(row);
+              if (found) *static_cast<volatile int*>(&sh.v_nan[b][at]) = kt + 1;
+              __threadfence_block();
+              if (found) clear_nan(row);
+            }
+            tc::fence_proxy_async_smem();
+          }
           const ScaleSlot& sc = sh.sc[slot];
           const uint32_t tS = tmem + lane_addr + b * 128 + part * 32;
           // the weights of this thread's 32 keys against the reference kLift - add, as the two
           // pieces of P; `top`: the largest exponent, `sum`: of the weights over the V scales
           float top, sum;
           uint32_t hi[8], lo[8];
+          auto seen = [&]() -> uint32_t {              // the keys that this row sees
+            const int pre = P - key0, left = kv_len - key0;
+            uint32_t vis = anc_window(arow, a.W, key0 - P);
+            vis |= pre >= 32 ? 0xFFFFFFFFu : pre > 0 ? (1u << pre) - 1u : 0u;
+            // (mask bits past the tree count for nothing)
+            return vis & (left >= 32 ? 0xFFFFFFFFu : left > 0 ? (1u << left) - 1u : 0u);
+          };
           auto weights = [&](float add) {
             const float shift = add == INFINITY ? 0.f : add;   // no key seen yet
             uint32_t x[32];
             tc::tmem_ld32(tS, x);
             tc::tmem_ld_wait();
             if (key0 + 32 > P) {
-              const int pre = P - key0, left = kv_len - key0;
-              uint32_t vis = anc_window(arow, a.W, key0 - P);
-              vis |= pre >= 32 ? 0xFFFFFFFFu : pre > 0 ? (1u << pre) - 1u : 0u;
-              // (mask bits past the tree count for nothing)
-              vis &= left >= 32 ? 0xFFFFFFFFu : left > 0 ? (1u << left) - 1u : 0u;
+              const uint32_t vis = seen();
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 if (!((vis >> e) & 1u)) x[e] = __float_as_uint(-INFINITY);
@@ -863,6 +916,18 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
             }
             weights(add);
           }
+          if (masked) {
+            const int last = *static_cast<volatile int*>(&sh.v_nan[b][part * 32 + lane]);
+            const uint32_t v_nan = __ballot_sync(0xffffffffu, last == kt + 1);
+            if (v_nan != 0) {
+              const uint32_t hit = v_nan & seen();
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const uint32_t n = (hit >> (4 * e)) & 15u;
+                hi[e] |= ((n & 1u) | (n & 2u) << 7 | (n & 4u) << 14 | (n & 8u) << 21) * 127u;
+              }
+            }
+          }
           tmem_st8(tS, hi);
           tmem_st8(tS + 8, lo);
           lsum += sum;
@@ -870,19 +935,6 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
         }
         tc::tc_fence_before();
         __syncwarp();
-        // the unit's last tile: stale V rows past the end (NaN codes) times zero must stay zero;
-        // each quarter clears its own 32 keys' rows
-        if (j * kBN + kBN > kv_len) {
-          const int st = kt % kVStages, row = part * 32 + (m >> 2);
-          ok &= wait1(&sh.v_full[st], kt / kVStages, abort_flag);
-          if (j * kBN + row >= kv_len) {
-            uint4* to = reinterpret_cast<uint4*>(sV + st * kTile + row * 128 + (m & 3) * 32);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) to[c] = make_uint4(0, 0, 0, 0);
-          }
-          tc::fence_proxy_async_smem();
-          __syncwarp();
-        }
         if (lane == 0) {
           tc::mbar_arrive(&sh.sc_empty[slot]);
           tc::mbar_arrive(&sh.p_full[b]);
@@ -969,8 +1021,8 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
       ok &= wait1(&sh.sum_full[par], li >> 1, abort_flag);
       const float l = (sh.sum[par][0][m] + sh.sum[par][1][m]) + (sh.sum[par][2][m] + sh.sum[par][3][m]);
       const float add = sh.add[par][m];
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      const float lse2 = l > 0.f ? log2f(l) - add : -INFINITY;
+      const float inv = l == 0.f ? 0.f : 1.f / l;    // (NaN stays NaN)
+      const float lse2 = l == 0.f ? -INFINITY : log2f(l) - add;
       const size_t row = cur.slot < 0 ? size_t(cur.o + t) * a.H_q + cur.h * a.G + gl
                                       : size_t(cur.slot) * kRows + m;
       __syncwarp();
@@ -995,7 +1047,7 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
         for (int e = 0; e < 32; e += 8) {
           float v[8];
 #pragma unroll
-          for (int u = 0; u < 8; ++u) v[u] = l > 0.f ? __uint_as_float(ov[e + u]) * inv : 0.f;
+          for (int u = 0; u < 8; ++u) v[u] = l == 0.f ? 0.f : __uint_as_float(ov[e + u]) * inv;
           if (cur.slot < 0) {
             uint32_t w[4];
 #pragma unroll
@@ -1063,9 +1115,13 @@ __global__ void __launch_bounds__(256) attn_kv8_join_kernel(TcDev d) {
       }
     }
     float top = M;
+    bool any = false;                                  // (a NaN counts, and makes the row NaN)
 #pragma unroll
-    for (int u = 0; u < 4; ++u) top = fmaxf(top, ls[u]);
-    if (top == -INFINITY) continue;
+    for (int u = 0; u < 4; ++u) {
+      top = fmaxf(top, ls[u]);
+      any = any || ls[u] != -INFINITY;
+    }
+    if (!any) continue;
     const float f = M == -INFINITY ? 0.f : ex2(M - top);
     sum *= f;
 #pragma unroll
@@ -1081,7 +1137,7 @@ __global__ void __launch_bounds__(256) attn_kv8_join_kernel(TcDev d) {
     }
     M = top;
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const size_t row = size_t(rec.o + t) * a.H_q + rec.h * a.G + g;
   __nv_bfloat162 lo = __floats2bfloat162_rn(acc[0] * inv, acc[1] * inv);
   __nv_bfloat162 hi = __floats2bfloat162_rn(acc[2] * inv, acc[3] * inv);
@@ -1090,7 +1146,7 @@ __global__ void __launch_bounds__(256) attn_kv8_join_kernel(TcDev d) {
   w.y = *reinterpret_cast<uint32_t*>(&hi);
   *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + row * kD + 4 * lane) = w;
   if (lane == 0 && a.lse)
-    a.lse[row] = sum > 0.f ? (M + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+    a.lse[row] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
 }
 
 // ------------------------------------------------------------------------------ host

@@ -501,6 +501,11 @@ __device__ __forceinline__ void split_p4(const float (&p)[4], uint32_t& hi, uint
       : "=r"(hi), "=r"(lo) : "f"(p[0]), "f"(p[1]), "f"(p[2]), "f"(p[3]));
 }
 
+// bit 7 of each byte of w that holds e4m3's NaN (0x7F, 0xFF)
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+
 // 32 lanes x 8 consecutive 32-bit columns
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile(

@@ -58,7 +58,8 @@ __global__ void __launch_bounds__(kCompact8Threads) kv8_compact_kernel(Compact8D
     for (int d = tid; d <= na; d += kCompact8Threads) {
       const int pd = prow[d];
       const long long src = (long long)P + pd, dst = (long long)P + d;
-      const bool good = (d == 0 ? pd == 0 : pd >= d) && src / a.bs < a.max_blocks;
+      const bool good = (d == 0 ? pd == 0 : pd >= d) && src / a.bs < a.max_blocks &&
+                        src <= (long long)INT32_MAX - 1024;   // (slot numbers stay in 32 bits)
       if (!good) {
         flags |= SPEC_REQ_BAD_PARENT;
       } else {

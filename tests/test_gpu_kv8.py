@@ -268,6 +268,67 @@ def test_attention_rows_of_very_different_size():
     U.check_attention(c)
 
 
+@pytest.mark.parametrize("where", ["k", "v", "q", "all keys"])
+@pytest.mark.parametrize("Hq,H,T,dtype", [(4, 2, 4, torch.bfloat16), (8, 2, 4, torch.bfloat16), (8, 2, 30, torch.bfloat16),
+                                          (16, 2, 60, torch.bfloat16), (6, 2, 6, torch.float32)])
+def test_attention_nan_of_one_branch(Hq, H, T, dtype, where):
+    """A NaN in a tree node's row reaches the rows that see the node, and no others."""
+    rng = np.random.default_rng(T)
+    trees = [U.tree_bits(T, rng) for _ in range(3)]
+    c = U.AttnCase([3000, 125, 0], [T] * 3, Hq, H, bits=[b for t in trees for b in t], dtype=dtype, seed=T + Hq)
+    hit = []
+    for r, (P, node) in enumerate(zip(c.prefix, (1, T - 1, T // 2))):
+        o = r * T
+        hit += [o + i for i in range(T) if (trees[r][i] >> node) & 1]
+        page, row = int(c.table_np[r][(P + node) // 16]), (P + node) % 16
+        if where == "q":
+            hit = hit[:-sum((b >> node) & 1 for b in trees[r])] + [o + node]
+            c.q[o + node, :, 77] = float("nan")
+        elif where == "all keys" and r < 2:            # a request whose prefix has nothing but NaN scores
+            hit = [n for n in hit if n < o] + list(range(o, o + T))
+            for s in range(P + T):
+                c.k.view(torch.uint8)[int(c.table_np[r][s // 16]), :, s % 16, 3] = 0xFF
+        else:
+            cache = c.v if where == "v" else c.k
+            cache.view(torch.uint8)[page, :, row, 5] = 0x7F
+            cache.view(torch.uint8)[page, :, row, 126] = 0xFF
+    clean = [n for n in range(c.N) if n not in hit]
+    assert hit and (clean or where == "all keys")
+    c.run()
+    assert c.status.cpu().tolist() == [0] * 3
+    o, lse = c.o[hit].float(), c.lse[hit]
+    if where == "v":
+        assert torch.isnan(o[..., 5]).all() and torch.isnan(o[..., 126]).all() and torch.isfinite(lse).all()
+    else:
+        assert torch.isnan(o).all() and torch.isnan(lse).all()
+    q = c.q.clone()
+    c.q = torch.nan_to_num(q, nan=0.0)                 # (the oracle's copy; these rows are not compared)
+    if clean:
+        U.check_attention(c, rows=clean)
+
+
+def test_a_pool_of_one_block():
+    for dtype in (torch.bfloat16, torch.float32):
+        k, v = (torch.full((1, 2, 16, 128), 0x7F, dtype=torch.uint8, device="cuda") for _ in range(2))
+        ks, vs = (torch.full((1, 2), float("nan"), device="cuda") for _ in range(2))
+        x = torch.randn((3, 2, 128), device="cuda").to(dtype)
+        table, st, start, off = U.ints([0]).view(1, 1), U.ints([0]), U.ints([0]), U.ints([0, 3])
+        B.spec_kv8_append(B.kv8_append_params(x, x, k, v, ks, vs, table, start, off, st))
+        o, lse = torch.empty_like(x), torch.empty((3, 2), device="cuda")
+        p = B.attention_kv8_params(x, k, v, ks, vs, table, start, off, U.mask_words([1, 2, 4], 3), 3, o, lse, st)
+        B.spec_tree_attention_kv8(p, torch.empty(max(256, B.spec_attention_kv8_workspace_size(p)), dtype=torch.uint8, device="cuda"))
+        torch.cuda.synchronize()
+        want = v.view(U.E4M3).float()[0, :, :3].transpose(0, 1) * vs[0][None, :, None]
+        # (one key a row: its V row, the weight's two pieces and the output's rounding apart)
+        assert st.cpu().tolist() == [0] and (o.float() - want).abs().max() <= 2.0 ** -6 * want.abs().max()
+
+
+def test_attention_refuses_a_workspace_elsewhere():
+    c = U.AttnCase([30], [1], 4, 2)
+    with pytest.raises(ValueError, match="workspace"):
+        B.spec_tree_attention_kv8(c.params(), torch.empty(1 << 24, dtype=torch.uint8))
+
+
 def test_attention_explicit_scale_and_no_lse():
     c = U.AttnCase([200, 4], [3, 20], 4, 2, seed=18)
     c.run(scale=0.02)
