@@ -11,9 +11,9 @@
 // next one (accumulators are double-buffered by unit).
 // Warps: 0 copies K, 2 copies V, 1 issues the scores' products, 3 the output's, 4-7 and 8-11
 // softmax, 12-15 split the queries and write the output, 16 brings the scales, 17 walks the items.
-// Measured: 64 single tokens over 1024 .. 32768 slots (2.2 GB) 340 us, 6.5 TB/s, 96% of the copy
-// rate; 16 chains of 6, 32 KV heads, 2048 slots (271 MB) 52.5 us, 5.2 TB/s; one token over 2047
-// slots (4 MB) 10.7 us, all of it latency: the start, the walk to the first page, a tile, the join.
+// Measured: 64 single tokens over 1024 .. 32768 slots (2.2 GB) 335 - 339 us, 6.6 TB/s, 97% of the
+// copy rate; 16 chains of 6, 32 KV heads, 2048 slots (271 MB) 53 us, 5.1 TB/s; one token over 2047
+// slots (4 MB) 11.0 us, all of it latency: the start, the walk to the first page, a tile, the join.
 //
 // attn_kv8_tile_kernel: longer units in tiles of 128 query rows (G heads x 128 / G tree tokens).
 // S = Q K^T (M = N = 128, both pieces of Q into one accumulator); P's pieces go to TMEM as the A
@@ -27,9 +27,10 @@
 // form them again.  Three S buffers (TMEM columns 0-383, P over S) keep the scores of the next
 // tiles coming while one is in the softmax and one in the output's product; O has columns 384-511.
 // Warps: 0-3 as above, 4-19 softmax, 20-23 queries and output, 24 scales, 25 items.
-// Measured: 32 trees of 46 over 8192 slots (32 query heads on 8) 280 us, 706 TFLOP/s of scores and
-// output, the tensor pipe busy 42% of the time; 64 ragged trees over 1024 .. 32768 slots (64 query
-// heads on 8) 1380 us, 890 TFLOP/s.  The bf16 cache takes 289 and 1554 us on these shapes.
+// Measured: 32 trees of 46 over 8192 slots (32 query heads on 8) 285 us, 693 TFLOP/s of scores and
+// output, the tensor pipe busy 42% of the time (5 us are the look for NaN in the tree slots' V
+// rows); 64 ragged trees over 1024 .. 32768 slots (64 query heads on 8) 1352 - 1400 us, 890
+// TFLOP/s.  The bf16 cache takes 289 and 1554 us on these shapes.
 //
 // Scales: a score is code product * (K scale of the slot's page * the row's query scale); the V
 // scale joins the exponent, y = score + log2(V scale), and the weight 2^(y - ref) goes into the
@@ -107,7 +108,7 @@ __device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[N]) {
 }
 
 // A V row of a tile in shared memory; a warp's lanes hold neighbouring rows and start at different
-// vectors of them, in different banks.  (Not unrolled: the masked tiles are few.)
+// vectors of them, in different banks.  (The stores are not unrolled: masked tiles are few.)
 __device__ __forceinline__ void clear_row(uint8_t* row) {
   uint4* w = reinterpret_cast<uint4*>(row);
 #pragma unroll 1
