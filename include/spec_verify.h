@@ -506,8 +506,8 @@ spec_status_t spec_kv8_append(const spec_kv8_append_params* p, spec_stream_t str
  * with head_dim 128, block_size 16, 32, 64 or 128 and H_q / H_kv <= 128 runs on the tcgen05
  * tensor cores, everything else on a CUDA-core kernel.
  * Requests with req_status bits other than BAD_BLOCK and TIMEOUT, or with T_r > T_max, have no
- * rows written; a request whose live slots lie beyond its table row gets SPEC_REQ_BAD_BLOCK and
- * no rows written; one with a bad block id gets SPEC_REQ_BAD_BLOCK and unspecified rows.
+ * rows written; a request whose live slots lie beyond its table row (or 2^31 - 1025) gets
+ * SPEC_REQ_BAD_BLOCK and no rows written; one with a bad block id gets SPEC_REQ_BAD_BLOCK and unspecified rows.
  * workspace: spec_attention_kv8_workspace_size bytes, 256-byte aligned, contents arbitrary; calls
  * that may overlap on the GPU (other streams, captured graphs) need one each.
  * Errors: as spec_tree_attention.

@@ -575,6 +575,27 @@ def test_fork_refuses_bad_pages_and_lengths():
 
 # ------------------------------------------------------------------------------ far addresses
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_slots_at_the_end_of_32_bits_are_refused(dtype):
+    """A table row of 2^27 - 1 pages of 16: the slots' numbers fit, a tile past them does not."""
+    H, d, P, T = 1, 128, 2 ** 31 - 25, 5
+    table = torch.zeros((1, 2 ** 27 - 1), dtype=torch.int32, device="cuda")
+    k, v = (torch.zeros((1, 4, H, 16, d), dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.ones((1, 4, H), device="cuda") for _ in range(2))
+    x = torch.ones((T, H, d), device="cuda").to(dtype)
+    pre, off = U.ints([P]), U.ints([0, T])
+    st = [U.ints([0]) for _ in range(2)]
+    o, lse = torch.full_like(x, 77.0), torch.full((T, H), 55.0, device="cuda")
+    p = B.attention_kv8_params(x, k[0], v[0], ks[0], vs[0], table, pre, off, U.mask_words(U.chain_bits(T), T), T, o, lse, st[0])
+    B.spec_tree_attention_kv8(p, torch.empty(max(256, B.spec_attention_kv8_workspace_size(p)), dtype=torch.uint8, device="cuda"))
+    outs = [U.ints([0]), torch.zeros((1, 3, 2), dtype=torch.int32, device="cuda"), U.ints([0])]
+    path = torch.tensor([[0, 2, 4]], dtype=torch.int32, device="cuda")
+    B.spec_kv8_compact(B.kv8_compact_params(k, v, ks, vs, table, pre, path, U.ints([2]), st[1], *outs, 3))
+    torch.cuda.synchronize()
+    assert [s.item() for s in st] == [32, 1] and outs[0].item() == P
+    assert (o == 77).all() and (lse == 55).all() and (k == 0).all() and (v == 0).all() and (ks == 1).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_pages_beyond_four_gigabytes(dtype):
     """The same calls on a small pool and on one whose pages lie past 2^32 bytes: bit for bit alike."""
     H, Hq, bs, d, L, far = 8, 16, 16, 128, 2, 2 ** 32 // (8 * 16 * 128)
