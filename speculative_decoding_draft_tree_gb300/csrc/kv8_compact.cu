@@ -48,10 +48,11 @@ __global__ void __launch_bounds__(kCompact8Threads) kv8_compact_kernel(Compact8D
   const int P = a.prefix_len[r], na = a.n_acc[r];
   const int32_t* prow = a.path + size_t(r) * a.max_path;
   const int32_t* trow = a.block_table + size_t(r) * a.max_blocks;
-  // every CTA of the request checks its path alike
-  bool ok = a.req_status[r] == 0 && na >= 0 && na < a.max_path && P >= 0;
+  // Every CTA of the request checks its path alike.  The reporting CTA's bits may appear in the status
+  // while another one reads it, so a CTA takes one verdict of it for all its threads: threads apart
+  // would check some steps of the path, skip others, and move rows by those that nobody checked.
   if (tid == 0) s_moves = 0;
-  __syncthreads();
+  bool ok = __syncthreads_and(a.req_status[r] == 0) && na >= 0 && na < a.max_path && P >= 0;
   int flags = 0;
   bool any = false;
   if (ok) {

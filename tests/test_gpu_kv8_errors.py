@@ -1,0 +1,57 @@
+"""GPU tests of data errors in the caches' operators: what has to be reported, and that nothing is
+written for a request that is refused."""
+import numpy as np
+import pytest
+import torch
+
+import kv8_util as U
+from speculative_decoding_draft_tree_gb300 import binding as B
+
+pytestmark = pytest.mark.gpu
+
+
+def _compact_case(late, T=200, Bn=24, bs=16, seed=0):
+    """Paths of T - 1 steps that move every row but the first; each odd request's `late` steps read a
+    page outside the pool (or, for "parent", step below their index)."""
+    rng = np.random.default_rng(seed)
+    prefix = rng.integers(0, 60, Bn).tolist()
+    nodes = 2 * T
+    need = [-(-(p + nodes) // bs) for p in prefix]
+    nb = sum(need) + 2
+    table = U.table_for(need, nb, rng)
+    path = np.array([[0] + [d + 100 for d in range(1, T)] for _ in range(Bn)], dtype=np.int32)
+    want = [0] * Bn
+    for r in range(1, Bn, 2):
+        if late == "page":
+            want[r] = 32                                   # slots that only steps from 64 on read or write
+            table[r, (prefix[r] + 100 + 64 + 5 * r) // bs + 1] = -1 if r % 4 == 1 else nb + 3
+        else:
+            want[r] = 1
+            path[r, 64 + 5 * r % 100] = 3
+    return prefix, table, path, nb, want
+
+
+@pytest.mark.parametrize("late", ["page", "parent"])
+def test_kv8_compact_refuses_a_late_bad_step_in_every_cta(late):
+    """Long paths whose bad step lies in other warps' share, many layers and heads, so that many CTAs
+    of a request check it while one of them reports it."""
+    L, H, d, bs, T = 24, 16, 32, 16, 200
+    prefix, table, path, nb, want = _compact_case(late, T)
+    rng = np.random.default_rng(1)
+    (k, ks), (v, vs) = [U.random_cache(L, nb, H, bs, d, rng) for _ in range(2)]
+    before = [t.clone() for t in (k.view(torch.uint8), v.view(torch.uint8), ks, vs)]
+    Bn = len(prefix)
+    tab, pre, pth = torch.from_numpy(table).cuda(), U.ints(prefix), torch.from_numpy(path).cuda()
+    n_acc = U.ints([T - 1] * Bn)
+    bad = [r for r in range(Bn) if want[r]]
+    pages = np.unique(np.concatenate([table[r][(table[r] >= 0) & (table[r] < nb)] for r in bad]))
+    for _ in range(5):
+        st, lens, used = (torch.zeros(Bn, dtype=torch.int32, device="cuda") for _ in range(3))
+        moves = torch.zeros((Bn, T, 2), dtype=torch.int32, device="cuda")
+        B.spec_kv8_compact(B.kv8_compact_params(k, v, ks, vs, tab, pre, pth, n_acc, st, lens, moves, used, T))
+        torch.cuda.synchronize()
+        assert st.cpu().tolist() == want
+        assert lens.cpu().tolist() == [p if want[r] else p + T for r, p in enumerate(prefix)]
+        assert (moves[bad] == -1).all()
+        for t, b in zip((k.view(torch.uint8), v.view(torch.uint8), ks, vs), before):
+            assert torch.equal(t[:, pages], b[:, pages])
