@@ -35,8 +35,9 @@ __global__ void __launch_bounds__(kCompactThreads) kv_compact_kernel(CompactDev 
   const int32_t* trow = a.block_table + size_t(r) * a.max_blocks;
   __shared__ int s_bad;
   if (tid == 0) s_bad = 0;
-  __syncthreads();
-  bool ok = a.req_status[r] == 0 && na >= 0 && na < a.max_path && P >= 0;
+  // one verdict of the status for the whole CTA: layer 0's bits may appear while another layer's CTA
+  // reads it, and threads apart would leave steps of the path unchecked
+  bool ok = __syncthreads_and(a.req_status[r] == 0) && na >= 0 && na < a.max_path && P >= 0;
   if (ok) {
     for (int d = tid; d <= na; d += blockDim.x) {
       const int pd = prow[d];

@@ -55,3 +55,28 @@ def test_kv8_compact_refuses_a_late_bad_step_in_every_cta(late):
         assert (moves[bad] == -1).all()
         for t, b in zip((k.view(torch.uint8), v.view(torch.uint8), ks, vs), before):
             assert torch.equal(t[:, pages], b[:, pages])
+
+
+@pytest.mark.parametrize("late", ["page", "parent"])
+def test_kv_compact_refuses_a_late_bad_step_in_every_cta(late):
+    """The same in the 16-bit cache."""
+    L, H, d, bs, T = 48, 4, 32, 16, 200
+    prefix, table, path, nb, want = _compact_case(late, T)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    k, v = (torch.randn((L, nb, H, bs, d), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    before = (k.clone(), v.clone())
+    Bn = len(prefix)
+    tab, pre, pth = torch.from_numpy(table).cuda(), U.ints(prefix), torch.from_numpy(path).cuda()
+    n_acc = U.ints([T - 1] * Bn)
+    bad = [r for r in range(Bn) if want[r]]
+    pages = np.unique(np.concatenate([table[r][(table[r] >= 0) & (table[r] < nb)] for r in bad]))
+    for _ in range(5):
+        st, lens, used = (torch.zeros(Bn, dtype=torch.int32, device="cuda") for _ in range(3))
+        moves = torch.zeros((Bn, T, 2), dtype=torch.int32, device="cuda")
+        B.spec_kv_compact(B.compact_params(k, v, tab, pre, pth, n_acc, st, lens, moves, used, T))
+        torch.cuda.synchronize()
+        assert st.cpu().tolist() == want
+        assert lens.cpu().tolist() == [p if want[r] else p + T for r, p in enumerate(prefix)]
+        assert (moves[bad] == -1).all()
+        for t, b in zip((k, v), before):
+            assert torch.equal(t[:, pages], b[:, pages])
