@@ -465,9 +465,12 @@ spec_status_t spec_echo_select_pack(const spec_draft_pool* pool, int32_t K_max,
  *   head_dim, 16-byte multiples), so that slices of a fused projection need no copy; rows from
  *   row_offset[B] on are ignored.  start [B], row_offset [B+1], block_table
  *   [B][max_blocks_per_req], req_status [B] int32.
- * Data errors: a request with other req_status bits than SPEC_REQ_BAD_BLOCK is not touched; a
- * negative start or inconsistent row_offset gives SPEC_REQ_BAD_SIZE and nothing is written;
- * rows whose page is beyond the table row or outside [0, num_blocks) are not written and give
+ * Data errors: a request with other req_status bits than SPEC_REQ_BAD_BLOCK is not touched.  A
+ * request, with rows or without, gets SPEC_REQ_BAD_SIZE and nothing is written for it if its start
+ * is negative, its slots pass 2^31 - 1, or its row_offset pair is negative, goes backwards, passes N
+ * or begins below an offset of an earlier request (so with row_offset 0, 5, 3, 8 the second and the
+ * third are refused).  N = 0 launches nothing and reports nothing.
+ * Rows whose page is beyond the table row or outside [0, num_blocks) are not written and give
  * SPEC_REQ_BAD_BLOCK.
  * Errors: SPEC_ERR_INVALID_ARG (null / misaligned pointers, bad sizes or strides),
  * SPEC_ERR_UNSUPPORTED (head_dim not a multiple of 16 or above 256, block_size above 1024, more

@@ -53,13 +53,14 @@ def append(codes, scale, x, table, start, row_offset, bs, status=None):
     num_blocks, H = scale.shape
     N = x.shape[0]
     added = [0] * len(start)
+    top = int(row_offset[0])                            # the largest offset so far
     for r in range(len(start)):
         o, o1, p0 = int(row_offset[r]), int(row_offset[r + 1]), int(start[r])
+        bad = o < 0 or o1 < o or o1 > N or o < top or p0 < 0 or p0 + o1 - o > 2 ** 31 - 1
+        top = max(top, o, o1)
         if status is not None and int(status[r]) & ~32:
             continue
-        if o1 <= o:
-            continue
-        if o < 0 or o1 > N or p0 < 0:
+        if bad:
             added[r] |= 2
             continue
         t = 0

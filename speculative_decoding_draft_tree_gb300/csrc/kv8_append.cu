@@ -71,6 +71,15 @@ template <> struct Codes<float> {
   }
 };
 
+// Offsets [o, o1) and first slot p0 of a request that cannot be appended, and its report (a request
+// that another call has flagged keeps its bits).
+__device__ __forceinline__ bool bad_request(const AppendDev& a, int o, int o1, int p0) {
+  return o < 0 || o1 < o || o1 > a.N || p0 < 0 || (long long)p0 + o1 - o > INT32_MAX;
+}
+__device__ __forceinline__ void report_bad(const AppendDev& a, int r) {
+  if ((a.req_status[r] & ~SPEC_REQ_BAD_BLOCK) == 0) atomicOr(&a.req_status[r], SPEC_REQ_BAD_SIZE);
+}
+
 template <typename T, int W>
 __global__ void __launch_bounds__(kAppendThreads, 3) kv8_append_kernel(AppendDev a) {
   constexpr int E = elem<T>::per16;
@@ -82,10 +91,37 @@ __global__ void __launch_bounds__(kAppendThreads, 3) kv8_append_kernel(AppendDev
   // heads vary fastest over the CTAs: a token's heads are neighbours in x
   const int win = int(blockIdx.x / a.columns), column = int(blockIdx.x - uint32_t(win) * a.columns);
   const int n0 = win * a.window, n1 = min(a.N, n0 + a.window);
-  // the request of token n0: as many requests end at or before it
+  // The request of token n0: as many requests end at or before it, where offsets only go up.  CTA 0
+  // reports the requests that cannot be appended, whether or not they own a token.
   int r = 0;
-  for (int i = 0; i < a.B; i += kAppendThreads)
-    r += __syncthreads_count(i + tid < a.B && a.row_offset[i + tid + 1] <= n0);
+  bool back = false;
+  for (int i = 0; i < a.B; i += kAppendThreads) {
+    const int q = i + tid;
+    int o = 0, o1 = 0;
+    if (q < a.B) {
+      o = a.row_offset[q];
+      o1 = a.row_offset[q + 1];
+      if (blockIdx.x == 0 && bad_request(a, o, o1, a.start[q])) report_bad(a, q);
+    }
+    back = back || o1 < o;
+    r += __syncthreads_count(q < a.B && o1 <= n0);
+  }
+  // Each warp's largest offset of the requests walked past (not in a register: the vectors in flight need
+  // them all).  It decides only where some offsets go backwards, which takes the walk from the
+  // first request on.
+  __shared__ int s_top[kAppendThreads / 32];
+  if (lane == 0) s_top[tid >> 5] = INT32_MIN;
+  back = __syncthreads_or(back);
+  if (back) {
+    r = 0;
+    if (blockIdx.x == 0 && tid == 0) {
+      for (int q = 0, t = INT32_MIN; q < a.B; ++q) {
+        const int o = a.row_offset[q];
+        if (o < t) report_bad(a, q);
+        t = max(t, max(o, a.row_offset[q + 1]));
+      }
+    }
+  }
   const int unit = column * kTeams + team;          // (head, cache)
   const bool mine = unit < 2 * a.H_kv;
   const int h = unit >> 1;
@@ -105,19 +141,20 @@ __global__ void __launch_bounds__(kAppendThreads, 3) kv8_append_kernel(AppendDev
   int n = n0;
   while (n < n1 && r < a.B) {                       // uniform across the CTA
     const int o = a.row_offset[r], o1 = a.row_offset[r + 1], p0 = a.start[r];
-    if (n >= o1) {
+    const bool bad = bad_request(a, o, o1, p0) || o < s_top[tid >> 5];
+    if (bad || n >= o1) {
+      __syncwarp();
+      if (lane == 0) s_top[tid >> 5] = max(s_top[tid >> 5], max(o, o1));
+      __syncwarp();
       ++r;
       continue;
     }
-    if (o > n) {                                    // offsets that start late or go backwards
+    if (o > n) {                                    // offsets that start late, or a bad request before
       n = o;
       continue;
     }
-    const bool bad = o < 0 || o1 > a.N || p0 < 0 || (long long)p0 + (o1 - o) > INT32_MAX;
-    if (bad || (a.req_status[r] & ~SPEC_REQ_BAD_BLOCK) != 0) {
-      if (bad && tid == 0) atomicOr(&a.req_status[r], SPEC_REQ_BAD_SIZE);
+    if ((a.req_status[r] & ~SPEC_REQ_BAD_BLOCK) != 0) {
       n = o1;
-      ++r;
       continue;
     }
     const int slot = p0 + (n - o), row = slot % a.bs;

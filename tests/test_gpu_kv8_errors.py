@@ -6,6 +6,7 @@ import torch
 
 import kv8_util as U
 from speculative_decoding_draft_tree_gb300 import binding as B
+from test_gpu_kv8 import AppendCase
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +81,43 @@ def test_kv_compact_refuses_a_late_bad_step_in_every_cta(late):
         assert (moves[bad] == -1).all()
         for t, b in zip((k, v), before):
             assert torch.equal(t[:, pages], b[:, pages])
+
+
+# ------------------------------------------------------------------------------------ append
+@pytest.mark.parametrize("off,start,want", [
+    ([0, 18, 30], [0, 0], [0, 2]),                        # begins at N and ends past it
+    ([0, 18, 25, 40], [3, 0, 0], [0, 2, 2]),
+    ([0, 5, 3, 8, 18], [0, 7, 1, 20], [0, 2, 2, 0]),      # goes backwards; begins below an earlier offset
+    ([6, 2, 2, 9, 18], [0, 0, 4, 1], [2, 2, 2, 0]),
+    ([0, 12, 5, 14, 18], [0, 0, 0, 9], [0, 2, 2, 0]),
+    ([-3, 0, 9, 18], [0, 2, 5], [2, 0, 0]),               # a negative offset without a row in [0, N)
+    ([-9, -4, 6, 18], [0, 0, 1], [2, 2, 0]),
+    ([0, 7, 7, 18, 18], [0, -1, 3, -8], [0, 2, 0, 2]),    # a negative start without rows
+    ([0, 9, 18], [2 ** 31 - 9, 4], [2, 0]),               # slots past 32 bits
+    ([18, 18, 18], [0, 0], [0, 0]),
+])
+@pytest.mark.parametrize("H", [2, 40])
+def test_append_reports_every_request_that_cannot_be_appended(off, start, want, H):
+    c = AppendCase([0] * len(start), [18] + [0] * (len(start) - 1), H=H, bs=4, seed=len(off), width=8, extra=40)
+    rng = np.random.default_rng(3)
+    c.table.copy_(torch.from_numpy(rng.permutation(c.nb)[:8 * len(start)].reshape(len(start), 8).astype(np.int32)))
+    c.start, c.off = start, np.array(off)
+    c.check()
+    assert c.status.cpu().tolist() == want
+    c.status.fill_(4)                                     # flagged by an earlier call: kept as it is
+    c.check()
+    assert c.status.cpu().tolist() == [4] * len(start)
+
+
+@pytest.mark.parametrize("n", [3, 200])
+def test_append_offsets_that_go_backwards_among_many_requests(n):
+    """Several hundred requests and windows of several tokens; two stretches go backwards."""
+    Bn, bs = 600, 16
+    rng = np.random.default_rng(n)
+    sizes = rng.integers(0, n, Bn)
+    c = AppendCase(rng.integers(0, 40, Bn).tolist(), sizes.tolist(), H=1, d=32, bs=bs, seed=n)
+    c.off[100] = c.off[103] + 2
+    c.off[400:403] = c.off[390]
+    c.check()
+    st = c.status.cpu().numpy()
+    assert (st == 2).sum() >= 3 and (st == 0).sum() > 500
