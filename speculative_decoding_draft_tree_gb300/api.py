@@ -114,7 +114,9 @@ class VerifyStep:
         H_kv, block_size, d] (torch.float8_e4m3fn or uint8) with scales [L, num_blocks, H_kv],
         addressed by the workload's block table.  The round quantises the tree tokens' rows k_new,
         v_new ([N, H_kv, d], keys already rotated) into layer 0's tree slots, attends over layer 0
-        and commits the accepted path in every layer."""
+        and commits the accepted path in every layer.  k_new and v_new are inputs of a round like q:
+        upload() brings them and twin() gives the second step its own; the cache is shared.  Call
+        this before twin() or RoundPipeline."""
         w = self.w
         if self.rope_p is not None:
             raise ValueError("enable_kv8 does not combine with enable_rope, which writes the 16- "
@@ -220,11 +222,14 @@ class VerifyStep:
         """Device tensors that a new round brings from the host: the draft tree, its logits,
         uniforms, Q and the tree tokens' K/V rows (slots P..P+T-1 are written by the caller;
         here the whole layer-0 tree region is represented by the block-table-addressed cache
-        rows, which stay resident) -- see run_from_host."""
+        rows, which stay resident) -- see run_from_host.  With enable_kv8, k_new and v_new too."""
         w = self.w
-        return dict(parent=w.parent, node_offset=w.node_offset, prefix_len=w.prefix_len,
-                    tokens=w.tokens, draft_row=w.draft_row, uniforms=w.uniforms, target=w.target,
-                    draft=w.draft, q=w.q, block_table=w.block_table)
+        inputs = dict(parent=w.parent, node_offset=w.node_offset, prefix_len=w.prefix_len,
+                      tokens=w.tokens, draft_row=w.draft_row, uniforms=w.uniforms, target=w.target,
+                      draft=w.draft, q=w.q, block_table=w.block_table)
+        if self.kv8 is not None:
+            inputs.update(k_new=self.kv8[4], v_new=self.kv8[5])
+        return inputs
 
     def pinned_host_inputs(self) -> Dict[str, torch.Tensor]:
         """The round's inputs in pinned host memory: one packed buffer ("_pack", same layout as
@@ -270,11 +275,12 @@ class VerifyStep:
         pack, fresh = _packed(src, self.w.target.device)
         for k, v in fresh.items():
             v.copy_(src[k])
+        rows = [fresh.pop(k) for k in ("k_new", "v_new") if k in fresh]
         step = VerifyStep(dataclasses.replace(self.w, **fresh), self.sibling_rule,
                           self.lse is not None, self.verify_path)
         step._in_pack = pack
         if self.kv8 is not None:
-            step.enable_kv8(*self.kv8)
+            step.enable_kv8(*self.kv8[:4], *rows)
         return step
 
     def host_output_buffers(self) -> Dict[str, torch.Tensor]:
