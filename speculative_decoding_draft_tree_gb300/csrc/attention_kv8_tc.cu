@@ -3,7 +3,7 @@
 // attn_kv8_rows_kernel: units of at most 8 or 16 query rows (T x G: single tokens and short chains).
 // S^T = K Q^T (M = 128 slots on the TMEM lanes, N = the rows' hi pieces, then their lo pieces), so
 // that the softmax spends its lanes on keys; O^T += V^T P^T with V read as an MN-major operand and
-// P^T's pieces stacked the same way.  Bound by the codes' bytes: a tile's 32 KB take ~1400 clocks
+// P^T's three pieces stacked the same way, each with columns of O of its own.  Bound by the codes' bytes: a tile's 32 KB take ~1400 clocks
 // of an SM's share of HBM and the products a quarter of that, so what has to keep up is the
 // softmax, whose step is a chain of latencies (wait, TMEM load, group vote, exponentials, stores).
 // Two groups of four warps take alternate tiles, each with references, sums and an accumulator of
@@ -11,9 +11,9 @@
 // next one (accumulators are double-buffered by unit).
 // Warps: 0 copies K, 2 copies V, 1 issues the scores' products, 3 the output's, 4-7 and 8-11
 // softmax, 12-15 split the queries and write the output, 16 brings the scales, 17 walks the items.
-// Measured: 64 single tokens over 1024 .. 32768 slots (2.2 GB) 335 - 339 us, 6.6 TB/s, 97% of the
-// copy rate; 16 chains of 6, 32 KV heads, 2048 slots (271 MB) 53 us, 5.1 TB/s; one token over 2047
-// slots (4 MB) 11.0 us, all of it latency: the start, the walk to the first page, a tile, the join.
+// Measured: 64 single tokens over 1024 .. 32768 slots (2.2 GB) 343 - 349 us, 6.4 TB/s, 95% of the
+// copy rate; 16 chains of 6, 32 KV heads, 2048 slots (271 MB) 54 us, 5.1 TB/s; one token over 2047
+// slots (4 MB) 10.8 us, all of it latency: the start, the walk to the first page, a tile, the join.
 //
 // attn_kv8_tile_kernel: longer units in tiles of 128 query rows (G heads x 128 / G tree tokens).
 // S = Q K^T (M = N = 128, both pieces of Q into one accumulator); P's pieces go to TMEM as the A
@@ -35,7 +35,7 @@
 // Scales: a score is code product * (K scale of the slot's page * the row's query scale); the V
 // scale joins the exponent, y = score + log2(V scale), and the weight 2^(y - ref) goes into the
 // product with V's codes while the row sum takes 2^(y - ref) / (V scale).  So the weights that
-// enter the product fill e4m3's range whatever the pages' scales are.
+// enter the product fill their format's range whatever the pages' scales are.
 //
 // The waits are bounded; one that runs out raises the CTA's abort flag, after which no wait
 // blocks: the softmax groups, which meet at hardware barriers, still walk through their tiles, the
@@ -61,15 +61,22 @@ constexpr int kVStages = 5;
 template <int NR>
 struct Layout {
   static constexpr int kPiece = NR * 128;                // bytes of one piece of the rows
-  static constexpr int kPair = 2 * kPiece;               // hi, then lo
+  static constexpr int kPair = 2 * kPiece;               // Q: hi, then lo
+  // P: hi, mid, lo, and with 8 rows a piece that is never written (the products take columns by 16;
+  // what comes of it is not read)
+  static constexpr int kPieces = NR == 8 ? 4 : 3;
+  static constexpr int kTriple = kPieces * kPiece;
   static constexpr int kSmemQ = 0;                       // 2 buffers
   static constexpr int kSmemP = kSmemQ + 2 * kPair;      // 2 groups x 2 buffers
-  static constexpr int kSmemK = kSmemP + 4 * kPair;
+  static constexpr int kSmemK = kSmemP + 4 * kTriple;
   static constexpr int kSmemV = kSmemK + kKStages * kTile;
   static constexpr int kSmemBar = kSmemV + kVStages * kTile;
-  static constexpr uint32_t kN = 2 * NR;                 // columns of a product
+  static constexpr uint32_t kN = 2 * NR;                 // columns of a product of scores
+  static constexpr uint32_t kNO = kPieces * NR;          // of the output
   static constexpr uint32_t kTmemO = 4 * kN;             // S: group, buffer; O: group, unit parity
-  static constexpr uint32_t kTmemCols = 8 * kN;
+  static constexpr uint32_t kOStride = NR == 8 ? 32 : 64;
+  static constexpr uint32_t kTmemCols = NR == 8 ? 256 : 512;
+  static_assert(kTmemO + 4 * kOStride <= kTmemCols && kNO <= kOStride && kNO % 16 == 0, "TMEM");
   static_assert(kSmemK % 1024 == 0, "swizzled tiles on 1024-byte bounds");
 };
 
@@ -98,13 +105,14 @@ static_assert(smem_bytes<16>() <= 232448, "fits one CTA's shared memory");
 
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[N]) {
-  if constexpr (N == 16) tc::tmem_ld16(addr, r);
+  if constexpr (N == 8) tmem_ld8(addr, r);
+  else if constexpr (N == 16) tc::tmem_ld16(addr, r);
   else tc::tmem_ld32(addr, r);
 }
 template <int N>
 __device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[N]) {
-  if constexpr (N == 16) tc::tmem_st16(addr, r);
-  else tc::tmem_st32(addr, r);
+  if constexpr (N == 8) tmem_st8(addr, r);
+  else tc::tmem_st16(addr, r);
 }
 
 // A V row of a tile in shared memory; a warp's lanes hold neighbouring rows and start at different
@@ -215,7 +223,7 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
       // elected lane issues
       const bool is_qk = warp == 1;
       const uint32_t id_qk = idesc_e4m3(128, kN, false, false);
-      const uint32_t id_pv = idesc_e4m3(128, kN, true, false);
+      const uint32_t id_pv = idesc_e4m3(128, int(L::kNO), true, false) | kIdescBE5m2;
       const uint64_t dQ = tc::smem_desc(tc::smem_u32(sQ), 16, 1024);
       const uint64_t dP = tc::smem_desc(tc::smem_u32(sP), 16, 1024);
       const uint64_t dK = tc::smem_desc(tc::smem_u32(sK), 16, 1024);
@@ -258,9 +266,9 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc::tc_fence_after();
-            const uint32_t tO = tmem + L::kTmemO + (g * 2 + par) * kN;
+            const uint32_t tO = tmem + L::kTmemO + (g * 2 + par) * L::kOStride;
             const uint64_t va = dV + uint64_t(st) * (kTile >> 4);
-            const uint64_t pb = dP + uint64_t(g * 2 + b) * (L::kPair >> 4);
+            const uint64_t pb = dP + uint64_t(g * 2 + b) * (L::kTriple >> 4);
             if (elect_one()) {
 #pragma unroll
               for (int k = 0; k < 4; ++k)            // 32 slots a step: four groups of 8 V rows
@@ -290,7 +298,7 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
     const int kl = q * 32 + lane;                    // this lane's slot of a tile
     const int si = kl >> d.log2bs;
     const int bar_g = 1 + grp;
-    uint8_t* const pcol = sP + grp * 2 * L::kPair + (kl & 15);
+    uint8_t* const pcol = sP + grp * 2 * L::kTriple + (kl & 15);
     const int chunk = kl >> 4;
     int kt = 0;
     bool ok = true;                                  // no early exit: see the file's comment
@@ -303,7 +311,7 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
       const int par = li & 1;
       const int T = it.T, P = it.P, kv_len = P + T;
       const int nt = it.j1 - it.j0;
-      const uint32_t tO = tmem + lane_addr + L::kTmemO + (grp * 2 + par) * kN;
+      const uint32_t tO = tmem + lane_addr + L::kTmemO + (grp * 2 + par) * L::kOStride;
       const float4* qmul = reinterpret_cast<const float4*>(sh.qmul[par]);
       ok &= wait1(&sh.q_full[par], li >> 1, abort_flag);
       float add[NR], lsum[NR];
@@ -387,19 +395,22 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
             ok &= wait1(&sh.pv_done[grp][(kp >> 1) & 1], kp >> 2, abort_flag);
             __syncwarp();
             tc::tc_fence_after();
-            uint32_t ov[kN];
-            tmem_ld<kN>(tO, ov);
-            tc::tmem_ld_wait();
 #pragma unroll
-            for (int n = 0; n < kN; ++n)
-              ov[n] = __float_as_uint(__uint_as_float(ov[n]) * factor[n % NR]);
-            tmem_st<kN>(tO, ov);
+            for (int piece = 0; piece < 3; ++piece) {
+              uint32_t ov[NR];
+              tmem_ld<NR>(tO + piece * NR, ov);
+              tc::tmem_ld_wait();
+#pragma unroll
+              for (int n = 0; n < NR; ++n)
+                ov[n] = __float_as_uint(__uint_as_float(ov[n]) * factor[n]);
+              tmem_st<NR>(tO + piece * NR, ov);
+            }
             tc::tmem_st_wait();
           }
         }
         // weights: this slot's column of P^T, after the product that last read the buffer
         if (use > 0) ok &= wait1(&sh.pv_done[grp][b], use - 1, abort_flag);
-        uint8_t* pc = pcol + b * L::kPair;
+        uint8_t* pc = pcol + b * L::kTriple;
 #pragma unroll
         for (int n = 0; n < NR; n += 2) {
           // (a row that has seen nothing: -infinity + infinity)
@@ -407,14 +418,15 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
           const float p1 = y[n + 1] == -INFINITY ? 0.f : ex2(y[n + 1] + add[n + 1]);
           lsum[n] = fmaf(p0, iv, lsum[n]);
           lsum[n + 1] = fmaf(p1, iv, lsum[n + 1]);
-          uint32_t hi, lo;
-          split_p2(p0, p1, hi, lo);
+          const Split2 s = split_p2(p0, p1);
           const int o0 = (n >> 3) * 1024 + (n & 7) * 128 + ((chunk ^ (n & 7)) << 4);
           const int o1 = (n >> 3) * 1024 + ((n & 7) + 1) * 128 + ((chunk ^ ((n & 7) + 1)) << 4);
-          pc[o0] = uint8_t(hi);
-          pc[o1] = uint8_t(hi >> 8);
-          pc[L::kPiece + o0] = uint8_t(lo);
-          pc[L::kPiece + o1] = uint8_t(lo >> 8);
+          pc[o0] = uint8_t(s.hi >> 8);
+          pc[o1] = uint8_t(s.hi >> 24);
+          pc[L::kPiece + o0] = uint8_t(s.mid >> 8);
+          pc[L::kPiece + o1] = uint8_t(s.mid >> 24);
+          pc[2 * L::kPiece + o0] = uint8_t(s.lo >> 8);
+          pc[2 * L::kPiece + o1] = uint8_t(s.lo >> 24);
         }
         // where keys are masked a NaN code of V times a zero weight must stay zero: stale rows past
         // the end are cleared, and a tree slot's NaN moves from V to the weights of the rows that
@@ -532,32 +544,39 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
         l1 += sh.sum[par][1][w][rn];
       }
       const float l = l0 * w0 + l1 * w1;
-      const float inv = l == 0.f ? 0.f : 1.f / l;    // (NaN stays NaN)
-      const float lse2 = l == 0.f ? -INFINITY : log2f(l) - top;
+      const float inv = l == 0.f ? 0.f : kSumMul / l;    // (NaN stays NaN)
+      const float lse2 = l == 0.f ? -INFINITY : log2f(l) + kSumShift - top;
       w0 *= inv;
       w1 *= inv;
       ok &= wait1(&sh.o_full[par], li >> 1, abort_flag);
       __syncwarp();
       tc::tc_fence_after();
       // (an accumulator that took no product in this unit has weight 0 and stale columns)
-      uint32_t ov[kN];
+      uint32_t ov[3][NR];
       float v[NR];
-      tmem_ld<kN>(tmem + lane_addr + L::kTmemO + par * kN, ov);
-      tc::tmem_ld_wait();
+      auto load_o = [&](int grp) {
+#pragma unroll
+        for (int piece = 0; piece < 3; ++piece)
+          tmem_ld<NR>(tmem + lane_addr + L::kTmemO + (grp * 2 + par) * L::kOStride + piece * NR, ov[piece]);
+        tc::tmem_ld_wait();
+      };
+      auto sum_o = [&](int n) {
+        return (__uint_as_float(ov[2][n]) + __uint_as_float(ov[1][n])) + __uint_as_float(ov[0][n]);
+      };
+      load_o(0);
 #pragma unroll
       for (int n = 0; n < NR; ++n) {
         const float u = __shfl_sync(0xffffffffu, w0, n);
-        v[n] = u != 0.f ? (__uint_as_float(ov[n]) + __uint_as_float(ov[n + NR])) * u : 0.f;
+        v[n] = u != 0.f ? sum_o(n) * u : 0.f;
       }
-      tmem_ld<kN>(tmem + lane_addr + L::kTmemO + (2 + par) * kN, ov);
-      tc::tmem_ld_wait();
+      load_o(1);
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sh.o_free[par]);
 #pragma unroll
       for (int n = 0; n < NR; ++n) {
         const float u = __shfl_sync(0xffffffffu, w1, n);
-        if (u != 0.f) v[n] = fmaf(__uint_as_float(ov[n]) + __uint_as_float(ov[n + NR]), u, v[n]);
+        if (u != 0.f) v[n] = fmaf(sum_o(n), u, v[n]);
         const size_t at = size_t(__shfl_sync(0xffffffffu, row, n)) * kD + col;
         if (n < nrows) {
           if (cur.slot < 0) static_cast<__nv_bfloat16*>(a.o)[at] = __float2bfloat16_rn(v[n]);
@@ -1022,8 +1041,8 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
       ok &= wait1(&sh.sum_full[par], li >> 1, abort_flag);
       const float l = (sh.sum[par][0][m] + sh.sum[par][1][m]) + (sh.sum[par][2][m] + sh.sum[par][3][m]);
       const float add = sh.add[par][m];
-      const float inv = l == 0.f ? 0.f : 1.f / l;    // (NaN stays NaN)
-      const float lse2 = l == 0.f ? -INFINITY : log2f(l) - add;
+      const float inv = l == 0.f ? 0.f : kSumMul / l;    // (NaN stays NaN)
+      const float lse2 = l == 0.f ? -INFINITY : log2f(l) + kSumShift - add;
       const size_t row = cur.slot < 0 ? size_t(cur.o + t) * a.H_q + cur.h * a.G + gl
                                       : size_t(cur.slot) * kRows + m;
       __syncwarp();

@@ -14,11 +14,11 @@
 // without.)
 //
 // 8-bit codes go to tcgen05.mma kind::f8f6f4 as they are.  The other operand of each product keeps
-// its precision as the sum of two 8-bit pieces, hi = e4m3(x) and lo = e4m3(x - hi), both multiplied
-// into the same fp32 accumulator: a bf16 query is exactly hi + lo (4 + 4 significant bits) but
-// for elements 2^-18 of the row's largest, a softmax weight keeps 8 bits (7 where hi is e5m2, in
-// the kernel of long units).  fp8 products run at
-// twice the bf16 rate, so the two pieces cost what one bf16 product does, and K and V are read by
+// its precision as a sum of 8-bit pieces, all multiplied into fp32 accumulators.  A bf16 query is
+// e4m3(x) + e4m3(x - e4m3(x)), exact (4 + 4 significant bits) but for elements 2^-18 of the row's
+// largest.  A softmax weight of a short unit is the sum of three e5m2 pieces (split_p2), 10 bits over 22
+// binades and 2^-17 of the range below; of a long one of two (split_p4).  fp8 products run at
+// twice the bf16 rate, so two pieces cost what one bf16 product does, and K and V are read by
 // the tensor core where TMA put them, one byte an element: converting them to bf16 first would
 // move 6 bytes of shared memory an element against 2, more than the SM has at HBM speed.
 #pragma once
@@ -37,11 +37,15 @@ constexpr int kTile = kBN * kD;                   // bytes
 constexpr long long kWaitLimit = 4000000000LL;    // clock cycles (~2 s)
 constexpr int kMaxCtas = 1024;
 // Weights enter the products as 2^(y - ref + kShift); the reference, a maximum seen before, moves
-// when a y passes it by more than 2, so that they stay below 2^8 <= 448 and a row's largest is at
+// when a y passes it by more than 2, so that they stay below 2^15 <= 57344 and a row's largest is at
 // least 2^kShift.  Two binades of slack: with one, the chains' units spent more on moving
 // references than on weights.
-constexpr float kShift = 6.f;
-constexpr float kCeil = 8.f;
+constexpr float kShift = 13.f;
+constexpr float kCeil = 15.f;
+// Row sums are kept times 2^-kSumShift: of weights up to 2^15.5 over V scales down to 2^-100, a million
+// keys' sum stays finite.
+constexpr float kSumShift = 10.f;
+constexpr float kSumMul = 1.f / 1024.f;
 constexpr float kMinVScale = 7.888609052210118e-31f;   // 2^-100
 
 struct MergeRec {
@@ -394,7 +398,7 @@ __device__ __forceinline__ void page_producer(const TcDev& d, ItemRing& items,
 }
 
 // The scales of each tile's pages into a ring: k[i] = K scale, lv[i] = log2 of the V scale, iv[i]
-// its reciprocal, i < 128 / bs.  One warp, four tiles at a time (lanes 8 u .. 8 u + 7: tile u), far
+// its reciprocal (times kSumMul), i < 128 / bs.  One warp, four tiles at a time (lanes 8 u .. 8 u + 7: tile u), far
 // enough ahead of the softmax to hide its dependent loads.
 struct ScaleSlot {
   float k[8], lv[8], iv[8];
@@ -447,7 +451,7 @@ __device__ __forceinline__ void scale_producer(const TcDev& d, ItemRing& items, 
         vs = fmaxf(vs, kMinVScale);
         o->k[i] = ks;
         o->lv[i] = log2f(vs);
-        o->iv[i] = 1.f / vs;
+        o->iv[i] = kSumMul / vs;
       }
       __syncwarp();
       if (lane < n) tc::mbar_arrive(full + (kt + lane) % kScaleRing);
@@ -473,20 +477,28 @@ __device__ __forceinline__ void split_q8(const uint4& w, float inv, uint2& hi, u
   kv8::unpack_e4m3x4(hi.y, b);
   lo.y = kv8::pack_e4m3x4(f[4] - b[0], f[5] - b[1], f[6] - b[2], f[7] - b[3]);
 }
-// two weights as two pieces of two codes each (16-bit words), by way of fp16: 11 bits, the
-// remainder after the first piece is exact
-__device__ __forceinline__ void split_p2(float a, float b, uint32_t& hi, uint32_t& lo) {
-  uint32_t w, back, rest;
-  uint16_t h, l;
-  asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(w) : "f"(a), "f"(b));
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(w));
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(h));
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(rest) : "r"(w), "r"(back));
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(rest));
-  hi = h;
-  lo = l;
+// Softmax weights as three e5m2 pieces of their fp16 value, hi + mid + lo.  An e5m2 code is the upper
+// byte of an fp16: a rounding add and a mask give a piece, and the subtractions are exact.  hi is
+// rounded to nearest (within 2^-3 of the weight), mid cut off (2^-2 of what is left; a NaN stays one
+// there), lo to nearest (2^-3 of the rest): over all fp16 values the sum is within 2^-10 of a weight
+// of at least 2^-7 and within 2^-17 of a smaller one.  (Pieces with more bits and less range, e4m3, lose
+// the weights below 2^-16 of a row's largest: of one key with most of the weight before a long flat
+// rest, the rest.)
+struct Split2 {
+  uint32_t hi, mid, lo;   // two weights: the codes are bytes 1 and 3
+};
+__device__ __forceinline__ Split2 split_p2(float a, float b) {
+  Split2 s;
+  asm("{\n\t.reg .b32 w, r;\n\t"
+      "cvt.rn.f16x2.f32 w, %4, %3;\n\t"
+      "add.u32 %0, w, 0x00800080;\n\tand.b32 %0, %0, 0xFF00FF00;\n\t"
+      "sub.rn.f16x2 r, w, %0;\n\t"
+      "and.b32 %1, r, 0xFF00FF00;\n\t"
+      "sub.rn.f16x2 r, r, %1;\n\t"
+      "add.u32 %2, r, 0x00800080;\n\t}"
+      : "=&r"(s.hi), "=&r"(s.mid), "=&r"(s.lo) : "f"(a), "f"(b));
+  return s;
 }
-
 // four weights (below 2^13) as two pieces of four codes: hi in e5m2, the upper byte of the fp16
 // value rounded to nearest, lo = e4m3 of the exact remainder (at most an eighth)
 __device__ __forceinline__ void split_p4(const float (&p)[4], uint32_t& hi, uint32_t& lo) {
@@ -507,6 +519,13 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
 }
 
 // 32 lanes x 8 consecutive 32-bit columns
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
@@ -550,7 +569,7 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool 
          (uint32_t(M >> 4) << 24);
 }
 
-constexpr uint32_t kIdescAE5m2 = 1u << 7;   // A's type field: e5m2
+constexpr uint32_t kIdescAE5m2 = 1u << 7, kIdescBE5m2 = 1u << 10;   // the type fields: e5m2
 
 // Reductions of NR values a lane over the 32 lanes: each of the first exchanges halves what a lane
 // holds, about NR shuffles instead of 5 NR.  Lane l ends with the result of row red_row<NR>(l).
