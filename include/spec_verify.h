@@ -504,8 +504,7 @@ spec_status_t spec_kv8_append(const spec_kv8_append_params* p, spec_stream_t str
  * or K; O alone for one in V, its column at least.
  * On the tensor cores a bf16 q enters the e4m3 products as two pieces, exact to 2^-18 of its row's
  * largest element.  A weight (times its slot's V scale) is kept to 2^-9 of itself or 2^-30 of the
- * row's largest, whichever is more; in units of more than 16 query rows to 2^-7 of itself or 2^-13 of
- * the largest.
+ * row's largest, whichever is more (2^-11 of itself in units of more than 16 query rows).
  * Every H_q / H_kv ratio, block_size and head_dim (multiple of 16, <= 256) is accepted; BF16
  * with head_dim 128, block_size 16, 32, 64 or 128 and H_q / H_kv <= 128 runs on the tcgen05
  * tensor cores, everything else on a CUDA-core kernel.

@@ -16,21 +16,25 @@
 // slots (4 MB) 10.8 us, all of it latency: the start, the walk to the first page, a tile, the join.
 //
 // attn_kv8_tile_kernel: longer units in tiles of 128 query rows (G heads x 128 / G tree tokens).
-// S = Q K^T (M = N = 128, both pieces of Q into one accumulator); P's pieces go to TMEM as the A
-// operand of O += P V.  Bound by the softmax's instructions before the tensor core (1024 clocks a
-// tile at the e4m3 rate; a tile takes ~2450): exponentials and e4m3 packing run at 32 results a
-// clock and SM, most of the rest at 64.  So P is split the cheapest way: hi is e5m2, which is the
-// upper byte of an fp16 (a rounding add and a mask), lo = e4m3(p - hi); e5m2's range also leaves
-// the reference eight binades of slack, so that it rarely moves.  A row belongs to four threads of
+// S = Q K^T (M = N = 128, both pieces of Q into one accumulator) on the e4m3 codes; O += P V in fp16:
+// four warps convert V's codes, which are fp16 values, in shared memory, ahead of the product, and P goes
+// to TMEM as the A operand with one conversion a pair of weights.  Each product runs 512 clocks a tile,
+// as two 8-bit pieces of P against the codes would, and P keeps fp16's 11 bits down to 2^-19 of a row's
+// largest weight.  (e5m2 and e4m3 pieces kept three bits below 2^-13: a long flat rest beside one heavy
+// key came out by up to an eighth wrong.  Three e5m2 pieces, right as well, took 367 and 1760 us on the
+// two shapes below.)  A tile takes ~2500 clocks: the exponentials and the conversion of V are ~770 of
+// them at 32 results a clock and SM, the products 1024, and no pipe is full; a step is a chain of waits,
+// TMEM loads, votes and stores, which all warps take together, tile after tile.
+// A row belongs to four threads of
 // four warps, each with 32 of a tile's keys: they form weights against the present reference at
 // once and vote on it meanwhile; where the vote says that it moves, they agree on the new one and
-// form them again.  Three S buffers (TMEM columns 0-383, P over S) keep the scores of the next
+// form them again; ten binades of slack make that rare.  Three S buffers (TMEM columns 0-383, P over S)
+// keep the scores of the next
 // tiles coming while one is in the softmax and one in the output's product; O has columns 384-511.
-// Warps: 0-3 as above, 4-19 softmax, 20-23 queries and output, 24 scales, 25 items.
-// Measured: 32 trees of 46 over 8192 slots (32 query heads on 8) 285 us, 693 TFLOP/s of scores and
-// output, the tensor pipe busy 42% of the time (5 us are the look for NaN in the tree slots' V
-// rows); 64 ragged trees over 1024 .. 32768 slots (64 query heads on 8) 1352 - 1400 us, 890
-// TFLOP/s.  The bf16 cache takes 289 and 1554 us on these shapes.
+// Warps: 0-3 as above, 4-19 softmax, 20-23 queries and output, 24 scales, 25 items, 28-31 V.
+// Measured: 32 trees of 46 over 8192 slots (32 query heads on 8) 294 us, 672 TFLOP/s of scores and
+// output; 64 ragged trees over 1024 .. 32768 slots (64 query heads on 8) 1447 us, 848 TFLOP/s.
+// The bf16 cache takes 289 and 1554 us on these shapes.
 //
 // Scales: a score is code product * (K scale of the slot's page * the row's query scale); the V
 // scale joins the exponent, y = score + log2(V scale), and the weight 2^(y - ref) goes into the
@@ -607,28 +611,31 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
 // ------------------------------------------------------------------------------ long units
 namespace tile {
 constexpr int kRows = 128;
-constexpr int kThreads = 896;
-constexpr int kCtlRegs = 56;       // warps 0-3 and 24-27
+constexpr int kThreads = 1024;
+constexpr int kCtlRegs = 40;       // warps 0-3 and 24-27
 constexpr int kSoftmaxRegs = 80;   // warps 4-19
-constexpr int kOutRegs = 72;       // warps 20-23, as launched
-static_assert(256 * kCtlRegs + 512 * kSoftmaxRegs + 128 * kOutRegs <= kThreads * 72, "register split");
-// Weights are 2^(y - ref + kLift); the reference moves when one passes 2^kTop (hi reaches 57344, lo
-// takes an eighth).  lo's step is 2^-9, i.e. 2^-12 of a row's largest weight; below that hi alone
-// still has three bits.
-constexpr float kLift = 3.f, kTop = 11.f;
-constexpr int kKStages = 4;
-constexpr int kVStages = 4;
+constexpr int kOutRegs = 56;       // warps 20-23 and 28-31
+static_assert(256 * kCtlRegs + 512 * kSoftmaxRegs + 256 * kOutRegs <= kThreads * 64, "register split");
+// Weights are 2^(y - ref + kLift), in fp16; the reference moves when one passes 2^kTop.  11 bits are
+// kept down to 2^-19 of a row's largest weight, and 2^-30 of it below.  (32 trees of 46, 64 ragged ones: lift
+// 3 297 and 1443 us, 5 302 and 1448, 7 307 and 1495, 9 315 and 1520.)
+constexpr float kLift = 5.f, kTop = 15.f;
+constexpr int kKStages = 3;
+constexpr int kVStages = 2;
 constexpr int kPair = 2 * kTile;                         // Q's two pieces
+constexpr int kHalves = 2 * kTile;                       // V in fp16: columns 0-63, then 64-127
 constexpr int kSmemQ = 0;                                // 2 buffers
 constexpr int kSmemK = kSmemQ + 2 * kPair;
 constexpr int kSmemV = kSmemK + kKStages * kTile;
-constexpr int kSmemBar = kSmemV + kVStages * kTile;
+constexpr int kSmemW = kSmemV + kVStages * kTile;        // 2 buffers of fp16
+constexpr int kSmemBar = kSmemW + 2 * kHalves;
 constexpr int kBufs = 3;                                 // S, with P over it
 constexpr uint32_t kTmemO = kBufs * 128;
 
 struct Shared {
   uint64_t q_full[2], q_empty[2];
   uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
+  uint64_t w_full[2], w_empty[2];
   uint64_t s_full[kBufs], p_full[kBufs], pv_done[kBufs];
   uint64_t sum_full[2], sum_free[2], o_full, o_free;
   uint64_t sc_full[kScaleRing], sc_empty[kScaleRing], drain[2];
@@ -637,7 +644,7 @@ struct Shared {
   float mx[4][kRows];             // per quarter of the keys: row maxima of an update
   float sum[2][4][kRows];         // per unit parity and quarter
   float add[2][kRows];            // per unit parity: kLift - reference
-  int v_nan[kBufs][kBN];          // per buffer and slot: 1 + the last tile whose V had a NaN there
+  uint32_t v_nan[2][4];           // per fp16 buffer of a masked tile: the slots whose V had a NaN
   uint32_t tmem;
   int abort, r0, r1;
   ItemRing items;
@@ -666,6 +673,7 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
   uint8_t* sQ = base + kSmemQ;
   uint8_t* sK = base + kSmemK;
   uint8_t* sV = base + kSmemV;
+  uint8_t* sW = base + kSmemW;
   Shared& sh = *reinterpret_cast<Shared*>(base + kSmemBar);
   const AttnKv8Dev& a = d.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -687,7 +695,9 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
     init(sh.k_full, kKStages, 1);
     init(sh.k_empty, kKStages, 1);
     init(sh.v_full, kVStages, 1);
-    init(sh.v_empty, kVStages, 1);
+    init(sh.v_empty, kVStages, 4);           // the converting warps
+    init(sh.w_full, 2, 4);
+    init(sh.w_empty, 2, 1);
     init(sh.s_full, kBufs, 1);
     init(sh.p_full, kBufs, 16);
     init(sh.pv_done, kBufs, 1);
@@ -699,11 +709,10 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
     init(sh.sc_empty, kScaleRing, 16);
     init(sh.drain, 2, 1);
     init(sh.items.full, kItemRing, 1);
-    init(sh.items.empty, kItemRing, 25);     // warps 0-24
+    init(sh.items.empty, kItemRing, 29);     // warps 0-24 and 28-31
     if (lane == 0) sh.abort = 0;
     tc::fence_mbar_init();
   }
-  if (tid < kBufs * kBN) (&sh.v_nan[0][0])[tid] = 0;
   tc::tc_fence_before();
   __syncthreads();
   pdl_wait();
@@ -712,7 +721,7 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
   const uint32_t tmem = sh.tmem;
   volatile int* abort_flag = &sh.abort;
 
-  if (warp < 4 || warp >= 24) {
+  if (warp < 4 || (warp >= 24 && warp < 28)) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtlRegs));
     if (warp == 0 || warp == 2) {
       const bool k = warp == 0;
@@ -736,10 +745,10 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
       // elected lane issues
       const bool is_qk = warp == 1;
       const uint32_t id_qk = idesc_e4m3(128, 128, false, false);
-      const uint32_t id_lo = idesc_e4m3(128, 128, false, true), id_hi = id_lo | kIdescAE5m2;
+      const uint32_t id_pv = idesc_e4m3(128, 128, false, true);   // kind::f16: type fields 0, fp16
       const uint64_t dQ = tc::smem_desc(tc::smem_u32(sQ), 16, 1024);
       const uint64_t dK = tc::smem_desc(tc::smem_u32(sK), 16, 1024);
-      const uint64_t dV = tc::smem_desc(tc::smem_u32(sV), kTile, 1024);
+      const uint64_t dW = tc::smem_desc(tc::smem_u32(sW), kHalves / 2, 1024);
       int kt = 0;
       bool ok = true;
       Item it;
@@ -774,20 +783,19 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
             }
             __syncwarp();
           } else {
-            const int st = kt % kVStages;
-            ok = __all_sync(0xffffffffu, ok && wait1(&sh.v_full[st], kt / kVStages, abort_flag) &&
+            const int wb = kt & 1;
+            ok = __all_sync(0xffffffffu, ok && wait1(&sh.w_full[wb], kt >> 1, abort_flag) &&
                                              wait1(&sh.p_full[b], use, abort_flag));
             if (!ok) break;
             tc::tc_fence_after();
-            const uint64_t vb = dV + uint64_t(st) * (kTile >> 4);
+            const uint64_t vb = dW + uint64_t(wb) * (kHalves >> 4);
             const uint32_t tP = tmem + b * 128, acc = j > it.j0 ? 1u : 0u;
             if (elect_one()) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {        // a quarter's 32 slots: 8 columns of P, 32 rows of V
-                mma_e4m3_ts(tmem + kTmemO, tP + 32 * k, vb + k * (4096 >> 4), id_hi, k > 0 ? 1u : acc);
-                mma_e4m3_ts(tmem + kTmemO, tP + 32 * k + 8, vb + k * (4096 >> 4), id_lo, 1u);
-              }
-              tc::mma_commit(&sh.v_empty[st]);
+              for (int k = 0; k < 8; ++k)          // 16 slots: 8 columns of P, 16 rows of V
+                tc::mma_bf16_ts(tmem + kTmemO, tP + 32 * (k >> 1) + 8 * (k & 1), vb + k * (2048 >> 4),
+                                id_pv, k > 0 ? 1u : acc);
+              tc::mma_commit(&sh.w_empty[wb]);
               tc::mma_commit(&sh.pv_done[b]);
               if (j == it.j1 - 1) tc::mma_commit(&sh.o_full);
             }
@@ -838,31 +846,13 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
         __syncwarp();
         tc::tc_fence_after();
         if (live) {
-          // where keys are masked a NaN code of V times a zero weight must stay zero: stale rows
-          // past the end are cleared, and a tree slot's NaN moves from V to the weights of the
-          // rows that see it.  The warps of these keys do so each for itself; the one that clears a
-          // NaN has left word of it before, for those that look later.
           const bool masked = j * kBN + kBN > P;
-          if (masked) {
-            const int st = kt % kVStages, at = part * 32 + lane;
-            ok &= wait1(&sh.v_full[st], kt / kVStages, abort_flag);
-            uint8_t* row = sV + st * kTile + at * 128;
-            if (j * kBN + at >= kv_len) {
-              clear_row(row);
-            } else if (j * kBN + at >= P) {
-              const bool found = has_nan(row);
-              if (found) *static_cast<volatile int*>(&sh.v_nan[b][at]) = kt + 1;
-              __threadfence_block();
-              if (found) clear_nan(row);
-            }
-            tc::fence_proxy_async_smem();
-          }
           const ScaleSlot& sc = sh.sc[slot];
           const uint32_t tS = tmem + lane_addr + b * 128 + part * 32;
-          // the weights of this thread's 32 keys against the reference kLift - add, as the two
-          // pieces of P; `top`: the largest exponent, `sum`: of the weights over the V scales
+          // the weights of this thread's 32 keys against the reference kLift - add, in fp16;
+          // `top`: the largest exponent, `sum`: of the weights over the V scales
           float top, sum;
-          uint32_t hi[8], lo[8];
+          uint32_t pk[16];
           auto seen = [&]() -> uint32_t {              // the keys that this row sees
             const int pre = P - key0, left = kv_len - key0;
             uint32_t vis = anc_window(arow, a.W, key0 - P);
@@ -904,7 +894,8 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
                 for (int u = 0; u < 4; ++u) p[u] = ex2(z[u]);
                 s0 += p[0] + p[1];
                 s1 += p[2] + p[3];
-                split_p4(p, hi[g * 4 + e / 4], lo[g * 4 + e / 4]);
+                pk[g * 8 + e / 2] = pack_f16x2(p[0], p[1]);
+                pk[g * 8 + e / 2 + 1] = pack_f16x2(p[2], p[3]);
               }
               sum = fmaf(s0 + s1, sc.iv[page], sum);
             }
@@ -937,19 +928,19 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
             weights(add);
           }
           if (masked) {
-            const int last = *static_cast<volatile int*>(&sh.v_nan[b][part * 32 + lane]);
-            const uint32_t v_nan = __ballot_sync(0xffffffffu, last == kt + 1);
+            ok &= wait1(&sh.w_full[kt & 1], kt >> 1, abort_flag);
+            const uint32_t v_nan = sh.v_nan[kt & 1][part];
+            __syncwarp();
             if (v_nan != 0) {
               const uint32_t hit = v_nan & seen();
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const uint32_t n = (hit >> (4 * e)) & 15u;
-                hi[e] |= ((n & 1u) | (n & 2u) << 7 | (n & 4u) << 14 | (n & 8u) << 21) * 127u;
+              for (int e = 0; e < 16; ++e) {
+                const uint32_t n = (hit >> (2 * e)) & 3u;
+                pk[e] |= ((n & 1u) | (n & 2u) << 15) * 0x7FFFu;
               }
             }
           }
-          tmem_st8(tS, hi);
-          tmem_st8(tS + 8, lo);
+          tc::tmem_st16(tS, pk);
           lsum += sum;
           tc::tmem_st_wait();
         }
@@ -967,7 +958,82 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
       if (lane == 0) tc::mbar_arrive(&sh.sum_full[par]);
     }
     if (!ok) *abort_flag = 1;
+  } else if (warp >= 28) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOutRegs));
+    // ===================================================================== V to fp16
+    // e4m3 values are fp16 values.  (The conversion by shifts and masks instead of cvt: 387 us against
+    // 303 on 32 trees of 46; two warps instead of four 519, two vectors at a time 316.)
+    // Eight lanes to a row, a 16-byte vector each, which becomes two (both tiles in 128-byte swizzle);
+    // lanes of the upper columns store their second vector first, so that the eight hit all
+    // banks.  Where keys are masked, a NaN code times a zero weight must stay zero: stale rows
+    // past the end become zeros, and a tree slot's NaN becomes a bit in v_nan, from which the
+    // softmax warps make it one in the weights of the rows that see it.
+    const int cw = warp - 28, c = lane & 7, rq = lane >> 3;
+    int kt = 0;
+    bool ok = true;
+    Item it;
+#pragma unroll 1
+    for (int li = 0; ok && __all_sync(0xffffffffu, next_item(sh.items, li, it, abort_flag)); ++li) {
+#pragma unroll 1
+      for (int j = it.j0; j < it.j1; ++j, ++kt) {
+        const int st = kt % kVStages, wb = kt & 1;
+        ok = __all_sync(0xffffffffu,
+                        wait1(&sh.v_full[st], kt / kVStages, abort_flag) &&
+                            (kt < 2 || wait1(&sh.w_empty[wb], (kt >> 1) - 1, abort_flag)));
+        if (!ok) break;
+        const uint8_t* const from = sV + st * kTile + (cw * 32 + rq) * 128;
+        uint8_t* const to = sW + wb * kHalves + (c >> 2) * (kHalves / 2) + (cw * 32 + rq) * 128;
+        const int live = it.P + it.T - j * kBN, tree = it.P - j * kBN;   // rows that exist; before the tree
+        uint32_t found = 0u;
+        uint4 v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          v[u] = *reinterpret_cast<const uint4*>(from + u * 512 + ((c ^ ((u & 1) * 4 + rq)) << 4));
+        if (tree < kBN) {
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const int r = cw * 32 + u * 4 + rq;
+            if (r < tree) continue;
+            uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w}, hit = 0u;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t n = nan_bytes(w[e]);
+              hit |= n;
+              w[e] = r >= live ? 0u : w[e] & ~((n >> 7) * 255u);
+            }
+            if (hit != 0u && r < live) found |= 1u << (u * 4 + rq);
+            v[u] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          found = __reduce_or_sync(0xffffffffu, found);
+          if (lane == 0) sh.v_nan[wb][cw] = found;
+        }
+        const bool second = c >= 4;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+          uint32_t h[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            h[2 * e] = kv8::e4m3x2_to_f16x2(w[e] & 0xFFFFu);
+            h[2 * e + 1] = kv8::e4m3x2_to_f16x2(w[e] >> 16);
+          }
+          uint8_t* const row = to + u * 512;
+          const int even = ((2 * (c & 3)) ^ ((u & 1) * 4 + rq)) << 4;
+          const uint4 h0 = make_uint4(h[0], h[1], h[2], h[3]), h1 = make_uint4(h[4], h[5], h[6], h[7]);
+          *reinterpret_cast<uint4*>(row + (second ? even ^ 16 : even)) = second ? h1 : h0;
+          *reinterpret_cast<uint4*>(row + (second ? even : even ^ 16)) = second ? h0 : h1;
+        }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tc::mbar_arrive(&sh.v_empty[st]);
+          tc::mbar_arrive(&sh.w_full[wb]);
+        }
+      }
+    }
+    if (!ok) *abort_flag = 1;
   } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOutRegs));
     // ===================================================================== queries, output
     const int q = warp & 3;
     const uint32_t lane_addr = uint32_t(q * 32) << 16;

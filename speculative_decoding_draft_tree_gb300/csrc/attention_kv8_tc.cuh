@@ -13,14 +13,15 @@
 // K and V come from HBM once a row tile: 64 ragged trees, 432 rows a head, 1376 us with, 1437
 // without.)
 //
-// 8-bit codes go to tcgen05.mma kind::f8f6f4 as they are.  The other operand of each product keeps
-// its precision as a sum of 8-bit pieces, all multiplied into fp32 accumulators.  A bf16 query is
-// e4m3(x) + e4m3(x - e4m3(x)), exact (4 + 4 significant bits) but for elements 2^-18 of the row's
-// largest.  A softmax weight of a short unit is the sum of three e5m2 pieces (split_p2), 10 bits over 22
-// binades and 2^-17 of the range below; of a long one of two (split_p4).  fp8 products run at
-// twice the bf16 rate, so two pieces cost what one bf16 product does, and K and V are read by
-// the tensor core where TMA put them, one byte an element: converting them to bf16 first would
-// move 6 bytes of shared memory an element against 2, more than the SM has at HBM speed.
+// K's codes go to tcgen05.mma kind::f8f6f4 as they are.  A bf16 query keeps its precision as the sum of
+// two 8-bit pieces, both multiplied into the same fp32 accumulator: e4m3(x) + e4m3(x - e4m3(x)), exact
+// (4 + 4 significant bits) but for elements 2^-18 of the row's largest.  fp8 products run at twice the
+// bf16 rate, so the two pieces cost what one bf16 product does.
+// V's codes go there as they are too in the kernel of short units, against weights that are the sum of
+// three e5m2 pieces (split_p2), 10 bits over 22 binades and 2^-17 of the range below: V is read where
+// TMA put it, one byte an element; converting it first would move 6 bytes of shared memory an element
+// against 2, more than the SM has at HBM speed.  The kernel of long units, whose tiles take several
+// times as long as HBM needs for them, converts V to fp16 for weights in fp16.
 #pragma once
 
 #include <cudaTypedefs.h>
@@ -499,18 +500,11 @@ __device__ __forceinline__ Split2 split_p2(float a, float b) {
       : "=&r"(s.hi), "=&r"(s.mid), "=&r"(s.lo) : "f"(a), "f"(b));
   return s;
 }
-// four weights (below 2^13) as two pieces of four codes: hi in e5m2, the upper byte of the fp16
-// value rounded to nearest, lo = e4m3 of the exact remainder (at most an eighth)
-__device__ __forceinline__ void split_p4(const float (&p)[4], uint32_t& hi, uint32_t& lo) {
-  asm("{\n\t.reg .b32 w0, w1, h0, h1, r0, r1;\n\t.reg .b16 l0, l1;\n\t"
-      "cvt.rn.f16x2.f32 w0, %3, %2;\n\tcvt.rn.f16x2.f32 w1, %5, %4;\n\t"
-      "add.u32 h0, w0, 0x00800080;\n\tadd.u32 h1, w1, 0x00800080;\n\t"
-      "and.b32 h0, h0, 0xFF00FF00;\n\tand.b32 h1, h1, 0xFF00FF00;\n\t"
-      "sub.rn.f16x2 r0, w0, h0;\n\tsub.rn.f16x2 r1, w1, h1;\n\t"
-      "prmt.b32 %0, h0, h1, 0x7531;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f16x2 l0, r0;\n\tcvt.rn.satfinite.e4m3x2.f16x2 l1, r1;\n\t"
-      "mov.b32 %1, {l0, l1};\n\t}"
-      : "=r"(hi), "=r"(lo) : "f"(p[0]), "f"(p[1]), "f"(p[2]), "f"(p[3]));
+// two weights in fp16
+__device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(a), "f"(b));
+  return r;
 }
 
 // bit 7 of each byte of w that holds e4m3's NaN (0x7F, 0xFF)
@@ -552,16 +546,6 @@ __device__ __forceinline__ void mma_e4m3_ss(uint32_t d_tmem, uint64_t a_desc, ui
       ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// the same with A in tensor memory, four codes to a 32-bit column
-__device__ __forceinline__ void mma_e4m3_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                            uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}"
-      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
 // Instruction descriptor of kind::f8f6f4: fp32 accumulator (bits 4-5 = 1), A and B e4m3 (both
 // type fields 0), major-ness in bits 15 / 16 (1 = MN-major), N >> 3 in bits 17-22, M >> 4 in 24-28.
 __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool b_mn) {
@@ -569,7 +553,7 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn, bool 
          (uint32_t(M >> 4) << 24);
 }
 
-constexpr uint32_t kIdescAE5m2 = 1u << 7, kIdescBE5m2 = 1u << 10;   // the type fields: e5m2
+constexpr uint32_t kIdescBE5m2 = 1u << 10;   // B's type field: e5m2
 
 // Reductions of NR values a lane over the 32 lanes: each of the first exchanges halves what a lane
 // holds, about NR shuffles instead of 5 NR.  Lane l ends with the result of row red_row<NR>(l).

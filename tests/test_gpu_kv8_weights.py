@@ -1,10 +1,11 @@
 """GPU tests of the softmax weights that tree attention over the 8-bit cache forms: long flat rests
 beside one key that has most of the weight, V scales that lie far apart, blocks of zeros.
 
-Bars, by arithmetic, elementwise.  A weight is rounded to fp16 (2^-11 of itself) and split in three
-e5m2 pieces that leave 2^-10 of it, or 2^-17 of a range in which the row's largest weight (times its
-V scale) is at least 2^13: 2^-30 of that, and twice that at most where a unit is joined of two
-references.  Scores: bf16 queries as two
+Bars, by arithmetic, elementwise.  A weight is rounded to fp16 (2^-11 of itself) and, in units of at
+most 16 query rows, split in three e5m2 pieces that leave 2^-10 of it, or 2^-17 of a range in which the
+row's largest weight (times its V scale) is at least 2^13: 2^-30 of that, and twice that at most where
+a unit is joined of two references.  Longer units: fp16 alone, whose smallest half step is 2^-25 of a
+range in which the largest is at least 2^5, 2^-30 as well.  Scores: bf16 queries as two
 e4m3 pieces, off by 2^-17.8 max|q| an element, sums in fp32 (2^-17 of their magnitudes), exponents up to
 2^7 in fp32 and exp2 (2^-16 together).  Output: one rounding to bf16 (2^-8).
 fp32 queries: fp32 products and sums, 2^-17 of the mean absolute value beside the scores' error.
@@ -44,7 +45,7 @@ def check(c):
     d, H, Hq = c.d, c.ks.shape[1], c.q.shape[1]
     G = Hq // H
     f32 = c.q.dtype == torch.float32
-    left = 2 * 2.0 ** -30
+    pieces, left = 2.0 ** -10 if c.T_max * G <= 16 else 0.0, 2 * 2.0 ** -30
     kc, vc = (torch.nan_to_num(t.double()).cpu() for t in (c.k, c.v))
     ks, vs, cq, co, cl = (t.double().cpu() for t in (c.ks, c.vs, c.q, c.o, c.lse))
     outs = []
@@ -73,7 +74,7 @@ def check(c):
             if f32:
                 tol = (2 * E[:, None] + 2.0 ** -17) * mass
             else:
-                tol = (2 * E[:, None] + 2.0 ** -10 + 2.0 ** -11) * mass + left * rest + 2.0 ** -8 * o.abs()
+                tol = (2 * E[:, None] + pieces + 2.0 ** -11) * mass + left * rest + 2.0 ** -8 * o.abs()
             go = co[n0:n0 + T, h * G:(h + 1) * G].reshape(T * G, d)
             gl = cl[n0:n0 + T, h * G:(h + 1) * G].reshape(T * G)
             worst = ((go - o).abs() / (tol + 1e-30)).max().item()
@@ -85,7 +86,8 @@ def check(c):
     return o
 
 
-FORMS = [(4, 1, 1, torch.bfloat16), (2, 2, 7, torch.bfloat16), (4, 1, 4, torch.bfloat16), (2, 1, 2, torch.float32)]
+FORMS = [(4, 1, 1, torch.bfloat16), (2, 2, 7, torch.bfloat16), (4, 1, 4, torch.bfloat16),
+         (4, 1, 20, torch.bfloat16), (2, 1, 80, torch.bfloat16), (2, 1, 2, torch.float32)]
 
 
 def sink_case(Hq, H, T, dtype, P, at, part, spread, seed):
