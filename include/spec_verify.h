@@ -439,9 +439,9 @@ spec_status_t spec_echo_select_pack(const spec_draft_pool* pool, int32_t K_max,
  * A cache of e4m3 codes [num_blocks][H_kv][block_size][head_dim] (one byte each, 16-byte aligned)
  * with one fp32 scale for each (block, KV head) in [num_blocks][H_kv], K and V apart:
  *   value = code * scale.
- * Scales are finite and >= 0.  spec_kv8_append writes powers of two in [2^-100, 2^119]; another
- * writer may use any scale there or 0 (the attention reads a V scale below 2^-100 as 2^-100, and
- * the V scales of one request's live pages in one head may lie at most 2^100 apart).
+ * Scales are finite and >= 0.  spec_kv8_append writes powers of two in [2^-100, 2^119], 2^-100 for
+ * rows of zeros; another writer may use any scale there or 0 (the attention reads a V scale below
+ * 2^-100 as 2^-100).
  * A block that receives rows belongs to one request (pages shared by a fork are only read).
  * head_dim is a multiple of 16, at most 256.  Round by round: spec_tree_build, rotary embedding,
  * spec_kv8_append of the tree's rows at slots prefix_len .., spec_tree_attention_kv8,
@@ -504,7 +504,10 @@ spec_status_t spec_kv8_append(const spec_kv8_append_params* p, spec_stream_t str
  * or K; O alone for one in V, its column at least.
  * On the tensor cores a bf16 q enters the e4m3 products as two pieces, exact to 2^-18 of its row's
  * largest element.  A weight (times its slot's V scale) is kept to 2^-9 of itself or 2^-30 of the
- * row's largest, whichever is more (2^-11 of itself in units of more than 16 query rows).
+ * row's largest, whichever is more (2^-11 of itself in units of more than 16 query rows).  In these
+ * longer units a key whose page's V scale is 2^-s of the largest of its request and head is left out
+ * of the softmax's sum where its weight is below 2^(s - 126) of the row's largest: of pages of zeros
+ * beside V scales up to 2^2, below 2^-24.
  * Every H_q / H_kv ratio, block_size and head_dim (multiple of 16, <= 256) is accepted; BF16
  * with head_dim 128, block_size 16, 32, 64 or 128 and H_q / H_kv <= 128 runs on the tcgen05
  * tensor cores, everything else on a CUDA-core kernel.

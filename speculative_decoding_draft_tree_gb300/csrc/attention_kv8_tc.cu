@@ -36,10 +36,13 @@
 // output; 64 ragged trees over 1024 .. 32768 slots (64 query heads on 8) 1447 us, 848 TFLOP/s.
 // The bf16 cache takes 289 and 1554 us on these shapes.
 //
-// Scales: a score is code product * (K scale of the slot's page * the row's query scale); the V
-// scale joins the exponent, y = score + log2(V scale), and the weight 2^(y - ref) goes into the
-// product with V's codes while the row sum takes 2^(y - ref) / (V scale).  So the weights that
-// enter the product fill their format's range whatever the pages' scales are.
+// Scales: a score x is code product * (K scale of the slot's page * the row's query scale).  The
+// reference is the largest y = x + log2(V scale), and the weight that goes into the product with V's
+// codes is 2^(y - ref), which fills its format's range whatever the pages' scales are.  The row sum
+// takes 2^(x - ref): in the rows kernel that is what the exponential forms, and the V scale is multiplied
+// in; in the tile kernel, where that multiplication costs 4% (308 against 296 us, 1530 against 1450),
+// the exponential forms 2^(y - ref) and the sum divides by the scale again, which loses keys whose
+// 2^(y - ref) is below 2^-126.
 //
 // The waits are bounded; one that runs out raises the CTA's abort flag, after which no wait
 // blocks: the softmax groups, which meet at hardware barriers, still walk through their tiles, the
@@ -331,7 +334,7 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
         const int b = (kg >> 1) & 1, use = kg >> 2;
         const int slot = kg % kScaleRing;
         ok &= wait1(&sh.sc_full[slot], kg / kScaleRing, abort_flag);
-        const float ks = sh.sc[slot].k[si], lv = sh.sc[slot].lv[si], iv = sh.sc[slot].iv[si];
+        const float ks = sh.sc[slot].k[si], lv = sh.sc[slot].lv[si], vs = sh.sc[slot].v[si];
         ok &= wait1(&sh.s_full[grp][b], use, abort_flag);
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&sh.sc_empty[slot]);
@@ -360,7 +363,7 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
               if ((w[t] >> sh_) & 1u) vis |= ((1u << a.G) - 1u) << (t * a.G);
           }
         }
-        float y[NR], zmax = -INFINITY;
+        float x[NR], zmax = -INFINITY;
 #pragma unroll
         for (int n4 = 0; n4 < NR / 4; ++n4) {
           const float4 qm = qmul[n4];
@@ -368,18 +371,21 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int n = n4 * 4 + e;
-            y[n] = fmaf(__uint_as_float(sv[n]) + __uint_as_float(sv[n + NR]), m4[e], lv);
+            x[n] = (__uint_as_float(sv[n]) + __uint_as_float(sv[n + NR])) * m4[e];
           }
         }
         if (masked) {
 #pragma unroll
-          for (int n = 0; n < NR; ++n) y[n] = ((vis >> n) & 1u) ? y[n] : -INFINITY;
+          for (int n = 0; n < NR; ++n) x[n] = ((vis >> n) & 1u) ? x[n] : -INFINITY;
         }
         // against the references (none yet: +infinity, or NaN under a masked key)
 #pragma unroll
-        for (int n = 0; n < NR; ++n) zmax = fmaxf(zmax, y[n] + add[n]);
-        if (bar_any(bar_g, 128, zmax > kCeil)) {
+        for (int n = 0; n < NR; ++n) zmax = fmaxf(zmax, x[n] + add[n]);
+        if (bar_any(bar_g, 128, zmax + lv > kCeil)) {
           // some row's reference moves up to its maximum so far
+          float y[NR];
+#pragma unroll
+          for (int n = 0; n < NR; ++n) y[n] = x[n] + lv;
           const float top = red_rows<NR, true>(y, lane);
           sh.mx[grp][q][red_row<NR>(lane)] = top;
           bar_sync(bar_g, 128);
@@ -390,9 +396,11 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
                                           fmaxf(sh.mx[grp][2][n], sh.mx[grp][3][n])),
                                     kShift - add[n]);
             const float now = kShift - ref;
-            factor[n] = add[n] == INFINITY ? 1.f : ex2(now - add[n]);
+            // (in two halves: pages of zeros before any other leave a sum that is far above the rest)
+            const float half = add[n] == INFINITY ? 1.f : ex2(0.5f * (now - add[n]));
+            factor[n] = half * half;
             add[n] = now;
-            lsum[n] *= factor[n];
+            lsum[n] = lsum[n] * half * half;
           }
           if (!fresh) {                              // the group's accumulator holds something
             const int kp = kg - 2;                   // the group's tile before
@@ -418,11 +426,11 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
 #pragma unroll
         for (int n = 0; n < NR; n += 2) {
           // (a row that has seen nothing: -infinity + infinity)
-          const float p0 = y[n] == -INFINITY ? 0.f : ex2(y[n] + add[n]);
-          const float p1 = y[n + 1] == -INFINITY ? 0.f : ex2(y[n + 1] + add[n + 1]);
-          lsum[n] = fmaf(p0, iv, lsum[n]);
-          lsum[n + 1] = fmaf(p1, iv, lsum[n + 1]);
-          const Split2 s = split_p2(p0, p1);
+          const float e0 = x[n] == -INFINITY ? 0.f : ex2(x[n] + add[n]);
+          const float e1 = x[n + 1] == -INFINITY ? 0.f : ex2(x[n + 1] + add[n + 1]);
+          lsum[n] = fmaf(e0, kSumMul, lsum[n]);
+          lsum[n + 1] = fmaf(e1, kSumMul, lsum[n + 1]);
+          const Split2 s = split_p2(e0 * vs, e1 * vs);
           const int o0 = (n >> 3) * 1024 + (n & 7) * 128 + ((chunk ^ (n & 7)) << 4);
           const int o1 = (n >> 3) * 1024 + ((n & 7) + 1) * 128 + ((chunk ^ ((n & 7) + 1)) << 4);
           pc[o0] = uint8_t(s.hi >> 8);
@@ -539,19 +547,19 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
                                    : cur.slot * d.part_rows + rn;
       const float a0 = sh.add[par][0][rn], a1 = sh.add[par][1][rn];
       const float top = fminf(a0, a1);               // of the larger reference
-      float w0 = a0 == INFINITY ? 0.f : ex2(top - a0);
-      float w1 = a1 == INFINITY ? 0.f : ex2(top - a1);
+      float w0 = a0 == INFINITY ? 0.f : ex2(0.5f * (top - a0));   // (their roots first, as above)
+      float w1 = a1 == INFINITY ? 0.f : ex2(0.5f * (top - a1));
       float l0 = 0.f, l1 = 0.f;
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         l0 += sh.sum[par][0][w][rn];
         l1 += sh.sum[par][1][w][rn];
       }
-      const float l = l0 * w0 + l1 * w1;
+      const float l = l0 * w0 * w0 + l1 * w1 * w1;
       const float inv = l == 0.f ? 0.f : kSumMul / l;    // (NaN stays NaN)
       const float lse2 = l == 0.f ? -INFINITY : log2f(l) + kSumShift - top;
-      w0 *= inv;
-      w1 *= inv;
+      w0 *= w0 * inv;
+      w1 *= w1 * inv;
       ok &= wait1(&sh.o_full[par], li >> 1, abort_flag);
       __syncwarp();
       tc::tc_fence_after();

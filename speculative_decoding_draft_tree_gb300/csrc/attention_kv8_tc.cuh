@@ -43,7 +43,7 @@ constexpr int kMaxCtas = 1024;
 // references than on weights.
 constexpr float kShift = 13.f;
 constexpr float kCeil = 15.f;
-// Row sums are kept times 2^-kSumShift: of weights up to 2^15.5 over V scales down to 2^-100, a million
+// Row sums are kept times 2^-kSumShift: of weights up to 2^15 over V scales down to 2^-100, a million
 // keys' sum stays finite.
 constexpr float kSumShift = 10.f;
 constexpr float kSumMul = 1.f / 1024.f;
@@ -398,11 +398,11 @@ __device__ __forceinline__ void page_producer(const TcDev& d, ItemRing& items,
   __syncwarp();
 }
 
-// The scales of each tile's pages into a ring: k[i] = K scale, lv[i] = log2 of the V scale, iv[i]
-// its reciprocal (times kSumMul), i < 128 / bs.  One warp, four tiles at a time (lanes 8 u .. 8 u + 7: tile u), far
+// The scales of each tile's pages into a ring: k[i] = K scale, v[i] = V scale, lv[i] its log2, iv[i] its
+// reciprocal (times kSumMul), i < 128 / bs.  One warp, four tiles at a time (lanes 8 u .. 8 u + 7: tile u), far
 // enough ahead of the softmax to hide its dependent loads.
 struct ScaleSlot {
-  float k[8], lv[8], iv[8];
+  float k[8], v[8], lv[8], iv[8];
 };
 constexpr int kScaleRing = 16;
 __device__ __forceinline__ void scale_producer(const TcDev& d, ItemRing& items, ScaleSlot* ring,
@@ -448,11 +448,12 @@ __device__ __forceinline__ void scale_producer(const TcDev& d, ItemRing& items, 
       if (!ok) break;
       if (sub < n) {
         ScaleSlot* o = ring + (kt + sub) % kScaleRing;
-        // a V scale of 0 (a block of zeros) must not make 0 * infinity
+        // a V scale of 0 (a block of zeros) has no logarithm
         vs = fmaxf(vs, kMinVScale);
         o->k[i] = ks;
-        o->lv[i] = log2f(vs);
+        o->v[i] = vs;
         o->iv[i] = kSumMul / vs;
+        o->lv[i] = log2f(vs);
       }
       __syncwarp();
       if (lane < n) tc::mbar_arrive(full + (kt + lane) % kScaleRing);

@@ -162,3 +162,22 @@ def test_a_long_cache_of_zero_v_rows(Hq, H, T, dtype):
     c.run()
     assert (c.o[:c.N] == 0).all()
     check(c)
+
+
+@pytest.mark.parametrize("Hq,H,T,dtype,big", [f + (b,) for f in FORMS[:3] + FORMS[-1:] for b in (1e3, 1e12)]
+                         + [(16, 8, 1, torch.bfloat16, 1e12), (16, 8, 7, torch.bfloat16, 1e12), (16, 8, 20, torch.bfloat16, 1e3)])
+@pytest.mark.parametrize("at", [5, 3000])
+def test_pages_of_zeros_beside_one_heavy_key_with_large_v(Hq, H, T, dtype, big, at):
+    """The rest is zeros in V (scales of 2^-100) and a third of the weight, the heavy key's V up to `big`;
+    with eight KV heads a CTA walks several tiles before that key and after it."""
+    P = 20000 if H < 8 else 6000
+    c = sink_case(Hq, H, T, dtype, P, at, 0.67, 0.3, seed=T)
+    rng = np.random.default_rng(T)
+    ids, S = c.table_np[0][:-(-(P + T) // c.bs)], P + T
+    kf = np.nan_to_num(U.values(c.k)[ids]) * c.ks.double().cpu().numpy()[ids][:, :, None, None]
+    vf = np.zeros((S, H, c.d))
+    vf[at] = big * rng.uniform(0.2, 1.0, (H, c.d))
+    fill(c, 0, kf.transpose(0, 2, 1, 3).reshape(-1, H, c.d)[:S], vf)
+    c.run()
+    o = check(c)
+    assert o.abs().mean() < 0.8 * np.abs(vf[at]).mean()
