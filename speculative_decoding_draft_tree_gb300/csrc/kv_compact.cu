@@ -42,9 +42,9 @@ __global__ void __launch_bounds__(kCompactThreads) kv_compact_kernel(CompactDev 
     for (int d = tid; d <= na; d += blockDim.x) {
       const int pd = prow[d];
       bool good = (d == 0) ? (pd == 0) : (pd >= d);
-      const int src = P + pd, dst = P + d;
-      const int lsb = src / a.bs, ldb = dst / a.bs;
-      good = good && lsb < a.max_blocks && ldb < a.max_blocks;
+      const long long src = (long long)P + pd, dst = (long long)P + d;
+      const long long lsb = src / a.bs, ldb = dst / a.bs;
+      good = good && src <= INT32_MAX && lsb < a.max_blocks && ldb < a.max_blocks;
       int flag = good ? 0 : SPEC_REQ_BAD_PARENT;
       if (good) {
         const int sb = trow[lsb], db = trow[ldb];

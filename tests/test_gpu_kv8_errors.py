@@ -83,6 +83,28 @@ def test_kv_compact_refuses_a_late_bad_step_in_every_cta(late):
             assert torch.equal(t[:, pages], b[:, pages])
 
 
+def test_kv_compact_refuses_steps_past_32_bits():
+    """P + path[d] beyond 2^31 - 1 is a bad step, in both caches."""
+    L, H, d, bs, T = 2, 2, 32, 16, 4
+    table = np.arange(16, dtype=np.int32).reshape(4, 4)
+    path = np.array([[0, 2, 3, -1], [0, 2 ** 31 - 1, 3, -1], [0, 2 ** 31 - 20, 2 ** 31 - 20, -1], [0, 2, 3, -1]], dtype=np.int32)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    k, v = (torch.randn((L, 16, H, bs, d), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    rng = np.random.default_rng(4)
+    (k8, ks), (v8, vs) = [U.random_cache(L, 16, H, bs, d, rng) for _ in range(2)]
+    held = (torch.from_numpy(table).cuda(), U.ints([20, 20, 30, 1]), torch.from_numpy(path).cuda(), U.ints([2] * 4))
+    for make, run, cache in ((lambda *a: B.compact_params(k, v, *a), B.spec_kv_compact, (k, v)),
+                             (lambda *a: B.kv8_compact_params(k8, v8, ks, vs, *a), B.spec_kv8_compact, (k8.view(torch.uint8), v8.view(torch.uint8)))):
+        before = [t.clone() for t in cache]
+        st, lens, used = (torch.zeros(4, dtype=torch.int32, device="cuda") for _ in range(3))
+        moves = torch.zeros((4, T, 2), dtype=torch.int32, device="cuda")
+        run(make(*held, st, lens, moves, used, T))
+        torch.cuda.synchronize()
+        assert st.cpu().tolist() == [0, 1, 1, 0] and lens.cpu().tolist() == [23, 20, 30, 4]
+        for t, b in zip(cache, before):
+            assert torch.equal(t[:, 4:12], b[:, 4:12]) and not torch.equal(t, b)
+
+
 # ------------------------------------------------------------------------------------ append
 @pytest.mark.parametrize("off,start,want", [
     ([0, 18, 30], [0, 0], [0, 2]),                        # begins at N and ends past it
