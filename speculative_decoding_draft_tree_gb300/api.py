@@ -116,7 +116,9 @@ class VerifyStep:
         v_new ([N, H_kv, d], keys already rotated) into layer 0's tree slots, attends over layer 0
         and commits the accepted path in every layer.  k_new and v_new are inputs of a round like q:
         upload() brings them and twin() gives the second step its own; the cache is shared.  Call
-        this before twin() or RoundPipeline."""
+        this before twin() or RoundPipeline.  The workload's own k_cache and v_cache are not read:
+        a single page of their shape ([1, 1, H_kv, block_size, d]) will do.  The keys' rotation is
+        the caller's: the library's rotary step writes a 16- or 32-bit cache."""
         w = self.w
         if self.rope_p is not None:
             raise ValueError("enable_kv8 does not combine with enable_rope, which writes the 16- "

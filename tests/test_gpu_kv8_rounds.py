@@ -1,8 +1,10 @@
 """GPU tests of several verification rounds over the 8-bit cache, one after the other."""
+import dataclasses
+
 import pytest
 import torch
 
-from speculative_decoding_draft_tree_gb300.api import RoundPipeline, _packed
+from speculative_decoding_draft_tree_gb300.api import RoundPipeline, VerifyStep, _packed
 from test_gpu_kv8 import _round_case
 
 pytestmark = pytest.mark.gpu
@@ -71,3 +73,25 @@ def test_run_from_host_brings_the_new_rows():
     torch.cuda.synchronize()
     for t, x in zip((k, v, ks, vs, step.o), want):
         assert torch.equal(_bytes(t), _bytes(x))
+
+
+def test_a_round_over_the_8_bit_cache_needs_no_16_bit_one():
+    """The workload's own cache may be a page of its shape: with enable_kv8 nothing reads it."""
+    w, step, (k, v, ks, vs, k_new, v_new) = _round_case(4, 2)
+    before = [t.clone() for t in (k, v, ks, vs)]
+    step.run()
+    torch.cuda.synchronize()
+    names = ("o", "lse", "out_tokens", "out_len", "path", "n_acc", "new_kv_len", "slot_map", "req_status")
+    want = [getattr(step, n).clone() for n in names] + [t.clone() for t in (k, v, ks, vs)]
+    for t, b in zip((k, v, ks, vs), before):
+        t.copy_(b)
+    page = torch.full_like(w.k_cache[:1, :1], float("nan"))
+    small = VerifyStep(dataclasses.replace(w, k_cache=page, v_cache=page.clone()))
+    small.enable_kv8(k, v, ks, vs, k_new, v_new)
+    for s in (small, small.twin()):
+        for t, b in zip((k, v, ks, vs), before):
+            t.copy_(b)
+        s.run()
+        torch.cuda.synchronize()
+        for t, x in zip([getattr(s, n) for n in names] + [k, v, ks, vs], want):
+            assert torch.equal(_bytes(t), _bytes(x))
