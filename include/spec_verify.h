@@ -587,7 +587,9 @@ spec_status_t spec_kv8_compact(const spec_kv8_compact_params* p, spec_stream_t s
  * [0, B), dst of another fork too, dst a src of this call, or new_block[f] named by another fork
  * that copies a partial page),
  * SPEC_REQ_BAD_SIZE (L < 0 or pages beyond the table row), SPEC_REQ_BAD_BLOCK (new_block[f] or a
- * page of the parent outside [0, num_blocks), or new_block[f] one of the parent's pages).
+ * page of the parent outside [0, num_blocks), or new_block[f] one of the parent's pages).  That no
+ * other request uses new_block[f] is the caller's to see to: a page of another row of the table is
+ * overwritten.
  * Layouts: layer_stride elements between layers of the caches, scale_layer_stride floats.
  * Errors: SPEC_ERR_INVALID_ARG, SPEC_ERR_UNSUPPORTED (more than 65535 layers), SPEC_ERR_CUDA.
  * ------------------------------------------------------------------------------------------ */
