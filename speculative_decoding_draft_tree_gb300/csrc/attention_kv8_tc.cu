@@ -32,15 +32,15 @@
 // keep the scores of the next
 // tiles coming while one is in the softmax and one in the output's product; O has columns 384-511.
 // Warps: 0-3 as above, 4-19 softmax, 20-23 queries and output, 24 scales, 25 items, 28-31 V.
-// Measured: 32 trees of 46 over 8192 slots (32 query heads on 8) 294 us, 672 TFLOP/s of scores and
-// output; 64 ragged trees over 1024 .. 32768 slots (64 query heads on 8) 1447 us, 848 TFLOP/s.
+// Measured: 32 trees of 46 over 8192 slots (32 query heads on 8) 301 us, 656 TFLOP/s of scores and
+// output; 64 ragged trees over 1024 .. 32768 slots (64 query heads on 8) 1465 us, 838 TFLOP/s.
 // The bf16 cache takes 289 and 1554 us on these shapes.
 //
 // Scales: a score x is code product * (K scale of the slot's page * the row's query scale).  The
 // reference is the largest y = x + log2(V scale), and the weight that goes into the product with V's
 // codes is 2^(y - ref), which fills its format's range whatever the pages' scales are.  The row sum
 // takes 2^(x - ref): in the rows kernel that is what the exponential forms, and the V scale is multiplied
-// in; in the tile kernel, where that multiplication costs 4% (308 against 296 us, 1530 against 1450),
+// in; in the tile kernel, where that multiplication costs 4% (308 us against 296, 1530 against 1450),
 // the exponential forms 2^(y - ref) and the sum divides by the scale again, which loses keys whose
 // 2^(y - ref) is below 2^-126.
 //
@@ -620,9 +620,11 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
 namespace tile {
 constexpr int kRows = 128;
 constexpr int kThreads = 1024;
-constexpr int kCtlRegs = 40;       // warps 0-3 and 24-27
-constexpr int kSoftmaxRegs = 80;   // warps 4-19
-constexpr int kOutRegs = 56;       // warps 20-23 and 28-31
+// (40 / 80 / 56 registers: 32 trees of 46 over 8192 slots 296 us, over 2048 slots 122, ragged trees over
+// 1024 .. 2048 slots 164; this split: 302, 119, 157; no split 328, 125, 161)
+constexpr int kCtlRegs = 48;       // warps 0-3 and 24-27
+constexpr int kSoftmaxRegs = 72;   // warps 4-19
+constexpr int kOutRegs = 64;       // warps 20-23 and 28-31, as launched
 static_assert(256 * kCtlRegs + 512 * kSoftmaxRegs + 256 * kOutRegs <= kThreads * 64, "register split");
 // Weights are 2^(y - ref + kLift), in fp16; the reference moves when one passes 2^kTop.  11 bits are
 // kept down to 2^-19 of a row's largest weight, and 2^-30 of it below.  (32 trees of 46, 64 ragged ones: lift
@@ -967,10 +969,10 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
     }
     if (!ok) *abort_flag = 1;
   } else if (warp >= 28) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOutRegs));
     // ===================================================================== V to fp16
     // e4m3 values are fp16 values.  (The conversion by shifts and masks instead of cvt: 387 us against
-    // 303 on 32 trees of 46; two warps instead of four 519, two vectors at a time 316.)
+    // 303 on 32 trees of 46; two warps instead of four 519, two vectors at a time 316; in halves of a
+    // tile that the product waits for one by one 307.)
     // Eight lanes to a row, a 16-byte vector each, which becomes two (both tiles in 128-byte swizzle);
     // lanes of the upper columns store their second vector first, so that the eight hit all
     // banks.  Where keys are masked, a NaN code times a zero weight must stay zero: stale rows
@@ -997,6 +999,8 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
 #pragma unroll
         for (int u = 0; u < 8; ++u)
           v[u] = *reinterpret_cast<const uint4*>(from + u * 512 + ((c ^ ((u & 1) * 4 + rq)) << 4));
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sh.v_empty[st]);   // (the tile is in registers)
         if (tree < kBN) {
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
@@ -1033,15 +1037,11 @@ attn_kv8_tile_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
         }
         tc::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          tc::mbar_arrive(&sh.v_empty[st]);
-          tc::mbar_arrive(&sh.w_full[wb]);
-        }
+        if (lane == 0) tc::mbar_arrive(&sh.w_full[wb]);
       }
     }
     if (!ok) *abort_flag = 1;
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOutRegs));
     // ===================================================================== queries, output
     const int q = warp & 3;
     const uint32_t lane_addr = uint32_t(q * 32) << 16;
