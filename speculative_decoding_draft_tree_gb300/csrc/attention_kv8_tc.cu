@@ -305,8 +305,12 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
     const int kl = q * 32 + lane;                    // this lane's slot of a tile
     const int si = kl >> d.log2bs;
     const int bar_g = 1 + grp;
-    uint8_t* const pcol = sP + grp * 2 * L::kTriple + (kl & 15);
-    const int chunk = kl >> 4;
+    // With 16 rows P^T is stored two keys at a time: of each pair of rows a lane takes one, the even lane
+    // the even row, for its key and its neighbour's (units of 16 rows over 8192 slots 67 us, 71 with
+    // bytes; with 8 rows the exchange costs more than the stores, 54.9 against 54.0 us on the chains)
+    const int odd = NR == 16 ? lane & 1 : 0, chunk = kl >> 4;
+    uint8_t* const pcol = sP + grp * 2 * L::kTriple + odd * 128 + (kl & (NR == 16 ? 14 : 15));
+    const uint32_t own_other = odd ? 0x3715u : 0x6240u;
     int kt = 0;
     bool ok = true;                                  // no early exit: see the file's comment
     Item it;
@@ -424,21 +428,43 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
         if (use > 0) ok &= wait1(&sh.pv_done[grp][b], use - 1, abort_flag);
         uint8_t* pc = pcol + b * L::kTriple;
 #pragma unroll
-        for (int n = 0; n < NR; n += 2) {
-          // (a row that has seen nothing: -infinity + infinity)
-          const float e0 = x[n] == -INFINITY ? 0.f : ex2(x[n] + add[n]);
-          const float e1 = x[n + 1] == -INFINITY ? 0.f : ex2(x[n + 1] + add[n + 1]);
-          lsum[n] = fmaf(e0, kSumMul, lsum[n]);
-          lsum[n + 1] = fmaf(e1, kSumMul, lsum[n + 1]);
-          const Split2 s = split_p2(e0 * vs, e1 * vs);
-          const int o0 = (n >> 3) * 1024 + (n & 7) * 128 + ((chunk ^ (n & 7)) << 4);
-          const int o1 = (n >> 3) * 1024 + ((n & 7) + 1) * 128 + ((chunk ^ ((n & 7) + 1)) << 4);
-          pc[o0] = uint8_t(s.hi >> 8);
-          pc[o1] = uint8_t(s.hi >> 24);
-          pc[L::kPiece + o0] = uint8_t(s.mid >> 8);
-          pc[L::kPiece + o1] = uint8_t(s.mid >> 24);
-          pc[2 * L::kPiece + o0] = uint8_t(s.lo >> 8);
-          pc[2 * L::kPiece + o1] = uint8_t(s.lo >> 24);
+        for (int n = 0; n < NR; n += 4) {
+          float p[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            // (a row that has seen nothing: -infinity + infinity)
+            const float e = x[n + u] == -INFINITY ? 0.f : ex2(x[n + u] + add[n + u]);
+            lsum[n + u] = fmaf(e, kSumMul, lsum[n + u]);
+            p[u] = e * vs;
+          }
+          const Split2 s0 = split_p2(p[0], p[1]), s1 = split_p2(p[2], p[3]);
+          auto at = [&](int n) { return (n >> 3) * 1024 + (n & 7) * 128 + ((chunk ^ odd ^ (n & 7)) << 4); };
+          if constexpr (NR == 16) {
+            auto pairs = [&](uint32_t w) {           // bytes of rows (0, 1), (0, 1) or (2, 3)
+              return __byte_perm(w, __shfl_xor_sync(0xffffffffu, w, 1), own_other);
+            };
+            auto put = [&](int o, uint32_t w) { *reinterpret_cast<uint16_t*>(pc + o) = uint16_t(w); };
+            const uint32_t a0 = pairs(__byte_perm(s0.hi, s0.mid, 0x7531));
+            const uint32_t a1 = pairs(__byte_perm(s1.hi, s1.mid, 0x7531));
+            const uint32_t lo = pairs(__byte_perm(s0.lo, s1.lo, 0x7531));
+            put(at(n), a0);
+            put(at(n + 2), a1);
+            put(L::kPiece + at(n), a0 >> 16);
+            put(L::kPiece + at(n + 2), a1 >> 16);
+            put(2 * L::kPiece + at(n), lo);
+            put(2 * L::kPiece + at(n + 2), lo >> 16);
+          } else {
+            auto put = [&](int n, const Split2& s) {
+              pc[at(n)] = uint8_t(s.hi >> 8);
+              pc[at(n + 1)] = uint8_t(s.hi >> 24);
+              pc[L::kPiece + at(n)] = uint8_t(s.mid >> 8);
+              pc[L::kPiece + at(n + 1)] = uint8_t(s.mid >> 24);
+              pc[2 * L::kPiece + at(n)] = uint8_t(s.lo >> 8);
+              pc[2 * L::kPiece + at(n + 1)] = uint8_t(s.lo >> 24);
+            };
+            put(n, s0);
+            put(n + 2, s1);
+          }
         }
         // where keys are masked a NaN code of V times a zero weight must stay zero: stale rows past
         // the end are cleared, and a tree slot's NaN moves from V to the weights of the rows that
@@ -447,14 +473,18 @@ attn_kv8_rows_kernel(const __grid_constant__ CUtensorMap mK, const __grid_consta
           const int st = kg % kVStages;
           ok &= wait1(&sh.v_full[st], kg / kVStages, abort_flag);
           uint8_t* row = sV + st * kTile + kl * 128;
+          uint32_t seen = 0u;                          // the rows that get a NaN
           if (key >= kv_len) {
             clear_row(row);
           } else if (key >= P && (~vis & ((1u << (T * a.G)) - 1u)) != 0 && has_nan(row)) {
             clear_nan(row);                            // (T G <= 16; some row does not see it)
-#pragma unroll 1
-            for (int n = 0; n < NR; ++n)
-              if ((vis >> n) & 1u) pc[(n >> 3) * 1024 + (n & 7) * 128 + ((chunk ^ (n & 7)) << 4)] = 0x7F;
+            seen = vis;
           }
+          if constexpr (NR == 16) __syncwarp();        // (the neighbour has stored this lane's weights)
+          uint8_t* const own = sP + (grp * 2 + b) * L::kTriple + (kl & 15);
+#pragma unroll 1
+          for (int n = 0; seen >> n; ++n)
+            if ((seen >> n) & 1u) own[(n >> 3) * 1024 + (n & 7) * 128 + ((chunk ^ (n & 7)) << 4)] = 0x7F;
         }
         tc::fence_proxy_async_smem();
         tc::tc_fence_before();
