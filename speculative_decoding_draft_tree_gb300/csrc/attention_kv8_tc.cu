@@ -3,17 +3,18 @@
 // attn_kv8_rows_kernel: units of at most 8 or 16 query rows (T x G: single tokens and short chains).
 // S^T = K Q^T (M = 128 slots on the TMEM lanes, N = the rows' hi pieces, then their lo pieces), so
 // that the softmax spends its lanes on keys; O^T += V^T P^T with V read as an MN-major operand and
-// P^T's three pieces stacked the same way, each with columns of O of its own.  Bound by the codes' bytes: a tile's 32 KB take ~1400 clocks
-// of an SM's share of HBM and the products a quarter of that, so what has to keep up is the
-// softmax, whose step is a chain of latencies (wait, TMEM load, group vote, exponentials, stores).
+// P^T's three pieces stacked the same way, each with columns of O of its own.  Bound by the codes'
+// bytes: a tile's 32 KB take ~1400 clocks of an SM's share of HBM and the products a quarter of that,
+// so what has to keep up is the softmax, whose step is a chain of latencies (wait, TMEM load, group
+// vote, exponentials, stores).
 // Two groups of four warps take alternate tiles, each with references, sums and an accumulator of
 // its own, and a third warpgroup joins the two and writes a unit's rows while they go on with the
 // next one (accumulators are double-buffered by unit).
 // Warps: 0 copies K, 2 copies V, 1 issues the scores' products, 3 the output's, 4-7 and 8-11
 // softmax, 12-15 split the queries and write the output, 16 brings the scales, 17 walks the items.
-// Measured: 64 single tokens over 1024 .. 32768 slots (2.2 GB) 343 - 349 us, 6.4 TB/s, 95% of the
-// copy rate; 16 chains of 6, 32 KV heads, 2048 slots (271 MB) 54 us, 5.1 TB/s; one token over 2047
-// slots (4 MB) 10.8 us, all of it latency: the start, the walk to the first page, a tile, the join.
+// Measured: 64 single tokens over 1024 .. 32768 slots (2.2 GB) 341 - 352 us, 6.4 TB/s, 93 - 96% of the
+// copy rate; 16 chains of 6, 32 KV heads, 2048 slots (271 MB) 54 us, 5.0 TB/s; one token over 2047
+// slots (4 MB) 11.0 us, all of it latency: the start, the walk to the first page, a tile, the join.
 //
 // attn_kv8_tile_kernel: longer units in tiles of 128 query rows (G heads x 128 / G tree tokens).
 // S = Q K^T (M = N = 128, both pieces of Q into one accumulator) on the e4m3 codes; O += P V in fp16:
@@ -22,15 +23,14 @@
 // as two 8-bit pieces of P against the codes would, and P keeps fp16's 11 bits down to 2^-19 of a row's
 // largest weight.  (e5m2 and e4m3 pieces kept three bits below 2^-13: a long flat rest beside one heavy
 // key came out by up to an eighth wrong.  Three e5m2 pieces, right as well, took 367 and 1760 us on the
-// two shapes below.)  A tile takes ~2500 clocks: the exponentials and the conversion of V are ~770 of
-// them at 32 results a clock and SM, the products 1024, and no pipe is full; a step is a chain of waits,
+// two shapes below.)  A tile takes ~2600 clocks: the exponentials are 512 of them at 32 results a clock
+// and SM, the conversion of V ~200, the products 1024, and no pipe is full; a step is a chain of waits,
 // TMEM loads, votes and stores, which all warps take together, tile after tile.
-// A row belongs to four threads of
-// four warps, each with 32 of a tile's keys: they form weights against the present reference at
-// once and vote on it meanwhile; where the vote says that it moves, they agree on the new one and
-// form them again; ten binades of slack make that rare.  Three S buffers (TMEM columns 0-383, P over S)
-// keep the scores of the next
-// tiles coming while one is in the softmax and one in the output's product; O has columns 384-511.
+// A row belongs to four threads of four warps, each with 32 of a tile's keys: they form weights against
+// the present reference at once and vote on it meanwhile; where the vote says that it moves, they agree
+// on the new one and form them again; ten binades of slack make that rare.  Three S buffers (TMEM columns
+// 0-383, P over S) keep the scores of the next tiles coming while one is in the softmax and one in the
+// output's product; O has columns 384-511.
 // Warps: 0-3 as above, 4-19 softmax, 20-23 queries and output, 24 scales, 25 items, 28-31 V.
 // Measured: 32 trees of 46 over 8192 slots (32 query heads on 8) 301 us, 656 TFLOP/s of scores and
 // output; 64 ragged trees over 1024 .. 32768 slots (64 query heads on 8) 1465 us, 838 TFLOP/s.
@@ -1324,9 +1324,8 @@ static bool encode_maps(PFN_cuTensorMapEncodeTiled_v12000 enc, const AttnKv8Dev&
 }
 
 // Query rows of a unit's row tile: the smallest form that holds a request's rows.  Over 8192 slots,
-// 16 requests, 8 KV heads: 8 rows 51.8 us in the form of 8, 58.1 in that of 16, 78.3 in tiles of
-// 128; 16 rows 61.0 and 79.9.  (A form of 32 rows was slower than the tiles: 24 rows 95.6 us
-// against 82.2.)
+// 16 requests, 8 KV heads: 8 rows 53.4 us in the form of 8, 63.1 in that of 16, 86.0 in tiles of
+// 128; 16 rows 67.2 and 87.0.
 static int rows_of(const AttnKv8Dev& a) {
   const int rows = a.T_max * a.G;
   return rows <= 8 ? 8 : rows <= 16 ? 16 : tile::kRows;
@@ -1341,7 +1340,7 @@ static int device_ctas() {
 
 // Whether the tensor-core kernels take this call: their types and tile shapes, a row tile that holds
 // a token's query heads, row coordinates of TMA in 32 bits.  (32 and 64 query heads of one KV head,
-// 64 x 1 and 16 x 4 tokens over 8192 slots: 48 and 44 us here, 1120 and 1596 us on CUDA cores.)
+// 64 x 1 and 16 x 4 tokens over 8192 slots: 54 and 46 us here, 1120 and 1596 us on CUDA cores.)
 bool attn_kv8_tc_takes(const AttnKv8Dev& a, bool bf16) {
   return bf16 && a.d == 128 && (a.bs == 16 || a.bs == 32 || a.bs == 64 || a.bs == 128) &&
          a.G <= kv8tc::tile::kRows &&
@@ -1364,7 +1363,7 @@ spec_status_t launch_attn_kv8_tc(const AttnKv8Dev& a, void* ws, size_t ws_bytes,
   d.log2bs = a.bs == 16 ? 4 : a.bs == 32 ? 5 : a.bs == 64 ? 6 : 7;
   d.kv_rows = a.num_blocks * a.H_kv * a.bs;
   d.ctas = ctas;
-  d.min_tiles = 2;   // one token over 2047 slots: 10.8 us; 12.1 with 1, 11.4 with 4, 14.0 with 8
+  d.min_tiles = 2;   // one token over 2047 slots: 11.1 us; 12.2 with 1, 11.5 with 4, 14.1 with 8
   d.pair = a.T_max * a.G > tile::kRows && ctas > 1;
   const WsLayout lay = ws_layout(ctas, d.part_rows);
   if (!ws || ws_bytes < lay.total || (reinterpret_cast<uintptr_t>(ws) & 255u))

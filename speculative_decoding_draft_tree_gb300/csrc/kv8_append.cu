@@ -14,8 +14,8 @@
 // one launch serves single tokens, trees and prompts alike.
 //
 // Measured (bf16, head_dim 128, blocks of 16): prompts, 49,000 tokens of 32 KV heads (1.2 GB) 191
-// us, 6.4 TB/s, 94% of the copy rate; 64 trees of 8 .. 56 tokens, 8 KV heads (12 MB) 8 us and 64
-// single tokens 4 us, both bound by the launch and the chain offsets -> page -> scale -> codes.
+// us, 6.4 TB/s, 94% of the copy rate (fp32: 298 us, at the copy rate); 64 trees of 8 .. 56 tokens, 8 KV
+// heads (12 MB) 8.2 us (fp32 10.6) and 64 single tokens 4 us, both bound by the launch and the chain offsets -> page -> scale -> codes.
 #include "kv8.cuh"
 
 namespace spec {
