@@ -10,7 +10,8 @@ e4m3 pieces, off by 2^-17.8 max|q| an element, sums in fp32 (2^-17 of their magn
 2^7 in fp32 and exp2 (2^-16 together).  Output: one rounding to bf16 (2^-8).
 fp32 queries: fp32 products and sums, 2^-17 of the mean absolute value beside the scores' error.
 Over all outputs the roundings to bf16 are independent: their root mean square is at most
-2^-8 / sqrt(3) of the outputs', which with the weights' 2^-10 + 2^-11 added in squares is below 2.8e-3."""
+2^-8 / sqrt(3) of the outputs', which with the weights' 2^-10 + 2^-11 added in squares is below 2.8e-3.
+(kv8_util.check_attention's bars are wider: they allow for weights in e4m3 pieces.)"""
 import numpy as np
 import pytest
 import torch
