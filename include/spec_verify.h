@@ -611,6 +611,164 @@ typedef struct {
 
 spec_status_t spec_kv_fork(const spec_fork_params* p, spec_stream_t stream);
 
+/* ==========================================================================================
+ * Attention over a part of the cache, or over a part that requests have in common -- no counterpart
+ * on the pages beyond [SURV 12.4.3] (paged caches that sequences share).  Both calls take
+ * spec_tree_attention's parameters as `attn` (the same layouts, masks, scale and data errors) with these
+ * differences:
+ *   - every H_q / H_kv ratio, block_size and head_dim (multiple of 8 bf16 / 4 fp32 elements, <= 256)
+ *     is accepted; BF16 with head_dim 128, block_size 16, 32, 64 or 128 and H_q / H_kv <= 128 runs on
+ *     the tcgen05 tensor cores, everything else on a CUDA-core kernel;
+ *   - a row that sees no key gets O = 0 and LSE = -infinity;
+ *   - a NaN or an infinity in q, K or V reaches the rows that see it and no others (of V: the output's
+ *     column at least).  Slots that no row of a request sees are not looked at;
+ *   - the ancestor mask's bits count only for nodes of the request's own tree;
+ *   - a request with T_r outside [1, T_max], a negative prefix or node offsets outside [0, N] gets
+ *     SPEC_REQ_BAD_SIZE; one whose slots lie beyond its table row (or 2^31 - 1025) SPEC_REQ_BAD_BLOCK; no
+ *     rows are written for either, nor for a request whose req_status holds other bits than BAD_BLOCK
+ *     and TIMEOUT.  One with a bad id among the pages that its rows see gets SPEC_REQ_BAD_BLOCK and
+ *     unspecified rows.
+ * workspace: the call's workspace_size bytes, 256-byte aligned, contents arbitrary; calls that may
+ * overlap on the GPU (other streams, captured graphs) need one each.
+ * Errors: SPEC_ERR_INVALID_ARG, SPEC_ERR_UNSUPPORTED (head_dim above 256, 2^31 rows of pages or of
+ * queries), SPEC_ERR_CUDA.
+ * ========================================================================================== */
+
+/* ------------------------------------------------------------------------------------------
+ * spec_tree_attention_window
+ * A sliding window with sinks: node i at position m = P_r + depth sees the slot of a token at position p
+ * (prefix slot p, or an ancestor or itself in the tree) iff p < sinks or m - p < window; window >= 1
+ * counts the node itself.  depth is the number of the node's mask bits less one, its ancestors' depths
+ * count up in increasing index (what spec_tree_build writes).  Pages all of whose slots are out of sight
+ * of every node (from max(sinks, 0) up to P_r - window) are not read, and their table entries may hold
+ * anything.
+ * Errors: SPEC_ERR_INVALID_ARG also for window < 1 or sinks < 0.
+ * ------------------------------------------------------------------------------------------ */
+typedef struct {
+  spec_attn_params attn;
+  int32_t window, sinks;
+} spec_attn_window_params;
+
+size_t spec_attention_window_workspace_size(const spec_attn_window_params* p);
+spec_status_t spec_tree_attention_window(const spec_attn_window_params* p, void* workspace,
+                                         size_t ws_bytes, spec_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * spec_tree_attention_shared
+ * spec_tree_attention for requests that have a prefix in common (samples or beams of one prompt, as
+ * spec_kv_fork and spec_beam_reorder leave them; requests under one system prompt): group g is the
+ * consecutive requests group_offset[g] .. group_offset[g+1]-1 (num_groups + 1 entries from 0 to B), whose
+ * first shared_len[g] slots hold the same keys and values.  Those slots are read by the table row of the
+ * group's first request, once for all of the group's rows; each request's slots from shared_len on by its
+ * own.  shared_len is any length from 0 to the members' prefix lengths; a group may have one member.
+ * The result is spec_tree_attention's.
+ * Data errors: a request that group_offset puts in no group, whose group's shared_len is negative or
+ * beyond its prefix, or whose group's node offsets lie outside [0, N] gets SPEC_REQ_BAD_SIZE and no rows.
+ * Bad ids among the shared pages flag every member with SPEC_REQ_BAD_BLOCK.
+ * The workspace grows with N x H_q x head_dim (two fp32 rows of partial results each).
+ * Errors: SPEC_ERR_INVALID_ARG also for num_groups outside [1, B] or null group arrays.
+ * ------------------------------------------------------------------------------------------ */
+typedef struct {
+  spec_attn_params attn;
+  int32_t num_groups;
+  const int32_t* group_offset;   /* [num_groups + 1] */
+  const int32_t* shared_len;     /* [num_groups] */
+} spec_attn_shared_params;
+
+size_t spec_attention_shared_workspace_size(const spec_attn_shared_params* p);
+spec_status_t spec_tree_attention_shared(const spec_attn_shared_params* p, void* workspace,
+                                         size_t ws_bytes, spec_stream_t stream);
+
+/* ==========================================================================================
+ * Beam search -- no counterpart on the pages.  Request b has W beams; beam j's row is row b * W + j of
+ * the logits, of the block table and of every call that takes requests.  A step: the model's forward
+ * (spec_tree_attention_shared with a group for each request), spec_beam_select on its logits,
+ * spec_beam_reorder on the cache.
+ * ========================================================================================== */
+
+/* ------------------------------------------------------------------------------------------
+ * spec_beam_select
+ * The best W continuations of each request.  Beam j with score s (the sum of its tokens' log
+ * probabilities) and length n offers, if it is not finished, every token x < V with
+ *   score s + log_softmax(row / tau)[x], length n + 1,
+ * and if it is finished only itself: token eos, score s, length n.  Continuations are ranked by
+ *   score / ((5 + length) / 6)^alpha,
+ * largest first, ties to the lower beam, then to the lower token; equal logits of a beam are a tie.  Out
+ * comes, best first: parent (beam), token, score, length, finished (1: was finished, or token == eos).
+ * A beam with score -infinity (a slot that is not in use yet) or NaN offers nothing, nor do logits of
+ * -infinity and NaN; a NaN or +infinity among a row's logits takes the whole row out.  If fewer than W are
+ * offered the rest is parent j, token 0, score -infinity, length n of beam j, finished 0 at place j.
+ * Sums of exponentials are in fp32 per thread and fp64 beyond, scores and ranks in fp64, rounded once.
+ * Layouts: logits [B * W][ld] F32 / BF16, rows 16-byte aligned (ld a multiple of 16 bytes); scores [B][W]
+ * fp32, lengths (>= 0), finished [B][W] int32; outputs [B][W].  out_score, out_length and out_finished
+ * may be the inputs' own buffers.  eos outside [0, V): no token finishes a beam (a finished one then
+ * carries token 0).
+ * workspace: spec_beam_select_workspace_size bytes, 256-byte aligned.
+ * Errors: SPEC_ERR_INVALID_ARG (null / misaligned pointers, V < 1, ld < V, tau <= 0 or so large or small
+ * that log2(e) / tau is no normal fp32 number, alpha < 0, not finite, small workspace),
+ * SPEC_ERR_UNSUPPORTED (W > 16, B * W > 65535), SPEC_ERR_CUDA.
+ * ------------------------------------------------------------------------------------------ */
+#define SPEC_MAX_BEAMS 16
+typedef struct {
+  spec_dtype_t dtype;          /* of logits */
+  int32_t B, W, V, eos;
+  int64_t ld;                  /* elements between rows */
+  double tau, alpha;
+  const void* logits;
+  const float* scores;
+  const int32_t* lengths;
+  const int32_t* finished;
+  int32_t* parent;
+  int32_t* token;
+  float* out_score;
+  int32_t* out_length;
+  int32_t* out_finished;
+} spec_beam_select_params;
+
+size_t spec_beam_select_workspace_size(const spec_beam_select_params* p);
+spec_status_t spec_beam_select(const spec_beam_select_params* p, void* workspace, size_t ws_bytes,
+                               spec_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * spec_beam_reorder
+ * Makes beam j of request b continue its beam parent[b][j], in place: the W rows b * W + j of block_table
+ * cover kv_len[b] = L tokens each, and entry L / block_size of a row, its writing page (the page of the
+ * next token), is the beam's own, also when L is a multiple of block_size.  For each request
+ *   - entries 0 .. L / block_size - 1 of row j become the parent's (full pages, shared, read-only);
+ *   - a parent's first child takes its writing page over; the parent's other children get, in increasing
+ *     order, the writing pages of the beams without children in increasing order, and the parent's
+ *     L % block_size rows of that page are copied into them for every layer, head, K and V (and the
+ *     page's scales in an 8-bit cache);
+ *   - later entries of the row stay.
+ * So the W writing pages of a request stay its own, and no page has to be found or given back: with W
+ * pages set aside for each entry past the prompt, a search never runs out.  Parents that are 0 for every
+ * beam spread one prompt over W beams.
+ * beam_status [B]: 0, or the request was left as it was: SPEC_REQ_BAD_PARENT (a parent outside [0, W)),
+ * SPEC_REQ_BAD_SIZE (L < 0 or L / block_size beyond the table row), SPEC_REQ_BAD_BLOCK (a writing page
+ * outside [0, num_blocks), or one that two beams of the request name).  Writing pages that two requests
+ * name are the caller's to avoid.
+ * `dtype`, layouts and strides as in spec_kv_fork; W <= 16.
+ * workspace: spec_beam_reorder_workspace_size bytes, 256-byte aligned.
+ * Errors: SPEC_ERR_INVALID_ARG, SPEC_ERR_UNSUPPORTED (W > 16, more than 65535 layers), SPEC_ERR_CUDA.
+ * ------------------------------------------------------------------------------------------ */
+typedef struct {
+  spec_dtype_t dtype;
+  int32_t B, W, H_kv, head_dim, block_size, num_blocks, max_blocks_per_req, num_layers;
+  int64_t layer_stride, scale_layer_stride;
+  void* k_cache;
+  void* v_cache;
+  float* k_scale;
+  float* v_scale;
+  int32_t* block_table;          /* [B * W][max_blocks_per_req], in / out */
+  const int32_t* kv_len;         /* [B] */
+  const int32_t* parent;         /* [B][W] */
+  int32_t* beam_status;          /* [B] */
+} spec_beam_reorder_params;
+
+size_t spec_beam_reorder_workspace_size(const spec_beam_reorder_params* p);
+spec_status_t spec_beam_reorder(const spec_beam_reorder_params* p, void* workspace, size_t ws_bytes,
+                                spec_stream_t stream);
+
 /* Human-readable name of a status code (static storage, never NULL). */
 const char* spec_status_string(spec_status_t status);
 

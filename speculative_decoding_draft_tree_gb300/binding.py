@@ -27,7 +27,12 @@ EXPORTS = ["spec_tree_build", "spec_tree_rope_kv_write", "spec_tree_build_rope_k
            "spec_draft_expand_select", "spec_draft_topk_append", "spec_echo_workspace_size",
            "spec_echo_select_pack", "spec_debug_draft_copy_stall", "spec_verify_compact",
            "spec_kernel_launches", "spec_kv8_append", "spec_tree_attention_kv8",
-           "spec_attention_kv8_workspace_size", "spec_kv8_compact", "spec_kv_fork"]
+           "spec_attention_kv8_workspace_size", "spec_kv8_compact", "spec_kv_fork",
+           "spec_tree_attention_window", "spec_attention_window_workspace_size",
+           "spec_tree_attention_shared", "spec_attention_shared_workspace_size",
+           "spec_beam_select", "spec_beam_select_workspace_size", "spec_beam_reorder",
+           "spec_beam_reorder_workspace_size"]
+SPEC_MAX_BEAMS = 16
 
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
@@ -110,6 +115,32 @@ class SpecForkParams(ctypes.Structure):
                 ("src", _vp), ("dst", _vp), ("new_block", _vp), ("fork_status", _vp)]
 
 
+class SpecAttnWindowParams(ctypes.Structure):
+    _fields_ = [("attn", SpecAttnParams), ("window", _i32), ("sinks", _i32)]
+
+
+class SpecAttnSharedParams(ctypes.Structure):
+    _fields_ = [("attn", SpecAttnParams), ("num_groups", _i32), ("group_offset", _vp),
+                ("shared_len", _vp)]
+
+
+class SpecBeamSelectParams(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("B", _i32), ("W", _i32), ("V", _i32), ("eos", _i32),
+                ("ld", _i64), ("tau", ctypes.c_double), ("alpha", ctypes.c_double),
+                ("logits", _vp), ("scores", _vp), ("lengths", _vp), ("finished", _vp),
+                ("parent", _vp), ("token", _vp), ("out_score", _vp), ("out_length", _vp),
+                ("out_finished", _vp)]
+
+
+class SpecBeamReorderParams(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("B", _i32), ("W", _i32), ("H_kv", _i32),
+                ("head_dim", _i32), ("block_size", _i32), ("num_blocks", _i32),
+                ("max_blocks_per_req", _i32), ("num_layers", _i32), ("layer_stride", _i64),
+                ("scale_layer_stride", _i64), ("k_cache", _vp), ("v_cache", _vp),
+                ("k_scale", _vp), ("v_scale", _vp), ("block_table", _vp), ("kv_len", _vp),
+                ("parent", _vp), ("beam_status", _vp)]
+
+
 class SpecDraftPool(ctypes.Structure):
     _fields_ = [("B", _i32), ("cap", _i32), ("parent", _vp), ("token", _vp), ("depth", _vp),
                 ("score", _vp), ("row", _vp), ("count", _vp)]
@@ -185,6 +216,14 @@ def load_library(build_if_missing=False):
     lib.spec_kv8_compact.argtypes = [ctypes.POINTER(SpecKv8CompactParams), _vp]
     lib.spec_kv_fork.restype = st
     lib.spec_kv_fork.argtypes = [ctypes.POINTER(SpecForkParams), _vp]
+    for name, params in (("spec_tree_attention_window", SpecAttnWindowParams),
+                         ("spec_tree_attention_shared", SpecAttnSharedParams),
+                         ("spec_beam_select", SpecBeamSelectParams),
+                         ("spec_beam_reorder", SpecBeamReorderParams)):
+        getattr(lib, name).restype = st
+        getattr(lib, name).argtypes = [ctypes.POINTER(params), _vp, ctypes.c_size_t, _vp]
+        size = getattr(lib, name.replace("spec_tree_attention", "spec_attention") + "_workspace_size")
+        size.restype, size.argtypes = ctypes.c_size_t, [ctypes.POINTER(params)]
     lib.spec_kernel_launches.restype = ctypes.c_uint64
     lib.spec_kernel_launches.argtypes = []
     lib.spec_status_string.restype = ctypes.c_char_p
@@ -644,6 +683,176 @@ def spec_kv_fork(params, stream=None):
     """Child sequences of cached ones: shared full pages, the partial page copied."""
     code = load_library().spec_kv_fork(_on_device(params), _stream(stream))
     _check(code, "spec_kv_fork")
+
+
+# ----------------------------------------------------------------------------------------------
+# Attention over a window of the cache, or over a prefix that requests have in common; beam search.
+def _paged_attention(q, k_cache, v_cache, block_table, prefix_len, node_offset, anc_mask, T_max, o,
+                     lse, req_status, scale):
+    """attention_params with every shape checked: one layer's caches [num_blocks, H_kv, block_size,
+    head_dim], q and o [N, H_q, head_dim]."""
+    _need(q, None, "q")
+    if q.dim() != 3:
+        raise ValueError(f"q must be [N, H_q, head_dim], got {tuple(q.shape)}")
+    N, H_q, d = q.shape
+    _need(k_cache, q.dtype, "k_cache")
+    if k_cache.dim() != 4 or k_cache.shape[3] != d:
+        raise ValueError(f"k_cache must be [num_blocks, H_kv, block_size, {d}], got "
+                         f"{tuple(k_cache.shape)}")
+    _need_shape(v_cache, k_cache.shape, "v_cache", q.dtype)
+    _need_shape(o, q.shape, "o", q.dtype)
+    if lse is not None:
+        _need_shape(lse, (N, H_q), "lse", torch.float32)
+    _need(block_table, torch.int32, "block_table")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_blocks]")
+    B = block_table.shape[0]
+    _need_shape(prefix_len, (B,), "prefix_len")
+    _need_shape(node_offset, (B + 1,), "node_offset")
+    _need_shape(anc_mask, (N, (int(T_max) + 31) // 32), "anc_mask")
+    _need_shape(req_status, (B,), "req_status")
+    return attention_params(q, k_cache, v_cache, block_table, prefix_len, node_offset, anc_mask,
+                            int(T_max), o, lse, req_status, scale)
+
+
+def _call(name, params, workspace, stream):
+    if workspace is not None:
+        _need(workspace, None, "workspace")
+        if workspace.device.index != params._device:
+            raise ValueError(f"workspace must be on cuda:{params._device}")
+    wsz = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    code = getattr(load_library(), name)(_on_device(params), _ptr(workspace), wsz, _stream(stream))
+    _check(code, name)
+
+
+def attention_window_params(q, k_cache, v_cache, block_table, prefix_len, node_offset, anc_mask,
+                            T_max, window, sinks, o, lse, req_status, scale=0.0):
+    """attention_params with a sliding window: a node sees the last `window` positions up to its own
+    and the first `sinks`.  Table entries of pages that no node sees may hold anything (-1)."""
+    p = SpecAttnWindowParams()
+    p.attn = _paged_attention(q, k_cache, v_cache, block_table, prefix_len, node_offset, anc_mask,
+                              T_max, o, lse, req_status, scale)
+    p.window, p.sinks = int(window), int(sinks)
+    return _held(p, q, k_cache, v_cache, block_table, prefix_len, node_offset, anc_mask, o, lse,
+                 req_status)
+
+
+def spec_attention_window_workspace_size(params):
+    return int(load_library().spec_attention_window_workspace_size(ctypes.byref(params)))
+
+
+def spec_tree_attention_window(params, workspace, stream=None):
+    """Tree attention with a sliding window and sinks; calls that may overlap need a workspace each."""
+    _call("spec_tree_attention_window", params, workspace, stream)
+
+
+def attention_shared_params(q, k_cache, v_cache, block_table, prefix_len, node_offset, anc_mask,
+                            T_max, group_offset, shared_len, o, lse, req_status, scale=0.0):
+    """attention_params for groups of consecutive requests (group_offset [groups + 1]) that have their
+    first shared_len [groups] slots in common; those are read once a group, by its first request's
+    table row."""
+    p = SpecAttnSharedParams()
+    p.attn = _paged_attention(q, k_cache, v_cache, block_table, prefix_len, node_offset, anc_mask,
+                              T_max, o, lse, req_status, scale)
+    _need(shared_len, torch.int32, "shared_len")
+    _need_shape(group_offset, (shared_len.numel() + 1,), "group_offset")
+    p.num_groups = shared_len.numel()
+    p.group_offset, p.shared_len = group_offset.data_ptr(), shared_len.data_ptr()
+    return _held(p, q, k_cache, v_cache, block_table, prefix_len, node_offset, anc_mask, o, lse,
+                 req_status, group_offset, shared_len)
+
+
+def spec_attention_shared_workspace_size(params):
+    return int(load_library().spec_attention_shared_workspace_size(ctypes.byref(params)))
+
+
+def spec_tree_attention_shared(params, workspace, stream=None):
+    """Tree attention under shared prefixes; calls that may overlap need a workspace each."""
+    _call("spec_tree_attention_shared", params, workspace, stream)
+
+
+def beam_select_params(logits, V, tau, scores, lengths, finished, eos, alpha, parent, token,
+                       out_score, out_length, out_finished):
+    """logits [B * W, ld] (fp32 or bf16, ld >= V); scores fp32, lengths, finished and the outputs
+    int32 (out_score fp32), all [B, W].  The outputs of score, length and finished may be the inputs'
+    own tensors."""
+    _need(scores, torch.float32, "scores")
+    if scores.dim() != 2:
+        raise ValueError("scores must be [B, W]")
+    B, W = scores.shape
+    _need(logits, None, "logits")
+    if logits.dim() != 2 or logits.shape[0] != B * W:
+        raise ValueError(f"logits must be [{B * W}, ld], got {tuple(logits.shape)}")
+    for t, n in ((lengths, "lengths"), (finished, "finished"), (parent, "parent"),
+                 (token, "token"), (out_length, "out_length"), (out_finished, "out_finished")):
+        _need_shape(t, (B, W), n)
+    _need_shape(out_score, (B, W), "out_score", torch.float32)
+    p = SpecBeamSelectParams()
+    p.dtype = _dtype_code(logits)
+    p.B, p.W, p.V, p.eos, p.ld = B, W, int(V), int(eos), logits.shape[1]
+    p.tau, p.alpha = float(tau), float(alpha)
+    p.logits, p.scores, p.lengths = logits.data_ptr(), scores.data_ptr(), lengths.data_ptr()
+    p.finished, p.parent, p.token = finished.data_ptr(), parent.data_ptr(), token.data_ptr()
+    p.out_score, p.out_length = out_score.data_ptr(), out_length.data_ptr()
+    p.out_finished = out_finished.data_ptr()
+    return _held(p, logits, scores, lengths, finished, parent, token, out_score, out_length,
+                 out_finished)
+
+
+def spec_beam_select_workspace_size(params):
+    return int(load_library().spec_beam_select_workspace_size(ctypes.byref(params)))
+
+
+def spec_beam_select(params, workspace, stream=None):
+    """The best W continuations of each request's W beams (params from beam_select_params)."""
+    _call("spec_beam_select", params, workspace, stream)
+
+
+def beam_reorder_params(k_cache, v_cache, block_table, kv_len, parent, beam_status, k_scale=None,
+                        v_scale=None):
+    """k_cache / v_cache: [L, num_blocks, H_kv, block_size, head_dim], fp32, bf16 or 8-bit (then with
+    k_scale / v_scale [L, num_blocks, H_kv]); block_table [B * W, max_blocks] (updated), kv_len,
+    beam_status [B], parent [B, W]."""
+    if k_scale is not None or v_scale is not None:
+        L, nb, H_kv, bs, d = _need_kv8(k_cache, v_cache, k_scale, v_scale, 1)
+        code = SPEC_E4M3
+    else:
+        _need(k_cache, None, "k_cache")
+        code = _dtype_code(k_cache)
+        if k_cache.dim() != 5:
+            raise ValueError("k_cache must be [L, num_blocks, H_kv, block_size, head_dim]")
+        _need_shape(v_cache, k_cache.shape, "v_cache", k_cache.dtype)
+        L, nb, H_kv, bs, d = k_cache.shape
+    _need(parent, torch.int32, "parent")
+    if parent.dim() != 2:
+        raise ValueError("parent must be [B, W]")
+    B, W = parent.shape
+    _need(block_table, torch.int32, "block_table")
+    if block_table.dim() != 2 or block_table.shape[0] != B * W:
+        raise ValueError(f"block_table must be [{B * W}, max_blocks], got "
+                         f"{tuple(block_table.shape)}")
+    _need_shape(kv_len, (B,), "kv_len")
+    _need_shape(beam_status, (B,), "beam_status")
+    p = SpecBeamReorderParams()
+    p.dtype, p.B, p.W = code, B, W
+    p.H_kv, p.head_dim, p.block_size, p.num_blocks = H_kv, d, bs, nb
+    p.max_blocks_per_req, p.num_layers = block_table.shape[1], L
+    p.layer_stride, p.scale_layer_stride = nb * H_kv * bs * d, nb * H_kv
+    p.k_cache, p.v_cache = k_cache.data_ptr(), v_cache.data_ptr()
+    p.k_scale = None if k_scale is None else k_scale.data_ptr()
+    p.v_scale = None if v_scale is None else v_scale.data_ptr()
+    p.block_table, p.kv_len = block_table.data_ptr(), kv_len.data_ptr()
+    p.parent, p.beam_status = parent.data_ptr(), beam_status.data_ptr()
+    return _held(p, k_cache, v_cache, block_table, kv_len, parent, beam_status, k_scale, v_scale)
+
+
+def spec_beam_reorder_workspace_size(params):
+    return int(load_library().spec_beam_reorder_workspace_size(ctypes.byref(params)))
+
+
+def spec_beam_reorder(params, workspace, stream=None):
+    """The beams' cache follows the selection, in place (params from beam_reorder_params)."""
+    _call("spec_beam_reorder", params, workspace, stream)
 
 
 # ----------------------------------------------------------------------------------------------

@@ -1,0 +1,553 @@
+// spec_tree_attention_shared and spec_tree_attention_window: argument checks, workspaces, the kernel on
+// the CUDA cores and the merge of pieces.  attention_span.cuh says how the work is laid out;
+// attention_span_tc.cu has the kernel on the tensor cores.
+//
+// Per query row, over its visible keys j: x_j = scale q.k_j, O = sum_j 2^(x_j - M) v_j / sum_j 2^(x_j - M)
+// in base 2 (scale holds log2 e), LSE = ln 2 (M + log2 sum).  Pieces of a row merge by the same sums:
+// O = sum_p 2^(L_p - M) O_p / sum_p 2^(L_p - M) with L_p the piece's log2-sum-exp.
+#include <math.h>
+
+#include "attention_span.cuh"
+
+namespace spec {
+namespace span {
+
+// ------------------------------------------------------------------------------ CUDA cores
+// Any head_dim up to 256 and any block size, fp32 and bf16.  A CTA takes 32 query rows by 64 keys at a
+// time; thread (ty, tx) has rows 2 ty, 2 ty + 1, keys tx + 16 k of the scores and columns 4 tx + 64 c of
+// the output, all in fp32.  Bound by its shared-memory reads (6 vectors for 32 multiply-adds of the
+// scores).
+constexpr int kSimtThreads = 256;
+constexpr int kSimtRows = 32;
+constexpr int kSimtKeys = 64;
+
+struct SimtShared {
+  RangeScratch scratch;
+  Item item;
+  int more;
+  int page[kSimtKeys];                 // cache row of a key's page row, -1: not needed
+  int row_lo[kSimtRows];
+  uint32_t anc[kSimtRows][8];
+  uint64_t vis[kSimtRows];             // a masked tile's visible keys
+  float p[kSimtRows][kSimtKeys + 4];
+};
+
+__host__ __device__ constexpr int simt_smem(int d) {
+  return int(sizeof(SimtShared)) + 16 + 4 * (kSimtRows * d + 2 * kSimtKeys * (d + 4));
+}
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p) {
+  if constexpr (sizeof(T) == 4) {
+    return *reinterpret_cast<const float4*>(p);
+  } else {
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
+    return make_float4(bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y));
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store4(T* p, float4 v) {
+  if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(p) = v;
+  } else {
+    __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+    uint2 w;
+    w.x = *reinterpret_cast<uint32_t*>(&lo);
+    w.y = *reinterpret_cast<uint32_t*>(&hi);
+    *reinterpret_cast<uint2*>(p) = w;
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kSimtThreads) span_simt_kernel(Dev a) {
+  extern __shared__ uint8_t smem_raw[];
+  SimtShared& s = *reinterpret_cast<SimtShared*>(smem_raw);
+  float* sq = reinterpret_cast<float*>(smem_raw + ((sizeof(SimtShared) + 15) & ~size_t(15)));
+  float* sk = sq + kSimtRows * a.d;
+  const int ldk = a.d + 4;
+  float* sv = sk + kSimtKeys * ldk;
+  pdl_wait();
+  pdl_trigger();
+  const Range R = cta_range<kSimtThreads>(a, s.scratch);
+  if (R.t0 >= R.t1) return;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int d4 = a.d >> 2;
+  const T* q = static_cast<const T*>(a.q);
+  const T* kc = static_cast<const T*>(a.k);
+  const T* vc = static_cast<const T*>(a.v);
+  Walker walker;
+  if (tid == 0) walker.start(a, R);
+  while (true) {
+    if (tid == 0) s.more = walker.next(a, R, s.item) ? 1 : 0;
+    __syncthreads();
+    if (!s.more) return;
+    const Item it = s.item;
+    const int rows = min(kSimtRows, it.T * a.G - it.mt * kSimtRows);
+    const bool tree = it.end > it.P;
+    // the rows' queries, ancestor words and bounds
+    for (int i = tid; i < kSimtRows * d4; i += kSimtThreads) {
+      const int m = i / d4, c = i - m * d4;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (m < rows) {
+        const int row = it.mt * kSimtRows + m, t = row / a.G, g = row - t * a.G;
+        x = load4(q + (size_t(it.o + t) * a.H_q + it.h * a.G + g) * a.d + 4 * c);
+      }
+      reinterpret_cast<float4*>(sq)[m * d4 + c] = x;
+    }
+    if (tid < kSimtRows) {
+      int lo = it.lo;
+      for (int w = 0; w < 8; ++w) s.anc[tid][w] = 0;
+      if (tid < rows && tree) {
+        const uint32_t* arow = a.anc + size_t(it.o + (it.mt * kSimtRows + tid) / a.G) * a.W;
+        if (a.window > 0) {
+          lo = window_words(a, arow, it.P, s.anc[tid]);
+        } else {
+          for (int w = 0; w < a.W; ++w) s.anc[tid][w] = arow[w];
+        }
+      }
+      s.row_lo[tid] = lo;
+    }
+    const int lo_max = a.window > 0 ? (int)max(0LL, (long long)it.P + it.T - a.window) : it.lo;
+    const int32_t* table = a.block_table + size_t(it.table) * a.max_blocks;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    float4 acc[2][4];
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = it.j0; j < it.j1; ++j) {
+      const int kb = key_base(a, it.nt0, it.w0, j);
+      const bool masked = !(kb + kSimtKeys <= it.P && (kb >= lo_max || (a.window > 0 && kb + kSimtKeys <= a.sinks)));
+      if (tid < kSimtKeys) {
+        const int key = kb + tid;
+        int at = -1;
+        if (key < it.sink || (key >= it.lo && key < it.end)) {
+          const int pb = table[key / a.bs];
+          if (pb < 0 || pb >= a.num_blocks) {
+            flag(a, it.req, it.nreq, SPEC_REQ_BAD_BLOCK);
+          } else {
+            at = pb * a.bs * a.H_kv + it.h * a.bs + key % a.bs;   // < num_blocks * bs * H_kv, checked on the host
+          }
+        }
+        s.page[tid] = at;
+      }
+      __syncthreads();
+      for (int i = tid; i < kSimtKeys * d4; i += kSimtThreads) {
+        const int n = i / d4, c = i - n * d4;
+        const int at = s.page[n];
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+        if (at >= 0) {
+          x = load4(kc + size_t(at) * a.d + 4 * c);
+          y = load4(vc + size_t(at) * a.d + 4 * c);
+        }
+        *reinterpret_cast<float4*>(sk + n * ldk + 4 * c) = x;
+        *reinterpret_cast<float4*>(sv + n * ldk + 4 * c) = y;
+      }
+      if (masked && tid < kSimtRows) {
+        uint64_t v = 0;
+        for (int n = 0; n < kSimtKeys; ++n) {
+          const int key = kb + n, t = key - it.P;
+          bool b = false;
+          if (tid < rows && s.page[n] >= 0) {
+            if (t < 0) b = key >= s.row_lo[tid] || (a.window > 0 && key < a.sinks);
+            else b = t < 32 * a.W && ((s.anc[tid][t >> 5] >> (t & 31)) & 1u);
+          }
+          v |= uint64_t(b ? 1 : 0) << n;
+        }
+        s.vis[tid] = v;
+      }
+      __syncthreads();
+      float x0[4] = {0.f, 0.f, 0.f, 0.f}, x1[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int c = 0; c < d4; ++c) {
+        const float4 qa = reinterpret_cast<const float4*>(sq)[(2 * ty) * d4 + c];
+        const float4 qb = reinterpret_cast<const float4*>(sq)[(2 * ty + 1) * d4 + c];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float4 kv = *reinterpret_cast<const float4*>(sk + (tx + 16 * k) * ldk + 4 * c);
+          x0[k] = fmaf(qa.x, kv.x, x0[k]); x0[k] = fmaf(qa.y, kv.y, x0[k]);
+          x0[k] = fmaf(qa.z, kv.z, x0[k]); x0[k] = fmaf(qa.w, kv.w, x0[k]);
+          x1[k] = fmaf(qb.x, kv.x, x1[k]); x1[k] = fmaf(qb.y, kv.y, x1[k]);
+          x1[k] = fmaf(qb.z, kv.z, x1[k]); x1[k] = fmaf(qb.w, kv.w, x1[k]);
+        }
+      }
+      const uint64_t v0 = masked ? s.vis[2 * ty] : ~0ull, v1 = masked ? s.vis[2 * ty + 1] : ~0ull;
+      float c0 = -INFINITY, c1 = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        x0[k] = (v0 >> (tx + 16 * k)) & 1 ? x0[k] * a.scale_log2 : -INFINITY;
+        x1[k] = (v1 >> (tx + 16 * k)) & 1 ? x1[k] * a.scale_log2 : -INFINITY;
+        c0 = fmaxf(c0, x0[k]);
+        c1 = fmaxf(c1, x1[k]);
+      }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) {
+        c0 = fmaxf(c0, __shfl_xor_sync(0xffffffffu, c0, o));
+        c1 = fmaxf(c1, __shfl_xor_sync(0xffffffffu, c1, o));
+      }
+      const float n0 = fmaxf(m0, c0), n1 = fmaxf(m1, c1);
+      const float f0 = m0 == -INFINITY ? 0.f : exp2f(m0 - n0), f1 = m1 == -INFINITY ? 0.f : exp2f(m1 - n1);
+      float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        // a masked score is -inf: weight 0, also while the row has seen nothing (its reference is -inf)
+        const float p0 = (v0 >> (tx + 16 * k)) & 1 ? exp2f(x0[k] - n0) : 0.f;
+        const float p1 = (v1 >> (tx + 16 * k)) & 1 ? exp2f(x1[k] - n1) : 0.f;
+        s.p[2 * ty][tx + 16 * k] = p0;
+        s.p[2 * ty + 1][tx + 16 * k] = p1;
+        s0 += p0;
+        s1 += p1;
+      }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) {
+        s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+        s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+      }
+      l0 = l0 * f0 + s0;
+      l1 = l1 * f1 + s1;
+      m0 = n0;
+      m1 = n1;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        acc[0][c].x *= f0; acc[0][c].y *= f0; acc[0][c].z *= f0; acc[0][c].w *= f0;
+        acc[1][c].x *= f1; acc[1][c].y *= f1; acc[1][c].z *= f1; acc[1][c].w *= f1;
+      }
+      __syncwarp();   // a row's weights come from its own half warp
+      for (int n = 0; n < kSimtKeys; ++n) {
+        const float p0 = s.p[2 * ty][n], p1 = s.p[2 * ty + 1][n];
+        const bool b0 = (v0 >> n) & 1, b1 = (v1 >> n) & 1;   // a masked NaN must not reach the row
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int col = 4 * tx + 64 * c;
+          if (col >= a.d) continue;
+          const float4 v = *reinterpret_cast<const float4*>(sv + n * ldk + col);
+          if (b0) {
+            acc[0][c].x = fmaf(p0, v.x, acc[0][c].x); acc[0][c].y = fmaf(p0, v.y, acc[0][c].y);
+            acc[0][c].z = fmaf(p0, v.z, acc[0][c].z); acc[0][c].w = fmaf(p0, v.w, acc[0][c].w);
+          }
+          if (b1) {
+            acc[1][c].x = fmaf(p1, v.x, acc[1][c].x); acc[1][c].y = fmaf(p1, v.y, acc[1][c].y);
+            acc[1][c].z = fmaf(p1, v.z, acc[1][c].z); acc[1][c].w = fmaf(p1, v.w, acc[1][c].w);
+          }
+        }
+      }
+      __syncthreads();   // sk, sv and page are rewritten
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int m = 2 * ty + r;
+      if (m >= rows) continue;
+      const float l = r == 0 ? l0 : l1, M = r == 0 ? m0 : m1;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float lse2 = l == 0.f ? -INFINITY : M + log2f(l);
+      const int row = it.mt * kSimtRows + m, t = row / a.G, g = row - t * a.G;
+      const size_t out = size_t(it.o + t) * a.H_q + it.h * a.G + g;
+      float* part = nullptr;
+      float* plse = nullptr;
+      if (it.slot >= 0) {
+        part = a.part_o + (size_t(it.slot) * a.part_rows + m) * a.d;
+        plse = a.part_lse + size_t(it.slot) * a.part_rows + m;
+      } else if (it.slot < -1) {
+        const size_t at = size_t(it.slot == -2 ? 0 : 1) * a.N * a.H_q + out;
+        part = a.row_o + at * a.d;
+        plse = a.row_lse + at;
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int col = 4 * tx + 64 * c;
+        if (col >= a.d) continue;
+        const float4 v = make_float4(acc[r][c].x * inv, acc[r][c].y * inv, acc[r][c].z * inv, acc[r][c].w * inv);
+        if (part) *reinterpret_cast<float4*>(part + col) = v;
+        else store4(static_cast<T*>(a.o) + out * a.d + col, v);
+      }
+      if (tx == 0) {
+        if (plse) *plse = lse2;
+        else if (a.lse) a.lse[out] = lse2 * 0.6931471805599453f;
+      }
+    }
+    __syncthreads();   // the item and the rows' words are rewritten
+  }
+}
+
+// ------------------------------------------------------------------------------ merge
+// CTA (r, h, z): rows 32 z .. 32 z + 31 of request r under KV head h, a warp per row, a lane for columns
+// 4 lane + 128 c.  A row's pieces: those of its request's own unit and, for a member of a group, those of
+// the group's unit, in stream order, so that the sum does not depend on who ran when.  Requests whose
+// units were not cut and that have no group have been written already.  Bound by its loads' latency when
+// there are few rows, by the pieces' bytes when there are many.
+constexpr int kMergeRows = 32;
+
+struct Pieces {
+  int np, ca, slot0;        // np = 1: not cut
+  long long unit;
+};
+__device__ __forceinline__ Pieces pieces_of(const Dev& a, const Entry& e, long long ebeg, long long total, int C, int h, int mt) {
+  const long long hc = head_cost(a, e);
+  const int np = a.pairing ? e.mts >> 1 : 0;
+  const bool pair = mt < 2 * np;
+  const int w = pair ? kPairCost : kSingleCost;
+  const long long ucost = (long long)w * e.nt;
+  const long long ubeg = ebeg + h * hc + (pair ? (mt >> 1) * ucost : (long long)np * kPairCost * e.nt + (mt - 2 * np) * ucost);
+  Pieces p;
+  p.ca = range_of(ubeg, total, C);
+  p.np = range_of(ubeg + ucost - w, total, C) - p.ca + 1;
+  p.slot0 = 2 * p.ca + (ubeg > range_start(total, C, p.ca) ? 1 : 0);
+  p.unit = ubeg;
+  return p;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) span_merge_kernel(Dev a) {
+  pdl_wait();
+  pdl_trigger();
+  const int r = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int bad;
+  const Entry own = entry_of(a, a.group_offset, a.Gn + r, bad);
+  const int nrows = own.T * a.G;
+  if (own.mts == 0 || int(blockIdx.z) * kMergeRows >= nrows) return;
+  const long long total = a.ebeg[a.Gn + a.B];
+  const int C = ranges(a, total);
+  const int g = own.group < -1 ? -2 - own.group : -1;
+  const long long obeg = a.ebeg[a.Gn + r];
+  Entry grp;
+  long long gbeg = 0;
+  if (g >= 0) {
+    grp = entry_of(a, a.group_offset, g, bad);
+    gbeg = a.ebeg[g];
+  }
+  for (int m = int(blockIdx.z) * kMergeRows + warp; m < min(nrows, (int(blockIdx.z) + 1) * kMergeRows); m += 8) {
+    const int mt = m / a.rt;
+    const Pieces po = pieces_of(a, own, obeg, total, C, h, mt);
+    if (g < 0 && po.np < 2) continue;
+    const int t = m / a.G;
+    const size_t out = size_t(own.o + t) * a.H_q + h * a.G + (m - t * a.G);
+    Pieces pg = po;
+    int gm = 0, gmt = 0;
+    if (g >= 0) {
+      gm = (own.o - grp.o) * a.G + m;
+      gmt = gm / a.rt;
+      pg = pieces_of(a, grp, gbeg, total, C, h, gmt);
+    }
+    // row of a piece's slot: the second tile of a pair lies behind the first
+    const int oc = m - mt * a.rt + ((a.pairing && (mt & 1)) ? a.part_rows / 2 : 0);
+    const int gc = gm - gmt * a.rt + ((a.pairing && (gmt & 1)) ? a.part_rows / 2 : 0);
+    const int ng = g >= 0 ? pg.np : 0, n = ng + po.np;
+    auto where = [&](int p, const float*& o, const float*& l) {
+      const bool isg = p < ng;
+      const Pieces& x = isg ? pg : po;
+      const int k = isg ? p : p - ng;
+      if (x.np == 1) {
+        const size_t at = size_t(isg ? 0 : 1) * a.N * a.H_q + out;
+        o = a.row_o + at * a.d;
+        l = a.row_lse + at;
+      } else {
+        const size_t at = size_t(k == 0 ? x.slot0 : 2 * (x.ca + k)) * a.part_rows + (isg ? gc : oc);
+        o = a.part_o + at * a.d;
+        l = a.part_lse + at;
+      }
+    };
+    // lane p holds the log2-sum-exp of pieces p, p + 32, ..
+    float M = -INFINITY;
+    for (int p = lane; p < n; p += 32) {
+      const float *o, *l;
+      where(p, o, l);
+      M = fmaxf(M, *l);
+    }
+    M = warp_max(M);
+    float sum = 0.f;
+    float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    for (int p = 0; p < n; ++p) {
+      const float *o, *l;
+      where(p, o, l);
+      const float L = *l;
+      if (L == -INFINITY) continue;        // nothing visible in this piece (M may be -inf as well)
+      const float wt = exp2f(L - M);
+      sum += wt;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int col = 4 * lane + 128 * c;
+        if (col < a.d) {
+          const float4 v = *reinterpret_cast<const float4*>(o + col);
+          acc[c].x = fmaf(wt, v.x, acc[c].x); acc[c].y = fmaf(wt, v.y, acc[c].y);
+          acc[c].z = fmaf(wt, v.z, acc[c].z); acc[c].w = fmaf(wt, v.w, acc[c].w);
+        }
+      }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int col = 4 * lane + 128 * c;
+      if (col < a.d)
+        store4(static_cast<T*>(a.o) + out * a.d + col,
+               make_float4(acc[c].x * inv, acc[c].y * inv, acc[c].z * inv, acc[c].w * inv));
+    }
+    if (lane == 0 && a.lse) a.lse[out] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
+  }
+}
+
+// ------------------------------------------------------------------------------ host
+// What the two calls have in common.
+struct Args {
+  const spec_attn_params* p;
+  const int32_t* group_offset;
+  const int32_t* shared_len;
+  int num_groups, window, sinks;
+};
+
+bool tc_takes(const spec_attn_params* p);
+int tc_row_tile(const spec_attn_params* p);
+spec_status_t launch_span_tc(const spec_attn_params* p, Dev d, cudaStream_t s);
+
+static spec_status_t check(const Args& x) {
+  const spec_attn_params* p = x.p;
+  if (p->dtype != SPEC_F32 && p->dtype != SPEC_BF16) return SPEC_ERR_INVALID_ARG;
+  if (p->B < 1 || p->N < 0 || p->T_max < 1 || p->T_max > SPEC_MAX_TREE) return SPEC_ERR_INVALID_ARG;
+  if (p->H_q < 1 || p->H_kv < 1 || p->H_q % p->H_kv || p->head_dim < 1 || p->block_size < 1 ||
+      p->num_blocks < 1 || p->max_blocks_per_req < 1)
+    return SPEC_ERR_INVALID_ARG;
+  if (!(p->scale == p->scale) || isinf(p->scale)) return SPEC_ERR_INVALID_ARG;
+  if (!p->block_table || !p->prefix_len || !p->node_offset || !p->req_status)
+    return SPEC_ERR_INVALID_ARG;
+  if (p->N > 0 && (!p->q || !p->k_cache || !p->v_cache || !p->o || !p->anc_mask))
+    return SPEC_ERR_INVALID_ARG;
+  if (p->N > 0 && (!aligned16(p->q) || !aligned16(p->k_cache) || !aligned16(p->v_cache) ||
+                   !aligned16(p->o)))
+    return SPEC_ERR_INVALID_ARG;
+  const int es = p->dtype == SPEC_BF16 ? 2 : 4;
+  if ((p->head_dim * es) % 16) return SPEC_ERR_INVALID_ARG;
+  if (p->head_dim > 256) return SPEC_ERR_UNSUPPORTED;
+  if ((long long)p->num_blocks * p->H_kv * p->block_size + 256 >= (1LL << 31)) return SPEC_ERR_UNSUPPORTED;
+  if ((long long)p->N * p->H_q >= (1LL << 31) || p->H_kv > 65535) return SPEC_ERR_UNSUPPORTED;
+  return SPEC_OK;
+}
+
+struct Plan {
+  bool tc;
+  int ctas, rt, bn, part_rows;
+  size_t ebeg, part_o, part_lse, row_o, row_lse, total;
+};
+
+static Plan plan(const Args& x) {
+  const spec_attn_params* p = x.p;
+  Plan w;
+  w.tc = tc_takes(p);
+  const int sms = sm_count_current_device();
+  if (w.tc) {
+    w.ctas = sms;
+    w.rt = tc_row_tile(p);
+    w.bn = 128;
+    w.part_rows = 256;
+  } else {
+    w.ctas = sms * (p->head_dim <= 64 ? 3 : p->head_dim <= 128 ? 2 : 1);   // resident at once
+    w.rt = kSimtRows;
+    w.bn = kSimtKeys;
+    w.part_rows = kSimtRows;
+  }
+  if (w.ctas > kMaxCtas) w.ctas = kMaxCtas;
+  const size_t d = size_t(p->head_dim), rows = size_t(p->N) * p->H_q;
+  size_t off = 0;
+  w.ebeg = off; off = align_up(off + sizeof(long long) * (size_t(x.num_groups) + p->B + 1), 256);
+  w.part_o = off; off = align_up(off + sizeof(float) * 2 * w.ctas * w.part_rows * d, 256);
+  w.part_lse = off; off = align_up(off + sizeof(float) * 2 * w.ctas * w.part_rows, 256);
+  w.row_o = w.row_lse = off;
+  if (x.num_groups > 0) {
+    w.row_o = off; off = align_up(off + sizeof(float) * 2 * rows * d, 256);
+    w.row_lse = off; off = align_up(off + sizeof(float) * 2 * rows, 256);
+  }
+  w.total = off;
+  return w;
+}
+
+static spec_status_t launch(const Args& x, void* ws, size_t ws_bytes, cudaStream_t s) {
+  const spec_attn_params* p = x.p;
+  const Plan w = plan(x);
+  if (w.ctas <= 0) return SPEC_ERR_CUDA;
+  if (!ws || ws_bytes < w.total || (reinterpret_cast<uintptr_t>(ws) & 255u)) return SPEC_ERR_INVALID_ARG;
+  char* base = static_cast<char*>(ws);
+  Dev d;
+  d.block_table = p->block_table;
+  d.prefix_len = p->prefix_len;
+  d.node_offset = p->node_offset;
+  d.anc = p->anc_mask;
+  d.group_offset = x.group_offset;
+  d.shared_len = x.shared_len;
+  d.q = p->q; d.k = p->k_cache; d.v = p->v_cache; d.o = p->o;
+  d.lse = p->lse;
+  d.req_status = p->req_status;
+  d.ebeg = reinterpret_cast<long long*>(base + w.ebeg);
+  d.part_o = reinterpret_cast<float*>(base + w.part_o);
+  d.part_lse = reinterpret_cast<float*>(base + w.part_lse);
+  d.row_o = reinterpret_cast<float*>(base + w.row_o);
+  d.row_lse = reinterpret_cast<float*>(base + w.row_lse);
+  d.B = p->B; d.N = p->N; d.Gn = x.num_groups; d.H_q = p->H_q; d.H_kv = p->H_kv; d.G = p->H_q / p->H_kv;
+  d.d = p->head_dim; d.bs = p->block_size; d.T_max = p->T_max; d.W = (p->T_max + 31) / 32;
+  d.num_blocks = p->num_blocks; d.max_blocks = p->max_blocks_per_req; d.ctas = w.ctas;
+  d.window = x.window; d.sinks = x.sinks;
+  d.rt = w.rt; d.bn = w.bn; d.part_rows = w.part_rows; d.pairing = w.tc ? 1 : 0;
+  const float scale = p->scale > 0.f ? p->scale : 1.f / sqrtf(float(p->head_dim));
+  d.scale_log2 = scale * 1.4426950408889634f;
+  const bool bf16 = p->dtype == SPEC_BF16;
+  spec_status_t st;
+  if (w.tc) {
+    st = launch_span_tc(p, d, s);
+  } else {
+    static DeviceOnce raised_f32, raised_bf16;
+    st = bf16 ? raise_dyn_smem_once(span_simt_kernel<__nv_bfloat16>, simt_smem(256), raised_bf16)
+              : raise_dyn_smem_once(span_simt_kernel<float>, simt_smem(256), raised_f32);
+    if (st == SPEC_OK)
+      st = launch_result(launch_pdl(bf16 ? span_simt_kernel<__nv_bfloat16> : span_simt_kernel<float>,
+                                    dim3(w.ctas), dim3(kSimtThreads), size_t(simt_smem(p->head_dim)), s, d));
+  }
+  if (st != SPEC_OK) return st;
+  const long long rows = (long long)p->T_max * d.G;
+  const unsigned z = unsigned((rows + kMergeRows - 1) / kMergeRows);
+  return launch_result(launch_pdl(bf16 ? span_merge_kernel<__nv_bfloat16> : span_merge_kernel<float>,
+                                  dim3(p->B, p->H_kv, z), dim3(256), 0, s, d));
+}
+
+static bool window_args(const spec_attn_window_params* p, Args& x) {
+  if (!p || p->window < 1 || p->sinks < 0) return false;
+  x = Args{&p->attn, nullptr, nullptr, 0, p->window, p->sinks};
+  return true;
+}
+static bool shared_args(const spec_attn_shared_params* p, Args& x) {
+  if (!p || p->num_groups < 1 || p->num_groups > p->attn.B || !p->group_offset || !p->shared_len) return false;
+  x = Args{&p->attn, p->group_offset, p->shared_len, p->num_groups, 0, 0};
+  return true;
+}
+
+}  // namespace span
+}  // namespace spec
+
+extern "C" {
+
+size_t spec_attention_window_workspace_size(const spec_attn_window_params* p) {
+  spec::span::Args x;
+  if (!spec::span::window_args(p, x) || spec::span::check(x) != SPEC_OK) return 0;
+  return spec::span::plan(x).total;
+}
+
+spec_status_t spec_tree_attention_window(const spec_attn_window_params* p, void* workspace,
+                                         size_t ws_bytes, spec_stream_t stream) {
+  spec::span::Args x;
+  if (!spec::span::window_args(p, x)) return SPEC_ERR_INVALID_ARG;
+  const spec_status_t st = spec::span::check(x);
+  if (st != SPEC_OK || p->attn.N == 0) return st;
+  return spec::span::launch(x, workspace, ws_bytes, (cudaStream_t)stream);
+}
+
+size_t spec_attention_shared_workspace_size(const spec_attn_shared_params* p) {
+  spec::span::Args x;
+  if (!spec::span::shared_args(p, x) || spec::span::check(x) != SPEC_OK) return 0;
+  return spec::span::plan(x).total;
+}
+
+spec_status_t spec_tree_attention_shared(const spec_attn_shared_params* p, void* workspace,
+                                         size_t ws_bytes, spec_stream_t stream) {
+  spec::span::Args x;
+  if (!spec::span::shared_args(p, x)) return SPEC_ERR_INVALID_ARG;
+  const spec_status_t st = spec::span::check(x);
+  if (st != SPEC_OK || p->attn.N == 0) return st;
+  return spec::span::launch(x, workspace, ws_bytes, (cudaStream_t)stream);
+}
+
+}  // extern "C"
