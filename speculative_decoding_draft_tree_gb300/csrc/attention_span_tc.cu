@@ -1,9 +1,789 @@
+// spec_tree_attention_shared and spec_tree_attention_window on the tcgen05 tensor cores: bf16, head_dim 128.
+//
+// A unit is one or two tiles of 128 query rows (G heads x 128 / G tokens) under a KV head; the rows of a
+// group's members lie in one unit, which is what a shared prefix gains: its keys and values meet full
+// tiles, and are read once for 256 rows.  Tiles are 128 x 128 in S = Q K^T and O += P V; per row tile and
+// key tile the two products take 1024 clocks of the tensor pipe (8192 flop a clock and SM), the
+// exponentials 512 of theirs at 32 results a clock, and the operands' reads from shared memory 768 (Q and K
+// for S, V alone for O since P is read from TMEM).  So two row tiles ("slots") alternate: while the
+// products of one run, the other's softmax does.
+//   pair unit    slot s has row tile s, both read every key tile;
+//   single unit  the slots take the key tiles in turn, and the epilogue joins their halves.
+// CTA (384 threads):
+//   warp 0  Q and K by TMA (three stages of K), warp 2 V (two stages): 128-byte-swizzled boxes of a page,
+//           or of all of a tile's pages when they follow one another; pages that no row sees come as zeros;
+//   warp 1  one thread issues PV_0(k) QK_0(k+1) PV_1(k) QK_1(k+1) ..; P_s lies over S_s in TMEM, which the
+//           issue order protects; PV starts on the first 64 keys while the softmax still writes the rest;
+//   warp 3  walks the CTA's range and hands the items to the others through a ring;
+//   warps 4-7 and 8-11  softmax of slot 0 and 1, a row per thread with all 128 scores in registers; the
+//           reference moves when the maximum has grown by more than 2^8, and only then is O rescaled.
+// P is rounded to bf16, V's type, which the product wants; the sum takes the unrounded weights.
+//
+// Masked tiles (a window's edges, a tree, a last tile): masked scores become -inf before anything is
+// formed from them.  Of V, whose product with a weight of zero would be NaN, the softmax warps look at the
+// tile in shared memory first: rows that no query row sees are cleared, infinities and NaN elsewhere are
+// taken out and put into the weights of the rows that see their key.
+//
+// Waits are bounded; one that runs out raises the CTA's abort flag, every role leaves, TMEM is freed, and
+// the requests of the CTA's range get SPEC_REQ_TIMEOUT.
+#include <cudaTypedefs.h>
+#include <math.h>
+
+#include <mutex>
+
 #include "attention_span.cuh"
+#include "tc_ptx.cuh"
 
 namespace spec {
 namespace span {
-bool tc_takes(const spec_attn_params*) { return false; }
-int tc_row_tile(const spec_attn_params*) { return 128; }
-spec_status_t launch_span_tc(const spec_attn_params*, Dev, cudaStream_t) { return SPEC_ERR_UNSUPPORTED; }
+
+constexpr int kD = 128;
+constexpr int kRows = 128;                    // rows of an MMA tile
+constexpr int kKeys = 128;
+constexpr int kThreads = 384;
+constexpr int kAtom = 16384;                  // 128 rows x 128 B
+constexpr int kTile = 2 * kAtom;
+constexpr int kKStages = 3;
+constexpr int kVStages = 2;
+constexpr int kItems = 4;                     // item ring
+constexpr int kSmemK = 2 * kTile;             // Q: one tile per slot
+constexpr int kSmemV = kSmemK + kKStages * kTile;
+constexpr int kSmemCtl = kSmemV + kVStages * kTile;
+constexpr int kCtlRegs = 96, kSoftmaxRegs = 200;   // setmaxnreg: warps 0-3, warps 4-11
+static_assert(kCtlRegs * 128 + kSoftmaxRegs * 256 <= kThreads * 168, "register split fits the launch");
+constexpr long long kWaitLimit = 4000000000LL;     // clock cycles (~2 s)
+constexpr float kLazy = 8.0f;                      // log2 units
+
+struct Control {
+  uint64_t q_full[2], q_empty[2];
+  uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
+  uint64_t s_full[2], p_full[2][2], o_full[2], o_free[2];
+  uint64_t exchange[4], vfix[3];                   // vfix: slot 0, slot 1, both
+  uint64_t item_full[kItems], item_empty[kItems], drain;
+  Item item[kItems];
+  uint32_t vbad[2][2][4];                          // tile parity, slot, 32 keys each: V not finite
+  uint32_t tmem;
+  int abort;
+  float row[2][2][kRows];                          // slot, (reference, sum)
+};
+constexpr int kSmemBytes = kSmemCtl + int(sizeof(Control));
+static_assert(kSmemBytes <= 232448, "fits one CTA's shared memory");
+static_assert(sizeof(RangeScratch) <= size_t(kSmemCtl), "the range's scratch lies in the tiles");
+
+// One lane waits (bounded), the warp gets the outcome.
+__device__ __forceinline__ bool lane0_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  bool r = true;
+  if ((threadIdx.x & 31) == 0) r = tc::mbar_wait(bar, parity, abort, kWaitLimit);
+  return __shfl_sync(0xffffffffu, r ? 1 : 0, 0) != 0;
+}
+// all lanes wait; the outcome is uniform, so that warp-wide TMEM accesses are made by all or none
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const bool ok = tc::mbar_wait(bar, parity, abort, kWaitLimit);
+  return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(a), "f"(b));
+  return r;
+}
+// maximum of 32 values by three-input maxima
+__device__ __forceinline__ float max32(const uint32_t (&x)[32]) {
+  float m[11];
+#pragma unroll
+  for (int c = 0; c < 10; ++c)
+    m[c] = fmax3(__uint_as_float(x[3 * c]), __uint_as_float(x[3 * c + 1]), __uint_as_float(x[3 * c + 2]));
+  m[10] = fmaxf(__uint_as_float(x[30]), __uint_as_float(x[31]));
+  return fmaxf(fmax3(fmax3(m[0], m[1], m[2]), fmax3(m[3], m[4], m[5]), fmax3(m[6], m[7], m[8])),
+               fmaxf(m[9], m[10]));
+}
+// 32 weights 2^(x sl + add), summed in pairs into `acc`, as 16 columns of bf16 pairs in TMEM at `dst`
+__device__ __forceinline__ void weights32(const uint32_t (&x)[32], uint64_t sl, uint64_t add, uint64_t& acc,
+                                          uint32_t dst) {
+  uint32_t pk[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float y0, y1;
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sl, add), y0, y1);
+    const float p0 = ex2(y0), p1 = ex2(y1);
+    acc = f2_add(acc, f2_pack(p0, p1));
+    pk[i] = pack_bf16(p0, p1);
+  }
+  tc::tmem_st16(dst, pk);
+}
+// the same where V is not finite at the keys of `bad` (which the row sees): their weights become NaN in
+// the product, and stay what they are in the sum
+__device__ __forceinline__ void weights32_bad(const uint32_t (&x)[32], uint64_t sl, uint64_t add, uint64_t& acc,
+                                              uint32_t dst, uint32_t bad) {
+  uint32_t pk[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float y0, y1;
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sl, add), y0, y1);
+    const float p0 = ex2(y0), p1 = ex2(y1);
+    acc = f2_add(acc, f2_pack(p0, p1));
+    pk[i] = pack_bf16((bad >> (2 * i)) & 1u ? NAN : p0, (bad >> (2 * i + 1)) & 1u ? NAN : p1);
+  }
+  tc::tmem_st16(dst, pk);
+}
+
+// bits 0 .. n - 1
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+// keys lo .. hi - 1 as bits of the 32 keys from key0 on
+__device__ __forceinline__ uint32_t keys_in(int key0, int lo, int hi) {
+  return below(hi - key0) & ~below(lo - key0);
+}
+// 32 bits of a row's ancestor words from tree index `pos` on (which may be negative)
+__device__ __forceinline__ uint32_t anc_bits(const uint32_t* row, int W, int pos) {
+  if (pos <= -32 || pos >= 32 * W) return 0u;
+  const int wi = pos >= 0 ? (pos >> 5) : -1;
+  const int sh = pos - 32 * wi;
+  const uint32_t lo = wi >= 0 ? __ldg(row + wi) : 0u;
+  const uint32_t hi = (sh != 0 && wi + 1 < W) ? __ldg(row + wi + 1) : 0u;
+  return sh == 0 ? lo : ((lo >> sh) | (hi << (32 - sh)));
+}
+
+// What a query row sees of its request.
+struct RowView {
+  const uint32_t* anc;    // its ancestor words (unused without a tree)
+  int lo;                 // prefix keys from here on
+  int first, sunk;        // window: ancestors of these depths are out of it / are sinks
+};
+
+// The row's visible keys among the 32 from key0 on.
+__device__ __forceinline__ uint32_t visible32(const Dev& a, const RowView& v, int key0, int P, int end) {
+  uint32_t w = keys_in(key0, v.lo, P);
+  if (a.window > 0) w |= keys_in(key0, 0, min(a.sinks, P));
+  if (key0 + 32 > P && end > P) {
+    uint32_t t = anc_bits(v.anc, a.W, key0 - P) & keys_in(key0, P, end);
+    if (v.first > 0 && t) {       // of the row's ancestors, in order of depth, the last `window` and the sinks
+      int k = 0;
+      const int pos = key0 - P;
+      for (int i = 0; i < a.W && 32 * i < pos; ++i) k += __popc(__ldg(v.anc + i) & below(pos - 32 * i));
+      uint32_t keep = 0;
+      for (uint32_t x = t; x; ++k) {
+        const uint32_t b = x & (0u - x);
+        if (k >= v.first || k < v.sunk) keep |= b;
+        x ^= b;
+      }
+      t = keep;
+    }
+    w |= t;
+  }
+  return w;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mQs,
+               const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
+               const __grid_constant__ CUtensorMap mKt, const __grid_constant__ CUtensorMap mVt, Dev a,
+               int q_tokens, int qs_tokens, int kv_rows) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* sQ = smem;
+  uint8_t* sK = smem + kSmemK;
+  uint8_t* sV = smem + kSmemV;
+  Control& c = *reinterpret_cast<Control*>(smem + kSmemCtl);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait();
+  pdl_trigger();
+  const Range R = cta_range<kThreads>(a, *reinterpret_cast<RangeScratch*>(smem));
+  if (R.t0 >= R.t1) return;       // uniform: no work, nothing allocated yet
+  if (tid == 0) {
+    for (int s = 0; s < 2; ++s) {
+      tc::mbar_init(&c.q_full[s], 1);
+      tc::mbar_init(&c.q_empty[s], 1);
+      tc::mbar_init(&c.s_full[s], 1);
+      tc::mbar_init(&c.p_full[s][0], 4);
+      tc::mbar_init(&c.p_full[s][1], 4);
+      tc::mbar_init(&c.o_full[s], 1);
+      tc::mbar_init(&c.o_free[s], 8);
+      tc::mbar_init(&c.vfix[s], 4);
+    }
+    tc::mbar_init(&c.vfix[2], 8);
+    for (int s = 0; s < kKStages; ++s) {
+      tc::mbar_init(&c.k_full[s], 1);
+      tc::mbar_init(&c.k_empty[s], 1);
+    }
+    for (int s = 0; s < kVStages; ++s) {
+      tc::mbar_init(&c.v_full[s], 1);
+      tc::mbar_init(&c.v_empty[s], 1);
+    }
+    for (int q = 0; q < 4; ++q) tc::mbar_init(&c.exchange[q], 2);
+    for (int i = 0; i < kItems; ++i) {
+      tc::mbar_init(&c.item_full[i], 1);
+      tc::mbar_init(&c.item_empty[i], 11);        // warps 0, 1, 2 and the eight of the softmax
+    }
+    tc::mbar_init(&c.drain, 1);
+    c.abort = (tc::smem_u32(smem) & 1023u) ? 1 : 0;      // the swizzle wants 1024-byte bounds
+    tc::fence_mbar_init();
+  }
+  if (warp == 0) {
+    tc::tmem_alloc(&c.tmem, 512);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
+  // the range's scratch was read and written through the generic proxy where TMA writes next
+  tc::fence_proxy_async_smem();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = c.tmem;
+  volatile int* abort_flag = &c.abort;
+  const bool layout_ok = *abort_flag == 0;
+  int ni = 0;                     // items taken so far
+  // the next item, copied; one lane of the warp gives the ring's slot back
+  auto take = [&](Item& it, bool one_lane) -> bool {
+    const int s = ni % kItems;
+    if (one_lane) {
+      if (!tc::mbar_wait(&c.item_full[s], (ni / kItems) & 1, abort_flag, kWaitLimit)) return false;
+    } else if (!warp_wait(&c.item_full[s], (ni / kItems) & 1, abort_flag)) {
+      return false;
+    }
+    it = c.item[s];
+    if (!one_lane) __syncwarp();
+    if (one_lane || lane == 0) tc::mbar_arrive(&c.item_empty[s]);
+    ++ni;
+    return true;
+  };
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtlRegs));
+    if (layout_ok && warp == 3) {
+      // ===================================================================== items
+      if (lane == 0) {
+        Walker w;
+        w.start(a, R);
+        Item it;
+        bool more = true, ok = true;
+        for (int n = 0; more && ok; ++n) {
+          more = w.next(a, R, it);
+          if (!more) it.j0 = it.j1 = -1;
+          const int s = n % kItems;
+          if (n >= kItems) ok = tc::mbar_wait(&c.item_empty[s], (n / kItems - 1) & 1, abort_flag, kWaitLimit);
+          if (ok) {
+            c.item[s] = it;
+            tc::mbar_arrive(&c.item_full[s]);
+          }
+        }
+        if (!ok) *abort_flag = 1;
+      }
+    } else if (layout_ok && (warp == 0 || warp == 2)) {
+      // ===================================================================== TMA producers
+      const bool is_k = warp == 0;
+      const CUtensorMap* page_map = is_k ? &mK : &mV;
+      const CUtensorMap* tile_map = is_k ? &mKt : &mVt;
+      if (lane == 0) {
+        tc::prefetch_tensormap(page_map);
+        tc::prefetch_tensormap(tile_map);
+        if (is_k) {
+          tc::prefetch_tensormap(&mQ);
+          tc::prefetch_tensormap(&mQs);
+        }
+      }
+      const int nstage = is_k ? kKStages : kVStages;
+      uint8_t* ring = is_k ? sK : sV;
+      uint64_t* full = is_k ? c.k_full : c.v_full;
+      uint64_t* empty = is_k ? c.k_empty : c.v_empty;
+      const int npg = kKeys / a.bs, page_bytes = a.bs * 128;
+      int kt = 0, qn[2] = {0, 0};
+      bool ok = true;
+      Item it;
+      while (ok) {
+        ok = take(it, false);
+        if (!ok || it.j1 < 0) break;
+        const int32_t* table = a.block_table + size_t(it.table) * a.max_blocks;
+        // the physical page of this lane's page of tile j: -1 if no row sees it (read as zeros), -2 if bad
+        auto tile_page = [&](int j) -> int {
+          if (lane >= npg) return -1;
+          const int first = key_base(a, it.nt0, it.w0, j) + lane * a.bs;
+          if (!page_needed(first, a.bs, it.lo, it.sink, it.end)) return -1;
+          const int pb = table[first / a.bs];
+          if (pb >= 0 && pb < a.num_blocks) return pb;
+          flag(a, it.req, it.nreq, SPEC_REQ_BAD_BLOCK);
+          return -2;
+        };
+        int pb = tile_page(it.j0);
+        if (is_k) {
+          const bool grp = it.end == it.P;
+          const int tokens = grp ? q_tokens : qs_tokens;
+          for (int b = 0; ok && b <= it.pair; ++b) {
+            if (qn[b] > 0) ok = lane0_wait(&c.q_empty[b], (qn[b] - 1) & 1, abort_flag);
+            if (!ok) break;
+            if (lane == 0) {
+              tc::mbar_arrive_expect_tx(&c.q_full[b], 2 * tokens * a.G * 128);
+              const int tok = it.o + (it.mt + b) * q_tokens;
+              uint8_t* dst = sQ + b * kTile;
+              if (grp) {
+                tc::tma_load_3d(dst, &mQ, 0, it.h * a.G, tok, &c.q_full[b]);
+                tc::tma_load_3d(dst + kAtom, &mQ, 64, it.h * a.G, tok, &c.q_full[b]);
+              } else {
+                tc::tma_load_3d(dst, &mQs, 0, it.h * a.G, tok, &c.q_full[b]);
+                tc::tma_load_3d(dst + kAtom, &mQs, 64, it.h * a.G, tok, &c.q_full[b]);
+              }
+            }
+            ++qn[b];
+          }
+        }
+        for (int j = it.j0; ok && j < it.j1; ++j, ++kt) {
+          const int ahead = j + 1 < it.j1 ? tile_page(j + 1) : -1;
+          const int st = kt % nstage, use = kt / nstage;
+          if (use > 0) ok = lane0_wait(&empty[st], (use - 1) & 1, abort_flag);
+          if (!ok) break;
+          const int pb0 = __shfl_sync(0xffffffffu, pb, 0);
+          const bool run = __all_sync(0xffffffffu, lane >= npg || pb == pb0 + lane) && pb0 >= 0;
+          if (lane == 0) tc::mbar_arrive_expect_tx(&full[st], kTile);
+          __syncwarp();
+          uint8_t* dst = ring + st * kTile;
+          if (run) {
+            if (lane == 0) {
+              tc::tma_load_4d(dst, tile_map, 0, 0, it.h, pb0, &full[st]);
+              tc::tma_load_4d(dst + kAtom, tile_map, 64, 0, it.h, pb0, &full[st]);
+            }
+          } else if (lane < npg) {
+            const int row = pb >= 0 ? (pb * a.H_kv + it.h) * a.bs : kv_rows;      // past the cache: zeros
+            tc::tma_load_2d(dst + lane * page_bytes, page_map, 0, row, &full[st]);
+            tc::tma_load_2d(dst + kAtom + lane * page_bytes, page_map, 64, row, &full[st]);
+          }
+          __syncwarp();
+          pb = ahead;
+        }
+      }
+      if (lane == 0) {
+        if (!ok) *abort_flag = 1;
+        // no copy may be in flight when the CTA ends
+        volatile int never = 0;
+        for (int k = max(0, kt - nstage); k < kt; ++k)
+          tc::mbar_wait(&full[k % nstage], (k / nstage) & 1, &never, kWaitLimit / 8);
+        for (int b = 0; is_k && b < 2; ++b)
+          if (qn[b] > 0) tc::mbar_wait(&c.q_full[b], (qn[b] - 1) & 1, &never, kWaitLimit / 8);
+      }
+    } else if (layout_ok && warp == 1 && lane == 0) {
+      // ===================================================================== MMA issuer
+      const uint32_t id_qk = tc::idesc_bf16_f32(128, 128, false, false);
+      const uint32_t id_pv = tc::idesc_bf16_f32(128, 128, false, true);
+      // descriptors of the first Q buffer, K stage and V stage; the others' lie kTile / 16 apart
+      const uint64_t dQ0 = tc::smem_desc(tc::smem_u32(sQ), 16, 1024), dK0 = tc::smem_desc(tc::smem_u32(sK), 16, 1024);
+      const uint64_t dV0 = tc::smem_desc(tc::smem_u32(sV), kAtom, 1024);
+      constexpr uint64_t kStep = kTile >> 4;
+      int g0 = 0, qn0 = 0, qn1 = 0, pn0 = 0, pn1 = 0, li = 0;
+      bool ok = true;
+      Item it;
+      for (; ok; ++li) {
+        ok = take(it, true);
+        if (!ok || it.j1 < 0) break;
+        const int nt = it.j1 - it.j0;
+        const bool pair = it.pair != 0;
+        const int n0 = pair ? nt : (nt + 1) >> 1, n1 = pair ? nt : nt >> 1;
+        ok = tc::mbar_wait(&c.q_full[0], qn0++ & 1, abort_flag, kWaitLimit);
+        if (ok && pair) ok = tc::mbar_wait(&c.q_full[1], qn1++ & 1, abort_flag, kWaitLimit);
+        if (!ok) break;
+        int qk_left = n0 + n1;
+        auto issue_qk = [&](int s, int k) -> bool {
+          const int g = g0 + (pair ? k : 2 * k + s), st = g % kKStages;
+          if (!tc::mbar_wait(&c.k_full[st], (g / kKStages) & 1, abort_flag, kWaitLimit)) return false;
+          tc::tc_fence_after();
+          const uint64_t dq = dQ0 + (pair ? s : 0) * kStep, dk = dK0 + uint64_t(st) * kStep;
+          uint64_t da[8], db[8];      // formed before the first product, so that the eight go back to back
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint64_t off = uint64_t(((kk >> 2) * kAtom + (kk & 3) * 32) >> 4);
+            da[kk] = dq + off;
+            db[kk] = dk + off;
+          }
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) tc::mma_bf16_ss(tmem + 128 * s, da[kk], db[kk], id_qk, kk > 0 ? 1u : 0u);
+          tc::mma_commit(&c.s_full[s]);
+          if (!pair || s == 1) tc::mma_commit(&c.k_empty[st]);     // the stage's last reader
+          if (--qk_left == 0) {
+            tc::mma_commit(&c.q_empty[0]);
+            if (pair) tc::mma_commit(&c.q_empty[1]);
+          }
+          return true;
+        };
+        auto issue_pv = [&](int s, int k, bool last) -> bool {
+          const int g = g0 + (pair ? k : 2 * k + s), st = g % kVStages;
+          int& pn = s == 0 ? pn0 : pn1;
+          if (!tc::mbar_wait(&c.p_full[s][0], pn & 1, abort_flag, kWaitLimit)) return false;
+          if (!tc::mbar_wait(&c.v_full[st], (g / kVStages) & 1, abort_flag, kWaitLimit)) return false;
+          // an item's first product overwrites O_s: the epilogue before has to have read it
+          if (k == 0 && li > 0 && !tc::mbar_wait(&c.o_free[s], (li - 1) & 1, abort_flag, kWaitLimit)) return false;
+          tc::tc_fence_after();
+          const uint32_t tO = tmem + 256 + 128 * s, tP = tmem + 128 * s + 64;
+          const uint64_t dv = dV0 + uint64_t(st) * kStep;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc::mma_bf16_ts(tO, tP + 8 * kk, dv + uint64_t(kk * (2048 >> 4)), id_pv, kk > 0 || k > 0 ? 1u : 0u);
+          if (!tc::mbar_wait(&c.p_full[s][1], pn & 1, abort_flag, kWaitLimit)) return false;
+          tc::tc_fence_after();
+#pragma unroll
+          for (int kk = 4; kk < 8; ++kk)
+            tc::mma_bf16_ts(tO, tP + 8 * kk, dv + uint64_t(kk * (2048 >> 4)), id_pv, 1u);
+          if (!pair || s == 1) tc::mma_commit(&c.v_empty[st]);
+          if (last) tc::mma_commit(&c.o_full[s]);
+          ++pn;
+          return true;
+        };
+        if (n0 > 0) ok = issue_qk(0, 0);
+        if (ok && n1 > 0) ok = issue_qk(1, 0);
+        for (int k = 0; ok && k < n0; ++k) {
+          ok = issue_pv(0, k, k + 1 == n0);
+          if (ok && k + 1 < n0) ok = issue_qk(0, k + 1);
+          if (ok && k < n1) {
+            ok = issue_pv(1, k, k + 1 == n1);
+            if (ok && k + 1 < n1) ok = issue_qk(1, k + 1);
+          }
+        }
+        g0 += nt;
+      }
+      if (!ok) *abort_flag = 1;
+      // TMEM may not be freed under a product: wait for all of them, also after an abort
+      tc::mma_commit(&c.drain);
+      volatile int never = 0;
+      tc::mbar_wait(&c.drain, 0, &never, kWaitLimit / 8);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    if (layout_ok) {
+      // ===================================================================== softmax, epilogue
+      const int s = (warp - 4) >> 2, q4 = warp & 3;
+      const int m = q4 * 32 + lane;                   // row of the slot's tile; also a key of V's check
+      const uint32_t lane_addr = uint32_t(q4 * 32) << 16;
+      const uint32_t tS = tmem + lane_addr + 128 * s, tO = tmem + lane_addr + 256;
+      const int t_loc = m / a.G, g = m - t_loc * a.G;
+      const float sl2 = a.scale_log2;
+      int sn = 0, on[2] = {0, 0}, xn = 0, vn1 = 0, vn2 = 0, g0 = 0;
+      bool ok = true;
+      Item it;
+      while (ok) {
+        ok = take(it, false);
+        if (!ok || it.j1 < 0) break;
+        const int nt = it.j1 - it.j0;
+        const bool pair = it.pair != 0;
+        const int n0 = pair ? nt : (nt + 1) >> 1, n1 = pair ? nt : nt >> 1;
+        const int ns = s == 0 ? n0 : n1;
+        const int t = (it.mt + (pair ? s : 0)) * q_tokens + t_loc;
+        const bool valid = t_loc < q_tokens && t < it.T;
+        const bool live = __any_sync(0xffffffffu, valid);   // else only handshakes and V's check
+        RowView view;
+        view.anc = nullptr;
+        view.lo = it.lo;
+        view.first = view.sunk = 0;
+        if (valid && it.end > it.P) {
+          view.anc = a.anc + size_t(it.o + t) * a.W;
+          if (a.window > 0) {
+            int n = 0;
+            for (int w = 0; w < a.W; ++w) n += __popc(__ldg(view.anc + w));
+            view.first = max(0, n - a.window);
+            view.sunk = max(0, a.sinks - it.P);
+            view.lo = int(min((long long)it.P, max(0LL, (long long)it.P + max(n - 1, 0) - a.window + 1)));
+          }
+        }
+        const int lo_max = a.window > 0 ? int(max(0LL, (long long)it.P + it.T - a.window)) : it.lo;
+        float ref = -INFINITY, l = 0.f;
+        for (int k = 0; k < ns; ++k) {
+          const int ti = pair ? k : 2 * k + s;
+          const int kb = key_base(a, it.nt0, it.w0, it.j0 + ti);
+          const bool masked = !(kb + kKeys <= it.P && (kb >= lo_max || (a.window > 0 && kb + kKeys <= a.sinks)));
+          uint32_t bad[4] = {0, 0, 0, 0};
+          if (!warp_wait(&c.s_full[s], sn & 1, abort_flag)) { ok = false; break; }
+          ++sn;
+          tc::tc_fence_after();
+          if (masked) {
+            // V's rows: thread m looks at key m (both halves of its columns, or one half in each slot).
+            // S of this tile came after the products before, so V's stage holds no older tile that is
+            // still to be read, and the phase waited for is the stage's next.
+            const int gv = g0 + ti, st = gv % kVStages;
+            if (!warp_wait(&c.v_full[st], (gv / kVStages) & 1, abort_flag)) { ok = false; break; }
+            const int key = kb + m;
+            const bool seen = key < it.sink || (key >= it.lo && key < it.end);
+            uint8_t* vrow = sV + st * kTile + (m >> 3) * 1024 + (m & 7) * 128;
+            bool wrong = false;
+            for (int half = pair ? s : 0; half < (pair ? s + 1 : 2); ++half) {
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                uint4* p = reinterpret_cast<uint4*>(vrow + half * kAtom + q * 16);
+                if (!seen) {
+                  *p = make_uint4(0, 0, 0, 0);
+                  continue;
+                }
+                uint4 x = *p;
+                uint32_t* w = &x.x;
+                bool hit = false;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  if ((w[e] & 0x7f80u) == 0x7f80u) { w[e] &= 0xffff0000u; hit = true; }
+                  if ((w[e] & 0x7f800000u) == 0x7f800000u) { w[e] &= 0xffffu; hit = true; }
+                }
+                if (hit) {
+                  *p = x;
+                  wrong = true;
+                }
+              }
+            }
+            tc::fence_proxy_async_smem();
+            const uint32_t word = __ballot_sync(0xffffffffu, wrong);
+            if (lane == 0) c.vbad[k & 1][s][q4] = word;
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&c.vfix[pair ? 2 : s]);
+            int& vn = pair ? vn2 : vn1;
+            if (!warp_wait(&c.vfix[pair ? 2 : s], vn & 1, abort_flag)) { ok = false; break; }
+            ++vn;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) bad[q] = c.vbad[k & 1][s][q] | (pair ? c.vbad[k & 1][1 - s][q] : 0u);
+          }
+          if (live) {
+            uint32_t x0[32], x1[32], x2[32], x3[32];
+            tc::tmem_ld32(tS, x0);
+            tc::tmem_ld32(tS + 32, x1);
+            tc::tmem_ld32(tS + 64, x2);
+            tc::tmem_ld32(tS + 96, x3);
+            tc::tmem_ld_wait();
+            if (masked) {
+              auto hide = [&](uint32_t (&x)[32], int q) {
+                const uint32_t vis = valid ? visible32(a, view, kb + 32 * q, it.P, it.end) : 0u;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = (vis >> i) & 1u ? x[i] : __float_as_uint(-INFINITY);
+                bad[q] &= vis;
+              };
+              hide(x0, 0);
+              hide(x1, 1);
+              hide(x2, 2);
+              hide(x3, 3);
+            }
+            const float mx = fmaxf(fmaxf(max32(x0), max32(x1)), fmaxf(max32(x2), max32(x3))) * sl2;
+            const float top = valid ? mx : -INFINITY;
+            if (__any_sync(0xffffffffu, top > ref + kLazy)) {
+              const bool up = top > ref + kLazy;
+              const float to = up ? top : ref;
+              const float f = up && ref != -INFINITY ? ex2(ref - to) : 1.f;
+              // S of this tile was issued after the product before, which has therefore landed in O
+              if (k > 0) {
+#pragma unroll 1
+                for (int c0 = 0; c0 < kD; c0 += 16) {
+                  uint32_t r[16];
+                  tc::tmem_ld16(tO + 128 * s + c0, r);
+                  tc::tmem_ld_wait();
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+                  tc::tmem_st16(tO + 128 * s + c0, r);
+                }
+              }
+              l *= f;
+              ref = to;
+            }
+            // a row that has seen nothing yet: 2^(x - inf) = 0 for every key (masked: -inf - inf)
+            const float sl = ref == -INFINITY ? 1.f : sl2, add = -INFINITY == ref ? -INFINITY : -ref;
+            const uint64_t slv = f2_pack(sl, sl), addv = f2_pack(add, add);
+            uint64_t acc0 = f2_pack(0.f, 0.f), acc1 = acc0;
+            const bool anybad = masked && __any_sync(0xffffffffu, (bad[0] | bad[1] | bad[2] | bad[3]) != 0u);
+            if (!anybad) {
+              weights32(x0, slv, addv, acc0, tS + 64);
+              weights32(x1, slv, addv, acc1, tS + 80);
+            } else {
+              weights32_bad(x0, slv, addv, acc0, tS + 64, bad[0]);
+              weights32_bad(x1, slv, addv, acc1, tS + 80, bad[1]);
+            }
+            tc::tmem_st_wait();
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&c.p_full[s][0]);
+            if (!anybad) {
+              weights32(x2, slv, addv, acc0, tS + 96);
+              weights32(x3, slv, addv, acc1, tS + 112);
+            } else {
+              weights32_bad(x2, slv, addv, acc0, tS + 96, bad[2]);
+              weights32_bad(x3, slv, addv, acc1, tS + 112, bad[3]);
+            }
+            tc::tmem_st_wait();
+            float r0, r1, r2, r3;
+            f2_unpack(acc0, r0, r1);
+            f2_unpack(acc1, r2, r3);
+            l += (r0 + r1) + (r2 + r3);
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&c.p_full[s][1]);
+          } else {
+            tc::tc_fence_before();
+            if (lane == 0) {
+              tc::mbar_arrive(&c.p_full[s][0]);
+              tc::mbar_arrive(&c.p_full[s][1]);
+            }
+          }
+        }
+        if (!ok) break;
+        // the products whose O this warp reads (both slots' of a single unit)
+        for (int u = 0; ok && u < 2; ++u) {
+          if ((u == 0 ? n0 : n1) == 0) continue;
+          if (u == s || !pair) ok = warp_wait(&c.o_full[u], on[u] & 1, abort_flag);
+          ++on[u];
+        }
+        if (!ok) break;
+        tc::tc_fence_after();
+        float lt = l, M = ref, w0 = 0.f, w1 = 0.f;
+        int c_lo = 0, c_hi = kD;
+        if (!pair) {
+          // exchange (reference, sum) with the other slot's warp of this quarter; 64 columns each
+          c.row[s][0][m] = ref;
+          c.row[s][1][m] = l;
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&c.exchange[q4]);
+          if (!warp_wait(&c.exchange[q4], xn & 1, abort_flag)) { ok = false; break; }
+          ++xn;
+          const float mo = c.row[1 - s][0][m], lo = c.row[1 - s][1][m];
+          const float m0 = s == 0 ? ref : mo, m1 = s == 0 ? mo : ref;
+          M = fmaxf(m0, m1);
+          w0 = m0 != -INFINITY ? ex2(m0 - M) : 0.f;
+          w1 = n1 > 0 && m1 != -INFINITY ? ex2(m1 - M) : 0.f;
+          // a slot that saw nothing but NaN has the reference -inf and the sum NaN
+          lt = (s == 0 ? l : lo) * w0 + (n1 > 0 ? (s == 0 ? lo : l) * w1 : 0.f);
+          c_lo = 64 * s;
+          c_hi = c_lo + 64;
+        }
+        const float inv = lt == 0.f ? 0.f : 1.f / lt;
+        const float lse2 = lt == 0.f ? -INFINITY : M + log2f(lt);
+        if (live) {
+          const size_t out = size_t(it.o + t) * a.H_q + it.h * a.G + g;
+          float* part = nullptr;
+          float* plse = nullptr;
+          if (it.slot >= 0) {
+            const size_t at = size_t(it.slot) * a.part_rows + (pair ? s * kRows : 0) + m;
+            part = a.part_o + at * kD;
+            plse = a.part_lse + at;
+          } else if (it.slot < -1) {
+            const size_t at = size_t(it.slot == -2 ? 0 : 1) * a.N * a.H_q + out;
+            part = a.row_o + at * kD;
+            plse = a.row_lse + at;
+          }
+          __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.o) + out * kD;
+#pragma unroll 1
+          for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
+            uint32_t r[32];
+            float v[32];
+            tc::tmem_ld32(tO + (pair ? 128 * s : 0) + c0, r);
+            tc::tmem_ld_wait();
+            const float wa = pair ? inv : w0 * inv;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = wa == 0.f ? 0.f : __uint_as_float(r[i]) * wa;
+            if (!pair && n1 > 0) {
+              tc::tmem_ld32(tO + 128 + c0, r);
+              tc::tmem_ld_wait();
+              const float wb = w1 * inv;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = wb == 0.f ? v[i] : fmaf(__uint_as_float(r[i]), wb, v[i]);
+            }
+            if (valid) {
+              if (part == nullptr) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                  uint4 w;
+                  w.x = pack_bf16(v[i], v[i + 1]);
+                  w.y = pack_bf16(v[i + 2], v[i + 3]);
+                  w.z = pack_bf16(v[i + 4], v[i + 5]);
+                  w.w = pack_bf16(v[i + 6], v[i + 7]);
+                  *reinterpret_cast<uint4*>(orow + c0 + i) = w;
+                }
+              } else {
+#pragma unroll
+                for (int i = 0; i < 32; i += 4)
+                  *reinterpret_cast<float4*>(part + c0 + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+              }
+            }
+          }
+          if (valid && (pair || s == 0)) {
+            if (plse) *plse = lse2;
+            else if (a.lse) a.lse[out] = lse2 * 0.6931471805599453f;
+          }
+        }
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          tc::mbar_arrive(&c.o_free[0]);
+          tc::mbar_arrive(&c.o_free[1]);
+        }
+        g0 += nt;
+      }
+      if (!ok) *abort_flag = 1;
+    }
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (*abort_flag && tid == 0) {
+    // every request of the range is unreliable after a wait that ran out
+    Walker w;
+    w.start(a, R);
+    Item it;
+    while (w.next(a, R, it)) flag(a, it.req, it.nreq, SPEC_REQ_TIMEOUT);
+  }
+  tc::tc_fence_after();
+  if (warp == 0) tc::tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------------------ host
+static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static std::once_flag once;
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+// Whether the tensor cores take this call: their types and tiles, and row coordinates in 32 bits.
+bool tc_takes(const spec_attn_params* p) {
+  const int G = p->H_q / p->H_kv;
+  return p->dtype == SPEC_BF16 && p->head_dim == kD && G <= kRows &&
+         (p->block_size == 16 || p->block_size == 32 || p->block_size == 64 || p->block_size == 128);
+}
+int tc_row_tile(const spec_attn_params* p) {
+  const int G = p->H_q / p->H_kv;
+  return kRows / G * G;
+}
+
+static bool encode(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, const void* ptr, int rank,
+                   const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapL2promotion l2) {
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(ptr), dims, strides, box, ones,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, l2, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+spec_status_t launch_span_tc(const spec_attn_params* p, Dev d, cudaStream_t s) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return SPEC_ERR_CUDA;
+  const int G = d.G, q_tokens = kRows / G, qs_tokens = p->T_max < q_tokens ? p->T_max : q_tokens;
+  const int kv_rows = p->num_blocks * p->H_kv * p->block_size;      // below 2^31 - 256, checked
+  CUtensorMap mQ, mQs, mK, mV, mKt, mVt;
+  bool ok = true;
+  for (int small = 0; small < 2; ++small) {
+    const cuuint64_t dims[3] = {cuuint64_t(kD), cuuint64_t(p->H_q), cuuint64_t(p->N)};
+    const cuuint64_t strides[2] = {cuuint64_t(kD) * 2, cuuint64_t(p->H_q) * kD * 2};
+    const cuuint32_t box[3] = {64, cuuint32_t(G), cuuint32_t(small ? qs_tokens : q_tokens)};
+    ok = ok && encode(enc, small ? &mQs : &mQ, p->q, 3, dims, strides, box, CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
+  }
+  for (int v = 0; v < 2; ++v) {
+    const void* cache = v ? p->v_cache : p->k_cache;
+    {
+      const cuuint64_t dims[2] = {cuuint64_t(kD), cuuint64_t(kv_rows)};
+      const cuuint64_t strides[1] = {cuuint64_t(kD) * 2};
+      const cuuint32_t box[2] = {64, cuuint32_t(p->block_size)};
+      ok = ok && encode(enc, v ? &mV : &mK, cache, 2, dims, strides, box, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+    }
+    {
+      const cuuint64_t dims[4] = {cuuint64_t(kD), cuuint64_t(p->block_size), cuuint64_t(p->H_kv), cuuint64_t(p->num_blocks)};
+      const cuuint64_t strides[3] = {cuuint64_t(kD) * 2, cuuint64_t(p->block_size) * kD * 2,
+                                     cuuint64_t(p->H_kv) * p->block_size * kD * 2};
+      const cuuint32_t box[4] = {64, cuuint32_t(p->block_size), 1, cuuint32_t(kKeys / p->block_size)};
+      ok = ok && encode(enc, v ? &mVt : &mKt, cache, 4, dims, strides, box, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+    }
+  }
+  if (!ok) return SPEC_ERR_INVALID_ARG;
+  static DeviceOnce raised;
+  const spec_status_t st = raise_dyn_smem_once(span_tc_kernel, kSmemBytes, raised);
+  if (st != SPEC_OK) return st;
+  return launch_result(launch_pdl(span_tc_kernel, dim3(d.ctas), dim3(kThreads), size_t(kSmemBytes), s, mQ, mQs, mK,
+                                  mV, mKt, mVt, d, q_tokens, qs_tokens, kv_rows));
+}
+
 }  // namespace span
 }  // namespace spec
