@@ -23,6 +23,7 @@ constexpr int kSimtKeys = 64;
 
 struct SimtShared {
   RangeScratch scratch;
+  Range range;
   Item item;
   int more;
   int page[kSimtKeys];                 // cache row of a key's page row, -1: not needed
@@ -68,7 +69,12 @@ __global__ void __launch_bounds__(kSimtThreads) span_simt_kernel(Dev a) {
   float* sv = sk + kSimtKeys * ldk;
   pdl_wait();
   pdl_trigger();
-  const Range R = cta_range<kSimtThreads>(a, s.scratch);
+  if (threadIdx.x < 32) {
+    const Range mine = warp_range(a, blockIdx.x, blockIdx.x == 0, s.scratch);
+    if (threadIdx.x == 0) s.range = mine;
+  }
+  __syncthreads();
+  const Range R = s.range;
   if (R.t0 >= R.t1) return;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int d4 = a.d >> 2;
@@ -76,7 +82,7 @@ __global__ void __launch_bounds__(kSimtThreads) span_simt_kernel(Dev a) {
   const T* kc = static_cast<const T*>(a.k);
   const T* vc = static_cast<const T*>(a.v);
   Walker walker;
-  if (tid == 0) walker.start(a, R);
+  if (tid == 0) walker.start(R);
   while (true) {
     if (tid == 0) s.more = walker.next(a, R, s.item) ? 1 : 0;
     __syncthreads();
@@ -278,9 +284,8 @@ constexpr int kMergeRows = 32;
 
 struct Pieces {
   int np, ca, slot0;        // np = 1: not cut
-  long long unit;
 };
-__device__ __forceinline__ Pieces pieces_of(const Dev& a, const Entry& e, long long ebeg, long long total, int C, int h, int mt) {
+__device__ __forceinline__ Pieces pieces_of(const Dev& a, const Entry& e, long long ebeg, const Cut& cut, int h, int mt) {
   const long long hc = head_cost(a, e);
   const int np = a.pairing ? e.mts >> 1 : 0;
   const bool pair = mt < 2 * np;
@@ -288,10 +293,9 @@ __device__ __forceinline__ Pieces pieces_of(const Dev& a, const Entry& e, long l
   const long long ucost = (long long)w * e.nt;
   const long long ubeg = ebeg + h * hc + (pair ? (mt >> 1) * ucost : (long long)np * kPairCost * e.nt + (mt - 2 * np) * ucost);
   Pieces p;
-  p.ca = range_of(ubeg, total, C);
-  p.np = range_of(ubeg + ucost - w, total, C) - p.ca + 1;
-  p.slot0 = 2 * p.ca + (ubeg > range_start(total, C, p.ca) ? 1 : 0);
-  p.unit = ubeg;
+  p.ca = range_of(cut, ubeg);
+  p.np = range_of(cut, ubeg + ucost - w) - p.ca + 1;
+  p.slot0 = 2 * p.ca + (ubeg > range_start(cut, p.ca) ? 1 : 0);
   return p;
 }
 
@@ -304,8 +308,7 @@ __global__ void __launch_bounds__(256) span_merge_kernel(Dev a) {
   const Entry own = entry_of(a, a.group_offset, a.Gn + r, bad);
   const int nrows = own.T * a.G;
   if (own.mts == 0 || int(blockIdx.z) * kMergeRows >= nrows) return;
-  const long long total = a.ebeg[a.Gn + a.B];
-  const int C = ranges(a, total);
+  const Cut cut = cut_of(a, a.ebeg[a.Gn + a.B]);
   const int g = own.group < -1 ? -2 - own.group : -1;
   const long long obeg = a.ebeg[a.Gn + r];
   Entry grp;
@@ -316,7 +319,7 @@ __global__ void __launch_bounds__(256) span_merge_kernel(Dev a) {
   }
   for (int m = int(blockIdx.z) * kMergeRows + warp; m < min(nrows, (int(blockIdx.z) + 1) * kMergeRows); m += 8) {
     const int mt = m / a.rt;
-    const Pieces po = pieces_of(a, own, obeg, total, C, h, mt);
+    const Pieces po = pieces_of(a, own, obeg, cut, h, mt);
     if (g < 0 && po.np < 2) continue;
     const int t = m / a.G;
     const size_t out = size_t(own.o + t) * a.H_q + h * a.G + (m - t * a.G);
@@ -325,7 +328,7 @@ __global__ void __launch_bounds__(256) span_merge_kernel(Dev a) {
     if (g >= 0) {
       gm = (own.o - grp.o) * a.G + m;
       gmt = gm / a.rt;
-      pg = pieces_of(a, grp, gbeg, total, C, h, gmt);
+      pg = pieces_of(a, grp, gbeg, cut, h, gmt);
     }
     // row of a piece's slot: the second tile of a pair lies behind the first
     const int oc = m - mt * a.rt + ((a.pairing && (mt & 1)) ? a.part_rows / 2 : 0);

@@ -20,7 +20,7 @@ namespace span {
 constexpr int kPairCost = 2, kSingleCost = 1;
 constexpr int kMinCost = 8;              // cost of a range at least: small calls use fewer ranges
 constexpr int kMaxCtas = 1024;
-constexpr int kGroupCache = 4096;        // group offsets held in shared memory while ranges are found
+constexpr int kGroupCache = 2048, kCostCache = 1024;   // group offsets, costs held in shared memory
 
 struct Dev {
   const int32_t* block_table;
@@ -160,109 +160,108 @@ __device__ __forceinline__ Entry entry_of(const Dev& a, const int32_t* off, int 
   return e;
 }
 
-__device__ __forceinline__ long long range_start(long long total, int C, int c) { return total * c / C; }
-// the range holding cost position t (0 <= t < total)
-__device__ __forceinline__ int range_of(long long t, long long total, int C) {
-  const long long c = ((t + 1) * C + total - 1) / total - 1;
-  return int(c < 0 ? 0 : (c >= C ? C - 1 : c));
+// The stream of `total` cost units in C ranges: the first `rem` have base + 1 units, the others base.
+struct Cut {
+  long long base;
+  int C, rem;
+};
+__device__ __forceinline__ long long div_ll(long long a, long long b) {     // a, b >= 0
+  return ((a | b) >> 32) == 0 ? (long long)(unsigned(a) / unsigned(b)) : a / b;
 }
-__device__ __forceinline__ int ranges(const Dev& a, long long total) {
-  return int(max(1LL, min((long long)a.ctas, total / kMinCost)));
+__device__ __forceinline__ Cut cut_of(const Dev& a, long long total) {
+  Cut c;
+  c.C = int(max(1LL, min((long long)a.ctas, total / kMinCost)));
+  c.base = div_ll(total, c.C);
+  c.rem = int(total - c.base * c.C);
+  return c;
+}
+__device__ __forceinline__ long long range_start(const Cut& c, int i) { return i * c.base + min(i, c.rem); }
+// the range holding cost position t (0 <= t < total)
+__device__ __forceinline__ int range_of(const Cut& c, long long t) {
+  const long long head = c.rem * (c.base + 1);
+  return t < head ? int(div_ll(t, c.base + 1)) : c.rem + int(div_ll(t - head, max(1LL, c.base)));
 }
 
-// This CTA's share: cost positions [t0, t1), from entry e0, before which the cost is ebeg0.
+// A CTA's share: cost positions [t0, t1), from entry e0, before which the cost is ebeg0.
 struct Range {
-  long long total, t0, t1, ebeg0;
-  int C, e0;
+  long long t0, t1, ebeg0;
+  int e0;
 };
 
-// Scratch of the search; the group offsets are copied here when they fit.
+// Scratch of the search: copies of the group offsets and of the entries' costs, where they fit.
 struct RangeScratch {
-  long long sum[34];
-  long long found_beg;
-  int found;
+  long long cost[kCostCache];
   int32_t off[kGroupCache + 1];
 };
 
-// All kThreads threads find the CTA's range.  CTA 0 also writes ebeg and reports the requests that
-// cannot be worked on.  Contains __syncthreads.
-template <int kThreads>
-__device__ Range cta_range(const Dev& a, RangeScratch& s) {
-  constexpr int kW = kThreads / 32;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int E = a.Gn + a.B;
+// One warp finds range c.  With `report` it goes through all entries, writes ebeg and flags the requests
+// that cannot be worked on.
+__device__ __forceinline__ Range warp_range(const Dev& a, int c, bool report, RangeScratch& s) {
+  const int lane = threadIdx.x & 31, E = a.Gn + a.B;
   const int32_t* off = a.group_offset;
   if (a.Gn > 0 && a.Gn <= kGroupCache) {
-    for (int i = tid; i <= a.Gn; i += kThreads) s.off[i] = a.group_offset[i];
+    for (int i = lane; i <= a.Gn; i += 32) s.off[i] = a.group_offset[i];
+    __syncwarp();
     off = s.off;
-    __syncthreads();
   }
-  auto cost_of = [&](int i) -> long long {
-    if (i >= E) return 0;
-    int bad;
-    const Entry e = entry_of(a, off, i, bad);
-    if (bad && blockIdx.x == 0) atomicOr(&a.req_status[i - a.Gn], bad);
-    return head_cost(a, e) * a.H_kv;
-  };
-  const long long mine0 = cost_of(tid);
-  long long mine = mine0;
-  for (int i = tid + kThreads; i < E; i += kThreads) mine += cost_of(i);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) s.sum[warp] = mine;
-  if (tid == 0) s.found = -1;
-  __syncthreads();
-  long long total = 0;
-#pragma unroll
-  for (int w = 0; w < kW; ++w) total += s.sum[w];
-  if (blockIdx.x == 0 && tid == 0) a.ebeg[E] = total;
   Range R;
-  R.total = total;
-  R.C = ranges(a, total);
   R.t0 = R.t1 = R.ebeg0 = 0;
   R.e0 = 0;
-  const int c = blockIdx.x;
-  const bool work = total > 0 && c < R.C;
-  if (work) {
-    R.t0 = range_start(total, R.C, c);
-    R.t1 = range_start(total, R.C, c + 1);
-  }
-  if (!work && c != 0) return R;
-  long long base = 0;
-  for (int i0 = 0; i0 < E; i0 += kThreads) {
-    const int i = i0 + tid;
-    const long long cost = i0 == 0 ? mine0 : cost_of(i);
-    long long incl = cost;
+  long long sum = 0;            // pass 0: this lane's costs; pass 1: the cost before the chunk
+  bool found = false;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+    for (int i0 = 0; i0 < E; i0 += 32) {
+      const int i = i0 + lane;
+      long long cost = 0;
+      if (pass == 1 && i0 < kCostCache) {
+        cost = s.cost[i];
+      } else if (i < E) {
+        int bad;
+        const Entry e = entry_of(a, off, i, bad);
+        cost = head_cost(a, e) * a.H_kv;
+        if (bad && report && pass == 0) atomicOr(&a.req_status[i - a.Gn], bad);
+      }
+      if (pass == 0) {
+        if (i0 < kCostCache) s.cost[i] = cost;
+        sum += cost;
+        continue;
+      }
+      long long hi = cost;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += x;
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, hi, o);
+        if (lane >= o) hi += x;
+      }
+      hi += sum;
+      const long long lo = hi - cost;
+      if (report && i < E) a.ebeg[i] = lo;
+      const uint32_t here = __ballot_sync(0xffffffffu, cost > 0 && lo <= R.t0 && R.t0 < hi);
+      if (here && !found) {
+        found = true;
+        R.e0 = i0 + __ffs(here) - 1;
+        R.ebeg0 = __shfl_sync(0xffffffffu, lo, __ffs(here) - 1);
+        if (!report) break;
+      }
+      sum = __shfl_sync(0xffffffffu, hi, 31);
     }
-    __syncthreads();   // s.sum is rewritten
-    if (lane == 31) s.sum[warp] = incl;
-    __syncthreads();
-    long long before = base, chunk = 0;
+    if (pass == 0) {
 #pragma unroll
-    for (int w = 0; w < kW; ++w) {
-      if (w < warp) before += s.sum[w];
-      chunk += s.sum[w];
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (report && lane == 0) a.ebeg[E] = sum;
+      const Cut cut = cut_of(a, sum);
+      if (sum > 0 && c < cut.C) {
+        R.t0 = range_start(cut, c);
+        R.t1 = range_start(cut, c + 1);
+      } else if (!report) {
+        break;
+      }
+      sum = 0;
+      __syncwarp();
     }
-    const long long hi = before + incl, lo = hi - cost;
-    if (c == 0 && i < E) a.ebeg[i] = lo;
-    if (work && cost > 0 && lo <= R.t0 && R.t0 < hi) {
-      s.found = i;
-      s.found_beg = lo;
-    }
-    base += chunk;
-    if (c != 0 && base > R.t0) break;   // uniform
   }
-  __syncthreads();
-  if (work) {
-    R.e0 = s.found;
-    R.ebeg0 = s.found_beg;
-    if (R.e0 < 0 || R.e0 >= E) R.t1 = R.t0;   // never: the scan finds the entry
-  }
-  __syncthreads();
+  if (!found) R.t1 = R.t0;      // no work
   return R;
 }
 
@@ -276,58 +275,60 @@ struct Item {
   int pad;
 };
 
-// Walks the CTA's range.  One thread or a whole warp alike.
+// Walks the CTA's range, one thread.
 struct Walker {
-  long long t, ebeg;     // next cost position; cost before the entry
-  int i, bad;
-  long long hcost;
+  long long t, ubeg;     // next cost position; cost before the present unit
+  long long eend;        // cost up to the entry's end
+  int i, h, u, np, units;
   Entry e;
-  const int32_t* off;    // group offsets
-  __device__ __forceinline__ void start(const Dev& a, const Range& R) {
+  __device__ __forceinline__ void start(const Range& R) {
     t = R.t0;
-    i = R.e0;
-    ebeg = R.ebeg0;
-    off = a.group_offset;
-    hcost = 0;
-    if (t < R.t1) {
-      e = entry_of(a, off, i, bad);
-      hcost = head_cost(a, e);
-    }
+    i = R.e0 - 1;
+    eend = R.ebeg0;      // next() enters e0
   }
   __device__ __forceinline__ bool next(const Dev& a, const Range& R, Item& it) {
     while (t < R.t1) {
-      while (t >= ebeg + hcost * a.H_kv) {
-        ebeg += hcost * a.H_kv;
+      while (t >= eend) {
         if (++i >= a.Gn + a.B) return false;
-        e = entry_of(a, off, i, bad);
-        hcost = head_cost(a, e);
+        int bad;
+        e = entry_of(a, a.group_offset, i, bad);
+        const long long hc = head_cost(a, e);
+        ubeg = eend;
+        eend += hc * a.H_kv;
+        np = a.pairing ? e.mts >> 1 : 0;
+        units = units_of(a, e);
+        h = u = 0;
+        if (t > ubeg && t < eend) {          // the range begins inside: the unit that holds t
+          h = int(div_ll(t - ubeg, hc));
+          ubeg += h * hc;
+          const long long pc = (long long)kPairCost * e.nt, sc = (long long)kSingleCost * e.nt, in = t - ubeg;
+          u = in < np * pc ? int(div_ll(in, pc)) : np + int(div_ll(in - np * pc, sc));
+          ubeg += min(u, np) * pc + max(u - np, 0) * sc;
+        }
       }
-      const long long in_entry = t - ebeg;
-      const int h = int(in_entry / hcost);
-      const long long in_head = in_entry - h * hcost;
-      const int np = a.pairing ? e.mts >> 1 : 0;
-      const long long pair_part = (long long)np * kPairCost * e.nt;
-      const bool pair = in_head < pair_part;
-      const int w = pair ? kPairCost : kSingleCost;
-      const long long ucost = (long long)w * e.nt;
-      const int u = int(pair ? in_head / ucost : (in_head - pair_part) / ucost);
-      const long long ubeg = ebeg + h * hcost + (pair ? 0 : pair_part) + u * ucost;
-      const int j0 = int((t - ubeg + w - 1) / w);
-      const int j1 = int(min((long long)e.nt, (R.t1 - ubeg + w - 1) / w));
-      t = min(R.t1, ubeg + ucost);
+      const int w = u < np ? kPairCost : kSingleCost;
+      const long long ucost = (long long)w * e.nt, beg = ubeg;
+      const int j0 = int((t - beg + w - 1) / w);
+      const int j1 = int(min((long long)e.nt, (R.t1 - beg + w - 1) / w));
+      it.h = h;
+      it.pair = u < np ? 1 : 0;
+      it.mt = it.pair ? 2 * u : np + u;
+      t = min(R.t1, beg + ucost);
+      ubeg += ucost;
+      if (++u == units) {
+        u = 0;
+        ++h;
+      }
       if (j1 <= j0) continue;
       it.o = e.o; it.T = e.T; it.P = e.P; it.end = e.end; it.lo = e.lo; it.sink = e.sink;
       it.table = e.table; it.nt0 = e.nt0; it.w0 = e.w0;
-      it.h = h;
-      it.pair = pair ? 1 : 0;
-      it.mt = pair ? 2 * u : 2 * np + u;
       it.j0 = j0;
       it.j1 = j1;
       const bool cut = j0 > 0 || j1 < e.nt;
-      it.slot = cut ? 2 * int(blockIdx.x) + (ubeg > R.t0 ? 1 : 0)
+      it.slot = cut ? 2 * int(blockIdx.x) + (beg > R.t0 ? 1 : 0)
                     : e.group >= 0 ? -2 : e.group == -1 ? -1 : -3;
-      it.req = e.group >= 0 ? off[e.group] : i - a.Gn;
-      it.nreq = e.group >= 0 ? off[e.group + 1] - it.req : 1;
+      it.req = e.group >= 0 ? e.table : i - a.Gn;
+      it.nreq = e.group >= 0 ? a.group_offset[e.group + 1] - it.req : 1;
       return true;
     }
     return false;

@@ -22,7 +22,7 @@
 // Masked tiles (a window's edges, a tree, a last tile): masked scores become -inf before anything is
 // formed from them.  Of V, whose product with a weight of zero would be NaN, the softmax warps look at the
 // tile in shared memory first: rows that no query row sees are cleared, infinities and NaN elsewhere are
-// taken out and put into the weights of the rows that see their key.
+// taken out, and the scores of the rows that see their key become NaN.
 //
 // Waits are bounded; one that runs out raises the CTA's abort flag, every role leaves, TMEM is freed, and
 // the requests of the CTA's range get SPEC_REQ_TIMEOUT.
@@ -43,12 +43,13 @@ constexpr int kKeys = 128;
 constexpr int kThreads = 384;
 constexpr int kAtom = 16384;                  // 128 rows x 128 B
 constexpr int kTile = 2 * kAtom;
-constexpr int kKStages = 3;
+constexpr int kKStages = 2;
 constexpr int kVStages = 2;
 constexpr int kItems = 4;                     // item ring
 constexpr int kSmemK = 2 * kTile;             // Q: one tile per slot
 constexpr int kSmemV = kSmemK + kKStages * kTile;
-constexpr int kSmemCtl = kSmemV + kVStages * kTile;
+constexpr int kSmemOut = kSmemV + kVStages * kTile;     // 4 KB a softmax warp: output rows on their way out
+constexpr int kSmemCtl = kSmemOut + 8 * 4096;
 constexpr int kCtlRegs = 96, kSoftmaxRegs = 200;   // setmaxnreg: warps 0-3, warps 4-11
 static_assert(kCtlRegs * 128 + kSoftmaxRegs * 256 <= kThreads * 168, "register split fits the launch");
 constexpr long long kWaitLimit = 4000000000LL;     // clock cycles (~2 s)
@@ -57,18 +58,19 @@ constexpr float kLazy = 8.0f;                      // log2 units
 struct Control {
   uint64_t q_full[2], q_empty[2];
   uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
-  uint64_t s_full[2], p_full[2][2], o_full[2], o_free[2];
+  uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
   uint64_t exchange[4], vfix[3];                   // vfix: slot 0, slot 1, both
   uint64_t item_full[kItems], item_empty[kItems], drain;
   Item item[kItems];
-  uint32_t vbad[2][2][4];                          // tile parity, slot, 32 keys each: V not finite
+  Range range;
+  alignas(16) uint32_t vbad[2][2][4];                          // tile parity, slot, 32 keys each: V not finite
   uint32_t tmem;
   int abort;
   float row[2][2][kRows];                          // slot, (reference, sum)
 };
 constexpr int kSmemBytes = kSmemCtl + int(sizeof(Control));
 static_assert(kSmemBytes <= 232448, "fits one CTA's shared memory");
-static_assert(sizeof(RangeScratch) <= size_t(kSmemCtl), "the range's scratch lies in the tiles");
+static_assert(2 * sizeof(RangeScratch) <= size_t(kSmemOut), "scratch of two searches lies in the tiles");
 
 // One lane waits (bounded), the warp gets the outcome.
 __device__ __forceinline__ bool lane0_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
@@ -96,34 +98,31 @@ __device__ __forceinline__ float max32(const uint32_t (&x)[32]) {
   return fmaxf(fmax3(fmax3(m[0], m[1], m[2]), fmax3(m[3], m[4], m[5]), fmax3(m[6], m[7], m[8])),
                fmaxf(m[9], m[10]));
 }
-// 32 weights 2^(x sl + add), summed in pairs into `acc`, as 16 columns of bf16 pairs in TMEM at `dst`
+// 32 weights 2^(x sl + add), summed in pairs into `acc`, as 16 columns of bf16 pairs in TMEM at `dst`; with
+// kTwo what the rounding left, rounded again, 64 columns behind
+template <bool kTwo>
 __device__ __forceinline__ void weights32(const uint32_t (&x)[32], uint64_t sl, uint64_t add, uint64_t& acc,
                                           uint32_t dst) {
-  uint32_t pk[16];
+  uint32_t hi[16], lo[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     float y0, y1;
     f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sl, add), y0, y1);
     const float p0 = ex2(y0), p1 = ex2(y1);
     acc = f2_add(acc, f2_pack(p0, p1));
-    pk[i] = pack_bf16(p0, p1);
+    hi[i] = pack_bf16(p0, p1);
+    if constexpr (kTwo) lo[i] = pack_bf16(p0 - bf16_lo(hi[i]), p1 - bf16_hi(hi[i]));
   }
-  tc::tmem_st16(dst, pk);
+  tc::tmem_st16(dst, hi);
+  if constexpr (kTwo) tc::tmem_st16(dst + 64, lo);
 }
-// the same where V is not finite at the keys of `bad` (which the row sees): their weights become NaN in
-// the product, and stay what they are in the sum
-__device__ __forceinline__ void weights32_bad(const uint32_t (&x)[32], uint64_t sl, uint64_t add, uint64_t& acc,
-                                              uint32_t dst, uint32_t bad) {
-  uint32_t pk[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    float y0, y1;
-    f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), sl, add), y0, y1);
-    const float p0 = ex2(y0), p1 = ex2(y1);
-    acc = f2_add(acc, f2_pack(p0, p1));
-    pk[i] = pack_bf16((bad >> (2 * i)) & 1u ? NAN : p0, (bad >> (2 * i + 1)) & 1u ? NAN : p1);
-  }
-  tc::tmem_st16(dst, pk);
+
+// true for one lane of the warp, which the compiler knows to be one (what a lane number would not tell it:
+// the products' operands then stay in uniform registers, and eight of them go out in 130 clocks, not 1000)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 // bits 0 .. n - 1
@@ -132,37 +131,31 @@ __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 
 __device__ __forceinline__ uint32_t keys_in(int key0, int lo, int hi) {
   return below(hi - key0) & ~below(lo - key0);
 }
-// 32 bits of a row's ancestor words from tree index `pos` on (which may be negative)
-__device__ __forceinline__ uint32_t anc_bits(const uint32_t* row, int W, int pos) {
-  if (pos <= -32 || pos >= 32 * W) return 0u;
-  const int wi = pos >= 0 ? (pos >> 5) : -1;
-  const int sh = pos - 32 * wi;
-  const uint32_t lo = wi >= 0 ? __ldg(row + wi) : 0u;
-  const uint32_t hi = (sh != 0 && wi + 1 < W) ? __ldg(row + wi + 1) : 0u;
-  return sh == 0 ? lo : ((lo >> sh) | (hi << (32 - sh)));
-}
-
 // What a query row sees of its request.
 struct RowView {
-  const uint32_t* anc;    // its ancestor words (unused without a tree)
-  int lo;                 // prefix keys from here on
-  int first, sunk;        // window: ancestors of these depths are out of it / are sinks
+  const uint32_t* anc;    // its W ancestor words, null: no tree
+  int W, lo, P, end;      // prefix keys lo .. P - 1, tree keys P .. end - 1
+  int sunk;               // window: prefix keys below
+  int first, deep;        // window: ancestors of depths below `first` are out of it, below `deep` sinks
 };
 
-// The row's visible keys among the 32 from key0 on.
-__device__ __forceinline__ uint32_t visible32(const Dev& a, const RowView& v, int key0, int P, int end) {
-  uint32_t w = keys_in(key0, v.lo, P);
-  if (a.window > 0) w |= keys_in(key0, 0, min(a.sinks, P));
-  if (key0 + 32 > P && end > P) {
-    uint32_t t = anc_bits(v.anc, a.W, key0 - P) & keys_in(key0, P, end);
+// The row's visible keys among the 32 from key0 on.  Not inlined: masked tiles are few, and the code of a
+// tile has to stay in the instruction cache.
+__device__ __noinline__ uint32_t visible32(const RowView& v, int key0) {
+  uint32_t w = keys_in(key0, v.lo, v.P) | keys_in(key0, 0, v.sunk);
+  const int pos = key0 - v.P;
+  if (pos > -32 && pos < 32 * v.W && v.anc != nullptr) {
+    const int wi = pos >= 0 ? (pos >> 5) : -1, sh = pos - 32 * wi;
+    const uint32_t lo = wi >= 0 ? __ldg(v.anc + wi) : 0u;
+    const uint32_t hi = (sh != 0 && wi + 1 < v.W) ? __ldg(v.anc + wi + 1) : 0u;
+    uint32_t t = (sh == 0 ? lo : ((lo >> sh) | (hi << (32 - sh)))) & keys_in(key0, v.P, v.end);
     if (v.first > 0 && t) {       // of the row's ancestors, in order of depth, the last `window` and the sinks
       int k = 0;
-      const int pos = key0 - P;
-      for (int i = 0; i < a.W && 32 * i < pos; ++i) k += __popc(__ldg(v.anc + i) & below(pos - 32 * i));
+      for (int i = 0; i < v.W && 32 * i < pos; ++i) k += __popc(__ldg(v.anc + i) & below(pos - 32 * i));
       uint32_t keep = 0;
       for (uint32_t x = t; x; ++k) {
         const uint32_t b = x & (0u - x);
-        if (k >= v.first || k < v.sunk) keep |= b;
+        if (k >= v.first || k < v.deep) keep |= b;
         x ^= b;
       }
       t = keep;
@@ -182,18 +175,14 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
   uint8_t* sK = smem + kSmemK;
   uint8_t* sV = smem + kSmemV;
   Control& c = *reinterpret_cast<Control*>(smem + kSmemCtl);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_wait();
-  pdl_trigger();
-  const Range R = cta_range<kThreads>(a, *reinterpret_cast<RangeScratch*>(smem));
-  if (R.t0 >= R.t1) return;       // uniform: no work, nothing allocated yet
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  // Warp 3 looks for the CTA's range while the others set up; it publishes items after the barrier below.
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
       tc::mbar_init(&c.q_full[s], 1);
       tc::mbar_init(&c.q_empty[s], 1);
       tc::mbar_init(&c.s_full[s], 1);
-      tc::mbar_init(&c.p_full[s][0], 4);
-      tc::mbar_init(&c.p_full[s][1], 4);
+      tc::mbar_init(&c.p_full[s], 4);
       tc::mbar_init(&c.o_full[s], 1);
       tc::mbar_init(&c.o_free[s], 8);
       tc::mbar_init(&c.vfix[s], 4);
@@ -219,9 +208,24 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
   if (warp == 0) {
     tc::tmem_alloc(&c.tmem, 512);
     tc::tmem_relinquish();
+  } else if (warp == 2 && lane == 0) {
+    tc::prefetch_tensormap(&mQ);
+    tc::prefetch_tensormap(&mQs);
+    tc::prefetch_tensormap(&mK);
+    tc::prefetch_tensormap(&mV);
+    tc::prefetch_tensormap(&mKt);
+    tc::prefetch_tensormap(&mVt);
+  }
+  pdl_wait();
+  pdl_trigger();
+  if (warp == 3) {
+    const Range mine = warp_range(a, blockIdx.x, false, *reinterpret_cast<RangeScratch*>(smem));
+    if (lane == 0) c.range = mine;
+  } else if (blockIdx.x == 0 && warp == 4) {
+    warp_range(a, 0, true, *(reinterpret_cast<RangeScratch*>(smem) + 1));     // for the merge
   }
   tc::tc_fence_before();
-  // the range's scratch was read and written through the generic proxy where TMA writes next
+  // the scratch was read and written through the generic proxy where TMA writes next
   tc::fence_proxy_async_smem();
   __syncthreads();
   tc::tc_fence_after();
@@ -229,27 +233,25 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
   volatile int* abort_flag = &c.abort;
   const bool layout_ok = *abort_flag == 0;
   int ni = 0;                     // items taken so far
-  // the next item, copied; one lane of the warp gives the ring's slot back
-  auto take = [&](Item& it, bool one_lane) -> bool {
-    const int s = ni % kItems;
-    if (one_lane) {
-      if (!tc::mbar_wait(&c.item_full[s], (ni / kItems) & 1, abort_flag, kWaitLimit)) return false;
-    } else if (!warp_wait(&c.item_full[s], (ni / kItems) & 1, abort_flag)) {
-      return false;
-    }
-    it = c.item[s];
+  // Waits for the next item, which stays in the ring until given back.
+  auto take = [&](bool one_lane) -> bool {
+    uint64_t* bar = &c.item_full[ni % kItems];
+    const uint32_t parity = (ni / kItems) & 1;
+    return one_lane ? tc::mbar_wait(bar, parity, abort_flag, kWaitLimit) : warp_wait(bar, parity, abort_flag);
+  };
+  auto give_back = [&](bool one_lane) {
     if (!one_lane) __syncwarp();
-    if (one_lane || lane == 0) tc::mbar_arrive(&c.item_empty[s]);
+    if (one_lane || lane == 0) tc::mbar_arrive(&c.item_empty[ni % kItems]);
     ++ni;
-    return true;
   };
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtlRegs));
     if (layout_ok && warp == 3) {
       // ===================================================================== items
       if (lane == 0) {
+        const Range R = c.range;
         Walker w;
-        w.start(a, R);
+        w.start(R);
         Item it;
         bool more = true, ok = true;
         for (int n = 0; more && ok; ++n) {
@@ -269,14 +271,6 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
       const bool is_k = warp == 0;
       const CUtensorMap* page_map = is_k ? &mK : &mV;
       const CUtensorMap* tile_map = is_k ? &mKt : &mVt;
-      if (lane == 0) {
-        tc::prefetch_tensormap(page_map);
-        tc::prefetch_tensormap(tile_map);
-        if (is_k) {
-          tc::prefetch_tensormap(&mQ);
-          tc::prefetch_tensormap(&mQs);
-        }
-      }
       const int nstage = is_k ? kKStages : kVStages;
       uint8_t* ring = is_k ? sK : sV;
       uint64_t* full = is_k ? c.k_full : c.v_full;
@@ -284,10 +278,11 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
       const int npg = kKeys / a.bs, page_bytes = a.bs * 128;
       int kt = 0, qn[2] = {0, 0};
       bool ok = true;
-      Item it;
       while (ok) {
-        ok = take(it, false);
-        if (!ok || it.j1 < 0) break;
+        ok = take(false);
+        if (!ok || c.item[ni % kItems].j1 < 0) break;
+        const Item it = c.item[ni % kItems];
+        give_back(false);
         const int32_t* table = a.block_table + size_t(it.table) * a.max_blocks;
         // the physical page of this lane's page of tile j: -1 if no row sees it (read as zeros), -2 if bad
         auto tile_page = [&](int j) -> int {
@@ -354,7 +349,7 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
         for (int b = 0; is_k && b < 2; ++b)
           if (qn[b] > 0) tc::mbar_wait(&c.q_full[b], (qn[b] - 1) & 1, &never, kWaitLimit / 8);
       }
-    } else if (layout_ok && warp == 1 && lane == 0) {
+    } else if (layout_ok && warp == 1 && elect_one()) {
       // ===================================================================== MMA issuer
       const uint32_t id_qk = tc::idesc_bf16_f32(128, 128, false, false);
       const uint32_t id_pv = tc::idesc_bf16_f32(128, 128, false, true);
@@ -364,12 +359,13 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
       constexpr uint64_t kStep = kTile >> 4;
       int g0 = 0, qn0 = 0, qn1 = 0, pn0 = 0, pn1 = 0, li = 0;
       bool ok = true;
-      Item it;
       for (; ok; ++li) {
-        ok = take(it, true);
+        ok = take(true);
+        const Item& it = c.item[ni % kItems];
         if (!ok || it.j1 < 0) break;
         const int nt = it.j1 - it.j0;
         const bool pair = it.pair != 0;
+        give_back(true);
         const int n0 = pair ? nt : (nt + 1) >> 1, n1 = pair ? nt : nt >> 1;
         ok = tc::mbar_wait(&c.q_full[0], qn0++ & 1, abort_flag, kWaitLimit);
         if (ok && pair) ok = tc::mbar_wait(&c.q_full[1], qn1++ & 1, abort_flag, kWaitLimit);
@@ -400,21 +396,21 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
         auto issue_pv = [&](int s, int k, bool last) -> bool {
           const int g = g0 + (pair ? k : 2 * k + s), st = g % kVStages;
           int& pn = s == 0 ? pn0 : pn1;
-          if (!tc::mbar_wait(&c.p_full[s][0], pn & 1, abort_flag, kWaitLimit)) return false;
+          if (!tc::mbar_wait(&c.p_full[s], pn & 1, abort_flag, kWaitLimit)) return false;
           if (!tc::mbar_wait(&c.v_full[st], (g / kVStages) & 1, abort_flag, kWaitLimit)) return false;
           // an item's first product overwrites O_s: the epilogue before has to have read it
           if (k == 0 && li > 0 && !tc::mbar_wait(&c.o_free[s], (li - 1) & 1, abort_flag, kWaitLimit)) return false;
           tc::tc_fence_after();
-          const uint32_t tO = tmem + 256 + 128 * s, tP = tmem + 128 * s + 64;
+          const uint32_t tO = tmem + 256 + 128 * s, tP = tmem + 128 * s;
           const uint64_t dv = dV0 + uint64_t(st) * kStep;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
+          for (int kk = 0; kk < 8; ++kk)
             tc::mma_bf16_ts(tO, tP + 8 * kk, dv + uint64_t(kk * (2048 >> 4)), id_pv, kk > 0 || k > 0 ? 1u : 0u);
-          if (!tc::mbar_wait(&c.p_full[s][1], pn & 1, abort_flag, kWaitLimit)) return false;
-          tc::tc_fence_after();
+          if (!pair) {
 #pragma unroll
-          for (int kk = 4; kk < 8; ++kk)
-            tc::mma_bf16_ts(tO, tP + 8 * kk, dv + uint64_t(kk * (2048 >> 4)), id_pv, 1u);
+            for (int kk = 0; kk < 8; ++kk)
+              tc::mma_bf16_ts(tO, tP + 64 + 8 * kk, dv + uint64_t(kk * (2048 >> 4)), id_pv, 1u);
+          }
           if (!pair || s == 1) tc::mma_commit(&c.v_empty[st]);
           if (last) tc::mma_commit(&c.o_full[s]);
           ++pn;
@@ -446,15 +442,15 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
       const int m = q4 * 32 + lane;                   // row of the slot's tile; also a key of V's check
       const uint32_t lane_addr = uint32_t(q4 * 32) << 16;
       const uint32_t tS = tmem + lane_addr + 128 * s, tO = tmem + lane_addr + 256;
-      const int t_loc = m / a.G, g = m - t_loc * a.G;
+      const int t_loc = m / a.G;
       const float sl2 = a.scale_log2;
       int sn = 0, on[2] = {0, 0}, xn = 0, vn1 = 0, vn2 = 0, g0 = 0;
       bool ok = true;
-      Item it;
       while (ok) {
-        ok = take(it, false);
+        ok = take(false);
+        const Item& it = c.item[ni % kItems];
         if (!ok || it.j1 < 0) break;
-        const int nt = it.j1 - it.j0;
+        const int nt = it.j1 - it.j0, j0 = it.j0, nt0 = it.nt0, skip = it.w0 - it.nt0, P = it.P;
         const bool pair = it.pair != 0;
         const int n0 = pair ? nt : (nt + 1) >> 1, n1 = pair ? nt : nt >> 1;
         const int ns = s == 0 ? n0 : n1;
@@ -463,70 +459,86 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
         const bool live = __any_sync(0xffffffffu, valid);   // else only handshakes and V's check
         RowView view;
         view.anc = nullptr;
+        view.W = a.W;
         view.lo = it.lo;
-        view.first = view.sunk = 0;
-        if (valid && it.end > it.P) {
+        view.P = P;
+        view.end = it.end;
+        view.sunk = min(a.sinks, P);
+        view.first = view.deep = 0;
+        if (valid && it.end > P) {
           view.anc = a.anc + size_t(it.o + t) * a.W;
           if (a.window > 0) {
             int n = 0;
             for (int w = 0; w < a.W; ++w) n += __popc(__ldg(view.anc + w));
             view.first = max(0, n - a.window);
-            view.sunk = max(0, a.sinks - it.P);
-            view.lo = int(min((long long)it.P, max(0LL, (long long)it.P + max(n - 1, 0) - a.window + 1)));
+            view.deep = max(0, a.sinks - P);
+            view.lo = int(min((long long)P, max(0LL, (long long)P + max(n - 1, 0) - a.window + 1)));
           }
         }
-        const int lo_max = a.window > 0 ? int(max(0LL, (long long)it.P + it.T - a.window)) : it.lo;
-        float ref = -INFINITY, l = 0.f;
+        if (!valid) view.lo = view.P = view.end = view.sunk = 0;
+        const int lo_max = a.window > 0 ? int(max(0LL, (long long)P + it.T - a.window)) : it.lo;
+        float ref = -INFINITY, l = 0.f;        // P_s is scaled by 2^-ref, O_s and l with it
         for (int k = 0; k < ns; ++k) {
-          const int ti = pair ? k : 2 * k + s;
-          const int kb = key_base(a, it.nt0, it.w0, it.j0 + ti);
-          const bool masked = !(kb + kKeys <= it.P && (kb >= lo_max || (a.window > 0 && kb + kKeys <= a.sinks)));
-          uint32_t bad[4] = {0, 0, 0, 0};
+          const int ti = pair ? k : 2 * k + s, j = j0 + ti;
+          const int kb = (j < nt0 ? j : j + skip) * kKeys;
+          const bool masked = !(kb + kKeys <= P && (kb >= lo_max || kb + kKeys <= a.sinks));
+          uint32_t vis0 = ~0u, vis1 = ~0u, vis2 = ~0u, vis3 = ~0u;
+          if (masked && live) {
+            vis0 = visible32(view, kb);
+            vis1 = visible32(view, kb + 32);
+            vis2 = visible32(view, kb + 64);
+            vis3 = visible32(view, kb + 96);
+          }
           if (!warp_wait(&c.s_full[s], sn & 1, abort_flag)) { ok = false; break; }
           ++sn;
           tc::tc_fence_after();
+          bool nan = false;        // the row sees a key whose V is not finite
           if (masked) {
-            // V's rows: thread m looks at key m (both halves of its columns, or one half in each slot).
+            // V's rows, 32 a warp, eight lanes a row (of a pair unit one half of the columns in each slot).
             // S of this tile came after the products before, so V's stage holds no older tile that is
             // still to be read, and the phase waited for is the stage's next.
             const int gv = g0 + ti, st = gv % kVStages;
             if (!warp_wait(&c.v_full[st], (gv / kVStages) & 1, abort_flag)) { ok = false; break; }
-            const int key = kb + m;
-            const bool seen = key < it.sink || (key >= it.lo && key < it.end);
-            uint8_t* vrow = sV + st * kTile + (m >> 3) * 1024 + (m & 7) * 128;
-            bool wrong = false;
+            uint8_t* tile = sV + st * kTile + (q4 * 32 + (lane >> 3)) * 128 + (lane & 7) * 16;
+            uint32_t word = 0;
+            bool wrote = false;
             for (int half = pair ? s : 0; half < (pair ? s + 1 : 2); ++half) {
-#pragma unroll
-              for (int q = 0; q < 8; ++q) {
-                uint4* p = reinterpret_cast<uint4*>(vrow + half * kAtom + q * 16);
-                if (!seen) {
-                  *p = make_uint4(0, 0, 0, 0);
-                  continue;
-                }
+#pragma unroll 4
+              for (int i = 0; i < 8; ++i) {
+                const int key = kb + q4 * 32 + 4 * i + (lane >> 3);
+                uint4* p = reinterpret_cast<uint4*>(tile + half * kAtom + i * 512);
                 uint4 x = *p;
-                uint32_t* w = &x.x;
+                const bool seen = key < it.sink || (key >= it.lo && key < it.end);
                 bool hit = false;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  if ((w[e] & 0x7f80u) == 0x7f80u) { w[e] &= 0xffff0000u; hit = true; }
-                  if ((w[e] & 0x7f800000u) == 0x7f800000u) { w[e] &= 0xffffu; hit = true; }
-                }
-                if (hit) {
+                auto clean = [&](uint32_t& w) {
+                  if ((w & 0x7f80u) == 0x7f80u) { w &= 0xffff0000u; hit = true; }
+                  if ((w & 0x7f800000u) == 0x7f800000u) { w &= 0xffffu; hit = true; }
+                };
+                clean(x.x);
+                clean(x.y);
+                clean(x.z);
+                clean(x.w);
+                if (!seen) x = make_uint4(0, 0, 0, 0);
+                if (hit || !seen) {
                   *p = x;
-                  wrong = true;
+                  wrote = true;
+                }
+                const uint32_t hits = __ballot_sync(0xffffffffu, hit && seen);
+                if (hits) {
+                  for (int r = 0; r < 4; ++r) word |= ((hits >> (8 * r)) & 0xffu) ? 1u << (4 * i + r) : 0u;
                 }
               }
             }
-            tc::fence_proxy_async_smem();
-            const uint32_t word = __ballot_sync(0xffffffffu, wrong);
+            if (wrote) tc::fence_proxy_async_smem();
             if (lane == 0) c.vbad[k & 1][s][q4] = word;
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&c.vfix[pair ? 2 : s]);
             int& vn = pair ? vn2 : vn1;
             if (!warp_wait(&c.vfix[pair ? 2 : s], vn & 1, abort_flag)) { ok = false; break; }
             ++vn;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) bad[q] = c.vbad[k & 1][s][q] | (pair ? c.vbad[k & 1][1 - s][q] : 0u);
+            const uint4 b0 = *reinterpret_cast<const uint4*>(c.vbad[k & 1][s]);
+            const uint4 b1 = *reinterpret_cast<const uint4*>(c.vbad[k & 1][pair ? 1 - s : s]);
+            nan = (((b0.x | b1.x) & vis0) | ((b0.y | b1.y) & vis1) | ((b0.z | b1.z) & vis2) | ((b0.w | b1.w) & vis3)) != 0u;
           }
           if (live) {
             uint32_t x0[32], x1[32], x2[32], x3[32];
@@ -536,23 +548,19 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
             tc::tmem_ld32(tS + 96, x3);
             tc::tmem_ld_wait();
             if (masked) {
-              auto hide = [&](uint32_t (&x)[32], int q) {
-                const uint32_t vis = valid ? visible32(a, view, kb + 32 * q, it.P, it.end) : 0u;
+              auto hide = [&](uint32_t (&x)[32], uint32_t vis) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) x[i] = (vis >> i) & 1u ? x[i] : __float_as_uint(-INFINITY);
-                bad[q] &= vis;
               };
-              hide(x0, 0);
-              hide(x1, 1);
-              hide(x2, 2);
-              hide(x3, 3);
+              hide(x0, vis0);
+              hide(x1, vis1);
+              hide(x2, vis2);
+              hide(x3, vis3);
             }
-            const float mx = fmaxf(fmaxf(max32(x0), max32(x1)), fmaxf(max32(x2), max32(x3))) * sl2;
-            const float top = valid ? mx : -INFINITY;
+            const float top = valid ? fmaxf(fmaxf(max32(x0), max32(x1)), fmaxf(max32(x2), max32(x3))) * sl2 : -INFINITY;
             if (__any_sync(0xffffffffu, top > ref + kLazy)) {
               const bool up = top > ref + kLazy;
-              const float to = up ? top : ref;
-              const float f = up && ref != -INFINITY ? ex2(ref - to) : 1.f;
+              const float f = up && ref != -INFINITY ? ex2(ref - top) : 1.f;
               // S of this tile was issued after the product before, which has therefore landed in O
               if (k > 0) {
 #pragma unroll 1
@@ -566,46 +574,33 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
                 }
               }
               l *= f;
-              ref = to;
+              ref = up ? top : ref;
             }
             // a row that has seen nothing yet: 2^(x - inf) = 0 for every key (masked: -inf - inf)
-            const float sl = ref == -INFINITY ? 1.f : sl2, add = -INFINITY == ref ? -INFINITY : -ref;
+            const float sl = ref == -INFINITY ? 1.f : sl2;
+            const float add = nan ? NAN : ref == -INFINITY ? -INFINITY : -ref;
             const uint64_t slv = f2_pack(sl, sl), addv = f2_pack(add, add);
             uint64_t acc0 = f2_pack(0.f, 0.f), acc1 = acc0;
-            const bool anybad = masked && __any_sync(0xffffffffu, (bad[0] | bad[1] | bad[2] | bad[3]) != 0u);
-            if (!anybad) {
-              weights32(x0, slv, addv, acc0, tS + 64);
-              weights32(x1, slv, addv, acc1, tS + 80);
+            if (pair) {
+              weights32<false>(x0, slv, addv, acc0, tS);
+              weights32<false>(x1, slv, addv, acc1, tS + 16);
+              weights32<false>(x2, slv, addv, acc0, tS + 32);
+              weights32<false>(x3, slv, addv, acc1, tS + 48);
             } else {
-              weights32_bad(x0, slv, addv, acc0, tS + 64, bad[0]);
-              weights32_bad(x1, slv, addv, acc1, tS + 80, bad[1]);
+              weights32<true>(x0, slv, addv, acc0, tS);
+              weights32<true>(x1, slv, addv, acc1, tS + 16);
+              weights32<true>(x2, slv, addv, acc0, tS + 32);
+              weights32<true>(x3, slv, addv, acc1, tS + 48);
             }
-            tc::tmem_st_wait();
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&c.p_full[s][0]);
-            if (!anybad) {
-              weights32(x2, slv, addv, acc0, tS + 96);
-              weights32(x3, slv, addv, acc1, tS + 112);
-            } else {
-              weights32_bad(x2, slv, addv, acc0, tS + 96, bad[2]);
-              weights32_bad(x3, slv, addv, acc1, tS + 112, bad[3]);
-            }
-            tc::tmem_st_wait();
             float r0, r1, r2, r3;
             f2_unpack(acc0, r0, r1);
             f2_unpack(acc1, r2, r3);
             l += (r0 + r1) + (r2 + r3);
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&c.p_full[s][1]);
-          } else {
-            tc::tc_fence_before();
-            if (lane == 0) {
-              tc::mbar_arrive(&c.p_full[s][0]);
-              tc::mbar_arrive(&c.p_full[s][1]);
-            }
+            tc::tmem_st_wait();
           }
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&c.p_full[s]);
         }
         if (!ok) break;
         // the products whose O this warp reads (both slots' of a single unit)
@@ -639,19 +634,17 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
         const float inv = lt == 0.f ? 0.f : 1.f / lt;
         const float lse2 = lt == 0.f ? -INFINITY : M + log2f(lt);
         if (live) {
-          const size_t out = size_t(it.o + t) * a.H_q + it.h * a.G + g;
-          float* part = nullptr;
-          float* plse = nullptr;
-          if (it.slot >= 0) {
-            const size_t at = size_t(it.slot) * a.part_rows + (pair ? s * kRows : 0) + m;
-            part = a.part_o + at * kD;
-            plse = a.part_lse + at;
-          } else if (it.slot < -1) {
-            const size_t at = size_t(it.slot == -2 ? 0 : 1) * a.N * a.H_q + out;
-            part = a.row_o + at * kD;
-            plse = a.row_lse + at;
-          }
-          __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.o) + out * kD;
+          // Rows leave through shared memory, 32 columns at a time, so that a store is of whole lines: row r's
+          // 16-byte unit u lies at u ^ (r & 7).
+          uint8_t* stage = smem + kSmemOut + (warp - 4) * 4096;
+          const bool direct = it.slot == -1;
+          const int nv = __popc(__ballot_sync(0xffffffffu, valid));    // the warp's rows 0 .. nv - 1
+          const size_t slot_row = size_t(max(it.slot, 0)) * a.part_rows + (pair ? s * kRows : 0);
+          // where this lane's row of 128 columns begins, in elements of its buffer
+          const size_t row_of = size_t(it.o + t) * a.H_q + it.h * a.G + (m - t_loc * a.G);
+          const unsigned long long mine = (it.slot >= 0 ? slot_row + m : row_of) * kD;
+          float* rows = it.slot >= 0 ? a.part_o : it.slot == -3 ? a.row_o + size_t(a.N) * a.H_q * kD : a.row_o;
+          const int shift = direct ? 2 : 3;                            // 4 or 8 units a row
 #pragma unroll 1
           for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
             uint32_t r[32];
@@ -668,27 +661,39 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = wb == 0.f ? v[i] : fmaf(__uint_as_float(r[i]), wb, v[i]);
             }
-            if (valid) {
-              if (part == nullptr) {
+            if (direct) {
 #pragma unroll
-                for (int i = 0; i < 32; i += 8) {
-                  uint4 w;
-                  w.x = pack_bf16(v[i], v[i + 1]);
-                  w.y = pack_bf16(v[i + 2], v[i + 3]);
-                  w.z = pack_bf16(v[i + 4], v[i + 5]);
-                  w.w = pack_bf16(v[i + 6], v[i + 7]);
-                  *reinterpret_cast<uint4*>(orow + c0 + i) = w;
-                }
-              } else {
+              for (int u = 0; u < 4; ++u) {
+                uint4 w;
+                w.x = pack_bf16(v[8 * u], v[8 * u + 1]);
+                w.y = pack_bf16(v[8 * u + 2], v[8 * u + 3]);
+                w.z = pack_bf16(v[8 * u + 4], v[8 * u + 5]);
+                w.w = pack_bf16(v[8 * u + 6], v[8 * u + 7]);
+                *reinterpret_cast<uint4*>(stage + lane * 128 + ((u ^ (lane & 7)) << 4)) = w;
+              }
+            } else {
 #pragma unroll
-                for (int i = 0; i < 32; i += 4)
-                  *reinterpret_cast<float4*>(part + c0 + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+              for (int u = 0; u < 8; ++u)
+                *reinterpret_cast<float4*>(stage + lane * 128 + ((u ^ (lane & 7)) << 4)) =
+                    make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+            }
+            __syncwarp();
+            const int u = lane & ((1 << shift) - 1);
+            for (int r0 = 0; r0 < nv; r0 += 32 >> shift) {
+              const int row = r0 + (lane >> shift);
+              const unsigned long long at = __shfl_sync(0xffffffffu, mine, row);
+              const uint4 w = *reinterpret_cast<const uint4*>(stage + row * 128 + ((u ^ (row & 7)) << 4));
+              if (row < nv) {
+                if (direct) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + at + c0 + 8 * u) = w;
+                else *reinterpret_cast<uint4*>(rows + at + c0 + 4 * u) = w;
               }
             }
+            __syncwarp();
           }
           if (valid && (pair || s == 0)) {
-            if (plse) *plse = lse2;
-            else if (a.lse) a.lse[out] = lse2 * 0.6931471805599453f;
+            if (it.slot >= 0) a.part_lse[slot_row + m] = lse2;
+            else if (!direct) a.row_lse[(it.slot == -3 ? size_t(a.N) * a.H_q : 0) + row_of] = lse2;
+            else if (a.lse) a.lse[row_of] = lse2 * 0.6931471805599453f;
           }
         }
         tc::tc_fence_before();
@@ -697,6 +702,7 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
           tc::mbar_arrive(&c.o_free[0]);
           tc::mbar_arrive(&c.o_free[1]);
         }
+        give_back(false);
         g0 += nt;
       }
       if (!ok) *abort_flag = 1;
@@ -706,8 +712,9 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
   __syncthreads();
   if (*abort_flag && tid == 0) {
     // every request of the range is unreliable after a wait that ran out
+    const Range R = c.range;
     Walker w;
-    w.start(a, R);
+    w.start(R);
     Item it;
     while (w.next(a, R, it)) flag(a, it.req, it.nreq, SPEC_REQ_TIMEOUT);
   }
