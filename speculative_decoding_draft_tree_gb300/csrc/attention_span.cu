@@ -70,7 +70,8 @@ __global__ void __launch_bounds__(kSimtThreads) span_simt_kernel(Dev a) {
   pdl_wait();
   pdl_trigger();
   if (threadIdx.x < 32) {
-    const Range mine = warp_range(a, blockIdx.x, blockIdx.x == 0, s.scratch);
+    const Range mine = warp_range(a, blockIdx.x, s.scratch);
+    if (reports(mine, gridDim.x)) write_recs(a, s.scratch);
     if (threadIdx.x == 0) s.range = mine;
   }
   __syncthreads();
@@ -275,119 +276,156 @@ __global__ void __launch_bounds__(kSimtThreads) span_simt_kernel(Dev a) {
 }
 
 // ------------------------------------------------------------------------------ merge
-// CTA (r, h, z): rows 32 z .. 32 z + 31 of request r under KV head h, a warp per row, a lane for columns
-// 4 lane + 128 c.  A row's pieces: those of its request's own unit and, for a member of a group, those of
-// the group's unit, in stream order, so that the sum does not depend on who ran when.  Requests whose
-// units were not cut and that have no group have been written already.  Bound by its loads' latency when
-// there are few rows, by the pieces' bytes when there are many.
-constexpr int kMergeRows = 32;
+// CTA (r, h, z): rows 8 kR z .. 8 kR (z + 1) - 1 of request r under KV head h, kR rows a warp.  A row's
+// pieces: for a member of a group those of the group's unit, then those of its request's own unit, in stream
+// order, so that the sum does not depend on who ran when.  Rows of requests on their own whose unit was
+// not cut have been written already.  Lane kR p + i holds the weight and the place of piece p (of 32 / kR at
+// a time) of row i, and eight vectors are loaded together: bound by latency (record, log-sum-exps, values)
+// when there are few rows (a row a warp then), by the pieces' bytes when there are many (two).
+constexpr int kMergeFew = 16;        // rows of a request and head up to which a warp takes one row
 
 struct Pieces {
   int np, ca, slot0;        // np = 1: not cut
 };
-__device__ __forceinline__ Pieces pieces_of(const Dev& a, const Entry& e, long long ebeg, const Cut& cut, int h, int mt) {
-  const long long hc = head_cost(a, e);
+__device__ __forceinline__ Pieces pieces_of(const Dev& a, const Rec& e, const Cut& cut, int h, int mt) {
   const int np = a.pairing ? e.mts >> 1 : 0;
   const bool pair = mt < 2 * np;
-  const int w = pair ? kPairCost : kSingleCost;
-  const long long ucost = (long long)w * e.nt;
-  const long long ubeg = ebeg + h * hc + (pair ? (mt >> 1) * ucost : (long long)np * kPairCost * e.nt + (mt - 2 * np) * ucost);
+  const int w = pair ? a.cost_pair : a.cost_single;
+  const long long first = e.beg + h * head_cost(a, e.mts, e.nt) + unit_begin(a, e.mts, e.nt, pair ? mt >> 1 : mt - np) + a.cost_unit;
   Pieces p;
-  p.ca = range_of(cut, ubeg);
-  p.np = range_of(cut, ubeg + ucost - w) - p.ca + 1;
-  p.slot0 = 2 * p.ca + (ubeg > range_start(cut, p.ca) ? 1 : 0);
+  p.ca = range_of(cut, first);
+  p.np = range_of(cut, first + (long long)(e.nt - 1) * w) - p.ca + 1;
+  p.slot0 = 2 * p.ca + (first > range_start(cut, p.ca) ? 1 : 0);
   return p;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) span_merge_kernel(Dev a) {
+// `a`: the requests' stream, `b`: the groups' (the same, or another kernel's)
+template <typename T, int kR>
+__global__ void __launch_bounds__(256) span_merge_kernel(Dev a, Dev b) {
+  constexpr int kP = 32 / kR, kBatch = 8 / kR;      // pieces a round, pieces loaded together
   pdl_wait();
   pdl_trigger();
   const int r = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int bad;
-  const Entry own = entry_of(a, a.group_offset, a.Gn + r, bad);
+  const Rec own = a.recs[a.Gn + r];
+  const long long total_a = *a.total, total_b = *b.total;
   const int nrows = own.T * a.G;
-  if (own.mts == 0 || int(blockIdx.z) * kMergeRows >= nrows) return;
-  const Cut cut = cut_of(a, a.ebeg[a.Gn + a.B]);
+  const int m0 = (int(blockIdx.z) * 8 + warp) * kR;
+  if (own.mts == 0 || m0 >= nrows) return;
+  // this lane's row and piece
+  const int i = lane % kR, m = min(m0 + i, nrows - 1);
+  const int mt = m / a.rt;
+  const Pieces po = pieces_of(a, own, cut_of(a, total_a), h, mt);
   const int g = own.group < -1 ? -2 - own.group : -1;
-  const long long obeg = a.ebeg[a.Gn + r];
-  Entry grp;
-  long long gbeg = 0;
+  if (g < 0 && !__any_sync(0xffffffffu, po.np > 1)) return;
+  const int t = m / a.G;
+  const size_t out = size_t(own.o + t) * a.H_q + h * a.G + (m - t * a.G);
+  Pieces pg = po;
+  int gc = 0, ng = 0;
   if (g >= 0) {
-    grp = entry_of(a, a.group_offset, g, bad);
-    gbeg = a.ebeg[g];
+    const Rec grp = b.recs[g];
+    const int gm = (own.o - grp.o) * a.G + m, gmt = gm / b.rt;
+    pg = pieces_of(b, grp, cut_of(b, total_b), h, gmt);
+    gc = gm - gmt * b.rt + ((b.pairing && (gmt & 1)) ? b.part_rows / 2 : 0);    // the second tile of a pair lies behind the first
+    ng = pg.np;
   }
-  for (int m = int(blockIdx.z) * kMergeRows + warp; m < min(nrows, (int(blockIdx.z) + 1) * kMergeRows); m += 8) {
-    const int mt = m / a.rt;
-    const Pieces po = pieces_of(a, own, obeg, cut, h, mt);
-    if (g < 0 && po.np < 2) continue;
-    const int t = m / a.G;
-    const size_t out = size_t(own.o + t) * a.H_q + h * a.G + (m - t * a.G);
-    Pieces pg = po;
-    int gm = 0, gmt = 0;
-    if (g >= 0) {
-      gm = (own.o - grp.o) * a.G + m;
-      gmt = gm / a.rt;
-      pg = pieces_of(a, grp, gbeg, cut, h, gmt);
-    }
-    // row of a piece's slot: the second tile of a pair lies behind the first
-    const int oc = m - mt * a.rt + ((a.pairing && (mt & 1)) ? a.part_rows / 2 : 0);
-    const int gc = gm - gmt * a.rt + ((a.pairing && (gmt & 1)) ? a.part_rows / 2 : 0);
-    const int ng = g >= 0 ? pg.np : 0, n = ng + po.np;
-    auto where = [&](int p, const float*& o, const float*& l) {
-      const bool isg = p < ng;
-      const Pieces& x = isg ? pg : po;
-      const int k = isg ? p : p - ng;
-      if (x.np == 1) {
-        const size_t at = size_t(isg ? 0 : 1) * a.N * a.H_q + out;
-        o = a.row_o + at * a.d;
-        l = a.row_lse + at;
-      } else {
-        const size_t at = size_t(k == 0 ? x.slot0 : 2 * (x.ca + k)) * a.part_rows + (isg ? gc : oc);
-        o = a.part_o + at * a.d;
-        l = a.part_lse + at;
-      }
-    };
-    // lane p holds the log2-sum-exp of pieces p, p + 32, ..
-    float M = -INFINITY;
-    for (int p = lane; p < n; p += 32) {
-      const float *o, *l;
-      where(p, o, l);
-      M = fmaxf(M, *l);
-    }
-    M = warp_max(M);
-    float sum = 0.f;
-    float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-    for (int p = 0; p < n; ++p) {
-      const float *o, *l;
-      where(p, o, l);
-      const float L = *l;
-      if (L == -INFINITY) continue;        // nothing visible in this piece (M may be -inf as well)
-      const float wt = exp2f(L - M);
-      sum += wt;
+  const int oc = m - mt * a.rt + ((a.pairing && (mt & 1)) ? a.part_rows / 2 : 0);
+  const bool mine = m0 + i < nrows && (g >= 0 || po.np > 1);
+  const int n = mine ? ng + po.np : 0;
+  int most = n;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int col = 4 * lane + 128 * c;
-        if (col < a.d) {
-          const float4 v = *reinterpret_cast<const float4*>(o + col);
-          acc[c].x = fmaf(wt, v.x, acc[c].x); acc[c].y = fmaf(wt, v.y, acc[c].y);
-          acc[c].z = fmaf(wt, v.z, acc[c].z); acc[c].w = fmaf(wt, v.w, acc[c].w);
+  for (int o = kR / 2; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+  // piece p of this lane's row: its values and its log2-sum-exp
+  auto where = [&](int p, const float*& o, const float*& l) {
+    const bool isg = p < ng;
+    const Pieces& x = isg ? pg : po;
+    const int k = isg ? p : p - ng;
+    if (x.np == 1) {
+      const size_t at = size_t(isg ? 0 : 1) * a.N * a.H_q + out;
+      o = a.row_o + at * a.d;
+      l = a.row_lse + at;
+    } else {
+      const size_t at = size_t(k == 0 ? x.slot0 : 2 * (x.ca + k)) * (isg ? b.part_rows : a.part_rows) + (isg ? gc : oc);
+      o = (isg ? b.part_o : a.part_o) + at * a.d;
+      l = (isg ? b.part_lse : a.part_lse) + at;
+    }
+  };
+  float M = -INFINITY, L0 = -INFINITY;
+  for (int p = lane / kR; p < n; p += kP) {
+    const float *o, *l;
+    where(p, o, l);
+    const float L = *l;
+    if (p < kP) L0 = L;
+    M = fmaxf(M, L);
+  }
+#pragma unroll
+  for (int o = kR; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float sum = 0.f;
+  float4 acc[kR][2];
+#pragma unroll
+  for (int k = 0; k < kR; ++k) acc[k][0] = acc[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int p0 = 0; p0 < most; p0 += kP) {
+    const int p = p0 + lane / kR;
+    float wt = 0.f;
+    unsigned long long src = 0;
+    if (p < n) {
+      const float *o, *l;
+      where(p, o, l);
+      const float L = p0 == 0 ? L0 : *l;
+      wt = L == -INFINITY ? 0.f : exp2f(L - M);     // nothing visible in this piece (M may be -inf as well)
+      src = reinterpret_cast<unsigned long long>(o);
+    }
+    sum += wt;
+    const int np = min(kP, most - p0);
+#pragma unroll 1
+    for (int c = 0; c < 2; ++c) {
+      const int col = 4 * lane + 128 * c;
+      if (128 * c >= a.d) break;
+#pragma unroll 1
+      for (int q0 = 0; q0 < np; q0 += kBatch) {
+        float4 v[8];
+        float w[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int from = min(q0 + u / kR, kP - 1) * kR + u % kR;
+          w[u] = __shfl_sync(0xffffffffu, wt, from);
+          const float* o = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, src, from));
+          if (q0 + u / kR >= np) w[u] = 0.f;
+          v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (w[u] != 0.f && col < a.d) v[u] = *reinterpret_cast<const float4*>(o + col);    // a NaN is not 0
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          float4& x = c == 0 ? acc[u % kR][0] : acc[u % kR][1];
+          x.x = fmaf(w[u], v[u].x, x.x); x.y = fmaf(w[u], v[u].y, x.y);
+          x.z = fmaf(w[u], v[u].z, x.z); x.w = fmaf(w[u], v[u].w, x.w);
         }
       }
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  }
+#pragma unroll
+  for (int o = kR; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int k = 0; k < kR; ++k) {
+    const float f = __shfl_sync(0xffffffffu, inv, k);
+    const unsigned long long at = __shfl_sync(0xffffffffu, (unsigned long long)out, k);
+    if (!__shfl_sync(0xffffffffu, mine ? 1 : 0, k)) continue;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int col = 4 * lane + 128 * c;
       if (col < a.d)
-        store4(static_cast<T*>(a.o) + out * a.d + col,
-               make_float4(acc[c].x * inv, acc[c].y * inv, acc[c].z * inv, acc[c].w * inv));
+        store4(static_cast<T*>(a.o) + at * a.d + col,
+               make_float4(acc[k][c].x * f, acc[k][c].y * f, acc[k][c].z * f, acc[k][c].w * f));
     }
-    if (lane == 0 && a.lse) a.lse[out] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
   }
+  if (mine && lane < kR && a.lse) a.lse[out] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
 }
 
 // ------------------------------------------------------------------------------ host
+// Costs on the tensor cores, about 800 clocks each: measured, a key tile takes a pair unit 3100 clocks and
+// a single one 2400, and a unit's start, masked tile and end together 8000 .. 10000.
+constexpr int kPairCost = 4, kSingleCost = 3, kUnitCost = 12, kMinCost = 24;
+
 // What the two calls have in common.
 struct Args {
   const spec_attn_params* p;
@@ -426,7 +464,7 @@ static spec_status_t check(const Args& x) {
 struct Plan {
   bool tc;
   int ctas, rt, bn, part_rows;
-  size_t ebeg, part_o, part_lse, row_o, row_lse, total;
+  size_t recs, sum, part_o, part_lse, row_o, row_lse, total;
 };
 
 static Plan plan(const Args& x) {
@@ -448,7 +486,8 @@ static Plan plan(const Args& x) {
   if (w.ctas > kMaxCtas) w.ctas = kMaxCtas;
   const size_t d = size_t(p->head_dim), rows = size_t(p->N) * p->H_q;
   size_t off = 0;
-  w.ebeg = off; off = align_up(off + sizeof(long long) * (size_t(x.num_groups) + p->B + 1), 256);
+  w.recs = off; off = align_up(off + sizeof(Rec) * (size_t(x.num_groups) + p->B), 256);
+  w.sum = off; off += 256;
   w.part_o = off; off = align_up(off + sizeof(float) * 2 * w.ctas * w.part_rows * d, 256);
   w.part_lse = off; off = align_up(off + sizeof(float) * 2 * w.ctas * w.part_rows, 256);
   w.row_o = w.row_lse = off;
@@ -476,7 +515,8 @@ static spec_status_t launch(const Args& x, void* ws, size_t ws_bytes, cudaStream
   d.q = p->q; d.k = p->k_cache; d.v = p->v_cache; d.o = p->o;
   d.lse = p->lse;
   d.req_status = p->req_status;
-  d.ebeg = reinterpret_cast<long long*>(base + w.ebeg);
+  d.recs = reinterpret_cast<Rec*>(base + w.recs);
+  d.total = reinterpret_cast<long long*>(base + w.sum);
   d.part_o = reinterpret_cast<float*>(base + w.part_o);
   d.part_lse = reinterpret_cast<float*>(base + w.part_lse);
   d.row_o = reinterpret_cast<float*>(base + w.row_o);
@@ -486,6 +526,10 @@ static spec_status_t launch(const Args& x, void* ws, size_t ws_bytes, cudaStream
   d.num_blocks = p->num_blocks; d.max_blocks = p->max_blocks_per_req; d.ctas = w.ctas;
   d.window = x.window; d.sinks = x.sinks;
   d.rt = w.rt; d.bn = w.bn; d.part_rows = w.part_rows; d.pairing = w.tc ? 1 : 0;
+  d.e_lo = 0;
+  d.e_hi = d.Gn + d.B;
+  d.cost_pair = kPairCost; d.cost_single = w.tc ? kSingleCost : 1;
+  d.cost_unit = w.tc ? kUnitCost : 0; d.cost_min = w.tc ? kMinCost : 4;
   const float scale = p->scale > 0.f ? p->scale : 1.f / sqrtf(float(p->head_dim));
   d.scale_log2 = scale * 1.4426950408889634f;
   const bool bf16 = p->dtype == SPEC_BF16;
@@ -502,9 +546,11 @@ static spec_status_t launch(const Args& x, void* ws, size_t ws_bytes, cudaStream
   }
   if (st != SPEC_OK) return st;
   const long long rows = (long long)p->T_max * d.G;
-  const unsigned z = unsigned((rows + kMergeRows - 1) / kMergeRows);
-  return launch_result(launch_pdl(bf16 ? span_merge_kernel<__nv_bfloat16> : span_merge_kernel<float>,
-                                  dim3(p->B, p->H_kv, z), dim3(256), 0, s, d));
+  const bool few = rows <= kMergeFew;
+  const int per = few ? 8 : 16;
+  return launch_result(launch_pdl(bf16 ? (few ? span_merge_kernel<__nv_bfloat16, 1> : span_merge_kernel<__nv_bfloat16, 2>)
+                                       : (few ? span_merge_kernel<float, 1> : span_merge_kernel<float, 2>),
+                                  dim3(p->B, p->H_kv, unsigned((rows + per - 1) / per)), dim3(256), 0, s, d, d));
 }
 
 static bool window_args(const spec_attn_window_params* p, Args& x) {

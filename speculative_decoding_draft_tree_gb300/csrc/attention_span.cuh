@@ -7,9 +7,10 @@
 //     keys [0, shared_len) by the first member's table row, every key visible to every row;
 //   request r: rows = its query rows, keys [lo, P + T) and [0, sink) by its own table row.
 // An entry has H_kv x (units) units; a unit is one or two row tiles of a KV head (`pairing`: two tiles
-// read every K/V tile once) over all of the entry's key tiles.  A tile of a pair costs kPairCost, of a
-// single row tile kSingleCost; ranges are equal in cost, and a tile belongs to the range that its first
-// cost unit lies in.
+// read every K/V tile once) over all of the entry's key tiles.  A unit costs cost_unit for its start and
+// end, and cost_pair or cost_single for each key tile; ranges are equal in cost, and a tile belongs to the
+// range that its first cost unit lies in.  A kernel's stream is a part of the entries (e_lo .. e_hi - 1):
+// a call's groups and requests may go to different kernels.
 #pragma once
 
 #include "common.cuh"
@@ -17,8 +18,6 @@
 namespace spec {
 namespace span {
 
-constexpr int kPairCost = 2, kSingleCost = 1;
-constexpr int kMinCost = 8;              // cost of a range at least: small calls use fewer ranges
 constexpr int kMaxCtas = 1024;
 constexpr int kGroupCache = 2048, kCostCache = 1024;   // group offsets, costs held in shared memory
 
@@ -35,7 +34,8 @@ struct Dev {
   void* o;
   float* lse;
   int32_t* req_status;
-  long long* ebeg;      // [Gn + B + 1]: cost before each entry, then the total (CTA 0, for the merge)
+  struct Rec* recs;     // [Gn + B]: the entries, for the merge
+  long long* total;     // cost of the stream, for the merge
   float* part_o;        // [2 ctas][part_rows][d]: pieces of cut units
   float* part_lse;      // [2 ctas][part_rows]: their log2-sum-exps
   float* row_o;         // [2][N][H_q][d]: uncut units of the shared form; 0: group, 1: own
@@ -45,7 +45,15 @@ struct Dev {
   int rt;               // query rows of a row tile
   int bn;               // keys of a key tile
   int part_rows, pairing;
+  int e_lo, e_hi;       // entries of this kernel's stream
+  int cost_pair, cost_single, cost_unit, cost_min;   // cost_min: of a range at least
   float scale_log2;
+};
+
+// What the merge has to know of an entry: where it lies in its kernel's stream, its tokens and tiles.
+struct Rec {
+  long long beg;
+  int o, T, nt, mts, group, pad;
 };
 
 // One entry: rows [0, T G) of tokens o .. o + T - 1; keys [0, sink) and [lo, end), those from P on
@@ -59,9 +67,14 @@ __device__ __forceinline__ int units_of(const Dev& a, const Entry& e) {
   return a.pairing ? (e.mts + 1) >> 1 : e.mts;
 }
 // cost of one KV head of the entry
-__device__ __forceinline__ long long head_cost(const Dev& a, const Entry& e) {
-  const int per = a.pairing ? (e.mts >> 1) * kPairCost + (e.mts & 1) * kSingleCost : e.mts * kSingleCost;
-  return (long long)e.nt * per;
+__device__ __forceinline__ long long head_cost(const Dev& a, int mts, int nt) {
+  const int np = a.pairing ? mts >> 1 : 0, ns = mts - 2 * np;
+  return (long long)(np * a.cost_pair + ns * a.cost_single) * nt + (long long)(np + ns) * a.cost_unit;
+}
+// cost before unit u of a KV head, from the head's beginning
+__device__ __forceinline__ long long unit_begin(const Dev& a, int mts, int nt, int u) {
+  const int np = a.pairing ? mts >> 1 : 0;
+  return (long long)(min(u, np) * a.cost_pair + max(u - np, 0) * a.cost_single) * nt + (long long)u * a.cost_unit;
 }
 
 // The group of request r: the g with off[g] <= r < off[g + 1], -1 if the offsets name none.
@@ -170,7 +183,7 @@ __device__ __forceinline__ long long div_ll(long long a, long long b) {     // a
 }
 __device__ __forceinline__ Cut cut_of(const Dev& a, long long total) {
   Cut c;
-  c.C = int(max(1LL, min((long long)a.ctas, total / kMinCost)));
+  c.C = int(max(1LL, min((long long)a.ctas, div_ll(total, a.cost_min))));
   c.base = div_ll(total, c.C);
   c.rem = int(total - c.base * c.C);
   return c;
@@ -182,10 +195,10 @@ __device__ __forceinline__ int range_of(const Cut& c, long long t) {
   return t < head ? int(div_ll(t, c.base + 1)) : c.rem + int(div_ll(t - head, max(1LL, c.base)));
 }
 
-// A CTA's share: cost positions [t0, t1), from entry e0, before which the cost is ebeg0.
+// A CTA's share: cost positions [t0, t1), from entry e0, before which the cost is beg0.
 struct Range {
-  long long t0, t1, ebeg0;
-  int e0;
+  long long t0, t1, beg0;
+  int e0, C;
 };
 
 // Scratch of the search: copies of the group offsets and of the entries' costs, where they fit.
@@ -194,21 +207,31 @@ struct RangeScratch {
   int32_t off[kGroupCache + 1];
 };
 
-// One warp finds range c.  With `report` it goes through all entries, writes ebeg and flags the requests
-// that cannot be worked on.
-__device__ __forceinline__ Range warp_range(const Dev& a, int c, bool report, RangeScratch& s) {
-  const int lane = threadIdx.x & 31, E = a.Gn + a.B;
-  const int32_t* off = a.group_offset;
-  if (a.Gn > 0 && a.Gn <= kGroupCache) {
-    for (int i = lane; i <= a.Gn; i += 32) s.off[i] = a.group_offset[i];
-    __syncwarp();
-    off = s.off;
+// the group offsets, copied by a warp where they fit
+__device__ __forceinline__ const int32_t* copy_offsets(const Dev& a, RangeScratch& s) {
+  if (a.Gn < 1 || a.Gn > kGroupCache) return a.group_offset;
+  for (int i = threadIdx.x & 31; i <= a.Gn; i += 32) s.off[i] = a.group_offset[i];
+  __syncwarp();
+  return s.off;
+}
+__device__ __forceinline__ long long warp_scan(long long v) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) >= o) v += x;
   }
+  return v;
+}
+
+// One warp finds range c.
+__device__ __forceinline__ Range warp_range(const Dev& a, int c, RangeScratch& s) {
+  const int lane = threadIdx.x & 31, E = a.e_hi - a.e_lo;
+  const int32_t* off = copy_offsets(a, s);
   Range R;
-  R.t0 = R.t1 = R.ebeg0 = 0;
-  R.e0 = 0;
+  R.t0 = R.t1 = R.beg0 = 0;
+  R.e0 = a.e_lo;
+  R.C = 0;
   long long sum = 0;            // pass 0: this lane's costs; pass 1: the cost before the chunk
-  bool found = false;
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll 1
@@ -219,50 +242,68 @@ __device__ __forceinline__ Range warp_range(const Dev& a, int c, bool report, Ra
         cost = s.cost[i];
       } else if (i < E) {
         int bad;
-        const Entry e = entry_of(a, off, i, bad);
-        cost = head_cost(a, e) * a.H_kv;
-        if (bad && report && pass == 0) atomicOr(&a.req_status[i - a.Gn], bad);
+        const Entry e = entry_of(a, off, a.e_lo + i, bad);
+        cost = head_cost(a, e.mts, e.nt) * a.H_kv;
       }
       if (pass == 0) {
         if (i0 < kCostCache) s.cost[i] = cost;
         sum += cost;
         continue;
       }
-      long long hi = cost;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, hi, o);
-        if (lane >= o) hi += x;
-      }
-      hi += sum;
-      const long long lo = hi - cost;
-      if (report && i < E) a.ebeg[i] = lo;
+      const long long hi = warp_scan(cost) + sum, lo = hi - cost;
       const uint32_t here = __ballot_sync(0xffffffffu, cost > 0 && lo <= R.t0 && R.t0 < hi);
-      if (here && !found) {
-        found = true;
-        R.e0 = i0 + __ffs(here) - 1;
-        R.ebeg0 = __shfl_sync(0xffffffffu, lo, __ffs(here) - 1);
-        if (!report) break;
+      if (here) {
+        R.e0 = a.e_lo + i0 + __ffs(here) - 1;
+        R.beg0 = __shfl_sync(0xffffffffu, lo, __ffs(here) - 1);
+        return R;
       }
       sum = __shfl_sync(0xffffffffu, hi, 31);
     }
     if (pass == 0) {
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (report && lane == 0) a.ebeg[E] = sum;
       const Cut cut = cut_of(a, sum);
-      if (sum > 0 && c < cut.C) {
-        R.t0 = range_start(cut, c);
-        R.t1 = range_start(cut, c + 1);
-      } else if (!report) {
-        break;
-      }
+      R.C = cut.C;
+      if (sum == 0 || c >= cut.C) return R;      // no work
+      R.t0 = range_start(cut, c);
+      R.t1 = range_start(cut, c + 1);
       sum = 0;
       __syncwarp();
     }
   }
-  if (!found) R.t1 = R.t0;      // no work
+  R.t1 = R.t0;      // never: the scan finds the entry
   return R;
+}
+
+// One warp of one CTA writes what the merge reads and flags the requests that cannot be worked on.  A CTA
+// without a range does it if there is one, else the first.
+__device__ __forceinline__ bool reports(const Range& R, int ctas) {
+  return int(blockIdx.x) == (R.C < ctas ? ctas - 1 : 0);
+}
+__device__ __forceinline__ void write_recs(const Dev& a, RangeScratch& s) {
+  const int lane = threadIdx.x & 31;
+  const int32_t* off = copy_offsets(a, s);
+  long long sum = 0;
+#pragma unroll 1
+  for (int i0 = a.e_lo; i0 < a.e_hi; i0 += 32) {
+    const int i = i0 + lane;
+    long long cost = 0;
+    Rec r;
+    if (i < a.e_hi) {
+      int bad;
+      const Entry e = entry_of(a, off, i, bad);
+      cost = head_cost(a, e.mts, e.nt) * a.H_kv;
+      if (bad) atomicOr(&a.req_status[i - a.Gn], bad);
+      r.o = e.o; r.T = e.T; r.nt = e.nt; r.mts = e.mts; r.group = e.group; r.pad = 0;
+    }
+    const long long hi = warp_scan(cost) + sum;
+    if (i < a.e_hi) {
+      r.beg = hi - cost;
+      a.recs[i] = r;
+    }
+    sum = __shfl_sync(0xffffffffu, hi, 31);
+  }
+  if (lane == 0) *a.total = sum;
 }
 
 // Key tiles [j0, j1) of one unit.
@@ -284,15 +325,15 @@ struct Walker {
   __device__ __forceinline__ void start(const Range& R) {
     t = R.t0;
     i = R.e0 - 1;
-    eend = R.ebeg0;      // next() enters e0
+    eend = R.beg0;      // next() enters e0
   }
   __device__ __forceinline__ bool next(const Dev& a, const Range& R, Item& it) {
     while (t < R.t1) {
       while (t >= eend) {
-        if (++i >= a.Gn + a.B) return false;
+        if (++i >= a.e_hi) return false;
         int bad;
         e = entry_of(a, a.group_offset, i, bad);
-        const long long hc = head_cost(a, e);
+        const long long hc = head_cost(a, e.mts, e.nt);
         ubeg = eend;
         eend += hc * a.H_kv;
         np = a.pairing ? e.mts >> 1 : 0;
@@ -301,20 +342,20 @@ struct Walker {
         if (t > ubeg && t < eend) {          // the range begins inside: the unit that holds t
           h = int(div_ll(t - ubeg, hc));
           ubeg += h * hc;
-          const long long pc = (long long)kPairCost * e.nt, sc = (long long)kSingleCost * e.nt, in = t - ubeg;
-          u = in < np * pc ? int(div_ll(in, pc)) : np + int(div_ll(in - np * pc, sc));
-          ubeg += min(u, np) * pc + max(u - np, 0) * sc;
+          const long long in = t - ubeg, pc = (long long)a.cost_pair * e.nt + a.cost_unit;
+          u = in < np * pc ? int(div_ll(in, pc)) : np + int(div_ll(in - np * pc, (long long)a.cost_single * e.nt + a.cost_unit));
+          ubeg += unit_begin(a, e.mts, e.nt, u);
         }
       }
-      const int w = u < np ? kPairCost : kSingleCost;
-      const long long ucost = (long long)w * e.nt, beg = ubeg;
-      const int j0 = int((t - beg + w - 1) / w);
-      const int j1 = int(min((long long)e.nt, (R.t1 - beg + w - 1) / w));
+      const int w = u < np ? a.cost_pair : a.cost_single;
+      const long long first = ubeg + a.cost_unit, uend = first + (long long)w * e.nt;      // the first tile's place
+      const int j0 = int(max(0LL, div_ll(max(0LL, t - first + w - 1), w)));
+      const int j1 = int(min((long long)e.nt, div_ll(max(0LL, R.t1 - first + w - 1), w)));
       it.h = h;
       it.pair = u < np ? 1 : 0;
       it.mt = it.pair ? 2 * u : np + u;
-      t = min(R.t1, beg + ucost);
-      ubeg += ucost;
+      t = min(R.t1, uend);
+      ubeg = uend;
       if (++u == units) {
         u = 0;
         ++h;
@@ -325,7 +366,7 @@ struct Walker {
       it.j0 = j0;
       it.j1 = j1;
       const bool cut = j0 > 0 || j1 < e.nt;
-      it.slot = cut ? 2 * int(blockIdx.x) + (beg > R.t0 ? 1 : 0)
+      it.slot = cut ? 2 * int(blockIdx.x) + (j0 == 0 && first > R.t0 ? 1 : 0)
                     : e.group >= 0 ? -2 : e.group == -1 ? -1 : -3;
       it.req = e.group >= 0 ? e.table : i - a.Gn;
       it.nreq = e.group >= 0 ? a.group_offset[e.group + 1] - it.req : 1;

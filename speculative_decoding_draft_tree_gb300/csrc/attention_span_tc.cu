@@ -70,7 +70,7 @@ struct Control {
 };
 constexpr int kSmemBytes = kSmemCtl + int(sizeof(Control));
 static_assert(kSmemBytes <= 232448, "fits one CTA's shared memory");
-static_assert(2 * sizeof(RangeScratch) <= size_t(kSmemOut), "scratch of two searches lies in the tiles");
+static_assert(sizeof(RangeScratch) <= 8 * 4096, "its scratch lies in the tiles, the report's in the rows on their way out");
 
 // One lane waits (bounded), the warp gets the outcome.
 __device__ __forceinline__ bool lane0_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
@@ -99,7 +99,7 @@ __device__ __forceinline__ float max32(const uint32_t (&x)[32]) {
                fmaxf(m[9], m[10]));
 }
 // 32 weights 2^(x sl + add), summed in pairs into `acc`, as 16 columns of bf16 pairs in TMEM at `dst`; with
-// kTwo what the rounding left, rounded again, 64 columns behind
+// kTwo what the rounding left, rounded again, in the 16 columns behind
 template <bool kTwo>
 __device__ __forceinline__ void weights32(const uint32_t (&x)[32], uint64_t sl, uint64_t add, uint64_t& acc,
                                           uint32_t dst) {
@@ -114,7 +114,7 @@ __device__ __forceinline__ void weights32(const uint32_t (&x)[32], uint64_t sl, 
     if constexpr (kTwo) lo[i] = pack_bf16(p0 - bf16_lo(hi[i]), p1 - bf16_hi(hi[i]));
   }
   tc::tmem_st16(dst, hi);
-  if constexpr (kTwo) tc::tmem_st16(dst + 64, lo);
+  if constexpr (kTwo) tc::tmem_st16(dst + 16, lo);
 }
 
 // true for one lane of the warp, which the compiler knows to be one (what a lane number would not tell it:
@@ -219,10 +219,8 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
   pdl_wait();
   pdl_trigger();
   if (warp == 3) {
-    const Range mine = warp_range(a, blockIdx.x, false, *reinterpret_cast<RangeScratch*>(smem));
+    const Range mine = warp_range(a, blockIdx.x, *reinterpret_cast<RangeScratch*>(smem));
     if (lane == 0) c.range = mine;
-  } else if (blockIdx.x == 0 && warp == 4) {
-    warp_range(a, 0, true, *(reinterpret_cast<RangeScratch*>(smem) + 1));     // for the merge
   }
   tc::tc_fence_before();
   // the scratch was read and written through the generic proxy where TMA writes next
@@ -403,13 +401,16 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
           tc::tc_fence_after();
           const uint32_t tO = tmem + 256 + 128 * s, tP = tmem + 128 * s;
           const uint64_t dv = dV0 + uint64_t(st) * kStep;
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            tc::mma_bf16_ts(tO, tP + 8 * kk, dv + uint64_t(kk * (2048 >> 4)), id_pv, kk > 0 || k > 0 ? 1u : 0u);
-          if (!pair) {
+          if (pair) {
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-              tc::mma_bf16_ts(tO, tP + 64 + 8 * kk, dv + uint64_t(kk * (2048 >> 4)), id_pv, 1u);
+              tc::mma_bf16_ts(tO, tP + 8 * kk, dv + uint64_t(kk * (2048 >> 4)), id_pv, kk > 0 || k > 0 ? 1u : 0u);
+          } else {
+#pragma unroll
+            for (int kk = 0; kk < 16; ++kk) {
+              const int q = (kk & 7) >> 1, col = 32 * q + 16 * (kk >> 3) + 8 * (kk & 1);
+              tc::mma_bf16_ts(tO, tP + col, dv + uint64_t((kk & 7) * (2048 >> 4)), id_pv, kk > 0 || k > 0 ? 1u : 0u);
+            }
           }
           if (!pair || s == 1) tc::mma_commit(&c.v_empty[st]);
           if (last) tc::mma_commit(&c.o_full[s]);
@@ -438,6 +439,7 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     if (layout_ok) {
       // ===================================================================== softmax, epilogue
+      if (warp == 4 && reports(c.range, gridDim.x)) write_recs(a, *reinterpret_cast<RangeScratch*>(smem + kSmemOut));
       const int s = (warp - 4) >> 2, q4 = warp & 3;
       const int m = q4 * 32 + lane;                   // row of the slot's tile; also a key of V's check
       const uint32_t lane_addr = uint32_t(q4 * 32) << 16;
@@ -500,32 +502,43 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
             const int gv = g0 + ti, st = gv % kVStages;
             if (!warp_wait(&c.v_full[st], (gv / kVStages) & 1, abort_flag)) { ok = false; break; }
             uint8_t* tile = sV + st * kTile + (q4 * 32 + (lane >> 3)) * 128 + (lane & 7) * 16;
+            const int key0 = kb + q4 * 32 + (lane >> 3), end = it.end;
+            const int sink = it.sink, lo = it.lo;
             uint32_t word = 0;
             bool wrote = false;
+#pragma unroll 1
             for (int half = pair ? s : 0; half < (pair ? s + 1 : 2); ++half) {
-#pragma unroll 4
+              uint8_t* p = tile + half * kAtom;
+              uint32_t hits = 0;           // bit i: an exponent of all ones in row 4 i + lane / 8
+#pragma unroll
               for (int i = 0; i < 8; ++i) {
-                const int key = kb + q4 * 32 + 4 * i + (lane >> 3);
-                uint4* p = reinterpret_cast<uint4*>(tile + half * kAtom + i * 512);
-                uint4 x = *p;
-                const bool seen = key < it.sink || (key >= it.lo && key < it.end);
-                bool hit = false;
-                auto clean = [&](uint32_t& w) {
-                  if ((w & 0x7f80u) == 0x7f80u) { w &= 0xffff0000u; hit = true; }
-                  if ((w & 0x7f800000u) == 0x7f800000u) { w &= 0xffffu; hit = true; }
-                };
-                clean(x.x);
-                clean(x.y);
-                clean(x.z);
-                clean(x.w);
-                if (!seen) x = make_uint4(0, 0, 0, 0);
-                if (hit || !seen) {
-                  *p = x;
+                const uint4 x = *reinterpret_cast<const uint4*>(p + i * 512);
+                const int key = key0 + 4 * i;
+                const bool seen = key < sink || (key >= lo && key < end);
+                // the addition carries into a half word's sign bit from an exponent of all ones only
+                const uint32_t t = ((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
+                                   ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u);
+                if (!seen) {
+                  *reinterpret_cast<uint4*>(p + i * 512) = make_uint4(0, 0, 0, 0);
                   wrote = true;
+                } else if (t & 0x80008000u) {
+                  hits |= 1u << i;
                 }
-                const uint32_t hits = __ballot_sync(0xffffffffu, hit && seen);
-                if (hits) {
-                  for (int r = 0; r < 4; ++r) word |= ((hits >> (8 * r)) & 0xffu) ? 1u << (4 * i + r) : 0u;
+              }
+              if (__any_sync(0xffffffffu, hits != 0u)) {
+#pragma unroll 1
+                for (int i = 0; i < 8; ++i) {
+                  const bool hit = (hits >> i) & 1u;
+                  if (hit) {
+                    uint32_t* w = reinterpret_cast<uint32_t*>(p + i * 512);
+                    for (int e = 0; e < 4; ++e) {
+                      if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u;
+                      if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0xffffu;
+                    }
+                    wrote = true;
+                  }
+                  const uint32_t lanes = __ballot_sync(0xffffffffu, hit);
+                  for (int r = 0; r < 4; ++r) word |= ((lanes >> (8 * r)) & 0xffu) ? 1u << (4 * i + r) : 0u;
                 }
               }
             }
@@ -541,24 +554,14 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
             nan = (((b0.x | b1.x) & vis0) | ((b0.y | b1.y) & vis1) | ((b0.z | b1.z) & vis2) | ((b0.w | b1.w) & vis3)) != 0u;
           }
           if (live) {
-            uint32_t x0[32], x1[32], x2[32], x3[32];
-            tc::tmem_ld32(tS, x0);
-            tc::tmem_ld32(tS + 32, x1);
-            tc::tmem_ld32(tS + 64, x2);
-            tc::tmem_ld32(tS + 96, x3);
-            tc::tmem_ld_wait();
-            if (masked) {
-              auto hide = [&](uint32_t (&x)[32], uint32_t vis) {
+            auto hide = [&](uint32_t (&x)[32], uint32_t vis) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] = (vis >> i) & 1u ? x[i] : __float_as_uint(-INFINITY);
-              };
-              hide(x0, vis0);
-              hide(x1, vis1);
-              hide(x2, vis2);
-              hide(x3, vis3);
-            }
-            const float top = valid ? fmaxf(fmaxf(max32(x0), max32(x1)), fmaxf(max32(x2), max32(x3))) * sl2 : -INFINITY;
-            if (__any_sync(0xffffffffu, top > ref + kLazy)) {
+              for (int i = 0; i < 32; ++i) x[i] = (vis >> i) & 1u ? x[i] : __float_as_uint(-INFINITY);
+            };
+            // the reference moves when the tile's maximum is 2^kLazy over it, and O_s and l follow
+            auto refer = [&](float top) {
+              if (!valid) top = -INFINITY;
+              if (!__any_sync(0xffffffffu, top > ref + kLazy)) return;
               const bool up = top > ref + kLazy;
               const float f = up && ref != -INFINITY ? ex2(ref - top) : 1.f;
               // S of this tile was issued after the product before, which has therefore landed in O
@@ -575,22 +578,53 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
               }
               l *= f;
               ref = up ? top : ref;
-            }
-            // a row that has seen nothing yet: 2^(x - inf) = 0 for every key (masked: -inf - inf)
-            const float sl = ref == -INFINITY ? 1.f : sl2;
-            const float add = nan ? NAN : ref == -INFINITY ? -INFINITY : -ref;
-            const uint64_t slv = f2_pack(sl, sl), addv = f2_pack(add, add);
+            };
             uint64_t acc0 = f2_pack(0.f, 0.f), acc1 = acc0;
+            // a row that has seen nothing yet: 2^(x - inf) = 0 for every key (masked: -inf - inf)
+            auto scale_of = [&] { const float v = ref == -INFINITY ? 1.f : sl2; return f2_pack(v, v); };
+            auto add_of = [&] { const float v = nan ? NAN : ref == -INFINITY ? -INFINITY : -ref; return f2_pack(v, v); };
             if (pair) {
-              weights32<false>(x0, slv, addv, acc0, tS);
-              weights32<false>(x1, slv, addv, acc1, tS + 16);
-              weights32<false>(x2, slv, addv, acc0, tS + 32);
-              weights32<false>(x3, slv, addv, acc1, tS + 48);
+              uint32_t x0[32], x1[32], x2[32], x3[32];
+              tc::tmem_ld32(tS, x0);
+              tc::tmem_ld32(tS + 32, x1);
+              tc::tmem_ld32(tS + 64, x2);
+              tc::tmem_ld32(tS + 96, x3);
+              tc::tmem_ld_wait();
+              if (masked) {
+                hide(x0, vis0);
+                hide(x1, vis1);
+                hide(x2, vis2);
+                hide(x3, vis3);
+              }
+              refer(fmaxf(fmaxf(max32(x0), max32(x1)), fmaxf(max32(x2), max32(x3))) * sl2);
+              const uint64_t sl = scale_of(), add = add_of();
+              weights32<false>(x0, sl, add, acc0, tS);
+              weights32<false>(x1, sl, add, acc1, tS + 16);
+              weights32<false>(x2, sl, add, acc0, tS + 32);
+              weights32<false>(x3, sl, add, acc1, tS + 48);
             } else {
-              weights32<true>(x0, slv, addv, acc0, tS);
-              weights32<true>(x1, slv, addv, acc1, tS + 16);
-              weights32<true>(x2, slv, addv, acc0, tS + 32);
-              weights32<true>(x3, slv, addv, acc1, tS + 48);
+              // Two pieces of P, 32 keys at a time, read twice: a single unit is bound by its K/V's bytes or
+              // by latency, and this is little code to fetch.
+              float top = -INFINITY;
+              uint64_t sl = 0, add = 0;
+#pragma unroll 1
+              for (int i = 0; i < 8; ++i) {
+                const int q = i & 3;
+                uint32_t x[32];
+                tc::tmem_ld32(tS + 32 * q, x);
+                tc::tmem_ld_wait();
+                if (masked) hide(x, q == 0 ? vis0 : q == 1 ? vis1 : q == 2 ? vis2 : vis3);
+                if (i < 4) {
+                  top = fmaxf(top, max32(x));
+                  if (i == 3) {
+                    refer(top * sl2);
+                    sl = scale_of();
+                    add = add_of();
+                  }
+                } else {
+                  weights32<true>(x, sl, add, acc0, tS + 32 * q);
+                }
+              }
             }
             float r0, r1, r2, r3;
             f2_unpack(acc0, r0, r1);
@@ -644,24 +678,27 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
           const size_t row_of = size_t(it.o + t) * a.H_q + it.h * a.G + (m - t_loc * a.G);
           const unsigned long long mine = (it.slot >= 0 ? slot_row + m : row_of) * kD;
           float* rows = it.slot >= 0 ? a.part_o : it.slot == -3 ? a.row_o + size_t(a.N) * a.H_q * kD : a.row_o;
-          const int shift = direct ? 2 : 3;                            // 4 or 8 units a row
+          unsigned long long at[8];        // where rows 4 i + lane / 8 begin
+#pragma unroll
+          for (int i = 0; i < 8; ++i) at[i] = __shfl_sync(0xffffffffu, mine, 4 * i + (lane >> 3));
+          const float wa = pair ? inv : w0 * inv, wb = pair || n1 == 0 ? 0.f : w1 * inv;
+          const int u8 = lane & 7;
 #pragma unroll 1
           for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
             uint32_t r[32];
             float v[32];
             tc::tmem_ld32(tO + (pair ? 128 * s : 0) + c0, r);
             tc::tmem_ld_wait();
-            const float wa = pair ? inv : w0 * inv;
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = wa == 0.f ? 0.f : __uint_as_float(r[i]) * wa;
             if (!pair && n1 > 0) {
               tc::tmem_ld32(tO + 128 + c0, r);
               tc::tmem_ld_wait();
-              const float wb = w1 * inv;
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = wb == 0.f ? v[i] : fmaf(__uint_as_float(r[i]), wb, v[i]);
             }
             if (direct) {
+              const int h4 = (c0 >> 3) & 4;        // 64 columns make a row's 128 bytes
 #pragma unroll
               for (int u = 0; u < 4; ++u) {
                 uint4 w;
@@ -669,8 +706,9 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
                 w.y = pack_bf16(v[8 * u + 2], v[8 * u + 3]);
                 w.z = pack_bf16(v[8 * u + 4], v[8 * u + 5]);
                 w.w = pack_bf16(v[8 * u + 6], v[8 * u + 7]);
-                *reinterpret_cast<uint4*>(stage + lane * 128 + ((u ^ (lane & 7)) << 4)) = w;
+                *reinterpret_cast<uint4*>(stage + lane * 128 + (((u + h4) ^ (lane & 7)) << 4)) = w;
               }
+              if (h4 == 0) continue;
             } else {
 #pragma unroll
               for (int u = 0; u < 8; ++u)
@@ -678,14 +716,13 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
                     make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
             }
             __syncwarp();
-            const int u = lane & ((1 << shift) - 1);
-            for (int r0 = 0; r0 < nv; r0 += 32 >> shift) {
-              const int row = r0 + (lane >> shift);
-              const unsigned long long at = __shfl_sync(0xffffffffu, mine, row);
-              const uint4 w = *reinterpret_cast<const uint4*>(stage + row * 128 + ((u ^ (row & 7)) << 4));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int row = 4 * i + (lane >> 3);
+              const uint4 w = *reinterpret_cast<const uint4*>(stage + row * 128 + ((u8 ^ (row & 7)) << 4));
               if (row < nv) {
-                if (direct) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + at + c0 + 8 * u) = w;
-                else *reinterpret_cast<uint4*>(rows + at + c0 + 4 * u) = w;
+                if (direct) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + at[i] + c0 - 32 + 8 * u8) = w;
+                else *reinterpret_cast<uint4*>(rows + at[i] + c0 + 4 * u8) = w;
               }
             }
             __syncwarp();
