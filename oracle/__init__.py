@@ -16,6 +16,8 @@ Modules (each function cites the passage it follows):
   rope       -- rotary position embedding at the tree's position ids and the tree K/V written
                 into its paged cache slots (the step before attention)
   lookahead  -- the lookahead-decoding mask (lookahead and verify branches in one forward)
+  span       -- tree attention with a sliding window and sinks, and under shared prefixes
+  beam       -- one step of beam search over beams and vocabulary, and the beams' paged cache
   draft_tree -- building the draft tree: EAGLE-2 expansion of the most probable leaves, top-K
                 of each expanded row, ECHO's batch-wide budget, packing for verification
 
@@ -31,7 +33,7 @@ and ECHO's optimality / ancestor closure for the draft-tree construction.
 tests/test_oracle_mutations.py plants 73 plausible mistakes, one at a time, in fresh copies of
 these modules, and each makes a named pin fail.  No oracle function is "parity unpinned".
 """
-from . import tree, attention, verify, compact, rope, lookahead, draft_tree  # noqa: F401
+from . import tree, attention, verify, compact, rope, lookahead, draft_tree, span, beam  # noqa: F401
 
 # request status bits (the oracle's own numbering of the data errors it detects)
 BAD_PARENT = 1

@@ -23,6 +23,11 @@ def _ws(nbytes: int, device) -> torch.Tensor:
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
+def _grown(ws, nbytes: int, device) -> torch.Tensor:
+    """`ws` if it holds nbytes, else a new workspace."""
+    return ws if ws is not None and ws.numel() >= nbytes else _ws(nbytes, device)
+
+
 def _packed(tensors: Dict[str, torch.Tensor], device, pin: bool = False):
     """One contiguous byte buffer holding tensors shaped like `tensors` at 256-byte aligned
     offsets, and the views into it (one copy moves them all)."""
@@ -91,6 +96,7 @@ class VerifyStep:
                                      self.slot_map, self.blocks_in_use, w.max_path)
         self.rope_p = None
         self.kv8 = None
+        self.span = None       # (kind, arguments) of enable_window or enable_shared
 
     def enable_rope(self, q_raw, k_new, v_new, base=10000.0, rotary_dim=None, interleaved=False,
                     fused=True):
@@ -120,6 +126,9 @@ class VerifyStep:
         a single page of their shape ([1, 1, H_kv, block_size, d]) will do.  The keys' rotation is
         the caller's: the library's rotary step writes a 16- or 32-bit cache."""
         w = self.w
+        if self.span is not None:
+            raise ValueError("enable_kv8 does not combine with enable_window or enable_shared, which "
+                             "read the 16- or 32-bit cache")
         if self.rope_p is not None:
             raise ValueError("enable_kv8 does not combine with enable_rope, which writes the 16- "
                              "or 32-bit cache; pass rotated keys as k_new")
@@ -136,6 +145,34 @@ class VerifyStep:
                                              w.prefix_len, self.path, self.n_acc, self.req_status,
                                              self.new_kv_len, self.slot_map, self.blocks_in_use,
                                              w.max_path)
+
+    def _enable_span(self, kind, args, params, size):
+        w = self.w
+        if self.kv8 is not None:
+            raise ValueError("enable_window and enable_shared read the 16- or 32-bit cache, not the "
+                             "8-bit one of enable_kv8")
+        if self.span is not None:
+            raise ValueError("enable_window and enable_shared do not combine")
+        self.span_p = params(w.q, self.k_layer0, self.v_layer0, w.block_table, w.prefix_len,
+                             w.node_offset, self.anc_mask, w.T_max, *args, self.o, self.lse,
+                             self.req_status)
+        self.span_ws = _ws(size(self.span_p), w.target.device)
+        self.span = (kind, args)
+
+    def enable_window(self, window: int, sinks: int = 0):
+        """Run every round's attention with a sliding window of `window` positions and the first
+        `sinks` tokens (spec_tree_attention_window): the target model's windowed layers.  Pages
+        out of sight may have been given back (table entries -1)."""
+        self._enable_span("window", (int(window), int(sinks)), B.attention_window_params,
+                          B.spec_attention_window_workspace_size)
+
+    def enable_shared(self, group_offset: torch.Tensor, shared_len: torch.Tensor):
+        """Run every round's attention with the prefixes that groups of requests have in common
+        read once a group (spec_tree_attention_shared): group g is the requests group_offset[g] ..
+        group_offset[g + 1] - 1, and its first shared_len[g] slots are the same (as spec_kv_fork
+        leaves them).  The results are the plain round's.  twin() shares the two tensors."""
+        self._enable_span("shared", (group_offset, shared_len), B.attention_shared_params,
+                          B.spec_attention_shared_workspace_size)
 
     # individual stages ---------------------------------------------------------------------
     def tree_build_rope(self, stream=None):
@@ -159,6 +196,10 @@ class VerifyStep:
     def attention(self, stream=None):
         if self.kv8 is not None:
             B.spec_tree_attention_kv8(self.kv8_attn, self.kv8_ws, stream)
+        elif self.span is not None:
+            call = (B.spec_tree_attention_window if self.span[0] == "window"
+                    else B.spec_tree_attention_shared)
+            call(self.span_p, self.span_ws, stream)
         else:
             B.spec_tree_attention(self.attn, self.attn_ws, stream)
 
@@ -283,6 +324,8 @@ class VerifyStep:
         step._in_pack = pack
         if self.kv8 is not None:
             step.enable_kv8(*self.kv8[:4], *rows)
+        if self.span is not None:
+            (step.enable_window if self.span[0] == "window" else step.enable_shared)(*self.span[1])
         return step
 
     def host_output_buffers(self) -> Dict[str, torch.Tensor]:
@@ -353,6 +396,101 @@ class RoundPipeline:
     def finish(self):
         """Make the compute stream wait for every submitted round's results on the host."""
         self.stream.wait_stream(self.dl)
+
+
+class BeamSearch:
+    """Beam search for B requests of W beams over a paged cache: the state of the beams, the calls
+    of a step, and the buffers that they need.  Row b * W + j of block_table, of q and of the logits
+    is beam j of request b.
+
+    The cache holds prompt_len[b] tokens of each request when a search begins: the prompt but its last
+    token, which is the first step's input of every beam.  Every beam's table row names the prompt's full
+    pages (spread() makes it so from beam 0's row), and its writing page (entry kv_len // block_size) and
+    the pages after it are its own.  A step:
+      write(layer, q_in, q_out, k_new, v_new), for each layer: the beams' new keys, rotated at their
+          positions, and values enter the cache, q is rotated;
+      attention(layer, q, o): each beam's token over its cache, the prompt's slots once a request;
+      advance(logits): the best W continuations, and the cache follows.
+    `tokens` then holds the next inputs and `parent` the beams that they continue; `scores`, `lengths`
+    and `finished` are the beams' state.  All asynchronous on the current stream, without
+    synchronisation, so a step can be captured as a graph once it has run (first calls set kernel
+    attributes and allocate workspaces).  8-bit caches take spread() and advance() alone."""
+
+    def __init__(self, k_cache, v_cache, block_table, prompt_len, W: int, H_q: int, V: int,
+                 eos: int = -1, tau: float = 1.0, alpha: float = 0.0, k_scale=None, v_scale=None,
+                 rope_base: float = 10000.0, rotary_dim=None, interleaved: bool = False):
+        dev = k_cache.device
+        i32 = dict(dtype=torch.int32, device=dev)
+        self.B, self.W, self.V = prompt_len.numel(), W, V
+        self.k_cache, self.v_cache, self.block_table = k_cache, v_cache, block_table
+        self.k_scale, self.v_scale = k_scale, v_scale
+        self.H_q, self.rope = H_q, (rope_base, rotary_dim, interleaved)
+        self.eos, self.tau, self.alpha = eos, tau, alpha
+        n = self.B * W
+        if block_table.shape[0] != n:
+            raise ValueError(f"block_table must have {n} rows, got {block_table.shape[0]}")
+        self.prompt_len = prompt_len
+        self.kv_len = prompt_len.clone()                       # tokens cached, [B]
+        self.prefix = prompt_len.repeat_interleave(W)          # the same for each beam, [B * W]
+        self.node_offset = torch.arange(n + 1, **i32)
+        self.group_offset = torch.arange(0, n + 1, W, **i32)
+        self.root = torch.full((n,), -1, **i32)
+        self.anc_mask = torch.ones((n, 1), **i32)
+        self.status = torch.zeros(n, **i32)
+        self.beam_status = torch.zeros(self.B, **i32)
+        self.scores = torch.zeros((self.B, W), dtype=torch.float32, device=dev)
+        self.lengths, self.finished = torch.zeros((self.B, W), **i32), torch.zeros((self.B, W), **i32)
+        self.parent, self.tokens = torch.zeros((self.B, W), **i32), torch.zeros((self.B, W), **i32)
+        self._reorder = B.beam_reorder_params(k_cache, v_cache, block_table, self.kv_len,
+                                              self.parent, self.beam_status, k_scale, v_scale)
+        self._reorder_ws = _ws(B.spec_beam_reorder_workspace_size(self._reorder), dev)
+        self._attn_ws = self._select_ws = None
+        self.begin()
+
+    def begin(self):
+        """Start from the prompts: beam 0 of each request is live, the others wait (score -infinity)."""
+        self.kv_len.copy_(self.prompt_len)
+        self.prefix.copy_(self.prompt_len.repeat_interleave(self.W))
+        self.scores.fill_(float("-inf"))
+        self.scores[:, 0] = 0
+        self.lengths.zero_()
+        self.finished.zero_()
+
+    def spread(self, stream=None):
+        """Make every beam continue beam 0's cache: the prompt's full pages shared, its partial page
+        copied into each beam's own writing page."""
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+            self.parent.zero_()
+            B.spec_beam_reorder(self._reorder, self._reorder_ws, stream)
+
+    def write(self, layer, q_in, q_out, k_new, v_new, stream=None):
+        """The beams' new tokens: q rotated into q_out, keys (rotated) and values into slot kv_len of
+        each beam ([B * W, H, head_dim] each; spec_tree_rope_kv_write)."""
+        p = B.rope_params(q_in, q_out, k_new, v_new, self.k_cache[layer], self.v_cache[layer],
+                          self.block_table, self.prefix, self.node_offset, self.prefix, self.status,
+                          *self.rope)
+        B.spec_tree_rope_kv_write(p, stream)
+
+    def attention(self, layer, q, o, stream=None):
+        """Each beam's new token over its cache (written before): o = attention(q), [B * W, H_q, d]."""
+        p = B.attention_shared_params(q, self.k_cache[layer], self.v_cache[layer], self.block_table,
+                                      self.prefix, self.node_offset, self.anc_mask, 1,
+                                      self.group_offset, self.prompt_len, o, None, self.status)
+        self._attn_ws = _grown(self._attn_ws, B.spec_attention_shared_workspace_size(p), q.device)
+        B.spec_tree_attention_shared(p, self._attn_ws, stream)
+
+    def advance(self, logits, stream=None):
+        """logits [B * W, ld >= V]: the best W continuations of each request become its beams, their
+        new token counts as cached, and tables and writing pages follow the parents."""
+        p = B.beam_select_params(logits, self.V, self.tau, self.scores, self.lengths, self.finished,
+                                 self.eos, self.alpha, self.parent, self.tokens, self.scores,
+                                 self.lengths, self.finished)
+        self._select_ws = _grown(self._select_ws, B.spec_beam_select_workspace_size(p), logits.device)
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+            B.spec_beam_select(p, self._select_ws, stream)
+            self.kv_len.add_(1)
+            self.prefix.add_(1)
+            B.spec_beam_reorder(self._reorder, self._reorder_ws, stream)
 
 
 class DraftTreeBuilder:
