@@ -321,11 +321,24 @@ __global__ void __launch_bounds__(256) span_merge_kernel(Dev a, Dev b) {
   const size_t out = size_t(own.o + t) * a.H_q + h * a.G + (m - t * a.G);
   Pieces pg = po;
   int gc = 0, ng = 0;
+  const float *g_part = a.part_o, *g_lse = a.part_lse;
+  int g_rows = a.part_rows;
   if (g >= 0) {
-    const Rec grp = b.recs[g];
-    const int gm = (own.o - grp.o) * a.G + m, gmt = gm / b.rt;
-    pg = pieces_of(b, grp, cut_of(b, total_b), h, gmt);
-    gc = gm - gmt * b.rt + ((b.pairing && (gmt & 1)) ? b.part_rows / 2 : 0);    // the second tile of a pair lies behind the first
+    // small groups are among the requests' stream
+    const bool in_a = a.recs[g].mts > 0;
+    const Rec grp = in_a ? a.recs[g] : b.recs[g];
+    const int gm = (own.o - grp.o) * a.G + m, gmt = gm / (in_a ? a.rt : b.rt);
+    gc = gm - gmt * (in_a ? a.rt : b.rt);
+    if (in_a) {
+      pg = pieces_of(a, grp, cut_of(a, total_a), h, gmt);
+      gc += a.pairing && (gmt & 1) ? a.part_rows / 2 : 0;        // the second tile of a pair lies behind the first
+    } else {
+      pg = pieces_of(b, grp, cut_of(b, total_b), h, gmt);
+      gc += b.pairing && (gmt & 1) ? b.part_rows / 2 : 0;
+      g_part = b.part_o;
+      g_lse = b.part_lse;
+      g_rows = b.part_rows;
+    }
     ng = pg.np;
   }
   const int oc = m - mt * a.rt + ((a.pairing && (mt & 1)) ? a.part_rows / 2 : 0);
@@ -344,9 +357,9 @@ __global__ void __launch_bounds__(256) span_merge_kernel(Dev a, Dev b) {
       o = a.row_o + at * a.d;
       l = a.row_lse + at;
     } else {
-      const size_t at = size_t(k == 0 ? x.slot0 : 2 * (x.ca + k)) * (isg ? b.part_rows : a.part_rows) + (isg ? gc : oc);
-      o = (isg ? b.part_o : a.part_o) + at * a.d;
-      l = (isg ? b.part_lse : a.part_lse) + at;
+      const size_t at = size_t(k == 0 ? x.slot0 : 2 * (x.ca + k)) * (isg ? g_rows : a.part_rows) + (isg ? gc : oc);
+      o = (isg ? g_part : a.part_o) + at * a.d;
+      l = (isg ? g_lse : a.part_lse) + at;
     }
   };
   float M = -INFINITY, L0 = -INFINITY;
@@ -425,6 +438,9 @@ __global__ void __launch_bounds__(256) span_merge_kernel(Dev a, Dev b) {
 // Costs on the tensor cores, about 800 clocks each: measured, a key tile takes a pair unit 3100 clocks and
 // a single one 2400, and a unit's start, masked tile and end together 8000 .. 10000.
 constexpr int kPairCost = 4, kSingleCost = 3, kUnitCost = 12, kMinCost = 24;
+// The rows kernel's: a tile, a unit, a range.
+constexpr int kRowsTileCost = 2, kRowsUnitCost = 2, kRowsMinCost = 8;
+constexpr int kFewRows = 16;       // query rows of a unit up to which the rows kernel takes it
 
 // What the two calls have in common.
 struct Args {
@@ -436,7 +452,9 @@ struct Args {
 
 bool tc_takes(const spec_attn_params* p);
 int tc_row_tile(const spec_attn_params* p);
-spec_status_t launch_span_tc(const spec_attn_params* p, Dev d, cudaStream_t s);
+spec_status_t make_tc_maps(const spec_attn_params* p, TcMaps& m);
+spec_status_t launch_span_tc(const Dev& d, const TcMaps& m, cudaStream_t s);
+spec_status_t launch_span_rows(const Dev& d, const TcMaps& m, cudaStream_t s);
 
 static spec_status_t check(const Args& x) {
   const spec_attn_params* p = x.p;
@@ -461,35 +479,57 @@ static spec_status_t check(const Args& x) {
   return SPEC_OK;
 }
 
-struct Plan {
-  bool tc;
+// The kernels of a call, each with a stream of its own: on the tensor cores the rows kernel when no request
+// has more than 16 query rows a head (all requests, and the groups that have no more either), and beside it
+// the tile kernel for larger groups; the tile kernel alone when requests have more rows (their groups do too);
+// else the kernel on the CUDA cores.  Single tokens of 64 requests (64 query heads on 8) over a window of
+// 4096: XX us by the rows kernel, 191 by the tile kernel.
+enum Kernel { kSimt, kTile, kFew };
+struct Part {
+  Kernel kernel;
   int ctas, rt, bn, part_rows;
-  size_t recs, sum, part_o, part_lse, row_o, row_lse, total;
+  size_t recs, sum, part_o, part_lse;
+};
+struct Plan {
+  int n;               // parts; the requests are in the first
+  Part part[2];
+  size_t row_o, row_lse, total;
 };
 
 static Plan plan(const Args& x) {
   const spec_attn_params* p = x.p;
   Plan w;
-  w.tc = tc_takes(p);
   const int sms = sm_count_current_device();
-  if (w.tc) {
-    w.ctas = sms;
-    w.rt = tc_row_tile(p);
-    w.bn = 128;
-    w.part_rows = 256;
-  } else {
-    w.ctas = sms * (p->head_dim <= 64 ? 3 : p->head_dim <= 128 ? 2 : 1);   // resident at once
-    w.rt = kSimtRows;
-    w.bn = kSimtKeys;
-    w.part_rows = kSimtRows;
-  }
-  if (w.ctas > kMaxCtas) w.ctas = kMaxCtas;
   const size_t d = size_t(p->head_dim), rows = size_t(p->N) * p->H_q;
+  const bool few = (long long)p->T_max * (p->H_q / p->H_kv) <= kFewRows;
+  w.n = 1;
+  w.part[0].kernel = !tc_takes(p) ? kSimt : few ? kFew : kTile;
+  if (w.part[0].kernel == kFew && x.num_groups > 0) {
+    w.n = 2;
+    w.part[1].kernel = kTile;
+  }
   size_t off = 0;
-  w.recs = off; off = align_up(off + sizeof(Rec) * (size_t(x.num_groups) + p->B), 256);
-  w.sum = off; off += 256;
-  w.part_o = off; off = align_up(off + sizeof(float) * 2 * w.ctas * w.part_rows * d, 256);
-  w.part_lse = off; off = align_up(off + sizeof(float) * 2 * w.ctas * w.part_rows, 256);
+  for (int i = 0; i < w.n; ++i) {
+    Part& t = w.part[i];
+    t.ctas = sms;
+    if (t.kernel == kSimt) {
+      t.ctas = sms * (p->head_dim <= 64 ? 3 : p->head_dim <= 128 ? 2 : 1);   // resident at once
+      t.rt = t.part_rows = kSimtRows;
+      t.bn = kSimtKeys;
+    } else if (t.kernel == kTile) {
+      t.rt = tc_row_tile(p);
+      t.bn = 128;
+      t.part_rows = 256;
+    } else {
+      t.rt = t.part_rows = kFewRows;
+      t.bn = 128;
+    }
+    if (t.ctas > kMaxCtas) t.ctas = kMaxCtas;
+    t.recs = off; off = align_up(off + sizeof(Rec) * (size_t(x.num_groups) + p->B), 256);
+    t.sum = off; off += 256;
+    t.part_o = off; off = align_up(off + sizeof(float) * 2 * t.ctas * t.part_rows * d, 256);
+    t.part_lse = off; off = align_up(off + sizeof(float) * 2 * t.ctas * t.part_rows, 256);
+  }
   w.row_o = w.row_lse = off;
   if (x.num_groups > 0) {
     w.row_o = off; off = align_up(off + sizeof(float) * 2 * rows * d, 256);
@@ -499,12 +539,8 @@ static Plan plan(const Args& x) {
   return w;
 }
 
-static spec_status_t launch(const Args& x, void* ws, size_t ws_bytes, cudaStream_t s) {
+static Dev device_params(const Args& x, const Plan& w, const Part& t, char* base) {
   const spec_attn_params* p = x.p;
-  const Plan w = plan(x);
-  if (w.ctas <= 0) return SPEC_ERR_CUDA;
-  if (!ws || ws_bytes < w.total || (reinterpret_cast<uintptr_t>(ws) & 255u)) return SPEC_ERR_INVALID_ARG;
-  char* base = static_cast<char*>(ws);
   Dev d;
   d.block_table = p->block_table;
   d.prefix_len = p->prefix_len;
@@ -515,42 +551,65 @@ static spec_status_t launch(const Args& x, void* ws, size_t ws_bytes, cudaStream
   d.q = p->q; d.k = p->k_cache; d.v = p->v_cache; d.o = p->o;
   d.lse = p->lse;
   d.req_status = p->req_status;
-  d.recs = reinterpret_cast<Rec*>(base + w.recs);
-  d.total = reinterpret_cast<long long*>(base + w.sum);
-  d.part_o = reinterpret_cast<float*>(base + w.part_o);
-  d.part_lse = reinterpret_cast<float*>(base + w.part_lse);
+  d.recs = reinterpret_cast<Rec*>(base + t.recs);
+  d.total = reinterpret_cast<long long*>(base + t.sum);
+  d.part_o = reinterpret_cast<float*>(base + t.part_o);
+  d.part_lse = reinterpret_cast<float*>(base + t.part_lse);
   d.row_o = reinterpret_cast<float*>(base + w.row_o);
   d.row_lse = reinterpret_cast<float*>(base + w.row_lse);
   d.B = p->B; d.N = p->N; d.Gn = x.num_groups; d.H_q = p->H_q; d.H_kv = p->H_kv; d.G = p->H_q / p->H_kv;
   d.d = p->head_dim; d.bs = p->block_size; d.T_max = p->T_max; d.W = (p->T_max + 31) / 32;
-  d.num_blocks = p->num_blocks; d.max_blocks = p->max_blocks_per_req; d.ctas = w.ctas;
+  d.num_blocks = p->num_blocks; d.max_blocks = p->max_blocks_per_req; d.ctas = t.ctas;
   d.window = x.window; d.sinks = x.sinks;
-  d.rt = w.rt; d.bn = w.bn; d.part_rows = w.part_rows; d.pairing = w.tc ? 1 : 0;
+  d.rt = t.rt; d.bn = t.bn; d.part_rows = t.part_rows; d.pairing = t.kernel == kTile ? 1 : 0;
   d.e_lo = 0;
   d.e_hi = d.Gn + d.B;
-  d.cost_pair = kPairCost; d.cost_single = w.tc ? kSingleCost : 1;
-  d.cost_unit = w.tc ? kUnitCost : 0; d.cost_min = w.tc ? kMinCost : 4;
+  d.rows_lo = 1;
+  d.rows_hi = 0x7fffffff;
+  if (t.kernel == kFew) {
+    d.rows_hi = kFewRows;
+  } else if (w.n == 2) {         // the groups that the rows kernel leaves
+    d.rows_lo = kFewRows + 1;
+    d.e_hi = d.Gn;
+  }
+  d.cost_pair = kPairCost;
+  d.cost_single = t.kernel == kTile ? kSingleCost : t.kernel == kFew ? kRowsTileCost : 1;
+  d.cost_unit = t.kernel == kTile ? kUnitCost : t.kernel == kFew ? kRowsUnitCost : 0;
+  d.cost_min = t.kernel == kTile ? kMinCost : t.kernel == kFew ? kRowsMinCost : 4;
   const float scale = p->scale > 0.f ? p->scale : 1.f / sqrtf(float(p->head_dim));
   d.scale_log2 = scale * 1.4426950408889634f;
+  return d;
+}
+
+static spec_status_t launch(const Args& x, void* ws, size_t ws_bytes, cudaStream_t s) {
+  const spec_attn_params* p = x.p;
+  const Plan w = plan(x);
+  if (w.part[0].ctas <= 0) return SPEC_ERR_CUDA;
+  if (!ws || ws_bytes < w.total || (reinterpret_cast<uintptr_t>(ws) & 255u)) return SPEC_ERR_INVALID_ARG;
+  const Dev a = device_params(x, w, w.part[0], static_cast<char*>(ws));
+  const Dev b = w.n == 2 ? device_params(x, w, w.part[1], static_cast<char*>(ws)) : a;
   const bool bf16 = p->dtype == SPEC_BF16;
-  spec_status_t st;
-  if (w.tc) {
-    st = launch_span_tc(p, d, s);
-  } else {
+  spec_status_t st = SPEC_OK;
+  if (w.part[0].kernel == kSimt) {
     static DeviceOnce raised_f32, raised_bf16;
     st = bf16 ? raise_dyn_smem_once(span_simt_kernel<__nv_bfloat16>, simt_smem(256), raised_bf16)
               : raise_dyn_smem_once(span_simt_kernel<float>, simt_smem(256), raised_f32);
     if (st == SPEC_OK)
       st = launch_result(launch_pdl(bf16 ? span_simt_kernel<__nv_bfloat16> : span_simt_kernel<float>,
-                                    dim3(w.ctas), dim3(kSimtThreads), size_t(simt_smem(p->head_dim)), s, d));
+                                    dim3(a.ctas), dim3(kSimtThreads), size_t(simt_smem(p->head_dim)), s, a));
+  } else {
+    TcMaps m;
+    st = make_tc_maps(p, m);
+    if (st == SPEC_OK && w.n == 2) st = launch_span_tc(b, m, s);
+    if (st == SPEC_OK) st = w.part[0].kernel == kFew ? launch_span_rows(a, m, s) : launch_span_tc(a, m, s);
   }
   if (st != SPEC_OK) return st;
-  const long long rows = (long long)p->T_max * d.G;
-  const bool few = rows <= kMergeFew;
-  const int per = few ? 8 : 16;
-  return launch_result(launch_pdl(bf16 ? (few ? span_merge_kernel<__nv_bfloat16, 1> : span_merge_kernel<__nv_bfloat16, 2>)
-                                       : (few ? span_merge_kernel<float, 1> : span_merge_kernel<float, 2>),
-                                  dim3(p->B, p->H_kv, unsigned((rows + per - 1) / per)), dim3(256), 0, s, d, d));
+  const long long rows = (long long)p->T_max * a.G;
+  const bool one = rows <= kMergeFew;
+  const int per = one ? 8 : 16;
+  return launch_result(launch_pdl(bf16 ? (one ? span_merge_kernel<__nv_bfloat16, 1> : span_merge_kernel<__nv_bfloat16, 2>)
+                                       : (one ? span_merge_kernel<float, 1> : span_merge_kernel<float, 2>),
+                                  dim3(p->B, p->H_kv, unsigned((rows + per - 1) / per)), dim3(256), 0, s, a, b));
 }
 
 static bool window_args(const spec_attn_window_params* p, Args& x) {

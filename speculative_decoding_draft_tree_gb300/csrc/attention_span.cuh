@@ -13,6 +13,8 @@
 // a call's groups and requests may go to different kernels.
 #pragma once
 
+#include <cuda.h>
+
 #include "common.cuh"
 
 namespace spec {
@@ -45,7 +47,8 @@ struct Dev {
   int rt;               // query rows of a row tile
   int bn;               // keys of a key tile
   int part_rows, pairing;
-  int e_lo, e_hi;       // entries of this kernel's stream
+  int e_lo, e_hi;       // entries of this kernel's stream,
+  int rows_lo, rows_hi; // those with so many query rows a head
   int cost_pair, cost_single, cost_unit, cost_min;   // cost_min: of a range at least
   float scale_log2;
 };
@@ -68,6 +71,7 @@ __device__ __forceinline__ int units_of(const Dev& a, const Entry& e) {
 }
 // cost of one KV head of the entry
 __device__ __forceinline__ long long head_cost(const Dev& a, int mts, int nt) {
+  if (mts == 0) return 0;
   const int np = a.pairing ? mts >> 1 : 0, ns = mts - 2 * np;
   return (long long)(np * a.cost_pair + ns * a.cost_single) * nt + (long long)(np + ns) * a.cost_unit;
 }
@@ -103,7 +107,8 @@ __device__ __forceinline__ void key_tiles(const Dev& a, Entry& e) {
   e.nt0 = (e.sink + a.bn - 1) / a.bn;
   e.w0 = max(e.lo / a.bn, e.nt0);
   e.nt = e.nt0 + (e.end + a.bn - 1) / a.bn - e.w0;
-  e.mts = (int)(((long long)e.T * a.G + a.rt - 1) / a.rt);
+  const long long rows = (long long)e.T * a.G;
+  e.mts = rows < a.rows_lo || rows > a.rows_hi ? 0 : int((rows + a.rt - 1) / a.rt);
 }
 
 // Entry i of the stream (groups first).  `off`: the group offsets, possibly a copy.  mts = 0: no work.
@@ -416,6 +421,13 @@ __device__ __forceinline__ int window_words(const Dev& a, const uint32_t* row, i
   const long long lo = (long long)P + depth - a.window + 1;
   return lo > 0 ? int(min(lo, (long long)P)) : 0;
 }
+
+// Tensor maps of a call on the tensor cores: q in boxes of a row tile's tokens, of at most T_max tokens and of
+// a 16-row unit's tokens; the caches by page and by whole key tiles of consecutive pages.
+struct TcMaps {
+  CUtensorMap q, q_own, q_rows, k_page, v_page, k_tile, v_tile;
+  int q_tokens, q_own_tokens, q_rows_tokens, kv_rows;
+};
 
 }  // namespace span
 }  // namespace spec

@@ -792,41 +792,48 @@ static bool encode(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap* map, cons
          CUDA_SUCCESS;
 }
 
-spec_status_t launch_span_tc(const spec_attn_params* p, Dev d, cudaStream_t s) {
+spec_status_t make_tc_maps(const spec_attn_params* p, TcMaps& m) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc) return SPEC_ERR_CUDA;
-  const int G = d.G, q_tokens = kRows / G, qs_tokens = p->T_max < q_tokens ? p->T_max : q_tokens;
-  const int kv_rows = p->num_blocks * p->H_kv * p->block_size;      // below 2^31 - 256, checked
-  CUtensorMap mQ, mQs, mK, mV, mKt, mVt;
+  const int G = p->H_q / p->H_kv;
+  m.q_tokens = kRows / G;
+  m.q_own_tokens = p->T_max < m.q_tokens ? p->T_max : m.q_tokens;
+  m.q_rows_tokens = G <= 16 ? 16 / G : 1;
+  m.kv_rows = p->num_blocks * p->H_kv * p->block_size;      // below 2^31 - 256, checked
   bool ok = true;
-  for (int small = 0; small < 2; ++small) {
+  CUtensorMap* q[3] = {&m.q, &m.q_own, &m.q_rows};
+  const int tokens[3] = {m.q_tokens, m.q_own_tokens, m.q_rows_tokens};
+  for (int i = 0; i < 3; ++i) {
     const cuuint64_t dims[3] = {cuuint64_t(kD), cuuint64_t(p->H_q), cuuint64_t(p->N)};
     const cuuint64_t strides[2] = {cuuint64_t(kD) * 2, cuuint64_t(p->H_q) * kD * 2};
-    const cuuint32_t box[3] = {64, cuuint32_t(G), cuuint32_t(small ? qs_tokens : q_tokens)};
-    ok = ok && encode(enc, small ? &mQs : &mQ, p->q, 3, dims, strides, box, CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
+    const cuuint32_t box[3] = {64, cuuint32_t(G), cuuint32_t(tokens[i])};
+    ok = ok && encode(enc, q[i], p->q, 3, dims, strides, box, CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
   }
   for (int v = 0; v < 2; ++v) {
     const void* cache = v ? p->v_cache : p->k_cache;
     {
-      const cuuint64_t dims[2] = {cuuint64_t(kD), cuuint64_t(kv_rows)};
+      const cuuint64_t dims[2] = {cuuint64_t(kD), cuuint64_t(m.kv_rows)};
       const cuuint64_t strides[1] = {cuuint64_t(kD) * 2};
       const cuuint32_t box[2] = {64, cuuint32_t(p->block_size)};
-      ok = ok && encode(enc, v ? &mV : &mK, cache, 2, dims, strides, box, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+      ok = ok && encode(enc, v ? &m.v_page : &m.k_page, cache, 2, dims, strides, box, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
     }
     {
       const cuuint64_t dims[4] = {cuuint64_t(kD), cuuint64_t(p->block_size), cuuint64_t(p->H_kv), cuuint64_t(p->num_blocks)};
       const cuuint64_t strides[3] = {cuuint64_t(kD) * 2, cuuint64_t(p->block_size) * kD * 2,
                                      cuuint64_t(p->H_kv) * p->block_size * kD * 2};
       const cuuint32_t box[4] = {64, cuuint32_t(p->block_size), 1, cuuint32_t(kKeys / p->block_size)};
-      ok = ok && encode(enc, v ? &mVt : &mKt, cache, 4, dims, strides, box, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+      ok = ok && encode(enc, v ? &m.v_tile : &m.k_tile, cache, 4, dims, strides, box, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
     }
   }
-  if (!ok) return SPEC_ERR_INVALID_ARG;
+  return ok ? SPEC_OK : SPEC_ERR_INVALID_ARG;
+}
+
+spec_status_t launch_span_tc(const Dev& d, const TcMaps& m, cudaStream_t s) {
   static DeviceOnce raised;
   const spec_status_t st = raise_dyn_smem_once(span_tc_kernel, kSmemBytes, raised);
   if (st != SPEC_OK) return st;
-  return launch_result(launch_pdl(span_tc_kernel, dim3(d.ctas), dim3(kThreads), size_t(kSmemBytes), s, mQ, mQs, mK,
-                                  mV, mKt, mVt, d, q_tokens, qs_tokens, kv_rows));
+  return launch_result(launch_pdl(span_tc_kernel, dim3(d.ctas), dim3(kThreads), size_t(kSmemBytes), s, m.q, m.q_own,
+                                  m.k_page, m.v_page, m.k_tile, m.v_tile, d, m.q_tokens, m.q_own_tokens, m.kv_rows));
 }
 
 }  // namespace span

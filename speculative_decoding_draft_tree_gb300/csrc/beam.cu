@@ -4,20 +4,22 @@
 // Within a beam the rank is increasing in the logit, so a beam's W best tokens suffice, and they and the
 // log-sum-exp come out of one pass over its row.
 //   beam_rows_kernel  one CTA per (segment, row): every thread keeps the running maximum and sum of its
-//                     elements (2^(x k2 - m k2), k2 = log2 e / tau) and nothing else.  The W-th largest of
-//                     the threads' maxima is a lower bound of the segment's W-th largest element, so only the
-//                     few threads whose maximum reaches it hold candidates: their elements are read once
-//                     more (from L2), a warp for each such thread, and the elements that reach the bound
-//                     are ranked by counting.  No list is kept while the row streams by.
+//                     elements (2^(x k2 - ref), k2 = log2 e / tau) and nothing else.  The W-th largest of
+//                     the maxima of 32 groups of eight threads is a lower bound of the segment's W-th largest
+//                     element, so only the few threads whose maximum reaches it hold candidates: their
+//                     elements are read once more (they are still in L2; read again by the second kernel
+//                     they are not, and the whole takes 63 us instead of 45), a warp for each such thread,
+//                     and the elements that reach the bound are ranked by counting.  No list is kept while
+//                     the row streams by.
 //   beam_pick_kernel  one CTA per request: the beams' candidates ranked by (score + log p) / penalty in
 //                     fp64, ties by beam and token.
 // Bound by the rows' bytes when there are many rows, by two launches and the chain load -> maxima ->
 // candidates when there are few; few rows are cut in segments.
 //
-// Ranks of different beams meet in one list, so log p has to be good: with the reference m k2 rounded
-// once and used alike in the exponents and in lse2 = m k2 + log2 sum, log p = (x k2 - lse2) ln 2 has the
-// sum's error (about 1e-7: fp32 partial sums of a few hundred terms, fp64 across threads) and a relative
-// 2^-25 of k2's rounding, whatever the logits' size.
+// Ranks of different beams meet in one list, so log p has to be good.  References are whole numbers (the
+// maximum of x k2, rounded up), so that sums over threads and segments join by exact powers of two; log p =
+// (x k2 - ref - log2 sum) ln 2 has the sum's error (about 1e-7: fp32 sums of a few hundred terms a thread, twice
+// that precision beyond) and a relative 2^-25 of k2's rounding, whatever the logits' size.
 #include <math.h>
 
 #include "common.cuh"
@@ -25,15 +27,49 @@
 namespace spec {
 namespace beam {
 
-constexpr int kRowThreads = 256;
-constexpr int kUnroll = 4;                 // 16-byte loads in flight per thread
+constexpr int kRowThreads = 256;           // 32 groups of eight
+constexpr int kUnroll = 2;                 // 16-byte loads in flight per thread
 constexpr int kList = 512;                 // candidates of a segment; more only where logits tie
 constexpr int kPickThreads = 256;
-static_assert(SPEC_MAX_BEAMS * SPEC_MAX_BEAMS <= kPickThreads, "a thread per candidate");
+static_assert(SPEC_MAX_BEAMS * SPEC_MAX_BEAMS <= kPickThreads && 16 * SPEC_MAX_BEAMS <= kPickThreads, "a thread per candidate, 16 per beam");
+static_assert(SPEC_MAX_BEAMS <= 32, "as many groups as beams at least");
 constexpr int kMaxSegLists = 64;           // segments x W
+constexpr float kNoRef = -3.0e38f;         // reference of elements that are all -infinity
+
+// log2 and a power in fp64 to about 1e-9, with few fp64 operations (a pow() takes 9 us of a request's
+// latency here, these 1): z = 2^e (1 + s) / (1 - s), log2 z = e + 2 / ln 2 (s + s^3 / 3 + ..), |s| <= 0.2; terms
+// from the second on are at most 0.014 of the first and are formed in fp32.
+__device__ __forceinline__ double log2_of(double z) {          // finite, positive, normal
+  const long long b = __double_as_longlong(z);
+  int e = int(b >> 52) - 1023;
+  double f = __longlong_as_double((b & 0xfffffffffffffLL) | 0x3ff0000000000000LL);
+  if (f > 1.5) {
+    f *= 0.5;
+    ++e;
+  }
+  const double d = f + 1.0;
+  double r = double(__frcp_rn(float(d)));
+  r = r * (2.0 - d * r);                                        // one Newton step: 2^-46
+  const double s = (f - 1.0) * r;
+  const float q = float(s) * float(s);
+  float t = 1.f / 15.f;
+  t = fmaf(t, q, 1.f / 13.f); t = fmaf(t, q, 1.f / 11.f); t = fmaf(t, q, 1.f / 9.f);
+  t = fmaf(t, q, 1.f / 7.f); t = fmaf(t, q, 1.f / 5.f); t = fmaf(t, q, 1.f / 3.f);
+  return double(e) + 2.8853900817779268 * (s + s * double(t * q));
+}
+// 2^w = 2^n e^g, |g| <= ln 2 / 2, by the exponential series; terms from the third on in fp32
+__device__ __forceinline__ double exp2_of(double w) {           // |w| < 1000
+  const double n = rint(w), g = (w - n) * 0.693147180559945309417;
+  const float h = float(g);
+  float t = 1.f / 40320.f;
+  t = fmaf(t, h, 1.f / 5040.f); t = fmaf(t, h, 1.f / 720.f); t = fmaf(t, h, 1.f / 120.f);
+  t = fmaf(t, h, 1.f / 24.f); t = fmaf(t, h, 1.f / 6.f);
+  const double y = 1.0 + g + g * g * (0.5 + double(t * h));
+  return y * __longlong_as_double((long long)(1023 + int(n)) << 52);
+}
 
 struct Seg {
-  double sum;        // sum of 2^(x k2 - ref)
+  dfloat sum;        // sum of 2^(x k2 - ref)
   float ref;
   int count;         // candidates
 };
@@ -74,33 +110,33 @@ template <typename T>
 __global__ void __launch_bounds__(kRowThreads) beam_rows_kernel(SelectDev a) {
   constexpr int kE = elem<T>::per16;
   constexpr int kWarps = kRowThreads / 32;
-  __shared__ float s_max[kRowThreads];
-  __shared__ double s_sum[kWarps];
-  __shared__ float s_ref[kWarps];
-  __shared__ float s_v[kList];
-  __shared__ int s_id[kList];
-  __shared__ int s_hot[kRowThreads];
-  __shared__ float s_thr, s_bv[kWarps];
-  __shared__ int s_bi[kWarps];
+  __shared__ float s_group[32], s_ref[kWarps], s_v[kList], s_bv[kWarps];
+  __shared__ dfloat s_sum[kWarps];
+  __shared__ int s_id[kList], s_hot[kRowThreads], s_bi[kWarps];
   __shared__ int s_n, s_nhot;
   pdl_wait();
   pdl_trigger();
   const int row = blockIdx.y, sg = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // a beam that offers no token of its row: the row is not read
-  if (a.finished[row] != 0 || !(a.scores[row] > -INFINITY)) return;
   const T* src = static_cast<const T*>(a.logits) + size_t(row) * a.ld;
   const int nvec = (a.V + kE - 1) / kE;
   const int v0 = sg * a.seg_vecs, v1 = min(nvec, v0 + a.seg_vecs);
-  if (tid == 0) s_n = s_nhot = 0;
-  float m = -INFINITY, mk2 = -INFINITY, sum = 0.f;
-  const uint64_t k2v = f2_pack(a.k2, a.k2);
-  for (int b = v0 + tid; b < v1; b += kUnroll * kRowThreads) {
-    uint4 raw[kUnroll];
+  uint4 raw[kUnroll];
+  auto fetch = [&](int b) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int v = b + u * kRowThreads;
       if (v < v1) raw[u] = ld_stream16(src + size_t(v) * kE);
     }
+  };
+  const int fin = a.finished[row];
+  const float score = a.scores[row];
+  fetch(v0 + tid);
+  // a beam that offers no token of its row: nothing more of it is read
+  if (fin != 0 || !(score > -INFINITY)) return;
+  if (tid == 0) s_n = s_nhot = 0;
+  float m = -INFINITY, ref = kNoRef, sum = 0.f;
+  const uint64_t k2v = f2_pack(a.k2, a.k2);
+  for (int b = v0 + tid; b < v1; b += kUnroll * kRowThreads) {
     float x[kUnroll * kE];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -112,22 +148,25 @@ __global__ void __launch_bounds__(kRowThreads) beam_rows_kernel(SelectDev a) {
         for (int k = 0; k < kE; ++k) x[u * kE + k] = -INFINITY;
       }
     }
+    fetch(b + kUnroll * kRowThreads);
     float cm = x[0];
 #pragma unroll
     for (int k = 1; k + 1 < kUnroll * kE; k += 2) cm = fmax3(cm, x[k], x[k + 1]);
     cm = fmaxf(cm, x[kUnroll * kE - 1]);
     if (cm > m) {
-      const float to = cm * a.k2;
-      sum *= ex2(mk2 - to);      // 2^-inf = 0 at first
       m = cm;
-      mk2 = to;
+      const float to = ceilf(cm * a.k2);
+      if (to > ref) {
+        sum = ref == kNoRef ? sum : sum * ex2(ref - to);     // exact: whole numbers (a NaN stays)
+        ref = to;
+      }
     }
     if (m == -INFINITY) {        // -inf only so far; a NaN still has to show
 #pragma unroll
       for (int k = 0; k < kUnroll * kE; ++k) sum = x[k] != x[k] ? x[k] : sum;
       continue;
     }
-    const uint64_t neg = f2_pack(-mk2, -mk2);
+    const uint64_t neg = f2_pack(-ref, -ref);
     uint64_t acc[4] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f), f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
 #pragma unroll
     for (int k = 0; k < kUnroll * kE; k += 2) {
@@ -141,32 +180,31 @@ __global__ void __launch_bounds__(kRowThreads) beam_rows_kernel(SelectDev a) {
     sum += (a0 + a1) + (a2 + a3);
   }
   // the segment's reference and sum
-  s_max[tid] = m;
-  float ref = warp_max(m);
-  if (lane == 0) s_ref[warp] = ref;
-  __syncthreads();
-  ref = s_ref[0];
+  const float mref = warp_max(ref);
+  const dfloat ws = warp_sum_df(df_make(ref == kNoRef ? sum : sum * ex2(ref - mref)));
+  float gm = m;
 #pragma unroll
-  for (int w = 1; w < kWarps; ++w) ref = fmaxf(ref, s_ref[w]);
-  const float refk2 = ref * a.k2;
-  double ds = m == -INFINITY ? double(sum) : double(sum) * double(ex2(mk2 - refk2));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) ds += __shfl_xor_sync(0xffffffffu, ds, o);
-  if (lane == 0) s_sum[warp] = ds;
-  // the W-th largest of the threads' maxima, ties by thread (a later tie passes the test below alike)
-  {
-    int rank = 0;
-    const float4* p = reinterpret_cast<const float4*>(s_max);
-#pragma unroll 4
-    for (int t = 0; t < kRowThreads / 4; ++t) {
-      const float4 o = p[t];
-      rank += (o.x > m || (o.x == m && 4 * t < tid)) + (o.y > m || (o.y == m && 4 * t + 1 < tid)) +
-              (o.z > m || (o.z == m && 4 * t + 2 < tid)) + (o.w > m || (o.w == m && 4 * t + 3 < tid));
-    }
-    if (rank == a.W - 1) s_thr = m;
+  for (int o = 1; o < 8; o <<= 1) gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, o));
+  if ((lane & 7) == 0) s_group[warp * 4 + (lane >> 3)] = gm;
+  if (lane == 0) {
+    s_ref[warp] = mref;
+    s_sum[warp] = ws;
   }
   __syncthreads();
-  const float thr = s_thr;       // -inf if fewer than W threads have elements: then all are candidates
+  // the W-th largest of the groups' maxima, ties by group (an equal element passes the test below alike);
+  // each warp finds it for itself
+  float thr;
+  {
+    const float mine = s_group[lane];
+    int rank = 0;
+#pragma unroll
+    for (int g = 0; g < 32; ++g) {
+      const float o = __shfl_sync(0xffffffffu, mine, g);
+      rank += (o > mine || (o == mine && g < lane)) ? 1 : 0;
+    }
+    // -inf if fewer than W groups have elements: then all are candidates
+    thr = __shfl_sync(0xffffffffu, mine, __ffs(__ballot_sync(0xffffffffu, rank == a.W - 1)) - 1);
+  }
   if (m >= thr && m > -INFINITY) s_hot[atomicAdd(&s_nhot, 1)] = tid;
   __syncthreads();
   const int nhot = s_nhot;
@@ -251,104 +289,152 @@ __global__ void __launch_bounds__(kRowThreads) beam_rows_kernel(SelectDev a) {
       }
     }
   }
-  if (tid == 0) {
-    double total = 0.0;
+  if (warp == 0) {
+    // fp64 runs at a sixteenth of fp32's rate and less here: the sums join as pairs of fp32 numbers
+    const float r = lane < kWarps ? s_ref[lane] : kNoRef;
+    const float top = warp_max(r);
+    const float f = r == kNoRef ? 1.f : ex2(r - top);
+    dfloat t = lane < kWarps ? s_sum[lane] : df_make(0.f);
+    t = {t.hi * f, t.lo * f};
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) total += s_sum[w];
-    Seg g;
-    g.sum = total;
-    g.ref = refk2;
-    g.count = min(n, a.W);
-    a.seg[out] = g;
+    for (int o = kWarps / 2; o > 0; o >>= 1) t = df_add(t, df_shfl_xor(t, o));
+    if (lane == 0) {
+      Seg g;
+      g.sum = t;
+      g.ref = top;
+      g.count = min(n, a.W);
+      a.seg[out] = g;
+    }
   }
 }
 
+// fp64 values in the order of signed whole numbers (no NaN)
+__device__ __forceinline__ long long rank_key(double v) {
+  const long long b = __double_as_longlong(v);
+  return b < 0 ? b ^ 0x7fffffffffffffffLL : b;
+}
+
 __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(SelectDev a) {
-  __shared__ float s_v[SPEC_MAX_BEAMS * kMaxSegLists];      // beam's segment lists, -inf where short
+  constexpr int kHold = SPEC_MAX_BEAMS * kMaxSegLists / kPickThreads;
+  __shared__ float s_v[SPEC_MAX_BEAMS * kMaxSegLists];      // beam's segment lists, id 0x7fffffff where short
   __shared__ int s_id[SPEC_MAX_BEAMS * kMaxSegLists];
-  __shared__ double s_lse[SPEC_MAX_BEAMS], s_inv[SPEC_MAX_BEAMS];
+  __shared__ double s_lse[SPEC_MAX_BEAMS], s_inv[SPEC_MAX_BEAMS];      // log2 of the row's sum; 1 / penalty
+  __shared__ dfloat s_sum[SPEC_MAX_BEAMS];
+  __shared__ float s_top[SPEC_MAX_BEAMS];
   __shared__ float s_score[SPEC_MAX_BEAMS];
   __shared__ int s_len[SPEC_MAX_BEAMS], s_fin[SPEC_MAX_BEAMS], s_live[SPEC_MAX_BEAMS];
-  __shared__ double s_rank[SPEC_MAX_BEAMS * SPEC_MAX_BEAMS], s_total[SPEC_MAX_BEAMS * SPEC_MAX_BEAMS];
+  __shared__ long long s_key[SPEC_MAX_BEAMS * SPEC_MAX_BEAMS];
+  __shared__ double s_total[SPEC_MAX_BEAMS * SPEC_MAX_BEAMS];
   __shared__ int s_tok[SPEC_MAX_BEAMS * SPEC_MAX_BEAMS];
   pdl_wait();
   pdl_trigger();
-  const int b = blockIdx.x, tid = threadIdx.x, W = a.W, per = a.S * W;
+  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, W = a.W, per = a.S * W;
   const int r0 = b * W;
-  if (tid < W) {
-    const int row = r0 + tid;
-    const float sc = a.scores[row];
-    const int fin = a.finished[row] != 0;
-    const int len = a.lengths[row];
-    bool live = sc > -INFINITY;      // false for NaN
-    double lse = 0.0;
-    if (live && !fin) {
-      float ref = -INFINITY;
-      for (int k = 0; k < a.S; ++k) ref = fmaxf(ref, a.seg[size_t(row) * a.S + k].ref);
-      double sum = 0.0;
-      for (int k = 0; k < a.S; ++k) {
-        const Seg g = a.seg[size_t(row) * a.S + k];
-        // a segment of -inf only has the sum 0, or NaN if it holds one
-        sum += g.ref == -INFINITY ? g.sum : g.sum * exp2(double(g.ref) - double(ref));
-      }
-      lse = double(ref) + log2(sum);
-      live = sum > 0.0 && sum < INFINITY && ref < INFINITY;    // a NaN or an infinity: the row is out
+  // all candidates on their way at once; what a beam that was not read left there is not used
+  float cv[kHold];
+  int ci[kHold];
+#pragma unroll
+  for (int k = 0; k < kHold; ++k) {
+    const int i = tid + k * kPickThreads;
+    if (i < W * per) {
+      cv[k] = a.cand_v[size_t(r0) * per + i];
+      ci[k] = a.cand_id[size_t(r0) * per + i];
+      const int j = i / per, sg = (i - j * per) / W;
+      if (i - j * per - sg * W >= a.seg[size_t(r0 + j) * a.S + sg].count) ci[k] = 0x7fffffff;
     }
-    s_lse[tid] = lse;
-    s_score[tid] = sc;
-    s_len[tid] = len;
-    s_fin[tid] = fin;
-    s_live[tid] = live ? 1 : 0;
-    const double pen = (5.0 + double(len + (fin ? 0 : 1))) / 6.0;
-    s_inv[tid] = a.alpha == 0.0 ? 1.0 : pow(pen, a.alpha);
   }
-  for (int i = tid; i < W * W; i += kPickThreads) s_tok[i] = -1;
+  // sixteen lanes a beam: the sum over its segments
+  {
+    const int w = tid >> 4, sub = tid & 15;
+    const bool mine = w < W;
+    const int row = r0 + (mine ? w : 0);
+    float ref = kNoRef;
+    dfloat sum = df_make(0.f);
+    const float sc = a.scores[row];
+    const int fin = a.finished[row] != 0, len = a.lengths[row];
+    if (mine && sub < a.S && fin == 0 && sc > -INFINITY) {      // 16 segments at most; false for NaN
+      const Seg g = a.seg[size_t(row) * a.S + sub];
+      ref = g.ref;
+      sum = g.sum;
+    }
+    float top = ref;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float f = ref == kNoRef ? 1.f : ex2(ref - top);     // a segment of -inf only has the sum 0, or NaN if it holds one
+    sum = {sum.hi * f, sum.lo * f};
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) sum = df_add(sum, df_shfl_xor(sum, o));
+    if (mine && sub == 0) {
+      // a NaN or an infinity: the row is out
+      const bool good = sum.hi > 0.f && sum.hi < INFINITY && top < INFINITY;
+      s_sum[w] = good ? sum : df_make(1.f);
+      s_top[w] = good ? top : 0.f;
+      s_score[w] = sc;
+      s_len[w] = len;
+      s_fin[w] = fin;
+      s_live[w] = sc > -INFINITY && (fin != 0 || good) ? 1 : 0;
+    }
+  }
+  if (tid < W * W) {
+    s_tok[tid] = -1;
+    s_key[tid] = (long long)0x8000000000000000LL;      // behind every rank
+  }
   __syncthreads();
-  for (int i = tid; i < W * per; i += kPickThreads) {
-    const int j = i / per, k = i - j * per, sg = k / W;
-    const size_t at = size_t(r0 + j) * a.S + sg;
-    const bool have = s_live[j] && !s_fin[j] && k - sg * W < a.seg[at].count;
-    s_v[i] = have ? a.cand_v[at * W + (k - sg * W)] : -INFINITY;
-    s_id[i] = have ? a.cand_id[at * W + (k - sg * W)] : 0x7fffffff;
+  // the fp64 functions, of all beams at once in one warp each
+  if (warp == 0 && lane < W) {
+    s_lse[lane] = double(s_top[lane]) + log2_of(df_to_d(s_sum[lane]));
+  } else if (warp == 1 && lane < W) {
+    // penalties beyond fp64's range stay at its ends
+    const double pen = (5 + s_len[lane] + (s_fin[lane] ? 0 : 1)) * (1.0 / 6.0);
+    s_inv[lane] = a.alpha == 0.0 ? 1.0 : exp2_of(fmin(fmax(-a.alpha * log2_of(fmax(pen, 0.5)), -990.0), 990.0));
+  }
+#pragma unroll
+  for (int k = 0; k < kHold; ++k) {
+    const int i = tid + k * kPickThreads;
+    if (i < W * per) {
+      const int j = i / per;
+      if (!s_live[j] || s_fin[j]) ci[k] = 0x7fffffff;
+      s_v[i] = ci[k] == 0x7fffffff ? -INFINITY : cv[k];
+      s_id[i] = ci[k];
+    }
   }
   __syncthreads();
   // a beam's W best, in order
-  for (int i = tid; i < W * per; i += kPickThreads) {
-    if (s_id[i] == 0x7fffffff) continue;
+#pragma unroll
+  for (int k = 0; k < kHold; ++k) {
+    const int i = tid + k * kPickThreads;
+    if (i >= W * per || ci[k] == 0x7fffffff) continue;
     const int j = i / per;
-    const float v = s_v[i];
-    const int id = s_id[i];
     int rank = 0;
-    for (int k = j * per; k < (j + 1) * per; ++k) rank += ahead(s_v[k], s_id[k], v, id) ? 1 : 0;
+#pragma unroll 8
+    for (int q = j * per; q < (j + 1) * per; ++q) rank += ahead(s_v[q], s_id[q], cv[k], ci[k]) ? 1 : 0;
     if (rank < W) {
-      const double total = double(s_score[j]) + (double(v) * double(a.k2) - s_lse[j]) * 0.693147180559945309417;
-      s_tok[j * W + rank] = id;
+      const double total = double(s_score[j]) + (double(cv[k]) * double(a.k2) - s_lse[j]) * 0.693147180559945309417;
+      s_tok[j * W + rank] = ci[k];
       s_total[j * W + rank] = total;
-      s_rank[j * W + rank] = total / s_inv[j];
+      s_key[j * W + rank] = rank_key(total * s_inv[j]);
     }
   }
   if (tid < W && s_live[tid] && s_fin[tid]) {
     s_tok[tid * W] = a.eos >= 0 && a.eos < a.V ? a.eos : 0;
     s_total[tid * W] = double(s_score[tid]);
-    s_rank[tid * W] = double(s_score[tid]) / s_inv[tid];
+    s_key[tid * W] = rank_key(double(s_score[tid]) * s_inv[tid]);
   }
   __syncthreads();
   const int offered = __syncthreads_count(tid < W * W && s_tok[tid] >= 0);
-  for (int i = tid; i < W * W; i += kPickThreads) {
-    if (s_tok[i] < 0) continue;
-    const double mine = s_rank[i];
+  if (tid < W * W && s_tok[tid] >= 0) {
+    const long long mine = s_key[tid];
     int rank = 0;
-    for (int k = 0; k < W * W; ++k) {
-      // equal logits of a beam have equal ranks: the list's order, beam by beam, settles ties
-      if (s_tok[k] >= 0 && (s_rank[k] > mine || (s_rank[k] == mine && k < i))) ++rank;
-    }
+    // equal logits of a beam have equal ranks: the list's order, beam by beam, settles ties
+#pragma unroll 8
+    for (int k = 0; k < W * W; ++k) rank += s_key[k] > mine || (s_key[k] == mine && k < tid) ? 1 : 0;
     if (rank < W) {
-      const int j = i / W, at = r0 + rank;
+      const int j = tid / W, at = r0 + rank;
       a.parent[at] = j;
-      a.token[at] = s_tok[i];
-      a.out_score[at] = float(s_total[i]);
+      a.token[at] = s_tok[tid];
+      a.out_score[at] = float(s_total[tid]);
       a.out_length[at] = s_len[j] + (s_fin[j] ? 0 : 1);
-      a.out_finished[at] = (s_fin[j] || s_tok[i] == a.eos) ? 1 : 0;
+      a.out_finished[at] = (s_fin[j] || s_tok[tid] == a.eos) ? 1 : 0;
     }
   }
   if (tid >= offered && tid < W) {
