@@ -24,6 +24,7 @@ constexpr int kSimtKeys = 64;
 struct SimtShared {
   RangeScratch scratch;
   Range range;
+  Entry first;
   Item item;
   int more;
   int page[kSimtKeys];                 // cache row of a key's page row, -1: not needed
@@ -69,9 +70,10 @@ __global__ void __launch_bounds__(kSimtThreads) span_simt_kernel(Dev a) {
   float* sv = sk + kSimtKeys * ldk;
   pdl_wait();
   pdl_trigger();
+  entry_costs(a, s.scratch);
   if (threadIdx.x < 32) {
-    const Range mine = warp_range(a, blockIdx.x, s.scratch);
-    if (reports(mine, gridDim.x)) write_recs(a, s.scratch);
+    const Range mine = warp_range(a, blockIdx.x, s.scratch, s.first);
+    if (reports(mine, gridDim.x)) write_recs(a);
     if (threadIdx.x == 0) s.range = mine;
   }
   __syncthreads();
@@ -83,7 +85,7 @@ __global__ void __launch_bounds__(kSimtThreads) span_simt_kernel(Dev a) {
   const T* kc = static_cast<const T*>(a.k);
   const T* vc = static_cast<const T*>(a.v);
   Walker walker;
-  if (tid == 0) walker.start(R);
+  if (tid == 0) walker.start(R, &s.first);
   while (true) {
     if (tid == 0) s.more = walker.next(a, R, s.item) ? 1 : 0;
     __syncthreads();
@@ -276,13 +278,15 @@ __global__ void __launch_bounds__(kSimtThreads) span_simt_kernel(Dev a) {
 }
 
 // ------------------------------------------------------------------------------ merge
-// CTA (r, h, z): rows 8 kR z .. 8 kR (z + 1) - 1 of request r under KV head h, kR rows a warp.  A row's
-// pieces: for a member of a group those of the group's unit, then those of its request's own unit, in stream
-// order, so that the sum does not depend on who ran when.  Rows of requests on their own whose unit was
-// not cut have been written already.  Lane kR p + i holds the weight and the place of piece p (of 32 / kR at
-// a time) of row i, and eight vectors are loaded together: bound by latency (record, log-sum-exps, values)
-// when there are few rows (a row a warp then), by the pieces' bytes when there are many (two).
-constexpr int kMergeFew = 16;        // rows of a request and head up to which a warp takes one row
+// CTA (r, h, z): rows kMergeRows z .. of request r under KV head h, kR rows a warp at a time.  A row's pieces:
+// for a member of a group those of the group's unit, then those of its request's own unit, in stream order, so
+// that the sum does not depend on who ran when.  Rows of requests on their own whose unit was not cut have been
+// written already.  Lane kR p + i holds the weight and the place of piece p (of 32 / kR at a time) of row i.
+// Bound by a chain of loads (record, group's record, log-sum-exps, values), so rows that share the first two
+// are taken by one CTA, two at a time (many rows), and a warp takes one row where there are few: 16 rows or
+// less a request and head.
+constexpr int kMergeFew = 16;
+constexpr int kMergeRows = 64;
 
 struct Pieces {
   int np, ca, slot0;        // np = 1: not cut
@@ -299,139 +303,146 @@ __device__ __forceinline__ Pieces pieces_of(const Dev& a, const Rec& e, const Cu
   return p;
 }
 
-// `a`: the requests' stream, `b`: the groups' (the same, or another kernel's)
-template <typename T, int kR>
-__global__ void __launch_bounds__(256) span_merge_kernel(Dev a, Dev b) {
-  constexpr int kP = 32 / kR, kBatch = 8 / kR;      // pieces a round, pieces loaded together
+template <typename T, int kR, int kCols>      // kCols: vectors of 128 columns of a row
+__global__ void __launch_bounds__(256) span_merge_kernel(Dev a) {
+  constexpr int kP = 32 / kR, kLoads = 4;      // pieces a round, vectors loaded together
+  constexpr int kBatch = kLoads / kR;
   pdl_wait();
   pdl_trigger();
   const int r = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Rec own = a.recs[a.Gn + r];
-  const long long total_a = *a.total, total_b = *b.total;
+  const long long total = *a.total;
   const int nrows = own.T * a.G;
-  const int m0 = (int(blockIdx.z) * 8 + warp) * kR;
-  if (own.mts == 0 || m0 >= nrows) return;
-  // this lane's row and piece
-  const int i = lane % kR, m = min(m0 + i, nrows - 1);
-  const int mt = m / a.rt;
-  const Pieces po = pieces_of(a, own, cut_of(a, total_a), h, mt);
+  const int last = min(nrows, (int(blockIdx.z) + 1) * kMergeRows);
+  if (own.mts == 0 || int(blockIdx.z) * kMergeRows + warp * kR >= last) return;
+  const Cut cut = cut_of(a, total);
   const int g = own.group < -1 ? -2 - own.group : -1;
-  if (g < 0 && !__any_sync(0xffffffffu, po.np > 1)) return;
-  const int t = m / a.G;
-  const size_t out = size_t(own.o + t) * a.H_q + h * a.G + (m - t * a.G);
-  Pieces pg = po;
-  int gc = 0, ng = 0;
-  const float *g_part = a.part_o, *g_lse = a.part_lse;
-  int g_rows = a.part_rows;
-  if (g >= 0) {
-    // small groups are among the requests' stream
-    const bool in_a = a.recs[g].mts > 0;
-    const Rec grp = in_a ? a.recs[g] : b.recs[g];
-    const int gm = (own.o - grp.o) * a.G + m, gmt = gm / (in_a ? a.rt : b.rt);
-    gc = gm - gmt * (in_a ? a.rt : b.rt);
-    if (in_a) {
-      pg = pieces_of(a, grp, cut_of(a, total_a), h, gmt);
-      gc += a.pairing && (gmt & 1) ? a.part_rows / 2 : 0;        // the second tile of a pair lies behind the first
-    } else {
-      pg = pieces_of(b, grp, cut_of(b, total_b), h, gmt);
-      gc += b.pairing && (gmt & 1) ? b.part_rows / 2 : 0;
-      g_part = b.part_o;
-      g_lse = b.part_lse;
-      g_rows = b.part_rows;
-    }
-    ng = pg.np;
-  }
-  const int oc = m - mt * a.rt + ((a.pairing && (mt & 1)) ? a.part_rows / 2 : 0);
-  const bool mine = m0 + i < nrows && (g >= 0 || po.np > 1);
-  const int n = mine ? ng + po.np : 0;
-  int most = n;
-#pragma unroll
-  for (int o = kR / 2; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-  // piece p of this lane's row: its values and its log2-sum-exp
-  auto where = [&](int p, const float*& o, const float*& l) {
-    const bool isg = p < ng;
-    const Pieces& x = isg ? pg : po;
-    const int k = isg ? p : p - ng;
-    if (x.np == 1) {
-      const size_t at = size_t(isg ? 0 : 1) * a.N * a.H_q + out;
-      o = a.row_o + at * a.d;
-      l = a.row_lse + at;
-    } else {
-      const size_t at = size_t(k == 0 ? x.slot0 : 2 * (x.ca + k)) * (isg ? g_rows : a.part_rows) + (isg ? gc : oc);
-      o = (isg ? g_part : a.part_o) + at * a.d;
-      l = (isg ? g_lse : a.part_lse) + at;
-    }
-  };
-  float M = -INFINITY, L0 = -INFINITY;
-  for (int p = lane / kR; p < n; p += kP) {
-    const float *o, *l;
-    where(p, o, l);
-    const float L = *l;
-    if (p < kP) L0 = L;
-    M = fmaxf(M, L);
-  }
-#pragma unroll
-  for (int o = kR; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float sum = 0.f;
-  float4 acc[kR][2];
-#pragma unroll
-  for (int k = 0; k < kR; ++k) acc[k][0] = acc[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int p0 = 0; p0 < most; p0 += kP) {
-    const int p = p0 + lane / kR;
-    float wt = 0.f;
-    unsigned long long src = 0;
-    if (p < n) {
-      const float *o, *l;
-      where(p, o, l);
-      const float L = p0 == 0 ? L0 : *l;
-      wt = L == -INFINITY ? 0.f : exp2f(L - M);     // nothing visible in this piece (M may be -inf as well)
-      src = reinterpret_cast<unsigned long long>(o);
-    }
-    sum += wt;
-    const int np = min(kP, most - p0);
+  Rec grp;
+  if (g >= 0) grp = a.recs[g];
+  const int i = lane % kR;
 #pragma unroll 1
-    for (int c = 0; c < 2; ++c) {
-      const int col = 4 * lane + 128 * c;
-      if (128 * c >= a.d) break;
+  for (int m0 = int(blockIdx.z) * kMergeRows + warp * kR; m0 < last; m0 += 8 * kR) {
+    // this lane's row and piece
+    const int m = min(m0 + i, nrows - 1);
+    const int mt = m / a.rt;
+    const Pieces po = pieces_of(a, own, cut, h, mt);
+    if (g < 0 && !__any_sync(0xffffffffu, po.np > 1)) continue;
+    const int t = m / a.G;
+    const size_t out = size_t(own.o + t) * a.H_q + h * a.G + (m - t * a.G);
+    // row of a piece's slot: the second tile of a pair lies behind the first
+    const int oc = m - mt * a.rt + ((a.pairing && (mt & 1)) ? a.part_rows / 2 : 0);
+    Pieces pg = po;
+    int gc = 0, ng = 0;
+    if (g >= 0) {
+      const int gm = (own.o - grp.o) * a.G + m, gmt = gm / a.rt;
+      pg = pieces_of(a, grp, cut, h, gmt);
+      gc = gm - gmt * a.rt + ((a.pairing && (gmt & 1)) ? a.part_rows / 2 : 0);
+      ng = pg.np;
+    }
+    const bool mine = m0 + i < last && (g >= 0 || po.np > 1);
+    const int n = mine ? ng + po.np : 0;
+    int most = n;
+#pragma unroll
+    for (int o = kR / 2; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+    // place of piece p of this lane's row, in rows of d values; bit 63: among row_o
+    auto where = [&](int p) -> unsigned long long {
+      const bool isg = p < ng;
+      const int k = isg ? p : p - ng, np = isg ? pg.np : po.np;
+      if (np == 1) return (1ULL << 63) | (size_t(isg ? 0 : 1) * a.N * a.H_q + out);
+      return size_t(k == 0 ? (isg ? pg.slot0 : po.slot0) : 2 * ((isg ? pg.ca : po.ca) + k)) * a.part_rows + (isg ? gc : oc);
+    };
+    auto lse_at = [&](unsigned long long at) { return (at >> 63) ? a.row_lse[at & ~(1ULL << 63)] : a.part_lse[at]; };
+    auto row_at = [&](unsigned long long at) {
+      return reinterpret_cast<unsigned long long>((at >> 63) ? a.row_o + (at & ~(1ULL << 63)) * a.d : a.part_o + at * a.d);
+    };
+    unsigned long long src = 0;
+    float M = -INFINITY, L0 = -INFINITY;
+    for (int p = lane / kR; p < n; p += kP) {
+      const unsigned long long at = where(p);
+      const float L = lse_at(at);
+      if (p < kP) {
+        L0 = L;
+        src = row_at(at);
+      }
+      M = fmaxf(M, L);
+    }
+#pragma unroll
+    for (int o = kR; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float sum = 0.f;
+    float4 acc[kR][kCols];
+#pragma unroll
+    for (int k = 0; k < kR; ++k)
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) acc[k][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int p0 = 0; p0 < most; p0 += kP) {
+      const int p = p0 + lane / kR;
+      float wt = 0.f;
+      if (p < n) {
+        if (p0 > 0) {
+          const unsigned long long at = where(p);
+          L0 = lse_at(at);
+          src = row_at(at);
+        }
+        wt = L0 == -INFINITY ? 0.f : exp2f(L0 - M);     // nothing visible in this piece (M may be -inf as well)
+      }
+      sum += wt;
+      const int np = min(kP, most - p0);
 #pragma unroll 1
       for (int q0 = 0; q0 < np; q0 += kBatch) {
-        float4 v[8];
-        float w[8];
+        float4 v[kLoads][kCols];
+        float w[kLoads];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int from = min(q0 + u / kR, kP - 1) * kR + u % kR;
+        for (int u = 0; u < kLoads; ++u) {
+          const int q = q0 + u / kR, from = min(q, kP - 1) * kR + u % kR;
           w[u] = __shfl_sync(0xffffffffu, wt, from);
           const float* o = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, src, from));
-          if (q0 + u / kR >= np) w[u] = 0.f;
-          v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (w[u] != 0.f && col < a.d) v[u] = *reinterpret_cast<const float4*>(o + col);    // a NaN is not 0
+          if (q >= np) w[u] = 0.f;
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) {
+            const int col = 4 * lane + 128 * c;
+            v[u][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (w[u] != 0.f && col < a.d) v[u][c] = *reinterpret_cast<const float4*>(o + col);    // a NaN is not 0
+          }
         }
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          float4& x = c == 0 ? acc[u % kR][0] : acc[u % kR][1];
-          x.x = fmaf(w[u], v[u].x, x.x); x.y = fmaf(w[u], v[u].y, x.y);
-          x.z = fmaf(w[u], v[u].z, x.z); x.w = fmaf(w[u], v[u].w, x.w);
-        }
+        for (int u = 0; u < kLoads; ++u)
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) {
+            float4& x = acc[u % kR][c];
+            x.x = fmaf(w[u], v[u][c].x, x.x); x.y = fmaf(w[u], v[u][c].y, x.y);
+            x.z = fmaf(w[u], v[u][c].z, x.z); x.w = fmaf(w[u], v[u][c].w, x.w);
+          }
       }
     }
-  }
 #pragma unroll
-  for (int o = kR; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    for (int o = kR; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
-  for (int k = 0; k < kR; ++k) {
-    const float f = __shfl_sync(0xffffffffu, inv, k);
-    const unsigned long long at = __shfl_sync(0xffffffffu, (unsigned long long)out, k);
-    if (!__shfl_sync(0xffffffffu, mine ? 1 : 0, k)) continue;
+    for (int k = 0; k < kR; ++k) {
+      const float f = __shfl_sync(0xffffffffu, inv, k);
+      const unsigned long long at = __shfl_sync(0xffffffffu, (unsigned long long)out, k);
+      if (!__shfl_sync(0xffffffffu, mine ? 1 : 0, k)) continue;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int col = 4 * lane + 128 * c;
-      if (col < a.d)
-        store4(static_cast<T*>(a.o) + at * a.d + col,
-               make_float4(acc[k][c].x * f, acc[k][c].y * f, acc[k][c].z * f, acc[k][c].w * f));
+      for (int c = 0; c < kCols; ++c) {
+        const int col = 4 * lane + 128 * c;
+        if (col < a.d)
+          store4(static_cast<T*>(a.o) + at * a.d + col,
+                 make_float4(acc[k][c].x * f, acc[k][c].y * f, acc[k][c].z * f, acc[k][c].w * f));
+      }
     }
+    if (mine && lane < kR && a.lse) a.lse[out] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
   }
-  if (mine && lane < kR && a.lse) a.lse[out] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
+}
+
+template <typename T>
+static spec_status_t launch_merge(const Dev& a, cudaStream_t s) {
+  const long long rows = (long long)a.T_max * a.G;
+  const dim3 grid(a.B, a.H_kv, unsigned((rows + kMergeRows - 1) / kMergeRows));
+  const bool few = rows <= kMergeFew, wide = a.d > 128;
+  return launch_result(launch_pdl(few ? (wide ? span_merge_kernel<T, 1, 2> : span_merge_kernel<T, 1, 1>)
+                                      : (wide ? span_merge_kernel<T, 2, 2> : span_merge_kernel<T, 2, 1>),
+                                  grid, dim3(256), 0, s, a));
 }
 
 // ------------------------------------------------------------------------------ host
@@ -479,21 +490,16 @@ static spec_status_t check(const Args& x) {
   return SPEC_OK;
 }
 
-// The kernels of a call, each with a stream of its own: on the tensor cores the rows kernel when no request
-// has more than 16 query rows a head (all requests, and the groups that have no more either), and beside it
-// the tile kernel for larger groups; the tile kernel alone when requests have more rows (their groups do too);
-// else the kernel on the CUDA cores.  Single tokens of 64 requests (64 query heads on 8) over a window of
-// 4096: XX us by the rows kernel, 191 by the tile kernel.
+// The kernel of a call: on the tensor cores the rows kernel for windows over at most 16 query rows a request
+// and head (64 single tokens, 64 query heads on 8, window 4096: 171 us against 191 by the tile kernel; one
+// token, window 1024: 18 against 25), else the tile kernel, which also takes a shared call's few-rowed requests
+// beside their groups (8 groups of 8 single tokens, 32 heads on 8, 8192 shared: 95 us; by one kernel for the
+// groups and then the other 112); the CUDA-core kernel for everything else.
 enum Kernel { kSimt, kTile, kFew };
-struct Part {
+struct Plan {
   Kernel kernel;
   int ctas, rt, bn, part_rows;
-  size_t recs, sum, part_o, part_lse;
-};
-struct Plan {
-  int n;               // parts; the requests are in the first
-  Part part[2];
-  size_t row_o, row_lse, total;
+  size_t recs, sum, part_o, part_lse, row_o, row_lse, total;
 };
 
 static Plan plan(const Args& x) {
@@ -501,35 +507,27 @@ static Plan plan(const Args& x) {
   Plan w;
   const int sms = sm_count_current_device();
   const size_t d = size_t(p->head_dim), rows = size_t(p->N) * p->H_q;
-  const bool few = (long long)p->T_max * (p->H_q / p->H_kv) <= kFewRows;
-  w.n = 1;
-  w.part[0].kernel = !tc_takes(p) ? kSimt : few ? kFew : kTile;
-  if (w.part[0].kernel == kFew && x.num_groups > 0) {
-    w.n = 2;
-    w.part[1].kernel = kTile;
+  const bool few = x.num_groups == 0 && (long long)p->T_max * (p->H_q / p->H_kv) <= kFewRows;
+  w.kernel = !tc_takes(p) ? kSimt : few ? kFew : kTile;
+  w.ctas = sms;
+  if (w.kernel == kSimt) {
+    w.ctas = sms * (p->head_dim <= 64 ? 3 : p->head_dim <= 128 ? 2 : 1);   // resident at once
+    w.rt = w.part_rows = kSimtRows;
+    w.bn = kSimtKeys;
+  } else if (w.kernel == kTile) {
+    w.rt = tc_row_tile(p);
+    w.bn = 128;
+    w.part_rows = 256;
+  } else {
+    w.rt = w.part_rows = kFewRows;
+    w.bn = 128;
   }
+  if (w.ctas > kMaxCtas) w.ctas = kMaxCtas;
   size_t off = 0;
-  for (int i = 0; i < w.n; ++i) {
-    Part& t = w.part[i];
-    t.ctas = sms;
-    if (t.kernel == kSimt) {
-      t.ctas = sms * (p->head_dim <= 64 ? 3 : p->head_dim <= 128 ? 2 : 1);   // resident at once
-      t.rt = t.part_rows = kSimtRows;
-      t.bn = kSimtKeys;
-    } else if (t.kernel == kTile) {
-      t.rt = tc_row_tile(p);
-      t.bn = 128;
-      t.part_rows = 256;
-    } else {
-      t.rt = t.part_rows = kFewRows;
-      t.bn = 128;
-    }
-    if (t.ctas > kMaxCtas) t.ctas = kMaxCtas;
-    t.recs = off; off = align_up(off + sizeof(Rec) * (size_t(x.num_groups) + p->B), 256);
-    t.sum = off; off += 256;
-    t.part_o = off; off = align_up(off + sizeof(float) * 2 * t.ctas * t.part_rows * d, 256);
-    t.part_lse = off; off = align_up(off + sizeof(float) * 2 * t.ctas * t.part_rows, 256);
-  }
+  w.recs = off; off = align_up(off + sizeof(Rec) * (size_t(x.num_groups) + p->B), 256);
+  w.sum = off; off += 256;
+  w.part_o = off; off = align_up(off + sizeof(float) * 2 * w.ctas * w.part_rows * d, 256);
+  w.part_lse = off; off = align_up(off + sizeof(float) * 2 * w.ctas * w.part_rows, 256);
   w.row_o = w.row_lse = off;
   if (x.num_groups > 0) {
     w.row_o = off; off = align_up(off + sizeof(float) * 2 * rows * d, 256);
@@ -539,9 +537,13 @@ static Plan plan(const Args& x) {
   return w;
 }
 
-static Dev device_params(const Args& x, const Plan& w, const Part& t, char* base) {
+static spec_status_t launch(const Args& x, void* ws, size_t ws_bytes, cudaStream_t s) {
   const spec_attn_params* p = x.p;
-  Dev d;
+  const Plan w = plan(x);
+  if (w.ctas <= 0) return SPEC_ERR_CUDA;
+  if (!ws || ws_bytes < w.total || (reinterpret_cast<uintptr_t>(ws) & 255u)) return SPEC_ERR_INVALID_ARG;
+  char* base = static_cast<char*>(ws);
+  Dev d{};
   d.block_table = p->block_table;
   d.prefix_len = p->prefix_len;
   d.node_offset = p->node_offset;
@@ -551,65 +553,39 @@ static Dev device_params(const Args& x, const Plan& w, const Part& t, char* base
   d.q = p->q; d.k = p->k_cache; d.v = p->v_cache; d.o = p->o;
   d.lse = p->lse;
   d.req_status = p->req_status;
-  d.recs = reinterpret_cast<Rec*>(base + t.recs);
-  d.total = reinterpret_cast<long long*>(base + t.sum);
-  d.part_o = reinterpret_cast<float*>(base + t.part_o);
-  d.part_lse = reinterpret_cast<float*>(base + t.part_lse);
+  d.recs = reinterpret_cast<Rec*>(base + w.recs);
+  d.total = reinterpret_cast<long long*>(base + w.sum);
+  d.part_o = reinterpret_cast<float*>(base + w.part_o);
+  d.part_lse = reinterpret_cast<float*>(base + w.part_lse);
   d.row_o = reinterpret_cast<float*>(base + w.row_o);
   d.row_lse = reinterpret_cast<float*>(base + w.row_lse);
   d.B = p->B; d.N = p->N; d.Gn = x.num_groups; d.H_q = p->H_q; d.H_kv = p->H_kv; d.G = p->H_q / p->H_kv;
   d.d = p->head_dim; d.bs = p->block_size; d.T_max = p->T_max; d.W = (p->T_max + 31) / 32;
-  d.num_blocks = p->num_blocks; d.max_blocks = p->max_blocks_per_req; d.ctas = t.ctas;
+  d.num_blocks = p->num_blocks; d.max_blocks = p->max_blocks_per_req; d.ctas = w.ctas;
   d.window = x.window; d.sinks = x.sinks;
-  d.rt = t.rt; d.bn = t.bn; d.part_rows = t.part_rows; d.pairing = t.kernel == kTile ? 1 : 0;
-  d.e_lo = 0;
-  d.e_hi = d.Gn + d.B;
-  d.rows_lo = 1;
-  d.rows_hi = 0x7fffffff;
-  if (t.kernel == kFew) {
-    d.rows_hi = kFewRows;
-  } else if (w.n == 2) {         // the groups that the rows kernel leaves
-    d.rows_lo = kFewRows + 1;
-    d.e_hi = d.Gn;
-  }
+  d.rt = w.rt; d.bn = w.bn; d.part_rows = w.part_rows; d.pairing = w.kernel == kTile ? 1 : 0;
   d.cost_pair = kPairCost;
-  d.cost_single = t.kernel == kTile ? kSingleCost : t.kernel == kFew ? kRowsTileCost : 1;
-  d.cost_unit = t.kernel == kTile ? kUnitCost : t.kernel == kFew ? kRowsUnitCost : 0;
-  d.cost_min = t.kernel == kTile ? kMinCost : t.kernel == kFew ? kRowsMinCost : 4;
+  d.cost_single = w.kernel == kTile ? kSingleCost : w.kernel == kFew ? kRowsTileCost : 1;
+  d.cost_unit = w.kernel == kTile ? kUnitCost : w.kernel == kFew ? kRowsUnitCost : 0;
+  d.cost_min = w.kernel == kTile ? kMinCost : w.kernel == kFew ? kRowsMinCost : 4;
   const float scale = p->scale > 0.f ? p->scale : 1.f / sqrtf(float(p->head_dim));
   d.scale_log2 = scale * 1.4426950408889634f;
-  return d;
-}
-
-static spec_status_t launch(const Args& x, void* ws, size_t ws_bytes, cudaStream_t s) {
-  const spec_attn_params* p = x.p;
-  const Plan w = plan(x);
-  if (w.part[0].ctas <= 0) return SPEC_ERR_CUDA;
-  if (!ws || ws_bytes < w.total || (reinterpret_cast<uintptr_t>(ws) & 255u)) return SPEC_ERR_INVALID_ARG;
-  const Dev a = device_params(x, w, w.part[0], static_cast<char*>(ws));
-  const Dev b = w.n == 2 ? device_params(x, w, w.part[1], static_cast<char*>(ws)) : a;
   const bool bf16 = p->dtype == SPEC_BF16;
-  spec_status_t st = SPEC_OK;
-  if (w.part[0].kernel == kSimt) {
+  spec_status_t st;
+  if (w.kernel == kSimt) {
     static DeviceOnce raised_f32, raised_bf16;
     st = bf16 ? raise_dyn_smem_once(span_simt_kernel<__nv_bfloat16>, simt_smem(256), raised_bf16)
               : raise_dyn_smem_once(span_simt_kernel<float>, simt_smem(256), raised_f32);
     if (st == SPEC_OK)
       st = launch_result(launch_pdl(bf16 ? span_simt_kernel<__nv_bfloat16> : span_simt_kernel<float>,
-                                    dim3(a.ctas), dim3(kSimtThreads), size_t(simt_smem(p->head_dim)), s, a));
+                                    dim3(w.ctas), dim3(kSimtThreads), size_t(simt_smem(p->head_dim)), s, d));
   } else {
     TcMaps m;
     st = make_tc_maps(p, m);
-    if (st == SPEC_OK && w.n == 2) st = launch_span_tc(b, m, s);
-    if (st == SPEC_OK) st = w.part[0].kernel == kFew ? launch_span_rows(a, m, s) : launch_span_tc(a, m, s);
+    if (st == SPEC_OK) st = w.kernel == kFew ? launch_span_rows(d, m, s) : launch_span_tc(d, m, s);
   }
   if (st != SPEC_OK) return st;
-  const long long rows = (long long)p->T_max * a.G;
-  const bool one = rows <= kMergeFew;
-  const int per = one ? 8 : 16;
-  return launch_result(launch_pdl(bf16 ? (one ? span_merge_kernel<__nv_bfloat16, 1> : span_merge_kernel<__nv_bfloat16, 2>)
-                                       : (one ? span_merge_kernel<float, 1> : span_merge_kernel<float, 2>),
-                                  dim3(p->B, p->H_kv, unsigned((rows + per - 1) / per)), dim3(256), 0, s, a, b));
+  return bf16 ? launch_merge<__nv_bfloat16>(d, s) : launch_merge<float>(d, s);
 }
 
 static bool window_args(const spec_attn_window_params* p, Args& x) {

@@ -9,8 +9,7 @@
 // An entry has H_kv x (units) units; a unit is one or two row tiles of a KV head (`pairing`: two tiles
 // read every K/V tile once) over all of the entry's key tiles.  A unit costs cost_unit for its start and
 // end, and cost_pair or cost_single for each key tile; ranges are equal in cost, and a tile belongs to the
-// range that its first cost unit lies in.  A kernel's stream is a part of the entries (e_lo .. e_hi - 1):
-// a call's groups and requests may go to different kernels.
+// range that its first cost unit lies in.
 #pragma once
 
 #include <cuda.h>
@@ -21,7 +20,7 @@ namespace spec {
 namespace span {
 
 constexpr int kMaxCtas = 1024;
-constexpr int kGroupCache = 2048, kCostCache = 1024;   // group offsets, costs held in shared memory
+constexpr int kGroupCache = 1024, kCostCache = 1024, kEntryCache = 256;   // held in shared memory at the start
 
 struct Dev {
   const int32_t* block_table;
@@ -47,13 +46,11 @@ struct Dev {
   int rt;               // query rows of a row tile
   int bn;               // keys of a key tile
   int part_rows, pairing;
-  int e_lo, e_hi;       // entries of this kernel's stream,
-  int rows_lo, rows_hi; // those with so many query rows a head
   int cost_pair, cost_single, cost_unit, cost_min;   // cost_min: of a range at least
   float scale_log2;
 };
 
-// What the merge has to know of an entry: where it lies in its kernel's stream, its tokens and tiles.
+// What the merge has to know of an entry: where it lies in the stream, its tokens and tiles.
 struct Rec {
   long long beg;
   int o, T, nt, mts, group, pad;
@@ -71,7 +68,6 @@ __device__ __forceinline__ int units_of(const Dev& a, const Entry& e) {
 }
 // cost of one KV head of the entry
 __device__ __forceinline__ long long head_cost(const Dev& a, int mts, int nt) {
-  if (mts == 0) return 0;
   const int np = a.pairing ? mts >> 1 : 0, ns = mts - 2 * np;
   return (long long)(np * a.cost_pair + ns * a.cost_single) * nt + (long long)(np + ns) * a.cost_unit;
 }
@@ -107,8 +103,7 @@ __device__ __forceinline__ void key_tiles(const Dev& a, Entry& e) {
   e.nt0 = (e.sink + a.bn - 1) / a.bn;
   e.w0 = max(e.lo / a.bn, e.nt0);
   e.nt = e.nt0 + (e.end + a.bn - 1) / a.bn - e.w0;
-  const long long rows = (long long)e.T * a.G;
-  e.mts = rows < a.rows_lo || rows > a.rows_hi ? 0 : int((rows + a.rt - 1) / a.rt);
+  e.mts = int(((long long)e.T * a.G + a.rt - 1) / a.rt);
 }
 
 // Entry i of the stream (groups first).  `off`: the group offsets, possibly a copy.  mts = 0: no work.
@@ -206,19 +201,13 @@ struct Range {
   int e0, C;
 };
 
-// Scratch of the search: copies of the group offsets and of the entries' costs, where they fit.
+// Scratch of the search: the group offsets, the entries' costs and the first entries, where they fit.
 struct RangeScratch {
   long long cost[kCostCache];
+  Entry entry[kEntryCache];
   int32_t off[kGroupCache + 1];
 };
 
-// the group offsets, copied by a warp where they fit
-__device__ __forceinline__ const int32_t* copy_offsets(const Dev& a, RangeScratch& s) {
-  if (a.Gn < 1 || a.Gn > kGroupCache) return a.group_offset;
-  for (int i = threadIdx.x & 31; i <= a.Gn; i += 32) s.off[i] = a.group_offset[i];
-  __syncwarp();
-  return s.off;
-}
 __device__ __forceinline__ long long warp_scan(long long v) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -228,13 +217,31 @@ __device__ __forceinline__ long long warp_scan(long long v) {
   return v;
 }
 
-// One warp finds range c.
-__device__ __forceinline__ Range warp_range(const Dev& a, int c, RangeScratch& s) {
-  const int lane = threadIdx.x & 31, E = a.e_hi - a.e_lo;
-  const int32_t* off = copy_offsets(a, s);
+// All threads of the CTA: the costs of the first entries, in one or two round trips to memory.
+__device__ __forceinline__ void entry_costs(const Dev& a, RangeScratch& s) {
+  const int E = a.Gn + a.B;
+  const int32_t* off = a.group_offset;
+  if (a.Gn > 0 && a.Gn <= kGroupCache) {
+    for (int i = threadIdx.x; i <= a.Gn; i += blockDim.x) s.off[i] = a.group_offset[i];
+    __syncthreads();
+    off = s.off;
+  }
+#pragma unroll 1
+  for (int i = threadIdx.x; i < min(E, kCostCache); i += blockDim.x) {
+    int bad;
+    const Entry e = entry_of(a, off, i, bad);
+    s.cost[i] = head_cost(a, e.mts, e.nt) * a.H_kv;
+    if (i < kEntryCache) s.entry[i] = e;
+  }
+  __syncthreads();
+}
+
+// One warp finds range c; entry_costs has been there.  `first`: entry e0, if its length is not 0.
+__device__ __forceinline__ Range warp_range(const Dev& a, int c, RangeScratch& s, Entry& first) {
+  const int lane = threadIdx.x & 31, E = a.Gn + a.B;
   Range R;
   R.t0 = R.t1 = R.beg0 = 0;
-  R.e0 = a.e_lo;
+  R.e0 = 0;
   R.C = 0;
   long long sum = 0;            // pass 0: this lane's costs; pass 1: the cost before the chunk
 #pragma unroll 1
@@ -243,23 +250,29 @@ __device__ __forceinline__ Range warp_range(const Dev& a, int c, RangeScratch& s
     for (int i0 = 0; i0 < E; i0 += 32) {
       const int i = i0 + lane;
       long long cost = 0;
-      if (pass == 1 && i0 < kCostCache) {
-        cost = s.cost[i];
-      } else if (i < E) {
-        int bad;
-        const Entry e = entry_of(a, off, a.e_lo + i, bad);
-        cost = head_cost(a, e.mts, e.nt) * a.H_kv;
+      if (i < E) {
+        if (i < kCostCache) {
+          cost = s.cost[i];
+        } else {
+          int bad;
+          const Entry e = entry_of(a, a.Gn <= kGroupCache ? s.off : a.group_offset, i, bad);
+          cost = head_cost(a, e.mts, e.nt) * a.H_kv;
+        }
       }
       if (pass == 0) {
-        if (i0 < kCostCache) s.cost[i] = cost;
         sum += cost;
         continue;
       }
       const long long hi = warp_scan(cost) + sum, lo = hi - cost;
       const uint32_t here = __ballot_sync(0xffffffffu, cost > 0 && lo <= R.t0 && R.t0 < hi);
       if (here) {
-        R.e0 = a.e_lo + i0 + __ffs(here) - 1;
+        const int at = i0 + __ffs(here) - 1;
+        R.e0 = at;
         R.beg0 = __shfl_sync(0xffffffffu, lo, __ffs(here) - 1);
+        if (lane == 0) {
+          if (at < kEntryCache) first = s.entry[at];
+          else first.T = 0;
+        }
         return R;
       }
       sum = __shfl_sync(0xffffffffu, hi, 31);
@@ -273,7 +286,6 @@ __device__ __forceinline__ Range warp_range(const Dev& a, int c, RangeScratch& s
       R.t0 = range_start(cut, c);
       R.t1 = range_start(cut, c + 1);
       sum = 0;
-      __syncwarp();
     }
   }
   R.t1 = R.t0;      // never: the scan finds the entry
@@ -285,16 +297,16 @@ __device__ __forceinline__ Range warp_range(const Dev& a, int c, RangeScratch& s
 __device__ __forceinline__ bool reports(const Range& R, int ctas) {
   return int(blockIdx.x) == (R.C < ctas ? ctas - 1 : 0);
 }
-__device__ __forceinline__ void write_recs(const Dev& a, RangeScratch& s) {
+__device__ __forceinline__ void write_recs(const Dev& a) {
   const int lane = threadIdx.x & 31;
-  const int32_t* off = copy_offsets(a, s);
+  const int32_t* off = a.group_offset;
   long long sum = 0;
 #pragma unroll 1
-  for (int i0 = a.e_lo; i0 < a.e_hi; i0 += 32) {
+  for (int i0 = 0; i0 < a.Gn + a.B; i0 += 32) {
     const int i = i0 + lane;
     long long cost = 0;
     Rec r;
-    if (i < a.e_hi) {
+    if (i < a.Gn + a.B) {
       int bad;
       const Entry e = entry_of(a, off, i, bad);
       cost = head_cost(a, e.mts, e.nt) * a.H_kv;
@@ -302,7 +314,7 @@ __device__ __forceinline__ void write_recs(const Dev& a, RangeScratch& s) {
       r.o = e.o; r.T = e.T; r.nt = e.nt; r.mts = e.mts; r.group = e.group; r.pad = 0;
     }
     const long long hi = warp_scan(cost) + sum;
-    if (i < a.e_hi) {
+    if (i < a.Gn + a.B) {
       r.beg = hi - cost;
       a.recs[i] = r;
     }
@@ -327,17 +339,23 @@ struct Walker {
   long long eend;        // cost up to the entry's end
   int i, h, u, np, units;
   Entry e;
-  __device__ __forceinline__ void start(const Range& R) {
+  bool known;            // e is the entry to enter next
+  __device__ __forceinline__ void start(const Range& R, const Entry* first) {
     t = R.t0;
     i = R.e0 - 1;
     eend = R.beg0;      // next() enters e0
+    known = first != nullptr && first->T > 0;
+    if (known) e = *first;
   }
   __device__ __forceinline__ bool next(const Dev& a, const Range& R, Item& it) {
     while (t < R.t1) {
       while (t >= eend) {
-        if (++i >= a.e_hi) return false;
-        int bad;
-        e = entry_of(a, a.group_offset, i, bad);
+        if (++i >= a.Gn + a.B) return false;
+        if (!known) {
+          int bad;
+          e = entry_of(a, a.group_offset, i, bad);
+        }
+        known = false;
         const long long hc = head_cost(a, e.mts, e.nt);
         ubeg = eend;
         eend += hc * a.H_kv;

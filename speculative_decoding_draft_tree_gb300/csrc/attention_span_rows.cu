@@ -9,11 +9,15 @@
 // it), the second in columns of O of its own: N = 32, and V is read once.
 // Two groups of four warps take alternate key tiles, each with references, sums and accumulators of its own;
 // a further group joins the two and writes a unit's rows while the next one is under way.
-//   warp 0 Q, K by TMA; warp 2 V; warp 1 issues S^T, warp 3 O^T; warps 4-7, 8-11 softmax; 12-15 output;
-//   warp 16 walks the items, and lays out what a unit's rows see.
+//   warp 0 Q and K by TMA, warp 2 V; warp 1 issues S^T two tiles ahead of O^T, across units; warp 3 walks the
+//   items and lays out what a unit's rows see; warps 4-7, 8-11 softmax; 12-15 output.
 // References: weights are formed against the row's reference at hand.  bf16 has fp32's exponents, so a weight
 // of 2^60 is as good as one of 2^-1; only beyond that, and at a row's first visible key, the group agrees on
 // a new one (one vote a tile, no maxima).
+//
+// What runs once a unit (a reference's first setting, the output, masks) is kept short in instructions rather
+// than in steps: it comes from beyond the instruction cache every time.  The output unrolled over 16 rows with
+// its divisions and addresses took 5000 .. 28000 clocks a unit, as below 1000.
 //
 // The waits on mbarriers are bounded; one that runs out raises the abort flag.  The groups of four warps meet
 // at hardware barriers as well, so their warps leave together: every such barrier carries a vote on it.
@@ -30,7 +34,7 @@ namespace rows {
 constexpr int kD = 128;
 constexpr int kN = 16;                        // query rows of a unit
 constexpr int kKeys = 128;
-constexpr int kThreads = 544;
+constexpr int kThreads = 512;                 // 128 registers a thread
 constexpr int kAtom = 16384;                  // 128 rows x 128 B
 constexpr int kTile = 2 * kAtom;
 constexpr int kQAtom = kN * 128;              // Q: 16 rows x 64 columns, two of them
@@ -41,7 +45,7 @@ constexpr int kSmemP = 2 * 2 * kQAtom;        // behind two Q buffers: P of each
 constexpr int kSmemK = kSmemP + 2 * kAtom;
 constexpr int kSmemV = kSmemK + kKStages * kTile;
 constexpr int kSmemCtl = kSmemV + kVStages * kTile;
-constexpr uint32_t kTmemCols = 256;           // S^T: group, buffer: 4 x 16; O^T from 64 on: unit parity, group: 4 x 32
+constexpr uint32_t kTmemCols = 256;           // S^T: a group's 16; O^T from 64 on: unit parity, group: 4 x 32
 constexpr uint32_t kTmemO = 64;
 constexpr long long kWaitLimit = 4000000000LL;     // clock cycles (~2 s)
 constexpr float kFar = 60.f;                       // log2 units
@@ -58,18 +62,19 @@ struct RowsItem {
 struct Control {
   uint64_t q_full[2], q_empty[2];
   uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
-  uint64_t s_full[2][2], s_free[2][2], p_full[2], pv_done[2];
+  uint64_t s_full[2], p_full[2], pv_done[2];
   uint64_t sum_full[2], o_full[2], o_free[2];      // by unit parity
-  uint64_t item_full[kItems], item_empty[kItems], drain[2];
+  uint64_t item_full[kItems], item_empty[kItems], drain;
   alignas(16) RowsItem item[kItems];
   float sum[2][2][4][kN];         // unit parity, group, warp
   float ref[2][2][kN];
-  float top[2][4][kN];            // group, warp: maxima when a reference moves
+  alignas(16) float top[2][4][kN];      // group, warp: maxima when a reference moves
   Range range;
+  Entry first;
   uint32_t tmem;
   int abort;
-  RangeScratch report;
 };
+static_assert(sizeof(RangeScratch) <= size_t(kKStages * kTile), "the search's scratch lies in the tiles");
 constexpr int kSmemBytes = kSmemCtl + int(sizeof(Control));
 static_assert(kSmemBytes <= 232448, "fits one CTA's shared memory");
 
@@ -87,6 +92,12 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
   return p != 0;
 }
+// 32 lanes x 8 consecutive 32-bit columns
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
 // the 128 threads of a group vote at its barrier
 __device__ __forceinline__ bool group_any(int bar, bool v) {
   uint32_t r;
@@ -103,7 +114,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(a), "f"(b));
   return r;
 }
-// Sums of v[n] over the warp's lanes: lanes 2 n and 2 n + 1 get that of n (16 shuffles).
+// Sums (or maxima) of v[n] over the warp's lanes: lanes 2 n and 2 n + 1 get that of n (16 shuffles).
+template <bool kMax>
 __device__ __forceinline__ float reduce16(float (&v)[kN], int lane) {
 #pragma unroll
   for (int o = 8; o >= 1; o >>= 1) {
@@ -112,10 +124,12 @@ __device__ __forceinline__ float reduce16(float (&v)[kN], int lane) {
     for (int i = 0; i < o; ++i) {
       const float give = up ? v[i] : v[i + o];
       const float keep = up ? v[i + o] : v[i];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, 2 * o);
+      const float got = __shfl_xor_sync(0xffffffffu, give, 2 * o);
+      v[i] = kMax ? fmaxf(keep, got) : keep + got;
     }
   }
-  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
+  const float got = __shfl_xor_sync(0xffffffffu, v[0], 1);
+  return kMax ? fmaxf(v[0], got) : v[0] + got;
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -132,17 +146,14 @@ span_rows_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&c.q_full[i], 1);
       tc::mbar_init(&c.q_empty[i], 1);
-      for (int b = 0; b < 2; ++b) {
-        tc::mbar_init(&c.s_full[i][b], 1);
-        tc::mbar_init(&c.s_free[i][b], 4);
-      }
+      tc::mbar_init(&c.s_full[i], 1);
       tc::mbar_init(&c.p_full[i], 4);
       tc::mbar_init(&c.pv_done[i], 1);
       tc::mbar_init(&c.sum_full[i], 8);
       tc::mbar_init(&c.o_full[i], 1);
       tc::mbar_init(&c.o_free[i], 4);
-      tc::mbar_init(&c.drain[i], 1);
     }
+    tc::mbar_init(&c.drain, 1);
     for (int s = 0; s < kKStages; ++s) {
       tc::mbar_init(&c.k_full[s], 1);
       tc::mbar_init(&c.k_empty[s], 1);
@@ -153,7 +164,7 @@ span_rows_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__
     }
     for (int i = 0; i < kItems; ++i) {
       tc::mbar_init(&c.item_full[i], 1);
-      tc::mbar_init(&c.item_empty[i], 16);        // warps 0-3, eight of the softmax, four of the output
+      tc::mbar_init(&c.item_empty[i], 15);        // warps 0, 1, 2, eight of the softmax, four of the output
     }
     c.abort = (tc::smem_u32(smem) & 1023u) ? 1 : 0;      // the swizzle wants 1024-byte bounds
     tc::fence_mbar_init();
@@ -161,7 +172,7 @@ span_rows_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__
   if (warp == 0) {
     tc::tmem_alloc(&c.tmem, kTmemCols);
     tc::tmem_relinquish();
-  } else if (warp == 2 && lane == 0) {
+  } else if (warp == 1 && lane == 0) {
     tc::prefetch_tensormap(&mQ);
     tc::prefetch_tensormap(&mK);
     tc::prefetch_tensormap(&mV);
@@ -170,8 +181,9 @@ span_rows_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__
   }
   pdl_wait();
   pdl_trigger();
-  if (warp == 16) {
-    const Range mine = warp_range(a, blockIdx.x, *reinterpret_cast<RangeScratch*>(sK));
+  entry_costs(a, *reinterpret_cast<RangeScratch*>(sK));
+  if (warp == 3) {
+    const Range mine = warp_range(a, blockIdx.x, *reinterpret_cast<RangeScratch*>(sK), c.first);
     if (lane == 0) c.range = mine;
   }
   tc::tc_fence_before();
@@ -187,18 +199,18 @@ span_rows_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__
     const uint32_t parity = (ni / kItems) & 1;
     return one_lane ? tc::mbar_wait(bar, parity, abort_flag, kWaitLimit) : warp_wait(bar, parity, abort_flag);
   };
-  auto give_back = [&](bool one_lane) {
-    if (!one_lane) __syncwarp();
-    if (one_lane || lane == 0) tc::mbar_arrive(&c.item_empty[ni % kItems]);
+  auto give_back = [&](bool) {
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&c.item_empty[ni % kItems]);
     ++ni;
   };
   if (!layout_ok) {
     // fall through to the end: the range is reported
-  } else if (warp == 16) {
+  } else if (warp == 3) {
     // ===================================================================== items
     const Range R = c.range;
     Walker w;
-    if (lane == 0) w.start(R);
+    if (lane == 0) w.start(R, &c.first);
     bool more = true, ok = true;
     for (int n = 0; more && ok; ++n) {
       const int s = n % kItems;
@@ -314,121 +326,145 @@ span_rows_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__
       for (int k = max(0, qn - 2); k < qn; ++k)
         tc::mbar_wait(&c.q_full[k & 1], (k >> 1) & 1, &never, kWaitLimit / 8);
     }
-  } else if (warp == 1 || warp == 3) {
-    // ===================================================================== MMA issuers
-    const bool is_qk = warp == 1;
+  } else if (warp == 1) {
+    // ===================================================================== MMA issuer
+    // One thread issues S(0) S(1) | O(t) S(t+2) | ..: a group's S goes over the one that its P came from, and
+    // whoever has S of tile t + 2 knows that O's product of tile t is done and V's stage free.
     if (elect_one()) {
       const uint32_t id_qk = tc::idesc_bf16_f32(128, kN, false, false);
       const uint32_t id_pv = tc::idesc_bf16_f32(128, 2 * kN, true, true);
       const uint64_t dQ0 = tc::smem_desc(tc::smem_u32(smem), 16, 1024), dK0 = tc::smem_desc(tc::smem_u32(sK), 16, 1024);
       const uint64_t dV0 = tc::smem_desc(tc::smem_u32(sV), kAtom, 1024), dP0 = tc::smem_desc(tc::smem_u32(sP), kAtom, 1024);
-      int kt = 0, li = 0, gn[2] = {0, 0};      // tiles; items; tiles of each group
       bool ok = true;
-      for (; ok; ++li) {
-        ok = take(true);
-        const Item& it = c.item[ni % kItems].it;
-        if (!ok || it.j1 < 0) break;
-        const int nt = it.j1 - it.j0;
-        give_back(true);
-        if (is_qk) {
-          ok = tc::mbar_wait(&c.q_full[li & 1], (li >> 1) & 1, abort_flag, kWaitLimit);
-          for (int k = 0; ok && k < nt; ++k, ++kt) {
-            const int g = k & 1, n = g == 0 ? gn[0]++ : gn[1]++, buf = n & 1, st = kt % kKStages;
-            // (the third wait: the product before in V's stage, so that whoever has S of a tile finds the stage
-            // free of older tiles, and the phase of its barrier is the tile's own)
-            ok = tc::mbar_wait(&c.k_full[st], (kt / kKStages) & 1, abort_flag, kWaitLimit) &&
-                 (kt < kVStages || tc::mbar_wait(&c.v_empty[kt % kVStages], (kt / kVStages - 1) & 1, abort_flag, kWaitLimit)) &&
-                 (n < 2 || tc::mbar_wait(&c.s_free[g][buf], ((n >> 1) - 1) & 1, abort_flag, kWaitLimit));
-            if (!ok) break;
-            tc::tc_fence_after();
-            const uint64_t dk = dK0 + uint64_t(st) * (kTile >> 4), dq = dQ0 + uint64_t(li & 1) * (2 * kQAtom >> 4);
+      // the scores' place in the stream: item, tile of it, its tiles; tiles before; and the output's
+      int qi = -1, qk = 0, qnt = 0, qt = 0, pi = -1, pk = 0, pnt = 0, pt = 0;
+      bool q_end = false, p_end = false;
+      auto item_tiles = [&](int i, int& nt) -> bool {       // of item i; false: the stream ends
+        ok = ok && tc::mbar_wait(&c.item_full[i % kItems], (i / kItems) & 1, abort_flag, kWaitLimit);
+        if (!ok) return false;
+        const Item& it = c.item[i % kItems].it;
+        nt = it.j1 - it.j0;
+        return it.j1 >= 0;
+      };
+      auto score = [&] {
+        if (q_end) return;
+        if (qk == qnt) {
+          qk = 0;
+          if (!item_tiles(++qi, qnt)) { q_end = true; return; }
+          ok = tc::mbar_wait(&c.q_full[qi & 1], (qi >> 1) & 1, abort_flag, kWaitLimit);
+        }
+        const int st = qt % kKStages;
+        ok = ok && tc::mbar_wait(&c.k_full[st], (qt / kKStages) & 1, abort_flag, kWaitLimit);
+        if (!ok) return;
+        tc::tc_fence_after();
+        const uint64_t dk = dK0 + uint64_t(st) * (kTile >> 4), dq = dQ0 + uint64_t(qi & 1) * (2 * kQAtom >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              tc::mma_bf16_ss(tmem + 16 * (2 * g + buf), dk + uint64_t(((kk >> 2) * kAtom + (kk & 3) * 32) >> 4),
-                              dq + uint64_t(((kk >> 2) * kQAtom + (kk & 3) * 32) >> 4), id_qk, kk > 0 ? 1u : 0u);
-            tc::mma_commit(&c.s_full[g][buf]);
-            tc::mma_commit(&c.k_empty[st]);
-            if (k + 1 == nt) tc::mma_commit(&c.q_empty[li & 1]);
-          }
-        } else {
-          const int par = li & 1;
+        for (int kk = 0; kk < 8; ++kk)
+          tc::mma_bf16_ss(tmem + 16 * (qt & 1), dk + uint64_t(((kk >> 2) * kAtom + (kk & 3) * 32) >> 4),
+                          dq + uint64_t(((kk >> 2) * kQAtom + (kk & 3) * 32) >> 4), id_qk, kk > 0 ? 1u : 0u);
+        tc::mma_commit(&c.s_full[qt & 1]);
+        tc::mma_commit(&c.k_empty[st]);
+        ++qt;
+        if (++qk == qnt) tc::mma_commit(&c.q_empty[qi & 1]);
+      };
+      while (ok && !p_end) {
+        if (pk == pnt) {
+          pk = 0;
+          if (!item_tiles(++pi, pnt)) { p_end = true; break; }
           // the output warps have to have read what this parity's accumulators held
-          if (li > 1) ok = tc::mbar_wait(&c.o_free[par], ((li >> 1) - 1) & 1, abort_flag, kWaitLimit);
-          for (int k = 0; ok && k < nt; ++k, ++kt) {
-            const int g = k & 1, n = g == 0 ? gn[0]++ : gn[1]++, st = kt % kVStages;
-            ok = tc::mbar_wait(&c.p_full[g], n & 1, abort_flag, kWaitLimit) &&
-                 tc::mbar_wait(&c.v_full[st], (kt / kVStages) & 1, abort_flag, kWaitLimit);
-            if (!ok) break;
-            tc::tc_fence_after();
-            const uint64_t dv = dV0 + uint64_t(st) * (kTile >> 4), dp = dP0 + uint64_t(g) * (kAtom >> 4);
+          if (pi > 1) ok = tc::mbar_wait(&c.o_free[pi & 1], ((pi >> 1) - 1) & 1, abort_flag, kWaitLimit);
+        }
+        while (ok && !q_end && qt < pt + 2) score();
+        const int g = pt & 1, st = pt % kVStages, par = pi & 1;
+        ok = ok && tc::mbar_wait(&c.p_full[g], (pt >> 1) & 1, abort_flag, kWaitLimit) &&
+             tc::mbar_wait(&c.v_full[st], (pt / kVStages) & 1, abort_flag, kWaitLimit);
+        if (!ok) break;
+        tc::tc_fence_after();
+        const uint64_t dv = dV0 + uint64_t(st) * (kTile >> 4), dp = dP0 + uint64_t(g) * (kAtom >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)      // 16 keys: 2048 bytes of V and of P
-              tc::mma_bf16_ss(tmem + kTmemO + 32 * (2 * par + g), dv + uint64_t(kk * (2048 >> 4)), dp + uint64_t(kk * (2048 >> 4)),
-                              id_pv, kk > 0 || k > 1 ? 1u : 0u);
-            tc::mma_commit(&c.v_empty[st]);
-            tc::mma_commit(&c.pv_done[g]);
-          }
-          if (ok) tc::mma_commit(&c.o_full[par]);
+        for (int kk = 0; kk < 8; ++kk)      // 16 keys: 2048 bytes of V and of P
+          tc::mma_bf16_ss(tmem + kTmemO + 32 * (2 * par + g), dv + uint64_t(kk * (2048 >> 4)), dp + uint64_t(kk * (2048 >> 4)),
+                          id_pv, kk > 0 || pk > 1 ? 1u : 0u);
+        tc::mma_commit(&c.v_empty[st]);
+        tc::mma_commit(&c.pv_done[g]);
+        ++pt;
+        if (++pk == pnt) {
+          tc::mma_commit(&c.o_full[par]);
+          tc::mbar_arrive(&c.item_empty[pi % kItems]);
         }
       }
       if (!ok) *abort_flag = 1;
       // TMEM may not be freed under a product
-      tc::mma_commit(&c.drain[is_qk ? 0 : 1]);
+      tc::mma_commit(&c.drain);
       volatile int never = 0;
-      tc::mbar_wait(&c.drain[is_qk ? 0 : 1], 0, &never, kWaitLimit / 8);
+      tc::mbar_wait(&c.drain, 0, &never, kWaitLimit / 8);
     }
   } else if (warp >= 12) {
     // ===================================================================== output
-    if (warp == 12 && reports(c.range, gridDim.x)) write_recs(a, c.report);
+    if (warp == 12 && reports(c.range, gridDim.x)) write_recs(a);
     const int q4 = warp & 3, d = q4 * 32 + lane;       // this thread's column of the head
     const uint32_t lane_addr = uint32_t(q4 * 32) << 16;
     bool ok = true;
+    int kt0 = 0;                                       // tiles before the item
     for (int li = 0; ok; ++li) {
       ok = take(false);
       if (!ok || c.item[ni % kItems].it.j1 < 0) break;
       const RowsItem& r = c.item[ni % kItems];
       const Item& it = r.it;
       const int par = li & 1;
-      const bool two = it.j1 - it.j0 > 1;
+      const int nt = it.j1 - it.j0;
+      const bool has0 = nt > 1 || (kt0 & 1) == 0, has1 = nt > 1 || (kt0 & 1) == 1;     // groups with a tile of it
+      kt0 += nt;
       ok = warp_wait(&c.o_full[par], (li >> 1) & 1, abort_flag) && warp_wait(&c.sum_full[par], (li >> 1) & 1, abort_flag);
       if (!ok) break;
       tc::tc_fence_after();
-      uint32_t o0[32], o1[32];
-      tc::tmem_ld32(tmem + lane_addr + kTmemO + 32 * (2 * par), o0);
-      if (two) tc::tmem_ld32(tmem + lane_addr + kTmemO + 32 * (2 * par + 1), o1);
-      tc::tmem_ld_wait();
+      // lane n: row n's weights of the groups, log-sum-exp and place
+      const int n0 = lane & (kN - 1), nrows = r.nrows;
+      float f0 = 0.f, f1 = 0.f, lse2;
+      {
+        const float r0 = has0 ? c.ref[par][0][n0] : -INFINITY, r1 = has1 ? c.ref[par][1][n0] : -INFINITY;
+        // (without a reference the sum is 0, or NaN of a row that saw nothing else)
+        const float s0 = has0 ? (c.sum[par][0][0][n0] + c.sum[par][0][1][n0]) + (c.sum[par][0][2][n0] + c.sum[par][0][3][n0]) : 0.f;
+        const float s1 = has1 ? (c.sum[par][1][0][n0] + c.sum[par][1][1][n0]) + (c.sum[par][1][2][n0] + c.sum[par][1][3][n0]) : 0.f;
+        const float M = fmaxf(r0, r1);
+        const float w0 = r0 == -INFINITY ? s0 : ex2(r0 - M), w1 = r1 == -INFINITY ? s1 : ex2(r1 - M);
+        const float l = (w0 != 0.f ? w0 * s0 : 0.f) + (w1 != 0.f ? w1 * s1 : 0.f);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        f0 = w0 * inv;
+        f1 = w1 * inv;
+        lse2 = l == 0.f ? -INFINITY : M + __log2f(l);
+      }
+      const int t = n0 / a.G;
+      const size_t row = size_t(it.o + t) * a.H_q + it.h * a.G + (n0 - t * a.G);
+      const bool direct = it.slot == -1;
+      const size_t at = it.slot >= 0 ? size_t(it.slot) * a.part_rows + n0 : row;
+      const size_t both = it.slot == -3 ? size_t(a.N) * a.H_q : 0;
+      if (q4 == 0 && lane < nrows && lane < kN) {
+        if (it.slot >= 0) a.part_lse[at] = lse2;
+        else if (!direct) a.row_lse[both + at] = lse2;
+        else if (a.lse) a.lse[at] = lse2 * 0.6931471805599453f;
+      }
+      char* base = direct ? static_cast<char*>(a.o) : reinterpret_cast<char*>(it.slot >= 0 ? a.part_o : a.row_o + both * kD);
+      const unsigned long long mine = reinterpret_cast<unsigned long long>(base) + at * kD * (direct ? 2 : 4);
+      const uint32_t to = tmem + lane_addr + kTmemO + 64 * par;
+#pragma unroll 1
+      for (int n8 = 0; n8 < nrows; n8 += 8) {
+        // eight rows at a time: both pieces of both groups
+        uint32_t x[4][8];
+        tmem_ld8(to + n8, x[0]);
+        tmem_ld8(to + kN + n8, x[1]);
+        tmem_ld8(to + 32 + n8, x[2]);
+        tmem_ld8(to + 32 + kN + n8, x[3]);
+        tc::tmem_ld_wait();
 #pragma unroll
-      for (int n = 0; n < kN; ++n) {
-        if (n < r.nrows) {
-          const float r0 = c.ref[par][0][n], r1 = two ? c.ref[par][1][n] : -INFINITY;
-          const float M = fmaxf(r0, r1);
-          // (without a reference the sum is 0, or NaN of a row that saw nothing else)
-          const float s0 = (c.sum[par][0][0][n] + c.sum[par][0][1][n]) + (c.sum[par][0][2][n] + c.sum[par][0][3][n]);
-          const float s1 = two ? (c.sum[par][1][0][n] + c.sum[par][1][1][n]) + (c.sum[par][1][2][n] + c.sum[par][1][3][n]) : 0.f;
-          const float w0 = r0 == -INFINITY ? s0 : ex2(r0 - M), w1 = r1 == -INFINITY ? s1 : ex2(r1 - M);
-          float l = 0.f, v = 0.f;
-          if (w0 != 0.f) {
-            l = w0 * s0;
-            v = w0 * (__uint_as_float(o0[n]) + __uint_as_float(o0[kN + n]));
-          }
-          if (w1 != 0.f) {
-            l += w1 * s1;
-            v += w1 * (__uint_as_float(o1[n]) + __uint_as_float(o1[kN + n]));
-          }
-          v = l == 0.f ? 0.f : v / l;
-          const float lse2 = l == 0.f ? -INFINITY : M + log2f(l);
-          const int t = n / a.G;
-          const size_t out = size_t(it.o + t) * a.H_q + it.h * a.G + (n - t * a.G);
-          if (it.slot == -1) {
-            static_cast<__nv_bfloat16*>(a.o)[out * kD + d] = __float2bfloat16_rn(v);
-            if (d == 0 && a.lse) a.lse[out] = lse2 * 0.6931471805599453f;
-          } else if (it.slot >= 0) {
-            a.part_o[(size_t(it.slot) * a.part_rows + n) * kD + d] = v;
-            if (d == 0) a.part_lse[size_t(it.slot) * a.part_rows + n] = lse2;
-          } else {
-            const size_t at = size_t(it.slot == -2 ? 0 : 1) * a.N * a.H_q + out;
-            a.row_o[at * kD + d] = v;
-            if (d == 0) a.row_lse[at] = lse2;
+        for (int i = 0; i < 8; ++i) {
+          const float a0 = __shfl_sync(0xffffffffu, f0, n8 + i), a1 = __shfl_sync(0xffffffffu, f1, n8 + i);
+          const unsigned long long dst = __shfl_sync(0xffffffffu, mine, n8 + i);
+          float v = a0 == 0.f ? 0.f : a0 * (__uint_as_float(x[0][i]) + __uint_as_float(x[1][i]));
+          if (a1 != 0.f) v = fmaf(a1, __uint_as_float(x[2][i]) + __uint_as_float(x[3][i]), v);
+          if (n8 + i < nrows) {
+            if (direct) *(reinterpret_cast<__nv_bfloat16*>(dst) + d) = __float2bfloat16_rn(v);
+            else *(reinterpret_cast<float*>(dst) + d) = v;
           }
         }
       }
@@ -461,144 +497,88 @@ span_rows_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__
         sum[n] = 0.f;
       }
       bool leave = false;
-      for (int k = g; k < nt; k += 2, ++sn) {
+      for (int k = (g ^ kt0) & 1; k < nt; k += 2, ++sn) {       // tiles alternate across units
         const int j = j0 + k, kb = (j < nt0 ? j : j + skip) * kKeys, key = kb + kl;
         const bool masked = !(kb + kKeys <= P && (kb >= lo_max || kb + kKeys <= a.sinks));
         uint32_t vis = (1u << kN) - 1u;
         if (masked) {
           vis = 0;
           const int tree = key - P;
-#pragma unroll
-          for (int n = 0; n < kN; ++n) {
+#pragma unroll 1
+          for (int n = 0; n < nrows; ++n) {
             const bool v = tree < 0 ? key >= r.lo[n] || key < a.sinks : tree < 32 && ((r.anc[n] >> (tree & 31)) & 1u);
-            vis |= n < nrows && v ? 1u << n : 0u;
+            vis |= v ? 1u << n : 0u;
           }
         }
-        ok = ok && warp_wait(&c.s_full[g][sn & 1], (sn >> 1) & 1, abort_flag);
-        bool broken = false;         // V of this thread's key is not finite
-        if (ok && masked) {
-          // V's rows, 32 a warp, eight lanes a row.  S of this tile was issued after the product that read the
-          // older tile in V's stage.
-          const int gv = kt0 + k, st = gv % kVStages;
-          ok = warp_wait(&c.v_full[st], (gv / kVStages) & 1, abort_flag);
-          if (ok) {
-            uint8_t* tile = sV + st * kTile + (q4 * 32 + (lane >> 3)) * 128 + (lane & 7) * 16;
-            const int key0 = kb + q4 * 32 + (lane >> 3), end = r.it.end, sink = r.it.sink, lo = r.it.lo;
-            uint32_t word = 0;
-            bool wrote = false;
-#pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-              uint8_t* p = tile + half * kAtom;
-              uint32_t hits = 0;           // bit i: an exponent of all ones in row 4 i + lane / 8
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const uint4 x = *reinterpret_cast<const uint4*>(p + i * 512);
-                const int kk = key0 + 4 * i;
-                const bool seen = kk < sink || (kk >= lo && kk < end);
-                // the addition carries into a half word's sign bit from an exponent of all ones only
-                const uint32_t t = ((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
-                                   ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u);
-                if (!seen) {
-                  *reinterpret_cast<uint4*>(p + i * 512) = make_uint4(0, 0, 0, 0);
-                  wrote = true;
-                } else if (t & 0x80008000u) {
-                  hits |= 1u << i;
-                }
-              }
-              if (__any_sync(0xffffffffu, hits != 0u)) {
-#pragma unroll 1
-                for (int i = 0; i < 8; ++i) {
-                  const bool hit = (hits >> i) & 1u;
-                  if (hit) {
-                    uint32_t* w = reinterpret_cast<uint32_t*>(p + i * 512);
-                    for (int e = 0; e < 4; ++e) {
-                      if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u;
-                      if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0xffffu;
-                    }
-                    wrote = true;
-                  }
-                  const uint32_t lanes = __ballot_sync(0xffffffffu, hit);
-                  for (int e = 0; e < 4; ++e) word |= ((lanes >> (8 * e)) & 0xffu) ? 1u << (4 * i + e) : 0u;
-                }
-              }
-            }
-            if (wrote) tc::fence_proxy_async_smem();
-            broken = (word >> lane) & 1u;      // a warp looks at its own lanes' keys
-          }
-        }
+        ok = ok && warp_wait(&c.s_full[g], sn & 1, abort_flag);
         uint32_t x[kN];
         if (ok) {
           tc::tc_fence_after();
-          tc::tmem_ld16(tmem + lane_addr + 16 * (2 * g + (sn & 1)), x);
+          tc::tmem_ld16(tmem + lane_addr + 16 * g, x);
           tc::tmem_ld_wait();
-          tc::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&c.s_free[g][sn & 1]);
         } else {
 #pragma unroll
           for (int n = 0; n < kN; ++n) x[n] = 0;
         }
-        if (masked) {
-#pragma unroll
-          for (int n = 0; n < kN; ++n) {
-            // a masked score is the most negative number there is, so that it stays one when a reference is
-            // taken off; a row that sees a key whose V is not finite becomes NaN
-            if (!((vis >> n) & 1u)) x[n] = __float_as_uint(-3.0e38f);
-            else if (broken) x[n] = __float_as_uint(NAN);
-          }
-        }
-        // exponents; beyond kFar (a row's first visible key: +inf) the references move
+        // Exponents; beyond kFar (a row's first visible key: +inf) the references move, and they are formed
+        // again.  A masked key has the exponent -inf.
         float y[kN];
-        auto exponents = [&] {
+        while (true) {
           const uint64_t slv = f2_pack(sl2, sl2);
+          float ym = -INFINITY;
 #pragma unroll
-          for (int n = 0; n < kN; n += 2)
+          for (int n = 0; n < kN; n += 2) {
             f2_unpack(f2_fma(f2_pack(__uint_as_float(x[n]), __uint_as_float(x[n + 1])), slv, f2_pack(neg[n], neg[n + 1])), y[n], y[n + 1]);
-          if (masked) {
-#pragma unroll
-            for (int n = 0; n < kN; ++n) y[n] = (vis >> n) & 1u ? y[n] : -INFINITY;
+            if (masked) {
+              y[n] = (vis >> n) & 1u ? y[n] : -INFINITY;
+              y[n + 1] = (vis >> (n + 1)) & 1u ? y[n + 1] : -INFINITY;
+            }
+            ym = fmax3(ym, y[n], y[n + 1]);
           }
-        };
-        exponents();
-        float ym = fmaxf(y[0], y[1]);
-#pragma unroll
-        for (int n = 2; n < kN; n += 2) ym = fmax3(ym, y[n], y[n + 1]);
-        if (group_any(bar, ym > kFar || !ok)) {
-          if (group_any(bar, !ok)) { leave = true; break; }
+          if (!group_any(bar, ym > kFar || !ok)) break;
           // the group's maxima of all rows
+          float v[kN];
 #pragma unroll
-          for (int n = 0; n < kN; ++n) {
-            const float v = n < nrows && ((vis >> n) & 1u) ? __uint_as_float(x[n]) * sl2 : -INFINITY;
-            const float t = warp_max(v);
-            if (lane == 0) c.top[g][q4][n] = t;
-          }
-          ok = k == g || warp_wait(&c.pv_done[g], (sn - 1) & 1, abort_flag);
+          for (int n = 0; n < kN; ++n) v[n] = (vis >> n) & 1u ? __uint_as_float(x[n]) : -INFINITY;
+          const float mine = reduce16<true>(v, lane) * sl2;
+          if ((lane & 1) == 0) c.top[g][q4][lane >> 1] = mine;
+          if (ok && k > 1) ok = warp_wait(&c.pv_done[g], (sn - 1) & 1, abort_flag);
           if (group_any(bar, !ok)) { leave = true; break; }       // and the maxima are there
           tc::tc_fence_after();
           float f[kN];
 #pragma unroll
-          for (int n = 0; n < kN; ++n) {
-            const float t = fmaxf(fmaxf(c.top[g][0][n], c.top[g][1][n]), fmaxf(c.top[g][2][n], c.top[g][3][n]));
-            f[n] = 1.f;
-            if (n < nrows && t > -neg[n]) {
-              f[n] = neg[n] == INFINITY ? 1.f : ex2(-neg[n] - t);
-              neg[n] = -t;
-            }
-            sum[n] *= f[n];
-          }
-          if (k != g) {
-            uint32_t o[32];
-            const uint32_t to = tmem + lane_addr + kTmemO + 32 * (2 * par + g);
-            tc::tmem_ld32(to, o);
-            tc::tmem_ld_wait();
+          for (int n = 0; n < kN; n += 4) {
+            float t[4];
+            *reinterpret_cast<float4*>(t) = *reinterpret_cast<const float4*>(&c.top[g][0][n]);
 #pragma unroll
-            for (int n = 0; n < 32; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * f[n & (kN - 1)]);
-            tc::tmem_st32(to, o);
+            for (int w = 1; w < 4; ++w) {
+              const float4 u = *reinterpret_cast<const float4*>(&c.top[g][w][n]);
+              t[0] = fmaxf(t[0], u.x); t[1] = fmaxf(t[1], u.y); t[2] = fmaxf(t[2], u.z); t[3] = fmaxf(t[3], u.w);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              // (not a row: neg = -inf, nothing is above +inf; no reference yet: 2^-inf = 0 of a sum of 0)
+              const bool up = t[i] > -neg[n + i];
+              f[n + i] = up && neg[n + i] != INFINITY ? ex2(-neg[n + i] - t[i]) : 1.f;
+              neg[n + i] = up ? -t[i] : neg[n + i];
+              sum[n + i] *= f[n + i];
+            }
+          }
+          if (k > 1) {
+#pragma unroll 1
+            for (int piece = 0; piece < 2; ++piece) {
+              uint32_t o[kN];
+              const uint32_t to = tmem + lane_addr + kTmemO + 32 * (2 * par + g) + kN * piece;
+              tc::tmem_ld16(to, o);
+              tc::tmem_ld_wait();
+#pragma unroll
+              for (int n = 0; n < kN; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * f[n]);
+              tc::tmem_st16(to, o);
+            }
             tc::tmem_st_wait();
           }
-          exponents();
-          if (group_any(bar, false)) { leave = true; break; }     // the maxima have been read
         }
+        if (leave) break;
         uint32_t hi[kN / 2], lo[kN / 2];
 #pragma unroll
         for (int n = 0; n < kN; n += 2) {
@@ -616,6 +596,57 @@ span_rows_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__
         *reinterpret_cast<uint4*>(prow + ((1 ^ sw) << 4)) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
         *reinterpret_cast<uint4*>(prow + ((2 ^ sw) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         *reinterpret_cast<uint4*>(prow + ((3 ^ sw) << 4)) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+        if (ok && masked) {
+          // V's rows, 32 a warp, eight lanes a row; by now V has mostly come.  S of this tile was issued after the
+          // product that read the older tile in V's stage.
+          const int gv = kt0 + k, st = gv % kVStages;
+          ok = warp_wait(&c.v_full[st], (gv / kVStages) & 1, abort_flag);
+          if (ok) {
+            uint8_t* tile = sV + st * kTile + (q4 * 32 + (lane >> 3)) * 128 + (lane & 7) * 16;
+            const int key0 = kb + q4 * 32 + (lane >> 3), end = r.it.end, sink = r.it.sink, lo = r.it.lo;
+            uint32_t word = 0;
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+              uint8_t* p = tile + half * kAtom;
+              uint32_t hits = 0;           // bit i: an exponent of all ones in row 4 i + lane / 8
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const uint4 x = *reinterpret_cast<const uint4*>(p + i * 512);
+                const int kk = key0 + 4 * i;
+                const bool seen = kk < sink || (kk >= lo && kk < end);
+                // the addition carries into a half word's sign bit from an exponent of all ones only
+                const uint32_t t = ((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
+                                   ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u);
+                if (!seen) {
+                  *reinterpret_cast<uint4*>(p + i * 512) = make_uint4(0, 0, 0, 0);
+                } else if (t & 0x80008000u) {
+                  hits |= 1u << i;
+                }
+              }
+              if (__any_sync(0xffffffffu, hits != 0u)) {
+#pragma unroll 1
+                for (int i = 0; i < 8; ++i) {
+                  const bool hit = (hits >> i) & 1u;
+                  if (hit) {
+                    uint32_t* w = reinterpret_cast<uint32_t*>(p + i * 512);
+                    for (int e = 0; e < 4; ++e) {
+                      if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u;
+                      if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0xffffu;
+                    }
+                  }
+                  const uint32_t lanes = __ballot_sync(0xffffffffu, hit);
+                  for (int e = 0; e < 4; ++e) word |= ((lanes >> (8 * e)) & 0xffu) ? 1u << (4 * i + e) : 0u;
+                }
+              }
+            }
+            // a key whose V is not finite: NaN for the rows that see it (a warp's lanes have the keys it looked at)
+            if ((word >> lane) & 1u) {
+#pragma unroll 1
+              for (int n = 0; n < nrows; ++n)
+                if ((vis >> n) & 1u) *reinterpret_cast<uint16_t*>(prow + (((n >> 3) ^ sw) << 4) + (n & 7) * 2) = 0x7fff;
+            }
+          }
+        }
         tc::fence_proxy_async_smem();
         tc::tc_fence_before();
         __syncwarp();
@@ -624,7 +655,7 @@ span_rows_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__
       }
       if (leave) { ok = false; break; }
       // the unit's sums; the output warps have to have read the ones before of this parity
-      const float total = reduce16(sum, lane);
+      const float total = reduce16<false>(sum, lane);
       bool fine = li < 2 || warp_wait(&c.o_free[par], ((li >> 1) - 1) & 1, abort_flag);
       fine = fine && ok;
       if ((lane & 1) == 0) c.sum[par][g][q4][lane >> 1] = total;
@@ -649,7 +680,7 @@ span_rows_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__
     // every request of the range is unreliable after a wait that ran out
     const Range R = c.range;
     Walker w;
-    w.start(R);
+    w.start(R, nullptr);
     Item it;
     while (w.next(a, R, it)) flag(a, it.req, it.nreq, SPEC_REQ_TIMEOUT);
   }

@@ -63,6 +63,7 @@ struct Control {
   uint64_t item_full[kItems], item_empty[kItems], drain;
   Item item[kItems];
   Range range;
+  Entry first;
   alignas(16) uint32_t vbad[2][2][4];                          // tile parity, slot, 32 keys each: V not finite
   uint32_t tmem;
   int abort;
@@ -70,7 +71,7 @@ struct Control {
 };
 constexpr int kSmemBytes = kSmemCtl + int(sizeof(Control));
 static_assert(kSmemBytes <= 232448, "fits one CTA's shared memory");
-static_assert(sizeof(RangeScratch) <= 8 * 4096, "its scratch lies in the tiles, the report's in the rows on their way out");
+static_assert(sizeof(RangeScratch) <= size_t(kSmemOut), "the search's scratch lies in the tiles");
 
 // One lane waits (bounded), the warp gets the outcome.
 __device__ __forceinline__ bool lane0_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
@@ -176,7 +177,6 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
   uint8_t* sV = smem + kSmemV;
   Control& c = *reinterpret_cast<Control*>(smem + kSmemCtl);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  // Warp 3 looks for the CTA's range while the others set up; it publishes items after the barrier below.
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
       tc::mbar_init(&c.q_full[s], 1);
@@ -218,8 +218,9 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
   }
   pdl_wait();
   pdl_trigger();
+  entry_costs(a, *reinterpret_cast<RangeScratch*>(smem));
   if (warp == 3) {
-    const Range mine = warp_range(a, blockIdx.x, *reinterpret_cast<RangeScratch*>(smem));
+    const Range mine = warp_range(a, blockIdx.x, *reinterpret_cast<RangeScratch*>(smem), c.first);
     if (lane == 0) c.range = mine;
   }
   tc::tc_fence_before();
@@ -249,7 +250,7 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
       if (lane == 0) {
         const Range R = c.range;
         Walker w;
-        w.start(R);
+        w.start(R, &c.first);
         Item it;
         bool more = true, ok = true;
         for (int n = 0; more && ok; ++n) {
@@ -439,7 +440,7 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     if (layout_ok) {
       // ===================================================================== softmax, epilogue
-      if (warp == 4 && reports(c.range, gridDim.x)) write_recs(a, *reinterpret_cast<RangeScratch*>(smem + kSmemOut));
+      if (warp == 4 && reports(c.range, gridDim.x)) write_recs(a);
       const int s = (warp - 4) >> 2, q4 = warp & 3;
       const int m = q4 * 32 + lane;                   // row of the slot's tile; also a key of V's check
       const uint32_t lane_addr = uint32_t(q4 * 32) << 16;
@@ -751,7 +752,7 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
     // every request of the range is unreliable after a wait that ran out
     const Range R = c.range;
     Walker w;
-    w.start(R);
+    w.start(R, nullptr);
     Item it;
     while (w.next(a, R, it)) flag(a, it.req, it.nreq, SPEC_REQ_TIMEOUT);
   }
