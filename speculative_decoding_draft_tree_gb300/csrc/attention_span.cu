@@ -295,7 +295,7 @@ __device__ __forceinline__ Pieces pieces_of(const Dev& a, const Rec& e, const Cu
   const int np = a.pairing ? e.mts >> 1 : 0;
   const bool pair = mt < 2 * np;
   const int w = pair ? a.cost_pair : a.cost_single;
-  const long long first = e.beg + h * head_cost(a, e.mts, e.nt) + unit_begin(a, e.mts, e.nt, pair ? mt >> 1 : mt - np) + a.cost_unit;
+  const long long first = e.beg + h * head_cost(a, e) + unit_begin(a, e, pair ? mt >> 1 : mt - np) + e.cu;
   Pieces p;
   p.ca = range_of(cut, first);
   p.np = range_of(cut, first + (long long)(e.nt - 1) * w) - p.ca + 1;
@@ -304,7 +304,7 @@ __device__ __forceinline__ Pieces pieces_of(const Dev& a, const Rec& e, const Cu
 }
 
 template <typename T, int kR, int kCols>      // kCols: vectors of 128 columns of a row
-__global__ void __launch_bounds__(256) span_merge_kernel(Dev a) {
+__global__ void __launch_bounds__(256, kCols > 1 ? 2 : kR == 1 ? 4 : 3) span_merge_kernel(Dev a) {
   constexpr int kP = 32 / kR, kLoads = 4;      // pieces a round, vectors loaded together
   constexpr int kBatch = kLoads / kR;
   pdl_wait();
@@ -320,22 +320,25 @@ __global__ void __launch_bounds__(256) span_merge_kernel(Dev a) {
   Rec grp;
   if (g >= 0) grp = a.recs[g];
   const int i = lane % kR;
+  Pieces po, pg;
+  int mt_seen = -1, gmt_seen = -1;
 #pragma unroll 1
   for (int m0 = int(blockIdx.z) * kMergeRows + warp * kR; m0 < last; m0 += 8 * kR) {
     // this lane's row and piece
     const int m = min(m0 + i, nrows - 1);
     const int mt = m / a.rt;
-    const Pieces po = pieces_of(a, own, cut, h, mt);
+    if (mt != mt_seen) po = pieces_of(a, own, cut, h, mt);
+    mt_seen = mt;
     if (g < 0 && !__any_sync(0xffffffffu, po.np > 1)) continue;
     const int t = m / a.G;
     const size_t out = size_t(own.o + t) * a.H_q + h * a.G + (m - t * a.G);
     // row of a piece's slot: the second tile of a pair lies behind the first
     const int oc = m - mt * a.rt + ((a.pairing && (mt & 1)) ? a.part_rows / 2 : 0);
-    Pieces pg = po;
     int gc = 0, ng = 0;
     if (g >= 0) {
       const int gm = (own.o - grp.o) * a.G + m, gmt = gm / a.rt;
-      pg = pieces_of(a, grp, cut, h, gmt);
+      if (gmt != gmt_seen) pg = pieces_of(a, grp, cut, h, gmt);
+      gmt_seen = gmt;
       gc = gm - gmt * a.rt + ((a.pairing && (gmt & 1)) ? a.part_rows / 2 : 0);
       ng = pg.np;
     }
@@ -355,17 +358,31 @@ __global__ void __launch_bounds__(256) span_merge_kernel(Dev a) {
     auto row_at = [&](unsigned long long at) {
       return reinterpret_cast<unsigned long long>((at >> 63) ? a.row_o + (at & ~(1ULL << 63)) * a.d : a.part_o + at * a.d);
     };
+    // values of kBatch pieces from q0 of the round; a piece that the row does not have: zeros
     unsigned long long src = 0;
-    float M = -INFINITY, L0 = -INFINITY;
-    for (int p = lane / kR; p < n; p += kP) {
-      const unsigned long long at = where(p);
-      const float L = lse_at(at);
-      if (p < kP) {
-        L0 = L;
-        src = row_at(at);
+    float4 v[kLoads][kCols];
+    auto load = [&](int q0) {
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) {
+        const int q = q0 + u / kR;
+        const float* o = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, src, min(q, kP - 1) * kR + u % kR));
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) {
+          const int col = 4 * lane + 128 * c;
+          v[u][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (o && q < kP && col < a.d) v[u][c] = *reinterpret_cast<const float4*>(o + col);
+        }
       }
-      M = fmaxf(M, L);
+    };
+    // the first pieces' values and the log-sum-exps are on their way together
+    float M = -INFINITY, L0 = -INFINITY;
+    if (lane / kR < n) {
+      const unsigned long long at = where(lane / kR);
+      M = L0 = lse_at(at);
+      src = row_at(at);
     }
+    load(0);
+    for (int p = lane / kR + kP; p < n; p += kP) M = fmaxf(M, lse_at(where(p)));
 #pragma unroll
     for (int o = kR; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     float sum = 0.f;
@@ -376,43 +393,34 @@ __global__ void __launch_bounds__(256) span_merge_kernel(Dev a) {
       for (int c = 0; c < kCols; ++c) acc[k][c] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
     for (int p0 = 0; p0 < most; p0 += kP) {
-      const int p = p0 + lane / kR;
-      float wt = 0.f;
-      if (p < n) {
-        if (p0 > 0) {
+      if (p0 > 0) {
+        const int p = p0 + lane / kR;
+        L0 = -INFINITY;
+        src = 0;
+        if (p < n) {
           const unsigned long long at = where(p);
           L0 = lse_at(at);
           src = row_at(at);
         }
-        wt = L0 == -INFINITY ? 0.f : exp2f(L0 - M);     // nothing visible in this piece (M may be -inf as well)
       }
+      const float wt = L0 == -INFINITY ? 0.f : exp2f(L0 - M);     // nothing visible in this piece (M may be -inf as well)
       sum += wt;
       const int np = min(kP, most - p0);
 #pragma unroll 1
       for (int q0 = 0; q0 < np; q0 += kBatch) {
-        float4 v[kLoads][kCols];
-        float w[kLoads];
+        if (p0 + q0 > 0) load(q0);
 #pragma unroll
         for (int u = 0; u < kLoads; ++u) {
-          const int q = q0 + u / kR, from = min(q, kP - 1) * kR + u % kR;
-          w[u] = __shfl_sync(0xffffffffu, wt, from);
-          const float* o = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, src, from));
-          if (q >= np) w[u] = 0.f;
-#pragma unroll
-          for (int c = 0; c < kCols; ++c) {
-            const int col = 4 * lane + 128 * c;
-            v[u][c] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (w[u] != 0.f && col < a.d) v[u][c] = *reinterpret_cast<const float4*>(o + col);    // a NaN is not 0
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < kLoads; ++u)
+          const int q = q0 + u / kR;
+          const float w = __shfl_sync(0xffffffffu, wt, min(q, kP - 1) * kR + u % kR);
+          if (w == 0.f || q >= np) continue;      // what such a piece holds may be a NaN, or nothing yet
 #pragma unroll
           for (int c = 0; c < kCols; ++c) {
             float4& x = acc[u % kR][c];
-            x.x = fmaf(w[u], v[u][c].x, x.x); x.y = fmaf(w[u], v[u][c].y, x.y);
-            x.z = fmaf(w[u], v[u][c].z, x.z); x.w = fmaf(w[u], v[u][c].w, x.w);
+            x.x = fmaf(w, v[u][c].x, x.x); x.y = fmaf(w, v[u][c].y, x.y);
+            x.z = fmaf(w, v[u][c].z, x.z); x.w = fmaf(w, v[u][c].w, x.w);
           }
+        }
       }
     }
 #pragma unroll
@@ -446,9 +454,9 @@ static spec_status_t launch_merge(const Dev& a, cudaStream_t s) {
 }
 
 // ------------------------------------------------------------------------------ host
-// Costs on the tensor cores, about 800 clocks each: measured, a key tile takes a pair unit 3100 clocks and
-// a single one 2400, and a unit's start, masked tile and end together 8000 .. 10000.
-constexpr int kPairCost = 4, kSingleCost = 3, kUnitCost = 12, kMinCost = 24;
+// Costs on the tensor cores, about 660 clocks each: measured, a key tile takes a pair unit 2650 clocks and
+// a single one 2000, a unit's start and end 9000, and a tile under a mask 2500 more.
+constexpr int kPairCost = 4, kSingleCost = 3, kUnitCost = 14, kMaskedCost = 4, kMinCost = 16;
 // The rows kernel's: a tile, a unit, a range.
 constexpr int kRowsTileCost = 2, kRowsUnitCost = 2, kRowsMinCost = 8;
 constexpr int kFewRows = 16;       // query rows of a unit up to which the rows kernel takes it
@@ -567,6 +575,7 @@ static spec_status_t launch(const Args& x, void* ws, size_t ws_bytes, cudaStream
   d.cost_pair = kPairCost;
   d.cost_single = w.kernel == kTile ? kSingleCost : w.kernel == kFew ? kRowsTileCost : 1;
   d.cost_unit = w.kernel == kTile ? kUnitCost : w.kernel == kFew ? kRowsUnitCost : 0;
+  d.cost_masked = w.kernel == kTile ? kMaskedCost : 0;
   d.cost_min = w.kernel == kTile ? kMinCost : w.kernel == kFew ? kRowsMinCost : 4;
   const float scale = p->scale > 0.f ? p->scale : 1.f / sqrtf(float(p->head_dim));
   d.scale_log2 = scale * 1.4426950408889634f;

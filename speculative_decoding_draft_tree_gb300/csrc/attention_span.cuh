@@ -7,8 +7,8 @@
 //     keys [0, shared_len) by the first member's table row, every key visible to every row;
 //   request r: rows = its query rows, keys [lo, P + T) and [0, sink) by its own table row.
 // An entry has H_kv x (units) units; a unit is one or two row tiles of a KV head (`pairing`: two tiles
-// read every K/V tile once) over all of the entry's key tiles.  A unit costs cost_unit for its start and
-// end, and cost_pair or cost_single for each key tile; ranges are equal in cost, and a tile belongs to the
+// read every K/V tile once) over all of the entry's key tiles.  A unit costs `cu`: cost_unit for its start
+// and end and cost_masked for each tile under a mask; and cost_pair or cost_single for each key tile; ranges are equal in cost, and a tile belongs to the
 // range that its first cost unit lies in.
 #pragma once
 
@@ -46,35 +46,38 @@ struct Dev {
   int rt;               // query rows of a row tile
   int bn;               // keys of a key tile
   int part_rows, pairing;
-  int cost_pair, cost_single, cost_unit, cost_min;   // cost_min: of a range at least
+  int cost_pair, cost_single, cost_unit, cost_masked, cost_min;   // cost_min: of a range at least
   float scale_log2;
 };
 
 // What the merge has to know of an entry: where it lies in the stream, its tokens and tiles.
 struct Rec {
   long long beg;
-  int o, T, nt, mts, group, pad;
+  int o, T, nt, mts, group, cu;
 };
 
 // One entry: rows [0, T G) of tokens o .. o + T - 1; keys [0, sink) and [lo, end), those from P on
 // under the ancestor mask; key tiles 0 .. nt0 - 1, then w0 ..: nt of them.
 struct Entry {
   int o, T, P, end, lo, sink, table, nt0, w0, nt, mts;
+  int cu;               // cost of a unit besides its tiles
   int group;            // >= 0: entry of a group; -1: a request on its own; -2 - g: a member of group g
 };
 
 __device__ __forceinline__ int units_of(const Dev& a, const Entry& e) {
   return a.pairing ? (e.mts + 1) >> 1 : e.mts;
 }
-// cost of one KV head of the entry
-__device__ __forceinline__ long long head_cost(const Dev& a, int mts, int nt) {
-  const int np = a.pairing ? mts >> 1 : 0, ns = mts - 2 * np;
-  return (long long)(np * a.cost_pair + ns * a.cost_single) * nt + (long long)(np + ns) * a.cost_unit;
+// cost of one KV head of the entry (an Entry or a Rec)
+template <typename E>
+__device__ __forceinline__ long long head_cost(const Dev& a, const E& e) {
+  const int np = a.pairing ? e.mts >> 1 : 0, ns = e.mts - 2 * np;
+  return (long long)(np * a.cost_pair + ns * a.cost_single) * e.nt + (long long)(np + ns) * e.cu;
 }
 // cost before unit u of a KV head, from the head's beginning
-__device__ __forceinline__ long long unit_begin(const Dev& a, int mts, int nt, int u) {
-  const int np = a.pairing ? mts >> 1 : 0;
-  return (long long)(min(u, np) * a.cost_pair + max(u - np, 0) * a.cost_single) * nt + (long long)u * a.cost_unit;
+template <typename E>
+__device__ __forceinline__ long long unit_begin(const Dev& a, const E& e, int u) {
+  const int np = a.pairing ? e.mts >> 1 : 0;
+  return (long long)(min(u, np) * a.cost_pair + max(u - np, 0) * a.cost_single) * e.nt + (long long)u * e.cu;
 }
 
 // The group of request r: the g with off[g] <= r < off[g + 1], -1 if the offsets name none.
@@ -104,6 +107,10 @@ __device__ __forceinline__ void key_tiles(const Dev& a, Entry& e) {
   e.w0 = max(e.lo / a.bn, e.nt0);
   e.nt = e.nt0 + (e.end + a.bn - 1) / a.bn - e.w0;
   e.mts = int(((long long)e.T * a.G + a.rt - 1) / a.rt);
+  // tiles that some row does not see whole: the last ones, those at the lower edge, the sinks' last
+  const int low = a.window > 0 ? int(max(0LL, (long long)e.P + e.T - a.window)) : e.lo;
+  const int masked = (e.end + a.bn - 1) / a.bn - e.P / a.bn + (low + a.bn - 1) / a.bn - e.lo / a.bn + (e.sink % a.bn ? 1 : 0);
+  e.cu = a.cost_unit + a.cost_masked * min(masked, e.nt);
 }
 
 // Entry i of the stream (groups first).  `off`: the group offsets, possibly a copy.  mts = 0: no work.
@@ -112,7 +119,7 @@ __device__ __forceinline__ void key_tiles(const Dev& a, Entry& e) {
 // roles of all CTAs derive the same stream from the same inputs.
 __device__ __forceinline__ Entry entry_of(const Dev& a, const int32_t* off, int i, int& bad) {
   Entry e;
-  e.o = e.T = e.P = e.end = e.lo = e.sink = e.nt0 = e.w0 = e.nt = e.mts = e.table = 0;
+  e.o = e.T = e.P = e.end = e.lo = e.sink = e.nt0 = e.w0 = e.nt = e.mts = e.cu = e.table = 0;
   e.group = -1;
   bad = 0;
   if (i < a.Gn) {
@@ -230,7 +237,7 @@ __device__ __forceinline__ void entry_costs(const Dev& a, RangeScratch& s) {
   for (int i = threadIdx.x; i < min(E, kCostCache); i += blockDim.x) {
     int bad;
     const Entry e = entry_of(a, off, i, bad);
-    s.cost[i] = head_cost(a, e.mts, e.nt) * a.H_kv;
+    s.cost[i] = head_cost(a, e) * a.H_kv;
     if (i < kEntryCache) s.entry[i] = e;
   }
   __syncthreads();
@@ -256,7 +263,7 @@ __device__ __forceinline__ Range warp_range(const Dev& a, int c, RangeScratch& s
         } else {
           int bad;
           const Entry e = entry_of(a, a.Gn <= kGroupCache ? s.off : a.group_offset, i, bad);
-          cost = head_cost(a, e.mts, e.nt) * a.H_kv;
+          cost = head_cost(a, e) * a.H_kv;
         }
       }
       if (pass == 0) {
@@ -309,9 +316,9 @@ __device__ __forceinline__ void write_recs(const Dev& a) {
     if (i < a.Gn + a.B) {
       int bad;
       const Entry e = entry_of(a, off, i, bad);
-      cost = head_cost(a, e.mts, e.nt) * a.H_kv;
+      cost = head_cost(a, e) * a.H_kv;
       if (bad) atomicOr(&a.req_status[i - a.Gn], bad);
-      r.o = e.o; r.T = e.T; r.nt = e.nt; r.mts = e.mts; r.group = e.group; r.pad = 0;
+      r.o = e.o; r.T = e.T; r.nt = e.nt; r.mts = e.mts; r.group = e.group; r.cu = e.cu;
     }
     const long long hi = warp_scan(cost) + sum;
     if (i < a.Gn + a.B) {
@@ -356,7 +363,7 @@ struct Walker {
           e = entry_of(a, a.group_offset, i, bad);
         }
         known = false;
-        const long long hc = head_cost(a, e.mts, e.nt);
+        const long long hc = head_cost(a, e);
         ubeg = eend;
         eend += hc * a.H_kv;
         np = a.pairing ? e.mts >> 1 : 0;
@@ -365,13 +372,13 @@ struct Walker {
         if (t > ubeg && t < eend) {          // the range begins inside: the unit that holds t
           h = int(div_ll(t - ubeg, hc));
           ubeg += h * hc;
-          const long long in = t - ubeg, pc = (long long)a.cost_pair * e.nt + a.cost_unit;
-          u = in < np * pc ? int(div_ll(in, pc)) : np + int(div_ll(in - np * pc, (long long)a.cost_single * e.nt + a.cost_unit));
-          ubeg += unit_begin(a, e.mts, e.nt, u);
+          const long long in = t - ubeg, pc = (long long)a.cost_pair * e.nt + e.cu;
+          u = in < np * pc ? int(div_ll(in, pc)) : np + int(div_ll(in - np * pc, (long long)a.cost_single * e.nt + e.cu));
+          ubeg += unit_begin(a, e, u);
         }
       }
       const int w = u < np ? a.cost_pair : a.cost_single;
-      const long long first = ubeg + a.cost_unit, uend = first + (long long)w * e.nt;      // the first tile's place
+      const long long first = ubeg + e.cu, uend = first + (long long)w * e.nt;      // the first tile's place
       const int j0 = int(max(0LL, div_ll(max(0LL, t - first + w - 1), w)));
       const int j1 = int(min((long long)e.nt, div_ll(max(0LL, R.t1 - first + w - 1), w)));
       it.h = h;

@@ -58,7 +58,7 @@ constexpr float kLazy = 8.0f;                      // log2 units
 struct Control {
   uint64_t q_full[2], q_empty[2];
   uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
-  uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+  uint64_t s_full[2], p_half[2], p_full[2], o_full[2], o_free[2];
   uint64_t exchange[4], vfix[3];                   // vfix: slot 0, slot 1, both
   uint64_t item_full[kItems], item_empty[kItems], drain;
   Item item[kItems];
@@ -182,6 +182,7 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
       tc::mbar_init(&c.q_full[s], 1);
       tc::mbar_init(&c.q_empty[s], 1);
       tc::mbar_init(&c.s_full[s], 1);
+      tc::mbar_init(&c.p_half[s], 4);
       tc::mbar_init(&c.p_full[s], 4);
       tc::mbar_init(&c.o_full[s], 1);
       tc::mbar_init(&c.o_free[s], 8);
@@ -356,7 +357,7 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
       const uint64_t dQ0 = tc::smem_desc(tc::smem_u32(sQ), 16, 1024), dK0 = tc::smem_desc(tc::smem_u32(sK), 16, 1024);
       const uint64_t dV0 = tc::smem_desc(tc::smem_u32(sV), kAtom, 1024);
       constexpr uint64_t kStep = kTile >> 4;
-      int g0 = 0, qn0 = 0, qn1 = 0, pn0 = 0, pn1 = 0, li = 0;
+      int g0 = 0, qn0 = 0, qn1 = 0, pn0 = 0, pn1 = 0, hn = 0, li = 0;
       bool ok = true;
       for (; ok; ++li) {
         ok = take(true);
@@ -368,67 +369,76 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
         const int n0 = pair ? nt : (nt + 1) >> 1, n1 = pair ? nt : nt >> 1;
         ok = tc::mbar_wait(&c.q_full[0], qn0++ & 1, abort_flag, kWaitLimit);
         if (ok && pair) ok = tc::mbar_wait(&c.q_full[1], qn1++ & 1, abort_flag, kWaitLimit);
-        if (!ok) break;
-        int qk_left = n0 + n1;
-        auto issue_qk = [&](int s, int k) -> bool {
-          const int g = g0 + (pair ? k : 2 * k + s), st = g % kKStages;
-          if (!tc::mbar_wait(&c.k_full[st], (g / kKStages) & 1, abort_flag, kWaitLimit)) return false;
-          tc::tc_fence_after();
-          const uint64_t dq = dQ0 + (pair ? s : 0) * kStep, dk = dK0 + uint64_t(st) * kStep;
-          uint64_t da[8], db[8];      // formed before the first product, so that the eight go back to back
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint64_t off = uint64_t(((kk >> 2) * kAtom + (kk & 3) * 32) >> 4);
-            da[kk] = dq + off;
-            db[kk] = dk + off;
-          }
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) tc::mma_bf16_ss(tmem + 128 * s, da[kk], db[kk], id_qk, kk > 0 ? 1u : 0u);
-          tc::mma_commit(&c.s_full[s]);
-          if (!pair || s == 1) tc::mma_commit(&c.k_empty[st]);     // the stage's last reader
-          if (--qk_left == 0) {
-            tc::mma_commit(&c.q_empty[0]);
-            if (pair) tc::mma_commit(&c.q_empty[1]);
-          }
-          return true;
-        };
-        auto issue_pv = [&](int s, int k, bool last) -> bool {
-          const int g = g0 + (pair ? k : 2 * k + s), st = g % kVStages;
-          int& pn = s == 0 ? pn0 : pn1;
-          if (!tc::mbar_wait(&c.p_full[s], pn & 1, abort_flag, kWaitLimit)) return false;
-          if (!tc::mbar_wait(&c.v_full[st], (g / kVStages) & 1, abort_flag, kWaitLimit)) return false;
-          // an item's first product overwrites O_s: the epilogue before has to have read it
-          if (k == 0 && li > 0 && !tc::mbar_wait(&c.o_free[s], (li - 1) & 1, abort_flag, kWaitLimit)) return false;
-          tc::tc_fence_after();
-          const uint32_t tO = tmem + 256 + 128 * s, tP = tmem + 128 * s;
-          const uint64_t dv = dV0 + uint64_t(st) * kStep;
-          if (pair) {
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              tc::mma_bf16_ts(tO, tP + 8 * kk, dv + uint64_t(kk * (2048 >> 4)), id_pv, kk > 0 || k > 0 ? 1u : 0u);
-          } else {
-#pragma unroll
-            for (int kk = 0; kk < 16; ++kk) {
-              const int q = (kk & 7) >> 1, col = 32 * q + 16 * (kk >> 3) + 8 * (kk & 1);
-              tc::mma_bf16_ts(tO, tP + col, dv + uint64_t((kk & 7) * (2048 >> 4)), id_pv, kk > 0 || k > 0 ? 1u : 0u);
+        // P of a pair in one piece, two groups of four products a tile; of a single unit in two, four groups
+        const int groups = pair ? 2 : 4;
+        const uint32_t wide = pair ? 16 : 32;
+        const uint64_t two = pair ? kStep : 0;
+        // PV_s(k) and QK_s(k + 1) in turn, from QK_s(0) on: one short body each for both slots
+#pragma unroll 1
+        for (int e = -2; ok && e < 2 * n0; ++e) {
+          const int s = e & 1, k = e >> 1, n = s ? n1 : n0;
+          const bool lead = !pair || s == 0, tail = !pair || s == 1;     // a stage's first and last reader
+          const uint32_t tP = tmem + 128 * s;
+          if (k >= 0 && k < n) {
+            const int g = g0 + (pair ? k : 2 * k + s), st = g % kVStages;
+            const uint32_t pp = ((s ? pn1 : pn0) + k) & 1;
+            // a pair's product starts on the first 64 keys
+            if (!tc::mbar_wait(pair ? &c.p_half[s] : &c.p_full[s], pair ? (hn + k) & 1 : pp, abort_flag, kWaitLimit) ||
+                (lead && !tc::mbar_wait(&c.v_full[st], (g / kVStages) & 1, abort_flag, kWaitLimit)) ||
+                // an item's first product overwrites O_s: the epilogue before has to have read it
+                (k == 0 && li > 0 && !tc::mbar_wait(&c.o_free[s], (li - 1) & 1, abort_flag, kWaitLimit))) {
+              ok = false;
+              break;
             }
+            const uint32_t tO = tmem + 256 + 128 * s;
+            const uint64_t dv = dV0 + uint64_t(st) * kStep;
+#pragma unroll 1
+            for (int q = 0; q < groups; ++q) {
+              if (pair && q == 1 && !tc::mbar_wait(&c.p_full[s], pp, abort_flag, kWaitLimit)) {
+                ok = false;
+                break;
+              }
+              tc::tc_fence_after();
+              const uint32_t col = tP + 2 * wide * (q & 1) + 16 * (q >> 1);
+              const uint64_t d = dv + uint64_t((q & 1) * (8192 >> 4));
+              tc::mma_bf16_ts(tO, col, d, id_pv, q > 0 || k > 0 ? 1u : 0u);
+              tc::mma_bf16_ts(tO, col + 8, d + (2048 >> 4), id_pv, 1u);
+              tc::mma_bf16_ts(tO, col + wide, d + (4096 >> 4), id_pv, 1u);
+              tc::mma_bf16_ts(tO, col + wide + 8, d + (6144 >> 4), id_pv, 1u);
+            }
+            if (!ok) break;
+            if (tail) tc::mma_commit(&c.v_empty[st]);
+            if (k + 1 == n) tc::mma_commit(&c.o_full[s]);
           }
-          if (!pair || s == 1) tc::mma_commit(&c.v_empty[st]);
-          if (last) tc::mma_commit(&c.o_full[s]);
-          ++pn;
-          return true;
-        };
-        if (n0 > 0) ok = issue_qk(0, 0);
-        if (ok && n1 > 0) ok = issue_qk(1, 0);
-        for (int k = 0; ok && k < n0; ++k) {
-          ok = issue_pv(0, k, k + 1 == n0);
-          if (ok && k + 1 < n0) ok = issue_qk(0, k + 1);
-          if (ok && k < n1) {
-            ok = issue_pv(1, k, k + 1 == n1);
-            if (ok && k + 1 < n1) ok = issue_qk(1, k + 1);
+          if (k + 1 < n) {
+            const int g = g0 + (pair ? k + 1 : 2 * (k + 1) + s), st = g % kKStages;
+            if (lead && !tc::mbar_wait(&c.k_full[st], (g / kKStages) & 1, abort_flag, kWaitLimit)) {
+              ok = false;
+              break;
+            }
+            tc::tc_fence_after();
+            const uint64_t dq = dQ0 + (s ? two : 0), dk = dK0 + uint64_t(st) * kStep;
+            uint64_t da[8], db[8];      // formed before the first product, so that the eight go back to back
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              const uint64_t off = uint64_t(((kk >> 2) * kAtom + (kk & 3) * 32) >> 4);
+              da[kk] = dq + off;
+              db[kk] = dk + off;
+            }
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) tc::mma_bf16_ss(tP, da[kk], db[kk], id_qk, kk > 0 ? 1u : 0u);
+            tc::mma_commit(&c.s_full[s]);
+            if (tail) tc::mma_commit(&c.k_empty[st]);
+            if (k + 2 == n && s == (n1 == n0 ? 1 : 0)) {      // the unit's last scores
+              tc::mma_commit(&c.q_empty[0]);
+              if (pair) tc::mma_commit(&c.q_empty[1]);
+            }
           }
         }
         g0 += nt;
+        pn0 += n0;
+        pn1 += n1;
+        if (pair) hn += nt;
       }
       if (!ok) *abort_flag = 1;
       // TMEM may not be freed under a product: wait for all of them, also after an abort
@@ -601,6 +611,10 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
               const uint64_t sl = scale_of(), add = add_of();
               weights32<false>(x0, sl, add, acc0, tS);
               weights32<false>(x1, sl, add, acc1, tS + 16);
+              tc::tmem_st_wait();
+              tc::tc_fence_before();
+              __syncwarp();
+              if (lane == 0) tc::mbar_arrive(&c.p_half[s]);
               weights32<false>(x2, sl, add, acc0, tS + 32);
               weights32<false>(x3, sl, add, acc1, tS + 48);
             } else {
@@ -635,7 +649,10 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
           }
           tc::tc_fence_before();
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&c.p_full[s]);
+          if (lane == 0) {
+            if (pair && !live) tc::mbar_arrive(&c.p_half[s]);
+            tc::mbar_arrive(&c.p_full[s]);
+          }
         }
         if (!ok) break;
         // the products whose O this warp reads (both slots' of a single unit)
