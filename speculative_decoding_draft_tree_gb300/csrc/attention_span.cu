@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kSimtThreads) span_simt_kernel(Dev a) {
 // are taken by one CTA, two at a time (many rows), and a warp takes one row where there are few: 16 rows or
 // less a request and head.
 constexpr int kMergeFew = 16;
-constexpr int kMergeRows = 64;
+constexpr int kMergeRows = 32;
 
 struct Pieces {
   int np, ca, slot0;        // np = 1: not cut
