@@ -290,16 +290,21 @@ constexpr int kMergeRows = 32;
 
 struct Pieces {
   int np, ca, slot0;        // np = 1: not cut
+  int row;                  // of a slot, where the row tile begins
 };
 __device__ __forceinline__ Pieces pieces_of(const Dev& a, const Rec& e, const Cut& cut, int h, int mt) {
-  const int np = a.pairing ? e.mts >> 1 : 0;
-  const bool pair = mt < 2 * np;
-  const int w = pair ? a.cost_pair : a.cost_single;
-  const long long first = e.beg + h * head_cost(a, e) + unit_begin(a, e, pair ? mt >> 1 : mt - np) + e.cu;
+  const Units n = units_of(a, e);
+  const int b = n.hb == 2 ? h >> 1 : h, heads = block_heads(a, n, b * n.hb), in = h - b * n.hb;
+  const bool pair = mt < 2 * n.pairs;
+  const int u = pair ? in * n.pairs + (mt >> 1) : heads * n.pairs + mt - 2 * n.pairs;
+  const int w = pair ? a.cost_pair : rest_cost(a, heads);
+  const int second = pair ? mt & 1 : heads == 2 ? in : 0;
+  const long long first = e.beg + b * block_cost(a, e, n, n.hb) + unit_begin(a, e, n, heads, u) + e.cu;
   Pieces p;
   p.ca = range_of(cut, first);
   p.np = range_of(cut, first + (long long)(e.nt - 1) * w) - p.ca + 1;
   p.slot0 = 2 * p.ca + (first > range_start(cut, p.ca) ? 1 : 0);
+  p.row = second * (a.part_rows / 2);
   return p;
 }
 
@@ -332,14 +337,14 @@ __global__ void __launch_bounds__(256, kCols > 1 ? 2 : kR == 1 ? 4 : 3) span_mer
     if (g < 0 && !__any_sync(0xffffffffu, po.np > 1)) continue;
     const int t = m / a.G;
     const size_t out = size_t(own.o + t) * a.H_q + h * a.G + (m - t * a.G);
-    // row of a piece's slot: the second tile of a pair lies behind the first
-    const int oc = m - mt * a.rt + ((a.pairing && (mt & 1)) ? a.part_rows / 2 : 0);
+    // row of a piece's slot
+    const int oc = m - mt * a.rt + po.row;
     int gc = 0, ng = 0;
     if (g >= 0) {
       const int gm = (own.o - grp.o) * a.G + m, gmt = gm / a.rt;
       if (gmt != gmt_seen) pg = pieces_of(a, grp, cut, h, gmt);
       gmt_seen = gmt;
-      gc = gm - gmt * a.rt + ((a.pairing && (gmt & 1)) ? a.part_rows / 2 : 0);
+      gc = gm - gmt * a.rt + pg.row;
       ng = pg.np;
     }
     const bool mine = m0 + i < last && (g >= 0 || po.np > 1);
@@ -454,11 +459,12 @@ static spec_status_t launch_merge(const Dev& a, cudaStream_t s) {
 }
 
 // ------------------------------------------------------------------------------ host
-// Costs on the tensor cores, about 660 clocks each: measured, a key tile takes a pair unit 2650 clocks and
-// a single one 2000, a unit's start and end 9000, and a tile under a mask 2500 more.
-constexpr int kPairCost = 4, kSingleCost = 3, kUnitCost = 14, kMaskedCost = 4, kMinCost = 16;
+// Costs on the tensor cores, about 660 clocks each: measured, a key tile takes a pair unit 2650 clocks, two
+// heads' a dual one 4000, one a lone one 2000, a unit's start and end 9000, and a tile under a mask 2500 more.
+constexpr int kPairCost = 4, kDualCost = 6, kSingleCost = 3, kUnitCost = 14, kMaskedCost = 4, kMinCost = 16;
 // The rows kernel's: a tile, a unit, a range.
 constexpr int kRowsTileCost = 2, kRowsUnitCost = 2, kRowsMinCost = 8;
+constexpr int kDualRows = 32;
 constexpr int kFewRows = 16;       // query rows of a unit up to which the rows kernel takes it
 
 // What the two calls have in common.
@@ -572,7 +578,13 @@ static spec_status_t launch(const Args& x, void* ws, size_t ws_bytes, cudaStream
   d.num_blocks = p->num_blocks; d.max_blocks = p->max_blocks_per_req; d.ctas = w.ctas;
   d.window = x.window; d.sinks = x.sinks;
   d.rt = w.rt; d.bn = w.bn; d.part_rows = w.part_rows; d.pairing = w.kernel == kTile ? 1 : 0;
+  // Two heads share a unit where its rows are few, its start, join and end then being most of it, and there are
+  // requests enough for every CTA (64 single tokens, 32 heads on 8, 8192 shared by groups of 8: 82 us against 94);
+  // not where the row tiles are fuller (32 trees, shared 8192: 169 against 166) or CTAs idle (4 requests: 26
+  // against 23).
+  d.dual_rows = (long long)p->B * p->H_kv >= 2LL * w.ctas ? kDualRows : 0;
   d.cost_pair = kPairCost;
+  d.cost_dual = kDualCost;
   d.cost_single = w.kernel == kTile ? kSingleCost : w.kernel == kFew ? kRowsTileCost : 1;
   d.cost_unit = w.kernel == kTile ? kUnitCost : w.kernel == kFew ? kRowsUnitCost : 0;
   d.cost_masked = w.kernel == kTile ? kMaskedCost : 0;

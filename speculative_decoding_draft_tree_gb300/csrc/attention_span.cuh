@@ -6,9 +6,12 @@
 //   group g (shared form, two members at least and shared_len > 0): rows = all members' query rows,
 //     keys [0, shared_len) by the first member's table row, every key visible to every row;
 //   request r: rows = its query rows, keys [lo, P + T) and [0, sink) by its own table row.
-// An entry has H_kv x (units) units; a unit is one or two row tiles of a KV head (`pairing`: two tiles
-// read every K/V tile once) over all of the entry's key tiles.  A unit costs `cu`: cost_unit for its start
-// and end and cost_masked for each tile under a mask; and cost_pair or cost_single for each key tile; ranges are equal in cost, and a tile belongs to the
+// An entry's units, each over all of its key tiles: with `pairing`, head by head, first its pair units (two row
+// tiles, which read every K/V tile once), then, if its row tiles are odd in number, the last one; two heads
+// make a block if that last tile has at most dual_rows rows, and share a dual unit for it; without `pairing`
+// every row tile of every head.  A unit costs `cu`: cost_unit for its start and end and cost_masked for each
+// tile under a mask; and cost_pair, cost_dual or cost_single for each key tile; ranges are equal in cost, and a
+// tile belongs to the
 // range that its first cost unit lies in.
 #pragma once
 
@@ -45,8 +48,8 @@ struct Dev {
   int window, sinks;    // window form; window = 0: none
   int rt;               // query rows of a row tile
   int bn;               // keys of a key tile
-  int part_rows, pairing;
-  int cost_pair, cost_single, cost_unit, cost_masked, cost_min;   // cost_min: of a range at least
+  int part_rows, pairing, dual_rows;
+  int cost_pair, cost_dual, cost_single, cost_unit, cost_masked, cost_min;   // cost_min: of a range at least
   float scale_log2;
 };
 
@@ -64,20 +67,36 @@ struct Entry {
   int group;            // >= 0: entry of a group; -1: a request on its own; -2 - g: a member of group g
 };
 
-__device__ __forceinline__ int units_of(const Dev& a, const Entry& e) {
-  return a.pairing ? (e.mts + 1) >> 1 : e.mts;
-}
-// cost of one KV head of the entry (an Entry or a Rec)
+// An entry's (or a Rec's) blocks: of hb heads with `pairs` pair units each and then `rest` others; a last head
+// that finds no second is a block of one.
+struct Units {
+  int hb, pairs, rest;
+};
 template <typename E>
-__device__ __forceinline__ long long head_cost(const Dev& a, const E& e) {
-  const int np = a.pairing ? e.mts >> 1 : 0, ns = e.mts - 2 * np;
-  return (long long)(np * a.cost_pair + ns * a.cost_single) * e.nt + (long long)(np + ns) * e.cu;
+__device__ __forceinline__ Units units_of(const Dev& a, const E& e) {
+  if (!a.pairing) return Units{1, 0, e.mts};
+  const int odd = e.mts & 1;
+  return Units{odd && e.T * a.G - (e.mts - 1) * a.rt <= a.dual_rows ? 2 : 1, e.mts >> 1, odd};
 }
-// cost before unit u of a KV head, from the head's beginning
+__device__ __forceinline__ int block_heads(const Dev& a, const Units& n, int h) { return h + n.hb <= a.H_kv ? n.hb : 1; }
+__device__ __forceinline__ int rest_cost(const Dev& a, int heads) { return heads == 2 ? a.cost_dual : a.cost_single; }
+// cost before unit u of a block of so many heads, from its beginning
 template <typename E>
-__device__ __forceinline__ long long unit_begin(const Dev& a, const E& e, int u) {
-  const int np = a.pairing ? e.mts >> 1 : 0;
-  return (long long)(min(u, np) * a.cost_pair + max(u - np, 0) * a.cost_single) * e.nt + (long long)u * e.cu;
+__device__ __forceinline__ long long unit_begin(const Dev& a, const E& e, const Units& n, int heads, int u) {
+  const int np = heads * n.pairs;
+  return min(u, np) * ((long long)a.cost_pair * e.nt + e.cu) +
+         max(u - np, 0) * ((long long)rest_cost(a, heads) * e.nt + e.cu);
+}
+template <typename E>
+__device__ __forceinline__ long long block_cost(const Dev& a, const E& e, const Units& n, int heads) {
+  return unit_begin(a, e, n, heads, heads * n.pairs + n.rest);
+}
+template <typename E>
+__device__ __forceinline__ long long entry_cost(const Dev& a, const E& e) {
+  const Units n = units_of(a, e);
+  const long long one = block_cost(a, e, n, n.hb);
+  if (n.hb == 1) return one * a.H_kv;
+  return one * (a.H_kv >> 1) + ((a.H_kv & 1) ? block_cost(a, e, n, 1) : 0);
 }
 
 // The group of request r: the g with off[g] <= r < off[g + 1], -1 if the offsets name none.
@@ -237,7 +256,7 @@ __device__ __forceinline__ void entry_costs(const Dev& a, RangeScratch& s) {
   for (int i = threadIdx.x; i < min(E, kCostCache); i += blockDim.x) {
     int bad;
     const Entry e = entry_of(a, off, i, bad);
-    s.cost[i] = head_cost(a, e) * a.H_kv;
+    s.cost[i] = entry_cost(a, e);
     if (i < kEntryCache) s.entry[i] = e;
   }
   __syncthreads();
@@ -263,7 +282,7 @@ __device__ __forceinline__ Range warp_range(const Dev& a, int c, RangeScratch& s
         } else {
           int bad;
           const Entry e = entry_of(a, a.Gn <= kGroupCache ? s.off : a.group_offset, i, bad);
-          cost = head_cost(a, e) * a.H_kv;
+          cost = entry_cost(a, e);
         }
       }
       if (pass == 0) {
@@ -316,7 +335,7 @@ __device__ __forceinline__ void write_recs(const Dev& a) {
     if (i < a.Gn + a.B) {
       int bad;
       const Entry e = entry_of(a, off, i, bad);
-      cost = head_cost(a, e) * a.H_kv;
+      cost = entry_cost(a, e);
       if (bad) atomicOr(&a.req_status[i - a.Gn], bad);
       r.o = e.o; r.T = e.T; r.nt = e.nt; r.mts = e.mts; r.group = e.group; r.cu = e.cu;
     }
@@ -331,9 +350,10 @@ __device__ __forceinline__ void write_recs(const Dev& a) {
 }
 
 // Key tiles [j0, j1) of one unit.
+enum { kLone, kPair, kDual };
 struct Item {
   int o, T, P, end, lo, sink, table, nt0, w0;
-  int h, mt, pair;       // KV head, first row tile, 1: two row tiles
+  int h, mt, kind;       // first KV head and row tile; one of kLone, kPair, kDual
   int j0, j1;
   int slot;              // >= 0: a piece of a cut unit, to part_o[slot]; -1: to o; -2, -3: to row_o[0], [1]
   int req, nreq;         // the requests that it concerns
@@ -344,7 +364,8 @@ struct Item {
 struct Walker {
   long long t, ubeg;     // next cost position; cost before the present unit
   long long eend;        // cost up to the entry's end
-  int i, h, u, np, units;
+  int i, h, heads, u;    // entry; first head and heads of the block, unit in the block
+  Units n;
   Entry e;
   bool known;            // e is the entry to enter next
   __device__ __forceinline__ void start(const Range& R, const Entry* first) {
@@ -363,33 +384,46 @@ struct Walker {
           e = entry_of(a, a.group_offset, i, bad);
         }
         known = false;
-        const long long hc = head_cost(a, e);
+        n = units_of(a, e);
         ubeg = eend;
-        eend += hc * a.H_kv;
-        np = a.pairing ? e.mts >> 1 : 0;
-        units = units_of(a, e);
+        eend += entry_cost(a, e);
         h = u = 0;
+        heads = block_heads(a, n, 0);
         if (t > ubeg && t < eend) {          // the range begins inside: the unit that holds t
-          h = int(div_ll(t - ubeg, hc));
-          ubeg += h * hc;
-          const long long in = t - ubeg, pc = (long long)a.cost_pair * e.nt + e.cu;
-          u = in < np * pc ? int(div_ll(in, pc)) : np + int(div_ll(in - np * pc, (long long)a.cost_single * e.nt + e.cu));
-          ubeg += unit_begin(a, e, u);
+          const long long bc = block_cost(a, e, n, n.hb);
+          const int b = int(min((long long)(a.H_kv / n.hb), div_ll(t - ubeg, bc)));
+          h = b * n.hb;
+          heads = block_heads(a, n, h);
+          ubeg += b * bc;
+          const long long in = t - ubeg, rest = unit_begin(a, e, n, heads, heads * n.pairs);
+          u = in < rest ? int(div_ll(in, (long long)a.cost_pair * e.nt + e.cu))
+                        : heads * n.pairs + int(div_ll(in - rest, (long long)rest_cost(a, heads) * e.nt + e.cu));
+          ubeg += unit_begin(a, e, n, heads, u);
         }
       }
-      const int w = u < np ? a.cost_pair : a.cost_single;
+      const int np = heads * n.pairs;
+      int w = a.cost_pair;
+      if (u < np) {
+        const int hi = u / n.pairs;
+        it.kind = kPair;
+        it.h = h + hi;
+        it.mt = 2 * (u - hi * n.pairs);
+      } else {
+        w = rest_cost(a, heads);
+        it.kind = heads == 2 ? kDual : kLone;
+        it.h = h;
+        it.mt = 2 * n.pairs + u - np;
+      }
+      if (++u == np + n.rest) {
+        u = 0;
+        h += heads;
+        heads = block_heads(a, n, h);
+      }
       const long long first = ubeg + e.cu, uend = first + (long long)w * e.nt;      // the first tile's place
       const int j0 = int(max(0LL, div_ll(max(0LL, t - first + w - 1), w)));
       const int j1 = int(min((long long)e.nt, div_ll(max(0LL, R.t1 - first + w - 1), w)));
-      it.h = h;
-      it.pair = u < np ? 1 : 0;
-      it.mt = it.pair ? 2 * u : np + u;
       t = min(R.t1, uend);
       ubeg = uend;
-      if (++u == units) {
-        u = 0;
-        ++h;
-      }
       if (j1 <= j0) continue;
       it.o = e.o; it.T = e.T; it.P = e.P; it.end = e.end; it.lo = e.lo; it.sink = e.sink;
       it.table = e.table; it.nt0 = e.nt0; it.w0 = e.w0;

@@ -295,48 +295,52 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
           return -2;
         };
         int pb = tile_page(it.j0);
+        const int pair = it.kind == kPair ? 1 : 0, dual = it.kind == kDual ? 1 : 0;
         if (is_k) {
           const bool grp = it.end == it.P;
           const int tokens = grp ? q_tokens : qs_tokens;
-          for (int b = 0; ok && b <= it.pair; ++b) {
+          for (int b = 0; ok && b <= (it.kind != kLone ? 1 : 0); ++b) {
             if (qn[b] > 0) ok = lane0_wait(&c.q_empty[b], (qn[b] - 1) & 1, abort_flag);
             if (!ok) break;
             if (lane == 0) {
               tc::mbar_arrive_expect_tx(&c.q_full[b], 2 * tokens * a.G * 128);
-              const int tok = it.o + (it.mt + b) * q_tokens;
+              const int tok = it.o + (it.mt + b * pair) * q_tokens, row = (it.h + b * dual) * a.G;
               uint8_t* dst = sQ + b * kTile;
               if (grp) {
-                tc::tma_load_3d(dst, &mQ, 0, it.h * a.G, tok, &c.q_full[b]);
-                tc::tma_load_3d(dst + kAtom, &mQ, 64, it.h * a.G, tok, &c.q_full[b]);
+                tc::tma_load_3d(dst, &mQ, 0, row, tok, &c.q_full[b]);
+                tc::tma_load_3d(dst + kAtom, &mQ, 64, row, tok, &c.q_full[b]);
               } else {
-                tc::tma_load_3d(dst, &mQs, 0, it.h * a.G, tok, &c.q_full[b]);
-                tc::tma_load_3d(dst + kAtom, &mQs, 64, it.h * a.G, tok, &c.q_full[b]);
+                tc::tma_load_3d(dst, &mQs, 0, row, tok, &c.q_full[b]);
+                tc::tma_load_3d(dst + kAtom, &mQs, 64, row, tok, &c.q_full[b]);
               }
             }
             ++qn[b];
           }
         }
-        for (int j = it.j0; ok && j < it.j1; ++j, ++kt) {
+        // a dual unit's tiles alternate between its heads, which lie in the same pages
+        for (int j = it.j0; ok && j < it.j1; ++j) {
           const int ahead = j + 1 < it.j1 ? tile_page(j + 1) : -1;
-          const int st = kt % nstage, use = kt / nstage;
-          if (use > 0) ok = lane0_wait(&empty[st], (use - 1) & 1, abort_flag);
-          if (!ok) break;
           const int pb0 = __shfl_sync(0xffffffffu, pb, 0);
           const bool run = __all_sync(0xffffffffu, lane >= npg || pb == pb0 + lane) && pb0 >= 0;
-          if (lane == 0) tc::mbar_arrive_expect_tx(&full[st], kTile);
-          __syncwarp();
-          uint8_t* dst = ring + st * kTile;
-          if (run) {
-            if (lane == 0) {
-              tc::tma_load_4d(dst, tile_map, 0, 0, it.h, pb0, &full[st]);
-              tc::tma_load_4d(dst + kAtom, tile_map, 64, 0, it.h, pb0, &full[st]);
+          for (int h = it.h; h <= it.h + dual; ++h, ++kt) {
+            const int st = kt % nstage, use = kt / nstage;
+            if (use > 0) ok = lane0_wait(&empty[st], (use - 1) & 1, abort_flag);
+            if (!ok) break;
+            if (lane == 0) tc::mbar_arrive_expect_tx(&full[st], kTile);
+            __syncwarp();
+            uint8_t* dst = ring + st * kTile;
+            if (run) {
+              if (lane == 0) {
+                tc::tma_load_4d(dst, tile_map, 0, 0, h, pb0, &full[st]);
+                tc::tma_load_4d(dst + kAtom, tile_map, 64, 0, h, pb0, &full[st]);
+              }
+            } else if (lane < npg) {
+              const int row = pb >= 0 ? (pb * a.H_kv + h) * a.bs : kv_rows;      // past the cache: zeros
+              tc::tma_load_2d(dst + lane * page_bytes, page_map, 0, row, &full[st]);
+              tc::tma_load_2d(dst + kAtom + lane * page_bytes, page_map, 64, row, &full[st]);
             }
-          } else if (lane < npg) {
-            const int row = pb >= 0 ? (pb * a.H_kv + it.h) * a.bs : kv_rows;      // past the cache: zeros
-            tc::tma_load_2d(dst + lane * page_bytes, page_map, 0, row, &full[st]);
-            tc::tma_load_2d(dst + kAtom + lane * page_bytes, page_map, 64, row, &full[st]);
+            __syncwarp();
           }
-          __syncwarp();
           pb = ahead;
         }
       }
@@ -364,15 +368,16 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
         const Item& it = c.item[ni % kItems];
         if (!ok || it.j1 < 0) break;
         const int nt = it.j1 - it.j0;
-        const bool pair = it.pair != 0;
+        const bool pair = it.kind == kPair, both = it.kind != kLone;      // both: a row tile for each slot
         give_back(true);
-        const int n0 = pair ? nt : (nt + 1) >> 1, n1 = pair ? nt : nt >> 1;
+        const int n0 = both ? nt : (nt + 1) >> 1, n1 = both ? nt : nt >> 1;
         ok = tc::mbar_wait(&c.q_full[0], qn0++ & 1, abort_flag, kWaitLimit);
-        if (ok && pair) ok = tc::mbar_wait(&c.q_full[1], qn1++ & 1, abort_flag, kWaitLimit);
-        // P of a pair in one piece, two groups of four products a tile; of a single unit in two, four groups
+        if (ok && both) ok = tc::mbar_wait(&c.q_full[1], qn1++ & 1, abort_flag, kWaitLimit);
+        const int it_tiles = pair ? nt : n0 + n1;
+        // P of a pair in one piece, two groups of four products a tile; else in two, four groups
         const int groups = pair ? 2 : 4;
         const uint32_t wide = pair ? 16 : 32;
-        const uint64_t two = pair ? kStep : 0;
+        const uint64_t two = both ? kStep : 0;
         // PV_s(k) and QK_s(k + 1) in turn, from QK_s(0) on: one short body each for both slots
 #pragma unroll 1
         for (int e = -2; ok && e < 2 * n0; ++e) {
@@ -431,11 +436,11 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
             if (tail) tc::mma_commit(&c.k_empty[st]);
             if (k + 2 == n && s == (n1 == n0 ? 1 : 0)) {      // the unit's last scores
               tc::mma_commit(&c.q_empty[0]);
-              if (pair) tc::mma_commit(&c.q_empty[1]);
+              if (both) tc::mma_commit(&c.q_empty[1]);
             }
           }
         }
-        g0 += nt;
+        g0 += it_tiles;
         pn0 += n0;
         pn1 += n1;
         if (pair) hn += nt;
@@ -464,8 +469,9 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
         const Item& it = c.item[ni % kItems];
         if (!ok || it.j1 < 0) break;
         const int nt = it.j1 - it.j0, j0 = it.j0, nt0 = it.nt0, skip = it.w0 - it.nt0, P = it.P;
-        const bool pair = it.pair != 0;
-        const int n0 = pair ? nt : (nt + 1) >> 1, n1 = pair ? nt : nt >> 1;
+        const bool pair = it.kind == kPair, both = it.kind != kLone;
+        const int n0 = both ? nt : (nt + 1) >> 1, n1 = both ? nt : nt >> 1;
+        const int h = it.h + (it.kind == kDual ? s : 0);
         const int ns = s == 0 ? n0 : n1;
         const int t = (it.mt + (pair ? s : 0)) * q_tokens + t_loc;
         const bool valid = t_loc < q_tokens && t < it.T;
@@ -492,7 +498,7 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
         const int lo_max = a.window > 0 ? int(max(0LL, (long long)P + it.T - a.window)) : it.lo;
         float ref = -INFINITY, l = 0.f;        // P_s is scaled by 2^-ref, O_s and l with it
         for (int k = 0; k < ns; ++k) {
-          const int ti = pair ? k : 2 * k + s, j = j0 + ti;
+          const int ti = pair ? k : 2 * k + s, j = j0 + (both ? k : 2 * k + s);      // in the ring; of the entry
           const int kb = (j < nt0 ? j : j + skip) * kKeys;
           const bool masked = !(kb + kKeys <= P && (kb >= lo_max || kb + kKeys <= a.sinks));
           uint32_t vis0 = ~0u, vis1 = ~0u, vis2 = ~0u, vis3 = ~0u;
@@ -658,14 +664,14 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
         // the products whose O this warp reads (both slots' of a single unit)
         for (int u = 0; ok && u < 2; ++u) {
           if ((u == 0 ? n0 : n1) == 0) continue;
-          if (u == s || !pair) ok = warp_wait(&c.o_full[u], on[u] & 1, abort_flag);
+          if (u == s || !both) ok = warp_wait(&c.o_full[u], on[u] & 1, abort_flag);
           ++on[u];
         }
         if (!ok) break;
         tc::tc_fence_after();
         float lt = l, M = ref, w0 = 0.f, w1 = 0.f;
         int c_lo = 0, c_hi = kD;
-        if (!pair) {
+        if (!both) {
           // exchange (reference, sum) with the other slot's warp of this quarter; 64 columns each
           c.row[s][0][m] = ref;
           c.row[s][1][m] = l;
@@ -691,25 +697,25 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
           uint8_t* stage = smem + kSmemOut + (warp - 4) * 4096;
           const bool direct = it.slot == -1;
           const int nv = __popc(__ballot_sync(0xffffffffu, valid));    // the warp's rows 0 .. nv - 1
-          const size_t slot_row = size_t(max(it.slot, 0)) * a.part_rows + (pair ? s * kRows : 0);
+          const size_t slot_row = size_t(max(it.slot, 0)) * a.part_rows + (both ? s * kRows : 0);
           // where this lane's row of 128 columns begins, in elements of its buffer
-          const size_t row_of = size_t(it.o + t) * a.H_q + it.h * a.G + (m - t_loc * a.G);
+          const size_t row_of = size_t(it.o + t) * a.H_q + h * a.G + (m - t_loc * a.G);
           const unsigned long long mine = (it.slot >= 0 ? slot_row + m : row_of) * kD;
           float* rows = it.slot >= 0 ? a.part_o : it.slot == -3 ? a.row_o + size_t(a.N) * a.H_q * kD : a.row_o;
           unsigned long long at[8];        // where rows 4 i + lane / 8 begin
 #pragma unroll
           for (int i = 0; i < 8; ++i) at[i] = __shfl_sync(0xffffffffu, mine, 4 * i + (lane >> 3));
-          const float wa = pair ? inv : w0 * inv, wb = pair || n1 == 0 ? 0.f : w1 * inv;
+          const float wa = both ? inv : w0 * inv, wb = both || n1 == 0 ? 0.f : w1 * inv;
           const int u8 = lane & 7;
 #pragma unroll 1
           for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
             uint32_t r[32];
             float v[32];
-            tc::tmem_ld32(tO + (pair ? 128 * s : 0) + c0, r);
+            tc::tmem_ld32(tO + (both ? 128 * s : 0) + c0, r);
             tc::tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = wa == 0.f ? 0.f : __uint_as_float(r[i]) * wa;
-            if (!pair && n1 > 0) {
+            if (!both && n1 > 0) {
               tc::tmem_ld32(tO + 128 + c0, r);
               tc::tmem_ld_wait();
 #pragma unroll
@@ -745,7 +751,7 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
             }
             __syncwarp();
           }
-          if (valid && (pair || s == 0)) {
+          if (valid && (both || s == 0)) {
             if (it.slot >= 0) a.part_lse[slot_row + m] = lse2;
             else if (!direct) a.row_lse[(it.slot == -3 ? size_t(a.N) * a.H_q : 0) + row_of] = lse2;
             else if (a.lse) a.lse[row_of] = lse2 * 0.6931471805599453f;
@@ -758,7 +764,7 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
           tc::mbar_arrive(&c.o_free[1]);
         }
         give_back(false);
-        g0 += nt;
+        g0 += pair ? nt : n0 + n1;
       }
       if (!ok) *abort_flag = 1;
     }
