@@ -309,7 +309,7 @@ __device__ __forceinline__ Pieces pieces_of(const Dev& a, const Rec& e, const Cu
 }
 
 template <typename T, int kR, int kCols>      // kCols: vectors of 128 columns of a row
-__global__ void __launch_bounds__(256, kCols > 1 ? 2 : kR == 1 ? 4 : 3) span_merge_kernel(Dev a) {
+__global__ void __launch_bounds__(256, kCols > 1 ? 2 : 4) span_merge_kernel(Dev a) {
   constexpr int kP = 32 / kR, kLoads = 4;      // pieces a round, vectors loaded together
   constexpr int kBatch = kLoads / kR;
   pdl_wait();
@@ -463,7 +463,7 @@ static spec_status_t launch_merge(const Dev& a, cudaStream_t s) {
 // heads' a dual one 4000, one a lone one 2000, a unit's start and end 9000, and a tile under a mask 2500 more.
 constexpr int kPairCost = 4, kDualCost = 6, kSingleCost = 3, kUnitCost = 14, kMaskedCost = 4, kMinCost = 16;
 // The rows kernel's: a tile, a unit, a range.
-constexpr int kRowsTileCost = 2, kRowsUnitCost = 2, kRowsMinCost = 8;
+constexpr int kRowsTileCost = 2, kRowsUnitCost = 2, kRowsMinCost = 6;
 constexpr int kDualRows = 32;
 constexpr int kFewRows = 16;       // query rows of a unit up to which the rows kernel takes it
 
@@ -588,7 +588,7 @@ static spec_status_t launch(const Args& x, void* ws, size_t ws_bytes, cudaStream
   d.cost_single = w.kernel == kTile ? kSingleCost : w.kernel == kFew ? kRowsTileCost : 1;
   d.cost_unit = w.kernel == kTile ? kUnitCost : w.kernel == kFew ? kRowsUnitCost : 0;
   d.cost_masked = w.kernel == kTile ? kMaskedCost : 0;
-  d.cost_min = w.kernel == kTile ? kMinCost : w.kernel == kFew ? kRowsMinCost : 4;
+  d.cost_min = w.kernel == kTile ? kMinCost : w.kernel == kFew ? kRowsMinCost : 1;
   const float scale = p->scale > 0.f ? p->scale : 1.f / sqrtf(float(p->head_dim));
   d.scale_log2 = scale * 1.4426950408889634f;
   const bool bf16 = p->dtype == SPEC_BF16;
