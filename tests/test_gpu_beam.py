@@ -98,6 +98,14 @@ def test_select_ties_go_to_the_lower_beam_and_token(V, dtype):
     assert got[1][0, 0] == V - 1 and got[0][0].tolist()[:2] == [0, 1]
 
 
+def test_select_zeros_of_both_signs_are_a_tie():
+    """Finished beams of score -0 and 0, and logits of both, go by beam and token."""
+    x = np.zeros((1, 4, 8))
+    x[0, 3] = [-np.inf, -0.0, 0.0, -0.0, -np.inf, -np.inf, -np.inf, -np.inf]
+    got = Select(x, np.array([[-0.0, 0.0, -0.0, -1.0]]), [[3, 3, 3, 3]], [[1, 1, 1, 0]], 8, eos=7).run()
+    assert got[0].tolist() == [[0, 1, 2, 3]] and got[1].tolist() == [[7, 7, 7, 1]]
+
+
 def test_select_equal_values_at_the_bound():
     """Two values only: the larger one in fewer places than W, then ties in order."""
     V = 9000
