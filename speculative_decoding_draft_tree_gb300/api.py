@@ -23,9 +23,12 @@ def _ws(nbytes: int, device) -> torch.Tensor:
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
-def _grown(ws, nbytes: int, device) -> torch.Tensor:
-    """`ws` if it holds nbytes, else a new workspace."""
-    return ws if ws is not None and ws.numel() >= nbytes else _ws(nbytes, device)
+def _grown(held: list, nbytes: int, device) -> torch.Tensor:
+    """The last workspace of `held` if it holds nbytes, else a new one behind it: the older ones stay, a
+    captured graph may use them."""
+    if not held or held[-1].numel() < nbytes:
+        held.append(_ws(nbytes, device))
+    return held[-1]
 
 
 def _packed(tensors: Dict[str, torch.Tensor], device, pin: bool = False):
@@ -444,7 +447,7 @@ class BeamSearch:
         self._reorder = B.beam_reorder_params(k_cache, v_cache, block_table, self.kv_len,
                                               self.parent, self.beam_status, k_scale, v_scale)
         self._reorder_ws = _ws(B.spec_beam_reorder_workspace_size(self._reorder), dev)
-        self._attn_ws = self._select_ws = None
+        self._attn_ws, self._select_ws = [], []
         self.begin()
 
     def begin(self):
@@ -476,8 +479,8 @@ class BeamSearch:
         p = B.attention_shared_params(q, self.k_cache[layer], self.v_cache[layer], self.block_table,
                                       self.prefix, self.node_offset, self.anc_mask, 1,
                                       self.group_offset, self.prompt_len, o, None, self.status)
-        self._attn_ws = _grown(self._attn_ws, B.spec_attention_shared_workspace_size(p), q.device)
-        B.spec_tree_attention_shared(p, self._attn_ws, stream)
+        ws = _grown(self._attn_ws, B.spec_attention_shared_workspace_size(p), q.device)
+        B.spec_tree_attention_shared(p, ws, stream)
 
     def advance(self, logits, stream=None):
         """logits [B * W, ld >= V]: the best W continuations of each request become its beams, their
@@ -485,9 +488,9 @@ class BeamSearch:
         p = B.beam_select_params(logits, self.V, self.tau, self.scores, self.lengths, self.finished,
                                  self.eos, self.alpha, self.parent, self.tokens, self.scores,
                                  self.lengths, self.finished)
-        self._select_ws = _grown(self._select_ws, B.spec_beam_select_workspace_size(p), logits.device)
+        ws = _grown(self._select_ws, B.spec_beam_select_workspace_size(p), logits.device)
         with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
-            B.spec_beam_select(p, self._select_ws, stream)
+            B.spec_beam_select(p, ws, stream)
             self.kv_len.add_(1)
             self.prefix.add_(1)
             B.spec_beam_reorder(self._reorder, self._reorder_ws, stream)

@@ -106,6 +106,43 @@ def test_shared_trees_and_groups_of_many_sizes():
     S.check(c)
 
 
+def _few_rows_each(kind, H, T):
+    """More (request, head) units of at most 32 rows than two per SM: neighbouring heads share theirs; 3 heads
+    leave one alone.  A group of 65 members has 260 rows and more: two full tiles and a small one."""
+    n = max(2 * torch.cuda.get_device_properties(0).multi_processor_count // H + 1, 80)
+    rng = np.random.default_rng(H * 10 + T)
+    prefix = [40 + int(x) for x in rng.integers(0, 300, n)]
+    if kind == "window":
+        return S.Case(prefix, [T] * n, Hq=4 * H, H=H, window=100, sinks=3, seed=H)
+    return S.Case(prefix, [T] * n, Hq=4 * H, H=H, groups=[(0, 8, 40), (8, 73, 33), (73, 74, 17), (74, n, 0)], seed=H)
+
+
+@pytest.mark.parametrize("kind", ["window", "shared"])
+@pytest.mark.parametrize("H,T", [(3, 5), (8, 8), (4, 1), (3, 1)])
+def test_many_units_of_few_rows(kind, H, T):
+    c = _few_rows_each(kind, H, T)
+    c.run()
+    S.check(c)
+
+
+@pytest.mark.parametrize("kind", ["window", "shared"])
+def test_a_bad_value_stays_under_its_head(kind):
+    """V's infinity in one head's slot does not reach the head that shares the unit, nor other requests."""
+    c = _few_rows_each(kind, 3, 5)
+    c.run()
+    o, lse = c.o.clone(), c.lse.clone()
+    r, h = 9, 1
+    slot = c.prefix[r] + 1                      # the second node's: it and its descendants see it
+    c.v[c.table_np[r, slot // c.bs], h, slot % c.bs, 7] = float("inf")
+    c.run()
+    hit = torch.zeros(c.o.shape[:2], dtype=torch.bool, device="cuda")
+    a = c.off_np[r]
+    for i in range(c.sizes[r]):
+        hit[a + i, 4 * h:4 * h + 4] = bool((c.bits[a + i] >> 1) & 1)
+    assert (~torch.isfinite(c.o[hit][:, 7])).all()
+    assert torch.equal(c.o[~hit].view(torch.int16), o[~hit].view(torch.int16)) and torch.equal(c.lse[~hit], lse[~hit])
+
+
 def test_shared_splits_a_long_prefix():
     c = S.Case([12000, 12100, 12010], [1, 1, 1], Hq=4, H=1, groups=[(0, 3, 12000)], seed=12)
     c.run()
@@ -316,6 +353,17 @@ def test_many_requests(kind):
     sizes = rng.integers(1, 4, n).tolist()
     kw = dict(window=9, sinks=2) if kind == "window" else dict(groups=[(i, min(n, i + 3), 5) for i in range(0, n, 3)])
     c = S.Case(prefix, sizes, Hq=2, H=1, seed=33, **kw)
+    c.run()
+    S.check(c)
+
+
+@pytest.mark.parametrize("members", [0, 1, 2])
+def test_more_requests_than_a_kernels_start_holds(members):
+    """Past 1024 entries and groups (1650 of groups of two, 2200 of one; 0: a window) costs and offsets are read again."""
+    n = 1100
+    prefix = np.random.default_rng(members).integers(5, 40, n).tolist()
+    kw = dict(groups=[(i, i + members, 5) for i in range(0, n, members)]) if members else dict(window=9, sinks=2)
+    c = S.Case(prefix, [1] * n, Hq=2, H=1, seed=35 + members, **kw)
     c.run()
     S.check(c)
 
