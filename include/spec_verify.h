@@ -621,7 +621,7 @@ spec_status_t spec_kv_fork(const spec_fork_params* p, spec_stream_t stream);
  *     the tcgen05 tensor cores, everything else on a CUDA-core kernel;
  *   - a row that sees no key gets O = 0 and LSE = -infinity;
  *   - a NaN or an infinity in q, K or V reaches the rows that see it and no others (of V: the output's
- *     column at least).  Slots that no row of a request sees are not looked at;
+ *     column at least, or the whole row and its LSE).  Slots that no row of a request sees are not looked at;
  *   - the ancestor mask's bits count only for nodes of the request's own tree;
  *   - a request with T_r outside [1, T_max], a negative prefix or node offsets outside [0, N] gets
  *     SPEC_REQ_BAD_SIZE; one whose slots lie beyond its table row (or 2^31 - 1025) SPEC_REQ_BAD_BLOCK; no
@@ -698,7 +698,8 @@ spec_status_t spec_tree_attention_shared(const spec_attn_shared_params* p, void*
  * A beam with score -infinity (a slot that is not in use yet) or NaN offers nothing, nor do logits of
  * -infinity and NaN; a NaN or +infinity among a row's logits takes the whole row out.  If fewer than W are
  * offered the rest is parent j, token 0, score -infinity, length n of beam j, finished 0 at place j.
- * Sums of exponentials are in fp32 per thread and fp64 beyond, scores and ranks in fp64, rounded once.
+ * Sums of exponentials are in fp32 per thread and pairs of fp32 numbers beyond, scores and ranks in fp64,
+ * rounded once.
  * Layouts: logits [B * W][ld] F32 / BF16, rows 16-byte aligned (ld a multiple of 16 bytes); scores [B][W]
  * fp32, lengths (>= 0), finished [B][W] int32; outputs [B][W].  out_score, out_length and out_finished
  * may be the inputs' own buffers.  eos outside [0, V): no token finishes a beam (a finished one then

@@ -7,17 +7,28 @@
 // exponentials 512 of theirs at 32 results a clock, and the operands' reads from shared memory 768 (Q and K
 // for S, V alone for O since P is read from TMEM).  So two row tiles ("slots") alternate: while the
 // products of one run, the other's softmax does.
-//   pair unit    slot s has row tile s, both read every key tile;
-//   single unit  the slots take the key tiles in turn, and the epilogue joins their halves.
+//   pair unit  slot s has row tile s of a head, both read every key tile;
+//   dual unit  slot s has a row tile of head h + s and key tiles of its own: for tiles of few rows, whose start,
+//              join and end are most of their time and are shared so;
+//   lone unit  the slots take the key tiles in turn, and the epilogue joins their halves.
 // CTA (384 threads):
-//   warp 0  Q and K by TMA (three stages of K), warp 2 V (two stages): 128-byte-swizzled boxes of a page,
+//   warp 0  Q and K by TMA (two stages of K), warp 2 V (two stages): 128-byte-swizzled boxes of a page,
 //           or of all of a tile's pages when they follow one another; pages that no row sees come as zeros;
-//   warp 1  one thread issues PV_0(k) QK_0(k+1) PV_1(k) QK_1(k+1) ..; P_s lies over S_s in TMEM, which the
-//           issue order protects; PV starts on the first 64 keys while the softmax still writes the rest;
+//   warp 1  one elected thread issues PV_0(k) QK_0(k+1) PV_1(k) QK_1(k+1) ..; P_s lies over S_s in TMEM, which
+//           the issue order protects; a pair's PV starts on the first 64 keys while the softmax writes the rest;
 //   warp 3  walks the CTA's range and hands the items to the others through a ring;
-//   warps 4-7 and 8-11  softmax of slot 0 and 1, a row per thread with all 128 scores in registers; the
-//           reference moves when the maximum has grown by more than 2^8, and only then is O rescaled.
-// P is rounded to bf16, V's type, which the product wants; the sum takes the unrounded weights.
+//   warps 4-7 and 8-11  softmax of slot 0 and 1, a row per thread, a pair unit's with all 128 scores in
+//           registers; the reference moves when the maximum has grown by more than 2^8, and only then is O
+//           rescaled.
+// The product wants P in V's type.  A pair unit's weights are rounded to bf16 once (error of the output against
+// 64 bits 0.0021 .. 0.0023 of it, 0.0017 being its own rounding's); the others' have the room for a second piece, what
+// that rounding left (0.0017).  The sum takes the unrounded weights.
+//
+// Bound, for long pair units, by the chain of a slot: products 1024 clocks, loads of S and maxima 420, weights 800,
+// waits; ~2650 clocks a key tile against 2048 of products alone (32 trees over 8192 shared slots: 171 us, and
+// 191 with the issuing thread's code unrolled for each slot, which took 1430 clocks a slot to get through, and
+// ranges cut without regard to masked tiles).  Short units are bound by what happens once in each: see the
+// costs in attention_span.cu.
 //
 // Masked tiles (a window's edges, a tree, a last tile): masked scores become -inf before anything is
 // formed from them.  Of V, whose product with a weight of zero would be NaN, the softmax warps look at the
