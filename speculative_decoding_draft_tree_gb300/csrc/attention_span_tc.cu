@@ -538,7 +538,7 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
             for (int half = pair ? s : 0; half < (pair ? s + 1 : 2); ++half) {
               uint8_t* p = tile + half * kAtom;
               uint32_t hits = 0;           // bit i: an exponent of all ones in row 4 i + lane / 8
-#pragma unroll
+#pragma unroll 2
               for (int i = 0; i < 8; ++i) {
                 const uint4 x = *reinterpret_cast<const uint4*>(p + i * 512);
                 const int key = key0 + 4 * i;
