@@ -70,14 +70,10 @@ __global__ void __launch_bounds__(kSimtThreads) span_simt_kernel(Dev a) {
   float* sv = sk + kSimtKeys * ldk;
   pdl_wait();
   pdl_trigger();
-  entry_costs(a, s.scratch);
-  if (threadIdx.x < 32) {
-    const Range mine = warp_range(a, blockIdx.x, s.scratch, s.first);
-    if (reports(mine, gridDim.x)) write_recs(a);
-    if (threadIdx.x == 0) s.range = mine;
-  }
+  find_range(a, s.scratch, s.range, s.first);
   __syncthreads();
   const Range R = s.range;
+  if (threadIdx.x < 32 && reports(R, gridDim.x)) write_recs(a);
   if (R.t0 >= R.t1) return;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int d4 = a.d >> 2;

@@ -23,7 +23,7 @@ namespace spec {
 namespace span {
 
 constexpr int kMaxCtas = 1024;
-constexpr int kGroupCache = 1024, kCostCache = 1024, kEntryCache = 256;   // held in shared memory at the start
+constexpr int kStartCache = 1024;      // requests whose inputs are held in shared memory at the start
 
 struct Dev {
   const int32_t* block_table;
@@ -99,6 +99,14 @@ __device__ __forceinline__ long long entry_cost(const Dev& a, const E& e) {
   return one * (a.H_kv >> 1) + ((a.H_kv & 1) ? block_cost(a, e, n, 1) : 0);
 }
 
+// The inputs that entries come from, possibly a copy.
+struct Inputs {
+  const int32_t *node, *prefix, *status, *off, *shared;
+};
+__device__ __forceinline__ Inputs inputs_of(const Dev& a) {
+  return Inputs{a.node_offset, a.prefix_len, a.req_status, a.group_offset, a.shared_len};
+}
+
 // The group of request r: the g with off[g] <= r < off[g + 1], -1 if the offsets name none.
 __device__ __forceinline__ int find_group(const int32_t* off, int Gn, int r) {
   int lo = 0, hi = Gn - 1;
@@ -111,12 +119,12 @@ __device__ __forceinline__ int find_group(const int32_t* off, int Gn, int r) {
 
 // Group g's tokens, if it is one that is computed together: two members at least, a shared part, and
 // node offsets that lie in [0, N] (a member's own error leaves the others' results as they are).
-__device__ __forceinline__ bool group_tokens(const Dev& a, const int32_t* off, int g, int& o, int& T, int& len) {
-  const int r0 = off[g], r1 = off[g + 1];
-  len = a.shared_len[g];
+__device__ __forceinline__ bool group_tokens(const Dev& a, const Inputs& in, int g, int& o, int& T, int& len) {
+  const int r0 = in.off[g], r1 = in.off[g + 1];
+  len = in.shared[g];
   if (r0 < 0 || r1 > a.B || r1 - r0 < 2 || len <= 0) return false;
-  o = a.node_offset[r0];
-  const int e = a.node_offset[r1];
+  o = in.node[r0];
+  const int e = in.node[r1];
   T = e - o;
   return o >= 0 && e <= a.N && T >= 1 && (long long)(len + a.bs - 1) / a.bs <= a.max_blocks;
 }
@@ -132,29 +140,29 @@ __device__ __forceinline__ void key_tiles(const Dev& a, Entry& e) {
   e.cu = a.cost_unit + a.cost_masked * min(masked, e.nt);
 }
 
-// Entry i of the stream (groups first).  `off`: the group offsets, possibly a copy.  mts = 0: no work.
+// Entry i of the stream (groups first).  mts = 0: no work.
 // `bad`: SPEC_REQ_* bits that the request gets.  The bits that this library's attention sets itself
 // (BAD_BLOCK, TIMEOUT) are ignored, and the others only take away a request's own units, so that all
 // roles of all CTAs derive the same stream from the same inputs.
-__device__ __forceinline__ Entry entry_of(const Dev& a, const int32_t* off, int i, int& bad) {
+__device__ __forceinline__ Entry entry_of(const Dev& a, const Inputs& in, int i, int& bad) {
   Entry e;
   e.o = e.T = e.P = e.end = e.lo = e.sink = e.nt0 = e.w0 = e.nt = e.mts = e.cu = e.table = 0;
   e.group = -1;
   bad = 0;
   if (i < a.Gn) {
     int o, T, len;
-    if (!group_tokens(a, off, i, o, T, len)) return e;
+    if (!group_tokens(a, in, i, o, T, len)) return e;
     e.o = o;
     e.T = T;
     e.P = e.end = len;
-    e.table = off[i];
+    e.table = in.off[i];
     e.group = i;
     key_tiles(a, e);
     return e;
   }
   const int r = i - a.Gn;
-  const int o = a.node_offset[r], T = a.node_offset[r + 1] - o, P = a.prefix_len[r];
-  const int st = a.req_status[r] & ~(SPEC_REQ_BAD_BLOCK | SPEC_REQ_TIMEOUT);
+  const int o = in.node[r], T = in.node[r + 1] - o, P = in.prefix[r];
+  const int st = in.status[r] & ~(SPEC_REQ_BAD_BLOCK | SPEC_REQ_TIMEOUT);
   if (st != 0) return e;
   if (T < 1 || T > a.T_max || P < 0 || o < 0 || o + T > a.N) {
     bad = SPEC_REQ_BAD_SIZE;
@@ -174,14 +182,14 @@ __device__ __forceinline__ Entry entry_of(const Dev& a, const int32_t* off, int 
     e.lo = max(0, P - a.window + 1);
     e.sink = min(a.sinks, e.lo);
   } else if (a.Gn > 0) {
-    const int g = find_group(off, a.Gn, r);
+    const int g = find_group(in.off, a.Gn, r);
     int go, gT, len;
-    if (g < 0 || a.shared_len[g] < 0 || a.shared_len[g] > P) {
+    if (g < 0 || in.shared[g] < 0 || in.shared[g] > P) {
       bad = SPEC_REQ_BAD_SIZE;
       e.T = 0;
       return e;
     }
-    if (group_tokens(a, off, g, go, gT, len)) {
+    if (group_tokens(a, in, g, go, gT, len)) {
       if (o < go || o + T > go + gT) {
         bad = SPEC_REQ_BAD_SIZE;
         e.T = 0;
@@ -189,7 +197,7 @@ __device__ __forceinline__ Entry entry_of(const Dev& a, const int32_t* off, int 
       }
       e.lo = len;
       e.group = -2 - g;
-    } else if (off[g + 1] - off[g] >= 2 && a.shared_len[g] > 0) {   // the group's offsets are bad
+    } else if (in.off[g + 1] - in.off[g] >= 2 && in.shared[g] > 0) {   // the group's offsets are bad
       bad = SPEC_REQ_BAD_SIZE;
       e.T = 0;
       return e;
@@ -227,11 +235,10 @@ struct Range {
   int e0, C;
 };
 
-// Scratch of the search: the group offsets, the entries' costs and the first entries, where they fit.
+// Scratch of the search: the warps' costs and the inputs, where they fit.
 struct RangeScratch {
-  long long cost[kCostCache];
-  Entry entry[kEntryCache];
-  int32_t off[kGroupCache + 1];
+  long long sum[32];
+  int32_t node[kStartCache + 1], prefix[kStartCache], status[kStartCache], off[kStartCache + 1], shared[kStartCache];
 };
 
 __device__ __forceinline__ long long warp_scan(long long v) {
@@ -243,79 +250,71 @@ __device__ __forceinline__ long long warp_scan(long long v) {
   return v;
 }
 
-// All threads of the CTA: the costs of the first entries, in one or two round trips to memory.
-__device__ __forceinline__ void entry_costs(const Dev& a, RangeScratch& s) {
-  const int E = a.Gn + a.B;
-  const int32_t* off = a.group_offset;
-  if (a.Gn > 0 && a.Gn <= kGroupCache) {
-    for (int i = threadIdx.x; i <= a.Gn; i += blockDim.x) s.off[i] = a.group_offset[i];
+// All threads of the CTA find its range, an entry (or a run of entries) a thread, and `first`, the entry that it
+// begins in, where a thread has only one (T = 0 else).  The inputs come in one round trip to memory, not in the
+// chain that an entry's checks make of them.  The caller synchronises before it reads R.
+__device__ __forceinline__ void find_range(const Dev& a, RangeScratch& s, Range& R, Entry& first) {
+  const int E = a.Gn + a.B, nthr = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Inputs in = inputs_of(a);
+  if (a.B <= kStartCache) {              // Gn <= B
+#pragma unroll 1
+    for (int i = threadIdx.x; i <= a.B; i += nthr) {
+      const bool r = i < a.B, g = i < a.Gn;
+      const int32_t node = in.node[i], prefix = r ? in.prefix[i] : 0, status = r ? in.status[i] : 0;
+      const int32_t off = i <= a.Gn && a.Gn > 0 ? in.off[i] : 0, shared = g ? in.shared[i] : 0;
+      s.node[i] = node;
+      if (r) {
+        s.prefix[i] = prefix;
+        s.status[i] = status;
+      }
+      s.off[i] = off;
+      if (g) s.shared[i] = shared;
+    }
     __syncthreads();
-    off = s.off;
+    in = Inputs{s.node, s.prefix, s.status, s.off, s.shared};
   }
+  const int run = (E + nthr - 1) / nthr, i0 = min(E, int(threadIdx.x) * run), i1 = min(E, i0 + run);
+  Entry e;
+  e.T = 0;
+  long long mine = 0;
 #pragma unroll 1
-  for (int i = threadIdx.x; i < min(E, kCostCache); i += blockDim.x) {
+  for (int i = i0; i < i1; ++i) {
     int bad;
-    const Entry e = entry_of(a, off, i, bad);
-    s.cost[i] = entry_cost(a, e);
-    if (i < kEntryCache) s.entry[i] = e;
+    e = entry_of(a, in, i, bad);
+    mine += entry_cost(a, e);
   }
+  long long lo = warp_scan(mine);
+  if (lane == 31) s.sum[warp] = lo;
   __syncthreads();
-}
-
-// One warp finds range c; entry_costs has been there.  `first`: entry e0, if its length is not 0.
-__device__ __forceinline__ Range warp_range(const Dev& a, int c, RangeScratch& s, Entry& first) {
-  const int lane = threadIdx.x & 31, E = a.Gn + a.B;
-  Range R;
-  R.t0 = R.t1 = R.beg0 = 0;
-  R.e0 = 0;
-  R.C = 0;
-  long long sum = 0;            // pass 0: this lane's costs; pass 1: the cost before the chunk
+  lo -= mine;
+  long long total = 0;
 #pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass) {
-#pragma unroll 1
-    for (int i0 = 0; i0 < E; i0 += 32) {
-      const int i = i0 + lane;
-      long long cost = 0;
-      if (i < E) {
-        if (i < kCostCache) {
-          cost = s.cost[i];
-        } else {
-          int bad;
-          const Entry e = entry_of(a, a.Gn <= kGroupCache ? s.off : a.group_offset, i, bad);
-          cost = entry_cost(a, e);
-        }
-      }
-      if (pass == 0) {
-        sum += cost;
-        continue;
-      }
-      const long long hi = warp_scan(cost) + sum, lo = hi - cost;
-      const uint32_t here = __ballot_sync(0xffffffffu, cost > 0 && lo <= R.t0 && R.t0 < hi);
-      if (here) {
-        const int at = i0 + __ffs(here) - 1;
-        R.e0 = at;
-        R.beg0 = __shfl_sync(0xffffffffu, lo, __ffs(here) - 1);
-        if (lane == 0) {
-          if (at < kEntryCache) first = s.entry[at];
-          else first.T = 0;
-        }
-        return R;
-      }
-      sum = __shfl_sync(0xffffffffu, hi, 31);
-    }
-    if (pass == 0) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      const Cut cut = cut_of(a, sum);
-      R.C = cut.C;
-      if (sum == 0 || c >= cut.C) return R;      // no work
-      R.t0 = range_start(cut, c);
-      R.t1 = range_start(cut, c + 1);
-      sum = 0;
-    }
+  for (int w = 0; w < nthr >> 5; ++w) {
+    if (w == warp) lo += total;
+    total += s.sum[w];
   }
-  R.t1 = R.t0;      // never: the scan finds the entry
-  return R;
+  const Cut cut = cut_of(a, total);
+  const bool none = total == 0 || int(blockIdx.x) >= cut.C;
+  const long long t0 = none ? 0 : range_start(cut, blockIdx.x);
+  if (none ? threadIdx.x == 0 : lo <= t0 && t0 < lo + mine) {
+    int at = i0;
+    if (!none && run > 1) {            // which of the thread's entries
+#pragma unroll 1
+      for (;; ++at) {
+        int bad;
+        e = entry_of(a, in, at, bad);
+        const long long cost = entry_cost(a, e);
+        if (t0 < lo + cost || at + 1 >= i1) break;
+        lo += cost;
+      }
+    }
+    R.t0 = t0;
+    R.t1 = none ? 0 : range_start(cut, blockIdx.x + 1);
+    R.beg0 = none ? 0 : lo;
+    R.e0 = at;
+    R.C = cut.C;
+    first = e;
+  }
 }
 
 // One warp of one CTA writes what the merge reads and flags the requests that cannot be worked on.  A CTA
@@ -325,7 +324,7 @@ __device__ __forceinline__ bool reports(const Range& R, int ctas) {
 }
 __device__ __forceinline__ void write_recs(const Dev& a) {
   const int lane = threadIdx.x & 31;
-  const int32_t* off = a.group_offset;
+  const Inputs in = inputs_of(a);
   long long sum = 0;
 #pragma unroll 1
   for (int i0 = 0; i0 < a.Gn + a.B; i0 += 32) {
@@ -334,7 +333,7 @@ __device__ __forceinline__ void write_recs(const Dev& a) {
     Rec r;
     if (i < a.Gn + a.B) {
       int bad;
-      const Entry e = entry_of(a, off, i, bad);
+      const Entry e = entry_of(a, in, i, bad);
       cost = entry_cost(a, e);
       if (bad) atomicOr(&a.req_status[i - a.Gn], bad);
       r.o = e.o; r.T = e.T; r.nt = e.nt; r.mts = e.mts; r.group = e.group; r.cu = e.cu;
@@ -381,7 +380,7 @@ struct Walker {
         if (++i >= a.Gn + a.B) return false;
         if (!known) {
           int bad;
-          e = entry_of(a, a.group_offset, i, bad);
+          e = entry_of(a, inputs_of(a), i, bad);
         }
         known = false;
         n = units_of(a, e);

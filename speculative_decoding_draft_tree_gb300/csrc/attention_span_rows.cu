@@ -181,11 +181,7 @@ span_rows_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__
   }
   pdl_wait();
   pdl_trigger();
-  entry_costs(a, *reinterpret_cast<RangeScratch*>(sK));
-  if (warp == 3) {
-    const Range mine = warp_range(a, blockIdx.x, *reinterpret_cast<RangeScratch*>(sK), c.first);
-    if (lane == 0) c.range = mine;
-  }
+  find_range(a, *reinterpret_cast<RangeScratch*>(sK), c.range, c.first);
   tc::tc_fence_before();
   tc::fence_proxy_async_smem();      // the scratch lies where TMA writes next
   __syncthreads();

@@ -230,11 +230,7 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
   }
   pdl_wait();
   pdl_trigger();
-  entry_costs(a, *reinterpret_cast<RangeScratch*>(smem));
-  if (warp == 3) {
-    const Range mine = warp_range(a, blockIdx.x, *reinterpret_cast<RangeScratch*>(smem), c.first);
-    if (lane == 0) c.range = mine;
-  }
+  find_range(a, *reinterpret_cast<RangeScratch*>(smem), c.range, c.first);
   tc::tc_fence_before();
   // the scratch was read and written through the generic proxy where TMA writes next
   tc::fence_proxy_async_smem();
