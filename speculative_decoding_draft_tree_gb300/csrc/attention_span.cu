@@ -459,7 +459,7 @@ static spec_status_t launch_merge(const Dev& a, cudaStream_t s) {
 // heads' a dual one 4000, one a lone one 2000, a unit's start and end 9000, and a tile under a mask 2500 more.
 constexpr int kPairCost = 4, kDualCost = 6, kSingleCost = 3, kUnitCost = 14, kMaskedCost = 4, kMinCost = 16;
 // The rows kernel's: a tile, a unit, a range.
-// (a range of one unit with a tile or two: 1 token, window 1024 17.6 us, 18.7 with a minimum of 8)
+// (a range of one unit with a tile or two: 1 token, window 1024 17.5 us, 18.7 with a minimum of 8)
 constexpr int kRowsTileCost = 2, kRowsUnitCost = 2, kRowsMinCost = 6;
 constexpr int kDualRows = 32;
 constexpr int kFewRows = 16;       // query rows of a unit up to which the rows kernel takes it
@@ -503,9 +503,9 @@ static spec_status_t check(const Args& x) {
 
 // The kernel of a call: on the tensor cores the rows kernel for windows over at most 16 query rows a request
 // and head (64 single tokens, 64 query heads on 8, window 4096: 171 us against 191 by the tile kernel; one
-// token, window 1024: 18 against 25), else the tile kernel, which also takes a shared call's few-rowed requests
-// beside their groups (8 groups of 8 single tokens, 32 heads on 8, 8192 shared: 95 us; by one kernel for the
-// groups and then the other 112); the CUDA-core kernel for everything else.
+// token, window 1024: 17.5 against 25), else the tile kernel, which also takes a shared call's few-rowed requests
+// beside their groups (8 groups of 8 single tokens, 32 heads on 8, 8192 shared: 94 us, 83 now; by one kernel for
+// the groups and then the other 112); the CUDA-core kernel for everything else.
 enum Kernel { kSimt, kTile, kFew };
 struct Plan {
   Kernel kernel;
@@ -576,7 +576,7 @@ static spec_status_t launch(const Args& x, void* ws, size_t ws_bytes, cudaStream
   d.window = x.window; d.sinks = x.sinks;
   d.rt = w.rt; d.bn = w.bn; d.part_rows = w.part_rows; d.pairing = w.kernel == kTile ? 1 : 0;
   // Two heads share a unit where its rows are few, its start, join and end then being most of it, and there are
-  // requests enough for every CTA (64 single tokens, 32 heads on 8, 8192 shared by groups of 8: 82 us against 94);
+  // requests enough for every CTA (64 single tokens, 32 heads on 8, 8192 shared by groups of 8: 83 us against 94);
   // not where the row tiles are fuller (32 trees, shared 8192: 169 against 166) or CTAs idle (4 requests: 26
   // against 23).
   d.dual_rows = (long long)p->B * p->H_kv >= 2LL * w.ctas ? kDualRows : 0;
