@@ -13,7 +13,9 @@
 //   items and lays out what a unit's rows see; warps 4-7, 8-11 softmax; 12-15 output.
 // References: weights are formed against the row's reference at hand.  bf16 has fp32's exponents, so a weight
 // of 2^60 is as good as one of 2^-1; only beyond that, and at a row's first visible key, the group agrees on
-// a new one (one vote a tile, no maxima).
+// a new one (one vote a tile, no maxima), once a tile: the new one is the largest score rounded down, so that it
+// may lie below that score by a step of fp32 in the end, which at 2^30 is more than 60.  Weights stop at 2^60, which
+// moves scores by less than that step; the fused product is rounded once in it as well.
 //
 // What runs once a unit (a reference's first setting, the output, masks) is kept short in instructions rather
 // than in steps: it comes from beyond the instruction cache every time.  The output unrolled over 16 rows with
@@ -519,7 +521,7 @@ span_rows_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__
         // Exponents; beyond kFar (a row's first visible key: +inf) the references move, and they are formed
         // again.  A masked key has the exponent -inf.
         float y[kN];
-        while (true) {
+        for (bool moved = false;; moved = true) {
           const uint64_t slv = f2_pack(sl2, sl2);
           float ym = -INFINITY;
 #pragma unroll
@@ -531,12 +533,18 @@ span_rows_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__
             }
             ym = fmax3(ym, y[n], y[n + 1]);
           }
+          if (moved) {
+            // (a NaN stays; +inf, of products beyond fp32, becomes one)
+#pragma unroll
+            for (int n = 0; n < kN; ++n) y[n] = y[n] > kFar ? (y[n] < INFINITY ? kFar : NAN) : y[n];
+            break;
+          }
           if (!group_any(bar, ym > kFar || !ok)) break;
           // the group's maxima of all rows
           float v[kN];
 #pragma unroll
           for (int n = 0; n < kN; ++n) v[n] = (vis >> n) & 1u ? __uint_as_float(x[n]) : -INFINITY;
-          const float mine = reduce16<true>(v, lane) * sl2;
+          const float mine = __fmul_rd(reduce16<true>(v, lane), sl2);
           if ((lane & 1) == 0) c.top[g][q4][lane >> 1] = mine;
           if (ok && k > 1) ok = warp_wait(&c.pv_done[g], (sn - 1) & 1, abort_flag);
           if (group_any(bar, !ok)) { leave = true; break; }       // and the maxima are there

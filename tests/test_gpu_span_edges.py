@@ -1,0 +1,103 @@
+"""Windowed and shared-prefix attention at their edges: masks with bits behind the tree, scores of any finite size,
+values that are not finite under weights that underflow, and group arrays that cannot be."""
+import numpy as np
+import pytest
+import torch
+
+import kv8_util as U
+import span_util as S
+from oracle import span
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+
+# Which kernel a call takes: at most 16 query rows a request and head, more of them (one row tile, two), fp32.
+KERNELS = {"rows": dict(dtype=BF16, T=2, Hq=8, H=2), "tile": dict(dtype=BF16, T=20, Hq=8, H=2), "pairs": dict(dtype=BF16, T=64, Hq=8, H=2),
+           "cores": dict(dtype=F32, T=5, Hq=4, H=2)}
+
+
+# ------------------------------------------------------------------------------------ large scores
+def _scores(c):
+    """(row, query head, its scores in 64 bits, their products' magnitudes, the slots' values) of every row that sees
+    something."""
+    G = c.q.shape[1] // c.k.shape[1]
+    q, table = c.q.double().cpu().numpy(), torch.from_numpy(c.table_np).long()
+    for r, (P, T) in enumerate(zip(c.prefix, c.sizes)):
+        first, length = r, 0
+        for a, b, ln in c.groups or []:
+            if a <= r < b:
+                first, length = a, ln
+        slots = torch.arange(P + T)
+        page = torch.where(slots < length, table[first][torch.clamp(slots // c.bs, max=table.shape[1] - 1)], table[r][slots // c.bs])
+        at = (page.clamp(min=0).cuda(), slice(None), (slots % c.bs).cuda())
+        K, V = [t[at[0], :, at[2]].double().cpu().numpy() for t in (c.k, c.v)]
+        for i in range(T):
+            n = int(c.off_np[r]) + i
+            seen = np.array(span.visible(c.bits[n], P, T, c.window, c.sinks), dtype=int)
+            for h in range(c.q.shape[1] if len(seen) else 0):
+                k, x = K[seen, h // G], q[n, h] / np.sqrt(q.shape[2])
+                yield n, h, k @ x, np.abs(k) @ np.abs(x), V[seen, h // G]
+
+
+def _one_hot(c):
+    """Rows whose best score stands out of what fp32 sums and one rounding of a score can move (2^-17 of the products'
+    magnitudes for each, 64 for an exponential that is nothing beside it): the output is that key's V, rounded
+    once (pair units round its weight before), and the log-sum-exp that score.  Returns how many there are."""
+    o, lse = c.o[:c.N].double().cpu().numpy(), c.lse[:c.N].double().cpu().numpy()
+    found = 0
+    for n, h, x, size, V in _scores(c):
+        at = int(np.argmax(x))
+        slack = 2.0 ** -17 * size.max()
+        rest = np.delete(x, at)
+        if len(rest) and x[at] - rest.max() < 2 * slack + 64:
+            continue
+        found += 1
+        assert (np.abs(o[n, h] - V[at]) <= 2.0 ** -7 * np.abs(V[at])).all(), (n, h)
+        assert abs(lse[n, h] - x[at]) <= slack + 2.0 ** -20 * abs(x[at]), (n, h)
+    return found
+
+
+def _large(kernel, kind, exps, sign, seed, prefix=(700, 90, 0, 1400), T=None):
+    k = KERNELS[kernel]
+    T = T or k["T"]
+    kw = dict(window=5000, sinks=2) if kind == "window" else dict(groups=[(0, 2, 90), (2, 4, 0)])
+    c = S.Case(list(prefix), [T] * len(prefix), Hq=k["Hq"], H=k["H"], dtype=k["dtype"], seed=seed, **kw)
+    if sign < 0:            # every score negative
+        c.k.copy_(c.k.abs())
+        c.q.copy_(-c.q.abs())
+    step = torch.tensor([float(exps[n % len(exps)]) for n in range(c.q.shape[0])], device="cuda")
+    c.q.copy_(c.q.float() * torch.exp2(step)[:, None, None])
+    c.run()
+    return c
+
+
+@pytest.mark.parametrize("kernel", ["rows", "cores"])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("exps", [(26,), (27, 28, 29), (30, 31), (33, 40), (60, 90), (0, 30, 5, 100)], ids=str)
+def test_finite_scores_of_any_size_under_a_window(kernel, exps, sign):
+    """A score of 2^30 and more is a rounded number whose last place is tens of units of the exponent."""
+    c = _large(kernel, "window", exps, sign, 41)
+    S.check(c)
+    assert _one_hot(c) > 0.5 * c.N * c.q.shape[1] * (1 - exps.count(0) / len(exps))
+
+
+@pytest.mark.parametrize("kernel", ["rows", "cores"])
+def test_large_scores_of_equal_keys(kernel):
+    """The best key stands in many slots of a unit's tiles: each of them has the same weight.  (Units that are not cut: a
+    piece's log-sum-exp is one fp32 number, which at 2^36 does not say how many keys it came from.)"""
+    k = KERNELS[kernel]
+    c = S.Case([50, 40] if kernel == "cores" else [250, 120], [k["T"]] * 2, Hq=k["Hq"], H=k["H"], dtype=k["dtype"], window=20000, seed=43)
+    u = torch.randn((128,), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    c.q.copy_((u * 2.0 ** 33).expand_as(c.q))
+    live = ~c.k.isnan()
+    keys = torch.where((torch.arange(c.k.shape[2], device="cuda") % 2 == 0)[:, None], u, -u).expand_as(c.k).to(c.k.dtype)
+    c.k.copy_(torch.where(live, keys, c.k))
+    c.run()
+    o, lse = c.o.double().cpu().numpy(), c.lse.double().cpu().numpy()
+    for n, h, x, size, V in _scores(c):
+        best = x.max() - x <= 1e-12 * np.abs(x).max()
+        assert best.sum() >= 20
+        want, mass = V[best].mean(axis=0), np.abs(V[best]).mean(axis=0)
+        # weights of 1, whose sum and products are exact in any order up to fp32's 2^-24 for each of 150 terms
+        assert (np.abs(o[n, h] - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -11 * mass).all(), (n, h)
+        assert abs(lse[n, h] - x.max()) <= 2.0 ** -17 * size.max()
