@@ -71,7 +71,7 @@ def _large(kernel, kind, exps, sign, seed, prefix=(700, 90, 0, 1400), T=None):
     return c
 
 
-@pytest.mark.parametrize("kernel", ["rows", "cores"])
+@pytest.mark.parametrize("kernel", list(KERNELS))
 @pytest.mark.parametrize("sign", [1, -1])
 @pytest.mark.parametrize("exps", [(26,), (27, 28, 29), (30, 31), (33, 40), (60, 90), (0, 30, 5, 100)], ids=str)
 def test_finite_scores_of_any_size_under_a_window(kernel, exps, sign):
@@ -81,12 +81,23 @@ def test_finite_scores_of_any_size_under_a_window(kernel, exps, sign):
     assert _one_hot(c) > 0.5 * c.N * c.q.shape[1] * (1 - exps.count(0) / len(exps))
 
 
-@pytest.mark.parametrize("kernel", ["rows", "cores"])
+@pytest.mark.parametrize("kernel", list(KERNELS))
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("exps", [(26,), (30, 31), (33, 40), (0, 30, 5, 100)], ids=str)
+def test_finite_scores_of_any_size_under_a_shared_prefix(kernel, exps, sign):
+    c = _large(kernel, "shared", exps, sign, 42)
+    S.check(c)
+    assert _one_hot(c) > 0.5 * c.N * c.q.shape[1] * (1 - exps.count(0) / len(exps))
+
+
+@pytest.mark.parametrize("kernel", list(KERNELS))
 def test_large_scores_of_equal_keys(kernel):
-    """The best key stands in many slots of a unit's tiles: each of them has the same weight.  (Units that are not cut: a
-    piece's log-sum-exp is one fp32 number, which at 2^36 does not say how many keys it came from.)"""
+    """The best key stands in many slots of a unit: each of them has the same weight.  (Units that are not cut, of one key tile
+    but for the rows kernel's: a piece's log-sum-exp is one fp32 number, which at 2^36 does not say how many keys it
+    came from.)"""
     k = KERNELS[kernel]
-    c = S.Case([50, 40] if kernel == "cores" else [250, 120], [k["T"]] * 2, Hq=k["Hq"], H=k["H"], dtype=k["dtype"], window=20000, seed=43)
+    prefix = {"rows": [250, 120], "tile": [100, 60], "pairs": [50, 60], "cores": [50, 40]}[kernel]
+    c = S.Case(prefix, [k["T"]] * 2, Hq=k["Hq"], H=k["H"], dtype=k["dtype"], window=20000, seed=43)
     u = torch.randn((128,), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
     c.q.copy_((u * 2.0 ** 33).expand_as(c.q))
     live = ~c.k.isnan()
