@@ -20,7 +20,9 @@
 // Ranks of different beams meet in one list, so log p has to be good.  References are whole numbers (the
 // maximum of x k2, rounded up), so that sums over threads and segments join by exact powers of two; log p =
 // (x k2 - ref - log2 sum) ln 2 has the sum's error (about 1e-7: fp32 sums of a few hundred terms a thread, twice
-// that precision beyond) and a relative 2^-25 of k2's rounding, whatever the logits' size.
+// that precision beyond) and a relative 2^-25 of k2's rounding, whatever the logits' size: where the largest one, times
+// k2, is 2^31 or more, the next ones in the type's order are 64 and more below it and weigh nothing beside it, so the sum is how
+// often it occurs, and logits enter log p by their difference from it.
 #include <math.h>
 
 #include "common.cuh"
@@ -72,8 +74,11 @@ __device__ __forceinline__ double exp2_of(double w) {           // |w| < 1000
 struct Seg {
   dfloat sum;        // sum of 2^(x k2 - ref)
   float ref;
-  int count;         // candidates
+  int count;         // candidates; + kCoarseSeg: ref is the largest logit, which is coarse, and sum how often it occurs
 };
+constexpr int kCoarseSeg = 256;
+// What stands for a part's largest logit where parts join: itself if it is coarse, 0 for others, -infinity for none.
+// Coarse ones beside a larger one count for nothing.
 
 struct SelectDev {
   const void* logits;
@@ -90,9 +95,11 @@ struct SelectDev {
   int32_t* cand_id;
   int64_t ld;
   int W, V, S, seg_vecs, eos;   // seg_vecs: 16-byte vectors of a segment
-  float k2;
+  float k2, coarse;             // coarse: logits of that magnitude and more are told apart by themselves, not by x k2
   double alpha;
 };
+// a finite or +infinite maximum that is; its row's sum is a count
+__device__ __forceinline__ bool is_coarse(const SelectDev& a, float m) { return fabsf(m) >= a.coarse && m > -INFINITY; }
 
 __device__ __forceinline__ bool ahead(float v, int id, float w, int jd) { return v > w || (v == w && id < jd); }
 
@@ -111,7 +118,7 @@ template <typename T>
 __global__ void __launch_bounds__(kRowThreads) beam_rows_kernel(SelectDev a) {
   constexpr int kE = elem<T>::per16;
   constexpr int kWarps = kRowThreads / 32;
-  __shared__ float s_group[32], s_ref[kWarps], s_v[kList], s_bv[kWarps];
+  __shared__ float s_group[32], s_ref[kWarps], s_max[kWarps], s_v[kList], s_bv[kWarps];
   __shared__ dfloat s_sum[kWarps];
   __shared__ int s_id[kList], s_hot[kRowThreads], s_bi[kWarps];
   __shared__ int s_n, s_nhot;
@@ -157,14 +164,18 @@ __global__ void __launch_bounds__(kRowThreads) beam_rows_kernel(SelectDev a) {
     if (cm > m) {
       m = cm;
       const float to = ceilf(cm * a.k2);
-      if (to > ref) {
-        sum = ref == kNoRef ? sum : sum * ex2(ref - to);     // exact: whole numbers (a NaN stays)
+      if (!(fabsf(cm) < a.coarse)) {
+        sum = sum != sum ? sum : 0.f;                        // what came before is nothing beside it
+      } else if (to > ref) {
+        // exact: whole numbers (a NaN stays; a coarse maximum's count does not)
+        sum = ref != kNoRef ? sum * ex2(ref - to) : sum != sum ? sum : 0.f;
         ref = to;
       }
     }
-    if (m == -INFINITY) {        // -inf only so far; a NaN still has to show
+    if (!(fabsf(m) < a.coarse)) {        // coarse, or -inf only so far; a NaN still has to show
 #pragma unroll
-      for (int k = 0; k < kUnroll * kE; ++k) sum = x[k] != x[k] ? x[k] : sum;
+      for (int k = 0; k < kUnroll * kE; ++k) sum = x[k] != x[k] ? x[k] : x[k] == m && m > -INFINITY ? sum + 1.f : sum;
+      if (m == INFINITY) sum = NAN;
       continue;
     }
     const uint64_t neg = f2_pack(-ref, -ref);
@@ -181,6 +192,13 @@ __global__ void __launch_bounds__(kRowThreads) beam_rows_kernel(SelectDev a) {
     sum += (a0 + a1) + (a2 + a3);
   }
   // the segment's reference and sum
+  float wm = 0.f;
+  if (__any_sync(0xffffffffu, is_coarse(a, m))) {
+    wm = warp_max(m);
+    if (is_coarse(a, wm) ? m != wm : is_coarse(a, m)) sum = sum != sum ? sum : 0.f;
+    if (is_coarse(a, wm)) ref = kNoRef;
+    else wm = 0.f;
+  }
   const float mref = warp_max(ref);
   const dfloat ws = warp_sum_df(df_make(ref == kNoRef ? sum : sum * ex2(ref - mref)));
   float gm = m;
@@ -189,6 +207,7 @@ __global__ void __launch_bounds__(kRowThreads) beam_rows_kernel(SelectDev a) {
   if ((lane & 7) == 0) s_group[warp * 4 + (lane >> 3)] = gm;
   if (lane == 0) {
     s_ref[warp] = mref;
+    s_max[warp] = wm == 0.f && mref == kNoRef ? -INFINITY : wm;
     s_sum[warp] = ws;
   }
   __syncthreads();
@@ -293,8 +312,17 @@ __global__ void __launch_bounds__(kRowThreads) beam_rows_kernel(SelectDev a) {
   if (warp == 0) {
     // fp64 runs at a sixteenth of fp32's rate and less here: the sums join as pairs of fp32 numbers
     const float r = lane < kWarps ? s_ref[lane] : kNoRef;
-    const float top = warp_max(r);
-    const float f = r == kNoRef ? 1.f : ex2(r - top);
+    const float mw = lane < kWarps ? s_max[lane] : -INFINITY;
+    float top = warp_max(r), f = r == kNoRef ? 1.f : ex2(r - top);
+    int coarse = 0;
+    if (__any_sync(0xffffffffu, is_coarse(a, mw))) {
+      const float best = warp_max(mw);
+      if (is_coarse(a, mw) ? mw != best : is_coarse(a, best)) f = 0.f;
+      if (is_coarse(a, best)) {
+        top = best;
+        coarse = kCoarseSeg;
+      }
+    }
     dfloat t = lane < kWarps ? s_sum[lane] : df_make(0.f);
     t = {t.hi * f, t.lo * f};
 #pragma unroll
@@ -303,7 +331,7 @@ __global__ void __launch_bounds__(kRowThreads) beam_rows_kernel(SelectDev a) {
       Seg g;
       g.sum = t;
       g.ref = top;
-      g.count = min(n, a.W);
+      g.count = min(n, a.W) + coarse;
       a.seg[out] = g;
     }
   }
@@ -320,6 +348,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(SelectDev a) {
   __shared__ float s_v[SPEC_MAX_BEAMS * kMaxSegLists];      // beam's segment lists, id 0x7fffffff where short
   __shared__ int s_id[SPEC_MAX_BEAMS * kMaxSegLists];
   __shared__ double s_lse[SPEC_MAX_BEAMS], s_inv[SPEC_MAX_BEAMS];      // log2 of the row's sum; 1 / penalty
+  __shared__ float s_base[SPEC_MAX_BEAMS];                             // what logits are taken from: 0, or a coarse maximum
   __shared__ dfloat s_sum[SPEC_MAX_BEAMS];
   __shared__ float s_top[SPEC_MAX_BEAMS];
   __shared__ float s_score[SPEC_MAX_BEAMS];
@@ -341,7 +370,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(SelectDev a) {
       cv[k] = a.cand_v[size_t(r0) * per + i];
       ci[k] = a.cand_id[size_t(r0) * per + i];
       const int j = i / per, sg = (i - j * per) / W;
-      if (i - j * per - sg * W >= a.seg[size_t(r0 + j) * a.S + sg].count) ci[k] = 0x7fffffff;
+      if (i - j * per - sg * W >= (a.seg[size_t(r0 + j) * a.S + sg].count & (kCoarseSeg - 1))) ci[k] = 0x7fffffff;
     }
   }
   // sixteen lanes a beam: the sum over its segments
@@ -349,7 +378,8 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(SelectDev a) {
     const int w = tid >> 4, sub = tid & 15;
     const bool mine = w < W;
     const int row = r0 + (mine ? w : 0);
-    float ref = kNoRef;
+    float ref = kNoRef, base = 0.f;
+    bool coarse = false;
     dfloat sum = df_make(0.f);
     const float sc = a.scores[row];
     const int fin = a.finished[row] != 0, len = a.lengths[row];
@@ -357,6 +387,17 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(SelectDev a) {
       const Seg g = a.seg[size_t(row) * a.S + sub];
       ref = g.ref;
       sum = g.sum;
+      coarse = (g.count & kCoarseSeg) != 0;
+    }
+    // sixteen lanes join what they have; a warp has two beams
+    if (__any_sync(0xffffffffu, coarse)) {
+      float best = coarse ? ref : ref == kNoRef ? -INFINITY : 0.f;
+      const float m = best;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
+      if (coarse ? m != best : is_coarse(a, best)) sum = {sum.hi * 0.f, sum.lo * 0.f};      // (a NaN stays)
+      if (coarse || is_coarse(a, best)) ref = kNoRef;
+      base = is_coarse(a, best) ? best : 0.f;
     }
     float top = ref;
 #pragma unroll
@@ -367,9 +408,10 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(SelectDev a) {
     for (int o = 8; o > 0; o >>= 1) sum = df_add(sum, df_shfl_xor(sum, o));
     if (mine && sub == 0) {
       // a NaN or an infinity: the row is out
-      const bool good = sum.hi > 0.f && sum.hi < INFINITY && top < INFINITY;
+      const bool good = sum.hi > 0.f && sum.hi < INFINITY && base < INFINITY;
       s_sum[w] = good ? sum : df_make(1.f);
-      s_top[w] = good ? top : 0.f;
+      s_top[w] = good && base == 0.f ? top : 0.f;
+      s_base[w] = good ? base : 0.f;
       s_score[w] = sc;
       s_len[w] = len;
       s_fin[w] = fin;
@@ -410,7 +452,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(SelectDev a) {
 #pragma unroll 8
     for (int q = j * per; q < (j + 1) * per; ++q) rank += ahead(s_v[q], s_id[q], cv[k], ci[k]) ? 1 : 0;
     if (rank < W) {
-      const double total = double(s_score[j]) + (double(cv[k]) * double(a.k2) - s_lse[j]) * 0.693147180559945309417;
+      const double total = double(s_score[j]) + (double(cv[k] - s_base[j]) * double(a.k2) - s_lse[j]) * 0.693147180559945309417;
       s_tok[j * W + rank] = ci[k];
       s_total[j * W + rank] = total;
       s_key[j * W + rank] = rank_key(total * s_inv[j]);
@@ -665,6 +707,7 @@ spec_status_t spec_beam_select(const spec_beam_select_params* p, void* workspace
   const int per = bf16 ? 8 : 4, nvec = (p->V + per - 1) / per;
   d.seg_vecs = (nvec + w.S - 1) / w.S;
   d.k2 = float(1.4426950408889634 / p->tau);
+  d.coarse = float(2147483648.0 / double(d.k2));
   d.alpha = p->alpha;
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e = launch_pdl(bf16 ? beam_rows_kernel<__nv_bfloat16> : beam_rows_kernel<float>,
