@@ -104,11 +104,8 @@ __global__ void __launch_bounds__(kSimtThreads) span_simt_kernel(Dev a) {
       for (int w = 0; w < 8; ++w) s.anc[tid][w] = 0;
       if (tid < rows && tree) {
         const uint32_t* arow = a.anc + size_t(it.o + (it.mt * kSimtRows + tid) / a.G) * a.W;
-        if (a.window > 0) {
-          lo = window_words(a, arow, it.P, s.anc[tid]);
-        } else {
-          for (int w = 0; w < a.W; ++w) s.anc[tid][w] = arow[w];
-        }
+        for (int w = 0; w < a.W; ++w) s.anc[tid][w] = mask_word(arow, w, it.T);
+        if (a.window > 0) lo = window_words(a, s.anc[tid], a.W, it.P);
       }
       s.row_lo[tid] = lo;
     }

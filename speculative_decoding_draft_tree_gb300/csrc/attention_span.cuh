@@ -450,16 +450,22 @@ __device__ __forceinline__ void flag(const Dev& a, int req, int nreq, int bits) 
   for (int r = req; r < req + nreq; ++r) atomicOr(&a.req_status[r], bits);
 }
 
-// The ancestor words of one query row under the window: of its n ancestors-or-self (depths 0 .. n - 1
+// Word w of a mask row, without the bits behind a tree of T nodes, which count for nothing.
+__device__ __forceinline__ uint32_t mask_word(const uint32_t* row, int w, int T) {
+  const int n = T - 32 * w;
+  return n <= 0 ? 0u : row[w] & (n >= 32 ? ~0u : (1u << n) - 1u);
+}
+
+// The ancestor words of one query row under the window, in place: of its n ancestors-or-self (depths 0 .. n - 1
 // in increasing index, since parents come before children) those at depth k with n - 1 - k < window or
 // P + k < sinks.  Returns the row's lower bound of visible prefix keys.
-__device__ __forceinline__ int window_words(const Dev& a, const uint32_t* row, int P, uint32_t* out) {
+__device__ __forceinline__ int window_words(const Dev& a, uint32_t* row, int W, int P) {
   int n = 0;
-  for (int w = 0; w < a.W; ++w) n += __popc(row[w]);
+  for (int w = 0; w < W; ++w) n += __popc(row[w]);
   const int first = n > a.window ? n - a.window : 0;       // depths below are out of the window
   const int sunk = a.sinks > P ? a.sinks - P : 0;          // depths below are sinks
   int k = 0;
-  for (int w = 0; w < a.W; ++w) {
+  for (int w = 0; w < W; ++w) {
     uint32_t x = row[w], keep = 0;
     const int c = __popc(x);
     if (k >= first || k + c <= sunk) {
@@ -473,7 +479,7 @@ __device__ __forceinline__ int window_words(const Dev& a, const uint32_t* row, i
         ++k;
       }
     }
-    out[w] = keep;
+    row[w] = keep;
   }
   const int depth = n > 0 ? n - 1 : 0;
   const long long lo = (long long)P + depth - a.window + 1;

@@ -228,15 +228,8 @@ span_rows_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__
           int lo = it.lo;
           uint32_t anc = 0;
           if (lane < nrows && it.end > it.P) {
-            const uint32_t* arow = a.anc + size_t(it.o + lane / a.G) * a.W;
-            if (a.window > 0) {
-              uint32_t words[8];
-              lo = window_words(a, arow, it.P, words);
-              anc = words[0];
-            } else {
-              anc = arow[0];
-            }
-            anc &= (1u << it.T) - 1u;       // T <= 16 here
+            anc = mask_word(a.anc + size_t(it.o + lane / a.G) * a.W, 0, it.T);      // T <= 16 here
+            if (a.window > 0) lo = window_words(a, &anc, 1, it.P);
           }
           r.lo[lane] = lo;
           r.anc[lane] = anc;

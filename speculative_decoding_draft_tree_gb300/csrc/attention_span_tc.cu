@@ -518,7 +518,7 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
           view.anc = a.anc + size_t(it.o + t) * a.W;
           if (a.window > 0) {
             int n = 0;
-            for (int w = 0; w < a.W; ++w) n += __popc(__ldg(view.anc + w));
+            for (int w = 0; w < a.W; ++w) n += __popc(mask_word(view.anc, w, it.T));
             view.first = max(0, n - a.window);
             view.deep = max(0, a.sinks - P);
             view.lo = int(min((long long)P, max(0LL, (long long)P + max(n - 1, 0) - a.window + 1)));

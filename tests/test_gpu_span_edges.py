@@ -16,6 +16,25 @@ KERNELS = {"rows": dict(dtype=BF16, T=2, Hq=8, H=2), "tile": dict(dtype=BF16, T=
            "cores": dict(dtype=F32, T=5, Hq=4, H=2)}
 
 
+# ------------------------------------------------------------------------------------ masks
+@pytest.mark.parametrize("kind", ["window", "shared"])
+@pytest.mark.parametrize("sizes,T_max,G,dtype", [([1, 3, 5], 8, 2, BF16), ([5, 33, 70], 100, 4, BF16), ([5, 33, 70], 100, 4, F32), ([31, 32, 64], 256, 1, BF16),
+                                                 ([2, 40, 9], 64, 2, F32)])
+def test_mask_bits_behind_the_tree_do_not_count(kind, sizes, T_max, G, dtype):
+    """Neither for what a node sees nor for its depth."""
+    rng = np.random.default_rng(T_max)
+    room = 32 * ((T_max + 31) // 32)
+    bits = []
+    for t in sizes:
+        for i, b in enumerate(U.chain_bits(t) if t < 40 else U.tree_bits(t, rng)):
+            stray = sum(1 << int(p) for p in rng.choice(np.arange(t, room), min(room - t, 1 + i % 9), replace=False))
+            bits.append(b | stray)
+    kw = dict(window=23, sinks=3) if kind == "window" else dict(groups=[(0, 2, 40), (2, 3, 7)])
+    c = S.Case([300, 45, 7], sizes, Hq=2 * G, H=2, dtype=dtype, T_max=T_max, bits=bits, seed=40, **kw)
+    c.run()
+    S.check(c)
+
+
 # ------------------------------------------------------------------------------------ large scores
 def _scores(c):
     """(row, query head, its scores in 64 bits, their products' magnitudes, the slots' values) of every row that sees
