@@ -663,7 +663,8 @@ spec_status_t spec_tree_attention_window(const spec_attn_window_params* p, void*
  * own.  shared_len is any length from 0 to the members' prefix lengths; a group may have one member.
  * The result is spec_tree_attention's.
  * Data errors: a request that group_offset puts in no group, whose group's shared_len is negative or
- * beyond its prefix, or whose group's node offsets lie outside [0, N] gets SPEC_REQ_BAD_SIZE and no rows.
+ * beyond its prefix, or whose group's node offsets lie outside [0, N] gets SPEC_REQ_BAD_SIZE and no rows; so does
+ * every request of a call whose group_offset goes backwards anywhere (equal entries are a group without requests).
  * Bad ids among the shared pages flag every member with SPEC_REQ_BAD_BLOCK.
  * The workspace grows with N x H_q x head_dim (two fp32 rows of partial results each).
  * Errors: SPEC_ERR_INVALID_ARG also for num_groups outside [1, B] or null group arrays.

@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kSimtThreads) span_simt_kernel(Dev a) {
   find_range(a, s.scratch, s.range, s.first);
   __syncthreads();
   const Range R = s.range;
-  if (threadIdx.x < 32 && reports(R, gridDim.x)) write_recs(a);
+  if (threadIdx.x < 32 && reports(R, gridDim.x)) write_recs(a, R.ordered);
   if (R.t0 >= R.t1) return;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int d4 = a.d >> 2;

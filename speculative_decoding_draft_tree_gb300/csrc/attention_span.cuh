@@ -99,12 +99,14 @@ __device__ __forceinline__ long long entry_cost(const Dev& a, const E& e) {
   return one * (a.H_kv >> 1) + ((a.H_kv & 1) ? block_cost(a, e, n, 1) : 0);
 }
 
-// The inputs that entries come from, possibly a copy.
+// The inputs that entries come from, possibly a copy.  Without `ordered` the groups' offsets go backwards somewhere, so
+// that groups could overlap: none is worked on then, nor any request.
 struct Inputs {
   const int32_t *node, *prefix, *status, *off, *shared;
+  bool ordered;
 };
-__device__ __forceinline__ Inputs inputs_of(const Dev& a) {
-  return Inputs{a.node_offset, a.prefix_len, a.req_status, a.group_offset, a.shared_len};
+__device__ __forceinline__ Inputs inputs_of(const Dev& a, bool ordered) {
+  return Inputs{a.node_offset, a.prefix_len, a.req_status, a.group_offset, a.shared_len, ordered};
 }
 
 // The group of request r: the g with off[g] <= r < off[g + 1], -1 if the offsets name none.
@@ -151,7 +153,7 @@ __device__ __forceinline__ Entry entry_of(const Dev& a, const Inputs& in, int i,
   bad = 0;
   if (i < a.Gn) {
     int o, T, len;
-    if (!group_tokens(a, in, i, o, T, len)) return e;
+    if (!in.ordered || !group_tokens(a, in, i, o, T, len)) return e;
     e.o = o;
     e.T = T;
     e.P = e.end = len;
@@ -184,7 +186,7 @@ __device__ __forceinline__ Entry entry_of(const Dev& a, const Inputs& in, int i,
   } else if (a.Gn > 0) {
     const int g = find_group(in.off, a.Gn, r);
     int go, gT, len;
-    if (g < 0 || in.shared[g] < 0 || in.shared[g] > P) {
+    if (!in.ordered || g < 0 || in.shared[g] < 0 || in.shared[g] > P) {
       bad = SPEC_REQ_BAD_SIZE;
       e.T = 0;
       return e;
@@ -233,6 +235,7 @@ __device__ __forceinline__ int range_of(const Cut& c, long long t) {
 struct Range {
   long long t0, t1, beg0;
   int e0, C;
+  bool ordered;         // of the inputs
 };
 
 // Scratch of the search: the warps' costs and the inputs, where they fit.
@@ -255,24 +258,29 @@ __device__ __forceinline__ long long warp_scan(long long v) {
 // chain that an entry's checks make of them.  The caller synchronises before it reads R.
 __device__ __forceinline__ void find_range(const Dev& a, RangeScratch& s, Range& R, Entry& first) {
   const int E = a.Gn + a.B, nthr = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Inputs in = inputs_of(a);
+  Inputs in = inputs_of(a, true);
+  bool back = false;
   if (a.B <= kStartCache) {              // Gn <= B
 #pragma unroll 1
     for (int i = threadIdx.x; i <= a.B; i += nthr) {
       const bool r = i < a.B, g = i < a.Gn;
       const int32_t node = in.node[i], prefix = r ? in.prefix[i] : 0, status = r ? in.status[i] : 0;
-      const int32_t off = i <= a.Gn && a.Gn > 0 ? in.off[i] : 0, shared = g ? in.shared[i] : 0;
+      const int32_t off = i <= a.Gn && a.Gn > 0 ? in.off[i] : 0, next = g ? in.off[i + 1] : off, shared = g ? in.shared[i] : 0;
       s.node[i] = node;
       if (r) {
         s.prefix[i] = prefix;
         s.status[i] = status;
       }
       s.off[i] = off;
+      back = back || off > next;
       if (g) s.shared[i] = shared;
     }
-    __syncthreads();
-    in = Inputs{s.node, s.prefix, s.status, s.off, s.shared};
+    in = Inputs{s.node, s.prefix, s.status, s.off, s.shared, true};
+  } else {
+#pragma unroll 1
+    for (int i = threadIdx.x; i < a.Gn; i += nthr) back = back || in.off[i] > in.off[i + 1];
   }
+  in.ordered = !__syncthreads_or(back);
   const int run = (E + nthr - 1) / nthr, i0 = min(E, int(threadIdx.x) * run), i1 = min(E, i0 + run);
   Entry e;
   e.T = 0;
@@ -313,6 +321,7 @@ __device__ __forceinline__ void find_range(const Dev& a, RangeScratch& s, Range&
     R.beg0 = none ? 0 : lo;
     R.e0 = at;
     R.C = cut.C;
+    R.ordered = in.ordered;
     first = e;
   }
 }
@@ -322,9 +331,9 @@ __device__ __forceinline__ void find_range(const Dev& a, RangeScratch& s, Range&
 __device__ __forceinline__ bool reports(const Range& R, int ctas) {
   return int(blockIdx.x) == (R.C < ctas ? ctas - 1 : 0);
 }
-__device__ __forceinline__ void write_recs(const Dev& a) {
+__device__ __forceinline__ void write_recs(const Dev& a, bool ordered) {
   const int lane = threadIdx.x & 31;
-  const Inputs in = inputs_of(a);
+  const Inputs in = inputs_of(a, ordered);
   long long sum = 0;
 #pragma unroll 1
   for (int i0 = 0; i0 < a.Gn + a.B; i0 += 32) {
@@ -380,7 +389,7 @@ struct Walker {
         if (++i >= a.Gn + a.B) return false;
         if (!known) {
           int bad;
-          e = entry_of(a, inputs_of(a), i, bad);
+          e = entry_of(a, inputs_of(a, R.ordered), i, bad);
         }
         known = false;
         n = units_of(a, e);

@@ -392,7 +392,7 @@ span_rows_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__
     }
   } else if (warp >= 12) {
     // ===================================================================== output
-    if (warp == 12 && reports(c.range, gridDim.x)) write_recs(a);
+    if (warp == 12 && reports(c.range, gridDim.x)) write_recs(a, c.range.ordered);
     const int q4 = warp & 3, d = q4 * 32 + lane;       // this thread's column of the head
     const uint32_t lane_addr = uint32_t(q4 * 32) << 16;
     bool ok = true;

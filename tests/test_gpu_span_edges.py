@@ -131,3 +131,34 @@ def test_large_scores_of_equal_keys(kernel):
         # weights of 1, whose sum and products are exact in any order up to fp32's 2^-24 for each of 150 terms
         assert (np.abs(o[n, h] - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -11 * mass).all(), (n, h)
         assert abs(lse[n, h] - x.max()) <= 2.0 ** -17 * size.max()
+
+
+# ------------------------------------------------------------------------------------ groups that cannot be
+GROUPS = [(0, 2, 30), (2, 4, 50), (4, 6, 10)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("offsets", [[0, 4, 2, 6], [0, 6, 6, 2], [3, 2, 4, 6], [0, 2, 1, 6], [6, 4, 2, 0]])
+def test_group_offsets_that_go_backwards(dtype, offsets):
+    """Groups would overlap: no request can be told which is its own, and no row is written."""
+    c = S.Case([60, 61, 90, 95, 40, 41], [1, 2, 1, 1, 2, 1], Hq=4, H=2, groups=GROUPS, dtype=dtype, seed=45)
+    c.group_off.copy_(torch.tensor(offsets))
+    c.run()
+    assert c.status.tolist() == [2] * 6
+    assert (c.o == 77).all() and (c.lse == 55).all()
+
+
+def test_group_offsets_that_go_backwards_among_many():
+    n = 1300
+    c = S.Case([9] * n, [1] * n, Hq=2, H=1, groups=[(i, i + 2, 5) for i in range(0, n, 2)], seed=46)
+    c.group_off[600] = 1205
+    c.run()
+    assert c.status.tolist() == [2] * n and (c.o == 77).all()
+
+
+def test_groups_without_requests():
+    c = S.Case([60, 61, 90, 95], [1, 2, 1, 1], Hq=4, H=2, groups=[(0, 2, 30), (2, 4, 50)], seed=47)
+    c.group_off, c.shared = U.ints([0, 0, 2, 4, 4]), U.ints([1000, 30, 50, -3])
+    c.run()
+    S.check(c)
+    assert c.status.tolist() == [0] * 4
