@@ -119,6 +119,11 @@ __device__ __forceinline__ int find_group(const int32_t* off, int Gn, int r) {
   return off[lo] <= r && r < off[lo + 1] ? lo : -1;
 }
 
+// Whether slots 0 .. end - 1 lie in a table row, and their tiles' bounds in 32 bits.
+__device__ __forceinline__ bool fits(const Dev& a, long long end) {
+  return (end + a.bs - 1) / a.bs <= a.max_blocks && end <= 0x7fffffffLL - 1024;
+}
+
 // Group g's tokens, if it is one that is computed together: two members at least, a shared part, and
 // node offsets that lie in [0, N] (a member's own error leaves the others' results as they are).
 __device__ __forceinline__ bool group_tokens(const Dev& a, const Inputs& in, int g, int& o, int& T, int& len) {
@@ -128,7 +133,7 @@ __device__ __forceinline__ bool group_tokens(const Dev& a, const Inputs& in, int
   o = in.node[r0];
   const int e = in.node[r1];
   T = e - o;
-  return o >= 0 && e <= a.N && T >= 1 && (long long)(len + a.bs - 1) / a.bs <= a.max_blocks;
+  return o >= 0 && e <= a.N && T >= 1 && fits(a, len);
 }
 
 __device__ __forceinline__ void key_tiles(const Dev& a, Entry& e) {
@@ -171,7 +176,7 @@ __device__ __forceinline__ Entry entry_of(const Dev& a, const Inputs& in, int i,
     return e;
   }
   const long long end = (long long)P + T;
-  if ((end + a.bs - 1) / a.bs > a.max_blocks || end > 0x7fffffffLL - 1024) {
+  if (!fits(a, end)) {
     bad = SPEC_REQ_BAD_BLOCK;
     return e;
   }

@@ -162,3 +162,14 @@ def test_groups_without_requests():
     c.run()
     S.check(c)
     assert c.status.tolist() == [0] * 4
+
+
+@pytest.mark.parametrize("length", [(1 << 31) - 1, (1 << 31) - 8, (1 << 31) - 1024, 1 << 30])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_a_shared_length_at_the_end_of_32_bits(dtype, length):
+    c = S.Case([60, 61, 90, 95], [1, 2, 1, 1], Hq=4, H=2, groups=[(0, 2, 30), (2, 4, 50)], dtype=dtype, seed=48)
+    c.shared[1] = length
+    c.run()
+    assert c.status.tolist() == [0, 0, 2, 2]
+    S.check(c, rows=[0, 1, 2])
+    assert (c.o[3:] == 77).all()
