@@ -437,7 +437,6 @@ class BeamSearch:
         self.prefix = prompt_len.repeat_interleave(W)          # the same for each beam, [B * W]
         self.node_offset = torch.arange(n + 1, **i32)
         self.group_offset = torch.arange(0, n + 1, W, **i32)
-        self.root = torch.full((n,), -1, **i32)
         self.anc_mask = torch.ones((n, 1), **i32)
         self.status = torch.zeros(n, **i32)
         self.beam_status = torch.zeros(self.B, **i32)
@@ -448,10 +447,21 @@ class BeamSearch:
                                               self.parent, self.beam_status, k_scale, v_scale)
         self._reorder_ws = _ws(B.spec_beam_reorder_workspace_size(self._reorder), dev)
         self._attn_ws, self._select_ws = [], []
+        self._first_table = block_table.clone()
         self.begin()
 
-    def begin(self):
-        """Start from the prompts: beam 0 of each request is live, the others wait (score -infinity)."""
+    def begin(self, block_table=None):
+        """Start from the prompts: beam 0 of each request is live, the others wait (score -infinity), and
+        nothing is left of an earlier search, whose statuses are cleared and whose moves among the
+        entries of block_table are undone: it is what it was when the object was made.  For other
+        prompts write prompt_len and pass their table; it is copied into the object's, now and at
+        every later begin(), and the prompts enter the cache by it, after this call."""
+        if block_table is not None:
+            B._need_shape(block_table, self.block_table.shape, "block_table")
+            self._first_table.copy_(block_table)
+        self.block_table.copy_(self._first_table)
+        self.status.zero_()
+        self.beam_status.zero_()
         self.kv_len.copy_(self.prompt_len)
         self.prefix.copy_(self.prompt_len.repeat_interleave(self.W))
         self.scores.fill_(float("-inf"))

@@ -1,9 +1,12 @@
-"""Beam selection at small temperatures and large logits, and its length penalty's precision."""
+"""Beam selection at small temperatures and large logits, its length penalty's precision, and searches one after
+another on one BeamSearch."""
 import numpy as np
 import pytest
 import torch
 
-from test_gpu_beam import Select
+import kv8_util as U
+from test_gpu_beam import Select, Toy, _rotate
+from speculative_decoding_draft_tree_gb300.api import BeamSearch
 
 pytestmark = pytest.mark.gpu
 F32, BF16 = torch.float32, torch.bfloat16
@@ -104,3 +107,105 @@ def test_the_length_penalty_tells_ranks_a_few_parts_in_1e9_apart():
             order.append([0, 1] if r[0] > r[1] else [1, 0])
     c = Select(np.zeros((400, 2, 8)), np.array(scores), lengths, np.ones((400, 2)), 8, alpha=alpha, eos=3)
     assert c.run()[0].tolist() == order
+
+
+# ------------------------------------------------------------------------------------ several searches
+class _Searches:
+    """A BeamSearch over one toy model's fp32 cache, and what a search gives: beams' tokens and scores."""
+
+    def __init__(self, prompts, W, room, bs=4):
+        self.toy, self.W, self.bs = Toy(61, 4, 2, 32, 1), W, bs
+        n = len(prompts)
+        wide = max(len(p) - 1 for p in prompts) // bs + room
+        nb = n * W * wide
+        self.table = torch.from_numpy(np.random.default_rng(5).permutation(nb).reshape(n * W, wide).astype(np.int32)).cuda()
+        self.k, self.v = [torch.zeros((1, nb, 2, bs, 32), device="cuda") for _ in range(2)]
+        self.prompt_len = U.ints([len(p) - 1 for p in prompts])
+        self.s = BeamSearch(self.k, self.v, self.table, self.prompt_len, W, 4, 61, eos=3, alpha=0.6)
+        t = self.toy
+        self.emb, self.wq, self.wk, self.wv, self.wo = [torch.from_numpy(m).float().cuda() for m in (t.emb, t.wq, t.wk, t.wv, t.wo)]
+        self.put(prompts)
+
+    def put(self, prompts):
+        """The prompts enter the pages of each request's beam 0."""
+        self.prompts = prompts
+        table, t = self.table.cpu().numpy(), self.toy
+        for b, p in enumerate(prompts):
+            for i, x in enumerate(p[:-1]):
+                page = int(table[b * self.W, i // self.bs])
+                self.k[0, page, :, i % self.bs] = torch.from_numpy(_rotate((t.emb[x] @ t.wk).reshape(2, 32), i)).float()
+                self.v[0, page, :, i % self.bs] = torch.from_numpy((t.emb[x] @ t.wv).reshape(2, 32)).float()
+
+    def search(self, steps):
+        s, W, n = self.s, self.W, len(self.prompts)
+        s.spread()
+        s.tokens.copy_(torch.tensor([[p[-1]] * W for p in self.prompts]))
+        q, o = [torch.empty((n * W, 4, 32), device="cuda") for _ in range(2)]
+        logits = torch.zeros((n * W, 64), device="cuda")
+        seqs = [[[] for _ in range(W)] for _ in range(n)]
+        for _ in range(steps):
+            e = self.emb[s.tokens.view(-1).long()]
+            s.write(0, (e @ self.wq).view(-1, 4, 32), q, (e @ self.wk).view(-1, 2, 32), (e @ self.wv).view(-1, 2, 32))
+            s.attention(0, q, o)
+            logits[:, :61] = o.view(n * W, -1) @ self.wo
+            s.advance(logits)
+            par, tok = s.parent.tolist(), s.tokens.tolist()
+            seqs = [[seqs[b][par[b][j]] + [tok[b][j]] for j in range(W)] for b in range(n)]
+        torch.cuda.synchronize()
+        return seqs, s.scores.clone(), s.lengths.clone()
+
+    def clean(self):
+        return (self.s.status == 0).all().item() and (self.s.beam_status == 0).all().item()
+
+
+PROMPTS = [[5, 9, 1, 30, 44, 2, 17], [8, 8, 60], [3] * 13]
+
+
+def _same(a, b):
+    return a[0] == b[0] and torch.equal(a[1], b[1]) and torch.equal(a[2], b[2])
+
+
+def test_a_second_search_is_the_first_again():
+    """The first one fills pages, so that beams name one in common; the second starts from the prompts."""
+    c = _Searches(PROMPTS, 4, 5)
+    first = c.search(11)
+    assert c.clean()
+    c.s.begin()
+    again = c.search(11)
+    assert c.clean() and _same(first, again)
+
+
+def test_a_search_after_one_that_ran_out_of_its_table():
+    c = _Searches(PROMPTS, 4, 3)
+    first = c.search(6)
+    c.s.begin()
+    c.search(18)                    # past the longest prompt's table row
+    assert not c.clean()
+    c.s.begin()
+    again = c.search(6)
+    assert c.clean() and _same(first, again)
+
+
+def test_other_prompts_by_another_table():
+    other = [[7, 50, 2, 2, 9], [1, 2, 3, 4, 5, 6, 7, 8, 9, 10], [33, 12]]
+    fresh = _Searches(other, 4, 6)
+    want = fresh.search(9)
+    c = _Searches(PROMPTS, 4, 5)
+    c.search(11)
+    table = torch.from_numpy(np.random.default_rng(9).permutation(c.k.shape[1]).reshape(c.table.shape).astype(np.int32)).cuda()
+    c.prompt_len.copy_(U.ints([len(p) - 1 for p in other]))
+    for _ in range(2):              # and again, from the table that was given last
+        c.s.begin(table)
+        table = None
+        c.put(other)
+        got = c.search(9)
+        assert c.clean() and got[0] == want[0]
+        torch.testing.assert_close(got[1], want[1], atol=1e-4, rtol=0)
+
+
+def test_begin_refuses_another_tables_shape():
+    c = _Searches(PROMPTS, 4, 5)
+    with pytest.raises(ValueError, match="block_table"):
+        c.s.begin(c.table[:, :-1].contiguous())
+    with pytest.raises(ValueError):
+        c.s.begin(c.table.long())
