@@ -401,8 +401,9 @@ __global__ void __launch_bounds__(256, kCols > 1 ? 2 : 4) span_merge_kernel(Dev 
           src = row_at(at);
         }
       }
-      const float wt = L0 == -INFINITY ? 0.f : exp2f(L0 - M);     // nothing visible in this piece (M may be -inf as well)
-      sum += wt;
+      // -1: nothing visible in this piece (M may be -inf as well), and what it holds does not count, not even a NaN
+      const float wt = L0 == -INFINITY ? -1.f : exp2f(L0 - M);
+      sum += wt < 0.f ? 0.f : wt;
       const int np = min(kP, most - p0);
 #pragma unroll 1
       for (int q0 = 0; q0 < np; q0 += kBatch) {
@@ -411,7 +412,7 @@ __global__ void __launch_bounds__(256, kCols > 1 ? 2 : 4) span_merge_kernel(Dev 
         for (int u = 0; u < kLoads; ++u) {
           const int q = q0 + u / kR;
           const float w = __shfl_sync(0xffffffffu, wt, min(q, kP - 1) * kR + u % kR);
-          if (w == 0.f || q >= np) continue;      // what such a piece holds may be a NaN, or nothing yet
+          if (w < 0.f || q >= np) continue;
 #pragma unroll
           for (int c = 0; c < kCols; ++c) {
             float4& x = acc[u % kR][c];

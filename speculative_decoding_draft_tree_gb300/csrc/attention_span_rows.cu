@@ -418,11 +418,12 @@ span_rows_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__
         const float s0 = has0 ? (c.sum[par][0][0][n0] + c.sum[par][0][1][n0]) + (c.sum[par][0][2][n0] + c.sum[par][0][3][n0]) : 0.f;
         const float s1 = has1 ? (c.sum[par][1][0][n0] + c.sum[par][1][1][n0]) + (c.sum[par][1][2][n0] + c.sum[par][1][3][n0]) : 0.f;
         const float M = fmaxf(r0, r1);
+        const bool any0 = r0 != -INFINITY || s0 != 0.f, any1 = r1 != -INFINITY || s1 != 0.f;      // something seen
         const float w0 = r0 == -INFINITY ? s0 : ex2(r0 - M), w1 = r1 == -INFINITY ? s1 : ex2(r1 - M);
-        const float l = (w0 != 0.f ? w0 * s0 : 0.f) + (w1 != 0.f ? w1 * s1 : 0.f);
+        const float l = (any0 ? w0 * s0 : 0.f) + (any1 ? w1 * s1 : 0.f);
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        f0 = w0 * inv;
-        f1 = w1 * inv;
+        f0 = any0 ? w0 * inv : -1.f;       // -1: what the group has does not count (a weight of 0 lets a NaN through)
+        f1 = any1 ? w1 * inv : -1.f;
         lse2 = l == 0.f ? -INFINITY : M + __log2f(l);
       }
       const int t = n0 / a.G;
@@ -451,8 +452,8 @@ span_rows_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__
         for (int i = 0; i < 8; ++i) {
           const float a0 = __shfl_sync(0xffffffffu, f0, n8 + i), a1 = __shfl_sync(0xffffffffu, f1, n8 + i);
           const unsigned long long dst = __shfl_sync(0xffffffffu, mine, n8 + i);
-          float v = a0 == 0.f ? 0.f : a0 * (__uint_as_float(x[0][i]) + __uint_as_float(x[1][i]));
-          if (a1 != 0.f) v = fmaf(a1, __uint_as_float(x[2][i]) + __uint_as_float(x[3][i]), v);
+          float v = a0 < 0.f ? 0.f : a0 * (__uint_as_float(x[0][i]) + __uint_as_float(x[1][i]));
+          if (!(a1 < 0.f)) v = fmaf(a1, __uint_as_float(x[2][i]) + __uint_as_float(x[3][i]), v);
           if (n8 + i < nrows) {
             if (direct) *(reinterpret_cast<__nv_bfloat16*>(dst) + d) = __float2bfloat16_rn(v);
             else *(reinterpret_cast<float*>(dst) + d) = v;

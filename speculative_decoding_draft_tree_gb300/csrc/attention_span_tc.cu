@@ -716,6 +716,7 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
         if (!ok) break;
         tc::tc_fence_after();
         float lt = l, M = ref, w0 = 0.f, w1 = 0.f;
+        bool any0 = true, any1 = false;        // the row has seen something in slot 0's and 1's tiles of a lone unit
         int c_lo = 0, c_hi = kD;
         if (!both) {
           // exchange (reference, sum) with the other slot's warp of this quarter; 64 columns each
@@ -726,12 +727,14 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
           if (!warp_wait(&c.exchange[q4], xn & 1, abort_flag)) { ok = false; break; }
           ++xn;
           const float mo = c.row[1 - s][0][m], lo = c.row[1 - s][1][m];
-          const float m0 = s == 0 ? ref : mo, m1 = s == 0 ? mo : ref;
+          const float m0 = s == 0 ? ref : mo, m1 = s == 0 ? mo : ref, l0 = s == 0 ? l : lo, l1 = s == 0 ? lo : l;
+          // a slot that saw nothing but NaN has the reference -inf and the sum NaN
+          any0 = m0 != -INFINITY || l0 != 0.f;
+          any1 = n1 > 0 && (m1 != -INFINITY || l1 != 0.f);
           M = fmaxf(m0, m1);
           w0 = m0 != -INFINITY ? ex2(m0 - M) : 0.f;
           w1 = n1 > 0 && m1 != -INFINITY ? ex2(m1 - M) : 0.f;
-          // a slot that saw nothing but NaN has the reference -inf and the sum NaN
-          lt = (s == 0 ? l : lo) * w0 + (n1 > 0 ? (s == 0 ? lo : l) * w1 : 0.f);
+          lt = l0 * w0 + (n1 > 0 ? l1 * w1 : 0.f);
           c_lo = 64 * s;
           c_hi = c_lo + 64;
         }
@@ -751,7 +754,8 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
           unsigned long long at[8];        // where rows 4 i + lane / 8 begin
 #pragma unroll
           for (int i = 0; i < 8; ++i) at[i] = __shfl_sync(0xffffffffu, mine, 4 * i + (lane >> 3));
-          const float wa = both ? inv : w0 * inv, wb = both || n1 == 0 ? 0.f : w1 * inv;
+          const float wa = both ? inv : w0 * inv, wb = w1 * inv;
+          any0 = any0 && lt != 0.f;            // (a weight of 0 lets a NaN through)
           const int u8 = lane & 7;
 #pragma unroll 1
           for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
@@ -760,12 +764,12 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
             tc::tmem_ld32(tO + (both ? 128 * s : 0) + c0, r);
             tc::tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = wa == 0.f ? 0.f : __uint_as_float(r[i]) * wa;
+            for (int i = 0; i < 32; ++i) v[i] = any0 ? __uint_as_float(r[i]) * wa : 0.f;
             if (!both && n1 > 0) {
               tc::tmem_ld32(tO + 128 + c0, r);
               tc::tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = wb == 0.f ? v[i] : fmaf(__uint_as_float(r[i]), wb, v[i]);
+              for (int i = 0; i < 32; ++i) v[i] = any1 ? fmaf(__uint_as_float(r[i]), wb, v[i]) : v[i];
             }
             if (direct) {
               const int h4 = (c0 >> 3) & 4;        // 64 columns make a row's 128 bytes

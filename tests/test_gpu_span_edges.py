@@ -133,6 +133,40 @@ def test_large_scores_of_equal_keys(kernel):
         assert abs(lse[n, h] - x.max()) <= 2.0 ** -17 * size.max()
 
 
+# ------------------------------------------------------------------------------------ not finite, and far away
+@pytest.mark.parametrize("kernel", list(KERNELS))
+@pytest.mark.parametrize("kind", ["window", "shared"])
+@pytest.mark.parametrize("far,length", [(128, 250), (128, 380), (128, 640), (4600, 9000), (6000, 6200)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_value_that_is_not_finite_shows_under_any_weight(kernel, kind, far, length, value):
+    """Slots below `far` have scores some 600 below the others', so that the weights of their tiles, of the slot or
+    the group of tiles that they are in, or of whole pieces are 0 in fp32; one of them has a bad V."""
+    k = KERNELS[kernel]
+    T = k["T"]
+    kw = dict(window=20000) if kind == "window" else dict(groups=[(0, 2, far)])
+    prefix = [length, length + 9]
+    c = S.Case(prefix, [T] * 2, Hq=k["Hq"], H=k["H"], dtype=k["dtype"], seed=44, **kw)
+    u = torch.randn((128,), generator=torch.Generator(device="cuda").manual_seed(2), device="cuda")
+    c.q.copy_(c.q.float() * 0.3 + u)
+    slot = far // 2 + 3
+    for r in range(2):
+        ids = torch.from_numpy(c.table_np[r]).long().cuda()
+        low = torch.arange(ids.numel() * c.bs, device="cuda").view(-1, c.bs) < far
+        for p in range(ids.numel()):
+            if ids[p] >= 0:
+                c.k[ids[p]] = torch.where(low[p][None, :, None], (-60 * u).to(c.k.dtype), c.k[ids[p]])
+    c.run()
+    S.check(c)
+    hit = c.table_np[0, slot // c.bs]
+    c.v[int(hit), 1, slot % c.bs, 5] = value
+    before = c.o.clone()
+    c.run()
+    rows = c.N if kind == "shared" else T       # who sees the slot
+    G = c.q.shape[1] // 2
+    assert (~torch.isfinite(c.o[:rows, G:, 5])).all()
+    assert torch.equal(c.o[:, :G], before[:, :G]) and torch.equal(c.o[rows:], before[rows:])
+
+
 # ------------------------------------------------------------------------------------ groups that cannot be
 GROUPS = [(0, 2, 30), (2, 4, 50), (4, 6, 10)]
 
