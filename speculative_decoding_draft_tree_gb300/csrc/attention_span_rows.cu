@@ -1,5 +1,5 @@
-// spec_tree_attention_shared and spec_tree_attention_window for units of at most 16 query rows (single tokens,
-// short chains, small groups) on the tcgen05 tensor cores: bf16, head_dim 128.
+// spec_tree_attention_window for at most 16 query rows a request and head (single tokens, short chains) on the
+// tcgen05 tensor cores: bf16, head_dim 128.
 //
 // Such a unit is bound by its keys' and values' bytes: 64 KB a tile of 128 keys take ~2800 clocks of an SM's
 // share of HBM.  With the rows on the TMEM lanes, as attention_span_tc.cu has them, 16 threads would form 128
@@ -192,12 +192,8 @@ span_rows_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__
   volatile int* abort_flag = &c.abort;
   const bool layout_ok = *abort_flag == 0;
   int ni = 0;                        // items taken so far
-  auto take = [&](bool one_lane) -> bool {
-    uint64_t* bar = &c.item_full[ni % kItems];
-    const uint32_t parity = (ni / kItems) & 1;
-    return one_lane ? tc::mbar_wait(bar, parity, abort_flag, kWaitLimit) : warp_wait(bar, parity, abort_flag);
-  };
-  auto give_back = [&](bool) {
+  auto take = [&]() -> bool { return warp_wait(&c.item_full[ni % kItems], (ni / kItems) & 1, abort_flag); };
+  auto give_back = [&] {
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(&c.item_empty[ni % kItems]);
     ++ni;
@@ -227,16 +223,16 @@ span_rows_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__
         if (lane < kN) {
           int lo = it.lo;
           uint32_t anc = 0;
-          if (lane < nrows && it.end > it.P) {
+          if (lane < nrows) {
             anc = mask_word(a.anc + size_t(it.o + lane / a.G) * a.W, 0, it.T);      // T <= 16 here
-            if (a.window > 0) lo = window_words(a, &anc, 1, it.P);
+            lo = window_words(a, &anc, 1, it.P);
           }
           r.lo[lane] = lo;
           r.anc[lane] = anc;
         }
         if (lane == 0) {
           r.nrows = nrows;
-          r.lo_max = a.window > 0 ? int(max(0LL, (long long)it.P + it.T - a.window)) : it.lo;
+          r.lo_max = int(max(0LL, (long long)it.P + it.T - a.window));
         }
       }
       __syncwarp();
@@ -256,10 +252,10 @@ span_rows_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__
     int kt = 0, qn = 0;
     bool ok = true;
     while (ok) {
-      ok = take(false);
+      ok = take();
       if (!ok || c.item[ni % kItems].it.j1 < 0) break;
       const Item it = c.item[ni % kItems].it;
-      give_back(false);
+      give_back();
       const int32_t* table = a.block_table + size_t(it.table) * a.max_blocks;
       // the physical page of this lane's page of tile j: -1 if no row sees it (read as zeros), -2 if bad
       auto tile_page = [&](int j) -> int {
@@ -268,7 +264,7 @@ span_rows_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__
         if (!page_needed(first, a.bs, it.lo, it.sink, it.end)) return -1;
         const int pb = table[first / a.bs];
         if (pb >= 0 && pb < a.num_blocks) return pb;
-        flag(a, it.req, it.nreq, SPEC_REQ_BAD_BLOCK);
+        flag(a, it.req, 1, SPEC_REQ_BAD_BLOCK);
         return -2;
       };
       int pb = tile_page(it.j0);
@@ -398,7 +394,7 @@ span_rows_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__
     bool ok = true;
     int kt0 = 0;                                       // tiles before the item
     for (int li = 0; ok; ++li) {
-      ok = take(false);
+      ok = take();
       if (!ok || c.item[ni % kItems].it.j1 < 0) break;
       const RowsItem& r = c.item[ni % kItems];
       const Item& it = r.it;
@@ -428,15 +424,13 @@ span_rows_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__
       }
       const int t = n0 / a.G;
       const size_t row = size_t(it.o + t) * a.H_q + it.h * a.G + (n0 - t * a.G);
-      const bool direct = it.slot == -1;
-      const size_t at = it.slot >= 0 ? size_t(it.slot) * a.part_rows + n0 : row;
-      const size_t both = it.slot == -3 ? size_t(a.N) * a.H_q : 0;
+      const bool direct = it.slot == -1;       // else a piece: a request on its own has no other places
+      const size_t at = direct ? row : size_t(it.slot) * a.part_rows + n0;
       if (q4 == 0 && lane < nrows && lane < kN) {
-        if (it.slot >= 0) a.part_lse[at] = lse2;
-        else if (!direct) a.row_lse[both + at] = lse2;
+        if (!direct) a.part_lse[at] = lse2;
         else if (a.lse) a.lse[at] = lse2 * 0.6931471805599453f;
       }
-      char* base = direct ? static_cast<char*>(a.o) : reinterpret_cast<char*>(it.slot >= 0 ? a.part_o : a.row_o + both * kD);
+      char* base = direct ? static_cast<char*>(a.o) : reinterpret_cast<char*>(a.part_o);
       const unsigned long long mine = reinterpret_cast<unsigned long long>(base) + at * kD * (direct ? 2 : 4);
       const uint32_t to = tmem + lane_addr + kTmemO + 64 * par;
 #pragma unroll 1
@@ -463,7 +457,7 @@ span_rows_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&c.o_free[par]);
-      give_back(false);
+      give_back();
     }
     if (!ok) *abort_flag = 1;
   } else {
@@ -476,7 +470,7 @@ span_rows_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__
     int sn = 0, kt0 = 0;       // tiles of this group; tiles before the item
     bool ok = true;
     for (int li = 0;; ++li) {
-      ok = take(false);
+      ok = take();
       if (group_any(bar, !ok)) { ok = false; break; }
       const RowsItem& r = c.item[ni % kItems];
       if (r.it.j1 < 0) break;
@@ -667,7 +661,7 @@ span_rows_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__
       if (lane == 0) tc::mbar_arrive(&c.sum_full[par]);
       ok = fine;
       kt0 += nt;
-      give_back(false);
+      give_back();
       if (group_any(bar, !ok)) { ok = false; break; }
     }
     if (!ok) *abort_flag = 1;
@@ -680,7 +674,7 @@ span_rows_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__
     Walker w;
     w.start(R, nullptr);
     Item it;
-    while (w.next(a, R, it)) flag(a, it.req, it.nreq, SPEC_REQ_TIMEOUT);
+    while (w.next(a, R, it)) flag(a, it.req, 1, SPEC_REQ_TIMEOUT);
   }
   tc::tc_fence_after();
   if (warp == 0) tc::tmem_dealloc(tmem, kTmemCols);
