@@ -631,7 +631,7 @@ spec_status_t spec_kv_fork(const spec_fork_params* p, spec_stream_t stream);
  * workspace: the call's workspace_size bytes, 256-byte aligned, contents arbitrary; calls that may
  * overlap on the GPU (other streams, captured graphs) need one each.
  * Errors: SPEC_ERR_INVALID_ARG, SPEC_ERR_UNSUPPORTED (head_dim above 256, 2^31 rows of pages or of
- * queries), SPEC_ERR_CUDA.
+ * queries, more than 65535 x 32 query rows a request and KV head), SPEC_ERR_CUDA.
  * ========================================================================================== */
 
 /* ------------------------------------------------------------------------------------------

@@ -496,6 +496,8 @@ static spec_status_t check(const Args& x) {
   if (p->head_dim > 256) return SPEC_ERR_UNSUPPORTED;
   if ((long long)p->num_blocks * p->H_kv * p->block_size + 256 >= (1LL << 31)) return SPEC_ERR_UNSUPPORTED;
   if ((long long)p->N * p->H_q >= (1LL << 31) || p->H_kv > 65535) return SPEC_ERR_UNSUPPORTED;
+  // the merge's grid
+  if ((long long)p->T_max * (p->H_q / p->H_kv) > 65535LL * kMergeRows) return SPEC_ERR_UNSUPPORTED;
   return SPEC_OK;
 }
 
