@@ -483,9 +483,10 @@ span_tc_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ C
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    // (the merge reads the records whatever becomes of the CTAs)
+    if (warp == 4 && reports(c.range, gridDim.x)) write_recs(a, c.range.ordered);
     if (layout_ok) {
       // ===================================================================== softmax, epilogue
-      if (warp == 4 && reports(c.range, gridDim.x)) write_recs(a, c.range.ordered);
       const int s = (warp - 4) >> 2, q4 = warp & 3;
       const int m = q4 * 32 + lane;                   // row of the slot's tile; also a key of V's check
       const uint32_t lane_addr = uint32_t(q4 * 32) << 16;
