@@ -173,7 +173,10 @@ class VerifyStep:
         """Run every round's attention with the prefixes that groups of requests have in common
         read once a group (spec_tree_attention_shared): group g is the requests group_offset[g] ..
         group_offset[g + 1] - 1, and its first shared_len[g] slots are the same (as spec_kv_fork
-        leaves them).  The results are the plain round's.  twin() shares the two tensors."""
+        leaves them).  The results are the plain round's.  Both are inputs of a round like the block
+        table: upload() brings them and twin() gives the second step its own.  Their number is fixed;
+        a round of fewer groups repeats an offset (a group without requests).  Call this before
+        twin() or RoundPipeline."""
         self._enable_span("shared", (group_offset, shared_len), B.attention_shared_params,
                           B.spec_attention_shared_workspace_size)
 
@@ -268,13 +271,16 @@ class VerifyStep:
         """Device tensors that a new round brings from the host: the draft tree, its logits,
         uniforms, Q and the tree tokens' K/V rows (slots P..P+T-1 are written by the caller;
         here the whole layer-0 tree region is represented by the block-table-addressed cache
-        rows, which stay resident) -- see run_from_host.  With enable_kv8, k_new and v_new too."""
+        rows, which stay resident) -- see run_from_host.  With enable_kv8, k_new and v_new too; with
+        enable_shared, the groups."""
         w = self.w
         inputs = dict(parent=w.parent, node_offset=w.node_offset, prefix_len=w.prefix_len,
                       tokens=w.tokens, draft_row=w.draft_row, uniforms=w.uniforms, target=w.target,
                       draft=w.draft, q=w.q, block_table=w.block_table)
         if self.kv8 is not None:
             inputs.update(k_new=self.kv8[4], v_new=self.kv8[5])
+        if self.span is not None and self.span[0] == "shared":
+            inputs.update(group_offset=self.span[1][0], shared_len=self.span[1][1])
         return inputs
 
     def pinned_host_inputs(self) -> Dict[str, torch.Tensor]:
@@ -322,13 +328,16 @@ class VerifyStep:
         for k, v in fresh.items():
             v.copy_(src[k])
         rows = [fresh.pop(k) for k in ("k_new", "v_new") if k in fresh]
+        groups = [fresh.pop(k) for k in ("group_offset", "shared_len") if k in fresh]
         step = VerifyStep(dataclasses.replace(self.w, **fresh), self.sibling_rule,
                           self.lse is not None, self.verify_path)
         step._in_pack = pack
         if self.kv8 is not None:
             step.enable_kv8(*self.kv8[:4], *rows)
-        if self.span is not None:
-            (step.enable_window if self.span[0] == "window" else step.enable_shared)(*self.span[1])
+        if self.span is not None and self.span[0] == "window":
+            step.enable_window(*self.span[1])
+        elif self.span is not None:
+            step.enable_shared(*groups)
         return step
 
     def host_output_buffers(self) -> Dict[str, torch.Tensor]:
