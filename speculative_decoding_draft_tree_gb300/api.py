@@ -155,7 +155,8 @@ class VerifyStep:
             raise ValueError("enable_window and enable_shared read the 16- or 32-bit cache, not the "
                              "8-bit one of enable_kv8")
         if self.span is not None:
-            raise ValueError("enable_window and enable_shared do not combine")
+            raise ValueError("enable_window and enable_shared do not combine, and a step takes one of "
+                             "them once")
         self.span_p = params(w.q, self.k_layer0, self.v_layer0, w.block_table, w.prefix_len,
                              w.node_offset, self.anc_mask, w.T_max, *args, self.o, self.lse,
                              self.req_status)

@@ -64,3 +64,16 @@ def test_a_pipelines_rounds_bring_their_groups():
         if name != "bad":
             out = pipe.host_outputs(i)
             assert torch.equal(out["out_tokens"], want[0].cpu()) and torch.equal(out["out_len"], want[1].cpu())
+
+
+def test_a_step_takes_one_form_once():
+    w, P, _, _ = _workload()
+    for first in ("window", "shared"):
+        step = VerifyStep(w)
+        if first == "window":
+            step.enable_window(100, 2)
+        else:
+            step.enable_shared(U.ints([0, w.B]), U.ints([P]))
+        for call in (lambda: step.enable_window(100, 2), lambda: step.enable_shared(U.ints([0, w.B]), U.ints([P]))):
+            with pytest.raises(ValueError, match="once"):
+                call()
