@@ -19,7 +19,7 @@ def offers(row, score, length, finished, tau, alpha, eos):
     if np.isnan(x).any() or np.isposinf(x).any() or not np.isfinite(x).any():
         return []
     m = x.max()
-    logp = x - (m + np.log(np.exp(x - m).sum()))
+    logp = (x - m) - np.log(np.exp(x - m).sum())       # (in this order a row of lowest values keeps its logarithm)
     pen = ((5 + length + 1) / 6) ** alpha
     return [((score + p) / pen, t, score + p, length + 1, int(t == eos)) for t, p in enumerate(logp) if p > -np.inf]
 
