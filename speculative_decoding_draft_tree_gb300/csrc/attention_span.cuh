@@ -362,6 +362,11 @@ __device__ __forceinline__ void write_recs(const Dev& a, bool ordered) {
   if (lane == 0) *a.total = sum;
 }
 
+// For CTAs that give up at their start: records that leave the merge nothing to do.
+__device__ __forceinline__ void clear_recs(const Dev& a) {
+  for (int i = threadIdx.x & 31; i < a.Gn + a.B; i += 32) a.recs[i].mts = 0;
+}
+
 // Key tiles [j0, j1) of one unit.
 enum { kLone, kPair, kDual };
 struct Item {

@@ -198,10 +198,9 @@ span_rows_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__
     if (lane == 0) tc::mbar_arrive(&c.item_empty[ni % kItems]);
     ++ni;
   };
-  // (the merge reads the records whatever becomes of the CTAs)
-  if (warp == 12 && reports(c.range, gridDim.x)) write_recs(a, c.range.ordered);
   if (!layout_ok) {
     // fall through to the end: the range is reported
+    if (warp == 12 && reports(c.range, gridDim.x)) clear_recs(a);
   } else if (warp == 3) {
     // ===================================================================== items
     const Range R = c.range;
@@ -390,6 +389,7 @@ span_rows_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__
     }
   } else if (warp >= 12) {
     // ===================================================================== output
+    if (warp == 12 && reports(c.range, gridDim.x)) write_recs(a, c.range.ordered);
     const int q4 = warp & 3, d = q4 * 32 + lane;       // this thread's column of the head
     const uint32_t lane_addr = uint32_t(q4 * 32) << 16;
     bool ok = true;
