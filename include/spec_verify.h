@@ -621,13 +621,17 @@ spec_status_t spec_kv_fork(const spec_fork_params* p, spec_stream_t stream);
  *     the tcgen05 tensor cores, everything else on a CUDA-core kernel;
  *   - a row that sees no key gets O = 0 and LSE = -infinity;
  *   - a NaN or an infinity in q, K or V reaches the rows that see it and no others (of V: the output's
- *     column at least, or the whole row and its LSE).  Slots that no row of a request sees are not looked at;
+ *     column at least, or the whole row and its LSE, under weights that underflow as well; a score of
+ *     -infinity weighs nothing, and a row that sees no other score is NaN or as one that sees no key).
+ *     Slots that no row of a request sees are not looked at;
+ *   - scores are fp32: finite ones of any size are told apart to a step of theirs, scale x q.k x log2(e) beyond
+ *     its range makes the row unspecified;
  *   - the ancestor mask's bits count only for nodes of the request's own tree;
  *   - a request with T_r outside [1, T_max], a negative prefix or node offsets outside [0, N] gets
  *     SPEC_REQ_BAD_SIZE; one whose slots lie beyond its table row (or 2^31 - 1025) SPEC_REQ_BAD_BLOCK; no
  *     rows are written for either, nor for a request whose req_status holds other bits than BAD_BLOCK
- *     and TIMEOUT.  One with a bad id among the pages that its rows see gets SPEC_REQ_BAD_BLOCK and
- *     unspecified rows.
+ *     and TIMEOUT.  One with a bad id among the pages of its tree and of the prefix that its rows see gets
+ *     SPEC_REQ_BAD_BLOCK and unspecified rows.
  * workspace: the call's workspace_size bytes, 256-byte aligned, contents arbitrary; calls that may
  * overlap on the GPU (other streams, captured graphs) need one each.
  * Errors: SPEC_ERR_INVALID_ARG, SPEC_ERR_UNSUPPORTED (head_dim above 256, 2^31 rows of pages or of
@@ -700,7 +704,7 @@ spec_status_t spec_tree_attention_shared(const spec_attn_shared_params* p, void*
  * -infinity and NaN; a NaN or +infinity among a row's logits takes the whole row out.  If fewer than W are
  * offered the rest is parent j, token 0, score -infinity, length n of beam j, finished 0 at place j.
  * Sums of exponentials are in fp32 per thread and pairs of fp32 numbers beyond, scores and ranks in fp64,
- * rounded once.
+ * rounded once (a score beyond fp32 becomes -infinity).
  * Layouts: logits [B * W][ld] F32 / BF16, rows 16-byte aligned (ld a multiple of 16 bytes); scores [B][W]
  * fp32, lengths (>= 0), finished [B][W] int32; outputs [B][W].  out_score, out_length and out_finished
  * may be the inputs' own buffers.  eos outside [0, V): no token finishes a beam (a finished one then

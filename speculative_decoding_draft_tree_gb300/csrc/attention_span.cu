@@ -274,9 +274,10 @@ __global__ void __launch_bounds__(kSimtThreads) span_simt_kernel(Dev a) {
 // CTA (r, h, z): rows kMergeRows z .. of request r under KV head h, kR rows a warp at a time.  A row's pieces:
 // for a member of a group those of the group's unit, then those of its request's own unit, in stream order, so
 // that the sum does not depend on who ran when.  Rows of requests on their own whose unit was not cut have been
-// written already.  Lane kR p + i holds the weight and the place of piece p (of 32 / kR at a time) of row i.
+// written already.  A piece's log-sum-exp is one fp32 number: at 2^k it weighs pieces to 2^(k - 24), which scores of
+// thousands do not show.  Lane kR p + i holds the weight and the place of piece p (of 32 / kR at a time) of row i.
 // Bound by a chain of loads (record, group's record, log-sum-exps, values), so rows that share the first two
-// are taken by one CTA, two at a time (many rows: 32 trees under a window of 2048 94 us in all, 101 by one row a
+// are taken by one CTA, two at a time (many rows: 32 trees under a window of 2048 95 us in all, 101 by one row a
 // time), and a warp takes one row where there are few: 16 rows or less a request and head.
 constexpr int kMergeFew = 16;
 constexpr int kMergeRows = 32;
@@ -504,7 +505,7 @@ static spec_status_t check(const Args& x) {
 // The kernel of a call: on the tensor cores the rows kernel for windows over at most 16 query rows a request
 // and head (64 single tokens, 64 query heads on 8, window 4096: 171 us against 191 by the tile kernel; one
 // token, window 1024: 17.5 against 25), else the tile kernel, which also takes a shared call's few-rowed requests
-// beside their groups (8 groups of 8 single tokens, 32 heads on 8, 8192 shared: 94 us, 83 now; by one kernel for
+// beside their groups (8 groups of 8 single tokens, 32 heads on 8, 8192 shared: 94 us, 84 now; by one kernel for
 // the groups and then the other 112); the CUDA-core kernel for everything else.
 enum Kernel { kSimt, kTile, kFew };
 struct Plan {

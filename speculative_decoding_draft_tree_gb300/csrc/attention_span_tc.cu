@@ -28,7 +28,7 @@
 // rounded first, by a function of its own that works in TMEM (8 groups of 8 samples 84.1 us, 83.3 without it; in line 85.6).
 //
 // Bound, for long pair units, by the chain of a slot: products 1024 clocks, loads of S and maxima 420, weights 800,
-// waits; ~2650 clocks a key tile against 2048 of products alone (32 trees over 8192 shared slots: 168 us, and
+// waits; ~2650 clocks a key tile against 2048 of products alone (32 trees over 8192 shared slots: 169 us, and
 // 191 with the issuing thread's code unrolled for each slot, which took 1430 clocks a slot to get through, and
 // ranges cut without regard to masked tiles).  Short units are bound by what happens once in each: see the
 // costs in attention_span.cu.

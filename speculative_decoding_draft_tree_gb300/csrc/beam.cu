@@ -13,9 +13,9 @@
 //                     the row streams by.
 //   beam_pick_kernel  one CTA per request: the beams' candidates ranked by (score + log p) / penalty in
 //                     fp64, ties by beam and token.
-// Bound by the rows' bytes when there are many rows (64 x 8 rows of 152064 bf16: 36 us, 4.4 TB/s), by two
-// launches and the chain load -> maxima -> candidates when there are few (1 x 4 rows of 32000: 8.0 us; 16 x 5 of
-// 128256 fp32: 17.6 us); few rows are cut in segments.
+// Bound by the rows' bytes when there are many rows (64 x 8 rows of 152064 bf16: 36.6 us, 4.3 TB/s), by two
+// launches and the chain load -> maxima -> candidates when there are few (1 x 4 rows of 32000: 8.4 us; 16 x 5 of
+// 128256 fp32: 17.8 us); few rows are cut in segments.
 //
 // Ranks of different beams meet in one list, so log p has to be good.  References are whole numbers (the
 // maximum of x k2, rounded up), so that sums over threads and segments join by exact powers of two; log p =

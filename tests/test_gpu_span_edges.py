@@ -214,7 +214,7 @@ def test_a_shared_length_at_the_end_of_32_bits(dtype, length):
 def test_weights_of_few_rowed_units_keep_two_pieces(kind, T, n):
     """Units of one row tile hold a weight as two bf16 pieces (2^-16 of it), so that the output's own rounding is all that
     is seen: the root mean square of the error is within a tenth of what rounding the exact output gives.  One piece
-    (2^-8 / sqrt(3) at most, 0.0014 measured on such weights) would add a third of it and more."""
+    (2^-8 / sqrt(3) of a weight at most) would add a third of it, as it does in pair units (0.0022 for 0.0017)."""
     rng = np.random.default_rng(T + n)
     prefix = [100 + int(x) for x in rng.integers(0, 200, n)]
     kw = dict(window=90) if kind == "window" else dict(groups=[(0, 2, 100), (2, n, 0)])
